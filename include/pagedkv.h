@@ -81,7 +81,7 @@ typedef enum {
                                    that row's output is left unwritten */
 #define PKV_DEV_TIMEOUT 0x8     /* a kernel's internal wait gave up (a bug, never expected);
                                    the outputs of that call are unspecified */
-#define PKV_DEV_BAD_POSITION 0x10 /* rope append: a position outside [0, max_pos); that row skipped */
+#define PKV_DEV_BAD_POSITION 0x10 /* rope and latent append: a position outside [0, max_pos); that row skipped */
 
 /* One layer's K (or V) page pool: contiguous
  * [num_pages, page_size, num_kv_heads, head_dim] of `dtype`. */
@@ -360,6 +360,143 @@ int pkv_paged_attention_no_alloc(const void* q, const int32_t* cu_seqlens_q, con
                                  int32_t num_q_heads, int32_t max_pages_per_seq, int32_t max_kv_len,
                                  const void* k_cache, const void* v_cache, const pkv_cache_desc* cache,
                                  float scale, void* out, float* lse, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Latent attention: keys and values of all heads from one shared vector a token.
+ *
+ * A latent cache keeps for each token a latent part c (latent_dim values) and a
+ * rotary key part r (rope_dim values), one row [c, r] shared by every head, in
+ * the same kind of page pool as above: contiguous
+ * [num_pages, page_size, latent_dim + rope_dim], PKV_BF16 or PKV_F16. Per token
+ * that is 576 values at latent_dim 512, against 2 * heads * head_dim for a K/V
+ * cache. Models attend over it in two forms with equal results in exact
+ * arithmetic:
+ *  - absorbed (pkv_latent_attention), for decode rows: the key up-projection is
+ *    multiplied into the query beforehand, so a head's query is latent_dim +
+ *    rope_dim wide, every head attends the cached rows themselves, and the
+ *    output is the weighted sum of the latent parts (the caller applies the
+ *    value up-projection to it);
+ *  - expanded (pkv_latent_prefill), for chunks: the caller gathers the cached
+ *    rows (pkv_latent_gather), up-projects the latent parts to a 128-wide key
+ *    and a 128-wide value per head, and attends over those and the shared
+ *    rotary key part. Per (query, key) pair and head it computes 320 products
+ *    against the absorbed form's 1088.
+ * The calls follow the conventions above (ownership, asynchrony, errors, the
+ * device status word). Page tables, cu_seqlens and kv_lens are those of
+ * pkv_pack_tick; every causal rule is bottom-right: row i of a sequence with
+ * q_len rows and kv_len keys sees keys 0 .. kv_len - q_len + i.
+ *
+ * latent_dim is 256 or 512 and rope_dim 64 (PKV_E_SHAPE otherwise). Any
+ * page_size >= 1 is taken; multiples and divisors of 64 move in the fewest TMA
+ * boxes. */
+typedef struct {
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t latent_dim; /* 256 or 512 */
+  int32_t rope_dim;   /* 64 */
+  int32_t dtype;      /* PKV_F16 or PKV_BF16 */
+} pkv_latent_desc;
+
+/* pkv_latent_append — write new tokens' rows [c, rotated r] into their slots,
+ * and rotate the rotary parts of the tick's queries.
+ *
+ *   c_kv       device, latent part of token t at c_kv + t * c_stride (elements of the
+ *              cache dtype, latent_dim of them)
+ *   k_rope     device, rotary key part of token t at k_rope + t * kr_stride, not yet rotated
+ *   q_rope     device or NULL, rotary part of head h of token t at
+ *              q_rope + t * q_stride_t + h * q_stride_h, not yet rotated
+ *   q_out      device, where its rotation goes: q_out + t * qo_stride_t + h *
+ *              qo_stride_h; may be q_rope itself with the same strides (in place), and must
+ *              not overlap it otherwise. NULL with a NULL q_rope.
+ *   positions, cos_sin, max_pos, slot_mapping  as pkv_rope_kv_append (half-split
+ *              rotation over rope_dim values, in fp32, rounded once)
+ * Strides are in elements and may be any multiple of 8 (views of wider
+ * projection outputs); c_kv, k_rope, q_rope, q_out and cache must be 16-byte
+ * aligned. A negative slot skips the token's cache row (its queries are still
+ * rotated); a slot past the pool sets PKV_DEV_BAD_SLOT and skips the row. A
+ * position outside [0, max_pos) sets PKV_DEV_BAD_POSITION and skips the token
+ * altogether, the latent part included. Duplicate slots are a caller error.
+ * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE (also a stride that is negative or not a multiple of 8,
+ * num_q_heads < 1 with queries), PKV_E_ALIGN, PKV_E_DEVICE, PKV_E_CUDA. */
+int pkv_latent_append(const void* c_kv, int64_t c_stride, const void* k_rope, int64_t kr_stride,
+                      const void* q_rope, int64_t q_stride_t, int64_t q_stride_h, void* q_out,
+                      int64_t qo_stride_t, int64_t qo_stride_h, int32_t num_q_heads, const int32_t* positions,
+                      const float* cos_sin, int32_t max_pos, const int64_t* slot_mapping, int32_t num_tokens,
+                      void* cache, const pkv_latent_desc* desc, pkv_stream_t stream);
+
+/* pkv_latent_gather — copy the cached rows of every sequence, in order, into
+ * one packed tensor (bit for bit).
+ *
+ *   page_tables   device, int32 [num_seqs, max_pages_per_seq]
+ *   cu_seqlens_k  device, int32 [num_seqs + 1]; sequence b's rows 0 .. cu[b+1] - cu[b] - 1
+ *                 go to out rows cu[b] .. cu[b+1] - 1
+ *   total_k       rows of `out`; rows from cu[num_seqs] on are left as they were
+ *   out           device, contiguous [total_k, latent_dim + rope_dim], cache dtype, not
+ *                 overlapping the cache
+ * cu_seqlens_k that does not start at 0, decreases, or ends past total_k sets
+ * PKV_DEV_BAD_LENGTHS and copies nothing; so does a sequence longer than its
+ * page table, for that sequence. A page id outside the pool sets
+ * PKV_DEV_BAD_PAGE and skips the rows of that page.
+ * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_DEVICE, PKV_E_CUDA. */
+int pkv_latent_gather(const void* cache, const pkv_latent_desc* desc, const int32_t* page_tables,
+                      int32_t max_pages_per_seq, const int32_t* cu_seqlens_k, int32_t num_seqs, int32_t total_k,
+                      void* out, pkv_stream_t stream);
+
+/* pkv_latent_attention — the absorbed form over the pages.
+ *
+ *   q             device, contiguous [total_q, num_q_heads, latent_dim + rope_dim], cache dtype:
+ *                 the absorbed part first, then the rotated rotary part
+ *   cu_seqlens_q, kv_lens, page_tables, max_kv_len, lse  as pkv_paged_attention, but for
+ *                 cu[num_seqs], which may be less than total_q: rows from there on
+ *                 are padding, not read and left as they were
+ *   scale         > 0 and finite; multiplies q . [c, r] before the softmax
+ *   out           device, contiguous [total_q, num_q_heads, latent_dim], cache dtype
+ *   workspace     device, >= pkv_latent_attention_workspace_size(...) bytes, 256-byte
+ *                 aligned; needs no initialisation. Calls that may overlap (two streams, two
+ *                 captured graphs replayed side by side) need one each.
+ * Sums and softmax statistics are fp32; the softmax weights are rounded to the
+ * cache dtype for the products with the latent parts. Keys of a sequence are
+ * split over the GPU by the tick's total work, so the order of a row's fp32 sums
+ * depends on the other rows of the tick (the same call gives the same bits).
+ * Bad lengths or pages skip the sequence's rows as in pkv_paged_attention (bad
+ * cu_seqlens_q: every row). num_q_heads is at most 4096.
+ * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_WORKSPACE, PKV_E_DEVICE, PKV_E_CUDA. */
+size_t pkv_latent_attention_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_q_heads,
+                                           const pkv_latent_desc* desc);
+int pkv_latent_attention(const void* q, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                         const int32_t* page_tables, int32_t num_seqs, int32_t total_q, int32_t num_q_heads,
+                         int32_t max_pages_per_seq, int32_t max_kv_len, const void* cache,
+                         const pkv_latent_desc* desc, float scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, pkv_stream_t stream);
+
+/* pkv_latent_prefill — the expanded form over packed keys and values.
+ *
+ *   q             device, contiguous [total_q, num_heads, 192]: 128 values against k_nope,
+ *                 then 64 rotated values against k_rope
+ *   k_nope, v     device, key and value of head h of packed key row t at + t * stride_t +
+ *                 h * stride_h, 128 values each (views of one up-projection output will do)
+ *   k_rope        device, shared rotary key part of row t at + t * kr_stride, 64 values
+ *   cu_seqlens_q, cu_seqlens_k  device, int32 [num_seqs + 1]: rows of q / of the keys by
+ *                 sequence; from 0, non-decreasing, ending at or before total_q /
+ *                 total_k (rows behind are padding, not read and left as they were)
+ *   dtype         PKV_BF16 or PKV_F16, of q, k_nope, v, k_rope and out
+ *   scale         > 0 and finite
+ *   out           device, contiguous [total_q, num_heads, 128]
+ *   lse           device, fp32 [total_q, num_heads] or NULL
+ *   workspace     device, >= pkv_latent_prefill_workspace_size(...) bytes, 256-byte aligned;
+ *                 needs no initialisation; one for each of calls that may overlap
+ * Sequence b has kv_len = cu_k[b+1] - cu_k[b] >= q_len keys; the last q_len of
+ * them are the chunk's own. A sequence with rows and fewer keys than rows sets
+ * PKV_DEV_BAD_LENGTHS and is skipped; a cu_seqlens array that breaks the rules
+ * above skips every row. Strides are in elements, multiples of 8; pointers
+ * 16-byte aligned. Values of other sequences' rows never reach a row, NaN or not.
+ * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_WORKSPACE, PKV_E_DEVICE, PKV_E_CUDA. */
+size_t pkv_latent_prefill_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_heads);
+int pkv_latent_prefill(const void* q, const int32_t* cu_seqlens_q, const void* k_nope, int64_t kn_stride_t,
+                       int64_t kn_stride_h, const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                       const void* k_rope, int64_t kr_stride, const int32_t* cu_seqlens_k, int32_t num_seqs,
+                       int32_t total_q, int32_t total_k, int32_t num_heads, int32_t dtype, float scale, void* out,
+                       float* lse, void* workspace, size_t workspace_bytes, pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Status and instrumentation. */

@@ -7,6 +7,7 @@ or cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import itertools
 import os
@@ -49,6 +50,12 @@ EXPORTED = (
     "pkv_tick_positions",
     "pkv_kv_append_quant",
     "pkv_paged_attention_fp8",
+    "pkv_latent_append",
+    "pkv_latent_gather",
+    "pkv_latent_attention_workspace_size",
+    "pkv_latent_attention",
+    "pkv_latent_prefill_workspace_size",
+    "pkv_latent_prefill",
 )
 
 
@@ -62,6 +69,11 @@ class PagedKVError(RuntimeError):
 class CacheDesc(ctypes.Structure):
     _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class LatentDesc(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -132,6 +144,22 @@ def lib():
     L.pkv_paged_attention_fp8.restype = ctypes.c_int
     L.pkv_tick_positions.argtypes = [i32, P32, P32, P32, i32]
     L.pkv_tick_positions.restype = ctypes.c_int
+    PL = ctypes.POINTER(LatentDesc)
+    L.pkv_latent_append.argtypes = [vp, i64, vp, i64, vp, i64, i64, vp, i64, i64, i32, vp, vp, i32, vp, i32, vp, PL,
+                                    vp]
+    L.pkv_latent_append.restype = ctypes.c_int
+    L.pkv_latent_gather.argtypes = [vp, PL, vp, i32, vp, i32, i32, vp, vp]
+    L.pkv_latent_gather.restype = ctypes.c_int
+    L.pkv_latent_attention_workspace_size.argtypes = [i32, i32, i32, PL]
+    L.pkv_latent_attention_workspace_size.restype = sz
+    L.pkv_latent_attention.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, PL, ctypes.c_float, vp, vp, vp,
+                                       sz, vp]
+    L.pkv_latent_attention.restype = ctypes.c_int
+    L.pkv_latent_prefill_workspace_size.argtypes = [i32, i32, i32]
+    L.pkv_latent_prefill_workspace_size.restype = sz
+    L.pkv_latent_prefill.argtypes = [vp, vp, vp, i64, i64, vp, i64, i64, vp, i64, vp, i32, i32, i32, i32, i32,
+                                     ctypes.c_float, vp, vp, vp, sz, vp]
+    L.pkv_latent_prefill.restype = ctypes.c_int
     L.pkv_version.argtypes = []
     L.pkv_version.restype = ctypes.c_char_p
     _lib = L
@@ -442,6 +470,245 @@ def rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, 
                                   _ptr(v_cache), ctypes.byref(desc), _ptr(q_out), _stream_ptr(stream))
     _check(st, "pkv_rope_kv_append")
     return q_out
+
+
+# ---------------------------------------------------------------------------
+# latent attention
+
+LATENT_NOPE, LATENT_ROPE, LATENT_V = 128, 64, 128
+
+
+def _latent_desc(where, cache) -> LatentDesc:
+    if cache.dim() != 3 or not cache.is_contiguous():
+        raise ValueError(f"{where}: the latent cache must be a contiguous [num_pages, page_size, latent_dim + 64] tensor")
+    N, P, R = cache.shape
+    return LatentDesc(N, P, R - LATENT_ROPE, LATENT_ROPE, _dtype_code(cache))
+
+
+def _on_device(where, tensors):
+    """Every tensor on one CUDA device; returns a context that makes it the
+    current one (the library launches on the current device)."""
+    import torch
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{where}: all tensors must be on one CUDA device")
+    if dev.type != "cuda":
+        raise ValueError(f"{where} needs CUDA tensors")
+    if dev.index == torch.cuda.current_device():
+        return _SAME_DEVICE
+    return torch.cuda.device(dev)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _rows_of(where, name, t, dims, width, dtype):
+    """A [..., width] view whose last dimension is contiguous and whose rows may
+    be strided: returns its leading strides (0 for a dimension of one entry)."""
+    if t.dim() != dims or t.shape[-1] != width or t.dtype != dtype:
+        raise ValueError(f"{where}: {name} must have {dims} dimensions, {width} wide, and the cache's dtype")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{where}: {name} must be contiguous in its last dimension")
+    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in range(dims - 1))
+
+
+def _int32s(where, *tensors):
+    import torch
+    for t in tensors:
+        if t.dtype != torch.int32:
+            raise TypeError(f"{where}: index tensors must be int32")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: index tensors must be contiguous")
+
+
+def _lent(t, stream):
+    """A tensor allocated here for a call on `stream`: its memory is not handed
+    out again before that stream's work on it is done."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _out_and_lse(where, q, width, out, lse, want_lse, stream):
+    """The caller's out [T, H, width] and lse [T, H], checked, or new ones."""
+    import torch
+    T, H = q.shape[:2]
+    if out is None:
+        out = _lent(torch.empty((T, H, width), dtype=q.dtype, device=q.device), stream)
+    elif out.dtype != q.dtype or tuple(out.shape) != (T, H, width) or not out.is_contiguous():
+        raise ValueError(f"{where}: out must be a contiguous [{T}, {H}, {width}] tensor of q's dtype")
+    if lse is None:
+        if want_lse:
+            lse = _lent(torch.empty((T, H), dtype=torch.float32, device=q.device), stream)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, H) or not lse.is_contiguous():
+        raise ValueError(f"{where}: lse must be a contiguous float32 tensor [T, H]")
+    return out, lse
+
+
+def latent_append(c_kv, k_rope, positions, cos_sin, slot_mapping, cache, q_rope=None, q_out=None, stream=None):
+    """Write new tokens into a latent cache, rotating on the way (pkv_latent_append).
+
+    c_kv [T, latent_dim] and k_rope [T, 64] (strided rows allowed), positions
+    int32 [T], cos_sin float32 [max_pos, 32, 2] (rope_table), slot_mapping int64
+    [T], cache [N, P, latent_dim + 64]. With q_rope [T, H, 64] its rotation goes
+    to q_out (strided views allowed; q_out may be q_rope; a new tensor when it is
+    None). Returns q_out (None without q_rope)."""
+    import torch
+    where = "latent_append"
+    desc = _latent_desc(where, cache)
+    guard = _on_device(where, (cache, c_kv, k_rope, positions, cos_sin, slot_mapping, q_rope, q_out))
+    T = int(slot_mapping.shape[0])
+    if positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64 or cos_sin.dtype != torch.float32:
+        raise TypeError(f"{where}: positions int32, slot_mapping int64, cos_sin float32")
+    if not (positions.is_contiguous() and slot_mapping.is_contiguous() and cos_sin.is_contiguous()):
+        raise ValueError(f"{where}: positions, slot_mapping and cos_sin must be contiguous")
+    if (slot_mapping.dim() != 1 or tuple(positions.shape) != (T,) or cos_sin.dim() != 3
+            or tuple(cos_sin.shape[1:]) != (LATENT_ROPE // 2, 2) or c_kv.shape[0] != T or k_rope.shape[0] != T):
+        raise ValueError(f"{where}: c_kv, k_rope, positions and slot_mapping must agree on the number of tokens, "
+                         f"and cos_sin be [max_pos, {LATENT_ROPE // 2}, 2]")
+    c_st, = _rows_of(where, "c_kv", c_kv, 2, int(desc.latent_dim), cache.dtype)
+    kr_st, = _rows_of(where, "k_rope", k_rope, 2, LATENT_ROPE, cache.dtype)
+    q_st = q_sh = qo_st = qo_sh = H = 0
+    if q_rope is not None:
+        q_st, q_sh = _rows_of(where, "q_rope", q_rope, 3, LATENT_ROPE, cache.dtype)
+        H = int(q_rope.shape[1])
+        if q_out is None:
+            q_out = _lent(torch.empty(q_rope.shape, dtype=q_rope.dtype, device=q_rope.device), stream)
+        qo_st, qo_sh = _rows_of(where, "q_out", q_out, 3, LATENT_ROPE, cache.dtype)
+        if q_rope.shape[0] != T or q_out.shape != q_rope.shape:
+            raise ValueError(f"{where}: q_rope and q_out must be [T, H, {LATENT_ROPE}]")
+        for n, st in ((T, qo_st), (H, qo_sh)):
+            if n > 1 and st == 0:
+                raise ValueError(f"{where}: q_out must not be a broadcast view")
+    elif q_out is not None:
+        raise ValueError(f"{where}: q_out without q_rope")
+    with guard:
+        st = lib().pkv_latent_append(_ptr(c_kv), c_st, _ptr(k_rope), kr_st, _ptr(q_rope), q_st, q_sh, _ptr(q_out),
+                                     qo_st, qo_sh, H, _ptr(positions), _ptr(cos_sin), int(cos_sin.shape[0]),
+                                     _ptr(slot_mapping), T, _ptr(cache), ctypes.byref(desc), _stream_ptr(stream))
+    _check(st, "pkv_latent_append")
+    return q_out
+
+
+def latent_gather(cache, page_tables, cu_seqlens_k, total_k: int, out=None, stream=None):
+    """Cached rows of every sequence, packed (pkv_latent_gather): out [total_k,
+    latent_dim + 64], sequence b in rows cu_seqlens_k[b] .. cu_seqlens_k[b + 1].
+    out[:, :latent_dim] is what the up-projection reads, out[:, latent_dim:] the
+    k_rope of latent_prefill."""
+    import torch
+    where = "latent_gather"
+    desc = _latent_desc(where, cache)
+    _int32s(where, page_tables, cu_seqlens_k)
+    guard = _on_device(where, (cache, page_tables, cu_seqlens_k, out))
+    B = int(cu_seqlens_k.shape[0]) - 1
+    if page_tables.dim() != 2 or cu_seqlens_k.dim() != 1 or B < 0 or page_tables.shape[0] < B:
+        raise ValueError(f"{where}: page_tables [B, W] and cu_seqlens_k [B + 1] disagree")
+    if out is None:
+        out = _lent(torch.empty((int(total_k), cache.shape[2]), dtype=cache.dtype, device=cache.device), stream)
+    elif out.dtype != cache.dtype or tuple(out.shape) != (int(total_k), cache.shape[2]) or not out.is_contiguous():
+        raise ValueError(f"{where}: out must be a contiguous [total_k, {cache.shape[2]}] tensor of the cache's dtype")
+    with guard:
+        st = lib().pkv_latent_gather(_ptr(cache), ctypes.byref(desc), _ptr(page_tables), int(page_tables.shape[1]),
+                                     _ptr(cu_seqlens_k), B, int(total_k), _ptr(out), _stream_ptr(stream))
+    _check(st, "pkv_latent_gather")
+    return out
+
+
+def latent_workspace_size(num_seqs: int, total_q: int, num_q_heads: int, cache) -> int:
+    desc = _latent_desc("latent_workspace_size", cache)
+    n = lib().pkv_latent_attention_workspace_size(int(num_seqs), int(total_q), int(num_q_heads), ctypes.byref(desc))
+    if n == 0:
+        raise PagedKVError(-3, "pkv_latent_attention_workspace_size")
+    return int(n)
+
+
+def alloc_latent_workspace(num_seqs: int, total_q: int, num_q_heads: int, cache):
+    import torch
+    return torch.empty(latent_workspace_size(num_seqs, total_q, num_q_heads, cache), dtype=torch.uint8,
+                       device=cache.device)
+
+
+def latent_attention(q, cu_seqlens_q, kv_lens, page_tables, cache, scale: float, max_kv_len: int, out=None,
+                     lse=None, workspace=None, want_lse: bool = True, stream=None):
+    """Absorbed latent attention over the pages (pkv_latent_attention).
+
+    q [T, H, latent_dim + 64] (cache dtype), cu_seqlens_q int32 [B + 1], kv_lens
+    int32 [B], page_tables int32 [B, W], cache [N, P, latent_dim + 64]. Returns
+    (out [T, H, latent_dim], lse [T, H])."""
+    where = "latent_attention"
+    desc = _latent_desc(where, cache)
+    _int32s(where, cu_seqlens_q, kv_lens, page_tables)
+    guard = _on_device(where, (q, cu_seqlens_q, kv_lens, page_tables, cache, out, lse, workspace))
+    if q.dtype != cache.dtype:
+        raise TypeError(f"{where}: q and cache must share one dtype")
+    if q.dim() != 3 or q.shape[2] != cache.shape[2] or not q.is_contiguous():
+        raise ValueError(f"{where}: q must be a contiguous [T, H, {cache.shape[2]}] tensor")
+    B = int(cu_seqlens_q.shape[0]) - 1
+    if (cu_seqlens_q.dim() != 1 or kv_lens.dim() != 1 or page_tables.dim() != 2 or B < 0 or kv_lens.shape[0] < B
+            or page_tables.shape[0] < B):
+        raise ValueError(f"{where}: cu_seqlens_q [B + 1], kv_lens [B] and page_tables [B, W] disagree")
+    out, lse = _out_and_lse(where, q, int(desc.latent_dim), out, lse, want_lse, stream)
+    T, H = int(q.shape[0]), int(q.shape[1])
+    if workspace is None:
+        workspace = _lent(alloc_latent_workspace(B, T, H, cache), stream)
+    elif not workspace.is_contiguous():
+        raise ValueError(f"{where}: workspace must be contiguous")
+    with guard:
+        st = lib().pkv_latent_attention(_ptr(q), _ptr(cu_seqlens_q), _ptr(kv_lens), _ptr(page_tables), B, T, H,
+                                        int(page_tables.shape[1]), int(max_kv_len), _ptr(cache), ctypes.byref(desc),
+                                        scale, _ptr(out), _ptr(lse), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _check(st, "pkv_latent_attention")
+    return out, lse
+
+
+def latent_prefill_workspace_size(num_seqs: int, total_q: int, num_heads: int) -> int:
+    n = lib().pkv_latent_prefill_workspace_size(int(num_seqs), int(total_q), int(num_heads))
+    if n == 0:
+        raise PagedKVError(-3, "pkv_latent_prefill_workspace_size")
+    return int(n)
+
+
+def alloc_latent_prefill_workspace(num_seqs: int, q):
+    import torch
+    return torch.empty(latent_prefill_workspace_size(num_seqs, q.shape[0], q.shape[1]), dtype=torch.uint8,
+                       device=q.device)
+
+
+def latent_prefill(q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, scale: float, out=None, lse=None,
+                   workspace=None, want_lse: bool = True, stream=None):
+    """Expanded latent attention of chunks over packed keys (pkv_latent_prefill).
+
+    q [Tq, H, 192]; k_nope and v [Tk, H, 128], k_rope [Tk, 64] (strided rows
+    allowed: views of the up-projection's output and of the gathered rows);
+    cu_seqlens_q, cu_seqlens_k int32 [B + 1]. Returns (out [Tq, H, 128], lse [Tq, H])."""
+    where = "latent_prefill"
+    _int32s(where, cu_seqlens_q, cu_seqlens_k)
+    guard = _on_device(where, (q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, out, lse, workspace))
+    if q.dim() != 3 or q.shape[2] != LATENT_NOPE + LATENT_ROPE or not q.is_contiguous():
+        raise ValueError(f"{where}: q must be a contiguous [T, H, {LATENT_NOPE + LATENT_ROPE}] tensor")
+    kn_st, kn_sh = _rows_of(where, "k_nope", k_nope, 3, LATENT_NOPE, q.dtype)
+    v_st, v_sh = _rows_of(where, "v", v, 3, LATENT_V, q.dtype)
+    kr_st, = _rows_of(where, "k_rope", k_rope, 2, LATENT_ROPE, q.dtype)
+    Tq, H, Tk = int(q.shape[0]), int(q.shape[1]), int(k_rope.shape[0])
+    if k_nope.shape[0] != Tk or v.shape[0] != Tk or k_nope.shape[1] != H or v.shape[1] != H:
+        raise ValueError(f"{where}: k_nope, v [Tk, H, 128] and k_rope [Tk, 64] disagree")
+    B = int(cu_seqlens_q.shape[0]) - 1
+    if cu_seqlens_q.dim() != 1 or B < 0 or cu_seqlens_k.shape != cu_seqlens_q.shape:
+        raise ValueError(f"{where}: cu_seqlens_q and cu_seqlens_k must both be [B + 1]")
+    out, lse = _out_and_lse(where, q, LATENT_V, out, lse, want_lse, stream)
+    if workspace is None:
+        workspace = _lent(alloc_latent_prefill_workspace(B, q), stream)
+    elif not workspace.is_contiguous():
+        raise ValueError(f"{where}: workspace must be contiguous")
+    with guard:
+        st = lib().pkv_latent_prefill(_ptr(q), _ptr(cu_seqlens_q), _ptr(k_nope), kn_st, kn_sh, _ptr(v), v_st, v_sh,
+                                      _ptr(k_rope), kr_st, _ptr(cu_seqlens_k), B, Tq, Tk, H, _dtype_code(q), scale,
+                                      _ptr(out), _ptr(lse), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _check(st, "pkv_latent_prefill")
+    return out, lse
 
 
 def selftest_bounded_wait(limit_us: int, result=None, stream=None) -> None:

@@ -59,6 +59,16 @@ int32_t* device_status_ptr() {
   return f ? f->status : nullptr;
 }
 
+int current_device(DeviceView* v) {
+  const DeviceFacts* f = device_facts();
+  if (!f) return PKV_E_CUDA;
+  if (!f->ok) return PKV_E_DEVICE;
+  cudaGetDevice(&v->id);
+  v->num_sms = f->num_sms;
+  v->status = f->status;
+  return PKV_OK;
+}
+
 // ---------------------------------------------------------------------------
 // kernel timing
 

@@ -14,6 +14,14 @@ namespace pkv {
 int32_t* device_status_ptr();  // device address of the status word on the current device
 int cuda_fail(cudaError_t e, const char* where);  // records the error text, returns PKV_E_CUDA
 
+// The current device as the entry points need it.
+struct DeviceView {
+  int id, num_sms;
+  int32_t* status;  // device address of the status word
+};
+// PKV_OK, PKV_E_CUDA (no device facts to be had) or PKV_E_DEVICE (not an sm_103 GPU).
+int current_device(DeviceView* v);
+
 // ---------------------------------------------------------------------------
 // kernel timing hooks (pkv_api.cu). A KernelTimer brackets one launch with
 // CUDA events on its stream when timing is enabled.
@@ -200,6 +208,59 @@ cudaError_t launch_rope_append(const void* q, const void* k, const void* v, cons
                                const float* cos_sin, int32_t max_pos, const int64_t* slots, int32_t T,
                                int32_t Hq, void* kc, void* vc, void* q_out, const pkv_cache_desc& c,
                                int32_t* dev_status, int num_sms, cudaStream_t s);
+
+// Latent cache (pkv_latent_*.cu). Row = latent_dim + rope_dim values.
+struct LatentAppendArgs {
+  const void *c, *kr, *q;
+  int64_t c_st, kr_st, q_st, q_sh, qo_st, qo_sh;   // strides, elements
+  void *q_out, *cache;
+  const int32_t* positions;
+  const float* cos_sin;
+  const int64_t* slots;
+  int32_t max_pos, T, Hq, dtype, latent_dim, rope_dim;
+  int64_t pool_slots;
+  int32_t* dev_status;
+  int num_sms;
+};
+cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t s);
+
+struct LatentGatherArgs {
+  const void* cache;
+  const int32_t *page_tables, *cu;
+  int32_t B, total, max_pages, P, num_pages, row_vecs;   // row_vecs: 16-byte vectors of a row
+  void* out;
+  int32_t* dev_status;
+  int num_sms;
+};
+cudaError_t launch_latent_gather(const LatentGatherArgs& a, cudaStream_t s);
+
+struct LatentAttnArgs {
+  const void *q, *cache;
+  const int32_t *cu, *kv_lens, *page_tables;
+  int32_t B, T, H, P, num_pages, max_pages, max_kv_len, latent_dim, dtype;
+  float scale;
+  void* out;
+  float* lse;
+  char* ws;
+  DeviceView dev;
+};
+size_t latent_attn_workspace(int32_t B, int32_t T, int32_t H, int32_t latent_dim);
+cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t s);
+
+struct LatentPrefillArgs {
+  const void *q, *kn, *v, *kr;
+  int64_t kn_st, kn_sh, v_st, v_sh, kr_st;   // strides, elements
+  const int32_t *cu_q, *cu_k;
+  int32_t B, Tq, Tk, H, dtype;
+  float scale;
+  void* out;
+  float* lse;
+  char* ws;
+  DeviceView dev;
+};
+size_t latent_prefill_workspace(int32_t B, int32_t Tq, int32_t H);
+cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, cudaStream_t s);
+
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_combine(const AttnArgs& a, cudaStream_t s);
 // Returns cudaErrorNotSupported when the shape has no tensor-core path.

@@ -1,0 +1,690 @@
+"""Latent attention: the oracle against closed forms and against torch, the
+calls' refusals on the host, and (GPU) every operator against the oracle in 64
+bits, alone and as the run a serving tick makes of them.
+
+Tolerances. u is half a step of the cache type (bf16 2^-8, f16 2^-11). A result
+is rounded once (u |out|) and every softmax weight once before its product with
+the values (u sum_j w_j |v_j|; f16 weights below 2^-14 are subnormal, off by up to
+2^-25 of a weight scale that is at least 1, so 2^-25 max|v| a key). A score is an fp32 sum
+of D products: off by at most D 2^-23 scale sum_d |q_d k_d| =: ds (2^-23: the
+tensor core may truncate), which moves every weight by a factor exp(+-ds) before
+and, through the sum, as much after: 2 ds sum_j w_j |v_j|. The output sums over L
+keys in fp32 add at most (L + 64) 2^-23 of sum_j w_j |v_j|, and the exponential's and
+the final scaling's errors, a few 2^-22 relative, are below 2^-20. lse moves by ds, by
+the sum's own relative error (L + 64) 2^-23, and by 2^-20 plus two roundings of its size.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import latent as O
+from oracle.rope import apply_rope
+from paged_kv_attention_mapping_gb300 import binding
+
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
+HALF_STEP = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+SCALE = 1.0 / math.sqrt(192)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from paged_kv_attention_mapping_gb300 import build
+    build.build()
+    return binding.lib()
+
+
+@pytest.fixture(scope="module")
+def dev(lib):
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    d = torch.device("cuda:0")
+    torch.cuda.set_device(d)
+    return d
+
+
+# ---------------------------------------------------------------------------
+# oracle pins (CPU)
+
+def test_oracle_attention_matches_torch():
+    g = np.random.default_rng(0)
+    n, L, H = 5, 11, 3
+    q, rows = g.standard_normal((n, H, 320)), g.standard_normal((L, 320))
+    mask = torch.ones(n, L, dtype=torch.bool).tril(L - n)
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a))
+    want = torch.nn.functional.scaled_dot_product_attention(
+        t(q).transpose(0, 1), t(rows).expand(H, L, 320), t(rows)[:, :256].expand(H, L, 256), mask, scale=0.1)
+    out, lse, _ = O.attend_absorbed(q, rows, 0.1)
+    assert np.abs(out - want.transpose(0, 1).numpy()).max() < 1e-12
+    x = 0.1 * np.einsum("nhd,ld->nhl", q, rows)
+    x[~np.broadcast_to(mask.numpy()[:, None], x.shape)] = -np.inf
+    assert np.abs(lse - torch.logsumexp(t(x), -1).numpy()).max() < 1e-12
+
+
+def test_oracle_expanded_equals_absorbed():
+    """The two forms agree: with k_nope = c Wk and v = c Wv, attending the expanded
+    keys equals attending the rows with q Wk^T and expanding the result."""
+    g = np.random.default_rng(1)
+    n, L, H, ld = 4, 9, 2, 32
+    c, r = g.standard_normal((L, ld)), g.standard_normal((L, 64))
+    wk, wv = g.standard_normal((H, ld, 128)) / 6, g.standard_normal((H, ld, 128)) / 6
+    q = g.standard_normal((n, H, 192))
+    kn, v = np.einsum("lc,hcd->lhd", c, wk), np.einsum("lc,hcd->lhd", c, wv)
+    e, el, _ = O.attend_expanded(q, kn, v, r, SCALE)
+    qa = np.concatenate([np.einsum("nhd,hcd->nhc", q[..., :128], wk), q[..., 128:]], -1)
+    a, al, _ = O.attend_absorbed(qa, np.concatenate([c, r], -1), SCALE)
+    assert np.abs(np.einsum("nhc,hcd->nhd", a, wv) - e).max() < 1e-12
+    assert np.abs(al - el).max() < 1e-12
+
+
+def test_oracle_one_key_and_rows_ahead():
+    rows = np.random.default_rng(2).standard_normal((3, 96))
+    q = np.random.default_rng(3).standard_normal((3, 1, 96))
+    out, lse, _ = O.attend_absorbed(q, rows, 0.2)
+    assert np.array_equal(out[0, 0], rows[0, :32])               # the first row sees one key
+    assert abs(lse[0, 0] - 0.2 * q[0, 0] @ rows[0]) < 1e-14
+
+
+def test_oracle_append_and_gather():
+    cache = np.zeros((3, 2, 66))
+    c, k = np.full((2, 2), 7.0), np.zeros((2, 64))
+    k[:, 0] = 1.0
+    got = O.append(cache, c, k, [0, 3], [5, -1], 100.0)
+    assert list(got[2, 1, :3]) == [7.0, 7.0, 1.0] and np.count_nonzero(got) == 3
+    assert np.array_equal(O.gather_sequence(got, [1, 2], 4)[3], got[2, 1])
+
+
+# ---------------------------------------------------------------------------
+# refusals (CPU: no pointer reaches a kernel)
+
+FAKE = ctypes.c_void_p(4096)
+ODD = ctypes.c_void_p(4098)
+
+
+def _desc(**kw):
+    d = dict(num_pages=4, page_size=16, latent_dim=512, rope_dim=64, dtype=binding.PKV_BF16)
+    d.update(kw)
+    return binding.LatentDesc(**d)
+
+
+BAD_DESCS = [(dict(dtype=binding.PKV_F32), -2), (dict(dtype=binding.PKV_FP8_E4M3), -2), (dict(dtype=9), -2),
+             (dict(latent_dim=384), -3), (dict(rope_dim=32), -3), (dict(page_size=0), -3), (dict(num_pages=0), -3),
+             (dict(num_pages=1 << 27, page_size=64), -3)]
+
+
+def _append(lib, desc=None, c=FAKE, cs=512, ks=64, q=FAKE, qst=192, qsh=64, qo=FAKE, H=4, pos=FAKE, T=3, slots=FAKE,
+            max_pos=8, cache=FAKE):
+    d = desc or _desc()
+    return lib.pkv_latent_append(c, cs, FAKE, ks, q, qst, qsh, qo, 192, 64, H, pos, FAKE, max_pos, slots, T, cache,
+                                 ctypes.byref(d), None)
+
+
+def _gather(lib, desc=None, B=1, total=4, width=1, out=FAKE, cu=FAKE):
+    d = desc or _desc()
+    return lib.pkv_latent_gather(FAKE, ctypes.byref(d), FAKE, width, cu, B, total, out, None)
+
+
+def _attend(lib, desc=None, q=FAKE, B=1, T=2, H=16, W=4, max_kv=64, scale=0.1, out=FAKE, lse=None, ws=FAKE,
+            ws_bytes=1 << 30):
+    d = desc or _desc()
+    return lib.pkv_latent_attention(q, FAKE, FAKE, FAKE, B, T, H, W, max_kv, FAKE, ctypes.byref(d), scale, out, lse,
+                                    ws, ws_bytes, None)
+
+
+def _prefill(lib, q=FAKE, kn=FAKE, kst=256, ksh=128, krs=64, B=1, Tq=2, Tk=4, H=2, dtype=binding.PKV_F16, scale=0.1,
+             out=FAKE, ws=FAKE, ws_bytes=1 << 30):
+    return lib.pkv_latent_prefill(q, FAKE, kn, kst, ksh, FAKE, 256, 128, FAKE, krs, FAKE, B, Tq, Tk, H, dtype, scale,
+                                  out, None, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", BAD_DESCS)
+def test_bad_caches_are_refused(lib, kw, status):
+    d = _desc(**kw)
+    assert _append(lib, desc=d) == status
+    assert _gather(lib, desc=d) == status
+    assert _attend(lib, desc=d) == status
+    assert lib.pkv_latent_attention_workspace_size(1, 1, 16, ctypes.byref(d)) == 0
+
+
+def test_append_refusals(lib):
+    assert _append(lib, T=-1) == -3 and _append(lib, max_pos=0) == -3
+    assert _append(lib, cs=510) == -3 and _append(lib, ks=-8) == -3
+    assert _append(lib, qst=100) == -3 and _append(lib, H=0) == -3
+    assert _append(lib, c=None) == -1 and _append(lib, qo=None) == -1 and _append(lib, q=None) == -1
+    assert _append(lib, pos=None) == -1 and _append(lib, slots=None) == -1 and _append(lib, cache=None) == -1
+    assert _append(lib, c=ODD) == -7 and _append(lib, q=ODD) == -7 and _append(lib, slots=ctypes.c_void_p(4100)) == -7
+    assert _append(lib, T=0) == 0
+
+
+def test_gather_refusals(lib):
+    assert _gather(lib, B=-1) == -3 and _gather(lib, total=-1) == -3 and _gather(lib, width=0) == -3
+    assert _gather(lib, out=None) == -1 and _gather(lib, cu=None) == -1 and _gather(lib, out=ODD) == -7
+    assert _gather(lib, total=0) == 0 and _gather(lib, B=0) == 0
+
+
+def test_attention_refusals(lib):
+    for kw in (dict(B=-1), dict(T=-1), dict(H=0), dict(H=4097), dict(max_kv=-1), dict(W=0), dict(scale=0.0),
+               dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(T=1 << 27, H=16),
+               dict(W=1 << 28)):
+        assert _attend(lib, **kw) == -3, kw
+    assert _attend(lib, q=None) == -1 and _attend(lib, out=None) == -1 and _attend(lib, ws=None) == -1
+    assert _attend(lib, q=ODD) == -7 and _attend(lib, out=ODD) == -7 and _attend(lib, lse=ODD) == -7
+    assert _attend(lib, ws_bytes=16) == -6 and _attend(lib, ws=ctypes.c_void_p(4096 + 64)) == -6
+    assert _attend(lib, T=0) == 0 and _attend(lib, B=0) == 0
+
+
+def test_prefill_refusals(lib):
+    for kw in (dict(B=-1), dict(Tq=-1), dict(Tk=-1), dict(H=0), dict(scale=0.0), dict(kst=100), dict(ksh=-8),
+               dict(krs=4), dict(Tk=0), dict(Tq=1 << 30, H=4)):
+        assert _prefill(lib, **kw) == -3, kw
+    assert _prefill(lib, dtype=binding.PKV_F32) == -2 and _prefill(lib, dtype=binding.PKV_FP8_E4M3) == -2
+    assert _prefill(lib, q=None) == -1 and _prefill(lib, kn=ODD) == -7
+    assert _prefill(lib, ws_bytes=16) == -6
+    assert _prefill(lib, Tq=0) == 0 and _prefill(lib, B=0) == 0
+
+
+def test_workspace_sizes(lib):
+    cache = torch.empty((4, 16, 576), dtype=torch.bfloat16)
+    n = binding.latent_workspace_size(4, 10, 16, cache)
+    assert n > 0 and n % 256 == 0
+    n = binding.latent_prefill_workspace_size(4, 10, 16)
+    assert n > 0 and n % 256 == 0
+    with pytest.raises(binding.PagedKVError):
+        binding.latent_workspace_size(4, 10, 0, cache)
+    with pytest.raises(binding.PagedKVError):
+        binding.latent_prefill_workspace_size(-1, 10, 16)
+
+
+def test_binding_refuses_wrong_tensors(lib):
+    z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t)
+    i32, i64, f32 = torch.int32, torch.int64, torch.float32
+    cache, q, tab = z(4, 16, 576), z(1, 8, 576), z(4, 32, 2, t=f32)
+    cu, kv, pt = torch.tensor([0, 1], dtype=i32), z(1, t=i32), z(1, 1, t=i32)
+    with pytest.raises(ValueError):                                        # host tensors
+        binding.latent_attention(q, cu, kv, pt, cache, 0.1, 16)
+    with pytest.raises(TypeError):
+        binding.latent_attention(q, cu.long(), kv, pt, cache, 0.1, 16)
+    with pytest.raises(ValueError):
+        binding.latent_attention(q, cu, kv, pt, cache.transpose(0, 1), 0.1, 16)
+    with pytest.raises(ValueError):
+        binding.latent_gather(cache, pt, cu, 1)
+    with pytest.raises(TypeError):
+        binding.latent_gather(cache, pt.long(), cu, 1)
+    with pytest.raises(ValueError):
+        binding.latent_append(z(1, 512), z(1, 64), z(1, t=i32), tab, z(1, t=i64), cache)
+    with pytest.raises(ValueError):
+        binding.latent_prefill(z(1, 2, 192), cu, z(1, 2, 128), z(1, 2, 128), z(1, 64), cu, 0.1)
+    with pytest.raises(TypeError):
+        binding.latent_prefill(z(1, 2, 192), cu.long(), z(1, 2, 128), z(1, 2, 128), z(1, 64), cu, 0.1)
+
+
+# ---------------------------------------------------------------------------
+# GPU
+
+def _cum(lens):
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+
+
+def _host(t):
+    return t.double().cpu().numpy()
+
+
+def _i32(a, dev):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(dev)
+
+
+def _bounds(dtype, D, L, out, lse, spread, vmax):
+    u = HALF_STEP[dtype]
+    mass, dot = spread
+    ds = D * 2.0 ** -23 * dot
+    small = L * 2.0 ** -25 * vmax if dtype == "f16" else 0.0
+    tol = u * np.abs(out) + (u + 2 * ds[..., None] + (L + 64) * 2.0 ** -23 + 2.0 ** -20) * mass + small
+    return tol * (1 + u), ds + (L + 64) * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * np.abs(lse)
+
+
+class Paged:
+    """A tick over a latent cache: random rows in scattered pages, NaN in every
+    slot that no sequence owns, -1 in unused table entries."""
+
+    def __init__(self, dev, dtype, ld, H, P, q_lens, kv_lens, seed=0, pad_rows=0):
+        g = np.random.default_rng(seed)
+        self.dev, self.dtype, self.ld, self.H, self.P = dev, dtype, ld, H, P
+        self.q_lens, self.kv_lens = list(q_lens), list(kv_lens)
+        need = [-(-L // P) for L in kv_lens]
+        pages = sum(need) + 3
+        perm = g.permutation(pages)
+        self.table = np.full((len(need), max(need + [1]) + 1), -1, np.int32)
+        cache = np.full((pages, P, ld + 64), np.nan, np.float32)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = perm[at:at + n]
+            at += n
+            for j in range(kv_lens[b]):
+                cache[self.table[b, j // P], j % P] = g.standard_normal(ld + 64)
+        self.cache = torch.from_numpy(cache).to(dev, TYPES[dtype])
+        self.total = int(sum(q_lens))
+        self.q = torch.from_numpy(g.standard_normal((self.total + pad_rows, H, ld + 64)).astype(np.float32)).to(
+            dev, TYPES[dtype])
+        self.cu = _cum(q_lens)
+
+    def call(self, **kw):
+        return binding.latent_attention(self.q, _i32(self.cu, self.dev), _i32(self.kv_lens, self.dev),
+                                        _i32(self.table, self.dev), self.cache, SCALE, max(self.kv_lens + [1]), **kw)
+
+    def check(self, out, lse):
+        out, lse, q, cache = _host(out), _host(lse), _host(self.q), _host(self.cache)
+        for b, (n, L) in enumerate(zip(self.q_lens, self.kv_lens)):
+            if n == 0:
+                continue
+            rows = O.gather_sequence(cache, self.table[b], L)
+            at = slice(int(self.cu[b]), int(self.cu[b]) + n)
+            o, l, spread = O.attend_absorbed(q[at], rows, SCALE)
+            tol, tol_lse = _bounds(self.dtype, self.ld + 64, L, o, l, spread, np.abs(rows).max())
+            bad = np.abs(out[at] - o) > tol
+            assert not bad.any(), (b, np.argwhere(bad)[:4], np.abs(out[at] - o).max())
+            assert (np.abs(lse[at] - l) <= tol_lse).all(), (b, np.abs(lse[at] - l).max(), tol_lse.min())
+            assert np.isfinite(out[at]).all()
+
+
+ABSORBED = [
+    # dtype, latent, heads, page, q_lens, kv_lens
+    ("bf16", 512, 16, 64, [1], [1]),
+    ("f16", 512, 16, 64, [1, 1, 1, 1], [63, 64, 65, 2]),
+    ("bf16", 512, 128, 64, [1, 1, 1], [127, 128, 129]),
+    ("bf16", 512, 128, 256, [1, 0, 1], [300, 77, 1000]),
+    ("f16", 512, 1, 16, [1, 1], [33, 500]),
+    ("bf16", 512, 3, 1, [2, 1], [70, 9]),
+    ("bf16", 512, 20, 24, [5, 1, 3], [261, 24, 130]),
+    ("f16", 512, 40, 48, [4, 2], [50, 513]),
+    ("bf16", 512, 136, 100, [2, 1], [205, 99]),
+    ("bf16", 512, 8, 128, [70, 1], [70, 5]),
+    ("f16", 512, 16, 32, [33, 20], [161, 258]),
+    ("bf16", 512, 64, 8, [3], [1000]),
+    ("bf16", 512, 16, 3, [1], [400]),
+    ("bf16", 512, 16, 64, [1], [20000]),
+    ("f16", 512, 128, 64, [1], [5003]),
+    ("bf16", 512, 32, 64, [5], [12 * 128 + 2]),
+    ("bf16", 512, 16, 7, [9], [9]),
+    ("bf16", 256, 16, 64, [1, 1], [1, 640]),
+    ("f16", 256, 128, 16, [1, 2], [129, 400]),
+    ("bf16", 256, 20, 24, [5, 1], [700, 25]),
+    ("bf16", 256, 5, 100, [17], [3001]),
+    ("bf16", 512, 16, 64, [1] * 90, [1 + 37 * k % 600 for k in range(90)]),
+    ("f16", 256, 4, 64, [k % 4 for k in range(60)], [1 + 53 * k % 300 + k % 4 for k in range(60)]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", ABSORBED, ids=lambda c: f"{c[0]}-{c[1]}-h{c[2]}-p{c[3]}-n{len(c[4])}-k{max(c[5])}")
+def test_absorbed_matches_the_oracle(dev, case):
+    t = Paged(dev, *case)
+    out, lse = t.call()
+    assert binding.device_status() == 0
+    t.check(out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ld", [256, 512])
+def test_absorbed_leaves_padding_rows_and_unrequested_lse_alone(dev, ld):
+    t = Paged(dev, "bf16", ld, 24, 16, [1, 3], [40, 200], pad_rows=3)
+    out = torch.full((t.total + 3, 24, ld), 5.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((t.total + 3, 24), 5.0, device=dev)
+    t.q[t.total:] = float("nan")
+    t.call(out=out, lse=lse)
+    assert binding.device_status() == 0
+    assert (out[t.total:] == 5).all() and (lse[t.total:] == 5).all()
+    t.check(out, lse)
+    again, none = t.call(want_lse=False)
+    assert none is None and torch.equal(again[:t.total], out[:t.total])
+
+
+@pytest.mark.gpu
+def test_absorbed_same_call_same_bits(dev):
+    t = Paged(dev, "bf16", 512, 128, 64, [1, 1, 2], [3000, 50, 700])
+    first = t.call()
+    for _ in range(3):
+        again = t.call()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.gpu
+def test_absorbed_bad_data_skips_the_sequence(dev):
+    """A bad length or page skips that sequence's rows, a bad cu_seqlens_q every row."""
+    t = Paged(dev, "bf16", 512, 16, 64, [1, 2, 1], [300, 4000, 100])
+    good, good_lse = t.call()
+    for what, bit in (("page", binding.DEV_BAD_PAGE), ("len", binding.DEV_BAD_LENGTHS), ("max", binding.DEV_BAD_LENGTHS)):
+        table, kv = t.table.copy(), list(t.kv_lens)
+        max_kv = max(kv)
+        if what == "page":
+            table[1, 40] = t.cache.shape[0]
+        elif what == "len":
+            kv[1] = 1
+        else:
+            max_kv = 3999
+        out = torch.full_like(good, 9.0)
+        lse = torch.full_like(good_lse, 9.0)
+        binding.latent_attention(t.q, _i32(t.cu, dev), _i32(kv, dev), _i32(table, dev), t.cache, SCALE, max_kv,
+                                 out=out, lse=lse)
+        assert binding.device_status() == bit, what
+        assert (out[1:3] == 9).all() and (lse[1:3] == 9).all(), what
+        t2 = [(0, 1), (3, 4)]
+        for a, b in t2:
+            assert torch.isfinite(out[a:b]).all() and (out[a:b].float() - good[a:b].float()).abs().max() < 0.05, what
+    for cu in ([0, 2, 1, 4], [1, 1, 3, 4], [0, 1, 3, 5]):
+        out = torch.full_like(good, 9.0)
+        binding.latent_attention(t.q, _i32(cu, dev), _i32(t.kv_lens, dev), _i32(t.table, dev), t.cache, SCALE, 4000,
+                                 out=out)
+        assert binding.device_status() == binding.DEV_BAD_LENGTHS, cu
+        assert (out == 9).all(), cu
+
+
+@pytest.mark.gpu
+def test_absorbed_pages_beyond_four_gigabytes(dev):
+    """Rows whose byte and element offsets pass 32 bits."""
+    P, rows = 64, 4_200_000
+    pages = rows // P
+    cache = torch.empty((pages, P, 576), dtype=torch.bfloat16, device=dev)
+    t = Paged(dev, "bf16", 512, 16, P, [1], [500])
+    n = -(-500 // P)
+    table = t.table.copy()
+    for k in range(n):
+        cache[pages - 1 - 3 * k] = t.cache[int(t.table[0, k])]
+        table[0, k] = pages - 1 - 3 * k
+    a = t.call()
+    t.cache, t.table = cache, table
+    b = t.call()
+    assert binding.device_status() == 0
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    got = binding.latent_gather(cache, _i32(table, dev), _i32([0, 500], dev), 500)
+    assert torch.equal(got, torch.cat([cache[int(p)] for p in table[0, :n]])[:500])
+
+
+class Packed:
+    """Packed chunks with expanded keys; NaN between and behind what belongs to them."""
+
+    def __init__(self, dev, dtype, H, q_lens, kv_lens, seed=0, strided=True, pad=0):
+        g = np.random.default_rng(seed)
+        r = lambda *s: torch.from_numpy(g.standard_normal(s).astype(np.float32)).to(dev, TYPES[dtype])
+        self.dev, self.dtype, self.H, self.q_lens, self.kv_lens = dev, dtype, H, list(q_lens), list(kv_lens)
+        self.cu_q, self.cu_k = _cum(q_lens), _cum(kv_lens)
+        self.Tq, self.Tk = int(self.cu_q[-1]) + pad, int(self.cu_k[-1]) + pad
+        self.q = r(self.Tq, H, 192)
+        if strided:
+            up = r(self.Tk, H, 256)
+            self.kn, self.v, self.kr = up[..., :128], up[..., 128:], r(self.Tk, 576)[:, 512:]
+        else:
+            self.kn, self.v, self.kr = r(self.Tk, H, 128), r(self.Tk, H, 128), r(self.Tk, 64)
+        if pad:
+            for x in (self.kn, self.v, self.kr):
+                x[self.Tk - pad:] = float("nan")
+
+    def call(self, **kw):
+        return binding.latent_prefill(self.q, _i32(self.cu_q, self.dev), self.kn, self.v, self.kr,
+                                      _i32(self.cu_k, self.dev), SCALE, **kw)
+
+    def check(self, out, lse, only=None):
+        out, lse, q, kn, v, kr = (_host(x) for x in (out, lse, self.q, self.kn, self.v, self.kr))
+        for b, (n, L) in enumerate(zip(self.q_lens, self.kv_lens)):
+            if n == 0 or (only is not None and b not in only):
+                continue
+            a, k = slice(int(self.cu_q[b]), int(self.cu_q[b]) + n), slice(int(self.cu_k[b]), int(self.cu_k[b]) + L)
+            o, l, spread = O.attend_expanded(q[a], kn[k], v[k], kr[k], SCALE)
+            tol, tol_lse = _bounds(self.dtype, 192, L, o, l, spread, np.abs(v[k]).max())
+            bad = np.abs(out[a] - o) > tol
+            assert not bad.any(), (b, np.argwhere(bad)[:4], np.abs(out[a] - o).max())
+            assert (np.abs(lse[a] - l) <= tol_lse).all(), (b, np.abs(lse[a] - l).max())
+
+
+EXPANDED = [
+    # dtype, heads, q_lens, kv_lens
+    ("bf16", 1, [1], [1]),
+    ("f16", 2, [1, 1], [1, 200]),
+    ("bf16", 2, [127, 128, 129], [127, 128, 129]),
+    ("f16", 1, [255, 256, 257], [255, 256, 257]),
+    ("bf16", 3, [5, 0, 60], [300, 40, 61]),
+    ("f16", 2, [300, 17], [700, 145]),
+    ("bf16", 1, [600], [1111]),
+    ("bf16", 5, [130, 1, 2], [258, 385, 128]),
+    ("f16", 16, [33], [95]),
+    ("bf16", 1, [k % 5 for k in range(40)], [k % 5 + 3 * k for k in range(40)]),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("strided", [True, False])
+@pytest.mark.parametrize("case", EXPANDED, ids=lambda c: f"{c[0]}-h{c[1]}-n{len(c[2])}-q{max(c[2])}-k{max(c[3])}")
+def test_expanded_matches_the_oracle(dev, case, strided):
+    t = Packed(dev, *case, strided=strided)
+    out, lse = t.call()
+    assert binding.device_status() == 0
+    t.check(out, lse)
+
+
+@pytest.mark.gpu
+def test_expanded_other_rows_never_reach_a_row(dev):
+    """NaN in another sequence's keys and values, and behind the last one, stays there."""
+    t = Packed(dev, "bf16", 2, [40, 50, 30], [100, 50, 77], pad=9)
+    for x in (t.kn, t.v, t.kr):
+        x[100:150] = float("nan")
+    out = torch.full((t.Tq, 2, 128), 5.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((t.Tq, 2), 5.0, device=dev)
+    t.call(out=out, lse=lse)
+    assert binding.device_status() == 0
+    t.check(out, lse, only=(0, 2))
+    assert (out[120:] == 5).all() and (lse[120:] == 5).all()
+    assert torch.isnan(out[40:90]).all()
+
+
+@pytest.mark.gpu
+def test_expanded_bad_lengths(dev):
+    t = Packed(dev, "bf16", 2, [40, 50, 30], [100, 50, 77])
+    good, _ = t.call()
+    out = torch.full_like(good, 9.0)
+    binding.latent_prefill(t.q, _i32(t.cu_q, dev), t.kn, t.v, t.kr, _i32([0, 100, 149, 227], dev), SCALE, out=out)
+    assert binding.device_status() == binding.DEV_BAD_LENGTHS
+    assert (out[40:90] == 9).all() and torch.equal(out[:40], good[:40]) and torch.isfinite(out[90:]).all()
+    for cq, ck in (([0, 40, 30, 120], t.cu_k), (t.cu_q, [0, 100, 90, 227]), ([0, 40, 90, 121], t.cu_k),
+                   (t.cu_q, [0, 100, 150, 228]), ([1, 40, 90, 120], t.cu_k), (t.cu_q, [2, 100, 150, 227])):
+        out = torch.full_like(good, 9.0)
+        binding.latent_prefill(t.q, _i32(cq, dev), t.kn, t.v, t.kr, _i32(ck, dev), SCALE, out=out)
+        assert binding.device_status() == binding.DEV_BAD_LENGTHS, (cq, ck)
+        assert (out == 9).all(), (cq, ck)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,ld,T,H,P", [("bf16", 512, 1, 1, 1), ("f16", 512, 33, 16, 16), ("bf16", 256, 70, 3, 24),
+                                            ("f16", 256, 9, 128, 64)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_append_matches_the_oracle(dev, dtype, ld, T, H, P, in_place):
+    """Rows land in their slots and nowhere else; rotated values are within half
+    a step of the exact rotation (fp32 angles and products add 2^-22 of the pair)."""
+    g = np.random.default_rng(T)
+    r = lambda *s: torch.from_numpy(g.standard_normal(s).astype(np.float32)).to(dev, TYPES[dtype])
+    pages = -(-2 * T // P) + 1
+    cache = r(pages, P, ld + 64)
+    slots = g.permutation(pages * P)[:T].astype(np.int64)
+    slots[::7] = -1
+    pos = g.integers(0, 5000, T).astype(np.int32)
+    table = torch.from_numpy(binding.rope_table(10000.0, 64, 5000)).to(dev)
+    c, kr, wide = r(T, ld), r(T, ld + 64)[:, ld:], r(T, H, 192)
+    q = wide[..., 128:]
+    before = wide.clone()
+    want = O.append(_host(cache), _host(c), _host(kr), pos, slots, 10000.0)
+    want_q = apply_rope(_host(q), pos, 10000.0)
+    big = r(T, H, ld + 64)
+    kept = big.clone()
+    q_out = q if in_place else big[..., ld:]
+    got = binding.latent_append(c, kr, torch.from_numpy(pos).to(dev), table, torch.from_numpy(slots).to(dev), cache,
+                                q_rope=q, q_out=q_out)
+    assert binding.device_status() == 0 and got is q_out
+    u = HALF_STEP[dtype]
+    pair = lambda x: np.abs(x[..., :32]) + np.abs(x[..., 32:])
+    near = lambda a, b: (np.abs(a - b) <= u * np.abs(b) + 2.0 ** -22 * np.concatenate([pair(b)] * 2, -1) + 2.0 ** -25).all()
+    assert np.array_equal(_host(cache)[..., :ld], want[..., :ld])
+    assert near(_host(cache)[..., ld:], want[..., ld:]) and near(_host(q_out), want_q)
+    if in_place:
+        assert torch.equal(wide[..., :128], before[..., :128])
+    else:
+        assert torch.equal(wide, before) and torch.equal(big[..., :ld], kept[..., :ld])
+
+
+@pytest.mark.gpu
+def test_append_without_queries_and_bad_tokens(dev):
+    cache = torch.zeros((4, 8, 320), dtype=torch.float16, device=dev)
+    c, kr = torch.ones((3, 256), dtype=torch.float16, device=dev), torch.ones((3, 64), dtype=torch.float16, device=dev)
+    q = torch.full((3, 2, 64), 3.0, dtype=torch.float16, device=dev)
+    table = torch.from_numpy(binding.rope_table(10000.0, 64, 16)).to(dev)
+    i64 = lambda *a: torch.tensor(a, dtype=torch.int64, device=dev)
+    assert binding.latent_append(c, kr, _i32([0, 0, 0], dev), table, i64(31, -1, 0), cache) is None
+    assert binding.device_status() == 0
+    rows = cache.view(32, 320)
+    assert (rows[[0, 31]] == 1).all() and rows.count_nonzero() == 640
+    out = torch.full_like(q, 7.0)
+    cache.zero_()
+    binding.latent_append(c, kr, _i32([16, 0, -1], dev), table, i64(1, 32, 2), cache, q_rope=q, q_out=out)
+    assert binding.device_status() == binding.DEV_BAD_SLOT | binding.DEV_BAD_POSITION
+    assert cache.count_nonzero() == 0 and (out[[0, 2]] == 7).all() and (out[1] == 3).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,ld,P,lens", [("bf16", 512, 1, [1]), ("f16", 512, 64, [64, 0, 65, 1000, 0]),
+                                             ("bf16", 256, 24, [0, 23, 24, 25, 500]), ("f16", 256, 100, [7] * 70)])
+def test_gather_is_bit_exact(dev, dtype, ld, P, lens):
+    t = Paged(dev, dtype, ld, 1, P, [0] * len(lens), lens)
+    cu = _cum(lens)
+    n = int(cu[-1])
+    out = torch.full((n + 5, ld + 64), 4.0, dtype=TYPES[dtype], device=dev)
+    binding.latent_gather(t.cache, _i32(t.table, dev), _i32(cu, dev), n + 5, out=out)
+    assert binding.device_status() == 0
+    cache = _host(t.cache)
+    want = np.concatenate([O.gather_sequence(cache, t.table[b], L) for b, L in enumerate(lens)])
+    assert np.array_equal(_host(out[:n]), want) and (out[n:] == 4).all()
+
+
+@pytest.mark.gpu
+def test_gather_bad_data(dev):
+    t = Paged(dev, "bf16", 256, 1, 8, [0, 0], [20, 20])
+    good = binding.latent_gather(t.cache, _i32(t.table, dev), _i32([0, 20, 40], dev), 40)
+    table = t.table.copy()
+    table[0, 1] = -1
+    out = torch.full_like(good, 4.0)
+    binding.latent_gather(t.cache, _i32(table, dev), _i32([0, 20, 40], dev), 40, out=out)
+    assert binding.device_status() == binding.DEV_BAD_PAGE
+    assert (out[8:16] == 4).all() and torch.equal(out[:8], good[:8]) and torch.equal(out[16:], good[16:])
+    for cu in ([0, 30, 20], [1, 20, 40], [0, 20, 41]):
+        out = torch.full_like(good, 4.0)
+        binding.latent_gather(t.cache, _i32(t.table, dev), _i32(cu, dev), 40, out=out)
+        assert binding.device_status() == binding.DEV_BAD_LENGTHS and (out == 4).all(), cu
+    out = torch.full((60, 320), 4.0, dtype=torch.bfloat16, device=dev)     # 40 rows from a table of 4 pages of 8
+    binding.latent_gather(t.cache, _i32(t.table, dev), _i32([0, 40, 60], dev), 60, out=out)
+    assert binding.device_status() == binding.DEV_BAD_LENGTHS
+    assert (out[:40] == 4).all() and torch.equal(out[40:], good[20:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,ld,H,P", [("bf16", 512, 16, 64), ("f16", 256, 5, 24)])
+def test_a_tick_through_both_forms(dev, dtype, ld, H, P):
+    """A tick as a server runs it: new tokens appended (keys and queries rotated),
+    a chunk through gather, up-projection and the expanded form, a decode row
+    through the absorbed form, both against one computation in 64 bits."""
+    g = np.random.default_rng(7)
+    r = lambda *s, k=1.0: torch.from_numpy((k * g.standard_normal(s)).astype(np.float32)).to(dev, TYPES[dtype])
+    kv, ql = [90, 200], [1, 70]                          # packed: the decode row first
+    need = [-(-L // P) for L in kv]
+    perm = g.permutation(sum(need) + 2)
+    pages = [list(map(int, perm[:need[0]])), list(map(int, perm[need[0]:sum(need)]))]
+    pk = binding.pack_tick(ql, kv, pages, P, sum(need) + 2)
+    T = sum(ql)
+    cache = r(sum(need) + 2, P, ld + 64)
+    c, kr, q = r(T, ld), r(T, 64), r(T, H, 192)
+    wk, wv = r(H, ld, 128, k=ld ** -0.5), r(H, ld, 128, k=ld ** -0.5)
+    table = torch.from_numpy(binding.rope_table(10000.0, 64, 256)).to(dev)
+    pos = binding.tick_positions(pk["cu_seqlens_q"], pk["kv_lens"])
+    rows64 = O.append(_host(cache), _host(c), _host(kr), pos, pk["slot_mapping"], 10000.0)
+    q64 = _host(q)
+    q64[..., 128:] = apply_rope(q64[..., 128:], pos, 10000.0)
+
+    binding.latent_append(c, kr, _i32(pos, dev), table, torch.from_numpy(pk["slot_mapping"]).to(dev), cache,
+                          q_rope=q[..., 128:], q_out=q[..., 128:])
+    # the chunk: gather, up-project, expanded attention
+    rows = binding.latent_gather(cache, _i32(pk["page_tables"][1:], dev), _i32([0, kv[1]], dev), kv[1])
+    up = torch.einsum("lc,hcd->lhd", rows[:, :ld], torch.cat([wk, wv], -1))
+    e, _ = binding.latent_prefill(q[1:].contiguous(), _i32([0, ql[1]], dev), up[..., :128], up[..., 128:],
+                                  rows[:, ld:], _i32([0, kv[1]], dev), SCALE)
+    # the decode row: absorb, attend the pages, project the values
+    qa = torch.cat([torch.einsum("nhd,hcd->nhc", q[:1, :, :128], wk), q[:1, :, 128:]], -1).contiguous()
+    a, _ = binding.latent_attention(qa, _i32([0, 1], dev), _i32(kv[:1], dev), _i32(pk["page_tables"][:1], dev), cache,
+                                    SCALE, kv[0])
+    a = torch.einsum("nhc,hcd->nhd", a, wv)
+    assert binding.device_status() == 0
+    wk64, wv64 = _host(wk), _host(wv)
+    got = np.concatenate([_host(a), _host(e)])
+    for b, at in ((0, slice(0, 1)), (1, slice(1, T))):
+        full = O.gather_sequence(rows64, pk["page_tables"][b], kv[b])
+        kn, v = (np.einsum("lc,hcd->lhd", full[:, :ld], w) for w in (wk64, wv64))
+        want, _, (mass, dot) = O.attend_expanded(q64[at], kn, v, full[:, ld:], SCALE)
+        # Scores: the queries' and keys' rotary parts, the up-projected keys (or the
+        # absorbed queries) are each rounded to u, so a score is off by 2 u of its
+        # absolute dot product (in the absorbed form of the wider one, which the
+        # up-projection of |q| and |c| bounds); values and outputs: three more roundings.
+        wide = np.einsum("nhd,hcd->nhc", np.abs(q64[at][..., :128]), np.abs(wk64))
+        dot = np.maximum(dot, SCALE * np.einsum("nhc,c->nh", wide, np.abs(full[:, :ld]).max(0)))
+        u = HALF_STEP[dtype]
+        vmass = np.einsum("c,hcd->hd", np.abs(full[:, :ld]).max(0), np.abs(wv64))
+        assert (np.abs(got[at] - want) <= u * (4 * dot[..., None] * mass + 3 * vmass)).all(), b
+
+
+@pytest.mark.gpu
+def test_graphs_replay_with_new_lengths_and_side_by_side(dev):
+    """One captured decode tick serves new lengths and tables; two captured graphs
+    with a workspace each give their results when replayed on two streams at once."""
+    big = Paged(dev, "bf16", 512, 16, 64, [1, 1, 1], [900, 2000, 333])
+    other = Paged(dev, "bf16", 512, 128, 64, [1, 1], [1500, 4000], seed=5)
+    chunk = Packed(dev, "bf16", 4, [200, 30], [300, 200], seed=6)
+
+    def captured(fn):
+        fn()
+        torch.cuda.synchronize()
+        s, gr = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=s):
+            got = fn()
+        return gr, got, s
+
+    kv, tab, cu = _i32(big.kv_lens, dev), _i32(big.table, dev), _i32(big.cu, dev)
+    ws = binding.alloc_latent_workspace(3, 3, 16, big.cache)
+    out, lse = torch.empty((3, 16, 512), dtype=torch.bfloat16, device=dev), torch.empty((3, 16), device=dev)
+    g1, _, s1 = captured(lambda: binding.latent_attention(big.q, cu, kv, tab, big.cache, SCALE, 4096, out=out, lse=lse,
+                                                          workspace=ws))
+    o_cu, o_kv, o_tab = _i32(other.cu, dev), _i32(other.kv_lens, dev), _i32(other.table, dev)
+    g2, got2, s2 = captured(lambda: binding.latent_attention(other.q, o_cu, o_kv, o_tab, other.cache, SCALE, 4096))
+    c_q, c_k = _i32(chunk.cu_q, dev), _i32(chunk.cu_k, dev)
+    g3, got3, s3 = captured(lambda: binding.latent_prefill(chunk.q, c_q, chunk.kn, chunk.v, chunk.kr, c_k, SCALE))
+    for lens in ([900, 2000, 333], [1, 64, 65], [899, 1999, 2]):
+        kv.copy_(_i32(lens, dev))
+        out.fill_(9)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for gr, s in ((g1, s1), (g2, s2), (g3, s3)):
+                with torch.cuda.stream(s):
+                    gr.replay()
+        torch.cuda.synchronize()
+        assert binding.device_status() == 0
+        big.kv_lens = lens
+        big.check(out, lse)
+    other.check(*got2)
+    chunk.check(*got3)
+
+
+@pytest.mark.gpu
+def test_calls_on_a_stream_argument(dev):
+    t = Paged(dev, "bf16", 512, 16, 64, [1], [700])
+    c = Packed(dev, "f16", 2, [50], [90])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a = t.call(stream=s)
+    b = c.call(stream=s)
+    s.synchronize()
+    t.check(*a)
+    c.check(*b)
