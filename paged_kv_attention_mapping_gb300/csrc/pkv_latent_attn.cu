@@ -2,101 +2,869 @@
 // sequence b, head h) with query q, and cached rows x_j = [c_j, r_j],
 //   s_j = scale q . x_j,  j <= kv_len - q_len + i,
 //   out = sum_j exp(s_j - m) c_j / sum_j exp(s_j - m),  lse = m + ln(sum).
-// One warp per row, one pass over the keys with the running maximum and sum.
+//
+// All heads of a token read the same rows, so (token, head) rows are the M side
+// of a matrix product and a cached row is read once for 128 of them. A work tile
+// is 128 consecutive (token, head) rows of one sequence, and a pair of CTAs
+// (tcgen05 cta_group::2) computes it in steps of 128 keys:
+//   S = Q X^T          M 128 (64 rows a CTA), N 128 keys, K = LD + 64
+//   O += P X[:, :LD]   M 128, N = LD as one or two products of 256, K 128 keys
+// O takes LD / 2 TMEM columns of each CTA, two S buffers 64 columns each. One CTA
+// alone could not do it: O of 128 rows x 512 fp32 is all the TMEM that an SM has.
+//
+// The product S wants half of the keys in each CTA, O wants half of the latent
+// columns of all keys, and one instruction names the same shared-memory offsets in
+// both CTAs, so the two operands cannot share storage: keys are loaded for S
+// (K ring), and again, from L2, for O (V buffers). HBM reads each row once.
+//
+//   warp 0   Q and K producer (TMA; the page table gives the rows of each box)
+//   warp 1   MMA issuer (even CTA): S(j + 1) is issued before O(j), so that the
+//            tensor pipe has work while the softmax of j runs
+//   warp 2   V producer; zeroes the rows behind the sequence's end in the last tile
+//   warp 3   scheduler: the segments of this pair
+//   warps 4-7  softmax. Lane l of TMEM holds row l & 63, keys (or output columns)
+//            of half l / 64; the halves exchange row maxima through shared memory.
+//            P goes to shared memory in the cache type, O is rescaled in TMEM only
+//            when a row's maximum grows by more than 2^8.
+//
+// Work split: the tick's steps (all tiles, one after the other) are cut into
+// equal runs, one per pair. A tile cut by a run's end leaves partial results
+// (normalised output in fp32 and log2 sum) that latent_combine_kernel joins.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
+#include "pkv_sm100.cuh"
 
 namespace pkv {
+using namespace sm100;
+
 namespace {
+
+constexpr int BM = 128;          // (token, head) rows of a tile
+constexpr int HM = 64;           // rows of one CTA
+constexpr int BN = 128;          // keys of a step
+constexpr int MAX_PAIRS = 76;    // 152 SMs; the workspace is laid out for these
+constexpr int NTHREADS = 256;
+constexpr uint32_t UNIT = 8192;  // 64 rows x 64 columns of 16 bits: one swizzle atom wide
+constexpr float RESCALE_LOG2 = 8.f;
+
+template <int LD>
+struct Cfg {
+  static constexpr int CH = LD / 64 + 1;         // 64-column chunks of a row, the rotary one last
+  static constexpr int GU = LD == 512 ? 3 : 5;   // chunks of a K group (one barrier)
+  static constexpr int TG = CH / GU;             // groups of a step
+  static constexpr int NG = 3;                   // groups of the K ring
+  static constexpr int NH = LD / 256;            // products of 256 output columns
+  static constexpr uint32_t Q_BYTES = CH * UNIT;
+  static constexpr uint32_t G_BYTES = GU * UNIT;
+  static constexpr uint32_t V_BYTES = 4 * UNIT;  // 2 chunks x 128 keys: this CTA's part of one product
+  static constexpr uint32_t P_BYTES = 2 * UNIT;
+  static constexpr uint32_t SMEM = Q_BYTES + NG * G_BYTES + NH * V_BYTES + P_BYTES + 1024;
+  static_assert(CH % GU == 0 && SMEM <= 231424, "shared memory");
+};
+
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t S_COL = 256;
+
+// Workspace: a record per pair (the tile that the pair's run cuts at its end),
+// then a bad flag, log2 sums and outputs for two partial results per pair.
+struct Record {
+  int32_t parts, row0, nrows, pad;   // parts 0: no cut tile
+};
+struct Layout {
+  static constexpr size_t rec = 0;
+  static constexpr size_t bad = 2048;
+  static constexpr size_t lse = 4096;
+  static constexpr size_t o = lse + (size_t)2 * MAX_PAIRS * BM * 4;
+  static size_t total(int LD) { return o + (size_t)2 * MAX_PAIRS * BM * LD * 4; }
+};
+static_assert(sizeof(Record) * MAX_PAIRS <= 2048 && 2 * MAX_PAIRS * 4 <= 2048 && Layout::o % 256 == 0, "layout");
 
 struct AttnP {
   const int32_t *cu, *kv_lens, *page_tables;
-  int32_t B, T, H, P, num_pages, max_pages, max_kv_len;
-  float scale_log2;
+  int32_t B, T, H, P, box, num_pages, max_pages, max_kv_len, table_cap;
+  float scale_log2;   // > 0
+  void* out;
   float* lse;
+  char* ws;
   int32_t* dev_status;
 };
 
-template <int LD, typename T>
-__global__ void __launch_bounds__(256) latent_rows_kernel(const T* __restrict__ q, const T* __restrict__ cache,
-                                                          T* __restrict__ out, AttnP p) {
-  constexpr int D = LD + 64, NC = LD / 32;
-  bool bad = threadIdx.x == 0 && __ldg(p.cu) != 0;
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) bad |= __ldg(p.cu + b + 1) < __ldg(p.cu + b);
-  const int n = __ldg(p.cu + p.B);
-  bad |= n > p.T;
-  if (__syncthreads_or(bad)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.dev_status, PKV_DEV_BAD_LENGTHS);
-    return;
+// A run of steps [j0, j1) of one tile.
+struct Segment {
+  int valid, b, L, base;      // base: keys before the sequence's first new token
+  int row0, frow0, nrows;     // first packed row, first row within the sequence, rows
+  int j0, j1, n;              // n: steps of the whole tile
+  int parts;                  // > 0: the cut tile starts here; pairs that share it
+};
+
+// One sequence's tiles. Tile t covers rows [128 t, 128 t + 128) of its q_len * H
+// and needs the keys up to its last row's position.
+struct Seq {
+  int q, L, base, H, rows, tiles;
+  __device__ __forceinline__ int steps(int t) const {
+    const int last = (min((t + 1) * BM, rows) - 1) / H;
+    return (base + last + BN) / BN;
   }
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-  const int64_t t = row / p.H;
-  if (t >= n) return;
-  int lo = 0, hi = p.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.cu + mid) <= t) lo = mid; else hi = mid - 1;
+  // tiles with at most v steps (steps() never falls from one tile to the next)
+  __device__ __forceinline__ int tiles_within(int v) const {
+    const int64_t e = (int64_t)v * BN - base;   // tokens that see at most v * BN keys
+    if (e >= q) return tiles;
+    if (e <= 0) return 0;
+    return min(tiles - 1, (int)(e * H / BM));
   }
-  const int c0 = __ldg(p.cu + lo), qlen = __ldg(p.cu + lo + 1) - c0, L = __ldg(p.kv_lens + lo);
-  if (L < qlen || L < 1 || L > p.max_kv_len || L > (int64_t)p.max_pages * p.P) {
-    if (lane == 0) atomicOr(p.dev_status, PKV_DEV_BAD_LENGTHS);
-    return;
+  __device__ __forceinline__ int64_t total() const {
+    if (tiles == 0) return 0;
+    if (tiles == 1) return (L + BN - 1) / BN;
+    const int lo = steps(0), hi = steps(tiles - 1);
+    int64_t s = (int64_t)hi * tiles;
+    for (int v = lo; v < hi; ++v) s -= tiles_within(v);
+    return s;
   }
-  const int keys = L - qlen + (int)(t - c0) + 1;
-  const int32_t* pt = p.page_tables + (int64_t)lo * p.max_pages;
-  for (int k = 0; k * (int64_t)p.P < keys; ++k) {
-    const int id = __ldg(pt + k);
-    if (id < 0 || id >= p.num_pages) {
-      if (lane == 0) atomicOr(p.dev_status, PKV_DEV_BAD_PAGE);
-      return;
+  // tile and step of the sequence's step number `at`
+  __device__ __forceinline__ void seek(int64_t at, int* tile, int* step) const {
+    const int lo = steps(0), hi = steps(tiles - 1);
+    int before = 0;
+    for (int v = lo; v <= hi; ++v) {
+      const int upto = v == hi ? tiles : tiles_within(v);
+      const int64_t s = (int64_t)(upto - before) * v;
+      if (at < s) {
+        *tile = before + (int)(at / v);
+        *step = (int)(at % v);
+        return;
+      }
+      at -= s;
+      before = upto;
     }
   }
-  float qc[NC], qr[2], o[NC];
-#pragma unroll
-  for (int k = 0; k < NC; ++k) {
-    qc[k] = to_f32(q[row * D + k * 32 + lane]);
-    o[k] = 0.f;
+};
+
+__device__ __forceinline__ Seq load_seq(const AttnP& p, int b, bool report) {
+  Seq s;
+  const int c0 = __ldg(p.cu + b);
+  s.q = __ldg(p.cu + b + 1) - c0;
+  s.L = __ldg(p.kv_lens + b);
+  s.H = p.H;
+  s.base = s.L - s.q;
+  s.rows = s.q * p.H;
+  s.tiles = (s.rows + BM - 1) / BM;
+  if (s.q > 0 && (s.L < s.q || s.L > p.max_kv_len || s.L > p.table_cap)) {
+    if (report) atomicOr(p.dev_status, PKV_DEV_BAD_LENGTHS);
+    s.tiles = 0;
   }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) qr[k] = to_f32(q[row * D + LD + k * 32 + lane]);
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < keys; ++j) {
-    const T* x = cache + ((int64_t)__ldg(pt + j / p.P) * p.P + j % p.P) * D;
-    float xc[NC], dot = 0.f;
-#pragma unroll
-    for (int k = 0; k < NC; ++k) {
-      xc[k] = to_f32(x[k * 32 + lane]);
-      dot += qc[k] * xc[k];
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) dot += qr[k] * to_f32(x[LD + k * 32 + lane]);
-    const float sc = warp_sum(dot) * p.scale_log2;
-    const float mn = fmaxf(m, sc), w = exp2f(sc - mn), f = exp2f(m - mn);
-    l = l * f + w;
-#pragma unroll
-    for (int k = 0; k < NC; ++k) o[k] = o[k] * f + w * xc[k];
-    m = mn;
+  if (s.q <= 0 || s.q > p.T) s.tiles = 0;
+  return s;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+  } else {
+    __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
   }
-  const float inv = 1.f / l;
-#pragma unroll
-  for (int k = 0; k < NC; ++k) out[row * LD + k * 32 + lane] = from_f32<T>(o[k] * inv);
-  if (p.lse && lane == 0) p.lse[row] = (m + log2f(l)) * LN2;
+}
+
+__device__ __forceinline__ void st_global_32B(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void pair_bar_sync(int id) {
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ void pair_bar_arrive(int id) {
+  asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
 }
 
 template <int LD, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
+    latent_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mx, AttnP p) {
+  using C = Cfg<LD>;
+  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int NSEG = 4;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char* sQ = sm;
+  unsigned char* sK = sQ + C::Q_BYTES;
+  unsigned char* sV = sK + C::NG * C::G_BYTES;
+  unsigned char* sP = sV + C::NH * C::V_BYTES;
+
+  // full barriers and bar_p live in the even CTA (both CTAs arrive there); the
+  // others are signalled in both CTAs by the MMA commits
+  __shared__ __align__(8) uint64_t bar_q, bar_qempty, bar_k[C::NG], bar_kempty[C::NG], bar_v[C::NH],
+      bar_vempty[C::NH], bar_vtail[C::NH], bar_s[2], bar_p, bar_o, bar_seg[NSEG], bar_segempty[NSEG], bar_drain;
+  __shared__ uint32_t s_tmem;
+  __shared__ Segment s_seg[NSEG];
+  __shared__ int s_bad[NSEG];
+  __shared__ volatile int s_abort;
+  __shared__ float s_x[2][2][HM];      // row figures of the two halves, by step parity
+  __shared__ int64_t s_scan[NTHREADS / 32];
+  __shared__ int64_t s_run, s_each;    // steps of this pair's run, and of every pair's but the last
+  __shared__ int s_b0, s_tile0, s_step0;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (tid == 0) {
+    mbar_init(&bar_q, 2);
+    mbar_init(&bar_qempty, 1);
+    for (int g = 0; g < C::NG; ++g) {
+      mbar_init(&bar_k[g], 2);
+      mbar_init(&bar_kempty[g], 1);
+    }
+    for (int i = 0; i < C::NH; ++i) {
+      mbar_init(&bar_v[i], 2);
+      mbar_init(&bar_vempty[i], 1);
+      mbar_init(&bar_vtail[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&bar_s[i], 1);
+    mbar_init(&bar_p, 8);        // the four softmax warps of both CTAs
+    mbar_init(&bar_o, 1);
+    for (int e = 0; e < NSEG; ++e) {
+      mbar_init(&bar_seg[e], 1);
+      mbar_init(&bar_segempty[e], rank == 0 ? 7 : 6);   // producers, MMA issuer, softmax warps
+    }
+    mbar_init(&bar_drain, 1);
+    fence_mbar_init();
+    s_abort = 0;
+    s_run = 0;
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mx);
+  }
+  if (warp == 1) tmem_alloc_pair(&s_tmem, TMEM_COLS);
+
+  // ------------------------------------------------------------------- plan
+  // Every CTA computes the whole tick's step count and where its own run starts
+  // (reads only the lengths, so this runs before the wait for the kernel before).
+  {
+    bool bad = tid == 0 && __ldg(p.cu) != 0;
+    const int per = (p.B + NTHREADS - 1) / NTHREADS;
+    const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
+    int64_t mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const Seq s = load_seq(p, b, blockIdx.x == 0);
+      bad |= s.q < 0;
+      mine += s.total();
+    }
+    bad |= __ldg(p.cu + p.B) > p.T;
+    int64_t scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += y;
+    }
+    if (lane == 31) s_scan[warp] = scan;
+    bad = __syncthreads_or(bad);
+    int64_t total = 0, before = scan - mine;
+#pragma unroll
+    for (int w = 0; w < NTHREADS / 32; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+    }
+    if (bad) {
+      if (blockIdx.x == 0 && tid == 0) atomicOr(p.dev_status, PKV_DEV_BAD_LENGTHS);
+      total = 0;
+    }
+    const int64_t each = (total + pairs - 1) / pairs;
+    const int64_t lo = pair * each, hi = min(lo + each, total);
+    if (lo < hi && lo >= before && lo < before + mine) {
+      int64_t at = lo - before;
+      for (int b = b_lo; b < b_hi; ++b) {
+        const Seq s = load_seq(p, b, false);
+        const int64_t n = s.total();
+        if (at < n) {
+          int tile, step;
+          s.seek(at, &tile, &step);
+          s_b0 = b;
+          s_tile0 = tile;
+          s_step0 = step;
+          break;
+        }
+        at -= n;
+      }
+      s_run = hi - lo;
+    }
+    if (tid == 0) s_each = each;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync_all();   // the peer's barriers are ready too
+  const uint32_t tmem = s_tmem;
+  // queries, cache rows and page tables may come from the kernel before
+  pdl_wait();
+  pdl_trigger();
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    bool ok = mbar_try_wait_cluster(bar, parity);
+    if (!ok) {
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t it = 0; !ok; ++it) {
+        ok = mbar_try_wait_cluster(bar, parity);
+        if (!ok && (it & 63u) == 63u) {
+          if (s_abort) break;
+          if (globaltimer_ns() - t0 > WAIT_LIMIT_NS || it > (1u << 28)) {
+            s_abort = 1;
+            atomicOr(p.dev_status, PKV_DEV_TIMEOUT);
+            break;
+          }
+        }
+      }
+    }
+    // a warp that gave up no longer takes part in the pairwise exchange, so
+    // nobody goes on once the flag is up
+    return __all_sync(0xffffffffu, ok && !s_abort);
+  };
+
+  bool ok = true;
+  if (warp == 3) {
+    // ------------------------------------------------------------- scheduler
+    Record* rec = (Record*)(p.ws + Layout::rec) + pair;
+    const int64_t each = s_each;
+    int64_t left = s_run;
+    int64_t done = 0;
+    int b = left > 0 ? s_b0 : 0, tile = left > 0 ? s_tile0 : 0, step = left > 0 ? s_step0 : 0;
+    Seq s{};
+    if (left > 0) s = load_seq(p, b, false);
+    Record r{0, 0, 0, 0};
+    for (uint32_t t = 0; ok; ++t) {
+      const uint32_t e = t % NSEG;
+      if (t >= NSEG && !(ok = wait(&bar_segempty[e], ((t / NSEG) - 1) & 1))) break;
+      Segment g;
+      g.valid = 0;
+      if (left > 0) {
+        // left > 0 promises one more tile, as long as nobody rewrites the lengths meanwhile
+        while (tile >= s.tiles && ++b < p.B) {
+          s = load_seq(p, b, false);
+          tile = 0;
+        }
+        g.valid = tile < s.tiles;
+      }
+      if (g.valid) {
+        g.b = b;
+        g.L = s.L;
+        g.base = s.base;
+        g.frow0 = tile * BM;
+        g.row0 = __ldg(p.cu + b) * p.H + tile * BM;
+        g.nrows = min(BM, s.rows - tile * BM);
+        g.n = s.steps(tile);
+        g.j0 = step;
+        g.j1 = (int)min((int64_t)g.n, step + left);
+        g.parts = 0;
+        if (g.j0 == 0 && g.j1 < g.n) {
+          // global step numbers: this run starts at pair * each
+          const int64_t end = pair * each + done + g.n;
+          g.parts = (int)((end - 1) / each) - pair + 1;
+          r.parts = g.parts;
+          r.row0 = g.row0;
+          r.nrows = g.nrows;
+        }
+        left -= g.j1 - g.j0;
+        done += g.j1 - g.j0;
+        ++tile;
+        step = 0;
+      }
+      if (lane == 0) {
+        s_seg[e] = g;
+        s_bad[e] = 0;
+        mbar_arrive(&bar_seg[e]);
+      }
+      __syncwarp();
+      if (!g.valid) break;
+    }
+    if (rank == 0 && lane == 0) *rec = r;
+  } else if (warp == 0) {
+    // -------------------------------------------------------- Q and K producer
+    const uint32_t q_bar = map_to_rank(&bar_q, 0);
+    uint32_t ring = 0;      // K groups before the current one
+    const int boxes = HM / p.box;   // boxes of this CTA's 64 keys; lane l takes boxes l and l + 32
+    for (uint32_t t = 0; ok; ++t) {
+      const uint32_t e = t % NSEG;
+      if (!(ok = wait(&bar_seg[e], (t / NSEG) & 1))) break;
+      const Segment g = s_seg[e];
+      if (!g.valid) break;
+      if (t >= 1 && !(ok = wait(&bar_qempty, (t - 1) & 1))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx_cluster(q_bar, C::Q_BYTES);
+#pragma unroll
+        for (int c = 0; c < C::CH; ++c) tma_load_2d_pair(sQ + c * UNIT, &mq, q_bar, c * 64, g.row0 + (int)rank * HM);
+      }
+      const int32_t* pt = p.page_tables + (int64_t)g.b * p.max_pages;
+      // row in the pool of the first key of box i of step j; rows behind the
+      // end and bad pages are read from page 0 (masked, or discarded)
+      auto box_row = [&](int j, int i) {
+        const int key = j * BN + (int)rank * HM + i * p.box;
+        if (i >= boxes || key >= g.L) return 0;
+        const int lp = key / p.P;
+        const int id = __ldg(pt + lp);
+        return id < 0 || id >= p.num_pages ? 0 : id * p.P + (key - lp * p.P);
+      };
+      int row[2] = {box_row(g.j0, lane), box_row(g.j0, lane + 32)};
+      for (int j = g.j0; j < g.j1 && ok; ++j) {
+        const int cur[2] = {row[0], row[1]};
+        if (j + 1 < g.j1) {
+          row[0] = box_row(j + 1, lane);
+          row[1] = box_row(j + 1, lane + 32);
+        }
+        for (int k = 0; k < C::TG; ++k, ++ring) {
+          const uint32_t slot = ring % C::NG, round = ring / C::NG;
+          if (!(ok = wait(&bar_kempty[slot], (round & 1) ^ 1))) break;
+          const uint32_t bar = map_to_rank(&bar_k[slot], 0);
+          if (lane == 0) mbar_arrive_expect_tx_cluster(bar, C::G_BYTES);
+          __syncwarp();
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int i = lane + w * 32;
+            if (i < boxes)
+#pragma unroll
+              for (int u = 0; u < C::GU; ++u)
+                tma_load_2d_pair(sK + slot * C::G_BYTES + u * UNIT + i * p.box * 128, &mx, bar, (k * C::GU + u) * 64,
+                                 cur[w]);
+          }
+          __syncwarp();
+        }
+      }
+      if (ok && lane == 0) mbar_arrive(&bar_segempty[e]);
+      __syncwarp();
+    }
+  } else if (warp == 2) {
+    // -------------------------------------------------------------- V producer
+    uint32_t n_load = 0;            // steps before the current one
+    uint32_t n_tail = 0;            // tail steps before the current one
+    const int boxes = BN / p.box;   // lane l takes boxes l, l + 32, l + 64, l + 96
+    for (uint32_t t = 0; ok; ++t) {
+      const uint32_t e = t % NSEG;
+      if (!(ok = wait(&bar_seg[e], (t / NSEG) & 1))) break;
+      const Segment g = s_seg[e];
+      if (!g.valid) break;
+      const int32_t* pt = p.page_tables + (int64_t)g.b * p.max_pages;
+      const int keys = min(g.L, g.n * BN);   // keys that the tile needs
+      auto box_row = [&](int j, int i, bool* bad) {
+        const int key = j * BN + i * p.box;
+        if (i >= boxes || key >= keys) return 0;
+        const int lp = key / p.P;
+        const int id = __ldg(pt + lp);
+        if (id >= 0 && id < p.num_pages) return id * p.P + (key - lp * p.P);
+        *bad = true;
+        return 0;
+      };
+      bool bad = false;
+      int row[4];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) row[w] = box_row(g.j0, lane + w * 32, &bad);
+      for (int j = g.j0; j < g.j1 && ok; ++j, ++n_load) {
+        const int cur[4] = {row[0], row[1], row[2], row[3]};
+        if (bad) s_bad[e] = 1;
+        if (j + 1 < g.j1) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) row[w] = box_row(j + 1, lane + w * 32, &bad);
+        }
+        const int end = g.L - j * BN;   // rows from here on are behind the sequence
+        const bool tail = end < BN;
+#pragma unroll
+        for (int i = 0; i < C::NH; ++i) {
+          if (!(ok = wait(&bar_vempty[i], (n_load & 1) ^ 1))) break;
+          const uint32_t bar = tail ? smem_u32(&bar_vtail[i]) : map_to_rank(&bar_v[i], 0);
+          if (lane == 0) {
+            if (tail) mbar_arrive_expect_tx(&bar_vtail[i], C::V_BYTES);
+            else mbar_arrive_expect_tx_cluster(bar, C::V_BYTES);
+          }
+          __syncwarp();
+          const int col = (int)rank * (LD / 2) + i * 128;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int x = lane + w * 32;
+            if (x < boxes) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                unsigned char* dst = sV + i * C::V_BYTES + c * 2 * UNIT + x * p.box * 128;
+                if (tail) tma_load_2d(dst, &mx, &bar_vtail[i], col + c * 64, cur[w]);
+                else tma_load_2d_pair(dst, &mx, bar, col + c * 64, cur[w]);
+              }
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (tail) {
+          // 0 * NaN must not reach O from the slots behind the end
+#pragma unroll
+          for (int i = 0; i < C::NH; ++i) {
+            if (!(ok = wait(&bar_vtail[i], n_tail & 1))) break;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint4* base = (uint4*)(sV + i * C::V_BYTES + c * 2 * UNIT);
+              for (int x = end * 8 + lane; x < BN * 8; x += 32) base[x] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(&bar_v[i], 0));
+          }
+          ++n_tail;
+        }
+      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&bar_segempty[e]);
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMA issuer
+    if (rank == 0) {
+      const uint32_t id_s = idesc_f16(BM, BN, BF16, false);
+      const uint32_t id_o = idesc_f16(BM, 256, BF16, true);
+      const uint64_t qd = smem_desc(smem_u32(sQ), 16, 1024, LAYOUT_SW128);
+      const uint64_t pd = smem_desc(smem_u32(sP), 16, 1024, LAYOUT_SW128);
+      const uint64_t kd = smem_desc(smem_u32(sK), 16, 1024, LAYOUT_SW128);
+      const uint64_t vd = smem_desc(smem_u32(sV), 2 * UNIT, 1024, LAYOUT_SW128);
+      uint32_t ring = 0, n_s = 0, n_o = 0;
+      auto issue_s = [&]() -> bool {
+        const uint32_t d = tmem + S_COL + (n_s & 1) * 64;
+        for (int k = 0; k < C::TG; ++k, ++ring) {
+          const uint32_t slot = ring % C::NG;
+          if (!wait(&bar_k[slot], (ring / C::NG) & 1)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int u = 0; u < C::GU; ++u)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              mma_f16_ss_pair_warp(d, qd + (uint64_t)(((k * C::GU + u) * UNIT + x * 32) >> 4),
+                                   kd + (uint64_t)((slot * C::G_BYTES + u * UNIT + x * 32) >> 4), id_s,
+                                   (k | u | x) ? 1u : 0u);
+          mma_commit_pair_warp(&bar_kempty[slot]);
+        }
+        mma_commit_pair_warp(&bar_s[n_s & 1]);
+        ++n_s;
+        return true;
+      };
+      for (uint32_t t = 0; ok; ++t) {
+        const uint32_t e = t % NSEG;
+        if (!(ok = wait(&bar_seg[e], (t / NSEG) & 1))) break;
+        const Segment g = s_seg[e];
+        if (!g.valid) break;
+        if (!(ok = wait(&bar_q, t & 1))) break;
+        if (!(ok = issue_s())) break;
+        const int steps = g.j1 - g.j0;
+        for (int j = 0; j < steps; ++j) {
+          if (j + 1 < steps && !(ok = issue_s())) break;
+          // the last product with Q is on its way: the next segment's may follow
+          if (j + 2 == steps || steps == 1) mma_commit_pair_warp(&bar_qempty);
+          if (!(ok = wait(&bar_p, n_o & 1))) break;
+#pragma unroll
+          for (int i = 0; i < C::NH; ++i) {
+            if (!(ok = wait(&bar_v[i], n_o & 1))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < BN / 16; ++x)
+              mma_f16_ss_pair_warp(tmem + i * 128, pd + (uint64_t)(((x >> 2) * UNIT + (x & 3) * 32) >> 4),
+                                   vd + (uint64_t)((i * C::V_BYTES + x * 16 * 128) >> 4), id_o,
+                                   (j | x) ? 1u : 0u);
+            mma_commit_pair_warp(&bar_vempty[i]);
+          }
+          if (!ok) break;
+          mma_commit_pair_warp(&bar_o);
+          ++n_o;
+        }
+        if (ok && lane == 0) mbar_arrive(&bar_segempty[e]);
+        __syncwarp();
+      }
+    }
+  } else {
+    // ----------------------------------------------------------------- softmax
+    const int quarter = warp & 3, half = quarter >> 1;
+    const int i = (quarter & 1) * 32 + lane;        // row of this CTA
+    const uint32_t lrow = (uint32_t)(quarter * 32) << 16;
+    const int bar_id = 1 + (quarter & 1);           // the two warps of the same rows
+    const uint32_t p_bar = map_to_rank(&bar_p, 0);
+    unsigned char* p_row = sP + half * UNIT + i * 128;
+    const float sc = p.scale_log2;
+    uint32_t n = 0;                                  // steps before the current one
+    for (uint32_t t = 0; ok; ++t) {
+      const uint32_t e = t % NSEG;
+      if (!(ok = wait(&bar_seg[e], (t / NSEG) & 1))) break;
+      const Segment g = s_seg[e];
+      if (!g.valid) break;
+      const int r = (int)rank * HM + i;              // row of the tile
+      const int pos = min(g.base + (g.frow0 + r) / p.H, g.L - 1);
+      const int j_mask = (g.base + g.frow0 / p.H + 1) / BN;   // steps before see no hidden key
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = g.j0; j < g.j1; ++j, ++n) {
+        if (!(ok = wait(&bar_s[n & 1], (n >> 1) & 1))) break;
+        tc_fence_after();
+        uint32_t x[2][32];
+        tmem_ld32(tmem + lrow + S_COL + (n & 1) * 64, x[0]);
+        tmem_ld32(tmem + lrow + S_COL + (n & 1) * 64 + 32, x[1]);
+        tmem_wait_ld();
+        reg_fence(x[0]);
+        reg_fence(x[1]);
+        if (j >= j_mask) {
+          const int lim = pos - j * BN - half * 64;  // keys of this half up to lim are visible
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c * 32 + k > lim) x[c][k] = __float_as_uint(-INFINITY);
+        }
+        float mx[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int k = 0; k < 32; k += 2)
+            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1]));
+        const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        s_x[n & 1][half][i] = mine;
+        pair_bar_sync(bar_id);
+        const float mt = fmaxf(mine, s_x[n & 1][half ^ 1][i]) * sc;
+        const bool first = j == g.j0;
+        const bool grow = first || mt > m_run + RESCALE_LOG2;
+        const float m_new = grow ? fmaxf(mt, m_run) : m_run;
+        const float alpha = grow && !first ? ex2(m_run - m_new) : 1.f;
+        const bool rescale = !first && __any_sync(0xffffffffu, grow);
+        // a row that sees no key of this run so far has m = -inf: its weights are 0
+        const float nm = m_new == -INFINITY ? 0.f : -m_new;
+        const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
+        float2 ls[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
+        uint32_t w[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int k0 = 2 * k;
+          const float2 y = __ffma2_rn(
+              make_float2(__uint_as_float(x[k0 >> 5][k0 & 31]), __uint_as_float(x[k0 >> 5][(k0 & 31) + 1])), sc2, nm2);
+          const float a = ex2(y.x), b = ex2(y.y);
+          ls[k & 3] = __fadd2_rn(ls[k & 3], make_float2(a, b));
+          w[k] = pack2<T>(a, b);
+        }
+        // m_run = m_new = -inf before the first visible key: alpha would be NaN
+        const float f = m_new == -INFINITY ? 1.f : alpha;
+        l_run = l_run * f + (((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y)));
+        m_run = m_new;
+        // the product before has read P and written O (a segment's first step
+        // follows its predecessor's epilogue, which waited for that)
+        if (!first) {
+          if (!(ok = wait(&bar_o, (n - 1) & 1))) break;
+          tc_fence_after();
+          if (rescale) {
+#pragma unroll 1
+            for (int c = 0; c < LD / 64; ++c) {
+              uint32_t o[32];
+              tmem_ld32_wait(tmem + lrow + c * 32, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st32_wait(tmem + lrow + c * 32, o);
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(p_row + ((c ^ (i & 7)) << 4)) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_bar);
+      }
+      if (!ok) break;
+      // epilogue: the two halves' sums, then this half's LD / 2 output columns
+      s_x[n & 1][half][i] = l_run;
+      pair_bar_sync(bar_id);
+      const float l = l_run + s_x[n & 1][half ^ 1][i];
+      if (!(ok = wait(&bar_o, (n - 1) & 1))) break;
+      tc_fence_after();
+      const int bad = *(volatile int*)&s_bad[e];
+      const bool whole = g.j0 == 0 && g.j1 == g.n;
+      const bool store = r < g.nrows && !(whole && bad);
+      const int slot = 2 * pair + (g.j0 == 0 ? 1 : 0);
+      const float inv = m_run == -INFINITY ? 0.f : 1.f / l;   // no visible key in a partial run: zeros
+      const int64_t row = (int64_t)g.row0 + r;
+      T* dst = (T*)p.out + row * LD + half * (LD / 2);
+      float* part = (float*)(p.ws + Layout::o) + ((int64_t)slot * BM + r) * LD + half * (LD / 2);
+#pragma unroll 1
+      for (int c = 0; c < LD / 64; ++c) {
+        uint32_t o[32];
+        tmem_ld32_wait(tmem + lrow + c * 32, o);
+        if (!store) continue;
+        if (whole) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              y[k] = pack2<T>(__uint_as_float(o[v * 16 + 2 * k]) * inv, __uint_as_float(o[v * 16 + 2 * k + 1]) * inv);
+            // out is 16-byte aligned, a row a multiple of 512 bytes
+            *reinterpret_cast<uint4*>(dst + c * 32 + v * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(dst + c * 32 + v * 16 + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(o[v * 8 + k]) * inv);
+            st_global_32B(part + c * 32 + v * 8, y);
+          }
+        }
+      }
+      if (store && half == 0) {
+        const float lg = m_run == -INFINITY ? -INFINITY : m_run + __log2f(l);
+        if (!whole) ((float*)(p.ws + Layout::lse))[slot * BM + r] = lg;
+        else if (p.lse) p.lse[row] = lg * LN2;
+      }
+      if (r == 0 && half == 0) {
+        if (!whole) ((int32_t*)(p.ws + Layout::bad))[slot] = bad;
+        if (bad) atomicOr(p.dev_status, PKV_DEV_BAD_PAGE);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_segempty[e]);
+    }
+    if (!ok) pair_bar_arrive(bar_id);   // lets the other warp of these rows leave its exchange
+  }
+
+  if (s_abort && (warp == 0 || warp == 2)) {
+    // copies of this CTA may still be on their way: give them time to land
+    const uint64_t t0 = globaltimer_ns();
+    for (int it = 0; it < (1 << 24) && globaltimer_ns() - t0 < 20000000ull; ++it) {}
+  }
+  if (warp == 1 && rank == 0) {
+    mma_commit_pair_warp(&bar_drain);
+    mbar_wait(&bar_drain, 0, 500000000ull);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // no CTA leaves while the pair's MMAs or barriers need it
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, TMEM_COLS);
+}
+
+// Joins the partial results of every cut tile. One warp per row: the weights
+// 2^(lse_s - max) of its parts, then the weighted sum of their outputs, in the
+// order of the keys.
+template <int LD, typename T>
+__global__ void __launch_bounds__(128) latent_combine_kernel(char* ws, T* out, float* lse) {
+  pdl_wait();
+  const int pair = blockIdx.x;
+  const Record rec = ((const Record*)(ws + Layout::rec))[pair];
+  if (rec.parts == 0) return;
+  const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= rec.nrows) return;
+  const float* sums = (const float*)(ws + Layout::lse);
+  const int32_t* bad = (const int32_t*)(ws + Layout::bad);
+  auto slot = [&](int s) { return s == 0 ? 2 * pair + 1 : 2 * (pair + s); };
+  float m = -INFINITY;
+  int any = 0;
+  for (int s = lane; s < rec.parts; s += 32) {
+    m = fmaxf(m, sums[slot(s) * BM + r]);
+    any |= bad[slot(s)];
+  }
+  m = warp_max(m);
+  if (__any_sync(0xffffffffu, any)) return;
+  constexpr int NV = LD / 128;   // float4s of a lane
+  float4 o[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float total = 0.f;
+  const float4* parts = (const float4*)(ws + Layout::o);
+#pragma unroll 4
+  for (int s = 0; s < rec.parts; ++s) {
+    const float w = exp2f(sums[slot(s) * BM + r] - m);
+    total += w;
+    const float4* x = parts + ((int64_t)slot(s) * BM + r) * (LD / 4) + lane;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const float4 y = x[k * 32];
+      o[k].x += w * y.x;
+      o[k].y += w * y.y;
+      o[k].z += w * y.z;
+      o[k].w += w * y.w;
+    }
+  }
+  const float inv = 1.f / total;
+  const int64_t row = (int64_t)rec.row0 + r;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    uint2 y;
+    y.x = pack2<T>(o[k].x * inv, o[k].y * inv);
+    y.y = pack2<T>(o[k].z * inv, o[k].w * inv);
+    *reinterpret_cast<uint2*>(out + row * LD + k * 128 + lane * 4) = y;
+  }
+  if (lse && lane == 0) lse[row] = (m + log2f(total)) * LN2;
+}
+
+int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+template <int LD, typename T>
 cudaError_t launch(const LatentAttnArgs& a, cudaStream_t s) {
-  AttnP p{a.cu, a.kv_lens, a.page_tables, a.B, a.T, a.H, a.P, a.num_pages, a.max_pages, a.max_kv_len,
-          a.scale * LOG2E, a.lse, a.dev.status};
-  const int64_t rows = (int64_t)a.T * a.H;
-  KernelTimer timer("latent_rows", s);
-  latent_rows_kernel<LD, T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T*)a.q, (const T*)a.cache, (T*)a.out, p);
-  return cudaGetLastError();
+  using C = Cfg<LD>;
+  static std::atomic<uint64_t> ready{0};   // devices whose kernel attribute is set
+  if (!(ready.load() >> a.dev.id & 1)) {
+    const cudaError_t e = cudaFuncSetAttribute(latent_attn_kernel<LD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               C::SMEM);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(1ull << a.dev.id);
+  }
+  const CUtensorMapDataType dt =
+      std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  AttnP p;
+  p.cu = a.cu;
+  p.kv_lens = a.kv_lens;
+  p.page_tables = a.page_tables;
+  p.B = a.B;
+  p.T = a.T;
+  p.H = a.H;
+  p.P = a.P;
+  p.box = gcd(a.P, HM);
+  p.num_pages = a.num_pages;
+  p.max_pages = a.max_pages;
+  p.max_kv_len = a.max_kv_len;
+  p.table_cap = a.max_pages * a.P;
+  p.scale_log2 = a.scale * LOG2E;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.ws = a.ws;
+  p.dev_status = a.dev.status;
+  CUtensorMap mq, mx;
+  if (!make_map_rows(&mq, a.q, dt, LD + 64, (int64_t)a.T * a.H, LD + 64, HM) ||
+      !make_map_rows(&mx, a.cache, dt, LD + 64, (int64_t)a.num_pages * a.P, LD + 64, p.box))
+    return cudaErrorInvalidValue;
+  const int pairs = a.dev.num_sms / 2 < MAX_PAIRS ? a.dev.num_sms / 2 : MAX_PAIRS;
+  cudaError_t e;
+  {
+    KernelTimer timer("latent_attn", s);
+    e = launch_after_trigger(latent_attn_kernel<LD, T>, dim3(2 * pairs), dim3(NTHREADS), C::SMEM, s, mq, mx, p);
+  }
+  if (e != cudaSuccess) return e;
+  KernelTimer timer("latent_combine", s);
+  return launch_after_trigger(latent_combine_kernel<LD, T>, dim3(pairs, BM / 4), dim3(128), 0, s, a.ws, (T*)a.out,
+                              a.lse);
 }
 
 }  // namespace
 
-size_t latent_attn_workspace(int32_t, int32_t, int32_t, int32_t) { return 256; }
+size_t latent_attn_workspace(int32_t, int32_t, int32_t, int32_t latent_dim) { return Layout::total(latent_dim); }
 
 cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t s) {
   if (a.dtype == PKV_BF16)
