@@ -14,18 +14,22 @@
 //
 // The product S wants half of the keys in each CTA, O wants half of the latent
 // columns of all keys, and one instruction names the same shared-memory offsets in
-// both CTAs, so the two operands cannot share storage: keys are loaded for S
-// (K ring), and again, from L2, for O (V buffers). HBM reads each row once.
+// both CTAs. Of a step's 64 loaded rows a CTA therefore keeps the columns that are
+// its own for O where they are; the others, once S has read them, are overwritten
+// in place with the peer's rows of its own columns (from L2). A row costs 1.44
+// times its bytes in L2 traffic and nothing beyond them in shared memory; loading
+// keys for S and O into buffers of their own costs 1.89 times and left room for one
+// step in flight only (decode of 128 sequences at 128 heads: 198 us).
 //
 //   warp 0   Q and K producer (TMA; the page table gives the rows of each box)
-//   warp 1   MMA issuer (even CTA): S(j + 1) is issued before O(j), so that the
-//            tensor pipe has work while the softmax of j runs
-//   warp 2   V producer; zeroes the rows behind the sequence's end in the last tile
-//   warp 3   scheduler: the segments of this pair
+//   warp 1   issues S (even CTA)
+//   warp 2   reload producer; zeroes the rows behind the sequence's end in the last step
+//   warp 3   issues O (even CTA)
 //   warps 4-7  softmax. Lane l of TMEM holds row l & 63, keys (or output columns)
 //            of half l / 64; the halves exchange row maxima through shared memory.
 //            P goes to shared memory in the cache type, O is rescaled in TMEM only
 //            when a row's maximum grows by more than 2^8.
+//   warp 8   scheduler: the segments of this pair
 //
 // Work split: the tick's steps (all tiles, one after the other) are cut into
 // equal runs, one per pair. A tile cut by a run's end leaves partial results
@@ -48,25 +52,30 @@ constexpr int BM = 128;          // (token, head) rows of a tile
 constexpr int HM = 64;           // rows of one CTA
 constexpr int BN = 128;          // keys of a step
 constexpr int MAX_PAIRS = 76;    // 152 SMs; the workspace is laid out for these
-constexpr int NTHREADS = 256;
+constexpr int NTHREADS = 288;
 constexpr uint32_t UNIT = 8192;  // 64 rows x 64 columns of 16 bits: one swizzle atom wide
 constexpr float RESCALE_LOG2 = 8.f;
 
+// A step's 64 rows of one CTA lie as LD / 64 units of 64 columns, in NG groups of
+// four: two units with columns of the even CTA's part of O, two of the odd CTA's;
+// one product of 256 output columns reads one group. The rotary columns have
+// units of their own, read by S alone.
 template <int LD>
 struct Cfg {
-  static constexpr int CH = LD / 64 + 1;         // 64-column chunks of a row, the rotary one last
-  static constexpr int GU = LD == 512 ? 3 : 5;   // chunks of a K group (one barrier)
-  static constexpr int TG = CH / GU;             // groups of a step
-  static constexpr int NG = 3;                   // groups of the K ring
-  static constexpr int NH = LD / 256;            // products of 256 output columns
+  static constexpr int CH = LD / 64 + 1;           // units of a row, the rotary one last
+  static constexpr int NG = LD / 256;              // groups
+  static constexpr int NST = LD == 512 ? 2 : 4;    // steps in shared memory
   static constexpr uint32_t Q_BYTES = CH * UNIT;
-  static constexpr uint32_t G_BYTES = GU * UNIT;
-  static constexpr uint32_t V_BYTES = 4 * UNIT;  // 2 chunks x 128 keys: this CTA's part of one product
-  static constexpr uint32_t P_BYTES = 2 * UNIT;
-  static constexpr uint32_t SMEM = Q_BYTES + NG * G_BYTES + NH * V_BYTES + P_BYTES + 1024;
-  static_assert(CH % GU == 0 && SMEM <= 231424, "shared memory");
+  static constexpr uint32_t G_BYTES = 4 * UNIT;
+  static constexpr uint32_t ST_BYTES = NG * G_BYTES;
+  static constexpr uint32_t X_BYTES = (1 + NST) * UNIT;   // P of keys 0-63; per step, the rotary unit, then P of keys 64-127
+  static constexpr uint32_t SMEM = Q_BYTES + NST * ST_BYTES + X_BYTES + 1024;
+  static_assert(SMEM <= 231424, "shared memory");
+  // 64-column chunk of a row that unit u of group g holds
+  static __host__ __device__ constexpr int chunk(int g, int u) { return (u < 2 ? 0 : LD / 128) + 2 * g + (u & 1); }
 };
 
+constexpr long long WAIT_LIMIT_CLOCKS = 4000000000ll;   // about two seconds
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t S_COL = 256;
 
@@ -201,18 +210,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mx, AttnP p) {
   using C = Cfg<LD>;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int NSEG = 4;
+  constexpr int NSEG = 4, NST = C::NST, NG = C::NG;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   unsigned char* sQ = sm;
-  unsigned char* sK = sQ + C::Q_BYTES;
-  unsigned char* sV = sK + C::NG * C::G_BYTES;
-  unsigned char* sP = sV + C::NH * C::V_BYTES;
+  unsigned char* sK = sQ + C::Q_BYTES;               // [step][group][unit]
+  unsigned char* sX = sK + NST * C::ST_BYTES;        // unit 0: P, keys 0-63; unit 1 + st: rotary unit of step slot st, then P, keys 64-127
 
-  // full barriers and bar_p live in the even CTA (both CTAs arrive there); the
-  // others are signalled in both CTAs by the MMA commits
-  __shared__ __align__(8) uint64_t bar_q, bar_qempty, bar_k[C::NG], bar_kempty[C::NG], bar_v[C::NH],
-      bar_vempty[C::NH], bar_vtail[C::NH], bar_s[2], bar_p, bar_o, bar_seg[NSEG], bar_segempty[NSEG], bar_drain;
+  // bar_k, bar_v, bar_q, bar_p and bar_sfree are waited on in the even CTA, where
+  // both CTAs arrive; the MMA commits signal bar_sdone, bar_odone and bar_qempty in both.
+  // Per step slot and group: loaded for S; read by S (after the last group: S
+  // is complete); loaded for O; read by O (after the last group: O is complete).
+  __shared__ __align__(8) uint64_t bar_k[NST][NG], bar_sdone[NST][NG], bar_v[NST][NG], bar_odone[NST][NG], bar_q,
+      bar_qempty, bar_vtail[NG], bar_s[2], bar_p, bar_sfree[2], bar_seg[NSEG], bar_segempty[NSEG], bar_drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ Segment s_seg[NSEG];
   __shared__ int s_bad[NSEG];
@@ -229,23 +239,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   if (tid == 0) {
     mbar_init(&bar_q, 2);
     mbar_init(&bar_qempty, 1);
-    for (int g = 0; g < C::NG; ++g) {
-      mbar_init(&bar_k[g], 2);
-      mbar_init(&bar_kempty[g], 1);
+    for (int g = 0; g < NG; ++g) {
+      for (int st = 0; st < NST; ++st) {
+        mbar_init(&bar_k[st][g], 2);
+        mbar_init(&bar_sdone[st][g], 1);
+        mbar_init(&bar_v[st][g], 2);
+        mbar_init(&bar_odone[st][g], 1);
+      }
+      mbar_init(&bar_vtail[g], 1);
     }
-    for (int i = 0; i < C::NH; ++i) {
-      mbar_init(&bar_v[i], 2);
-      mbar_init(&bar_vempty[i], 1);
-      mbar_init(&bar_vtail[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) mbar_init(&bar_s[i], 1);
     mbar_init(&bar_p, 8);        // the four softmax warps of both CTAs
-    mbar_init(&bar_o, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_sfree[i], 8);
+      mbar_init(&bar_drain[i], 1);
+    }
     for (int e = 0; e < NSEG; ++e) {
       mbar_init(&bar_seg[e], 1);
-      mbar_init(&bar_segempty[e], rank == 0 ? 7 : 6);   // producers, MMA issuer, softmax warps
+      mbar_init(&bar_segempty[e], rank == 0 ? 8 : 6);   // producers, MMA issuers, softmax warps
     }
-    mbar_init(&bar_drain, 1);
     fence_mbar_init();
     s_abort = 0;
     s_run = 0;
@@ -317,28 +329,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   pdl_trigger();
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    bool ok = mbar_try_wait_cluster(bar, parity);
-    if (!ok) {
-      const uint64_t t0 = globaltimer_ns();
-      for (uint32_t it = 0; !ok; ++it) {
-        ok = mbar_try_wait_cluster(bar, parity);
-        if (!ok && (it & 63u) == 63u) {
-          if (s_abort) break;
-          if (globaltimer_ns() - t0 > WAIT_LIMIT_NS || it > (1u << 28)) {
-            s_abort = 1;
-            atomicOr(p.dev_status, PKV_DEV_TIMEOUT);
-            break;
-          }
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    bool ok = false;
+    const long long t0 = clock64();   // (reading the global timer takes longer than most waits)
+    for (uint32_t it = 0; !ok; ++it) {
+      ok = mbar_try_wait(bar, parity);
+      if (!ok && (it & 63u) == 63u) {
+        if (s_abort) break;
+        if (clock64() - t0 > WAIT_LIMIT_CLOCKS || it > (1u << 28)) {
+          s_abort = 1;
+          atomicOr(p.dev_status, PKV_DEV_TIMEOUT);
+          break;
         }
       }
     }
-    // a warp that gave up no longer takes part in the pairwise exchange, so
-    // nobody goes on once the flag is up
-    return __all_sync(0xffffffffu, ok && !s_abort);
+    return __all_sync(0xffffffffu, ok);
   };
 
   bool ok = true;
-  if (warp == 3) {
+  if (warp == 8) {
     // ------------------------------------------------------------- scheduler
     Record* rec = (Record*)(p.ws + Layout::rec) + pair;
     const int64_t each = s_each;
@@ -394,65 +403,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (!g.valid) break;
     }
     if (rank == 0 && lane == 0) *rec = r;
-  } else if (warp == 0) {
-    // -------------------------------------------------------- Q and K producer
+  } else if (warp == 0 || warp == 2) {
+    // --------------------------------------------------------------- producers
+    // Warp 0 loads Q and this CTA's 64 keys of each step, warp 2 the peer's 64
+    // keys of this CTA's output columns. Lane l takes boxes l and l + 32 of the 64
+    // keys. Rows behind the end and bad pages are read from page 0 (masked, or
+    // discarded), so that a step's bytes are always the same.
+    const bool reload = warp == 2;
+    const int key_half = (int)rank ^ (reload ? 1 : 0);
     const uint32_t q_bar = map_to_rank(&bar_q, 0);
-    uint32_t ring = 0;      // K groups before the current one
-    const int boxes = HM / p.box;   // boxes of this CTA's 64 keys; lane l takes boxes l and l + 32
-    for (uint32_t t = 0; ok; ++t) {
-      const uint32_t e = t % NSEG;
-      if (!(ok = wait(&bar_seg[e], (t / NSEG) & 1))) break;
-      const Segment g = s_seg[e];
-      if (!g.valid) break;
-      if (t >= 1 && !(ok = wait(&bar_qempty, (t - 1) & 1))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx_cluster(q_bar, C::Q_BYTES);
-#pragma unroll
-        for (int c = 0; c < C::CH; ++c) tma_load_2d_pair(sQ + c * UNIT, &mq, q_bar, c * 64, g.row0 + (int)rank * HM);
-      }
-      const int32_t* pt = p.page_tables + (int64_t)g.b * p.max_pages;
-      // row in the pool of the first key of box i of step j; rows behind the
-      // end and bad pages are read from page 0 (masked, or discarded)
-      auto box_row = [&](int j, int i) {
-        const int key = j * BN + (int)rank * HM + i * p.box;
-        if (i >= boxes || key >= g.L) return 0;
-        const int lp = key / p.P;
-        const int id = __ldg(pt + lp);
-        return id < 0 || id >= p.num_pages ? 0 : id * p.P + (key - lp * p.P);
-      };
-      int row[2] = {box_row(g.j0, lane), box_row(g.j0, lane + 32)};
-      for (int j = g.j0; j < g.j1 && ok; ++j) {
-        const int cur[2] = {row[0], row[1]};
-        if (j + 1 < g.j1) {
-          row[0] = box_row(j + 1, lane);
-          row[1] = box_row(j + 1, lane + 32);
-        }
-        for (int k = 0; k < C::TG; ++k, ++ring) {
-          const uint32_t slot = ring % C::NG, round = ring / C::NG;
-          if (!(ok = wait(&bar_kempty[slot], (round & 1) ^ 1))) break;
-          const uint32_t bar = map_to_rank(&bar_k[slot], 0);
-          if (lane == 0) mbar_arrive_expect_tx_cluster(bar, C::G_BYTES);
-          __syncwarp();
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int i = lane + w * 32;
-            if (i < boxes)
-#pragma unroll
-              for (int u = 0; u < C::GU; ++u)
-                tma_load_2d_pair(sK + slot * C::G_BYTES + u * UNIT + i * p.box * 128, &mx, bar, (k * C::GU + u) * 64,
-                                 cur[w]);
-          }
-          __syncwarp();
-        }
-      }
-      if (ok && lane == 0) mbar_arrive(&bar_segempty[e]);
-      __syncwarp();
-    }
-  } else if (warp == 2) {
-    // -------------------------------------------------------------- V producer
-    uint32_t n_load = 0;            // steps before the current one
-    uint32_t n_tail = 0;            // tail steps before the current one
-    const int boxes = BN / p.box;   // lane l takes boxes l, l + 32, l + 64, l + 96
+    const int boxes = HM / p.box;
+    uint32_t n = 0, n_tail = 0;     // steps, and last steps with rows to zero, before the current one
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t % NSEG;
       if (!(ok = wait(&bar_seg[e], (t / NSEG) & 1))) break;
@@ -460,66 +421,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (!g.valid) break;
       const int32_t* pt = p.page_tables + (int64_t)g.b * p.max_pages;
       const int keys = min(g.L, g.n * BN);   // keys that the tile needs
-      auto box_row = [&](int j, int i, bool* bad) {
-        const int key = j * BN + i * p.box;
+      bool bad = false;
+      auto box_row = [&](int j, int i) {
+        const int key = j * BN + key_half * HM + i * p.box;
         if (i >= boxes || key >= keys) return 0;
         const int lp = key / p.P;
         const int id = __ldg(pt + lp);
         if (id >= 0 && id < p.num_pages) return id * p.P + (key - lp * p.P);
-        *bad = true;
+        bad = true;
         return 0;
       };
-      bool bad = false;
-      int row[4];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) row[w] = box_row(g.j0, lane + w * 32, &bad);
-      for (int j = g.j0; j < g.j1 && ok; ++j, ++n_load) {
-        const int cur[4] = {row[0], row[1], row[2], row[3]};
+      int row[2] = {box_row(g.j0, lane), box_row(g.j0, lane + 32)};
+      for (int j = g.j0; j < g.j1 && ok; ++j, ++n) {
+        const int cur[2] = {row[0], row[1]};
         if (bad) s_bad[e] = 1;
         if (j + 1 < g.j1) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) row[w] = box_row(j + 1, lane + w * 32, &bad);
+          row[0] = box_row(j + 1, lane);
+          row[1] = box_row(j + 1, lane + 32);
         }
-        const int end = g.L - j * BN;   // rows from here on are behind the sequence
-        const bool tail = end < BN;
+        const uint32_t st = n % NST, par = (n / NST) & 1;
+        unsigned char* stage = sK + st * C::ST_BYTES;
+        const int end = g.L - j * BN;        // rows from here on are behind the sequence
+        const bool tail = reload && end < BN;
 #pragma unroll
-        for (int i = 0; i < C::NH; ++i) {
-          if (!(ok = wait(&bar_vempty[i], (n_load & 1) ^ 1))) break;
-          const uint32_t bar = tail ? smem_u32(&bar_vtail[i]) : map_to_rank(&bar_v[i], 0);
+        for (int k = 0; k < NG; ++k) {
+          // units that this warp fills, and their columns
+          const int u0 = reload ? (rank ? 0 : 2) : 0, nu = reload ? 2 : 4;
+          const int c0 = reload ? (rank ? 2 : 0) : 0;
+          if (!(ok = reload ? wait(&bar_sdone[st][k], par) : wait(&bar_odone[st][k], par ^ 1))) break;
+          const uint32_t bar = map_to_rank(reload ? &bar_v[st][k] : &bar_k[st][k], 0);
+          const bool rot = !reload && k == NG - 1;
           if (lane == 0) {
-            if (tail) mbar_arrive_expect_tx(&bar_vtail[i], C::V_BYTES);
-            else mbar_arrive_expect_tx_cluster(bar, C::V_BYTES);
+            if (tail) mbar_arrive_expect_tx(&bar_vtail[k], 2 * UNIT);
+            else mbar_arrive_expect_tx_cluster(bar, (nu + (rot ? 1 : 0)) * UNIT);
           }
           __syncwarp();
-          const int col = (int)rank * (LD / 2) + i * 128;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int x = lane + w * 32;
-            if (x < boxes) {
+          for (int w = 0; w < 2; ++w) {
+            const int i = lane + w * 32;
+            if (i < boxes) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                unsigned char* dst = sV + i * C::V_BYTES + c * 2 * UNIT + x * p.box * 128;
-                if (tail) tma_load_2d(dst, &mx, &bar_vtail[i], col + c * 64, cur[w]);
-                else tma_load_2d_pair(dst, &mx, bar, col + c * 64, cur[w]);
+              for (int u = 0; u < 4; ++u) {
+                if (u >= nu) break;
+                unsigned char* dst = stage + k * C::G_BYTES + (u0 + u) * UNIT + i * p.box * 128;
+                const int col = C::chunk(k, c0 + u) * 64;
+                if (tail) tma_load_2d(dst, &mx, &bar_vtail[k], col, cur[w]);
+                else tma_load_2d_pair(dst, &mx, bar, col, cur[w]);
               }
+            }
+          }
+          if (rot) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const int i = lane + w * 32;
+              if (i < boxes) tma_load_2d_pair(sX + (1 + st) * UNIT + i * p.box * 128, &mx, bar, LD, cur[w]);
             }
           }
           __syncwarp();
         }
         if (!ok) break;
+        if (!reload && j == g.j0) {
+          // Q replaces the segment before's once its last S is done; the first keys go ahead
+          if (t >= 1 && !(ok = wait(&bar_qempty, (t - 1) & 1))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx_cluster(q_bar, C::Q_BYTES);
+#pragma unroll
+            for (int c = 0; c < C::CH; ++c)
+              tma_load_2d_pair(sQ + c * UNIT, &mq, q_bar, c * 64, g.row0 + (int)rank * HM);
+          }
+          __syncwarp();
+        }
         if (tail) {
-          // 0 * NaN must not reach O from the slots behind the end
+          // 0 * NaN must not reach O from the slots behind the end: units 0 and 1
+          // of a group hold keys 0-63 of the step, 2 and 3 keys 64-127
 #pragma unroll
-          for (int i = 0; i < C::NH; ++i) {
-            if (!(ok = wait(&bar_vtail[i], n_tail & 1))) break;
+          for (int k = 0; k < NG; ++k) {
+            if (!(ok = wait(&bar_vtail[k], n_tail & 1))) break;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint4* base = (uint4*)(sV + i * C::V_BYTES + c * 2 * UNIT);
-              for (int x = end * 8 + lane; x < BN * 8; x += 32) base[x] = make_uint4(0, 0, 0, 0);
+            for (int u = 0; u < 4; ++u) {
+              const int from = max(0, end - (u >> 1) * HM);
+              uint4* base = (uint4*)(stage + k * C::G_BYTES + u * UNIT);
+              for (int x = from * 8 + lane; x < HM * 8; x += 32) base[x] = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(&bar_v[i], 0));
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(&bar_v[st][k], 0));
           }
           ++n_tail;
         }
@@ -527,64 +513,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&bar_segempty[e]);
     }
-  } else if (warp == 1) {
-    // -------------------------------------------------------------- MMA issuer
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------- MMA issuers
     if (rank == 0) {
       const uint32_t id_s = idesc_f16(BM, BN, BF16, false);
       const uint32_t id_o = idesc_f16(BM, 256, BF16, true);
       const uint64_t qd = smem_desc(smem_u32(sQ), 16, 1024, LAYOUT_SW128);
-      const uint64_t pd = smem_desc(smem_u32(sP), 16, 1024, LAYOUT_SW128);
       const uint64_t kd = smem_desc(smem_u32(sK), 16, 1024, LAYOUT_SW128);
-      const uint64_t vd = smem_desc(smem_u32(sV), 2 * UNIT, 1024, LAYOUT_SW128);
-      uint32_t ring = 0, n_s = 0, n_o = 0;
-      auto issue_s = [&]() -> bool {
-        const uint32_t d = tmem + S_COL + (n_s & 1) * 64;
-        for (int k = 0; k < C::TG; ++k, ++ring) {
-          const uint32_t slot = ring % C::NG;
-          if (!wait(&bar_k[slot], (ring / C::NG) & 1)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int u = 0; u < C::GU; ++u)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mma_f16_ss_pair_warp(d, qd + (uint64_t)(((k * C::GU + u) * UNIT + x * 32) >> 4),
-                                   kd + (uint64_t)((slot * C::G_BYTES + u * UNIT + x * 32) >> 4), id_s,
-                                   (k | u | x) ? 1u : 0u);
-          mma_commit_pair_warp(&bar_kempty[slot]);
-        }
-        mma_commit_pair_warp(&bar_s[n_s & 1]);
-        ++n_s;
-        return true;
-      };
+      const uint64_t xd = smem_desc(smem_u32(sX), 16, 1024, LAYOUT_SW128);
+      const uint64_t vd = smem_desc(smem_u32(sK), UNIT, 1024, LAYOUT_SW128);
+      uint32_t n = 0;
       for (uint32_t t = 0; ok; ++t) {
         const uint32_t e = t % NSEG;
         if (!(ok = wait(&bar_seg[e], (t / NSEG) & 1))) break;
         const Segment g = s_seg[e];
         if (!g.valid) break;
-        if (!(ok = wait(&bar_q, t & 1))) break;
-        if (!(ok = issue_s())) break;
         const int steps = g.j1 - g.j0;
-        for (int j = 0; j < steps; ++j) {
-          if (j + 1 < steps && !(ok = issue_s())) break;
-          // the last product with Q is on its way: the next segment's may follow
-          if (j + 2 == steps || steps == 1) mma_commit_pair_warp(&bar_qempty);
-          if (!(ok = wait(&bar_p, n_o & 1))) break;
+        if (warp == 1) {
+          if (!(ok = wait(&bar_q, t & 1))) break;
+          for (int j = 0; j < steps; ++j, ++n) {
+            const uint32_t st = n % NST, par = (n / NST) & 1;
+            const uint32_t d = tmem + S_COL + (n & 1) * 64;
+            if (n >= 2 && !(ok = wait(&bar_sfree[n & 1], ((n >> 1) - 1) & 1))) break;
 #pragma unroll
-          for (int i = 0; i < C::NH; ++i) {
-            if (!(ok = wait(&bar_v[i], n_o & 1))) break;
-            tc_fence_after();
+            for (int k = 0; k < NG; ++k) {
+              if (!(ok = wait(&bar_k[st][k], par))) break;
+              tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < BN / 16; ++x)
-              mma_f16_ss_pair_warp(tmem + i * 128, pd + (uint64_t)(((x >> 2) * UNIT + (x & 3) * 32) >> 4),
-                                   vd + (uint64_t)((i * C::V_BYTES + x * 16 * 128) >> 4), id_o,
-                                   (j | x) ? 1u : 0u);
-            mma_commit_pair_warp(&bar_vempty[i]);
+              for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  mma_f16_ss_pair_warp(d, qd + (uint64_t)((C::chunk(k, u) * UNIT + x * 32) >> 4),
+                                       kd + (uint64_t)((st * C::ST_BYTES + k * C::G_BYTES + u * UNIT + x * 32) >> 4),
+                                       id_s, (k | u | x) ? 1u : 0u);
+              mma_commit_pair_warp(&bar_sdone[st][k]);
+              if (k == NG - 1) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  mma_f16_ss_pair_warp(d, qd + (uint64_t)(((C::CH - 1) * UNIT + x * 32) >> 4),
+                                       xd + (uint64_t)(((1 + st) * UNIT + x * 32) >> 4), id_s, 1u);
+                mma_commit_pair_warp(&bar_s[n & 1]);
+              }
+            }
+            if (!ok) break;
           }
           if (!ok) break;
-          mma_commit_pair_warp(&bar_o);
-          ++n_o;
+          mma_commit_pair_warp(&bar_qempty);
+        } else {
+          for (int j = 0; j < steps; ++j, ++n) {
+            const uint32_t st = n % NST, par = (n / NST) & 1;
+            if (!(ok = wait(&bar_p, n & 1))) break;
+#pragma unroll
+            for (int k = 0; k < NG; ++k) {
+              if (!(ok = wait(&bar_v[st][k], par))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int x = 0; x < BN / 16; ++x)
+                mma_f16_ss_pair_warp(tmem + k * 128, xd + (uint64_t)(((x >> 2) * (1 + st) * UNIT + (x & 3) * 32) >> 4),
+                                     vd + (uint64_t)((st * C::ST_BYTES + k * C::G_BYTES + (x >> 2) * 2 * UNIT +
+                                                      (x & 3) * 2048) >>
+                                                     4),
+                                     id_o, (j | x) ? 1u : 0u);
+              mma_commit_pair_warp(&bar_odone[st][k]);
+            }
+            if (!ok) break;
+          }
+          if (!ok) break;
         }
-        if (ok && lane == 0) mbar_arrive(&bar_segempty[e]);
+        if (lane == 0) mbar_arrive(&bar_segempty[e]);
         __syncwarp();
       }
     }
@@ -594,8 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const int i = (quarter & 1) * 32 + lane;        // row of this CTA
     const uint32_t lrow = (uint32_t)(quarter * 32) << 16;
     const int bar_id = 1 + (quarter & 1);           // the two warps of the same rows
-    const uint32_t p_bar = map_to_rank(&bar_p, 0);
-    unsigned char* p_row = sP + half * UNIT + i * 128;
+    const uint32_t p_bar = map_to_rank(&bar_p, 0), sfree_bar = map_to_rank(bar_sfree, 0);
     const float sc = p.scale_log2;
     uint32_t n = 0;                                  // steps before the current one
     for (uint32_t t = 0; ok; ++t) {
@@ -613,9 +608,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         uint32_t x[2][32];
         tmem_ld32(tmem + lrow + S_COL + (n & 1) * 64, x[0]);
         tmem_ld32(tmem + lrow + S_COL + (n & 1) * 64 + 32, x[1]);
+        // a warp that gave up takes part in no further exchange, so nobody goes on once the flag is up
+        if (!(ok = !__any_sync(0xffffffffu, s_abort))) break;
         tmem_wait_ld();
         reg_fence(x[0]);
         reg_fence(x[1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(sfree_bar + (n & 1) * 8);
         if (j >= j_mask) {
           const int lim = pos - j * BN - half * 64;  // keys of this half up to lim are visible
 #pragma unroll
@@ -664,7 +664,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         // the product before has read P and written O (a segment's first step
         // follows its predecessor's epilogue, which waited for that)
         if (!first) {
-          if (!(ok = wait(&bar_o, (n - 1) & 1))) break;
+          if (!(ok = wait(&bar_odone[(n - 1) % NST][NG - 1], ((n - 1) / NST) & 1))) break;
           tc_fence_after();
           if (rescale) {
 #pragma unroll 1
@@ -677,6 +677,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
           }
         }
+        unsigned char* p_row = sX + (half ? 1 + n % NST : 0) * UNIT + i * 128;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           *reinterpret_cast<uint4*>(p_row + ((c ^ (i & 7)) << 4)) =
@@ -691,7 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       s_x[n & 1][half][i] = l_run;
       pair_bar_sync(bar_id);
       const float l = l_run + s_x[n & 1][half ^ 1][i];
-      if (!(ok = wait(&bar_o, (n - 1) & 1))) break;
+      if (!(ok = wait(&bar_odone[(n - 1) % NST][NG - 1], ((n - 1) / NST) & 1))) break;
       tc_fence_after();
       const int bad = *(volatile int*)&s_bad[e];
       const bool whole = g.j0 == 0 && g.j1 == g.n;
@@ -748,9 +749,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const uint64_t t0 = globaltimer_ns();
     for (int it = 0; it < (1 << 24) && globaltimer_ns() - t0 < 20000000ull; ++it) {}
   }
-  if (warp == 1 && rank == 0) {
-    mma_commit_pair_warp(&bar_drain);
-    mbar_wait(&bar_drain, 0, 500000000ull);
+  if ((warp == 1 || warp == 3) && rank == 0) {
+    // every MMA this warp issued is complete before TMEM is released
+    mma_commit_pair_warp(&bar_drain[warp >> 1]);
+    mbar_wait(&bar_drain[warp >> 1], 0, 500000000ull);
     __syncwarp();
   }
   tc_fence_before();

@@ -300,25 +300,15 @@ __device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
   return a;
 }
 
-// Arrivals on a barrier given by its cluster address (own CTA or peer).
+// Arrivals on a barrier given by its cluster address (own CTA or peer). What they
+// announce is read by TMA or MMA hardware of the announcing CTA (after a proxy
+// fence), or is tensor memory (after a tcgen05 fence), so no cluster-scope
+// release goes with them: it cost the latent decode kernel 10 % of its time.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-
-// mbar_try_wait that also acquires what the peer CTA released.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 // 2-D tiled load of one box into this CTA's shared memory.
