@@ -285,6 +285,9 @@ int decode_inflight_bytes(int kv_dtype, int D, int group);
 bool make_map_boxed(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elt, int D, int heads,
                     int64_t rows, int box_cols, int box_rows);
 
+// 3-D map [rows, heads, cols] with element strides, boxes of 64 columns of one head.
+bool make_map_strided(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int cols, int heads, int64_t rows,
+                      int64_t head_stride, int64_t row_stride, int box_rows);
 // 2-D map over rows of `cols` 16-bit elements (row_stride elements apart), boxes of 64 columns.
 bool make_map_rows(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int cols, int64_t rows,
                    int64_t row_stride, int box_rows);

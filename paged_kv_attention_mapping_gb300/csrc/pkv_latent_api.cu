@@ -184,6 +184,8 @@ extern "C" int pkv_latent_prefill(const void* q, const int32_t* cu_seqlens_q, co
   if ((int64_t)total_q * num_heads > INT32_MAX - 256 || total_k > INT32_MAX - 256) return PKV_E_SHAPE;
   if (total_q == 0 || num_seqs == 0) return PKV_OK;
   if (total_k == 0) return PKV_E_SHAPE;   // rows without keys
+  // a key row per token; a head stride of 0 (one key or value for all heads) is fine
+  if (total_k > 1 && (kn_stride_t == 0 || v_stride_t == 0 || kr_stride == 0)) return PKV_E_SHAPE;
   if (!q || !cu_seqlens_q || !k_nope || !v || !k_rope || !cu_seqlens_k || !out || !workspace) return PKV_E_NULL;
   if (!aligned16(q) || !aligned16(k_nope) || !aligned16(v) || !aligned16(k_rope) || !aligned16(out) ||
       !aligned4(lse) || !aligned4(cu_seqlens_q) || !aligned4(cu_seqlens_k))

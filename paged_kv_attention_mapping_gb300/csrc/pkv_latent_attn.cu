@@ -41,6 +41,7 @@
 
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
+#include "pkv_latent.cuh"
 #include "pkv_sm100.cuh"
 
 namespace pkv {
@@ -167,29 +168,6 @@ __device__ __forceinline__ Seq load_seq(const AttnP& p, int b, bool report) {
   }
   if (s.q <= 0 || s.q > p.T) s.tiles = 0;
   return s;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&v);
-  } else {
-    __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&v);
-  }
 }
 
 __device__ __forceinline__ void st_global_32B(void* p, const uint32_t (&w)[8]) {

@@ -38,6 +38,21 @@ bool make_map_boxed(CUtensorMap* m, const void* base, CUtensorMapDataType dt, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D view [rows, heads, cols] of 16-bit elements with strides in elements; boxes of
+// 64 columns x 1 head x box_rows rows, 128-byte swizzled.
+bool make_map_strided(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int cols, int heads, int64_t rows,
+                      int64_t head_stride, int64_t row_stride, int box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)row_stride * 2};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 2-D view of `rows` rows of `cols` 16-bit elements, row_stride elements apart; boxes of
 // 64 columns (one 128-byte swizzle atom) x box_rows rows, 128-byte swizzled.
 bool make_map_rows(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int cols, int64_t rows,
