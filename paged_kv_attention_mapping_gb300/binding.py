@@ -7,8 +7,8 @@ or cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import itertools
 import os
 from typing import Optional, Sequence
@@ -249,15 +249,20 @@ def pack_tick_flat(q_lens, kv_lens, page_offsets, page_ids, page_size: int, num_
 # ---------------------------------------------------------------------------
 # device calls (torch tensors)
 
-def _dtype_code(t) -> int:
+@functools.lru_cache(maxsize=None)
+def _code_of(dtype) -> int:
     import torch
     m = {torch.float32: PKV_F32, torch.float16: PKV_F16, torch.bfloat16: PKV_BF16,
          torch.uint8: PKV_FP8_E4M3}
     if hasattr(torch, "float8_e4m3fn"):
         m[torch.float8_e4m3fn] = PKV_FP8_E4M3
-    if t.dtype not in m:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    if dtype not in m:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return m[dtype]
+
+
+def _dtype_code(t) -> int:
+    return _code_of(t.dtype)
 
 
 def cache_desc(k_cache) -> CacheDesc:
@@ -478,39 +483,47 @@ def rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, 
 LATENT_NOPE, LATENT_ROPE, LATENT_V = 128, 64, 128
 
 
+@functools.lru_cache(maxsize=256)
+def _latent_desc_of(N, P, R, dtype) -> LatentDesc:
+    return LatentDesc(N, P, R - LATENT_ROPE, LATENT_ROPE, dtype)
+
+
 def _latent_desc(where, cache) -> LatentDesc:
     if cache.dim() != 3 or not cache.is_contiguous():
         raise ValueError(f"{where}: the latent cache must be a contiguous [num_pages, page_size, latent_dim + 64] tensor")
-    N, P, R = cache.shape
-    return LatentDesc(N, P, R - LATENT_ROPE, LATENT_ROPE, _dtype_code(cache))
+    return _latent_desc_of(*cache.shape, _dtype_code(cache))
 
 
-def _on_device(where, tensors):
-    """Every tensor on one CUDA device; returns a context that makes it the
-    current one (the library launches on the current device)."""
-    import torch
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{where}: all tensors must be on one CUDA device")
-    if dev.type != "cuda":
+def _on_one_device(where, first, *rest) -> int:
+    """The index of the CUDA device that every tensor is on (None: not given)."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError(f"{where} needs CUDA tensors")
-    if dev.index == torch.cuda.current_device():
-        return _SAME_DEVICE
-    return torch.cuda.device(dev)
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: all tensors must be on one CUDA device")
+    return dev
 
 
-_SAME_DEVICE = contextlib.nullcontext()
+def _call_on(dev, stream, fn, *args) -> int:
+    """fn(*args, stream) with device `dev` current (the library launches on the
+    current device); stream None is torch's current one there."""
+    import torch
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return fn(*args, _stream_ptr(stream))
+    return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream))
 
 
 def _rows_of(where, name, t, dims, width, dtype):
-    """A [..., width] view whose last dimension is contiguous and whose rows may
-    be strided: returns its leading strides (0 for a dimension of one entry)."""
-    if t.dim() != dims or t.shape[-1] != width or t.dtype != dtype:
-        raise ValueError(f"{where}: {name} must have {dims} dimensions, {width} wide, and the cache's dtype")
-    if t.stride(-1) != 1:
+    """Strides of a [..., width] view whose last dimension is contiguous and whose
+    rows may be strided (0 for a dimension of one entry)."""
+    st, shape = t.stride(), t.shape
+    if len(st) != dims or shape[-1] != width or t.dtype != dtype:
+        raise ValueError(f"{where}: {name} must have {dims} dimensions, be {width} wide, and share the others' dtype")
+    if st[-1] != 1:
         raise ValueError(f"{where}: {name} must be contiguous in its last dimension")
-    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in range(dims - 1))
+    return tuple(0 if n == 1 else x for n, x in zip(shape, st)) if 1 in shape else st
 
 
 def _int32s(where, *tensors):
@@ -536,12 +549,12 @@ def _out_and_lse(where, q, width, out, lse, want_lse, stream):
     T, H = q.shape[:2]
     if out is None:
         out = _lent(torch.empty((T, H, width), dtype=q.dtype, device=q.device), stream)
-    elif out.dtype != q.dtype or tuple(out.shape) != (T, H, width) or not out.is_contiguous():
+    elif out.dtype != q.dtype or out.shape != (T, H, width) or not out.is_contiguous():
         raise ValueError(f"{where}: out must be a contiguous [{T}, {H}, {width}] tensor of q's dtype")
     if lse is None:
         if want_lse:
             lse = _lent(torch.empty((T, H), dtype=torch.float32, device=q.device), stream)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, H) or not lse.is_contiguous():
+    elif lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
         raise ValueError(f"{where}: lse must be a contiguous float32 tensor [T, H]")
     return out, lse
 
@@ -557,36 +570,36 @@ def latent_append(c_kv, k_rope, positions, cos_sin, slot_mapping, cache, q_rope=
     import torch
     where = "latent_append"
     desc = _latent_desc(where, cache)
-    guard = _on_device(where, (cache, c_kv, k_rope, positions, cos_sin, slot_mapping, q_rope, q_out))
-    T = int(slot_mapping.shape[0])
+    dev = _on_one_device(where, cache, c_kv, k_rope, positions, cos_sin, slot_mapping, q_rope, q_out)
+    T = slot_mapping.shape[0]
     if positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64 or cos_sin.dtype != torch.float32:
         raise TypeError(f"{where}: positions int32, slot_mapping int64, cos_sin float32")
     if not (positions.is_contiguous() and slot_mapping.is_contiguous() and cos_sin.is_contiguous()):
         raise ValueError(f"{where}: positions, slot_mapping and cos_sin must be contiguous")
-    if (slot_mapping.dim() != 1 or tuple(positions.shape) != (T,) or cos_sin.dim() != 3
-            or tuple(cos_sin.shape[1:]) != (LATENT_ROPE // 2, 2) or c_kv.shape[0] != T or k_rope.shape[0] != T):
+    if (slot_mapping.dim() != 1 or positions.shape != (T,) or cos_sin.dim() != 3
+            or cos_sin.shape[1:] != (LATENT_ROPE // 2, 2) or c_kv.shape[0] != T or k_rope.shape[0] != T):
         raise ValueError(f"{where}: c_kv, k_rope, positions and slot_mapping must agree on the number of tokens, "
                          f"and cos_sin be [max_pos, {LATENT_ROPE // 2}, 2]")
-    c_st, = _rows_of(where, "c_kv", c_kv, 2, int(desc.latent_dim), cache.dtype)
-    kr_st, = _rows_of(where, "k_rope", k_rope, 2, LATENT_ROPE, cache.dtype)
+    dtype = cache.dtype
+    c_st, _ = _rows_of(where, "c_kv", c_kv, 2, desc.latent_dim, dtype)
+    kr_st, _ = _rows_of(where, "k_rope", k_rope, 2, LATENT_ROPE, dtype)
     q_st = q_sh = qo_st = qo_sh = H = 0
     if q_rope is not None:
-        q_st, q_sh = _rows_of(where, "q_rope", q_rope, 3, LATENT_ROPE, cache.dtype)
-        H = int(q_rope.shape[1])
+        q_st, q_sh, _ = _rows_of(where, "q_rope", q_rope, 3, LATENT_ROPE, dtype)
+        H = q_rope.shape[1]
         if q_out is None:
             q_out = _lent(torch.empty(q_rope.shape, dtype=q_rope.dtype, device=q_rope.device), stream)
-        qo_st, qo_sh = _rows_of(where, "q_out", q_out, 3, LATENT_ROPE, cache.dtype)
+        qo_st, qo_sh, _ = _rows_of(where, "q_out", q_out, 3, LATENT_ROPE, dtype)
         if q_rope.shape[0] != T or q_out.shape != q_rope.shape:
             raise ValueError(f"{where}: q_rope and q_out must be [T, H, {LATENT_ROPE}]")
-        for n, st in ((T, qo_st), (H, qo_sh)):
-            if n > 1 and st == 0:
-                raise ValueError(f"{where}: q_out must not be a broadcast view")
+        if (T > 1 and qo_st == 0) or (H > 1 and qo_sh == 0):
+            raise ValueError(f"{where}: q_out must not be a broadcast view")
     elif q_out is not None:
         raise ValueError(f"{where}: q_out without q_rope")
-    with guard:
-        st = lib().pkv_latent_append(_ptr(c_kv), c_st, _ptr(k_rope), kr_st, _ptr(q_rope), q_st, q_sh, _ptr(q_out),
-                                     qo_st, qo_sh, H, _ptr(positions), _ptr(cos_sin), int(cos_sin.shape[0]),
-                                     _ptr(slot_mapping), T, _ptr(cache), ctypes.byref(desc), _stream_ptr(stream))
+    q, qo = (None, None) if q_rope is None else (q_rope.data_ptr(), q_out.data_ptr())
+    st = _call_on(dev, stream, lib().pkv_latent_append, c_kv.data_ptr(), c_st, k_rope.data_ptr(), kr_st, q, q_st, q_sh,
+                  qo, qo_st, qo_sh, H, positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0],
+                  slot_mapping.data_ptr(), T, cache.data_ptr(), desc)
     _check(st, "pkv_latent_append")
     return q_out
 
@@ -600,17 +613,16 @@ def latent_gather(cache, page_tables, cu_seqlens_k, total_k: int, out=None, stre
     where = "latent_gather"
     desc = _latent_desc(where, cache)
     _int32s(where, page_tables, cu_seqlens_k)
-    guard = _on_device(where, (cache, page_tables, cu_seqlens_k, out))
-    B = int(cu_seqlens_k.shape[0]) - 1
+    dev = _on_one_device(where, cache, page_tables, cu_seqlens_k, out)
+    B = cu_seqlens_k.shape[0] - 1
     if page_tables.dim() != 2 or cu_seqlens_k.dim() != 1 or B < 0 or page_tables.shape[0] < B:
         raise ValueError(f"{where}: page_tables [B, W] and cu_seqlens_k [B + 1] disagree")
     if out is None:
         out = _lent(torch.empty((int(total_k), cache.shape[2]), dtype=cache.dtype, device=cache.device), stream)
-    elif out.dtype != cache.dtype or tuple(out.shape) != (int(total_k), cache.shape[2]) or not out.is_contiguous():
+    elif out.dtype != cache.dtype or out.shape != (total_k, cache.shape[2]) or not out.is_contiguous():
         raise ValueError(f"{where}: out must be a contiguous [total_k, {cache.shape[2]}] tensor of the cache's dtype")
-    with guard:
-        st = lib().pkv_latent_gather(_ptr(cache), ctypes.byref(desc), _ptr(page_tables), int(page_tables.shape[1]),
-                                     _ptr(cu_seqlens_k), B, int(total_k), _ptr(out), _stream_ptr(stream))
+    st = _call_on(dev, stream, lib().pkv_latent_gather, cache.data_ptr(), desc, page_tables.data_ptr(),
+                  page_tables.shape[1], cu_seqlens_k.data_ptr(), B, int(total_k), out.data_ptr())
     _check(st, "pkv_latent_gather")
     return out
 
@@ -639,26 +651,24 @@ def latent_attention(q, cu_seqlens_q, kv_lens, page_tables, cache, scale: float,
     where = "latent_attention"
     desc = _latent_desc(where, cache)
     _int32s(where, cu_seqlens_q, kv_lens, page_tables)
-    guard = _on_device(where, (q, cu_seqlens_q, kv_lens, page_tables, cache, out, lse, workspace))
+    dev = _on_one_device(where, q, cu_seqlens_q, kv_lens, page_tables, cache, out, lse, workspace)
     if q.dtype != cache.dtype:
         raise TypeError(f"{where}: q and cache must share one dtype")
     if q.dim() != 3 or q.shape[2] != cache.shape[2] or not q.is_contiguous():
         raise ValueError(f"{where}: q must be a contiguous [T, H, {cache.shape[2]}] tensor")
-    B = int(cu_seqlens_q.shape[0]) - 1
+    B = cu_seqlens_q.shape[0] - 1
     if (cu_seqlens_q.dim() != 1 or kv_lens.dim() != 1 or page_tables.dim() != 2 or B < 0 or kv_lens.shape[0] < B
             or page_tables.shape[0] < B):
         raise ValueError(f"{where}: cu_seqlens_q [B + 1], kv_lens [B] and page_tables [B, W] disagree")
-    out, lse = _out_and_lse(where, q, int(desc.latent_dim), out, lse, want_lse, stream)
-    T, H = int(q.shape[0]), int(q.shape[1])
+    out, lse = _out_and_lse(where, q, desc.latent_dim, out, lse, want_lse, stream)
+    T, H, _ = q.shape
     if workspace is None:
         workspace = _lent(alloc_latent_workspace(B, T, H, cache), stream)
     elif not workspace.is_contiguous():
         raise ValueError(f"{where}: workspace must be contiguous")
-    with guard:
-        st = lib().pkv_latent_attention(_ptr(q), _ptr(cu_seqlens_q), _ptr(kv_lens), _ptr(page_tables), B, T, H,
-                                        int(page_tables.shape[1]), int(max_kv_len), _ptr(cache), ctypes.byref(desc),
-                                        scale, _ptr(out), _ptr(lse), _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    st = _call_on(dev, stream, lib().pkv_latent_attention, q.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
+                  page_tables.data_ptr(), B, T, H, page_tables.shape[1], int(max_kv_len), cache.data_ptr(), desc, scale,
+                  out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     _check(st, "pkv_latent_attention")
     return out, lse
 
@@ -685,16 +695,18 @@ def latent_prefill(q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, scale: floa
     cu_seqlens_q, cu_seqlens_k int32 [B + 1]. Returns (out [Tq, H, 128], lse [Tq, H])."""
     where = "latent_prefill"
     _int32s(where, cu_seqlens_q, cu_seqlens_k)
-    guard = _on_device(where, (q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, out, lse, workspace))
+    dev = _on_one_device(where, q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, out, lse, workspace)
     if q.dim() != 3 or q.shape[2] != LATENT_NOPE + LATENT_ROPE or not q.is_contiguous():
         raise ValueError(f"{where}: q must be a contiguous [T, H, {LATENT_NOPE + LATENT_ROPE}] tensor")
-    kn_st, kn_sh = _rows_of(where, "k_nope", k_nope, 3, LATENT_NOPE, q.dtype)
-    v_st, v_sh = _rows_of(where, "v", v, 3, LATENT_V, q.dtype)
-    kr_st, = _rows_of(where, "k_rope", k_rope, 2, LATENT_ROPE, q.dtype)
-    Tq, H, Tk = int(q.shape[0]), int(q.shape[1]), int(k_rope.shape[0])
-    if k_nope.shape[0] != Tk or v.shape[0] != Tk or k_nope.shape[1] != H or v.shape[1] != H:
+    dtype = q.dtype
+    kn_st, kn_sh, _ = _rows_of(where, "k_nope", k_nope, 3, LATENT_NOPE, dtype)
+    v_st, v_sh, _ = _rows_of(where, "v", v, 3, LATENT_V, dtype)
+    kr_st, _ = _rows_of(where, "k_rope", k_rope, 2, LATENT_ROPE, dtype)
+    Tq, H, _ = q.shape
+    Tk = k_rope.shape[0]
+    if k_nope.shape[:2] != (Tk, H) or v.shape[:2] != (Tk, H):
         raise ValueError(f"{where}: k_nope, v [Tk, H, 128] and k_rope [Tk, 64] disagree")
-    B = int(cu_seqlens_q.shape[0]) - 1
+    B = cu_seqlens_q.shape[0] - 1
     if cu_seqlens_q.dim() != 1 or B < 0 or cu_seqlens_k.shape != cu_seqlens_q.shape:
         raise ValueError(f"{where}: cu_seqlens_q and cu_seqlens_k must both be [B + 1]")
     out, lse = _out_and_lse(where, q, LATENT_V, out, lse, want_lse, stream)
@@ -702,11 +714,10 @@ def latent_prefill(q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, scale: floa
         workspace = _lent(alloc_latent_prefill_workspace(B, q), stream)
     elif not workspace.is_contiguous():
         raise ValueError(f"{where}: workspace must be contiguous")
-    with guard:
-        st = lib().pkv_latent_prefill(_ptr(q), _ptr(cu_seqlens_q), _ptr(k_nope), kn_st, kn_sh, _ptr(v), v_st, v_sh,
-                                      _ptr(k_rope), kr_st, _ptr(cu_seqlens_k), B, Tq, Tk, H, _dtype_code(q), scale,
-                                      _ptr(out), _ptr(lse), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    st = _call_on(dev, stream, lib().pkv_latent_prefill, q.data_ptr(), cu_seqlens_q.data_ptr(), k_nope.data_ptr(),
+                  kn_st, kn_sh, v.data_ptr(), v_st, v_sh, k_rope.data_ptr(), kr_st, cu_seqlens_k.data_ptr(), B, Tq, Tk,
+                  H, _dtype_code(q), scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                  workspace.data_ptr(), workspace.nbytes)
     _check(st, "pkv_latent_prefill")
     return out, lse
 

@@ -25,11 +25,12 @@
 //   warp 1   issues S (even CTA)
 //   warp 2   reload producer; zeroes the rows behind the sequence's end in the last step
 //   warp 3   issues O (even CTA)
-//   warps 4-7  softmax. Lane l of TMEM holds row l & 63, keys (or output columns)
-//            of half l / 64; the halves exchange row maxima through shared memory.
-//            P goes to shared memory in the cache type, O is rescaled in TMEM only
-//            when a row's maximum grows by more than 2^8.
-//   warp 8   scheduler: the segments of this pair
+//   warps 4-11 softmax. Lane l of TMEM holds row l & 63, keys (or output columns)
+//            of half l / 64; two warps share a lane quarter, each with half of its
+//            columns, so four threads have a row and exchange its maximum through
+//            shared memory. P goes to shared memory in the cache type, O is rescaled
+//            in TMEM only when a row's maximum grows by more than 2^8.
+//   warp 12  scheduler: the segments of this pair
 //
 // Work split: the tick's steps (all tiles, one after the other) are cut into
 // equal runs, one per pair. A tile cut by a run's end leaves partial results
@@ -53,7 +54,9 @@ constexpr int BM = 128;          // (token, head) rows of a tile
 constexpr int HM = 64;           // rows of one CTA
 constexpr int BN = 128;          // keys of a step
 constexpr int MAX_PAIRS = 76;    // 152 SMs; the workspace is laid out for these
-constexpr int NTHREADS = 288;
+constexpr int SM_WARPS = 8;         // softmax warps of a CTA
+constexpr int SM_FIRST = 4;         // the first of them: its TMEM lanes are those of warp & 3
+constexpr int NTHREADS = (SM_FIRST + SM_WARPS + 1) * 32;
 constexpr uint32_t UNIT = 8192;  // 64 rows x 64 columns of 16 bits: one swizzle atom wide
 constexpr float RESCALE_LOG2 = 8.f;
 
@@ -70,8 +73,7 @@ struct Cfg {
   static constexpr uint32_t G_BYTES = 4 * UNIT;
   static constexpr uint32_t ST_BYTES = NG * G_BYTES;
   static constexpr uint32_t X_BYTES = (1 + NST) * UNIT;   // P of keys 0-63; per step, the rotary unit, then P of keys 64-127
-  static constexpr uint32_t SMEM = Q_BYTES + NST * ST_BYTES + X_BYTES + 1024;
-  static_assert(SMEM <= 231424, "shared memory");
+  static constexpr uint32_t TILES = Q_BYTES + NST * ST_BYTES + X_BYTES;
   // 64-column chunk of a row that unit u of group g holds
   static __host__ __device__ constexpr int chunk(int g, int u) { return (u < 2 ? 0 : LD / 128) + 2 * g + (u & 1); }
 };
@@ -90,13 +92,19 @@ struct Layout {
   static constexpr size_t bad = 2048;
   static constexpr size_t lse = 4096;
   static constexpr size_t o = lse + (size_t)2 * MAX_PAIRS * BM * 4;
+  // Partial outputs lie as the epilogue's threads hold them: for a slot and a CTA,
+  // four columns at a time, the 128 TMEM lanes side by side. This is the vector of
+  // lane `lane` (row lane & 63 of the CTA, columns from lane / 64 * LD / 2 + 4 c).
+  static __device__ int64_t vec(int LD, int slot, int rank, int c, int lane) {
+    return ((int64_t)(slot * 2 + rank) * (LD / 8) + c) * BM + lane;
+  }
   static size_t total(int LD) { return o + (size_t)2 * MAX_PAIRS * BM * LD * 4; }
 };
 static_assert(sizeof(Record) * MAX_PAIRS <= 2048 && 2 * MAX_PAIRS * 4 <= 2048 && Layout::o % 256 == 0, "layout");
 
 struct AttnP {
   const int32_t *cu, *kv_lens, *page_tables;
-  int32_t B, T, H, P, box, num_pages, max_pages, max_kv_len, table_cap;
+  int32_t B, T, H, P, box, num_pages, max_pages, max_kv_len, table_cap, out_32;
   float scale_log2;   // > 0
   void* out;
   float* lse;
@@ -170,45 +178,79 @@ __device__ __forceinline__ Seq load_seq(const AttnP& p, int b, bool report) {
   return s;
 }
 
-__device__ __forceinline__ void st_global_32B(void* p, const uint32_t (&w)[8]) {
+__device__ __forceinline__ void st_global_32B(void* p, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
 
-__device__ __forceinline__ void pair_bar_sync(int id) {
-  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
-}
-__device__ __forceinline__ void pair_bar_arrive(int id) {
-  asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
-}
+__device__ __forceinline__ void row_bar_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void row_bar_arrive(int id) { asm volatile("bar.arrive %0, 128;" ::"r"(id) : "memory"); }
+
+// A CTA's barriers and shared words, behind the tiles. k, v, q, p and sfree are
+// waited on in the even CTA, where both CTAs arrive; the MMA commits signal sdone,
+// odone, s and qempty in both.
+constexpr int NSEG = 4;
+template <int LD>
+struct State {
+  using C = Cfg<LD>;
+  // per step slot and group: loaded for S; read by S; loaded for O; read by O (after
+  // the last group: O is complete)
+  uint64_t k[C::NST][C::NG], sdone[C::NST][C::NG], v[C::NST][C::NG], odone[C::NST][C::NG];
+  uint64_t q, qempty;                 // Q loaded; the last S that reads it done
+  uint64_t vtail[C::NG];              // the reload of a last step, before its rows are zeroed
+  uint64_t s[2], sfree[2];            // S complete; read by the softmax warps
+  uint64_t p;                         // P written
+  uint64_t segfull[NSEG], segempty[NSEG], drain[2];
+  int64_t scan[NTHREADS / 32];
+  int64_t run, each;                  // steps of this pair's run, and of every pair's but the last
+  float x[2][4][HM];                  // row figures of a row's four threads, by step parity
+  Segment seg[NSEG];
+  int bad[NSEG];
+  int b0, tile0, step0;
+  int abort;
+  uint32_t tmem;
+};
 
 template <int LD, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mx, AttnP p) {
   using C = Cfg<LD>;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int NSEG = 4, NST = C::NST, NG = C::NG;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  constexpr int NST = C::NST, NG = C::NG;
+  extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char* sQ = sm;
   unsigned char* sK = sQ + C::Q_BYTES;               // [step][group][unit]
   unsigned char* sX = sK + NST * C::ST_BYTES;        // unit 0: P, keys 0-63; unit 1 + st: rotary unit of step slot st, then P, keys 64-127
-
-  // bar_k, bar_v, bar_q, bar_p and bar_sfree are waited on in the even CTA, where
-  // both CTAs arrive; the MMA commits signal bar_sdone, bar_odone and bar_qempty in both.
-  // Per step slot and group: loaded for S; read by S (after the last group: S
-  // is complete); loaded for O; read by O (after the last group: O is complete).
-  __shared__ __align__(8) uint64_t bar_k[NST][NG], bar_sdone[NST][NG], bar_v[NST][NG], bar_odone[NST][NG], bar_q,
-      bar_qempty, bar_vtail[NG], bar_s[2], bar_p, bar_sfree[2], bar_seg[NSEG], bar_segempty[NSEG], bar_drain[2];
-  __shared__ uint32_t s_tmem;
-  __shared__ Segment s_seg[NSEG];
-  __shared__ int s_bad[NSEG];
-  __shared__ volatile int s_abort;
-  __shared__ float s_x[2][2][HM];      // row figures of the two halves, by step parity
-  __shared__ int64_t s_scan[NTHREADS / 32];
-  __shared__ int64_t s_run, s_each;    // steps of this pair's run, and of every pair's but the last
-  __shared__ int s_b0, s_tile0, s_step0;
+  State<LD>& sh = *reinterpret_cast<State<LD>*>(sX + C::X_BYTES);
+  auto& bar_k = sh.k;
+  auto& bar_sdone = sh.sdone;
+  auto& bar_v = sh.v;
+  auto& bar_odone = sh.odone;
+  auto& bar_q = sh.q;
+  auto& bar_qempty = sh.qempty;
+  auto& bar_vtail = sh.vtail;
+  auto& bar_s = sh.s;
+  auto& bar_p = sh.p;
+  auto& bar_sfree = sh.sfree;
+  auto& bar_seg = sh.segfull;
+  auto& bar_segempty = sh.segempty;
+  auto& bar_drain = sh.drain;
+  auto& s_tmem = sh.tmem;
+  auto& s_seg = sh.seg;
+  auto& s_bad = sh.bad;
+  volatile int& s_abort = sh.abort;
+  auto& s_x = sh.x;
+  auto& s_scan = sh.scan;
+  auto& s_run = sh.run;
+  auto& s_each = sh.each;
+  auto& s_b0 = sh.b0;
+  auto& s_tile0 = sh.tile0;
+  auto& s_step0 = sh.step0;
+  if (smem_u32(sm) & 1023u) {   // the swizzled tiles need it; the array is declared so
+    if (threadIdx.x == 0) atomicOr(p.dev_status, PKV_DEV_TIMEOUT);
+    return;
+  }
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
@@ -226,15 +268,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       }
       mbar_init(&bar_vtail[g], 1);
     }
-    mbar_init(&bar_p, 8);        // the four softmax warps of both CTAs
+    mbar_init(&bar_p, 2 * SM_WARPS);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_s[i], 1);
-      mbar_init(&bar_sfree[i], 8);
+      mbar_init(&bar_sfree[i], 2 * SM_WARPS);
       mbar_init(&bar_drain[i], 1);
     }
     for (int e = 0; e < NSEG; ++e) {
       mbar_init(&bar_seg[e], 1);
-      mbar_init(&bar_segempty[e], rank == 0 ? 8 : 6);   // producers, MMA issuers, softmax warps
+      mbar_init(&bar_segempty[e], SM_WARPS + (rank == 0 ? 4 : 2));   // softmax, producers, MMA issuers
     }
     fence_mbar_init();
     s_abort = 0;
@@ -325,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   };
 
   bool ok = true;
-  if (warp == 8) {
+  if (warp == SM_FIRST + SM_WARPS) {
     // ------------------------------------------------------------- scheduler
     Record* rec = (Record*)(p.ws + Layout::rec) + pair;
     const int64_t each = s_each;
@@ -540,10 +582,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         } else {
           for (int j = 0; j < steps; ++j, ++n) {
             const uint32_t st = n % NST, par = (n / NST) & 1;
+            // the rows are there before P as a rule: their wait is over when P comes
+            if (!(ok = wait(&bar_v[st][0], par))) break;
             if (!(ok = wait(&bar_p, n & 1))) break;
 #pragma unroll
             for (int k = 0; k < NG; ++k) {
-              if (!(ok = wait(&bar_v[st][k], par))) break;
+              if (k > 0 && !(ok = wait(&bar_v[st][k], par))) break;
               tc_fence_after();
 #pragma unroll
               for (int x = 0; x < BN / 16; ++x)
@@ -565,10 +609,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   } else {
     // ----------------------------------------------------------------- softmax
     const int quarter = warp & 3, half = quarter >> 1;
+    const int sub = (warp - SM_FIRST) >> 2;         // which half of the lane's columns
+    const int who = half * 2 + sub;
     const int i = (quarter & 1) * 32 + lane;        // row of this CTA
     const uint32_t lrow = (uint32_t)(quarter * 32) << 16;
-    const int bar_id = 1 + (quarter & 1);           // the two warps of the same rows
+    const int bar_id = 1 + (quarter & 1);           // the four warps of the same rows
     const uint32_t p_bar = map_to_rank(&bar_p, 0), sfree_bar = map_to_rank(bar_sfree, 0);
+    constexpr int OC = LD / 4;                      // output columns of a thread
+    const uint32_t o_tmem = tmem + lrow + sub * OC;
     const float sc = p.scale_log2;
     uint32_t n = 0;                                  // steps before the current one
     for (uint32_t t = 0; ok; ++t) {
@@ -583,37 +631,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       for (int j = g.j0; j < g.j1; ++j, ++n) {
         if (!(ok = wait(&bar_s[n & 1], (n >> 1) & 1))) break;
         tc_fence_after();
-        uint32_t x[2][32];
-        tmem_ld32(tmem + lrow + S_COL + (n & 1) * 64, x[0]);
-        tmem_ld32(tmem + lrow + S_COL + (n & 1) * 64 + 32, x[1]);
+        uint32_t x[32];
+        tmem_ld32(tmem + lrow + S_COL + (n & 1) * 64 + sub * 32, x);
         // a warp that gave up takes part in no further exchange, so nobody goes on once the flag is up
         if (!(ok = !__any_sync(0xffffffffu, s_abort))) break;
         tmem_wait_ld();
-        reg_fence(x[0]);
-        reg_fence(x[1]);
+        reg_fence(x);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(sfree_bar + (n & 1) * 8);
         if (j >= j_mask) {
-          const int lim = pos - j * BN - half * 64;  // keys of this half up to lim are visible
+          const int lim = pos - j * BN - half * 64 - sub * 32;  // this thread's keys up to lim are visible
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c * 32 + k > lim) x[c][k] = __float_as_uint(-INFINITY);
+          for (int k = 0; k < 32; ++k)
+            if (k > lim) x[k] = __float_as_uint(-INFINITY);
         }
         float mx[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) mx[k] = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int k = 0; k < 32; k += 2)
-            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1]));
-        const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-        s_x[n & 1][half][i] = mine;
-        pair_bar_sync(bar_id);
-        const float mt = fmaxf(mine, s_x[n & 1][half ^ 1][i]) * sc;
+        for (int k = 0; k < 32; k += 2)
+          mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+        float (*sx)[HM] = s_x[n & 1];
+        sx[who][i] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        row_bar_sync(bar_id);
+        const float mt = fmaxf(max3(sx[0][i], sx[1][i], sx[2][i]), sx[3][i]) * sc;
         const bool first = j == g.j0;
         const bool grow = first || mt > m_run + RESCALE_LOG2;
         const float m_new = grow ? fmaxf(mt, m_run) : m_run;
@@ -625,12 +667,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         float2 ls[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
-        uint32_t w[32];
+        uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int k0 = 2 * k;
-          const float2 y = __ffma2_rn(
-              make_float2(__uint_as_float(x[k0 >> 5][k0 & 31]), __uint_as_float(x[k0 >> 5][(k0 & 31) + 1])), sc2, nm2);
+        for (int k = 0; k < 16; ++k) {
+          const float2 y =
+              __ffma2_rn(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sc2, nm2);
           const float a = ex2(y.x), b = ex2(y.y);
           ls[k & 3] = __fadd2_rn(ls[k & 3], make_float2(a, b));
           w[k] = pack2<T>(a, b);
@@ -646,19 +687,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           tc_fence_after();
           if (rescale) {
 #pragma unroll 1
-            for (int c = 0; c < LD / 64; ++c) {
+            for (int c = 0; c < OC / 32; ++c) {
               uint32_t o[32];
-              tmem_ld32_wait(tmem + lrow + c * 32, o);
+              tmem_ld32_wait(o_tmem + c * 32, o);
 #pragma unroll
               for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st32_wait(tmem + lrow + c * 32, o);
+              tmem_st32_wait(o_tmem + c * 32, o);
             }
           }
         }
         unsigned char* p_row = sX + (half ? 1 + n % NST : 0) * UNIT + i * 128;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(p_row + ((c ^ (i & 7)) << 4)) =
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(p_row + (((sub * 4 + c) ^ (i & 7)) << 4)) =
               make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
@@ -666,10 +707,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         if (lane == 0) mbar_arrive_cluster(p_bar);
       }
       if (!ok) break;
-      // epilogue: the two halves' sums, then this half's LD / 2 output columns
-      s_x[n & 1][half][i] = l_run;
-      pair_bar_sync(bar_id);
-      const float l = l_run + s_x[n & 1][half ^ 1][i];
+      // epilogue: the row's sum, then this thread's OC output columns
+      float (*sx)[HM] = s_x[n & 1];
+      sx[who][i] = l_run;
+      row_bar_sync(bar_id);
+      const float l = (sx[0][i] + sx[1][i]) + (sx[2][i] + sx[3][i]);
       if (!(ok = wait(&bar_odone[(n - 1) % NST][NG - 1], ((n - 1) / NST) & 1))) break;
       tc_fence_after();
       const int bad = *(volatile int*)&s_bad[e];
@@ -678,40 +720,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       const int slot = 2 * pair + (g.j0 == 0 ? 1 : 0);
       const float inv = m_run == -INFINITY ? 0.f : 1.f / l;   // no visible key in a partial run: zeros
       const int64_t row = (int64_t)g.row0 + r;
-      T* dst = (T*)p.out + row * LD + half * (LD / 2);
-      float* part = (float*)(p.ws + Layout::o) + ((int64_t)slot * BM + r) * LD + half * (LD / 2);
+      T* dst = (T*)p.out + row * LD + half * (LD / 2) + sub * OC;
+      float4* part = (float4*)(p.ws + Layout::o) + Layout::vec(LD, slot, rank, sub * (OC / 4), quarter * 32 + lane);
 #pragma unroll 1
-      for (int c = 0; c < LD / 64; ++c) {
+      for (int c = 0; c < OC / 32; ++c) {
         uint32_t o[32];
-        tmem_ld32_wait(tmem + lrow + c * 32, o);
+        tmem_ld32_wait(o_tmem + c * 32, o);
         if (!store) continue;
         if (whole) {
+          uint32_t y[16];
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            uint32_t y[8];
+          for (int k = 0; k < 16; ++k)
+            y[k] = pack2<T>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+          if (p.out_32) {   // whole sectors, where out's alignment allows it
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              y[k] = pack2<T>(__uint_as_float(o[v * 16 + 2 * k]) * inv, __uint_as_float(o[v * 16 + 2 * k + 1]) * inv);
-            // out is 16-byte aligned, a row a multiple of 512 bytes
-            *reinterpret_cast<uint4*>(dst + c * 32 + v * 16) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(dst + c * 32 + v * 16 + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+            for (int v = 0; v < 2; ++v) st_global_32B(dst + c * 32 + v * 16, y + v * 8);
+          } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              *reinterpret_cast<uint4*>(dst + c * 32 + v * 8) =
+                  make_uint4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
           }
         } else {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t y[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(o[v * 8 + k]) * inv);
-            st_global_32B(part + c * 32 + v * 8, y);
-          }
+          for (int v = 0; v < 8; ++v)
+            part[(c * 8 + v) * BM] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                                 __uint_as_float(o[4 * v + 2]) * inv,
+                                                 __uint_as_float(o[4 * v + 3]) * inv);
         }
       }
-      if (store && half == 0) {
+      if (store && who == 0) {
         const float lg = m_run == -INFINITY ? -INFINITY : m_run + __log2f(l);
         if (!whole) ((float*)(p.ws + Layout::lse))[slot * BM + r] = lg;
         else if (p.lse) p.lse[row] = lg * LN2;
       }
-      if (r == 0 && half == 0) {
+      if (r == 0 && who == 0) {
         if (!whole) ((int32_t*)(p.ws + Layout::bad))[slot] = bad;
         if (bad) atomicOr(p.dev_status, PKV_DEV_BAD_PAGE);
       }
@@ -719,7 +762,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_segempty[e]);
     }
-    if (!ok) pair_bar_arrive(bar_id);   // lets the other warp of these rows leave its exchange
+    if (!ok) row_bar_arrive(bar_id);   // lets the other warps of these rows leave their exchange
   }
 
   if (s_abort && (warp == 0 || warp == 2)) {
@@ -740,69 +783,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, TMEM_COLS);
 }
 
-// Joins the partial results of every cut tile. One warp per row: the weights
-// 2^(lse_s - max) of its parts, then the weighted sum of their outputs, in the
-// order of the keys.
+// Joins the partial results of every cut tile: a row's parts weighted by
+// 2^(lse_s - max), in the order of the keys. A block takes 8 rows of a CTA's 64 and
+// 32 column vectors of one half; 8 threads read the 128 bytes of 8 lanes.
+constexpr int CROWS = 8, CVECS = 32;
 template <int LD, typename T>
-__global__ void __launch_bounds__(128) latent_combine_kernel(char* ws, T* out, float* lse) {
+__global__ void __launch_bounds__(CROWS * CVECS) latent_combine_kernel(char* ws, T* out, float* lse) {
+  __shared__ float s_w[CROWS][MAX_PAIRS];
+  __shared__ float s_m[CROWS], s_inv[CROWS];
   pdl_wait();
   const int pair = blockIdx.x;
   const Record rec = ((const Record*)(ws + Layout::rec))[pair];
-  if (rec.parts == 0) return;
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= rec.nrows) return;
+  const int r0 = blockIdx.y * CROWS;
+  if (r0 >= rec.nrows) return;   // no cut tile (nrows 0), or not that many rows
   const float* sums = (const float*)(ws + Layout::lse);
   const int32_t* bad = (const int32_t*)(ws + Layout::bad);
   auto slot = [&](int s) { return s == 0 ? 2 * pair + 1 : 2 * (pair + s); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // warp w: the weights of row r0 + w (rows behind nrows: unused values)
   float m = -INFINITY;
   int any = 0;
   for (int s = lane; s < rec.parts; s += 32) {
-    m = fmaxf(m, sums[slot(s) * BM + r]);
+    const float y = sums[slot(s) * BM + r0 + warp];
+    s_w[warp][s] = y;
+    m = fmaxf(m, y);
     any |= bad[slot(s)];
   }
   m = warp_max(m);
-  if (__any_sync(0xffffffffu, any)) return;
-  constexpr int NV = LD / 128;   // float4s of a lane
-  float4 o[NV];
-#pragma unroll
-  for (int k = 0; k < NV; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   float total = 0.f;
-  const float4* parts = (const float4*)(ws + Layout::o);
-#pragma unroll 4
-  for (int s = 0; s < rec.parts; ++s) {
-    const float w = exp2f(sums[slot(s) * BM + r] - m);
+  for (int s = lane; s < rec.parts; s += 32) {
+    const float w = exp2f(s_w[warp][s] - m);
+    s_w[warp][s] = w;
     total += w;
-    const float4* x = parts + ((int64_t)slot(s) * BM + r) * (LD / 4) + lane;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const float4 y = x[k * 32];
-      o[k].x += w * y.x;
-      o[k].y += w * y.y;
-      o[k].z += w * y.z;
-      o[k].w += w * y.w;
+  }
+  total = warp_sum(total);
+  if (lane == 0) {
+    s_m[warp] = m + log2f(total);
+    s_inv[warp] = 1.f / total;
+  }
+  if (__syncthreads_or(any)) return;
+  const int rr = threadIdx.x % CROWS, r = r0 + rr, rank = r / HM;
+  constexpr int ZH = LD / 8 / CVECS;   // blocks along a half's columns
+  const int half = blockIdx.z / ZH, c = blockIdx.z % ZH * CVECS + threadIdx.x / CROWS;
+  const float4* parts = (const float4*)(ws + Layout::o);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < rec.nrows) {
+#pragma unroll 8
+    for (int s = 0; s < rec.parts; ++s) {
+      const float w = s_w[rr][s];
+      const float4 y = parts[Layout::vec(LD, slot(s), rank, c, half * HM + r % HM)];
+      o.x += w * y.x;
+      o.y += w * y.y;
+      o.z += w * y.z;
+      o.w += w * y.w;
     }
-  }
-  const float inv = 1.f / total;
-  const int64_t row = (int64_t)rec.row0 + r;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
+    const float inv = s_inv[rr];
+    const int64_t row = (int64_t)rec.row0 + r;
     uint2 y;
-    y.x = pack2<T>(o[k].x * inv, o[k].y * inv);
-    y.y = pack2<T>(o[k].z * inv, o[k].w * inv);
-    *reinterpret_cast<uint2*>(out + row * LD + k * 128 + lane * 4) = y;
+    y.x = pack2<T>(o.x * inv, o.y * inv);
+    y.y = pack2<T>(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(out + row * LD + half * (LD / 2) + c * 4) = y;
+    if (lse && blockIdx.z == 0 && threadIdx.x < CROWS) lse[row] = s_m[rr] * LN2;
   }
-  if (lse && lane == 0) lse[row] = (m + log2f(total)) * LN2;
 }
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
 template <int LD, typename T>
 cudaError_t launch(const LatentAttnArgs& a, cudaStream_t s) {
-  using C = Cfg<LD>;
+  constexpr int smem = Cfg<LD>::TILES + sizeof(State<LD>);
+  static_assert(smem <= 232448, "shared memory");
   static std::atomic<uint64_t> ready{0};   // devices whose kernel attribute is set
   if (!(ready.load() >> a.dev.id & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(latent_attn_kernel<LD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               C::SMEM);
+                                               smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << a.dev.id);
   }
@@ -823,6 +877,7 @@ cudaError_t launch(const LatentAttnArgs& a, cudaStream_t s) {
   p.table_cap = a.max_pages * a.P;
   p.scale_log2 = a.scale * LOG2E;
   p.out = a.out;
+  p.out_32 = ((uintptr_t)a.out & 31) == 0;
   p.lse = a.lse;
   p.ws = a.ws;
   p.dev_status = a.dev.status;
@@ -834,11 +889,12 @@ cudaError_t launch(const LatentAttnArgs& a, cudaStream_t s) {
   cudaError_t e;
   {
     KernelTimer timer("latent_attn", s);
-    e = launch_after_trigger(latent_attn_kernel<LD, T>, dim3(2 * pairs), dim3(NTHREADS), C::SMEM, s, mq, mx, p);
+    e = launch_after_trigger(latent_attn_kernel<LD, T>, dim3(2 * pairs), dim3(NTHREADS), smem, s, mq, mx, p);
   }
   if (e != cudaSuccess) return e;
   KernelTimer timer("latent_combine", s);
-  return launch_after_trigger(latent_combine_kernel<LD, T>, dim3(pairs, BM / 4), dim3(128), 0, s, a.ws, (T*)a.out,
+  return launch_after_trigger(latent_combine_kernel<LD, T>, dim3(pairs, BM / CROWS, 2 * LD / 8 / CVECS),
+                              dim3(CROWS * CVECS), 0, s, a.ws, (T*)a.out,
                               a.lse);
 }
 
