@@ -82,10 +82,11 @@ constexpr long long WAIT_LIMIT_CLOCKS = 4000000000ll;   // about two seconds
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t S_COL = 256;
 
-// Workspace: a record per pair (the tile that the pair's run cuts at its end),
+// Workspace: a record per pair (the tile that the pair's run cuts at its end: its
+// first pair, and how many pairs share it),
 // then a bad flag, log2 sums and outputs for two partial results per pair.
 struct Record {
-  int32_t parts, row0, nrows, pad;   // parts 0: no cut tile
+  int32_t parts, row0, nrows, owner;   // nrows 0: no cut tile
 };
 struct Layout {
   static constexpr size_t rec = 0;
@@ -117,7 +118,6 @@ struct Segment {
   int valid, b, L, base;      // base: keys before the sequence's first new token
   int row0, frow0, nrows;     // first packed row, first row within the sequence, rows
   int j0, j1, n;              // n: steps of the whole tile
-  int parts;                  // > 0: the cut tile starts here; pairs that share it
 };
 
 // One sequence's tiles. Tile t covers rows [128 t, 128 t + 128) of its q_len * H
@@ -145,6 +145,11 @@ struct Seq {
   }
   // tile and step of the sequence's step number `at`
   __device__ __forceinline__ void seek(int64_t at, int* tile, int* step) const {
+    if (tiles == 1) {
+      *tile = 0;
+      *step = (int)at;
+      return;
+    }
     const int lo = steps(0), hi = steps(tiles - 1);
     int before = 0;
     for (int v = lo; v <= hi; ++v) {
@@ -400,12 +405,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         g.n = s.steps(tile);
         g.j0 = step;
         g.j1 = (int)min((int64_t)g.n, step + left);
-        g.parts = 0;
-        if (g.j0 == 0 && g.j1 < g.n) {
-          // global step numbers: this run starts at pair * each
-          const int64_t end = pair * each + done + g.n;
-          g.parts = (int)((end - 1) / each) - pair + 1;
-          r.parts = g.parts;
+        if (g.j1 < g.n) {
+          // the tile's first step among the tick's (this run starts at pair * each)
+          const int64_t begin = pair * each + done - g.j0;
+          r.owner = (int)(begin / each);
+          r.parts = (int)((begin + g.n - 1) / each) - r.owner + 1;
           r.row0 = g.row0;
           r.nrows = g.nrows;
         }
@@ -625,6 +629,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       const Segment g = s_seg[e];
       if (!g.valid) break;
       const int r = (int)rank * HM + i;              // row of the tile
+      const bool warp_rows = (int)rank * HM + (quarter & 1) * 32 < g.nrows;   // some row of this warp is there
       const int pos = min(g.base + (g.frow0 + r) / p.H, g.L - 1);
       const int j_mask = (g.base + g.frow0 / p.H + 1) / BN;   // steps before see no hidden key
       float m_run = -INFINITY, l_run = 0.f;
@@ -668,6 +673,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
         uint32_t w[16];
+        if (warp_rows) {   // else: P of rows that nobody reads stays as it is
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const float2 y =
@@ -675,6 +681,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           const float a = ex2(y.x), b = ex2(y.y);
           ls[k & 3] = __fadd2_rn(ls[k & 3], make_float2(a, b));
           w[k] = pack2<T>(a, b);
+        }
         }
         // m_run = m_new = -inf before the first visible key: alpha would be NaN
         const float f = m_new == -INFINITY ? 1.f : alpha;
@@ -697,6 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
         }
         unsigned char* p_row = sX + (half ? 1 + n % NST : 0) * UNIT + i * 128;
+        if (warp_rows)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<uint4*>(p_row + (((sub * 4 + c) ^ (i & 7)) << 4)) =
@@ -784,66 +792,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 }
 
 // Joins the partial results of every cut tile: a row's parts weighted by
-// 2^(lse_s - max), in the order of the keys. A block takes 8 rows of a CTA's 64 and
-// 32 column vectors of one half; 8 threads read the 128 bytes of 8 lanes.
-constexpr int CROWS = 8, CVECS = 32;
+// 2^(lse_s - max), in the order of the keys. A block takes 32 column vectors of one
+// half and every 8th group of 8 rows; 8 threads read the 128 bytes of 8 lanes. The
+// blocks of all pairs but the last that share a tile divide its row groups, so that
+// a tile of many parts has many blocks (one pair's blocks alone took 60 us for a
+// context of 131 k keys, against 18). No shared memory: the blocks get resident beside the attention kernel's,
+// which leave none, and start when the last of those ends.
+constexpr int CROWS = 8, CVECS = 32, CY = 8;
 template <int LD, typename T>
-__global__ void __launch_bounds__(CROWS * CVECS) latent_combine_kernel(char* ws, T* out, float* lse) {
-  __shared__ float s_w[CROWS][MAX_PAIRS];
-  __shared__ float s_m[CROWS], s_inv[CROWS];
+__global__ void __launch_bounds__(CROWS * CVECS, 4) latent_combine_kernel(char* ws, T* out, float* lse) {
   pdl_wait();
+  pdl_trigger();   // what the next call does before its own wait touches nothing of this one's
   const int pair = blockIdx.x;
   const Record rec = ((const Record*)(ws + Layout::rec))[pair];
-  const int r0 = blockIdx.y * CROWS;
+  const int step = CY * CROWS * (rec.parts - 1);
+  const int r0 = ((int)blockIdx.y + CY * (pair - rec.owner)) * CROWS;   // this block's first row
   if (r0 >= rec.nrows) return;   // no cut tile (nrows 0), or not that many rows
   const float* sums = (const float*)(ws + Layout::lse);
   const int32_t* bad = (const int32_t*)(ws + Layout::bad);
-  auto slot = [&](int s) { return s == 0 ? 2 * pair + 1 : 2 * (pair + s); };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // warp w: the weights of row r0 + w (rows behind nrows: unused values)
-  float m = -INFINITY;
-  int any = 0;
-  for (int s = lane; s < rec.parts; s += 32) {
-    const float y = sums[slot(s) * BM + r0 + warp];
-    s_w[warp][s] = y;
-    m = fmaxf(m, y);
-    any |= bad[slot(s)];
-  }
-  m = warp_max(m);
-  float total = 0.f;
-  for (int s = lane; s < rec.parts; s += 32) {
-    const float w = exp2f(s_w[warp][s] - m);
-    s_w[warp][s] = w;
-    total += w;
-  }
-  total = warp_sum(total);
-  if (lane == 0) {
-    s_m[warp] = m + log2f(total);
-    s_inv[warp] = 1.f / total;
-  }
-  if (__syncthreads_or(any)) return;
-  const int rr = threadIdx.x % CROWS, r = r0 + rr, rank = r / HM;
+  auto slot = [&](int s) { return s == 0 ? 2 * rec.owner + 1 : 2 * (rec.owner + s); };
+  const int rr = threadIdx.x % CROWS, q = threadIdx.x / CROWS % 4;   // a warp: 8 rows x 4 vectors
   constexpr int ZH = LD / 8 / CVECS;   // blocks along a half's columns
   const int half = blockIdx.z / ZH, c = blockIdx.z % ZH * CVECS + threadIdx.x / CROWS;
   const float4* parts = (const float4*)(ws + Layout::o);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (r < rec.nrows) {
-#pragma unroll 8
-    for (int s = 0; s < rec.parts; ++s) {
-      const float w = s_w[rr][s];
-      const float4 y = parts[Layout::vec(LD, slot(s), rank, c, half * HM + r % HM)];
-      o.x += w * y.x;
-      o.y += w * y.y;
-      o.z += w * y.z;
-      o.w += w * y.w;
+  int any = 0;
+  for (int s = threadIdx.x; s < rec.parts; s += blockDim.x) any |= bad[slot(s)];
+  if (__syncthreads_or(any)) return;
+  constexpr int K = BM / CROWS / CY;   // row groups of a block
+  float m[K], total[K];
+  float4 o[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    m[k] = -INFINITY;
+    total[k] = 0.f;
+    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // the four threads of a row in a warp share the search for its maximum
+  for (int s = q; s < rec.parts; s += 4)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int r = r0 + step * k + rr;
+      if (r < rec.nrows) m[k] = fmaxf(m[k], sums[slot(s) * BM + r]);
     }
-    const float inv = s_inv[rr];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 8));
+    m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 16));
+  }
+  // two parts of every row group at a time: 8 loads in flight a thread
+  for (int s = 0; s < rec.parts; s += 2) {
+    float w[2][K];
+    float4 y[2][K];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int r = r0 + step * k + rr;
+        w[u][k] = -INFINITY;
+        y[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rec.nrows && s + u < rec.parts) {
+          w[u][k] = sums[slot(s + u) * BM + r];
+          y[u][k] = parts[Layout::vec(LD, slot(s + u), r / HM, c, half * HM + r % HM)];
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const float f = exp2f(w[u][k] - m[k]);
+        total[k] += f;
+        o[k].x += f * y[u][k].x;
+        o[k].y += f * y[u][k].y;
+        o[k].z += f * y[u][k].z;
+        o[k].w += f * y[u][k].w;
+      }
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int r = r0 + step * k + rr;
+    if (r >= rec.nrows) continue;
+    const float inv = 1.f / total[k];
     const int64_t row = (int64_t)rec.row0 + r;
     uint2 y;
-    y.x = pack2<T>(o.x * inv, o.y * inv);
-    y.y = pack2<T>(o.z * inv, o.w * inv);
+    y.x = pack2<T>(o[k].x * inv, o[k].y * inv);
+    y.y = pack2<T>(o[k].z * inv, o[k].w * inv);
     *reinterpret_cast<uint2*>(out + row * LD + half * (LD / 2) + c * 4) = y;
-    if (lse && blockIdx.z == 0 && threadIdx.x < CROWS) lse[row] = s_m[rr] * LN2;
+    if (lse && blockIdx.z == 0 && threadIdx.x < CROWS) lse[row] = (m[k] + log2f(total[k])) * LN2;
   }
 }
 
@@ -893,7 +927,7 @@ cudaError_t launch(const LatentAttnArgs& a, cudaStream_t s) {
   }
   if (e != cudaSuccess) return e;
   KernelTimer timer("latent_combine", s);
-  return launch_after_trigger(latent_combine_kernel<LD, T>, dim3(pairs, BM / CROWS, 2 * LD / 8 / CVECS),
+  return launch_after_trigger(latent_combine_kernel<LD, T>, dim3(pairs, CY, 2 * LD / 8 / CVECS),
                               dim3(CROWS * CVECS), 0, s, a.ws, (T*)a.out,
                               a.lse);
 }
