@@ -21,7 +21,8 @@ SOURCES = ["pkv_api.cu", "pkv_append.cu", "pkv_plan.cu", "pkv_rows.cu", "pkv_pre
            "pkv_no_alloc.cu", "pkv_decode.cu", "pkv_decode_bf16.cu", "pkv_decode_f16.cu", "pkv_decode_f32.cu",
            "pkv_decode_fp8.cu", "pkv_tma.cu",
            "pkv_prefill_tc2.cu", "pkv_pool.cpp", "pkv_rope.cu", "pkv_selftest.cu",
-           "pkv_latent_api.cu", "pkv_latent_move.cu", "pkv_latent_attn.cu", "pkv_latent_prefill.cu"]
+           "pkv_latent_api.cu", "pkv_latent_move.cu", "pkv_latent_attn.cu",
+           "pkv_latent_rows.cu", "pkv_latent_prefill.cu"]
 
 
 def nvcc():

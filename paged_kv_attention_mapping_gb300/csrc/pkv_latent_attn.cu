@@ -43,6 +43,7 @@
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 #include "pkv_latent.cuh"
+#include "pkv_latent_sched.cuh"
 #include "pkv_sm100.cuh"
 
 namespace pkv {
@@ -82,12 +83,7 @@ constexpr long long WAIT_LIMIT_CLOCKS = 4000000000ll;   // about two seconds
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t S_COL = 256;
 
-// Workspace: a record per pair (the tile that the pair's run cuts at its end: its
-// first pair, and how many pairs share it),
-// then a bad flag, log2 sums and outputs for two partial results per pair.
-struct Record {
-  int32_t parts, row0, nrows, owner;   // nrows 0: no cut tile
-};
+// Workspace: a record per pair, then a bad flag, log2 sums and outputs for two partial results per pair.
 struct Layout {
   static constexpr size_t rec = 0;
   static constexpr size_t bad = 2048;
@@ -101,87 +97,7 @@ struct Layout {
   }
   static size_t total(int LD) { return o + (size_t)2 * MAX_PAIRS * BM * LD * 4; }
 };
-static_assert(sizeof(Record) * MAX_PAIRS <= 2048 && 2 * MAX_PAIRS * 4 <= 2048 && Layout::o % 256 == 0, "layout");
-
-struct AttnP {
-  const int32_t *cu, *kv_lens, *page_tables;
-  int32_t B, T, H, P, box, num_pages, max_pages, max_kv_len, table_cap, out_32;
-  float scale_log2;   // > 0
-  void* out;
-  float* lse;
-  char* ws;
-  int32_t* dev_status;
-};
-
-// A run of steps [j0, j1) of one tile.
-struct Segment {
-  int valid, b, L, base;      // base: keys before the sequence's first new token
-  int row0, frow0, nrows;     // first packed row, first row within the sequence, rows
-  int j0, j1, n;              // n: steps of the whole tile
-};
-
-// One sequence's tiles. Tile t covers rows [128 t, 128 t + 128) of its q_len * H
-// and needs the keys up to its last row's position.
-struct Seq {
-  int q, L, base, H, rows, tiles;
-  __device__ __forceinline__ int steps(int t) const {
-    const int last = (min((t + 1) * BM, rows) - 1) / H;
-    return (base + last + BN) / BN;
-  }
-  // tiles with at most v steps (steps() never falls from one tile to the next)
-  __device__ __forceinline__ int tiles_within(int v) const {
-    const int64_t e = (int64_t)v * BN - base;   // tokens that see at most v * BN keys
-    if (e >= q) return tiles;
-    if (e <= 0) return 0;
-    return min(tiles - 1, (int)(e * H / BM));
-  }
-  __device__ __forceinline__ int64_t total() const {
-    if (tiles == 0) return 0;
-    if (tiles == 1) return (L + BN - 1) / BN;
-    const int lo = steps(0), hi = steps(tiles - 1);
-    int64_t s = (int64_t)hi * tiles;
-    for (int v = lo; v < hi; ++v) s -= tiles_within(v);
-    return s;
-  }
-  // tile and step of the sequence's step number `at`
-  __device__ __forceinline__ void seek(int64_t at, int* tile, int* step) const {
-    if (tiles == 1) {
-      *tile = 0;
-      *step = (int)at;
-      return;
-    }
-    const int lo = steps(0), hi = steps(tiles - 1);
-    int before = 0;
-    for (int v = lo; v <= hi; ++v) {
-      const int upto = v == hi ? tiles : tiles_within(v);
-      const int64_t s = (int64_t)(upto - before) * v;
-      if (at < s) {
-        *tile = before + (int)(at / v);
-        *step = (int)(at % v);
-        return;
-      }
-      at -= s;
-      before = upto;
-    }
-  }
-};
-
-__device__ __forceinline__ Seq load_seq(const AttnP& p, int b, bool report) {
-  Seq s;
-  const int c0 = __ldg(p.cu + b);
-  s.q = __ldg(p.cu + b + 1) - c0;
-  s.L = __ldg(p.kv_lens + b);
-  s.H = p.H;
-  s.base = s.L - s.q;
-  s.rows = s.q * p.H;
-  s.tiles = (s.rows + BM - 1) / BM;
-  if (s.q > 0 && (s.L < s.q || s.L > p.max_kv_len || s.L > p.table_cap)) {
-    if (report) atomicOr(p.dev_status, PKV_DEV_BAD_LENGTHS);
-    s.tiles = 0;
-  }
-  if (s.q <= 0 || s.q > p.T) s.tiles = 0;
-  return s;
-}
+static_assert(sizeof(LatentRecord) * MAX_PAIRS <= 2048 && 2 * MAX_PAIRS * 4 <= 2048 && Layout::o % 256 == 0, "layout");
 
 __device__ __forceinline__ void st_global_32B(void* p, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
@@ -207,19 +123,17 @@ struct State {
   uint64_t s[2], sfree[2];            // S complete; read by the softmax warps
   uint64_t p;                         // P written
   uint64_t segfull[NSEG], segempty[NSEG], drain[2];
-  int64_t scan[NTHREADS / 32];
-  int64_t run, each;                  // steps of this pair's run, and of every pair's but the last
+  LatentPlan<NTHREADS> plan;
   float x[2][4][HM];                  // row figures of a row's four threads, by step parity
-  Segment seg[NSEG];
+  LatentSegment seg[NSEG];
   int bad[NSEG];
-  int b0, tile0, step0;
   int abort;
   uint32_t tmem;
 };
 
 template <int LD, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
-    latent_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mx, AttnP p) {
+    latent_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mx, LatentAttnP p) {
   using C = Cfg<LD>;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int NST = C::NST, NG = C::NG;
@@ -246,12 +160,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   auto& s_bad = sh.bad;
   volatile int& s_abort = sh.abort;
   auto& s_x = sh.x;
-  auto& s_scan = sh.scan;
-  auto& s_run = sh.run;
-  auto& s_each = sh.each;
-  auto& s_b0 = sh.b0;
-  auto& s_tile0 = sh.tile0;
-  auto& s_step0 = sh.step0;
   if (smem_u32(sm) & 1023u) {   // the swizzled tiles need it; the array is declared so
     if (threadIdx.x == 0) atomicOr(p.dev_status, PKV_DEV_TIMEOUT);
     return;
@@ -285,65 +193,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     }
     fence_mbar_init();
     s_abort = 0;
-    s_run = 0;
+    sh.plan.run = 0;
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mx);
   }
   if (warp == 1) tmem_alloc_pair(&s_tmem, TMEM_COLS);
 
-  // ------------------------------------------------------------------- plan
-  // Every CTA computes the whole tick's step count and where its own run starts
-  // (reads only the lengths, so this runs before the wait for the kernel before).
-  {
-    bool bad = tid == 0 && __ldg(p.cu) != 0;
-    const int per = (p.B + NTHREADS - 1) / NTHREADS;
-    const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
-    int64_t mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) {
-      const Seq s = load_seq(p, b, blockIdx.x == 0);
-      bad |= s.q < 0;
-      mine += s.total();
-    }
-    bad |= __ldg(p.cu + p.B) > p.T;
-    int64_t scan = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, scan, o);
-      if (lane >= o) scan += y;
-    }
-    if (lane == 31) s_scan[warp] = scan;
-    bad = __syncthreads_or(bad);
-    int64_t total = 0, before = scan - mine;
-#pragma unroll
-    for (int w = 0; w < NTHREADS / 32; ++w) {
-      if (w < warp) before += s_scan[w];
-      total += s_scan[w];
-    }
-    if (bad) {
-      if (blockIdx.x == 0 && tid == 0) atomicOr(p.dev_status, PKV_DEV_BAD_LENGTHS);
-      total = 0;
-    }
-    const int64_t each = (total + pairs - 1) / pairs;
-    const int64_t lo = pair * each, hi = min(lo + each, total);
-    if (lo < hi && lo >= before && lo < before + mine) {
-      int64_t at = lo - before;
-      for (int b = b_lo; b < b_hi; ++b) {
-        const Seq s = load_seq(p, b, false);
-        const int64_t n = s.total();
-        if (at < n) {
-          int tile, step;
-          s.seek(at, &tile, &step);
-          s_b0 = b;
-          s_tile0 = tile;
-          s_step0 = step;
-          break;
-        }
-        at -= n;
-      }
-      s_run = hi - lo;
-    }
-    if (tid == 0) s_each = each;
-  }
+  __syncthreads();
+  latent_plan<BM, BN, NTHREADS>(p, pair, pairs, &sh.plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -374,50 +231,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   bool ok = true;
   if (warp == SM_FIRST + SM_WARPS) {
     // ------------------------------------------------------------- scheduler
-    Record* rec = (Record*)(p.ws + Layout::rec) + pair;
-    const int64_t each = s_each;
-    int64_t left = s_run;
-    int64_t done = 0;
-    int b = left > 0 ? s_b0 : 0, tile = left > 0 ? s_tile0 : 0, step = left > 0 ? s_step0 : 0;
-    Seq s{};
-    if (left > 0) s = load_seq(p, b, false);
-    Record r{0, 0, 0, 0};
+    LatentRun<BM, BN> run(p, sh.plan, pair);
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t % NSEG;
       if (t >= NSEG && !(ok = wait(&bar_segempty[e], ((t / NSEG) - 1) & 1))) break;
-      Segment g;
-      g.valid = 0;
-      if (left > 0) {
-        // left > 0 promises one more tile, as long as nobody rewrites the lengths meanwhile
-        while (tile >= s.tiles && ++b < p.B) {
-          s = load_seq(p, b, false);
-          tile = 0;
-        }
-        g.valid = tile < s.tiles;
-      }
-      if (g.valid) {
-        g.b = b;
-        g.L = s.L;
-        g.base = s.base;
-        g.frow0 = tile * BM;
-        g.row0 = __ldg(p.cu + b) * p.H + tile * BM;
-        g.nrows = min(BM, s.rows - tile * BM);
-        g.n = s.steps(tile);
-        g.j0 = step;
-        g.j1 = (int)min((int64_t)g.n, step + left);
-        if (g.j1 < g.n) {
-          // the tile's first step among the tick's (this run starts at pair * each)
-          const int64_t begin = pair * each + done - g.j0;
-          r.owner = (int)(begin / each);
-          r.parts = (int)((begin + g.n - 1) / each) - r.owner + 1;
-          r.row0 = g.row0;
-          r.nrows = g.nrows;
-        }
-        left -= g.j1 - g.j0;
-        done += g.j1 - g.j0;
-        ++tile;
-        step = 0;
-      }
+      const LatentSegment g = run.next(p);
       if (lane == 0) {
         s_seg[e] = g;
         s_bad[e] = 0;
@@ -426,7 +244,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       __syncwarp();
       if (!g.valid) break;
     }
-    if (rank == 0 && lane == 0) *rec = r;
+    if (rank == 0 && lane == 0) ((LatentRecord*)(p.ws + Layout::rec))[pair] = run.r;
   } else if (warp == 0 || warp == 2) {
     // --------------------------------------------------------------- producers
     // Warp 0 loads Q and this CTA's 64 keys of each step, warp 2 the peer's 64
@@ -441,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t % NSEG;
       if (!(ok = wait(&bar_seg[e], (t / NSEG) & 1))) break;
-      const Segment g = s_seg[e];
+      const LatentSegment g = s_seg[e];
       if (!g.valid) break;
       const int32_t* pt = p.page_tables + (int64_t)g.b * p.max_pages;
       const int keys = min(g.L, g.n * BN);   // keys that the tile needs
@@ -550,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       for (uint32_t t = 0; ok; ++t) {
         const uint32_t e = t % NSEG;
         if (!(ok = wait(&bar_seg[e], (t / NSEG) & 1))) break;
-        const Segment g = s_seg[e];
+        const LatentSegment g = s_seg[e];
         if (!g.valid) break;
         const int steps = g.j1 - g.j0;
         if (warp == 1) {
@@ -626,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t % NSEG;
       if (!(ok = wait(&bar_seg[e], (t / NSEG) & 1))) break;
-      const Segment g = s_seg[e];
+      const LatentSegment g = s_seg[e];
       if (!g.valid) break;
       const int r = (int)rank * HM + i;              // row of the tile
       const bool warp_rows = (int)rank * HM + (quarter & 1) * 32 < g.nrows;   // some row of this warp is there
@@ -802,9 +620,8 @@ constexpr int CROWS = 8, CVECS = 32, CY = 8;
 template <int LD, typename T>
 __global__ void __launch_bounds__(CROWS * CVECS, 4) latent_combine_kernel(char* ws, T* out, float* lse) {
   pdl_wait();
-  pdl_trigger();   // what the next call does before its own wait touches nothing of this one's
   const int pair = blockIdx.x;
-  const Record rec = ((const Record*)(ws + Layout::rec))[pair];
+  const LatentRecord rec = ((const LatentRecord*)(ws + Layout::rec))[pair];
   const int step = CY * CROWS * (rec.parts - 1);
   const int r0 = ((int)blockIdx.y + CY * (pair - rec.owner)) * CROWS;   // this block's first row
   if (r0 >= rec.nrows) return;   // no cut tile (nrows 0), or not that many rows
@@ -884,7 +701,7 @@ __global__ void __launch_bounds__(CROWS * CVECS, 4) latent_combine_kernel(char* 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
 template <int LD, typename T>
-cudaError_t launch(const LatentAttnArgs& a, cudaStream_t s) {
+cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s) {
   constexpr int smem = Cfg<LD>::TILES + sizeof(State<LD>);
   static_assert(smem <= 232448, "shared memory");
   static std::atomic<uint64_t> ready{0};   // devices whose kernel attribute is set
@@ -896,25 +713,6 @@ cudaError_t launch(const LatentAttnArgs& a, cudaStream_t s) {
   }
   const CUtensorMapDataType dt =
       std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  AttnP p;
-  p.cu = a.cu;
-  p.kv_lens = a.kv_lens;
-  p.page_tables = a.page_tables;
-  p.B = a.B;
-  p.T = a.T;
-  p.H = a.H;
-  p.P = a.P;
-  p.box = gcd(a.P, HM);
-  p.num_pages = a.num_pages;
-  p.max_pages = a.max_pages;
-  p.max_kv_len = a.max_kv_len;
-  p.table_cap = a.max_pages * a.P;
-  p.scale_log2 = a.scale * LOG2E;
-  p.out = a.out;
-  p.out_32 = ((uintptr_t)a.out & 31) == 0;
-  p.lse = a.lse;
-  p.ws = a.ws;
-  p.dev_status = a.dev.status;
   CUtensorMap mq, mx;
   if (!make_map_rows(&mq, a.q, dt, LD + 64, (int64_t)a.T * a.H, LD + 64, HM) ||
       !make_map_rows(&mx, a.cache, dt, LD + 64, (int64_t)a.num_pages * a.P, LD + 64, p.box))
@@ -934,12 +732,39 @@ cudaError_t launch(const LatentAttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t latent_attn_workspace(int32_t, int32_t, int32_t, int32_t latent_dim) { return Layout::total(latent_dim); }
+size_t latent_attn_workspace(int32_t, int32_t, int32_t, int32_t latent_dim) {
+  const size_t a = Layout::total(latent_dim), b = latent_rows_workspace(latent_dim);
+  return a > b ? a : b;
+}
 
 cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t s) {
+  // Up to 16 rows a sequence on average go 16 to a tile on mma.sync, which HBM
+  // bounds; with more of them the tensor cores' tiles of 128 rows read the keys
+  // less often (rows of one sequence share a pass over its keys).
+  const bool rows = (int64_t)a.T * a.H <= (int64_t)16 * a.B;
+  LatentAttnP p;
+  p.cu = a.cu;
+  p.kv_lens = a.kv_lens;
+  p.page_tables = a.page_tables;
+  p.B = a.B;
+  p.T = a.T;
+  p.H = a.H;
+  p.P = a.P;
+  p.box = gcd(a.P, rows ? latent_rows_box() : HM);   // rows of a TMA box: they lie in one page and in one slot
+  p.num_pages = a.num_pages;
+  p.max_pages = a.max_pages;
+  p.max_kv_len = a.max_kv_len;
+  p.table_cap = a.max_pages * a.P;
+  p.scale_log2 = a.scale * LOG2E;
+  p.out = a.out;
+  p.out_32 = ((uintptr_t)a.out & 31) == 0;
+  p.lse = a.lse;
+  p.ws = a.ws;
+  p.dev_status = a.dev.status;
+  if (rows) return launch_latent_rows(a, p, s);
   if (a.dtype == PKV_BF16)
-    return a.latent_dim == 512 ? launch<512, __nv_bfloat16>(a, s) : launch<256, __nv_bfloat16>(a, s);
-  return a.latent_dim == 512 ? launch<512, __half>(a, s) : launch<256, __half>(a, s);
+    return a.latent_dim == 512 ? launch<512, __nv_bfloat16>(a, p, s) : launch<256, __nv_bfloat16>(a, p, s);
+  return a.latent_dim == 512 ? launch<512, __half>(a, p, s) : launch<256, __half>(a, p, s);
 }
 
 }  // namespace pkv

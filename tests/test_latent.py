@@ -313,6 +313,16 @@ ABSORBED = [
     ("bf16", 256, 5, 100, [17], [3001]),
     ("bf16", 512, 16, 64, [1] * 90, [1 + 37 * k % 600 for k in range(90)]),
     ("f16", 256, 4, 64, [k % 4 for k in range(60)], [1 + 53 * k % 300 + k % 4 for k in range(60)]),
+    # at most 16 rows a sequence on average, tiles of 16 rows
+    ("bf16", 512, 8, 64, [2, 1, 1], [66, 64, 1]),
+    ("f16", 512, 3, 16, [5, 4, 1], [33, 700, 32]),
+    ("bf16", 512, 5, 100, [9, 0, 0, 0, 1], [9, 3, 1, 4, 31]),
+    ("f16", 256, 16, 48, [1] * 7, [31, 32, 33, 95, 96, 97, 4000]),
+    ("bf16", 256, 2, 1, [8, 7], [130, 65]),
+    ("bf16", 512, 1, 32, [16], [16 * 64 + 9]),
+    ("f16", 512, 16, 5, [1, 0], [7000, 12]),
+    ("bf16", 512, 7, 256, [40] + [0] * 30 + [1], [3000] + [1] * 31),
+    ("bf16", 512, 16, 64, [1] * 200, [1 + 97 * k % 500 for k in range(200)]),
 ]
 
 
@@ -326,11 +336,12 @@ def test_absorbed_matches_the_oracle(dev, case):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("ld", [256, 512])
-def test_absorbed_leaves_padding_rows_and_unrequested_lse_alone(dev, ld):
-    t = Paged(dev, "bf16", ld, 24, 16, [1, 3], [40, 200], pad_rows=3)
-    out = torch.full((t.total + 3, 24, ld), 5.0, dtype=torch.bfloat16, device=dev)
-    lse = torch.full((t.total + 3, 24), 5.0, device=dev)
+@pytest.mark.parametrize("ld,heads,q_lens,kv_lens", [(256, 24, [1, 3], [40, 200]), (512, 24, [1, 3], [40, 200]),
+                                                     (256, 4, [1, 2], [40, 200]), (512, 3, [2, 1, 1], [40, 3000, 9])])
+def test_absorbed_leaves_padding_rows_and_unrequested_lse_alone(dev, ld, heads, q_lens, kv_lens):
+    t = Paged(dev, "bf16", ld, heads, 16, q_lens, kv_lens, pad_rows=3)
+    out = torch.full((t.total + 3, heads, ld), 5.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((t.total + 3, heads), 5.0, device=dev)
     t.q[t.total:] = float("nan")
     t.call(out=out, lse=lse)
     assert binding.device_status() == 0
@@ -341,8 +352,9 @@ def test_absorbed_leaves_padding_rows_and_unrequested_lse_alone(dev, ld):
 
 
 @pytest.mark.gpu
-def test_absorbed_same_call_same_bits(dev):
-    t = Paged(dev, "bf16", 512, 128, 64, [1, 1, 2], [3000, 50, 700])
+@pytest.mark.parametrize("heads", [128, 12])
+def test_absorbed_same_call_same_bits(dev, heads):
+    t = Paged(dev, "bf16", 512, heads, 64, [1, 1, 2], [3000, 50, 700])
     first = t.call()
     for _ in range(3):
         again = t.call()
@@ -350,9 +362,10 @@ def test_absorbed_same_call_same_bits(dev):
 
 
 @pytest.mark.gpu
-def test_absorbed_bad_data_skips_the_sequence(dev):
+@pytest.mark.parametrize("heads", [16, 4])
+def test_absorbed_bad_data_skips_the_sequence(dev, heads):
     """A bad length or page skips that sequence's rows, a bad cu_seqlens_q every row."""
-    t = Paged(dev, "bf16", 512, 16, 64, [1, 2, 1], [300, 4000, 100])
+    t = Paged(dev, "bf16", 512, heads, 64, [1, 2, 1], [300, 4000, 100])
     good, good_lse = t.call()
     for what, bit in (("page", binding.DEV_BAD_PAGE), ("len", binding.DEV_BAD_LENGTHS), ("max", binding.DEV_BAD_LENGTHS)):
         table, kv = t.table.copy(), list(t.kv_lens)
@@ -381,12 +394,13 @@ def test_absorbed_bad_data_skips_the_sequence(dev):
 
 
 @pytest.mark.gpu
-def test_absorbed_pages_beyond_four_gigabytes(dev):
+@pytest.mark.parametrize("heads", [16, 40])
+def test_absorbed_pages_beyond_four_gigabytes(dev, heads):
     """Rows whose byte and element offsets pass 32 bits."""
     P, rows = 64, 4_200_000
     pages = rows // P
     cache = torch.empty((pages, P, 576), dtype=torch.bfloat16, device=dev)
-    t = Paged(dev, "bf16", 512, 16, P, [1], [500])
+    t = Paged(dev, "bf16", 512, heads, P, [1], [500])
     n = -(-500 // P)
     table = t.table.copy()
     for k in range(n):
