@@ -4,20 +4,29 @@
 //   out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  lse = m + ln(sum).
 //
 // Every head has its own keys, so the tensor cores get their work from the query
-// rows: a work tile is 256 rows of one head, as two query tiles of 128 whose
-// products alternate, so that one tile's softmax runs under the other's MMAs.
-// Per 128 keys and query tile: S = Q K^T (M 128, N 128, K 128 + 64) and O += P V
-// (M 128, N 128, K 128): 2560 tensor cycles for both tiles, the bound.
+// rows. A pair of CTAs (tcgen05 cta_group::2) works on two query tiles of 256 rows
+// whose products alternate, so that one tile's softmax runs under the other's MMAs;
+// each CTA has 128 rows of either tile, half of the keys of a step (for S) and half
+// of the value columns (for O). Per 128 keys and query tile: S = Q K^T (M 256, N 128,
+// K 128 + 64) and O += P V (M 256, N 128, K 128): 2560 tensor cycles for both tiles.
+// The two tiles are 512 rows of one head, which share every key tile, or, for a
+// sequence's 256 rows or fewer that do not fill such a tile, the same rows of two heads.
+// (One CTA with two tiles of 128 rows needs twice the shared memory for a step's
+// keys: beside Q it held 1.6 steps, waited for loads, and took 499 us instead of
+// @FULL@ for 4096 tokens at 128 heads.)
 //
-//   warp 0   TMA producer: Q of both tiles, then K_j (nope part and rotary part)
-//            and V_j into a ring of three 32 KB slots (nope keys or values) and two
-//            rotary units; V rows behind the sequence's end are zeroed
-//   warp 1   TMEM owner and MMA issuer: per key tile j and query tile w,
-//            O_w += P_w V_{j-1}, then S_w = Q_w K_j^T over the same TMEM columns as
-//            P_w (MMAs run in issue order, so the product has read P_w by then)
-//   warps 2-5, 6-9  softmax of query tile 0, 1, a thread per row; P goes back
-//            over S in TMEM as the A operand of the next product. O is rescaled
-//            only when a row's maximum grows by more than 2^8.
+//   warp 0     TMA producer (each CTA its halves): Q of both tiles, K_j (nope part
+//              and rotary part) and V_j into rings of three; V rows behind the
+//              sequence's end are zeroed. The even CTA's claims the tiles.
+//   warps 1, 2 MMA issuers of query tile 0, 1 (even CTA): per key tile j,
+//              O_w += P_w V_{j-1}, then S_w = Q_w K_j^T over the same TMEM columns as
+//              P_w (a warp's MMAs run in issue order, so the product has read P_w by
+//              then). The tensor pipe queues next to nothing, and a wait or commit costs
+//              its warp 100-400 cycles: the two take turns, and each does its waits and
+//              commits under the other's MMAs.
+//   warps 4-7, 8-11  softmax of query tile 0, 1, a thread per row; P goes back
+//              over S in TMEM as the A operand of the next product, handed over in two
+//              halves. O is rescaled only when a row's maximum grows by more than 2^8.
 //
 // Tiles go head by head, each head's from its last rows (most keys) to its first:
 // the CTAs that run at one time share few heads' keys, which stay in L2, and the
@@ -40,20 +49,24 @@ namespace {
 constexpr int NOPE = 128, DV = 128;
 constexpr int BM = 128;          // rows of a query tile
 constexpr int BN = 128;          // keys of a step
-constexpr int ROWS = 2 * BM;     // rows of a work tile
-constexpr int NTHREADS = 320;
+constexpr int QM = 2 * BM;       // rows of a query tile
+constexpr int ROWS = 2 * QM;     // rows of a work tile of one head
+constexpr int NTHREADS = 384;
 constexpr uint32_t UNIT = 16384;            // 128 rows x 64 columns of 16 bits
-constexpr uint32_t Q_BYTES = 3 * UNIT;      // one query tile
-constexpr int NSLOT = 3;
-constexpr uint32_t SLOT_BYTES = 2 * UNIT;
-constexpr uint32_t SMEM = 2 * Q_BYTES + NSLOT * SLOT_BYTES + 2 * UNIT + 1024;
+constexpr uint32_t Q_BYTES = 3 * UNIT;      // one CTA's rows of a query tile
+constexpr int NK = 3, NV = 3;               // ring slots
+constexpr uint32_t KUNIT = UNIT / 2;        // 64 keys x 64 columns
+constexpr uint32_t K_BYTES = 3 * KUNIT;     // one CTA's keys of a step: nope columns, rotary columns
+constexpr uint32_t V_BYTES = UNIT;          // one CTA's 64 value columns of a step's keys
+constexpr uint32_t SMEM = 2 * Q_BYTES + NK * K_BYTES + NV * V_BYTES + 1024;
 static_assert(SMEM <= 231424, "shared memory");
 constexpr uint32_t TMEM_COLS = 512;         // S of both tiles, then O of both
 constexpr float RESCALE_LOG2 = 8.f;
+constexpr long long WAIT_LIMIT_CLOCKS = 4000000000ll;   // about two seconds
 constexpr int PLAN_THREADS = 1024;
 
-// Workspace: the next tile to claim, the number of tiles, then the sequences in
-// the order they are worked on and the tiles before each.
+// Workspace: the next tile to claim, the number of tiles, heads of a tile of few
+// rows, then the sequences in the order they are worked on and the tiles before each.
 struct Layout {
   size_t order, first, total;
 };
@@ -77,14 +90,24 @@ struct PrefillP {
   int32_t* dev_status;
 };
 
+// A sequence's rows: tiles of ROWS rows of one head, the last of them with more than
+// QM, or, where no more than QM are left over, those (its first rows) as tiles of
+// one query tile a head.
+__device__ __forceinline__ int narrow_rows(int q) {
+  const int rest = q % ROWS;
+  return rest <= QM ? rest : 0;
+}
+__device__ __forceinline__ int wide_tiles(int q) { return q / ROWS + (q % ROWS > QM); }
+
 // One CTA: checks the lengths, orders the sequences by keys (descending, up to
 // PLAN_THREADS of them; more stay in their own order) and counts their tiles.
 __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const int32_t* __restrict__ cu_q,
                                                                           const int32_t* __restrict__ cu_k,
                                                                           int32_t B, int32_t Tq, int32_t Tk,
-                                                                          int32_t H, int32_t* ctrl, int32_t* order,
-                                                                          int32_t* first, int32_t* dev_status) {
-  __shared__ int s_cost[PLAN_THREADS], s_rank[PLAN_THREADS], s_scan[32], s_carry;
+                                                                          int32_t H, int32_t pairs, int32_t* ctrl,
+                                                                          int32_t* order, int32_t* first,
+                                                                          int32_t* dev_status) {
+  __shared__ int s_cost[PLAN_THREADS], s_rank[PLAN_THREADS], s_scan[32], s_carry, s_all;
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool sorted = B <= PLAN_THREADS;
@@ -92,6 +115,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
   for (int b = tid; b < B; b += PLAN_THREADS)
     bad |= __ldg(cu_q + b + 1) < __ldg(cu_q + b) || __ldg(cu_k + b + 1) < __ldg(cu_k + b);
   bad = __syncthreads_or(bad);
+  if (tid == 0) s_all = 0;
+  int heads = 1;   // heads of a tile of few rows
   auto tiles_of = [&](int b, int* keys) {
     const int q = __ldg(cu_q + b + 1) - __ldg(cu_q + b), L = __ldg(cu_k + b + 1) - __ldg(cu_k + b);
     *keys = L;
@@ -100,8 +125,17 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
       atomicOr(dev_status, PKV_DEV_BAD_LENGTHS);
       return 0;
     }
-    return (q + ROWS - 1) / ROWS;
+    return wide_tiles(q) * H + (narrow_rows(q) ? (H + heads - 1) / heads : 0);
   };
+  __syncthreads();
+  {
+    // one head a tile when that leaves pairs of CTAs without any
+    int keys, mine = 0;
+    for (int b = tid; b < B; b += PLAN_THREADS) mine = min(pairs + 1, mine + min(pairs + 1, tiles_of(b, &keys)));
+    if (mine > 0) atomicAdd(&s_all, mine);
+  }
+  __syncthreads();
+  heads = s_all > pairs ? 2 : 1;
   if (sorted) {
     int keys = 0;
     const int n = tid < B ? tiles_of(tid, &keys) : 0;
@@ -123,7 +157,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
     int b = 0, keys, n = 0;
     if (k < B) {
       b = sorted ? s_rank[k] : k;
-      n = tiles_of(b, &keys) * H;
+      n = tiles_of(b, &keys);
     }
     int scan = n;
 #pragma unroll
@@ -150,275 +184,325 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
     first[B] = s_carry;
     ctrl[0] = 0;
     ctrl[1] = s_carry;
+    ctrl[2] = heads;
     if (bad) atomicOr(dev_status, PKV_DEV_BAD_LENGTHS);
   }
 }
 
-// A work tile. Query tile w has rows row0 + 128 w .. (nr[w] of them, 0: none),
-// its first at position pos[w], and reads n[w] key tiles.
+// A work tile. Query tile w: head h[w], nr[w] rows (0: none) from packed row row0[w],
+// the first at position pos[w], reading n[w] key tiles. split: the two tiles
+// are of two heads, with keys of their own.
 struct Tile {
-  int valid, h, k0, L, row0;
-  int nr[2], pos[2], n[2];
+  int valid, split, k0, L;
+  int h[2], row0[2], nr[2], pos[2], n[2];
 };
 
 template <typename T>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                           const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mr,
                           PrefillP p) {
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  unsigned char* sQ = sm;                                  // [query tile][3 units]
-  unsigned char* sRing = sQ + 2 * Q_BYTES;                 // [slot][2 units]
-  unsigned char* sRope = sRing + NSLOT * SLOT_BYTES;       // [2]
+  unsigned char* sQ = sm;                         // [query tile][3 units]
+  unsigned char* sK = sQ + 2 * Q_BYTES;           // [slot][nope, nope, rotary]
+  unsigned char* sV = sK + NK * K_BYTES;          // [slot]
 
-  __shared__ __align__(8) uint64_t bar_q, bar_qempty, bar_full[NSLOT], bar_empty[NSLOT], bar_sfull[2], bar_pfull[2],
-      bar_odone[2], bar_tfull[2], bar_tempty[2], bar_vfix[2], bar_drain;
+  // q, k, v and p are waited on in the even CTA, where both CTAs arrive; the MMA
+  // commits signal kempty, vempty, qempty, s and o in both
+  __shared__ __align__(8) uint64_t bar_q, bar_qempty, bar_k[NK], bar_kempty[NK], bar_v[NV], bar_vempty[NV], bar_vtail,
+      bar_s[2], bar_p[2][2], bar_o[2], bar_tfull[2], bar_tempty[2], bar_turn[2], bar_drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ Tile s_tile[2];
   __shared__ volatile int s_abort;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
   if (tid == 0) {
-    mbar_init(&bar_q, 1);
-    mbar_init(&bar_qempty, 1);
-    for (int s = 0; s < NSLOT; ++s) {
-      mbar_init(&bar_full[s], 1);
-      mbar_init(&bar_empty[s], 1);
+    mbar_init(&bar_q, 2);
+    mbar_init(&bar_qempty, 2);             // both issuers
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(&bar_k[s], 2);
+      mbar_init(&bar_kempty[s], 2);        // both issuers, or one of them twice
     }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(&bar_v[s], 2);
+      mbar_init(&bar_vempty[s], 2);
+    }
+    mbar_init(&bar_vtail, 1);
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&bar_sfull[w], 1);
-      mbar_init(&bar_pfull[w], BM);
-      mbar_init(&bar_odone[w], 1);
+      mbar_init(&bar_s[w], 1);
+      for (int hf = 0; hf < 2; ++hf) mbar_init(&bar_p[w][hf], 8);   // four softmax warps of either CTA
+      mbar_init(&bar_o[w], 1);
       mbar_init(&bar_tfull[w], 1);
-      mbar_init(&bar_tempty[w], 1 + 8);   // the MMA warp and every softmax warp
-      mbar_init(&bar_vfix[w], 1);
+      mbar_init(&bar_tempty[w], 2 + 8 + 8 + 1);   // issuers, softmax warps of both CTAs, the odd CTA's producer
+      mbar_init(&bar_turn[w], 1);
+      mbar_init(&bar_drain[w], 1);
     }
-    mbar_init(&bar_drain, 1);
     fence_mbar_init();
+    mbar_arrive(&bar_turn[0]);   // query tile 0 has the first turn
     s_abort = 0;
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
     tma_prefetch_desc(&mr);
   }
-  if (warp == 1) tmem_alloc(&s_tmem, TMEM_COLS);
+  if (warp == 1) tmem_alloc_pair(&s_tmem, TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  cluster_sync_all();   // the peer's barriers are ready too
   const uint32_t tmem = s_tmem;
   pdl_wait();   // the plan, and whatever wrote the inputs
 
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return warp_wait_or_abort(bar, parity, &s_abort, p.dev_status, p.dev_status);
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    bool ok = false;
+    const long long t0 = clock64();
+    for (uint32_t it = 0; !ok; ++it) {
+      ok = mbar_try_wait(bar, parity);
+      if (!ok && (it & 63u) == 63u) {
+        if (s_abort) break;
+        if (clock64() - t0 > WAIT_LIMIT_CLOCKS || it > (1u << 28)) {
+          s_abort = 1;
+          atomicOr(p.dev_status, PKV_DEV_TIMEOUT);
+          break;
+        }
+      }
+    }
+    return __all_sync(0xffffffffu, ok);
   };
-  const int n_tiles = *(volatile const int32_t*)&p.ctrl[1];
+  // the tile of entry e, once it is there
+  auto wait_tile = [&](uint32_t t) -> bool {
+    const bool there = wait(&bar_tfull[t & 1], (t >> 1) & 1);
+    if (rank) fence_cluster();   // the even CTA wrote it
+    return there;
+  };
+  const uint32_t tempty = map_to_rank(bar_tempty, 0);
   bool ok = true;
 
   if (warp == 0) {
     // --------------------------------------------------------------- producer
-    uint32_t ring = 0, ropes = 0;    // loads and steps before the current one
+    const int n_tiles = *(volatile const int32_t*)&p.ctrl[1], heads = *(volatile const int32_t*)&p.ctrl[2];
+    const uint32_t q_bar = map_to_rank(&bar_q, 0);
+    uint32_t n_k = 0, n_v = 0, n_tail = 0;    // K, V loads and last tiles with rows to zero so far
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t & 1;
-      // entry e is free again once every consumer is done with tile t - 2
-      if (t >= 2 && !(ok = wait(&bar_tempty[e], ((t >> 1) - 1) & 1))) break;
-      if (lane == 0) {
-        Tile ti{};
-        const int tt = s_abort ? n_tiles : atomicAdd(&p.ctrl[0], 1);
-        if (tt < n_tiles) {
-          int lo = 0, hi = p.B - 1;   // the last sequence that starts at or before tile tt
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.first[mid] <= tt) lo = mid; else hi = mid - 1;
-          }
-          const int b = p.order[lo];
-          const int q_lo = __ldg(p.cu_q + b), q = __ldg(p.cu_q + b + 1) - q_lo;
-          ti.k0 = __ldg(p.cu_k + b);
-          ti.L = __ldg(p.cu_k + b + 1) - ti.k0;
-          const int per = (q + ROWS - 1) / ROWS, at = tt - p.first[lo];
-          ti.h = at / per;
-          const int q0 = (per - 1 - (at - ti.h * per)) * ROWS;
-          ti.row0 = q_lo + q0;
+      if (rank == 0) {
+        // entry e is free again once every consumer is done with tile t - 2
+        if (t >= 2 && !(ok = wait(&bar_tempty[e], ((t >> 1) - 1) & 1))) break;
+        if (lane == 0) {
+          Tile ti{};
+          const int tt = s_abort ? n_tiles : atomicAdd(&p.ctrl[0], 1);
+          if (tt < n_tiles) {
+            int lo = 0, hi = p.B - 1;   // the last sequence that starts at or before tile tt
+            while (lo < hi) {
+              const int mid = (lo + hi + 1) >> 1;
+              if (p.first[mid] <= tt) lo = mid; else hi = mid - 1;
+            }
+            const int b = p.order[lo];
+            const int q_lo = __ldg(p.cu_q + b), q = __ldg(p.cu_q + b + 1) - q_lo;
+            ti.k0 = __ldg(p.cu_k + b);
+            ti.L = __ldg(p.cu_k + b + 1) - ti.k0;
+            const int wide = wide_tiles(q), rest = narrow_rows(q);
+            int at = tt - p.first[lo];
+            ti.split = at >= wide * p.H;
+            const int h = ti.split ? (at - wide * p.H) * heads : at / wide;
+            const int q0 = ti.split ? 0 : rest + (wide - 1 - (at - h * wide)) * ROWS;
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            ti.nr[w] = max(0, min(BM, q - q0 - w * BM));
-            ti.pos[w] = ti.L - q + q0 + w * BM;
-            ti.n[w] = ti.nr[w] ? (ti.pos[w] + ti.nr[w] + BN - 1) / BN : 0;
+            for (int w = 0; w < 2; ++w) {
+              const int q_w = ti.split ? 0 : q0 + w * QM;
+              ti.h[w] = h + (ti.split ? w : 0);
+              ti.row0[w] = q_lo + q_w;
+              ti.nr[w] = ti.split ? (w < heads && ti.h[w] < p.H ? rest : 0) : max(0, min(QM, q - q_w));
+              ti.pos[w] = ti.L - q + q_w;
+              ti.n[w] = ti.nr[w] ? (ti.pos[w] + ti.nr[w] + BN - 1) / BN : 0;
+            }
+            ti.valid = 1;
           }
-          ti.valid = 1;
+          s_tile[e] = ti;
+          const uint32_t peer = map_to_rank(&s_tile[e], 1);
+          const uint32_t* words = reinterpret_cast<const uint32_t*>(&ti);
+#pragma unroll
+          for (int i = 0; i < (int)(sizeof(Tile) / 4); ++i) st_cluster_u32(peer + 4 * i, words[i]);
+          fence_cluster();
+          mbar_arrive(&bar_tfull[e]);
+          mbar_arrive_cluster(map_to_rank(&bar_tfull[e], 1));
         }
-        s_tile[e] = ti;
-        mbar_arrive(&bar_tfull[e]);
+        __syncwarp();
       }
-      __syncwarp();
+      if (!(ok = wait_tile(t))) break;
       const Tile ti = s_tile[e];
       if (!ti.valid) break;
-      const int W = ti.nr[1] ? 2 : 1, n = max(ti.n[0], ti.n[1]);
+      const int n = max(ti.n[0], ti.n[1]), streams = ti.split && ti.nr[1] ? 2 : 1;
       // Q of this tile replaces the one before once its last S is done
       if (t >= 1 && !(ok = wait(&bar_qempty, (t - 1) & 1))) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&bar_q, W * Q_BYTES);
+        mbar_arrive_expect_tx_cluster(q_bar, (ti.nr[1] ? 2 : 1) * Q_BYTES);
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int c = 0; c < 3; ++c)
-            if (w < W) tma_load_3d(sQ + w * Q_BYTES + c * UNIT, &mq, &bar_q, c * 64, ti.h, ti.row0 + w * BM);
+            if (ti.nr[w])
+              tma_load_3d_pair(sQ + w * Q_BYTES + c * UNIT, &mq, q_bar, c * 64, ti.h[w], ti.row0[w] + (int)rank * BM);
       }
       __syncwarp();
-      for (int j = 0; j < n && ok; ++j, ++ropes) {
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++ring) {
-          const uint32_t slot = ring % NSLOT, round = ring / NSLOT;
-          if (!(ok = wait(&bar_empty[slot], (round & 1) ^ 1))) break;
-          unsigned char* dst = sRing + slot * SLOT_BYTES;
-          const int row = ti.k0 + j * BN;
+      for (int j = 0; j < n && ok; ++j) {
+        for (int w = 0; w < streams; ++w, ++n_k) {
+          const uint32_t slot = n_k % NK;
+          if (!(ok = wait(&bar_kempty[slot], ((n_k / NK) & 1) ^ 1))) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(&bar_full[slot], (kv ? 2 : 3) * UNIT);
-            const int h = ti.h * (kv ? p.v_heads : p.kn_heads);
-            tma_load_3d(dst, kv ? &mv : &mk, &bar_full[slot], 0, h, row);
-            tma_load_3d(dst + UNIT, kv ? &mv : &mk, &bar_full[slot], 64, h, row);
-            // the rotary unit of two steps ago: its S is done, or the slot would not be free
-            if (!kv) tma_load_2d(sRope + (ropes & 1) * UNIT, &mr, &bar_full[slot], 0, row);
+            const uint32_t bar = map_to_rank(&bar_k[slot], 0);
+            unsigned char* dst = sK + slot * K_BYTES;
+            const int row = ti.k0 + j * BN + (int)rank * (BN / 2), h = ti.h[w] * p.kn_heads;
+            mbar_arrive_expect_tx_cluster(bar, K_BYTES);
+            tma_load_3d_pair(dst, &mk, bar, 0, h, row);
+            tma_load_3d_pair(dst + KUNIT, &mk, bar, 64, h, row);
+            tma_load_2d_pair(dst + 2 * KUNIT, &mr, bar, 0, row);
           }
           __syncwarp();
-          if (kv && j == n - 1) {
-            // 0 * NaN must not reach O from the rows behind the sequence's end
-            const int end = ti.L - j * BN;
+        }
+        if (!ok) break;
+        for (int w = 0; w < streams; ++w, ++n_v) {
+          const uint32_t slot = n_v % NV;
+          if (!(ok = wait(&bar_vempty[slot], ((n_v / NV) & 1) ^ 1))) break;
+          const uint32_t bar = map_to_rank(&bar_v[slot], 0);
+          unsigned char* dst = sV + slot * V_BYTES;
+          const int end = ti.L - j * BN;   // rows from here on are behind the sequence
+          if (lane == 0) {
+            const int col = (int)rank * (DV / 2), h = ti.h[w] * p.v_heads, row = ti.k0 + j * BN;
             if (end < BN) {
-              if (!(ok = wait(&bar_full[slot], round & 1))) break;
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint4* base = (uint4*)(dst + c * UNIT);
-                for (int x = end * 8 + lane; x < BN * 8; x += 32) base[x] = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
+              mbar_arrive_expect_tx(&bar_vtail, V_BYTES);
+              tma_load_3d(dst, &mv, &bar_vtail, col, h, row);
+            } else {
+              mbar_arrive_expect_tx_cluster(bar, V_BYTES);
+              tma_load_3d_pair(dst, &mv, bar, col, h, row);
             }
-            if (lane == 0) mbar_arrive(&bar_vfix[e]);
+          }
+          __syncwarp();
+          if (end < BN) {
+            // 0 * NaN must not reach O from the rows behind the sequence's end
+            if (!(ok = wait(&bar_vtail, n_tail++ & 1))) break;
+            uint4* base = (uint4*)dst;
+            for (int x = end * 8 + lane; x < BN * 8; x += 32) base[x] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(bar);
           }
         }
       }
+      if (rank && ok && lane == 0) mbar_arrive_cluster(tempty + e * 8);
+      __syncwarp();
     }
     if (!ok && lane == 0) {
       // let every copy this warp issued land before the CTA may exit
       const uint64_t t0 = globaltimer_ns();
       for (int it = 0; it < (1 << 24) && globaltimer_ns() - t0 < 20000000ull; ++it) {}
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------- MMA issuer
-    // The tensor pipe holds a few MMAs ahead of the issue and a wait costs on the
-    // order of 100 cycles, so the waits for the next operands sit behind MMAs
-    // already queued.
-    const uint32_t id_s = idesc_f16(BM, BN, BF16, false);
-    const uint32_t id_o = idesc_f16(BM, DV, BF16, true);
-    const uint64_t qd = smem_desc(smem_u32(sQ), 16, 1024, LAYOUT_SW128);
-    const uint64_t kd = smem_desc(smem_u32(sRing), 16, 1024, LAYOUT_SW128);
-    const uint64_t rd = smem_desc(smem_u32(sRope), 16, 1024, LAYOUT_SW128);
-    const uint64_t vd = smem_desc(smem_u32(sRing), UNIT, 1024, LAYOUT_SW128);
-    uint32_t ring = 0, ropes = 0, p_use[2] = {0, 0};
-    auto issue_s = [&](int w, uint32_t slot, uint32_t rope) {
+  } else if (warp < 3) {
+    // ------------------------------------------------------------ MMA issuers
+    if (rank == 0) {
+      const int w = warp - 1;
+      const uint32_t id_s = idesc_f16(QM, BN, BF16, false);
+      const uint32_t id_o = idesc_f16(QM, DV, BF16, true);
+      const uint64_t qd = smem_desc(smem_u32(sQ) + w * Q_BYTES, 16, 1024, LAYOUT_SW128);
+      const uint64_t kd = smem_desc(smem_u32(sK), 16, 1024, LAYOUT_SW128);
+      const uint64_t vd = smem_desc(smem_u32(sV), UNIT, 1024, LAYOUT_SW128);
+      const uint32_t s_tm = tmem + w * 128, o_tm = tmem + 256 + w * 128;
+      uint32_t base = 0;                  // K (and V) loads before the current tile
+      uint32_t n_p = 0, turns = 0;
+      for (uint32_t t = 0; ok; ++t) {
+        const uint32_t e = t & 1;
+        if (!(ok = wait_tile(t))) break;
+        if (!s_tile[e].valid) break;
+        const int mine = s_tile[e].n[w], n = max(s_tile[e].n[0], s_tile[e].n[1]);
+        const bool both = s_tile[e].nr[1] != 0, split = s_tile[e].split && both;
+        const bool active = mine > 0;
+        // a slot that one tile alone reads is released by two commits of its issuer
+        const bool twice = split || !both;
+        if (!(ok = wait(&bar_q, t & 1))) break;
+        // turn j: O_w (+)= P_w V_{j-1}, then S_w = Q_w K_j^T. The first product of a
+        // tile overwrites O_w: its P comes after the softmax threads read the
+        // tile before out of TMEM. A query tile that is done, or absent, takes its
+        // turns, and releases what it shares, like the other.
+        for (int j = 0; j <= n; ++j) {
+          const uint32_t kl = base + (split ? 2 * j + w : j), vl = base + (split ? 2 * (j - 1) + w : j - 1);
+          const uint32_t ks = kl % NK, vs = vl % NV;
+          const bool o = j > 0 && j - 1 < mine, sj = j < mine;
+          const bool has_v = j > 0 && (active || !twice), has_k = j < n && (active || !twice);
+          if (has_v && !(ok = wait(&bar_v[vs], (vl / NV) & 1))) break;
+          if (has_k && !(ok = wait(&bar_k[ks], (kl / NK) & 1))) break;
+          // the turn before P: P comes last in the steady state, and the product follows it at once
+          if (!(ok = wait(&bar_turn[w], turns++ & 1))) break;
+          if (o) {
+            const uint64_t v = vd + (uint64_t)((vs * V_BYTES) >> 4);
 #pragma unroll
-      for (int k = 0; k < 12; ++k) {
-        const uint32_t off = (k >> 2) * UNIT + (k & 3) * 32;
-        mma_f16_ss_warp(tmem + w * 128, qd + (uint64_t)((w * Q_BYTES + off) >> 4),
-                        k < 8 ? kd + (uint64_t)((slot * SLOT_BYTES + off) >> 4)
-                              : rd + (uint64_t)((rope * UNIT + (k & 3) * 32) >> 4),
-                        id_s, k ? 1u : 0u);
-      }
-      mma_commit_warp(&bar_sfull[w]);
-    };
-    for (uint32_t t = 0; ok; ++t) {
-      const uint32_t e = t & 1;
-      if (!(ok = wait(&bar_tfull[e], (t >> 1) & 1))) break;
-      const Tile ti = s_tile[e];
-      if (!ti.valid) break;
-      const int W = ti.nr[1] ? 2 : 1, n = max(ti.n[0], ti.n[1]);
-      // K_j is the tile's load 2j, V_j load 2j + 1
-      uint32_t ks = ring % NSLOT, kph = (ring / NSLOT) & 1;
-      uint32_t vs = (ring + 1) % NSLOT, vph = ((ring + 1) / NSLOT) & 1;
-      ring += 2 * n;
-      auto advance = [](uint32_t& s, uint32_t& ph) {
-        s += 2;
-        if (s >= (uint32_t)NSLOT) {
-          s -= NSLOT;
-          ph ^= 1;
-        }
-      };
-      if (!(ok = wait(&bar_q, t & 1))) break;
-      if (!(ok = wait(&bar_full[ks], kph))) break;
-      tc_fence_after();
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-        if (w < W) issue_s(w, ks, ropes & 1);
-      mma_commit_warp(&bar_empty[ks]);
-      if (n == 1) mma_commit_warp(&bar_qempty);
-      advance(ks, kph);
-      if (!(ok = wait(&bar_full[vs], vph))) break;
-      // step j: O_w (+)= P_w V_{j-1}, then S_w = Q_w K_j^T. The first product of a
-      // tile overwrites O_w: its P comes after the softmax threads read the
-      // tile before out of TMEM.
-      for (int j = 1; j <= n; ++j) {
-        if (j == n && !(ok = wait(&bar_vfix[e], (t >> 1) & 1))) break;
-        const uint64_t v = vd + (uint64_t)((vs * SLOT_BYTES) >> 4);
-        bool have_k = false;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          if (w >= W) break;
-          if (j - 1 < ti.n[w]) {
-            if (!(ok = wait(&bar_pfull[w], p_use[w] & 1))) break;
-            ++p_use[w];
+            for (int k = 0; k < BN / 16; ++k) {
+              if ((k & 3) == 0) {
+                if (!(ok = wait(&bar_p[w][k >> 2], n_p & 1))) break;
+                tc_fence_after();
+              }
+              mma_f16_ta_pair_warp(o_tm, s_tm + k * 8, v + (uint64_t)((k * 2048) >> 4), id_o,
+                                   (j > 1 || k > 0) ? 1u : 0u);
+            }
+            if (!ok) break;
+            ++n_p;
+          }
+          if (has_v) {
+            mma_commit_pair_warp(&bar_vempty[vs]);
+            if (twice) mma_commit_pair_warp(&bar_vempty[vs]);
+          }
+          if (sj) {
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < BN / 16; ++k)
-              mma_f16_ta_warp(tmem + 256 + w * 128, tmem + w * 128 + k * 8, v + (uint64_t)((k * 2048) >> 4), id_o,
-                              (j > 1 || k > 0) ? 1u : 0u);
-            if (j == ti.n[w]) mma_commit_warp(&bar_odone[w]);
+            for (int k = 0; k < 12; ++k) {
+              // the other tile's first MMAs may follow the last two of this turn at once
+              if (k == 10 && lane == 0) mbar_arrive(&bar_turn[w ^ 1]);
+              mma_f16_ss_pair_warp(s_tm, qd + (uint64_t)(((k >> 2) * UNIT + (k & 3) * 32) >> 4),
+                                   kd + (uint64_t)((ks * K_BYTES + (k >> 2) * KUNIT + (k & 3) * 32) >> 4), id_s,
+                                   k ? 1u : 0u);
+            }
+            mma_commit_pair_warp(&bar_s[w]);
+          } else if (lane == 0) {
+            mbar_arrive(&bar_turn[w ^ 1]);
           }
-          if (w == W - 1) {   // V_{j-1} has no reader left
-            mma_commit_warp(&bar_empty[vs]);
-            advance(vs, vph);
+          __syncwarp();
+          if (o && j == mine) mma_commit_pair_warp(&bar_o[w]);
+          if (has_k) {
+            mma_commit_pair_warp(&bar_kempty[ks]);
+            if (twice) mma_commit_pair_warp(&bar_kempty[ks]);
           }
-          if (j < ti.n[w]) {
-            if (!have_k && !(ok = wait(&bar_full[ks], kph))) break;
-            have_k = true;
-            if (w == W - 1 && !(ok = wait(&bar_full[vs], vph))) break;
-            issue_s(w, ks, (ropes + j) & 1);
-          }
+          if (j == n - 1) mma_commit_pair_warp(&bar_qempty);
         }
-        if (!ok) break;
-        if (j < n) {
-          mma_commit_warp(&bar_empty[ks]);
-          if (j == n - 1) mma_commit_warp(&bar_qempty);
-          advance(ks, kph);
-        }
+        base += split ? 2 * n : n;
+        if (ok && lane == 0) mbar_arrive_cluster(tempty + e * 8);
+        __syncwarp();
       }
-      ropes += n;
-      if (ok && lane == 0) mbar_arrive(&bar_tempty[e]);
-      __syncwarp();
     }
-  } else {
+  } else if (warp >= 4) {
     // ---------------------------------------------------------------- softmax
-    const int w = (warp - 2) >> 2;                // query tile
+    const int w = (warp - 4) >> 2;                // query tile
     const int quarter = warp & 3;                 // TMEM lanes of this warp
-    const int i = quarter * 32 + lane;            // row of the query tile
+    const int i = (int)rank * BM + quarter * 32 + lane;   // row of the query tile
     const uint32_t lrow = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_col = w * 128, o_col = 256 + w * 128;
+    const uint32_t p_bar = map_to_rank(bar_p[w], 0);
     const float sc = p.scale_log2;
     uint32_t n_s = 0, n_o = 0;                    // S and O hand-offs taken
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t & 1;
-      if (!(ok = wait(&bar_tfull[e], (t >> 1) & 1))) break;
+      if (!(ok = wait_tile(t))) break;
       const Tile& ti = s_tile[e];
       if (!ti.valid) break;
       const int n = ti.n[w];
       if (n > 0) {
         const int pos = min(ti.pos[w] + i, ti.L - 1);
-        const int j_mask = (ti.pos[w] + 1) / BN;   // key tiles before have no hidden key
+        const int j_mask = (ti.pos[w] + (int)rank * BM + 1) / BN;   // key tiles before have no hidden key
         float m_run = -INFINITY, l_run = 0.f;
         for (int j = 0; j < n; ++j) {
           // S complete also means that the product that read P is
-          if (!(ok = wait(&bar_sfull[w], n_s & 1))) break;
+          if (!(ok = wait(&bar_s[w], n_s & 1))) break;
           ++n_s;
           tc_fence_after();
           uint32_t r[4][32];
@@ -480,18 +564,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tmem_st32(tmem + lrow + s_col + hf * 32, pw);
             tmem_wait_st();
             reg_fence(pw);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(p_bar + hf * 8);
           }
           l_run += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
-          tc_fence_before();
-          mbar_arrive(&bar_pfull[w]);
         }
         if (!ok) break;
-        if (!(ok = wait(&bar_odone[w], n_o & 1))) break;
+        if (!(ok = wait(&bar_o[w], n_o & 1))) break;
         ++n_o;
         tc_fence_after();
         const bool store = i < ti.nr[w];
         const float inv = 1.f / l_run;
-        const int64_t row = (int64_t)(ti.row0 + w * BM + i) * p.H + ti.h;
+        const int64_t row = (int64_t)(ti.row0[w] + i) * p.H + ti.h[w];
         T* dst = (T*)p.out + row * DV;
 #pragma unroll 1
         for (int c = 0; c < DV / 32; ++c) {
@@ -511,20 +596,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_tempty[e]);
+      if (lane == 0) mbar_arrive_cluster(tempty + e * 8);
     }
   }
 
-  if (warp == 1) {
+  if ((warp == 1 || warp == 2) && rank == 0) {
     // every MMA this warp issued is complete before TMEM is released
-    mma_commit_warp(&bar_drain);
-    mbar_wait(&bar_drain, 0, 500000000ull);
+    mma_commit_pair_warp(&bar_drain[warp - 1]);
+    mbar_wait(&bar_drain[warp - 1], 0, 500000000ull);
     __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();   // no CTA leaves while the pair's MMAs or barriers need it
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
+  if (warp == 1) tmem_dealloc_pair(tmem, TMEM_COLS);
 }
 
 template <typename T>
@@ -559,20 +645,20 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
   CUtensorMap mq, mk, mv, mr;
   if (!make_map_boxed(&mq, a.q, dt, 2, NOPE + 64, a.H, a.Tq, 64, BM) ||
       !make_map_strided(&mk, a.kn, dt, NOPE, p.kn_heads ? a.H : 1, a.Tk, p.kn_heads ? a.kn_sh : NOPE,
-                        row_stride(a.kn_st), BN) ||
+                        row_stride(a.kn_st), BN / 2) ||
       !make_map_strided(&mv, a.v, dt, DV, p.v_heads ? a.H : 1, a.Tk, p.v_heads ? a.v_sh : DV, row_stride(a.v_st),
                         BN) ||
-      !make_map_rows(&mr, a.kr, dt, 64, a.Tk, row_stride(a.kr_st), BN))
+      !make_map_rows(&mr, a.kr, dt, 64, a.Tk, row_stride(a.kr_st), BN / 2))
     return cudaErrorInvalidValue;
   cudaError_t e;
   {
     KernelTimer timer("latent_prefill_plan", s);
     e = launch_after_trigger(latent_prefill_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, s, a.cu_q, a.cu_k, a.B, a.Tq,
-                             a.Tk, a.H, p.ctrl, p.order, p.first, a.dev.status);
+                             a.Tk, a.H, a.dev.num_sms / 2, p.ctrl, p.order, p.first, a.dev.status);
   }
   if (e != cudaSuccess) return e;
   KernelTimer timer("latent_prefill", s);
-  return launch_after_trigger(latent_prefill_kernel<T>, dim3(a.dev.num_sms), dim3(NTHREADS), SMEM, s, mq, mk, mv, mr,
+  return launch_after_trigger(latent_prefill_kernel<T>, dim3(a.dev.num_sms / 2 * 2), dim3(NTHREADS), SMEM, s, mq, mk, mv, mr,
                               p);
 }
 

@@ -463,6 +463,14 @@ EXPANDED = [
     ("bf16", 5, [130, 1, 2], [258, 385, 128]),
     ("f16", 16, [33], [95]),
     ("bf16", 1, [k % 5 for k in range(40)], [k % 5 + 3 * k for k in range(40)]),
+    # whole tiles of 512 rows, and what is left over (more than 256 rows, or fewer)
+    ("bf16", 1, [511, 512, 513], [511, 600, 640]),
+    ("f16", 2, [767, 768, 769], [767, 900, 769]),
+    ("bf16", 1, [1200], [1333]),
+    # enough tiles for every pair of CTAs: few rows of two heads go together
+    ("bf16", 81, [100, 3], [200, 131]),
+    ("f16", 80, [200, 600], [200, 700]),
+    ("bf16", 161, [1, 129], [300, 129]),
 ]
 
 
