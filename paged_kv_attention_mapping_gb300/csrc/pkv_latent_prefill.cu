@@ -13,7 +13,7 @@
 // sequence's 256 rows or fewer that do not fill such a tile, the same rows of two heads.
 // (One CTA with two tiles of 128 rows needs twice the shared memory for a step's
 // keys: beside Q it held 1.6 steps, waited for loads, and took 499 us instead of
-// @FULL@ for 4096 tokens at 128 heads.)
+// 450 for 4096 tokens at 128 heads in bf16: 1526 TFLOP/s.)
 //
 //   warp 0     TMA producer (each CTA its halves): Q of both tiles, K_j (nope part
 //              and rotary part) and V_j into rings of three; V rows behind the
@@ -505,20 +505,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           if (!(ok = wait(&bar_s[w], n_s & 1))) break;
           ++n_s;
           tc_fence_after();
-          uint32_t r[4][32];
+          uint32_t r[2][2][32];   // two halves of 64 keys
+          auto load = [&](int hf, uint32_t (&x)[2][32]) {
+            tmem_ld32(tmem + lrow + s_col + hf * 64, x[0]);
+            tmem_ld32(tmem + lrow + s_col + hf * 64 + 32, x[1]);
+          };
+          const bool masked = j >= j_mask;
+          auto arrived = [&](int hf, uint32_t (&x)[2][32]) {
+            reg_fence(x[0]);
+            reg_fence(x[1]);
+            if (masked) {
+              const int lim = pos - j * BN - hf * 64;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lrow + s_col + c * 32, r[c]);
+              for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (c * 32 + k > lim) x[c][k] = __float_as_uint(-INFINITY);
+            }
+          };
+          load(0, r[0]);
+          load(1, r[1]);
           tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) reg_fence(r[c]);
-          if (j >= j_mask) {
-            const int lim = pos - j * BN;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (c * 32 + k > lim) r[c][k] = __float_as_uint(-INFINITY);
-          }
+          arrived(0, r[0]);
+          arrived(1, r[1]);
           float mx[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
@@ -526,7 +535,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int k = 0; k < 32; k += 2)
-              mx[(k >> 1) & 7] = max3(mx[(k >> 1) & 7], __uint_as_float(r[c][k]), __uint_as_float(r[c][k + 1]));
+              mx[(k >> 1) & 7] = max3(mx[(k >> 1) & 7], __uint_as_float(r[c >> 1][c & 1][k]),
+                                      __uint_as_float(r[c >> 1][c & 1][k + 1]));
           const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
           const bool first = j == 0;
           const bool grow = first || mt > m_run + RESCALE_LOG2;
@@ -550,16 +560,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
+            if (hf == 1) {   // read again: held through the first half's exponentials it spills (475 us, not 450)
+              load(1, r[0]);
+              tmem_wait_ld();
+              arrived(1, r[0]);
+            }
             uint32_t pw[32];
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-              const int k0 = hf * 64 + 2 * k;
-              const float2 x = __ffma2_rn(
-                  make_float2(__uint_as_float(r[k0 >> 5][k0 & 31]), __uint_as_float(r[k0 >> 5][(k0 & 31) + 1])), sc2,
-                  nm2);
-              const float a = ex2(x.x), b = ex2(x.y);
-              ls[k & 3] = __fadd2_rn(ls[k & 3], make_float2(a, b));
-              pw[k] = pack2<T>(a, b);
+              const int k0 = 2 * k;
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[0][k0 >> 5][k0 & 31]),
+                                                      __uint_as_float(r[0][k0 >> 5][(k0 & 31) + 1])), sc2, nm2);
+              const float2 y = make_float2(ex2(x.x), ex2(x.y));
+              ls[k & 3] = __fadd2_rn(ls[k & 3], y);
+              pw[k] = pack2<T>(y.x, y.y);
             }
             tmem_st32(tmem + lrow + s_col + hf * 32, pw);
             tmem_wait_st();
