@@ -169,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
-  if (tid == 0) {
+  if (tid == NTHREADS - 1) {   // a thread with no other set-up to do
     mbar_init(&bar_q, 2);
     mbar_init(&bar_qempty, 1);
     for (int g = 0; g < NG; ++g) {
@@ -198,13 +198,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     tma_prefetch_desc(&mx);
   }
   if (warp == 1) tmem_alloc_pair(&s_tmem, TMEM_COLS);
-
-  __syncthreads();
+  __syncwarp();
+  cluster_arrive();     // the peer may use this CTA's barriers once every thread of both is here
   latent_plan<BM, BN, NTHREADS>(p, pair, pairs, &sh.plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  cluster_sync_all();   // the peer's barriers are ready too
+  cluster_wait();
   const uint32_t tmem = s_tmem;
   // queries, cache rows and page tables may come from the kernel before
   pdl_wait();
@@ -617,25 +617,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 // context of 131 k keys, against 18). No shared memory: the blocks get resident beside the attention kernel's,
 // which leave none, and start when the last of those ends.
 constexpr int CROWS = 8, CVECS = 32, CY = 8;
-template <int LD, typename T>
-__global__ void __launch_bounds__(CROWS * CVECS, 4) latent_combine_kernel(char* ws, T* out, float* lse) {
-  pdl_wait();
-  const int pair = blockIdx.x;
-  const LatentRecord rec = ((const LatentRecord*)(ws + Layout::rec))[pair];
-  const int step = CY * CROWS * (rec.parts - 1);
-  const int r0 = ((int)blockIdx.y + CY * (pair - rec.owner)) * CROWS;   // this block's first row
-  if (r0 >= rec.nrows) return;   // no cut tile (nrows 0), or not that many rows
+
+// Rows r0 + rr + step * k of the tile, k < K, for this thread's column vector; U
+// parts of each in flight.
+template <int LD, typename T, int K, int U>
+__device__ __forceinline__ void latent_join(const LatentRecord& rec, char* ws, T* out, float* lse, int r0, int step) {
   const float* sums = (const float*)(ws + Layout::lse);
   const int32_t* bad = (const int32_t*)(ws + Layout::bad);
+  const float4* parts = (const float4*)(ws + Layout::o);
   auto slot = [&](int s) { return s == 0 ? 2 * rec.owner + 1 : 2 * (rec.owner + s); };
   const int rr = threadIdx.x % CROWS, q = threadIdx.x / CROWS % 4;   // a warp: 8 rows x 4 vectors
   constexpr int ZH = LD / 8 / CVECS;   // blocks along a half's columns
   const int half = blockIdx.z / ZH, c = blockIdx.z % ZH * CVECS + threadIdx.x / CROWS;
-  const float4* parts = (const float4*)(ws + Layout::o);
-  int any = 0;
-  for (int s = threadIdx.x; s < rec.parts; s += blockDim.x) any |= bad[slot(s)];
-  if (__syncthreads_or(any)) return;
-  constexpr int K = BM / CROWS / CY;   // row groups of a block
   float m[K], total[K];
   float4 o[K];
 #pragma unroll
@@ -645,23 +638,26 @@ __global__ void __launch_bounds__(CROWS * CVECS, 4) latent_combine_kernel(char* 
     o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   // the four threads of a row in a warp share the search for its maximum
-  for (int s = q; s < rec.parts; s += 4)
+  int any = 0;
+  for (int s = q; s < rec.parts; s += 4) {
+    any |= bad[slot(s)];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int r = r0 + step * k + rr;
       if (r < rec.nrows) m[k] = fmaxf(m[k], sums[slot(s) * BM + r]);
     }
+  }
+  if (__any_sync(0xffffffffu, any)) return;   // (the warp looked at every part)
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 8));
     m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 16));
   }
-  // two parts of every row group at a time: 8 loads in flight a thread
-  for (int s = 0; s < rec.parts; s += 2) {
-    float w[2][K];
-    float4 y[2][K];
+  for (int s = 0; s < rec.parts; s += U) {
+    float w[U][K];
+    float4 y[U][K];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int r = r0 + step * k + rr;
@@ -673,7 +669,7 @@ __global__ void __launch_bounds__(CROWS * CVECS, 4) latent_combine_kernel(char* 
         }
       }
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const float f = exp2f(w[u][k] - m[k]);
@@ -696,6 +692,20 @@ __global__ void __launch_bounds__(CROWS * CVECS, 4) latent_combine_kernel(char* 
     *reinterpret_cast<uint2*>(out + row * LD + half * (LD / 2) + c * 4) = y;
     if (lse && blockIdx.z == 0 && threadIdx.x < CROWS) lse[row] = (m[k] + log2f(total[k])) * LN2;
   }
+}
+
+template <int LD, typename T>
+__global__ void __launch_bounds__(CROWS * CVECS, 4) latent_combine_kernel(char* ws, T* out, float* lse) {
+  pdl_wait();
+  const int pair = blockIdx.x;
+  const LatentRecord rec = ((const LatentRecord*)(ws + Layout::rec))[pair];
+  const int step = CY * CROWS * (rec.parts - 1);
+  const int r0 = ((int)blockIdx.y + CY * (pair - rec.owner)) * CROWS;   // this block's first row
+  if (r0 >= rec.nrows) return;   // no cut tile (nrows 0), or not that many rows
+  constexpr int K = BM / CROWS / CY;   // row groups of a block where two pairs share the tile
+  // eight parts of one row group in flight a thread, or two of each of its groups
+  if (r0 + step >= rec.nrows) latent_join<LD, T, 1, 8>(rec, ws, out, lse, r0, step);
+  else latent_join<LD, T, K, 8 / K / 2>(rec, ws, out, lse, r0, step);
 }
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }

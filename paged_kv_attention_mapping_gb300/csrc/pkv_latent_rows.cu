@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
+  if (tid == NTHREADS - 1) {   // a thread with no other set-up to do
     for (int s = 0; s < NS; ++s) {
       mbar_init(&sh.full[s], 1);
       mbar_init(&sh.empty[s], WARPS);
@@ -141,7 +141,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     sh.plan.run = 0;
     tma_prefetch_desc(&mx);
   }
-  __syncthreads();
   latent_plan<TM, BN, NTHREADS>(p, blockIdx.x, gridDim.x, &sh.plan);
   __syncthreads();
   pdl_wait();   // queries, cache rows and page tables may come from the kernel before

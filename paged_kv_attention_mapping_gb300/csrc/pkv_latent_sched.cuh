@@ -109,8 +109,8 @@ struct LatentPlan {
 
 // By all threads of a CTA: every CTA counts the whole tick's steps and finds where
 // its own run starts. Reads only the lengths, so it may run before the wait for the
-// kernel before. pl->run is 0 on entry (and visible); the results are visible after
-// the caller's next block barrier.
+// kernel before. One thread has set pl->run to 0 before; the results are visible
+// after the caller's next block barrier.
 template <int TM, int BN, int NTHREADS>
 __device__ __forceinline__ void latent_plan(const LatentAttnP& p, int worker, int workers, LatentPlan<NTHREADS>* pl) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -156,6 +156,7 @@ __device__ __forceinline__ void latent_plan(const LatentAttnP& p, int worker, in
         pl->b = b;
         pl->tile = tile;
         pl->step = step;
+        prefetch_l2(p.page_tables + (int64_t)b * p.max_pages + (int64_t)step * BN / p.P);   // wanted first
         break;
       }
       at -= n;
