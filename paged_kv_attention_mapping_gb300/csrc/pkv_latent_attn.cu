@@ -31,6 +31,9 @@
 //            shared memory. P goes to shared memory in the cache type, O is rescaled
 //            in TMEM only when a row's maximum grows by more than 2^8.
 //   warp 12  scheduler: the segments of this pair
+//   warps 13-15  where rows come by thread copies instead of TMA (page sizes that
+//            share no factor of 32 with a step): more loaders beside warp 0 and warp 2,
+//            taking groups in turn, since each waits for its own copies
 //
 // Work split: the tick's steps (all tiles, one after the other) are cut into
 // equal runs, one per pair. A tile cut by a run's end leaves partial results
@@ -57,7 +60,11 @@ constexpr int BN = 128;          // keys of a step
 constexpr int MAX_PAIRS = 76;    // 152 SMs; the workspace is laid out for these
 constexpr int SM_WARPS = 8;         // softmax warps of a CTA
 constexpr int SM_FIRST = 4;         // the first of them: its TMEM lanes are those of warp & 3
-constexpr int NTHREADS = (SM_FIRST + SM_WARPS + 1) * 32;
+constexpr int SCHED = SM_FIRST + SM_WARPS;   // the scheduler's warp; K loaders 1.. and the second reloader follow
+constexpr int K_LOADERS = 3, V_LOADERS = 2;  // for thread copies
+// Threads of a CTA. Without thread copies there are no idle warps: with them, the
+// decode of 128 sequences at 128 heads took 174 us instead of 151.
+constexpr int nthreads(bool gather) { return (SCHED + 1 + (gather ? K_LOADERS + V_LOADERS - 2 : 0)) * 32; }
 constexpr uint32_t UNIT = 8192;  // 64 rows x 64 columns of 16 bits: one swizzle atom wide
 constexpr float RESCALE_LOG2 = 8.f;
 
@@ -112,7 +119,7 @@ __device__ __forceinline__ void row_bar_arrive(int id) { asm volatile("bar.arriv
 // waited on in the even CTA, where both CTAs arrive; the MMA commits signal sdone,
 // odone, s and qempty in both.
 constexpr int NSEG = 4;
-template <int LD>
+template <int LD, int NTHREADS>
 struct State {
   using C = Cfg<LD>;
   // per step slot and group: loaded for S; read by S; loaded for O; read by O (after
@@ -131,17 +138,18 @@ struct State {
   uint32_t tmem;
 };
 
-template <int LD, typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
+template <int LD, typename T, bool GATHER>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
     latent_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mx, LatentAttnP p) {
   using C = Cfg<LD>;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int NST = C::NST, NG = C::NG;
+  constexpr int NST = C::NST, NG = C::NG, NTHREADS = nthreads(GATHER);
   extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char* sQ = sm;
   unsigned char* sK = sQ + C::Q_BYTES;               // [step][group][unit]
   unsigned char* sX = sK + NST * C::ST_BYTES;        // unit 0: P, keys 0-63; unit 1 + st: rotary unit of step slot st, then P, keys 64-127
-  State<LD>& sh = *reinterpret_cast<State<LD>*>(sX + C::X_BYTES);
+  using Sh = State<LD, NTHREADS>;
+  Sh& sh = *reinterpret_cast<Sh*>(sX + C::X_BYTES);
   auto& bar_k = sh.k;
   auto& bar_sdone = sh.sdone;
   auto& bar_v = sh.v;
@@ -189,7 +197,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     }
     for (int e = 0; e < NSEG; ++e) {
       mbar_init(&bar_seg[e], 1);
-      mbar_init(&bar_segempty[e], SM_WARPS + (rank == 0 ? 4 : 2));   // softmax, producers, MMA issuers
+      // softmax, producers, MMA issuers
+      mbar_init(&bar_segempty[e], SM_WARPS + (GATHER ? K_LOADERS + V_LOADERS : 2) + (rank == 0 ? 2 : 0));
     }
     fence_mbar_init();
     s_abort = 0;
@@ -229,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   };
 
   bool ok = true;
-  if (warp == SM_FIRST + SM_WARPS) {
+  if (warp == SCHED) {
     // ------------------------------------------------------------- scheduler
     LatentRun<BM, BN> run(p, sh.plan, pair);
     for (uint32_t t = 0; ok; ++t) {
@@ -245,16 +254,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (!g.valid) break;
     }
     if (rank == 0 && lane == 0) ((LatentRecord*)(p.ws + Layout::rec))[pair] = run.r;
-  } else if (warp == 0 || warp == 2) {
+  } else if (warp == 0 || warp == 2 || (GATHER && warp > SCHED)) {
     // --------------------------------------------------------------- producers
     // Warp 0 loads Q and this CTA's 64 keys of each step, warp 2 the peer's 64
     // keys of this CTA's output columns. Lane l takes boxes l and l + 32 of the 64
     // keys. Rows behind the end and bad pages are read from page 0 (masked, or
-    // discarded), so that a step's bytes are always the same.
-    const bool reload = warp == 2;
+    // discarded), so that a step's bytes are always the same. With thread copies
+    // K_LOADERS and V_LOADERS warps share that, a group each in turn.
+    const bool reload = warp == 2 || (GATHER && warp >= SCHED + K_LOADERS);
+    const uint32_t loaders = !GATHER ? 1 : reload ? V_LOADERS : K_LOADERS;
+    const uint32_t loader = warp < SM_FIRST ? 0 : reload ? warp - (SCHED + K_LOADERS) + 1 : warp - SCHED;
     const int key_half = (int)rank ^ (reload ? 1 : 0);
     const uint32_t q_bar = map_to_rank(&bar_q, 0);
     const int boxes = HM / p.box;
+    // 0 * NaN must not reach O from the slots behind the end: units 0 and 1 of a
+    // group hold keys 0-63 of the step, 2 and 3 keys 64-127
+    auto zero_rows = [&](unsigned char* group, int end) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int from = max(0, end - (u >> 1) * HM);
+        uint4* base = (uint4*)(group + u * UNIT);
+        for (int x = from * 8 + lane; x < HM * 8; x += 32) base[x] = make_uint4(0, 0, 0, 0);
+      }
+    };
     uint32_t n = 0, n_tail = 0;     // steps, and last steps with rows to zero, before the current one
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t % NSEG;
@@ -290,9 +312,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           // units that this warp fills, and their columns
           const int u0 = reload ? (rank ? 0 : 2) : 0, nu = reload ? 2 : 4;
           const int c0 = reload ? (rank ? 2 : 0) : 0;
+          if (GATHER && (n * NG + k) % loaders != loader) continue;
           if (!(ok = reload ? wait(&bar_sdone[st][k], par) : wait(&bar_odone[st][k], par ^ 1))) break;
           const uint32_t bar = map_to_rank(reload ? &bar_v[st][k] : &bar_k[st][k], 0);
           const bool rot = !reload && k == NG - 1;
+          if constexpr (GATHER) {
+            // eight lanes copy 128 bytes of a row, four rows at a time
+#pragma unroll 4
+            for (int y = 0; y < HM / 4; ++y) {
+              const int r = y * 4 + (lane >> 3);
+              const int from = __shfl_sync(0xffffffffu, y < HM / 8 ? cur[0] : cur[1], r & 31);
+              const char* src = (const char*)p.cache + (int64_t)from * ((LD + 64) * 2) + (lane & 7) * 16;
+              const uint32_t at = r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+              const uint32_t dst = smem_u32(stage) + k * C::G_BYTES + u0 * UNIT + at;
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                if (u < nu) cp_async_16(dst + u * UNIT, src + C::chunk(k, c0 + u) * 128);
+              if (rot) cp_async_16(smem_u32(sX) + (1 + st) * UNIT + at, src + LD * 2);
+            }
+            cp_async_wait_all();
+            if (tail) zero_rows(stage + k * C::G_BYTES, end);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(bar);
+            continue;
+          }
           if (lane == 0) {
             if (tail) mbar_arrive_expect_tx(&bar_vtail[k], 2 * UNIT);
             else mbar_arrive_expect_tx_cluster(bar, (nu + (rot ? 1 : 0)) * UNIT);
@@ -322,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           __syncwarp();
         }
         if (!ok) break;
-        if (!reload && j == g.j0) {
+        if ((GATHER ? warp == 0 : !reload) && j == g.j0) {
           // Q replaces the segment before's once its last S is done; the first keys go ahead
           if (t >= 1 && !(ok = wait(&bar_qempty, (t - 1) & 1))) break;
           if (lane == 0) {
@@ -333,18 +377,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           __syncwarp();
         }
-        if (tail) {
-          // 0 * NaN must not reach O from the slots behind the end: units 0 and 1
-          // of a group hold keys 0-63 of the step, 2 and 3 keys 64-127
+        if (!GATHER && tail) {
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
             if (!(ok = wait(&bar_vtail[k], n_tail & 1))) break;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int from = max(0, end - (u >> 1) * HM);
-              uint4* base = (uint4*)(stage + k * C::G_BYTES + u * UNIT);
-              for (int x = from * 8 + lane; x < HM * 8; x += 32) base[x] = make_uint4(0, 0, 0, 0);
-            }
+            zero_rows(stage + k * C::G_BYTES, end);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_rank(&bar_v[st][k], 0));
@@ -428,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         __syncwarp();
       }
     }
-  } else {
+  } else if (!GATHER || (warp >= SM_FIRST && warp < SCHED)) {
     // ----------------------------------------------------------------- softmax
     const int quarter = warp & 3, half = quarter >> 1;
     const int sub = (warp - SM_FIRST) >> 2;         // which half of the lane's columns
@@ -591,7 +628,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     if (!ok) row_bar_arrive(bar_id);   // lets the other warps of these rows leave their exchange
   }
 
-  if (s_abort && (warp == 0 || warp == 2)) {
+  if (s_abort && (warp == 0 || warp == 2 || warp > SCHED)) {
+    if (GATHER) cp_async_wait_all();
     // copies of this CTA may still be on their way: give them time to land
     const uint64_t t0 = globaltimer_ns();
     for (int it = 0; it < (1 << 24) && globaltimer_ns() - t0 < 20000000ull; ++it) {}
@@ -710,14 +748,14 @@ __global__ void __launch_bounds__(CROWS * CVECS, 4) latent_combine_kernel(char* 
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
-template <int LD, typename T>
+template <int LD, typename T, bool GATHER>
 cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s) {
-  constexpr int smem = Cfg<LD>::TILES + sizeof(State<LD>);
+  constexpr int smem = Cfg<LD>::TILES + sizeof(State<LD, nthreads(GATHER)>);
   static_assert(smem <= 232448, "shared memory");
   static std::atomic<uint64_t> ready{0};   // devices whose kernel attribute is set
   if (!(ready.load() >> a.dev.id & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(latent_attn_kernel<LD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               smem);
+    const cudaError_t e = cudaFuncSetAttribute(latent_attn_kernel<LD, T, GATHER>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << a.dev.id);
   }
@@ -725,19 +763,24 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s
       std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap mq, mx;
   if (!make_map_rows(&mq, a.q, dt, LD + 64, (int64_t)a.T * a.H, LD + 64, HM) ||
-      !make_map_rows(&mx, a.cache, dt, LD + 64, (int64_t)a.num_pages * a.P, LD + 64, p.box))
+      !make_map_rows(&mx, a.cache, dt, LD + 64, (int64_t)a.num_pages * a.P, LD + 64, GATHER ? HM : p.box))
     return cudaErrorInvalidValue;
   const int pairs = a.dev.num_sms / 2 < MAX_PAIRS ? a.dev.num_sms / 2 : MAX_PAIRS;
   cudaError_t e;
   {
     KernelTimer timer("latent_attn", s);
-    e = launch_after_trigger(latent_attn_kernel<LD, T>, dim3(2 * pairs), dim3(NTHREADS), smem, s, mq, mx, p);
+    e = launch_after_trigger(latent_attn_kernel<LD, T, GATHER>, dim3(2 * pairs), dim3(nthreads(GATHER)), smem, s, mq,
+                             mx, p);
   }
   if (e != cudaSuccess) return e;
   KernelTimer timer("latent_combine", s);
   return launch_after_trigger(latent_combine_kernel<LD, T>, dim3(pairs, CY, 2 * LD / 8 / CVECS),
-                              dim3(CROWS * CVECS), 0, s, a.ws, (T*)a.out,
-                              a.lse);
+                              dim3(CROWS * CVECS), 0, s, a.ws, (T*)a.out, a.lse);
+}
+
+template <int LD, typename T>
+cudaError_t launch_either(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s) {
+  return p.gather ? launch<LD, T, true>(a, p, s) : launch<LD, T, false>(a, p, s);
 }
 
 }  // namespace
@@ -760,7 +803,11 @@ cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t s) {
   p.T = a.T;
   p.H = a.H;
   p.P = a.P;
-  p.box = gcd(a.P, rows ? latent_rows_box() : HM);   // rows of a TMA box: they lie in one page and in one slot
+// Rows of a TMA box: they lie in one page and in one slot.
+  p.box = gcd(a.P, rows ? latent_rows_slot() : HM);
+  p.gather = p.box < 32;
+  if (p.gather) p.box = 1;
+  p.cache = a.cache;
   p.num_pages = a.num_pages;
   p.max_pages = a.max_pages;
   p.max_kv_len = a.max_kv_len;
@@ -773,8 +820,9 @@ cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t s) {
   p.dev_status = a.dev.status;
   if (rows) return launch_latent_rows(a, p, s);
   if (a.dtype == PKV_BF16)
-    return a.latent_dim == 512 ? launch<512, __nv_bfloat16>(a, p, s) : launch<256, __nv_bfloat16>(a, p, s);
-  return a.latent_dim == 512 ? launch<512, __half>(a, p, s) : launch<256, __half>(a, p, s);
+    return a.latent_dim == 512 ? launch_either<512, __nv_bfloat16>(a, p, s)
+                               : launch_either<256, __nv_bfloat16>(a, p, s);
+  return a.latent_dim == 512 ? launch_either<512, __half>(a, p, s) : launch_either<256, __half>(a, p, s);
 }
 
 }  // namespace pkv

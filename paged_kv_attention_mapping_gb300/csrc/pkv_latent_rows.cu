@@ -13,7 +13,8 @@
 //   warps 0-7  all of a step: the scores of 32 keys over a quarter of the columns
 //              (partial sums joined through shared memory), the softmax of two
 //              rows, then LD / 8 columns of O
-//   warp 8     TMA producer: 32-key slots of a ring, 128-byte swizzled
+//   warp 8     producer (TMA, or cp.async for small boxes): 32-key slots of a ring,
+//              128-byte swizzled
 //   warp 9     scheduler: the segments of this CTA
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == NTHREADS - 1) {   // a thread with no other set-up to do
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.full[s], p.gather ? 32 : 1);
       mbar_init(&sh.empty[s], WARPS);
     }
     for (int e = 0; e < NSEG; ++e) {
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (lane == 0) ((LatentRecord*)(p.ws + Layout::rec))[blockIdx.x] = run.r;
   } else if (warp == WARPS) {
     // --------------------------------------------------------------- producer
-    // Lane l takes box l of a slot. Rows behind the end and bad pages are read from
+    // Lane l takes box l of a slot, or finds row l for the copies. Rows behind the end and bad pages are read from
     // page 0 (masked, or discarded); a slot with no key of the tile is not read.
     const int boxes = HB / p.box;
     uint32_t h = 0;   // slots before the current one
@@ -213,6 +214,25 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const uint32_t slot = h % NS;
         if (!(ok = wait(&sh.empty[slot], ((h / NS) & 1) ^ 1))) break;
         const bool some = i * HB < keys;
+        if (p.gather) {
+          if (some) {
+            // eight lanes copy 128 bytes of a row, four rows at a time
+            const uint32_t dst = smem_u32(sm) + slot * C::SLOT;
+#pragma unroll
+            for (int y = 0; y < HB / 4; ++y) {
+              const int r = y * 4 + (lane >> 3);
+              const char* src = (const char*)p.cache + (int64_t)__shfl_sync(0xffffffffu, cur, r) * (D * 2) + (lane & 7) * 16;
+              const uint32_t at = dst + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+#pragma unroll
+              for (int u = 0; u < C::CH; ++u) cp_async_16(at + u * UNIT, src + u * 128);
+            }
+            cp_async_arrive(&sh.full[slot]);
+          } else {
+            mbar_arrive(&sh.full[slot]);
+          }
+          __syncwarp();
+          continue;
+        }
         if (lane == 0) {
           if (some) mbar_arrive_expect_tx(&sh.full[slot], C::SLOT);
           else mbar_arrive(&sh.full[slot]);
@@ -229,6 +249,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (lane == 0) mbar_arrive(&sh.segempty[e]);
       __syncwarp();
     }
+    if (p.gather) cp_async_wait_all();
     if (!ok && lane == 0) {
       // copies may still be on their way: give them time to land
       const uint64_t t0 = globaltimer_ns();
@@ -499,7 +520,7 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s
   if (!make_map_rows(&mx, a.cache,
                      std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                     LD + 64, (int64_t)a.num_pages * a.P, LD + 64, p.box))
+                     LD + 64, (int64_t)a.num_pages * a.P, LD + 64, p.gather ? HB : p.box))
     return cudaErrorInvalidValue;
   const int ctas = a.dev.num_sms < MAX_CTAS ? a.dev.num_sms : MAX_CTAS;
   cudaError_t e;
@@ -515,7 +536,7 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s
 
 }  // namespace
 
-int latent_rows_box() { return HB; }
+int latent_rows_slot() { return HB; }
 size_t latent_rows_workspace(int latent_dim) { return Layout::total(latent_dim); }
 
 cudaError_t launch_latent_rows(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s) {

@@ -8,9 +8,13 @@
 
 namespace pkv {
 
+// gather: rows come by 16-byte copies of threads (box is 1), not by TMA boxes. A
+// TMA instruction costs its warp about 90 cycles whatever its box holds, so small
+// boxes (pages that share no large power of two with a slot) starve the tensor cores.
 struct LatentAttnP {
   const int32_t *cu, *kv_lens, *page_tables;
-  int32_t B, T, H, P, box, num_pages, max_pages, max_kv_len, table_cap, out_32;
+  const void* cache;
+  int32_t B, T, H, P, box, gather, num_pages, max_pages, max_kv_len, table_cap, out_32;
   float scale_log2;   // > 0
   void* out;
   float* lse;
@@ -20,7 +24,7 @@ struct LatentAttnP {
 
 // The kernel for few rows a sequence (pkv_latent_rows.cu): rows of its ring slots,
 // its workspace, its launch.
-int latent_rows_box();
+int latent_rows_slot();
 size_t latent_rows_workspace(int latent_dim);
 cudaError_t launch_latent_rows(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s);
 
