@@ -100,7 +100,9 @@ __device__ __forceinline__ int narrow_rows(int q) {
 __device__ __forceinline__ int wide_tiles(int q) { return q / ROWS + (q % ROWS > QM); }
 
 // One CTA: checks the lengths, orders the sequences by keys (descending, up to
-// PLAN_THREADS of them; more stay in their own order) and counts their tiles.
+// PLAN_THREADS of them; more stay in their own order) and counts their tiles. The
+// launch takes as many warps as there are sequences to look at: every block barrier
+// here is on the way to the first tile.
 __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const int32_t* __restrict__ cu_q,
                                                                           const int32_t* __restrict__ cu_k,
                                                                           int32_t B, int32_t Tq, int32_t Tk,
@@ -110,9 +112,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
   __shared__ int s_cost[PLAN_THREADS], s_rank[PLAN_THREADS], s_scan[32], s_carry, s_all;
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool sorted = B <= PLAN_THREADS;
+  const int nt = blockDim.x;
+  const bool sorted = B <= nt;
   bool bad = tid == 0 && (__ldg(cu_q) != 0 || __ldg(cu_k) != 0 || __ldg(cu_q + B) > Tq || __ldg(cu_k + B) > Tk);
-  for (int b = tid; b < B; b += PLAN_THREADS)
+  for (int b = tid; b < B; b += nt)
     bad |= __ldg(cu_q + b + 1) < __ldg(cu_q + b) || __ldg(cu_k + b + 1) < __ldg(cu_k + b);
   bad = __syncthreads_or(bad);
   if (tid == 0) s_all = 0;
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
   {
     // one head a tile when that leaves pairs of CTAs without any
     int keys, mine = 0;
-    for (int b = tid; b < B; b += PLAN_THREADS) mine = min(pairs + 1, mine + min(pairs + 1, tiles_of(b, &keys)));
+    for (int b = tid; b < B; b += nt) mine = min(pairs + 1, mine + min(pairs + 1, tiles_of(b, &keys)));
     if (mine > 0) atomicAdd(&s_all, mine);
   }
   __syncthreads();
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
   }
   if (tid == 0) s_carry = 0;
   pdl_wait();   // an earlier call may still be reading the workspace until here
-  for (int base = 0; base < B; base += PLAN_THREADS) {
+  for (int base = 0; base < B; base += nt) {
     __syncthreads();
     const int carry = s_carry;
     const int k = base + tid;
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
     if (lane == 31) s_scan[warp] = scan;
     __syncthreads();
     int before = carry, all = carry;
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < nt / 32; ++w) {
       if (w < warp) before += s_scan[w];
       all += s_scan[w];
     }
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
   __syncthreads();
   if (tid == 0) {
     first[B] = s_carry;
-    ctrl[0] = 0;
+    ctrl[0] = pairs;   // a pair's first tile has the pair's number
     ctrl[1] = s_carry;
     ctrl[2] = heads;
     if (bad) atomicOr(dev_status, PKV_DEV_BAD_LENGTHS);
@@ -292,15 +295,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (rank == 0) {
         // entry e is free again once every consumer is done with tile t - 2
         if (t >= 2 && !(ok = wait(&bar_tempty[e], ((t >> 1) - 1) & 1))) break;
+        int tt = t == 0 ? (int)(blockIdx.x >> 1) : lane == 0 ? atomicAdd(&p.ctrl[0], 1) : 0;
+        tt = __shfl_sync(0xffffffffu, tt, 0);
+        if (__any_sync(0xffffffffu, s_abort)) tt = n_tiles;
+        int lo = 0;   // the last sequence that starts at or before tile tt, searched 32 ways
+        for (int m = p.B; m > 1;) {
+          const int step = (m + 31) / 32, at = lo + lane * step;
+          const bool before = lane * step < m && p.first[at] <= tt;
+          lo += (__popc(__ballot_sync(0xffffffffu, before)) - 1) * step;
+          m = min(step, p.B - lo);
+        }
         if (lane == 0) {
           Tile ti{};
-          const int tt = s_abort ? n_tiles : atomicAdd(&p.ctrl[0], 1);
           if (tt < n_tiles) {
-            int lo = 0, hi = p.B - 1;   // the last sequence that starts at or before tile tt
-            while (lo < hi) {
-              const int mid = (lo + hi + 1) >> 1;
-              if (p.first[mid] <= tt) lo = mid; else hi = mid - 1;
-            }
             const int b = p.order[lo];
             const int q_lo = __ldg(p.cu_q + b), q = __ldg(p.cu_q + b + 1) - q_lo;
             ti.k0 = __ldg(p.cu_k + b);
@@ -667,7 +674,8 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
   cudaError_t e;
   {
     KernelTimer timer("latent_prefill_plan", s);
-    e = launch_after_trigger(latent_prefill_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, s, a.cu_q, a.cu_k, a.B, a.Tq,
+    e = launch_after_trigger(latent_prefill_plan_kernel, dim3(1),
+                             dim3(a.B < PLAN_THREADS ? (a.B + 31) / 32 * 32 : PLAN_THREADS), 0, s, a.cu_q, a.cu_k, a.B, a.Tq,
                              a.Tk, a.H, a.dev.num_sms / 2, p.ctrl, p.order, p.first, a.dev.status);
   }
   if (e != cudaSuccess) return e;

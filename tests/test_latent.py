@@ -177,7 +177,8 @@ def test_attention_refusals(lib):
 
 def test_prefill_refusals(lib):
     for kw in (dict(B=-1), dict(Tq=-1), dict(Tk=-1), dict(H=0), dict(scale=0.0), dict(kst=100), dict(ksh=-8),
-               dict(krs=4), dict(Tk=0), dict(Tq=1 << 30, H=4)):
+               dict(krs=4), dict(Tk=0), dict(Tq=1 << 30, H=4),
+               dict(kst=0), dict(krs=0)):
         assert _prefill(lib, **kw) == -3, kw
     assert _prefill(lib, dtype=binding.PKV_F32) == -2 and _prefill(lib, dtype=binding.PKV_FP8_E4M3) == -2
     assert _prefill(lib, q=None) == -1 and _prefill(lib, kn=ODD) == -7
@@ -323,6 +324,11 @@ ABSORBED = [
     ("f16", 512, 16, 5, [1, 0], [7000, 12]),
     ("bf16", 512, 7, 256, [40] + [0] * 30 + [1], [3000] + [1] * 31),
     ("bf16", 512, 16, 64, [1] * 200, [1 + 97 * k % 500 for k in range(200)]),
+    # rows by thread copies, more steps than slots, tails of every kind
+    ("bf16", 512, 128, 16, [1, 1, 1], [1025, 640, 1000]),
+    ("f16", 512, 33, 1, [1, 2], [777, 513]),
+    ("bf16", 256, 130, 20, [1, 1], [1023, 1100]),
+    ("f16", 256, 16, 16, [1, 1, 1], [1000, 65, 31]),
 ]
 
 
@@ -482,6 +488,24 @@ def test_expanded_matches_the_oracle(dev, case, strided):
     out, lse = t.call()
     assert binding.device_status() == 0
     t.check(out, lse)
+
+
+@pytest.mark.gpu
+def test_expanded_takes_views(dev):
+    """Keys and values laid out head by head, or one key and value for all heads."""
+    t = Packed(dev, "bf16", 3, [40, 50, 300], [100, 50, 777], strided=False)
+    out, lse = t.call()
+    kn, v = t.kn, t.v
+    t.kn, t.v = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (kn, v))
+    again = t.call()
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    t.kn, t.v = kn[:, :1].expand(-1, 3, -1), v[:, 1:2].expand(-1, 3, -1)
+    got = t.call()
+    assert binding.device_status() == 0
+    t.check(*got)
+    t.kn = kn[:1].expand(kn.shape[0], -1, -1)
+    with pytest.raises(binding.PagedKVError):          # one key row for all tokens
+        t.call()
 
 
 @pytest.mark.gpu
@@ -697,6 +721,39 @@ def test_graphs_replay_with_new_lengths_and_side_by_side(dev):
         big.check(out, lse)
     other.check(*got2)
     chunk.check(*got3)
+
+
+@pytest.mark.gpu
+def test_eager_calls_on_two_streams_at_once(dev):
+    ticks = [Paged(dev, "bf16", 512, 16, 64, [1, 1], [3000, 20], seed=1),
+             Paged(dev, "f16", 512, 64, 16, [1, 2], [700, 2500], seed=2)]
+    chunks = [Packed(dev, "bf16", 3, [70, 300], [90, 800], seed=k) for k in (3, 4)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for t, c in zip(ticks, chunks):
+            s = torch.cuda.Stream()
+            got.append((t, t.call(stream=s)))
+            got.append((c, c.call(stream=s)))
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0
+    for t, (out, lse) in got:
+        t.check(out, lse)
+
+
+@pytest.mark.gpu
+def test_no_rows_and_no_sequences(dev):
+    t = Paged(dev, "bf16", 256, 4, 16, [0, 0], [5, 0])
+    out, lse = t.call()
+    assert out.shape == (0, 4, 256) and lse.shape == (0, 4)
+    q, cu = torch.zeros((0, 2, 192), dtype=torch.bfloat16, device=dev), _i32([0, 0], dev)
+    k = torch.zeros((3, 2, 128), dtype=torch.bfloat16, device=dev)
+    out, lse = binding.latent_prefill(q, cu, k, k, k[:, 0, :64], cu, SCALE)
+    assert out.shape == (0, 2, 128)
+    none = lambda *shape, t=torch.bfloat16: torch.zeros(shape, dtype=t, device=dev)
+    binding.latent_append(none(0, 256), none(0, 64), none(0, t=torch.int32), none(4, 32, 2, t=torch.float32),
+                          none(0, t=torch.int64), t.cache)
+    assert binding.device_status() == 0
 
 
 @pytest.mark.gpu
