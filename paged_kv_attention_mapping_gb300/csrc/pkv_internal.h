@@ -288,6 +288,9 @@ bool make_map_boxed(CUtensorMap* m, const void* base, CUtensorMapDataType dt, in
 // 3-D map [rows, heads, cols] with element strides, boxes of 64 columns of one head.
 bool make_map_strided(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int cols, int heads, int64_t rows,
                       int64_t head_stride, int64_t row_stride, int box_rows);
+// Map [chunks, rows, 64] over rows of chunks * 64 elements, boxes of several chunks.
+bool make_map_chunks(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int chunks, int64_t rows,
+                     int64_t row_stride, int box_rows, int box_chunks);
 // 2-D map over rows of `cols` 16-bit elements (row_stride elements apart), boxes of 64 columns.
 bool make_map_rows(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int cols, int64_t rows,
                    int64_t row_stride, int box_rows);

@@ -140,7 +140,8 @@ struct State {
 
 template <int LD, typename T, bool GATHER>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
-    latent_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mx, LatentAttnP p) {
+    latent_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mx,
+                       const __grid_constant__ CUtensorMap m2, LatentAttnP p) {
   using C = Cfg<LD>;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int NST = C::NST, NG = C::NG, NTHREADS = nthreads(GATHER);
@@ -205,6 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
     sh.plan.run = 0;
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mx);
+    tma_prefetch_desc(&m2);
   }
   if (warp == 1) tmem_alloc_pair(&s_tmem, TMEM_COLS);
   __syncwarp();
@@ -342,17 +344,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
             else mbar_arrive_expect_tx_cluster(bar, (nu + (rot ? 1 : 0)) * UNIT);
           }
           __syncwarp();
+          if (boxes == 1) {
+            // two units at a time: an instruction costs its warp about 90 cycles
+            if (lane == 0) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int i = lane + w * 32;
-            if (i < boxes) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
+              for (int u = 0; u < 4; u += 2) {
                 if (u >= nu) break;
-                unsigned char* dst = stage + k * C::G_BYTES + (u0 + u) * UNIT + i * p.box * 128;
-                const int col = C::chunk(k, c0 + u) * 64;
-                if (tail) tma_load_2d(dst, &mx, &bar_vtail[k], col, cur[w]);
-                else tma_load_2d_pair(dst, &mx, bar, col, cur[w]);
+                unsigned char* dst = stage + k * C::G_BYTES + (u0 + u) * UNIT;
+                if (tail) tma_load_3d(dst, &m2, &bar_vtail[k], 0, cur[0], C::chunk(k, c0 + u));
+                else tma_load_3d_pair(dst, &m2, bar, 0, cur[0], C::chunk(k, c0 + u));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const int i = lane + w * 32;
+              if (i < boxes) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  if (u >= nu) break;
+                  unsigned char* dst = stage + k * C::G_BYTES + (u0 + u) * UNIT + i * p.box * 128;
+                  if (tail) tma_load_3d(dst, &mx, &bar_vtail[k], 0, cur[w], C::chunk(k, c0 + u));
+                  else tma_load_3d_pair(dst, &mx, bar, 0, cur[w], C::chunk(k, c0 + u));
+                }
               }
             }
           }
@@ -360,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const int i = lane + w * 32;
-              if (i < boxes) tma_load_2d_pair(sX + (1 + st) * UNIT + i * p.box * 128, &mx, bar, LD, cur[w]);
+              if (i < boxes) tma_load_3d_pair(sX + (1 + st) * UNIT + i * p.box * 128, &mx, bar, 0, cur[w], LD / 64);
             }
           }
           __syncwarp();
@@ -371,9 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
           if (t >= 1 && !(ok = wait(&bar_qempty, (t - 1) & 1))) break;
           if (lane == 0) {
             mbar_arrive_expect_tx_cluster(q_bar, C::Q_BYTES);
-#pragma unroll
-            for (int c = 0; c < C::CH; ++c)
-              tma_load_2d_pair(sQ + c * UNIT, &mq, q_bar, c * 64, g.row0 + (int)rank * HM);
+            tma_load_3d_pair(sQ, &mq, q_bar, 0, g.row0 + (int)rank * HM, 0);
           }
           __syncwarp();
         }
@@ -761,16 +773,19 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s
   }
   const CUtensorMapDataType dt =
       std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  CUtensorMap mq, mx;
-  if (!make_map_rows(&mq, a.q, dt, LD + 64, (int64_t)a.T * a.H, LD + 64, HM) ||
-      !make_map_rows(&mx, a.cache, dt, LD + 64, (int64_t)a.num_pages * a.P, LD + 64, GATHER ? HM : p.box))
+  const int box = GATHER ? HM : p.box;
+  const int64_t pool_rows = (int64_t)a.num_pages * a.P;
+  CUtensorMap mq, mx, m2;
+  if (!make_map_chunks(&mq, a.q, dt, Cfg<LD>::CH, (int64_t)a.T * a.H, LD + 64, HM, Cfg<LD>::CH) ||
+      !make_map_chunks(&mx, a.cache, dt, Cfg<LD>::CH, pool_rows, LD + 64, box, 1) ||
+      !make_map_chunks(&m2, a.cache, dt, Cfg<LD>::CH, pool_rows, LD + 64, box, 2))
     return cudaErrorInvalidValue;
   const int pairs = a.dev.num_sms / 2 < MAX_PAIRS ? a.dev.num_sms / 2 : MAX_PAIRS;
   cudaError_t e;
   {
     KernelTimer timer("latent_attn", s);
     e = launch_after_trigger(latent_attn_kernel<LD, T, GATHER>, dim3(2 * pairs), dim3(nthreads(GATHER)), smem, s, mq,
-                             mx, p);
+                             mx, m2, p);
   }
   if (e != cudaSuccess) return e;
   KernelTimer timer("latent_combine", s);

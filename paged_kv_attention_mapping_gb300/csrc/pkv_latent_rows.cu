@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // --------------------------------------------------------------- producer
     // Lane l takes box l of a slot, or finds row l for the copies. Rows behind the end and bad pages are read from
     // page 0 (masked, or discarded); a slot with no key of the tile is not read.
-    const int boxes = HB / p.box;
+    const int boxes = HB / p.box;   // 1 (TMA), or 32 (copies)
     uint32_t h = 0;   // slots before the current one
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t % NSEG;
@@ -238,11 +238,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           else mbar_arrive(&sh.full[slot]);
         }
         __syncwarp();
-        if (some && lane < boxes) {
-#pragma unroll
-          for (int u = 0; u < C::CH; ++u)
-            tma_load_2d(sm + slot * C::SLOT + u * UNIT + lane * p.box * 128, &mx, &sh.full[slot], u * 64, cur);
-        }
+        // the slot's rows lie in one page: all of its columns at once
+        if (some && lane == 0) tma_load_3d(sm + slot * C::SLOT, &mx, &sh.full[slot], 0, cur, 0);
         __syncwarp();
       }
       if (!ok) break;
@@ -517,10 +514,10 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s
     ready.fetch_or(1ull << a.dev.id);
   }
   CUtensorMap mx;
-  if (!make_map_rows(&mx, a.cache,
+  if (!make_map_chunks(&mx, a.cache,
                      std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                     LD + 64, (int64_t)a.num_pages * a.P, LD + 64, p.gather ? HB : p.box))
+                     Cfg<LD>::CH, (int64_t)a.num_pages * a.P, LD + 64, HB, Cfg<LD>::CH))
     return cudaErrorInvalidValue;
   const int ctas = a.dev.num_sms < MAX_CTAS ? a.dev.num_sms : MAX_CTAS;
   cudaError_t e;

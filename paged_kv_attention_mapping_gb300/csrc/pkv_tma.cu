@@ -53,6 +53,22 @@ bool make_map_strided(CUtensorMap* m, const void* base, CUtensorMapDataType dt, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// View of `rows` rows of `chunks` * 64 16-bit elements, row_stride elements apart, as
+// [chunks, rows, 64]; boxes of box_chunks x box_rows x 64, 128-byte swizzled: the chunks
+// of a box land one after the other, each as box_rows rows of 128 bytes.
+bool make_map_chunks(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int chunks, int64_t rows,
+                     int64_t row_stride, int box_rows, int box_chunks) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)chunks};
+  cuuint64_t strides[2] = {(cuuint64_t)row_stride * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_chunks};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 2-D view of `rows` rows of `cols` 16-bit elements, row_stride elements apart; boxes of
 // 64 columns (one 128-byte swizzle atom) x box_rows rows, 128-byte swizzled.
 bool make_map_rows(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int cols, int64_t rows,
