@@ -65,8 +65,8 @@ constexpr float RESCALE_LOG2 = 8.f;
 constexpr long long WAIT_LIMIT_CLOCKS = 4000000000ll;   // about two seconds
 constexpr int PLAN_THREADS = 1024;
 
-// Workspace: the next tile to claim, the number of tiles, heads of a tile of few
-// rows, then the sequences in the order they are worked on and the tiles before each.
+// Workspace: the next tile to claim, the number of tiles, then the sequences in
+// the order they are worked on and the tiles before each.
 struct Layout {
   size_t order, first, total;
 };
@@ -92,7 +92,8 @@ struct PrefillP {
 
 // A sequence's rows: tiles of ROWS rows of one head, the last of them with more than
 // QM, or, where no more than QM are left over, those (its first rows) as tiles of
-// one query tile a head.
+// one query tile of each of two heads (one head a tile: 189 us, not 170, for eight
+// chunks after prefixes; no difference where pairs of CTAs are left without a tile).
 __device__ __forceinline__ int narrow_rows(int q) {
   const int rest = q % ROWS;
   return rest <= QM ? rest : 0;
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
                                                                           int32_t H, int32_t pairs, int32_t* ctrl,
                                                                           int32_t* order, int32_t* first,
                                                                           int32_t* dev_status) {
-  __shared__ int s_cost[PLAN_THREADS], s_rank[PLAN_THREADS], s_scan[32], s_carry, s_all;
+  __shared__ int s_cost[PLAN_THREADS], s_rank[PLAN_THREADS], s_scan[32], s_carry;
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nt = blockDim.x;
@@ -118,8 +119,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
   for (int b = tid; b < B; b += nt)
     bad |= __ldg(cu_q + b + 1) < __ldg(cu_q + b) || __ldg(cu_k + b + 1) < __ldg(cu_k + b);
   bad = __syncthreads_or(bad);
-  if (tid == 0) s_all = 0;
-  int heads = 1;   // heads of a tile of few rows
   auto tiles_of = [&](int b, int* keys) {
     const int q = __ldg(cu_q + b + 1) - __ldg(cu_q + b), L = __ldg(cu_k + b + 1) - __ldg(cu_k + b);
     *keys = L;
@@ -128,17 +127,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
       atomicOr(dev_status, PKV_DEV_BAD_LENGTHS);
       return 0;
     }
-    return wide_tiles(q) * H + (narrow_rows(q) ? (H + heads - 1) / heads : 0);
+    return wide_tiles(q) * H + (narrow_rows(q) ? (H + 1) / 2 : 0);
   };
-  __syncthreads();
-  {
-    // one head a tile when that leaves pairs of CTAs without any
-    int keys, mine = 0;
-    for (int b = tid; b < B; b += nt) mine = min(pairs + 1, mine + min(pairs + 1, tiles_of(b, &keys)));
-    if (mine > 0) atomicAdd(&s_all, mine);
-  }
-  __syncthreads();
-  heads = s_all > pairs ? 2 : 1;
   if (sorted) {
     int keys = 0;
     const int n = tid < B ? tiles_of(tid, &keys) : 0;
@@ -187,7 +177,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
     first[B] = s_carry;
     ctrl[0] = pairs;   // a pair's first tile has the pair's number
     ctrl[1] = s_carry;
-    ctrl[2] = heads;
     if (bad) atomicOr(dev_status, PKV_DEV_BAD_LENGTHS);
   }
 }
@@ -287,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 
   if (warp == 0) {
     // --------------------------------------------------------------- producer
-    const int n_tiles = *(volatile const int32_t*)&p.ctrl[1], heads = *(volatile const int32_t*)&p.ctrl[2];
+    const int n_tiles = *(volatile const int32_t*)&p.ctrl[1];
     const uint32_t q_bar = map_to_rank(&bar_q, 0);
     uint32_t n_k = 0, n_v = 0, n_tail = 0;    // K, V loads and last tiles with rows to zero so far
     for (uint32_t t = 0; ok; ++t) {
@@ -315,14 +304,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const int wide = wide_tiles(q), rest = narrow_rows(q);
             int at = tt - p.first[lo];
             ti.split = at >= wide * p.H;
-            const int h = ti.split ? (at - wide * p.H) * heads : at / wide;
+            const int h = ti.split ? (at - wide * p.H) * 2 : at / wide;
             const int q0 = ti.split ? 0 : rest + (wide - 1 - (at - h * wide)) * ROWS;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const int q_w = ti.split ? 0 : q0 + w * QM;
               ti.h[w] = h + (ti.split ? w : 0);
               ti.row0[w] = q_lo + q_w;
-              ti.nr[w] = ti.split ? (w < heads && ti.h[w] < p.H ? rest : 0) : max(0, min(QM, q - q_w));
+              ti.nr[w] = ti.split ? (ti.h[w] < p.H ? rest : 0) : max(0, min(QM, q - q_w));
               ti.pos[w] = ti.L - q + q_w;
               ti.n[w] = ti.nr[w] ? (ti.pos[w] + ti.nr[w] + BN - 1) / BN : 0;
             }
