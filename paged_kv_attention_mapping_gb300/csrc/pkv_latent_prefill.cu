@@ -28,6 +28,9 @@
 //              over S in TMEM as the A operand of the next product, handed over in two
 //              halves. O is rescaled only when a row's maximum grows by more than 2^8.
 //
+// Where the tiles are at most half as many as the pairs of CTAs (short chunks, few
+// heads), each tile's keys are cut into parts, as many as there are pairs for; latent_prefill_combine_kernel joins their partial results.
+//
 // Tiles go head by head, each head's from its last rows (most keys) to its first:
 // the CTAs that run at one time share few heads' keys, which stay in L2, and the
 // last tiles to be claimed are short. Longer sequences come before shorter ones.
@@ -65,17 +68,31 @@ constexpr float RESCALE_LOG2 = 8.f;
 constexpr long long WAIT_LIMIT_CLOCKS = 4000000000ll;   // about two seconds
 constexpr int PLAN_THREADS = 1024;
 
-// Workspace: the next tile to claim, the number of tiles, then the sequences in
-// the order they are worked on and the tiles before each.
+// Workspace: the next tile to claim, the number of tiles (parts of one count), the
+// largest number of parts; the sequences in the order they are worked on, the
+// tiles before each; and for calls that may split: a record, log2 sums and outputs
+// (fp32, normalised) per part.
 struct Layout {
-  size_t order, first, total;
+  size_t order, first, rec, lse, o, total;
 };
-Layout layout(int32_t B) {
+constexpr int MAX_PAIRS = 76;      // 152 SMs
+// A tile is cut into parts of MIN_STEPS or more if its longest part is at least
+// MIN_SAVED steps shorter than the whole: the partial results and their join take 6-8
+// us, a step 1.6. (16 heads, chunk 512 after 32768 keys: 394 -> 117 us; 128 after 8192:
+// 106 -> 32; cut all the same, 256 after 700 took 29 us instead of 25.)
+constexpr int MIN_STEPS = 4, MIN_SAVED = 8;
+// Whether a call's tiles can be few enough to split (its padding rows aside).
+bool may_split(int32_t Tq, int32_t H) { return (int64_t)Tq * H * 2 <= (int64_t)ROWS * MAX_PAIRS; }
+Layout layout(int32_t B, int32_t Tq, int32_t H) {
   auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t parts = may_split(Tq, H) ? MAX_PAIRS : 0;
   Layout l;
   l.order = 256;
   l.first = l.order + al((size_t)B * 4);
-  l.total = l.first + al(((size_t)B + 1) * 4);
+  l.rec = l.first + al(((size_t)B + 1) * 4);
+  l.lse = l.rec + al(parts * 128);
+  l.o = l.lse + parts * ROWS * 4;
+  l.total = l.o + parts * ROWS * DV * 4;
   return l;
 }
 
@@ -87,6 +104,9 @@ struct PrefillP {
   void* out;
   float* lse;
   int32_t *ctrl, *order, *first;
+  char* rec;        // null: the call does not split
+  float* part_lse;
+  float4* part_o;
   int32_t* dev_status;
 };
 
@@ -99,6 +119,11 @@ __device__ __forceinline__ int narrow_rows(int q) {
   return rest <= QM ? rest : 0;
 }
 __device__ __forceinline__ int wide_tiles(int q) { return q / ROWS + (q % ROWS > QM); }
+// Parts of a tile of a sequence with L keys, of which there may be `most`.
+__device__ __forceinline__ int parts_of(int L, int most) {
+  const int n = (L + BN - 1) / BN, parts = max(1, min(most, n / MIN_STEPS));
+  return n - (n + parts - 1) / parts >= MIN_SAVED ? parts : 1;
+}
 
 // One CTA: checks the lengths, orders the sequences by keys (descending, up to
 // PLAN_THREADS of them; more stay in their own order) and counts their tiles. The
@@ -107,10 +132,11 @@ __device__ __forceinline__ int wide_tiles(int q) { return q / ROWS + (q % ROWS >
 __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const int32_t* __restrict__ cu_q,
                                                                           const int32_t* __restrict__ cu_k,
                                                                           int32_t B, int32_t Tq, int32_t Tk,
-                                                                          int32_t H, int32_t pairs, int32_t* ctrl,
+                                                                          int32_t H, int32_t pairs, int32_t split,
+                                                                          int32_t* ctrl,
                                                                           int32_t* order, int32_t* first,
                                                                           int32_t* dev_status) {
-  __shared__ int s_cost[PLAN_THREADS], s_rank[PLAN_THREADS], s_scan[32], s_carry;
+  __shared__ int s_cost[PLAN_THREADS], s_rank[PLAN_THREADS], s_scan[32], s_carry, s_all;
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nt = blockDim.x;
@@ -119,6 +145,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
   for (int b = tid; b < B; b += nt)
     bad |= __ldg(cu_q + b + 1) < __ldg(cu_q + b) || __ldg(cu_k + b + 1) < __ldg(cu_k + b);
   bad = __syncthreads_or(bad);
+  if (tid == 0) s_all = 0;
+  int parts = 1;
   auto tiles_of = [&](int b, int* keys) {
     const int q = __ldg(cu_q + b + 1) - __ldg(cu_q + b), L = __ldg(cu_k + b + 1) - __ldg(cu_k + b);
     *keys = L;
@@ -127,8 +155,16 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
       atomicOr(dev_status, PKV_DEV_BAD_LENGTHS);
       return 0;
     }
-    return wide_tiles(q) * H + (narrow_rows(q) ? (H + 1) / 2 : 0);
+    return (wide_tiles(q) * H + (narrow_rows(q) ? (H + 1) / 2 : 0)) * parts_of(L, parts);
   };
+  if (split) {
+    __syncthreads();
+    int keys, mine = 0;   // (no more than pairs + 1 counts)
+    for (int b = tid; b < B; b += nt) mine = min(pairs + 1, mine + min(pairs + 1, tiles_of(b, &keys)));
+    if (mine > 0) atomicAdd(&s_all, mine);
+    __syncthreads();
+    if (s_all > 0) parts = max(1, pairs / s_all);
+  }
   if (sorted) {
     int keys = 0;
     const int n = tid < B ? tiles_of(tid, &keys) : 0;
@@ -177,6 +213,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
     first[B] = s_carry;
     ctrl[0] = pairs;   // a pair's first tile has the pair's number
     ctrl[1] = s_carry;
+    ctrl[2] = parts;
     if (bad) atomicOr(dev_status, PKV_DEV_BAD_LENGTHS);
   }
 }
@@ -184,10 +221,22 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
 // A work tile. Query tile w: head h[w], nr[w] rows (0: none) from packed row row0[w],
 // the first at position pos[w], reading n[w] key tiles. split: the two tiles
 // are of two heads, with keys of their own.
+// The work is steps [j0, j1) of the n[] key tiles: part number part of parts,
+// the tile's first part being item number item0.
 struct Tile {
   int valid, split, k0, L;
+  int j0, j1, part, parts, item0;
   int h[2], row0[2], nr[2], pos[2], n[2];
 };
+static_assert(sizeof(Tile) <= 128, "record");
+// First step of a part of n steps (fewer than 2^24 steps and 2^7 parts).
+__device__ __forceinline__ int part_begin(int n, int part, int parts) { return n * part / parts; }
+
+// Partial outputs: for a part and 128 rows (a CTA's of a query tile), four columns
+// at a time, the rows side by side. The vector of row r (of ROWS) and columns 4 c ..
+__device__ __forceinline__ int64_t part_vec(int item, int r, int c) {
+  return (((int64_t)item * (ROWS / BM) + r / BM) * (DV / 4) + c) * BM + r % BM;
+}
 
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
@@ -276,33 +325,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 
   if (warp == 0) {
     // --------------------------------------------------------------- producer
-    const int n_tiles = *(volatile const int32_t*)&p.ctrl[1];
+    const int n_tiles = *(volatile const int32_t*)&p.ctrl[1], most_parts = *(volatile const int32_t*)&p.ctrl[2];
     const uint32_t q_bar = map_to_rank(&bar_q, 0);
+    uint32_t n_claims = 0;
     uint32_t n_k = 0, n_v = 0, n_tail = 0;    // K, V loads and last tiles with rows to zero so far
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t & 1;
       if (rank == 0) {
         // entry e is free again once every consumer is done with tile t - 2
         if (t >= 2 && !(ok = wait(&bar_tempty[e], ((t >> 1) - 1) & 1))) break;
-        int tt = t == 0 ? (int)(blockIdx.x >> 1) : lane == 0 ? atomicAdd(&p.ctrl[0], 1) : 0;
-        tt = __shfl_sync(0xffffffffu, tt, 0);
-        if (__any_sync(0xffffffffu, s_abort)) tt = n_tiles;
-        int lo = 0;   // the last sequence that starts at or before tile tt, searched 32 ways
-        for (int m = p.B; m > 1;) {
-          const int step = (m + 31) / 32, at = lo + lane * step;
-          const bool before = lane * step < m && p.first[at] <= tt;
-          lo += (__popc(__ballot_sync(0xffffffffu, before)) - 1) * step;
-          m = min(step, p.B - lo);
-        }
-        if (lane == 0) {
-          Tile ti{};
+        Tile ti{};
+        for (bool skip = true; skip;) {
+          int tt = n_claims++ == 0 ? (int)(blockIdx.x >> 1) : lane == 0 ? atomicAdd(&p.ctrl[0], 1) : 0;
+          tt = __shfl_sync(0xffffffffu, tt, 0);
+          if (__any_sync(0xffffffffu, s_abort)) tt = n_tiles;
+          int lo = 0;   // the last sequence that starts at or before tile tt, searched 32 ways
+          for (int m = p.B; m > 1;) {
+            const int step = (m + 31) / 32, at = lo + lane * step;
+            const bool before = lane * step < m && p.first[at] <= tt;
+            lo += (__popc(__ballot_sync(0xffffffffu, before)) - 1) * step;
+            m = min(step, p.B - lo);
+          }
+          skip = false;
           if (tt < n_tiles) {
-            const int b = p.order[lo];
+            const int b = p.order[lo], before = p.first[lo];
             const int q_lo = __ldg(p.cu_q + b), q = __ldg(p.cu_q + b + 1) - q_lo;
             ti.k0 = __ldg(p.cu_k + b);
             ti.L = __ldg(p.cu_k + b + 1) - ti.k0;
             const int wide = wide_tiles(q), rest = narrow_rows(q);
-            int at = tt - p.first[lo];
+            int at = tt - before;
+            ti.parts = 1;
+            ti.part = 0;
+            if (most_parts > 1) {
+              ti.parts = parts_of(ti.L, most_parts);
+              ti.part = at % ti.parts;
+              at /= ti.parts;
+            }
+            ti.item0 = tt - ti.part;
             ti.split = at >= wide * p.H;
             const int h = ti.split ? (at - wide * p.H) * 2 : at / wide;
             const int q0 = ti.split ? 0 : rest + (wide - 1 - (at - h * wide)) * ROWS;
@@ -315,8 +374,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
               ti.pos[w] = ti.L - q + q_w;
               ti.n[w] = ti.nr[w] ? (ti.pos[w] + ti.nr[w] + BN - 1) / BN : 0;
             }
+            const int n = max(ti.n[0], ti.n[1]);
+            ti.parts = min(ti.parts, n);   // (a tile's own steps may be fewer than its sequence's)
+            skip = ti.part >= ti.parts;
+            ti.j0 = 0;
+            ti.j1 = n;
+            if (ti.parts > 1 && !skip) {
+              ti.j0 = part_begin(n, ti.part, ti.parts);
+              ti.j1 = part_begin(n, ti.part + 1, ti.parts);
+            }
             ti.valid = 1;
+            if (most_parts > 1 && lane == 0) *reinterpret_cast<Tile*>(p.rec + (size_t)tt * 128) = ti;
+          } else {
+            ti.valid = 0;
           }
+        }
+        if (lane == 0) {
           s_tile[e] = ti;
           const uint32_t peer = map_to_rank(&s_tile[e], 1);
           const uint32_t* words = reinterpret_cast<const uint32_t*>(&ti);
@@ -331,7 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (!(ok = wait_tile(t))) break;
       const Tile ti = s_tile[e];
       if (!ti.valid) break;
-      const int n = max(ti.n[0], ti.n[1]), streams = ti.split && ti.nr[1] ? 2 : 1;
+      const int streams = ti.split && ti.nr[1] ? 2 : 1;
       // Q of this tile replaces the one before once its last S is done
       if (t >= 1 && !(ok = wait(&bar_qempty, (t - 1) & 1))) break;
       if (lane == 0) {
@@ -344,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
               tma_load_3d_pair(sQ + w * Q_BYTES + c * UNIT, &mq, q_bar, c * 64, ti.h[w], ti.row0[w] + (int)rank * BM);
       }
       __syncwarp();
-      for (int j = 0; j < n && ok; ++j) {
+      for (int j = ti.j0; j < ti.j1 && ok; ++j) {
         for (int w = 0; w < streams; ++w, ++n_k) {
           const uint32_t slot = n_k % NK;
           if (!(ok = wait(&bar_kempty[slot], ((n_k / NK) & 1) ^ 1))) break;
@@ -412,7 +485,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         const uint32_t e = t & 1;
         if (!(ok = wait_tile(t))) break;
         if (!s_tile[e].valid) break;
-        const int mine = s_tile[e].n[w], n = max(s_tile[e].n[0], s_tile[e].n[1]);
+        const int n = s_tile[e].j1 - s_tile[e].j0;               // steps, and those of this query tile
+        const int mine = max(0, min(n, s_tile[e].n[w] - s_tile[e].j0));
         const bool both = s_tile[e].nr[1] != 0, split = s_tile[e].split && both;
         const bool active = mine > 0;
         // a slot that one tile alone reads is released by two commits of its issuer
@@ -491,12 +565,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (!(ok = wait_tile(t))) break;
       const Tile& ti = s_tile[e];
       if (!ti.valid) break;
-      const int n = ti.n[w];
-      if (n > 0) {
+      const int j0 = ti.j0, j1 = min(ti.j1, ti.n[w]);
+      if (j0 < j1) {
         const int pos = min(ti.pos[w] + i, ti.L - 1);
         const int j_mask = (ti.pos[w] + (int)rank * BM + 1) / BN;   // key tiles before have no hidden key
         float m_run = -INFINITY, l_run = 0.f;
-        for (int j = 0; j < n; ++j) {
+        for (int j = j0; j < j1; ++j) {
           // S complete also means that the product that read P is
           if (!(ok = wait(&bar_s[w], n_s & 1))) break;
           ++n_s;
@@ -534,10 +608,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
               mx[(k >> 1) & 7] = max3(mx[(k >> 1) & 7], __uint_as_float(r[c >> 1][c & 1][k]),
                                       __uint_as_float(r[c >> 1][c & 1][k + 1]));
           const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
-          const bool first = j == 0;
+          const bool first = j == j0;
           const bool grow = first || mt > m_run + RESCALE_LOG2;
           const float m_new = grow ? fmaxf(mt, m_run) : m_run;
           if (!first && __any_sync(0xffffffffu, grow)) {
+            // (m_new is finite: it grew)
             const float alpha = grow ? ex2(m_run - m_new) : 1.f;
             l_run *= alpha;
 #pragma unroll 1
@@ -550,7 +625,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
           }
           m_run = m_new;
-          const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-m_run, -m_run);
+          // a row that sees no key of this part so far has m = -inf: its weights are 0
+          const float nm = m_run == -INFINITY ? 0.f : -m_run;
+          const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
           float2 ls[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
@@ -585,14 +662,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         ++n_o;
         tc_fence_after();
         const bool store = i < ti.nr[w];
-        const float inv = 1.f / l_run;
+        const bool whole = ti.parts == 1;
+        const float inv = m_run == -INFINITY ? 0.f : 1.f / l_run;   // no visible key in a part: zeros
         const int64_t row = (int64_t)(ti.row0[w] + i) * p.H + ti.h[w];
+        const int prow = (ti.item0 + ti.part) * ROWS + w * QM + i;
+        float4* part = p.part_o + part_vec(ti.item0 + ti.part, w * QM + i, 0);
         T* dst = (T*)p.out + row * DV;
 #pragma unroll 1
         for (int c = 0; c < DV / 32; ++c) {
           uint32_t o[32];
           tmem_ld32_wait(tmem + lrow + o_col + c * 32, o);
           if (!store) continue;
+          if (!whole) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              part[(c * 8 + v) * BM] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                                   __uint_as_float(o[4 * v + 2]) * inv,
+                                                   __uint_as_float(o[4 * v + 3]) * inv);
+            continue;
+          }
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             uint32_t y[4];
@@ -602,7 +690,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             *reinterpret_cast<uint4*>(dst + c * 32 + v * 8) = make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
-        if (store && p.lse) p.lse[row] = (m_run + __log2f(l_run)) * LN2;
+        const float lg = m_run == -INFINITY ? -INFINITY : m_run + __log2f(l_run);
+        if (store && !whole) p.part_lse[prow] = lg;
+        else if (store && p.lse) p.lse[row] = lg * LN2;
         tc_fence_before();
       }
       __syncwarp();
@@ -623,6 +713,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, TMEM_COLS);
 }
 
+// Joins a tile's parts: a row's parts weighted by 2^(lse_s - max), in the order of
+// the keys. The blocks of all its parts share the tile's groups of 8 rows; 8 threads
+// read the 128 bytes of 8 rows.
+constexpr int CROWS = 8, CY = 8;
+template <typename T>
+__global__ void __launch_bounds__(CROWS * DV / 4) latent_prefill_combine_kernel(PrefillP p) {
+  pdl_wait();
+  const int item = blockIdx.x;
+  if (p.ctrl[2] == 1 || item >= p.ctrl[1]) return;
+  const Tile ti = *reinterpret_cast<const Tile*>(p.rec + (size_t)item * 128);
+  if (ti.parts == 1 || ti.part >= ti.parts) return;
+  const int n = max(ti.n[0], ti.n[1]);
+  const int c = threadIdx.x / CROWS;
+  for (int g = blockIdx.y + CY * ti.part; g < ROWS / CROWS; g += CY * ti.parts) {
+    const int r = g * CROWS + threadIdx.x % CROWS, w = r / QM;
+    if (r % QM >= ti.nr[w]) continue;
+    // parts that begin behind the query tile's last key have nothing for it
+    int parts = ti.parts;
+    while (part_begin(n, parts - 1, ti.parts) >= ti.n[w]) --parts;
+    float m = -INFINITY;
+    for (int s = 0; s < parts; ++s) m = fmaxf(m, p.part_lse[(ti.item0 + s) * ROWS + r]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float total = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+      const float f = exp2f(p.part_lse[(ti.item0 + s) * ROWS + r] - m);
+      const float4 y = p.part_o[part_vec(ti.item0 + s, r, c)];
+      total += f;
+      o.x += f * y.x;
+      o.y += f * y.y;
+      o.z += f * y.z;
+      o.w += f * y.w;
+    }
+    const float inv = 1.f / total;
+    const int64_t row = (int64_t)(ti.row0[w] + r % QM) * p.H + ti.h[w];
+    *reinterpret_cast<uint2*>((T*)p.out + row * DV + c * 4) =
+        make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+    if (p.lse && c == 0) p.lse[row] = (m + log2f(total)) * LN2;
+  }
+}
+
 template <typename T>
 cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};   // devices whose kernel attribute is set
@@ -634,7 +765,10 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
   }
   const CUtensorMapDataType dt =
       std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const Layout lay = layout(a.B);
+  const Layout lay = layout(a.B, a.Tq, a.H);
+  const int pairs = a.dev.num_sms / 2 < MAX_PAIRS ? a.dev.num_sms / 2 : MAX_PAIRS;
+  // (a tile of fewer steps than the two add up to is never cut)
+  const bool split = may_split(a.Tq, a.H) && a.Tk > (MIN_SAVED + MIN_STEPS - 1) * BN;
   PrefillP p;
   p.cu_q = a.cu_q;
   p.cu_k = a.cu_k;
@@ -650,6 +784,9 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
   p.ctrl = (int32_t*)a.ws;
   p.order = (int32_t*)(a.ws + lay.order);
   p.first = (int32_t*)(a.ws + lay.first);
+  p.rec = split ? a.ws + lay.rec : nullptr;
+  p.part_lse = (float*)(a.ws + lay.lse);
+  p.part_o = (float4*)(a.ws + lay.o);
   p.dev_status = a.dev.status;
   auto row_stride = [&](int64_t st) { return a.Tk > 1 ? st : (int64_t)NOPE; };
   CUtensorMap mq, mk, mv, mr;
@@ -665,17 +802,21 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
     KernelTimer timer("latent_prefill_plan", s);
     e = launch_after_trigger(latent_prefill_plan_kernel, dim3(1),
                              dim3(a.B < PLAN_THREADS ? (a.B + 31) / 32 * 32 : PLAN_THREADS), 0, s, a.cu_q, a.cu_k, a.B, a.Tq,
-                             a.Tk, a.H, a.dev.num_sms / 2, p.ctrl, p.order, p.first, a.dev.status);
+                             a.Tk, a.H, pairs, split ? 1 : 0, p.ctrl, p.order, p.first, a.dev.status);
   }
   if (e != cudaSuccess) return e;
-  KernelTimer timer("latent_prefill", s);
-  return launch_after_trigger(latent_prefill_kernel<T>, dim3(a.dev.num_sms / 2 * 2), dim3(NTHREADS), SMEM, s, mq, mk, mv, mr,
-                              p);
+  {
+    KernelTimer timer("latent_prefill", s);
+    e = launch_after_trigger(latent_prefill_kernel<T>, dim3(2 * pairs), dim3(NTHREADS), SMEM, s, mq, mk, mv, mr, p);
+  }
+  if (e != cudaSuccess || !split) return e;
+  KernelTimer timer("latent_combine", s);
+  return launch_after_trigger(latent_prefill_combine_kernel<T>, dim3(pairs, CY), dim3(CROWS * DV / 4), 0, s, p);
 }
 
 }  // namespace
 
-size_t latent_prefill_workspace(int32_t B, int32_t, int32_t) { return layout(B).total; }
+size_t latent_prefill_workspace(int32_t B, int32_t Tq, int32_t H) { return layout(B, Tq, H).total; }
 
 cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, cudaStream_t s) {
   return a.dtype == PKV_BF16 ? launch<__nv_bfloat16>(a, s) : launch<__half>(a, s);

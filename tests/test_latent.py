@@ -477,6 +477,13 @@ EXPANDED = [
     ("bf16", 81, [100, 3], [200, 131]),
     ("f16", 80, [200, 600], [200, 700]),
     ("bf16", 161, [1, 129], [300, 129]),
+    # few tiles and many keys: the keys are split, and some parts hold no key of some rows
+    ("bf16", 1, [5], [5000]),
+    ("f16", 3, [300, 20], [3000, 1500]),
+    ("bf16", 2, [700], [2100]),
+    ("bf16", 1, [2048], [2048]),
+    ("f16", 1, [1300, 1, 40], [1300, 900, 1025]),
+    ("bf16", 5, [256, 0, 257], [1153, 50, 1024]),
 ]
 
 
