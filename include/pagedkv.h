@@ -448,7 +448,7 @@ int pkv_latent_gather(const void* cache, const pkv_latent_desc* desc, const int3
  *                 the absorbed part first, then the rotated rotary part
  *   cu_seqlens_q, kv_lens, page_tables, max_kv_len, lse  as pkv_paged_attention, but for
  *                 cu[num_seqs], which may be less than total_q: rows from there on
- *                 are padding, not read and left as they were
+ *                 are padding, may hold anything and are left as they were
  *   scale         > 0 and finite; multiplies q . [c, r] before the softmax
  *   out           device, contiguous [total_q, num_q_heads, latent_dim], cache dtype
  *   workspace     device, >= pkv_latent_attention_workspace_size(...) bytes, 256-byte
@@ -458,8 +458,13 @@ int pkv_latent_gather(const void* cache, const pkv_latent_desc* desc, const int3
  * cache dtype for the products with the latent parts. Keys of a sequence are
  * split over the GPU by the tick's total work, so the order of a row's fp32 sums
  * depends on the other rows of the tick (the same call gives the same bits).
- * Bad lengths or pages skip the sequence's rows as in pkv_paged_attention (bad
- * cu_seqlens_q: every row). num_q_heads is at most 4096.
+ * Bad lengths skip the sequence's rows as in pkv_paged_attention (bad
+ * cu_seqlens_q: every row). A page id outside the pool sets PKV_DEV_BAD_PAGE, and the
+ * rows that need the page, with up to 127 (token, head) rows of the sequence beside
+ * them, are left unwritten. Slots that no sequence owns may hold anything. A NaN or an
+ * infinity in a sequence's own row reaches every row that sees it, and may reach
+ * earlier rows of the same chunk (0 * NaN, as in a product with a masked weight
+ * matrix). num_q_heads is at most 4096.
  * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_WORKSPACE, PKV_E_DEVICE, PKV_E_CUDA. */
 size_t pkv_latent_attention_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_q_heads,
                                            const pkv_latent_desc* desc);
@@ -478,7 +483,7 @@ int pkv_latent_attention(const void* q, const int32_t* cu_seqlens_q, const int32
  *   k_rope        device, shared rotary key part of row t at + t * kr_stride, 64 values
  *   cu_seqlens_q, cu_seqlens_k  device, int32 [num_seqs + 1]: rows of q / of the keys by
  *                 sequence; from 0, non-decreasing, ending at or before total_q /
- *                 total_k (rows behind are padding, not read and left as they were)
+ *                 total_k (rows behind are padding, may hold anything and are left as they were)
  *   dtype         PKV_BF16 or PKV_F16, of q, k_nope, v, k_rope and out
  *   scale         > 0 and finite
  *   out           device, contiguous [total_q, num_heads, 128]
@@ -489,7 +494,11 @@ int pkv_latent_attention(const void* q, const int32_t* cu_seqlens_q, const int32
  * them are the chunk's own. A sequence with rows and fewer keys than rows sets
  * PKV_DEV_BAD_LENGTHS and is skipped; a cu_seqlens array that breaks the rules
  * above skips every row. Strides are in elements, multiples of 8; pointers
- * 16-byte aligned. Values of other sequences' rows never reach a row, NaN or not.
+ * 16-byte aligned. Values of other sequences' rows never reach a row, NaN or not; a
+ * NaN or an infinity in a sequence's own key or value reaches every row that sees
+ * it, and may reach earlier rows of the same chunk (0 * NaN). Calls of few tiles
+ * split their keys over the GPU by the tick's total work: the order of a row's
+ * fp32 sums then depends on the other rows (the same call gives the same bits).
  * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_WORKSPACE, PKV_E_DEVICE, PKV_E_CUDA. */
 size_t pkv_latent_prefill_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_heads);
 int pkv_latent_prefill(const void* q, const int32_t* cu_seqlens_q, const void* k_nope, int64_t kn_stride_t,

@@ -601,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
       const bool whole = g.j0 == 0 && g.j1 == g.n;
       const bool store = r < g.nrows && !(whole && bad);
       const int slot = 2 * pair + (g.j0 == 0 ? 1 : 0);
-      const float inv = m_run == -INFINITY ? 0.f : 1.f / l;   // no visible key in a partial run: zeros
+      const float inv = l == 0.f ? 0.f : 1.f / l;   // no visible key in a partial run: zeros
       const int64_t row = (int64_t)g.row0 + r;
       T* dst = (T*)p.out + row * LD + half * (LD / 2) + sub * OC;
       float4* part = (float4*)(p.ws + Layout::o) + Layout::vec(LD, slot, rank, sub * (OC / 4), quarter * 32 + lane);
@@ -633,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
         }
       }
       if (store && who == 0) {
-        const float lg = m_run == -INFINITY ? -INFINITY : m_run + __log2f(l);
+        const float lg = l == 0.f ? -INFINITY : m_run + __log2f(l);   // (NaN scores: m may be -inf, l is NaN)
         if (!whole) ((float*)(p.ws + Layout::lse))[slot * BM + r] = lg;
         else if (p.lse) p.lse[row] = lg * LN2;
       }

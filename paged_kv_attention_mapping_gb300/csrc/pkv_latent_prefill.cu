@@ -663,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         tc_fence_after();
         const bool store = i < ti.nr[w];
         const bool whole = ti.parts == 1;
-        const float inv = m_run == -INFINITY ? 0.f : 1.f / l_run;   // no visible key in a part: zeros
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;   // no visible key in a part: zeros
         const int64_t row = (int64_t)(ti.row0[w] + i) * p.H + ti.h[w];
         const int prow = (ti.item0 + ti.part) * ROWS + w * QM + i;
         float4* part = p.part_o + part_vec(ti.item0 + ti.part, w * QM + i, 0);
@@ -690,7 +690,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             *reinterpret_cast<uint4*>(dst + c * 32 + v * 8) = make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
-        const float lg = m_run == -INFINITY ? -INFINITY : m_run + __log2f(l_run);
+        const float lg = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);   // (NaN scores: m may be -inf, l_run is NaN)
         if (store && !whole) p.part_lse[prow] = lg;
         else if (store && p.lse) p.lse[row] = lg * LN2;
         tc_fence_before();

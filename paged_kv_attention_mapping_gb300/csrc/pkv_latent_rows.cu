@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int r = fr + x * 8;
         if (r >= g.nrows || (whole && bad)) continue;
         // no visible key in a partial run: zeros
-        const float inv = sh.m[r] == -INFINITY ? 0.f : 1.f / sh.l[r];
+        const float inv = sh.l[r] == 0.f ? 0.f : 1.f / sh.l[r];
         const int64_t row = (int64_t)g.row0 + r;
         T* dst = (T*)p.out + row * LD + d0 + fc;
         float* part = (float*)(p.ws + Layout::o) + ((int64_t)slot * TM + r) * LD + d0 + fc;
@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
       if (tid < TM && tid < g.nrows) {
-        const float m = sh.m[tid];
-        const float lg = m == -INFINITY ? -INFINITY : m + __log2f(sh.l[tid]);
+        const float l = sh.l[tid];
+        const float lg = l == 0.f ? -INFINITY : sh.m[tid] + __log2f(l);   // (NaN scores: m may be -inf, l is NaN)
         if (!whole) ((float*)(p.ws + Layout::lse))[slot * TM + tid] = lg;
         else if (p.lse && !bad) p.lse[(int64_t)g.row0 + tid] = lg * LN2;
       }

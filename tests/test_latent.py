@@ -368,6 +368,23 @@ def test_absorbed_same_call_same_bits(dev, heads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv", [(40, 90), (40, 9000), (4, 50), (4, 9000)])
+def test_absorbed_nan_in_a_query_or_a_visible_key(dev, heads, kv):
+    """NaN stays with the rows that it belongs to, in out and in lse."""
+    t = Paged(dev, "bf16", 512, heads, 64, [1, 1, 1], [kv, 70, kv])
+    good, good_lse = t.call()
+    t.q[0, 1] = float("nan")
+    key = kv - 3
+    t.cache[int(t.table[2, key // 64]), key % 64, 5] = float("nan")
+    out, lse = t.call()
+    assert binding.device_status() == 0
+    assert out[0, 1].isnan().all() and lse[0, 1].isnan()
+    assert out[2].isnan().all() and lse[2].isnan().all()
+    for rows in ((0, slice(0, 1)), (0, slice(2, None)), (1, slice(None))):
+        assert torch.equal(out[rows], good[rows]) and torch.equal(lse[rows], good_lse[rows])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("heads", [16, 4])
 def test_absorbed_bad_data_skips_the_sequence(dev, heads):
     """A bad length or page skips that sequence's rows, a bad cu_seqlens_q every row."""
@@ -528,6 +545,24 @@ def test_expanded_other_rows_never_reach_a_row(dev):
     t.check(out, lse, only=(0, 2))
     assert (out[120:] == 5).all() and (lse[120:] == 5).all()
     assert torch.isnan(out[40:90]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", [200, 6000])
+def test_expanded_nan_in_a_query_or_a_visible_key(dev, kv):
+    """NaN stays with the rows that it belongs to, in out and in lse."""
+    t = Packed(dev, "bf16", 4, [3, 2], [kv, kv])
+    good, good_lse = t.call()
+    t.q[0, 1] = float("nan")
+    t.kn[kv + 7, 2, 3] = float("nan")
+    out, lse = t.call()
+    assert binding.device_status() == 0
+    assert out[0, 1].isnan().all() and lse[0, 1].isnan()
+    assert out[3:, 2].isnan().all() and lse[3:, 2].isnan().all()
+    keep = torch.ones((5, 4), dtype=torch.bool, device=dev)
+    keep[0, 1] = False
+    keep[3:, 2] = False
+    assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], good_lse[keep])
 
 
 @pytest.mark.gpu
