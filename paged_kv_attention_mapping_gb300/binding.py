@@ -483,15 +483,19 @@ def rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, 
 LATENT_NOPE, LATENT_ROPE, LATENT_V = 128, 64, 128
 
 
+# The smallest ticks are a few microseconds of GPU work, so these checks are written
+# for few attribute reads: a tensor's shape, strides or type is read once.
+
 @functools.lru_cache(maxsize=256)
-def _latent_desc_of(N, P, R, dtype) -> LatentDesc:
-    return LatentDesc(N, P, R - LATENT_ROPE, LATENT_ROPE, dtype)
+def _latent_desc_of(shape, dtype) -> LatentDesc:
+    N, P, R = shape
+    return LatentDesc(N, P, R - LATENT_ROPE, LATENT_ROPE, _code_of(dtype))
 
 
 def _latent_desc(where, cache) -> LatentDesc:
     if cache.dim() != 3 or not cache.is_contiguous():
         raise ValueError(f"{where}: the latent cache must be a contiguous [num_pages, page_size, latent_dim + 64] tensor")
-    return _latent_desc_of(*cache.shape, _dtype_code(cache))
+    return _latent_desc_of(cache.shape, cache.dtype)
 
 
 def _on_one_device(where, first, *rest) -> int:
@@ -515,24 +519,16 @@ def _call_on(dev, stream, fn, *args) -> int:
     return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream))
 
 
-def _rows_of(where, name, t, dims, width, dtype):
-    """Strides of a [..., width] view whose last dimension is contiguous and whose
-    rows may be strided (0 for a dimension of one entry)."""
-    st, shape = t.stride(), t.shape
-    if len(st) != dims or shape[-1] != width or t.dtype != dtype:
-        raise ValueError(f"{where}: {name} must have {dims} dimensions, be {width} wide, and share the others' dtype")
-    if st[-1] != 1:
-        raise ValueError(f"{where}: {name} must be contiguous in its last dimension")
-    return tuple(0 if n == 1 else x for n, x in zip(shape, st)) if 1 in shape else st
+def _rows_only(where, *last):
+    """Refuses views whose last stride is not 1."""
+    for x in last:
+        if x != 1:
+            raise ValueError(f"{where}: tensors of rows must be contiguous in their last dimension")
 
 
-def _int32s(where, *tensors):
-    import torch
-    for t in tensors:
-        if t.dtype != torch.int32:
-            raise TypeError(f"{where}: index tensors must be int32")
-        if not t.is_contiguous():
-            raise ValueError(f"{where}: index tensors must be contiguous")
+def _bad_out(where, width):
+    return ValueError(f"{where}: out must be a contiguous [T, H, {width}] tensor of q's dtype, lse a contiguous "
+                      "float32 tensor [T, H]")
 
 
 def _lent(t, stream):
@@ -541,22 +537,6 @@ def _lent(t, stream):
     if stream is not None:
         t.record_stream(stream)
     return t
-
-
-def _out_and_lse(where, q, width, out, lse, want_lse, stream):
-    """The caller's out [T, H, width] and lse [T, H], checked, or new ones."""
-    import torch
-    T, H = q.shape[:2]
-    if out is None:
-        out = _lent(torch.empty((T, H, width), dtype=q.dtype, device=q.device), stream)
-    elif out.dtype != q.dtype or out.shape != (T, H, width) or not out.is_contiguous():
-        raise ValueError(f"{where}: out must be a contiguous [{T}, {H}, {width}] tensor of q's dtype")
-    if lse is None:
-        if want_lse:
-            lse = _lent(torch.empty((T, H), dtype=torch.float32, device=q.device), stream)
-    elif lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
-        raise ValueError(f"{where}: lse must be a contiguous float32 tensor [T, H]")
-    return out, lse
 
 
 def latent_append(c_kv, k_rope, positions, cos_sin, slot_mapping, cache, q_rope=None, q_out=None, stream=None):
@@ -571,35 +551,44 @@ def latent_append(c_kv, k_rope, positions, cos_sin, slot_mapping, cache, q_rope=
     where = "latent_append"
     desc = _latent_desc(where, cache)
     dev = _on_one_device(where, cache, c_kv, k_rope, positions, cos_sin, slot_mapping, q_rope, q_out)
-    T = slot_mapping.shape[0]
-    if positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64 or cos_sin.dtype != torch.float32:
+    if (positions.dtype is not torch.int32 or slot_mapping.dtype is not torch.int64
+            or cos_sin.dtype is not torch.float32):
         raise TypeError(f"{where}: positions int32, slot_mapping int64, cos_sin float32")
     if not (positions.is_contiguous() and slot_mapping.is_contiguous() and cos_sin.is_contiguous()):
         raise ValueError(f"{where}: positions, slot_mapping and cos_sin must be contiguous")
-    if (slot_mapping.dim() != 1 or positions.shape != (T,) or cos_sin.dim() != 3
-            or cos_sin.shape[1:] != (LATENT_ROPE // 2, 2) or c_kv.shape[0] != T or k_rope.shape[0] != T):
-        raise ValueError(f"{where}: c_kv, k_rope, positions and slot_mapping must agree on the number of tokens, "
-                         f"and cos_sin be [max_pos, {LATENT_ROPE // 2}, 2]")
-    dtype = cache.dtype
-    c_st, _ = _rows_of(where, "c_kv", c_kv, 2, desc.latent_dim, dtype)
-    kr_st, _ = _rows_of(where, "k_rope", k_rope, 2, LATENT_ROPE, dtype)
+    dtype, tokens, table = cache.dtype, slot_mapping.shape, cos_sin.shape
+    if len(tokens) != 1 or positions.shape != tokens or len(table) != 3 or table[1:] != (LATENT_ROPE // 2, 2):
+        raise ValueError(f"{where}: positions and slot_mapping must be [T], cos_sin [max_pos, {LATENT_ROPE // 2}, 2]")
+    T, = tokens
+    if (c_kv.dtype is not dtype or k_rope.dtype is not dtype or c_kv.shape != (T, desc.latent_dim)
+            or k_rope.shape != (T, LATENT_ROPE)):
+        raise ValueError(f"{where}: c_kv must be [T, {desc.latent_dim}], k_rope [T, {LATENT_ROPE}], of the cache's dtype")
+    (c_st, c_1), (kr_st, kr_1) = c_kv.stride(), k_rope.stride()
+    _rows_only(where, c_1, kr_1)
+    q = qo = None
     q_st = q_sh = qo_st = qo_sh = H = 0
     if q_rope is not None:
-        q_st, q_sh, _ = _rows_of(where, "q_rope", q_rope, 3, LATENT_ROPE, dtype)
-        H = q_rope.shape[1]
+        shape = q_rope.shape
         if q_out is None:
-            q_out = _lent(torch.empty(q_rope.shape, dtype=q_rope.dtype, device=q_rope.device), stream)
-        qo_st, qo_sh, _ = _rows_of(where, "q_out", q_out, 3, LATENT_ROPE, dtype)
-        if q_rope.shape[0] != T or q_out.shape != q_rope.shape:
-            raise ValueError(f"{where}: q_rope and q_out must be [T, H, {LATENT_ROPE}]")
+            q_out = _lent(torch.empty(shape, dtype=dtype, device=q_rope.device), stream)
+        if (q_rope.dtype is not dtype or q_out.dtype is not dtype or len(shape) != 3 or shape[0] != T
+                or shape[2] != LATENT_ROPE or q_out.shape != shape):
+            raise ValueError(f"{where}: q_rope and q_out must be [T, H, {LATENT_ROPE}] of the cache's dtype")
+        H = shape[1]
+        (q_st, q_sh, q_1), (qo_st, qo_sh, qo_1) = q_rope.stride(), q_out.stride()
+        _rows_only(where, q_1, qo_1)
         if (T > 1 and qo_st == 0) or (H > 1 and qo_sh == 0):
             raise ValueError(f"{where}: q_out must not be a broadcast view")
+        if H == 1:
+            q_sh = qo_sh = 0
+        q, qo = q_rope.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError(f"{where}: q_out without q_rope")
-    q, qo = (None, None) if q_rope is None else (q_rope.data_ptr(), q_out.data_ptr())
+    if T == 1:   # (a dimension of one entry may have any stride)
+        c_st = kr_st = q_st = qo_st = 0
     st = _call_on(dev, stream, lib().pkv_latent_append, c_kv.data_ptr(), c_st, k_rope.data_ptr(), kr_st, q, q_st, q_sh,
-                  qo, qo_st, qo_sh, H, positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0],
-                  slot_mapping.data_ptr(), T, cache.data_ptr(), desc)
+                  qo, qo_st, qo_sh, H, positions.data_ptr(), cos_sin.data_ptr(), table[0], slot_mapping.data_ptr(), T,
+                  cache.data_ptr(), desc)
     _check(st, "pkv_latent_append")
     return q_out
 
@@ -612,17 +601,21 @@ def latent_gather(cache, page_tables, cu_seqlens_k, total_k: int, out=None, stre
     import torch
     where = "latent_gather"
     desc = _latent_desc(where, cache)
-    _int32s(where, page_tables, cu_seqlens_k)
+    if page_tables.dtype is not torch.int32 or cu_seqlens_k.dtype is not torch.int32:
+        raise TypeError(f"{where}: index tensors must be int32")
     dev = _on_one_device(where, cache, page_tables, cu_seqlens_k, out)
-    B = cu_seqlens_k.shape[0] - 1
-    if page_tables.dim() != 2 or cu_seqlens_k.dim() != 1 or B < 0 or page_tables.shape[0] < B:
+    tables, cu = page_tables.shape, cu_seqlens_k.shape
+    if len(tables) != 2 or len(cu) != 1 or not 1 <= cu[0] <= tables[0] + 1:
         raise ValueError(f"{where}: page_tables [B, W] and cu_seqlens_k [B + 1] disagree")
+    if not (page_tables.is_contiguous() and cu_seqlens_k.is_contiguous()):
+        raise ValueError(f"{where}: index tensors must be contiguous")
+    total_k, R = int(total_k), desc.latent_dim + LATENT_ROPE
     if out is None:
-        out = _lent(torch.empty((int(total_k), cache.shape[2]), dtype=cache.dtype, device=cache.device), stream)
-    elif out.dtype != cache.dtype or out.shape != (total_k, cache.shape[2]) or not out.is_contiguous():
-        raise ValueError(f"{where}: out must be a contiguous [total_k, {cache.shape[2]}] tensor of the cache's dtype")
-    st = _call_on(dev, stream, lib().pkv_latent_gather, cache.data_ptr(), desc, page_tables.data_ptr(),
-                  page_tables.shape[1], cu_seqlens_k.data_ptr(), B, int(total_k), out.data_ptr())
+        out = _lent(torch.empty((total_k, R), dtype=cache.dtype, device=cache.device), stream)
+    elif out.dtype is not cache.dtype or out.shape != (total_k, R) or not out.is_contiguous():
+        raise ValueError(f"{where}: out must be a contiguous [total_k, {R}] tensor of the cache's dtype")
+    st = _call_on(dev, stream, lib().pkv_latent_gather, cache.data_ptr(), desc, page_tables.data_ptr(), tables[1],
+                  cu_seqlens_k.data_ptr(), cu[0] - 1, total_k, out.data_ptr())
     _check(st, "pkv_latent_gather")
     return out
 
@@ -648,26 +641,39 @@ def latent_attention(q, cu_seqlens_q, kv_lens, page_tables, cache, scale: float,
     q [T, H, latent_dim + 64] (cache dtype), cu_seqlens_q int32 [B + 1], kv_lens
     int32 [B], page_tables int32 [B, W], cache [N, P, latent_dim + 64]. Returns
     (out [T, H, latent_dim], lse [T, H])."""
+    import torch
     where = "latent_attention"
     desc = _latent_desc(where, cache)
-    _int32s(where, cu_seqlens_q, kv_lens, page_tables)
-    dev = _on_one_device(where, q, cu_seqlens_q, kv_lens, page_tables, cache, out, lse, workspace)
-    if q.dtype != cache.dtype:
+    i32, dtype, width = torch.int32, cache.dtype, desc.latent_dim
+    if cu_seqlens_q.dtype is not i32 or kv_lens.dtype is not i32 or page_tables.dtype is not i32:
+        raise TypeError(f"{where}: index tensors must be int32")
+    if q.dtype is not dtype:
         raise TypeError(f"{where}: q and cache must share one dtype")
-    if q.dim() != 3 or q.shape[2] != cache.shape[2] or not q.is_contiguous():
-        raise ValueError(f"{where}: q must be a contiguous [T, H, {cache.shape[2]}] tensor")
-    B = cu_seqlens_q.shape[0] - 1
-    if (cu_seqlens_q.dim() != 1 or kv_lens.dim() != 1 or page_tables.dim() != 2 or B < 0 or kv_lens.shape[0] < B
-            or page_tables.shape[0] < B):
+    dev = _on_one_device(where, q, cu_seqlens_q, kv_lens, page_tables, cache, out, lse, workspace)
+    shape, tables, cu, lens = q.shape, page_tables.shape, cu_seqlens_q.shape, kv_lens.shape
+    if len(shape) != 3 or shape[2] != width + LATENT_ROPE or not q.is_contiguous():
+        raise ValueError(f"{where}: q must be a contiguous [T, H, {width + LATENT_ROPE}] tensor")
+    T, H, _ = shape
+    if len(cu) != 1 or len(lens) != 1 or len(tables) != 2 or not 0 <= cu[0] - 1 <= min(lens[0], tables[0]):
         raise ValueError(f"{where}: cu_seqlens_q [B + 1], kv_lens [B] and page_tables [B, W] disagree")
-    out, lse = _out_and_lse(where, q, desc.latent_dim, out, lse, want_lse, stream)
-    T, H, _ = q.shape
+    if not (cu_seqlens_q.is_contiguous() and kv_lens.is_contiguous() and page_tables.is_contiguous()):
+        raise ValueError(f"{where}: index tensors must be contiguous")
+    B = cu[0] - 1
+    if out is None:
+        out = _lent(torch.empty((T, H, width), dtype=dtype, device=q.device), stream)
+    elif out.dtype is not dtype or out.shape != (T, H, width) or not out.is_contiguous():
+        raise _bad_out(where, width)
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
+            raise _bad_out(where, width)
+    elif want_lse:
+        lse = _lent(torch.empty((T, H), dtype=torch.float32, device=q.device), stream)
     if workspace is None:
         workspace = _lent(alloc_latent_workspace(B, T, H, cache), stream)
     elif not workspace.is_contiguous():
         raise ValueError(f"{where}: workspace must be contiguous")
     st = _call_on(dev, stream, lib().pkv_latent_attention, q.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
-                  page_tables.data_ptr(), B, T, H, page_tables.shape[1], int(max_kv_len), cache.data_ptr(), desc, scale,
+                  page_tables.data_ptr(), B, T, H, tables[1], int(max_kv_len), cache.data_ptr(), desc, scale,
                   out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     _check(st, "pkv_latent_attention")
     return out, lse
@@ -693,30 +699,46 @@ def latent_prefill(q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, scale: floa
     q [Tq, H, 192]; k_nope and v [Tk, H, 128], k_rope [Tk, 64] (strided rows
     allowed: views of the up-projection's output and of the gathered rows);
     cu_seqlens_q, cu_seqlens_k int32 [B + 1]. Returns (out [Tq, H, 128], lse [Tq, H])."""
+    import torch
     where = "latent_prefill"
-    _int32s(where, cu_seqlens_q, cu_seqlens_k)
+    if cu_seqlens_q.dtype is not torch.int32 or cu_seqlens_k.dtype is not torch.int32:
+        raise TypeError(f"{where}: index tensors must be int32")
     dev = _on_one_device(where, q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, out, lse, workspace)
-    if q.dim() != 3 or q.shape[2] != LATENT_NOPE + LATENT_ROPE or not q.is_contiguous():
+    shape, dtype, rope, cu = q.shape, q.dtype, k_rope.shape, cu_seqlens_q.shape
+    if len(shape) != 3 or shape[2] != LATENT_NOPE + LATENT_ROPE or not q.is_contiguous():
         raise ValueError(f"{where}: q must be a contiguous [T, H, {LATENT_NOPE + LATENT_ROPE}] tensor")
-    dtype = q.dtype
-    kn_st, kn_sh, _ = _rows_of(where, "k_nope", k_nope, 3, LATENT_NOPE, dtype)
-    v_st, v_sh, _ = _rows_of(where, "v", v, 3, LATENT_V, dtype)
-    kr_st, _ = _rows_of(where, "k_rope", k_rope, 2, LATENT_ROPE, dtype)
-    Tq, H, _ = q.shape
-    Tk = k_rope.shape[0]
-    if k_nope.shape[:2] != (Tk, H) or v.shape[:2] != (Tk, H):
-        raise ValueError(f"{where}: k_nope, v [Tk, H, 128] and k_rope [Tk, 64] disagree")
-    B = cu_seqlens_q.shape[0] - 1
-    if cu_seqlens_q.dim() != 1 or B < 0 or cu_seqlens_k.shape != cu_seqlens_q.shape:
+    if len(cu) != 1 or cu[0] < 1 or cu_seqlens_k.shape != cu:
         raise ValueError(f"{where}: cu_seqlens_q and cu_seqlens_k must both be [B + 1]")
-    out, lse = _out_and_lse(where, q, LATENT_V, out, lse, want_lse, stream)
+    if not (cu_seqlens_q.is_contiguous() and cu_seqlens_k.is_contiguous()):
+        raise ValueError(f"{where}: index tensors must be contiguous")
+    Tq, H, _ = shape
+    B, Tk = cu[0] - 1, rope[0] if len(rope) == 2 else -1
+    if Tk < 0 or rope[1] != LATENT_ROPE or k_nope.shape != (Tk, H, LATENT_NOPE) or v.shape != (Tk, H, LATENT_V):
+        raise ValueError(f"{where}: k_nope, v [Tk, H, 128] and k_rope [Tk, 64] disagree")
+    if k_nope.dtype is not dtype or v.dtype is not dtype or k_rope.dtype is not dtype:
+        raise ValueError(f"{where}: q, k_nope, v and k_rope must share one dtype")
+    (kn_st, kn_sh, kn_1), (v_st, v_sh, v_1), (kr_st, kr_1) = k_nope.stride(), v.stride(), k_rope.stride()
+    _rows_only(where, kn_1, v_1, kr_1)
+    if Tk == 1:   # (a dimension of one entry may have any stride)
+        kn_st = v_st = kr_st = 0
+    if H == 1:
+        kn_sh = v_sh = 0
+    if out is None:
+        out = _lent(torch.empty((Tq, H, LATENT_V), dtype=dtype, device=q.device), stream)
+    elif out.dtype is not dtype or out.shape != (Tq, H, LATENT_V) or not out.is_contiguous():
+        raise _bad_out(where, LATENT_V)
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (Tq, H) or not lse.is_contiguous():
+            raise _bad_out(where, LATENT_V)
+    elif want_lse:
+        lse = _lent(torch.empty((Tq, H), dtype=torch.float32, device=q.device), stream)
     if workspace is None:
         workspace = _lent(alloc_latent_prefill_workspace(B, q), stream)
     elif not workspace.is_contiguous():
         raise ValueError(f"{where}: workspace must be contiguous")
     st = _call_on(dev, stream, lib().pkv_latent_prefill, q.data_ptr(), cu_seqlens_q.data_ptr(), k_nope.data_ptr(),
                   kn_st, kn_sh, v.data_ptr(), v_st, v_sh, k_rope.data_ptr(), kr_st, cu_seqlens_k.data_ptr(), B, Tq, Tk,
-                  H, _dtype_code(q), scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                  H, _code_of(dtype), scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
                   workspace.data_ptr(), workspace.nbytes)
     _check(st, "pkv_latent_prefill")
     return out, lse
