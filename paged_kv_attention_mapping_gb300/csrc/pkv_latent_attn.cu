@@ -21,7 +21,7 @@
 // keys for S and O into buffers of their own costs 1.89 times and left room for one
 // step in flight only (decode of 128 sequences at 128 heads: 198 us).
 //
-//   warp 0   Q and K producer (TMA; the page table gives the rows of each box)
+//   warp 0   K producer (TMA; the page table gives the rows of each box)
 //   warp 1   issues S (even CTA)
 //   warp 2   reload producer; zeroes the rows behind the sequence's end in the last step
 //   warp 3   issues O (even CTA)
@@ -30,7 +30,7 @@
 //            columns, so four threads have a row and exchange its maximum through
 //            shared memory. P goes to shared memory in the cache type, O is rescaled
 //            in TMEM only when a row's maximum grows by more than 2^8.
-//   warp 12  scheduler: the segments of this pair
+//   warp 12  scheduler: the segments of this pair, and their Q
 //   warps 13-15  where rows come by thread copies instead of TMA (page sizes that
 //            share no factor of 32 with a step): more loaders beside warp 0 and warp 2,
 //            taking groups in turn, since each waits for its own copies
@@ -212,6 +212,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
     fence_mbar_init();
     s_abort = 0;
     sh.plan.run = 0;
+    s_seg[0].valid = 0;
+    s_bad[0] = 0;
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mx);
     tma_prefetch_desc(&m2);
@@ -219,7 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
   if (warp == 1) tmem_alloc_pair(&s_tmem, TMEM_COLS);
   __syncwarp();
   cluster_arrive();     // the peer may use this CTA's barriers once every thread of both is here
-  latent_plan<BM, BN, NTHREADS>(p, pair, pairs, &sh.plan);
+  latent_plan<BM, BN, NTHREADS>(p, pair, pairs, &sh.plan, s_seg);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -249,25 +251,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
 
   bool ok = true;
   if (warp == SCHED) {
-    // ------------------------------------------------------------- scheduler
+    // ---------------------------------------------- scheduler, and producer of Q
+    const uint32_t q_bar = map_to_rank(&bar_q, 0);
+    auto load_q = [&](uint32_t t, int row0) -> bool {
+      // Q replaces the segment before's once its last S is done
+      if (t >= 1 && !wait(&bar_qempty, (t - 1) & 1)) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx_cluster(q_bar, C::Q_BYTES);
+        tma_load_3d_pair(sQ, &mq, q_bar, 0, row0 + (int)rank * HM, 0);
+      }
+      __syncwarp();
+      return true;
+    };
+    if (lane == 0) mbar_arrive(&bar_seg[0]);   // the plan left the first segment there
+    if (s_seg[0].valid) load_q(0, s_seg[0].row0);
     LatentRun<BM, BN> run(p, sh.plan, pair);
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t % NSEG;
       if (t >= NSEG && !(ok = wait(&bar_segempty[e], ((t / NSEG) - 1) & 1))) break;
       const LatentSegment g = run.next(p);
-      if (lane == 0) {
+      if (t > 0 && lane == 0) {
         s_seg[e] = g;
         s_bad[e] = 0;
         mbar_arrive(&bar_seg[e]);
       }
       __syncwarp();
       if (!g.valid) break;
+      if (t > 0) ok = load_q(t, g.row0);
     }
     if (rank == 0 && lane == 0) ((LatentRecord*)(p.ws + Layout::rec))[pair] = run.r;
   } else if (warp == 0 || warp == 2 || (GATHER && warp > SCHED)) {
     // --------------------------------------------------------------- producers
-    // Warp 0 loads Q and this CTA's 64 keys of each step, warp 2 the peer's 64
-    // keys of this CTA's output columns. Lane l takes boxes l and l + 32 of the 64
+    // Warp 0 loads this CTA's 64 keys of each step, warp 2 the peer's 64 keys of this
+    // CTA's output columns. Lane l takes boxes l and l + 32 of the 64
     // keys. Rows behind the end and bad pages are read from page 0 (masked, or
     // discarded), so that a step's bytes are always the same. With thread copies
     // K_LOADERS and V_LOADERS warps share that, a group each in turn.
@@ -275,7 +291,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
     const uint32_t loaders = !GATHER ? 1 : reload ? V_LOADERS : K_LOADERS;
     const uint32_t loader = warp < SM_FIRST ? 0 : reload ? warp - (SCHED + K_LOADERS) + 1 : warp - SCHED;
     const int key_half = (int)rank ^ (reload ? 1 : 0);
-    const uint32_t q_bar = map_to_rank(&bar_q, 0);
     const int boxes = HM / p.box;
     // 0 * NaN must not reach O from the slots behind the end: units 0 and 1 of a
     // group hold keys 0-63 of the step, 2 and 3 keys 64-127
@@ -388,15 +403,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
           __syncwarp();
         }
         if (!ok) break;
-        if ((GATHER ? warp == 0 : !reload) && j == g.j0) {
-          // Q replaces the segment before's once its last S is done; the first keys go ahead
-          if (t >= 1 && !(ok = wait(&bar_qempty, (t - 1) & 1))) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx_cluster(q_bar, C::Q_BYTES);
-            tma_load_3d_pair(sQ, &mq, q_bar, 0, g.row0 + (int)rank * HM, 0);
-          }
-          __syncwarp();
-        }
         if (!GATHER && tail) {
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
@@ -648,7 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
     if (!ok) row_bar_arrive(bar_id);   // lets the other warps of these rows leave their exchange
   }
 
-  if (s_abort && (warp == 0 || warp == 2 || warp > SCHED)) {
+  if (s_abort && (warp == 0 || warp == 2 || warp >= SCHED)) {
     if (GATHER) cp_async_wait_all();
     // copies of this CTA may still be on their way: give them time to land
     const uint64_t t0 = globaltimer_ns();

@@ -141,9 +141,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     fence_mbar_init();
     sh.abort = 0;
     sh.plan.run = 0;
+    sh.seg[0].valid = 0;
+    sh.bad[0] = 0;
     tma_prefetch_desc(&mx);
   }
-  latent_plan<TM, BN, NTHREADS>(p, blockIdx.x, gridDim.x, &sh.plan);
+  latent_plan<TM, BN, NTHREADS>(p, blockIdx.x, gridDim.x, &sh.plan, sh.seg);
   __syncthreads();
   pdl_wait();   // queries, cache rows and page tables may come from the kernel before
   pdl_trigger();
@@ -169,12 +171,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   bool ok = true;
   if (warp == WARPS + 1) {
     // ------------------------------------------------------------- scheduler
+    if (lane == 0) mbar_arrive(&sh.segfull[0]);   // the plan left the first one there
     LatentRun<TM, BN> run(p, sh.plan, blockIdx.x);
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t % NSEG;
       if (t >= NSEG && !(ok = wait(&sh.segempty[e], ((t / NSEG) - 1) & 1))) break;
       const LatentSegment g = run.next(p);
-      if (lane == 0) {
+      if (t > 0 && lane == 0) {
         sh.seg[e] = g;
         sh.bad[e] = 0;
         mbar_arrive(&sh.segfull[e]);
@@ -462,12 +465,14 @@ __global__ void __launch_bounds__(CTHREADS) latent_rows_combine_kernel(char* ws,
   const float4* parts = (const float4*)(ws + Layout::o);
   auto slot = [&](int s) { return s == 0 ? 2 * rec.owner + 1 : 2 * (rec.owner + s); };
   const int tid = threadIdx.x, lane = tid & 31, v = tid % NV, pg = tid / NV;
-  int any = 0;
-  for (int s = tid; s < rec.parts; s += CTHREADS) any |= bad[slot(s)];
-  if (__syncthreads_or(any)) return;
   for (int r = r0; r < rec.nrows; r += CY * (rec.parts - 1)) {
     float m = -INFINITY;
-    for (int s = lane; s < rec.parts; s += 32) m = fmaxf(m, sums[slot(s) * TM + r]);
+    int any = 0;
+    for (int s = lane; s < rec.parts; s += 32) {
+      any |= bad[slot(s)];
+      m = fmaxf(m, sums[slot(s) * TM + r]);
+    }
+    if (__any_sync(0xffffffffu, any)) return;   // (every warp looked at every part)
     m = warp_max(m);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f;

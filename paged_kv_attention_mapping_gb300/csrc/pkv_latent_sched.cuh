@@ -103,6 +103,24 @@ struct LatentSeq {
   }
 };
 
+// The segment of a run with `left` steps to go that begins at step `step` of a tile.
+template <int TM, int BN>
+__device__ __forceinline__ LatentSegment latent_segment(const LatentAttnP& p, const LatentSeq<TM, BN>& s, int b, int tile,
+                                                        int step, int64_t left) {
+  LatentSegment g;
+  g.valid = 1;
+  g.b = b;
+  g.L = s.L;
+  g.base = s.base;
+  g.frow0 = tile * TM;
+  g.row0 = __ldg(p.cu + b) * p.H + tile * TM;
+  g.nrows = min(TM, s.rows - tile * TM);
+  g.n = s.steps(tile);
+  g.j0 = step;
+  g.j1 = (int)min((int64_t)g.n, step + left);
+  return g;
+}
+
 // Where a worker's run starts, in shared memory.
 template <int NTHREADS>
 struct LatentPlan {
@@ -113,10 +131,11 @@ struct LatentPlan {
 
 // By all threads of a CTA: every CTA counts the whole tick's steps and finds where
 // its own run starts. Reads only the lengths, so it may run before the wait for the
-// kernel before. One thread has set pl->run to 0 before; the results are visible
-// after the caller's next block barrier.
+// kernel before. One thread has set pl->run and first->valid to 0 before; the results,
+// the run's first segment among them, are visible after the caller's next block barrier.
 template <int TM, int BN, int NTHREADS>
-__device__ __forceinline__ void latent_plan(const LatentAttnP& p, int worker, int workers, LatentPlan<NTHREADS>* pl) {
+__device__ __forceinline__ void latent_plan(const LatentAttnP& p, int worker, int workers, LatentPlan<NTHREADS>* pl,
+                                            LatentSegment* first) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   bool bad = tid == 0 && __ldg(p.cu) != 0;
   const int per = (p.B + NTHREADS - 1) / NTHREADS;
@@ -161,6 +180,7 @@ __device__ __forceinline__ void latent_plan(const LatentAttnP& p, int worker, in
         pl->tile = tile;
         pl->step = step;
         prefetch_l2(p.page_tables + (int64_t)b * p.max_pages + (int64_t)step * BN / p.P);   // wanted first
+        *first = latent_segment<TM, BN>(p, s, b, tile, step, hi - lo);
         break;
       }
       at -= n;
@@ -197,24 +217,14 @@ struct LatentRun {
   __device__ __forceinline__ LatentSegment next(const LatentAttnP& p) {
     LatentSegment g;
     g.valid = 0;
-    if (left > 0) {
-      // left > 0 promises one more tile, as long as nobody rewrites the lengths meanwhile
-      while (tile >= s.tiles && ++b < p.B) {
-        s.load(p, b, false);
-        tile = 0;
-      }
-      g.valid = tile < s.tiles;
+    if (left <= 0) return g;
+    // left > 0 promises one more tile, as long as nobody rewrites the lengths meanwhile
+    while (tile >= s.tiles && ++b < p.B) {
+      s.load(p, b, false);
+      tile = 0;
     }
-    if (!g.valid) return g;
-    g.b = b;
-    g.L = s.L;
-    g.base = s.base;
-    g.frow0 = tile * TM;
-    g.row0 = __ldg(p.cu + b) * p.H + tile * TM;
-    g.nrows = min(TM, s.rows - tile * TM);
-    g.n = s.steps(tile);
-    g.j0 = step;
-    g.j1 = (int)min((int64_t)g.n, step + left);
+    if (tile >= s.tiles) return g;
+    g = latent_segment<TM, BN>(p, s, b, tile, step, left);
     if (g.j1 < g.n) {
       // the tile's first step among the tick's (this run starts at worker * each)
       const int64_t begin = worker * each + done - g.j0;
