@@ -35,8 +35,8 @@
 //            share no factor of 32 with a step): more loaders beside warp 0 and warp 2,
 //            taking groups in turn, since each waits for its own copies
 //
-// Work split: the tick's steps (all tiles, one after the other) are cut into
-// equal runs, one per pair. A tile cut by a run's end leaves partial results
+// Work split: the tick's steps (all tiles, one after the other, each with START more for its
+// start and end) are cut into equal runs, one per pair. A tile cut by a run's end leaves partial results
 // (normalised output in fp32 and log2 sum) that latent_combine_kernel joins.
 //
 // Decode of 128 sequences of 512-8192 keys at 128 heads (bf16): 142 us, 4.7 TB/s and 1.09
@@ -65,6 +65,10 @@ namespace {
 constexpr int BM = 128;          // (token, head) rows of a tile
 constexpr int HM = 64;           // rows of one CTA
 constexpr int BN = 128;          // keys of a step
+// What a tile counts beside its steps in the split. 40 sequences of up to 3000 keys, 1-5
+// tokens, 20 heads, latent 256 with 0 / 1 / 2 / 4 / 6: 24.4 / 22.4 / 22.4 / 22.9 / 24.0 us; decode of 128
+// sequences at 128 heads: 145.8 / 145.3 / 146.8 / 148.5 / 151.
+constexpr int START = 1;
 constexpr int MAX_PAIRS = 76;    // 152 SMs; the workspace is laid out for these
 constexpr int SM_WARPS = 8;         // softmax warps of a CTA
 constexpr int SM_FIRST = 4;         // the first of them: its TMEM lanes are those of warp & 3
@@ -221,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
   if (warp == 1) tmem_alloc_pair(&s_tmem, TMEM_COLS);
   __syncwarp();
   cluster_arrive();     // the peer may use this CTA's barriers once every thread of both is here
-  latent_plan<BM, BN, NTHREADS>(p, pair, pairs, &sh.plan, s_seg);
+  latent_plan<BM, BN, START, NTHREADS>(p, pair, pairs, &sh.plan, s_seg);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -265,7 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
     };
     if (lane == 0) mbar_arrive(&bar_seg[0]);   // the plan left the first segment there
     if (s_seg[0].valid) load_q(0, s_seg[0].row0);
-    LatentRun<BM, BN> run(p, sh.plan, pair);
+    LatentRun<BM, BN, START> run(p, sh.plan, pair);
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t % NSEG;
       if (t >= NSEG && !(ok = wait(&bar_segempty[e], ((t / NSEG) - 1) & 1))) break;

@@ -42,8 +42,11 @@ struct LatentRecord {
 };
 
 // One sequence's tiles. Tile t covers rows [TM t, TM t + TM) of its q_len * H
-// and needs the keys up to its last row's position, BN of them a step.
-template <int TM, int BN>
+// and needs the keys up to its last row's position, BN of them a step. In the split
+// a tile counts START units, for its queries' loading and its results' storing, then one
+// a step: workers with many short tiles get fewer steps. A place in a tile is an
+// offset in units; one in the first START of them stands before its first step.
+template <int TM, int BN, int START>
 struct LatentSeq {
   int q, L, base, H, rows, tiles;
   __device__ __forceinline__ int steps(int t) const {
@@ -59,27 +62,27 @@ struct LatentSeq {
   }
   __device__ __forceinline__ int64_t total() const {
     if (tiles == 0) return 0;
-    if (tiles == 1) return (L + BN - 1) / BN;
+    if (tiles == 1) return (L + BN - 1) / BN + START;
     const int lo = steps(0), hi = steps(tiles - 1);
-    int64_t s = (int64_t)hi * tiles;
+    int64_t s = (int64_t)(hi + START) * tiles;
     for (int v = lo; v < hi; ++v) s -= tiles_within(v);
     return s;
   }
-  // tile and step of the sequence's step number `at`
-  __device__ __forceinline__ void seek(int64_t at, int* tile, int* step) const {
+  // tile, and offset in it, of the sequence's unit number `at`
+  __device__ __forceinline__ void seek(int64_t at, int* tile, int* off) const {
     if (tiles == 1) {
       *tile = 0;
-      *step = (int)at;
+      *off = (int)at;
       return;
     }
     const int lo = steps(0), hi = steps(tiles - 1);
     int before = 0;
     for (int v = lo; v <= hi; ++v) {
       const int upto = v == hi ? tiles : tiles_within(v);
-      const int64_t s = (int64_t)(upto - before) * v;
+      const int64_t s = (int64_t)(upto - before) * (v + START);
       if (at < s) {
-        *tile = before + (int)(at / v);
-        *step = (int)(at % v);
+        *tile = before + (int)(at / (v + START));
+        *off = (int)(at % (v + START));
         return;
       }
       at -= s;
@@ -103,12 +106,12 @@ struct LatentSeq {
   }
 };
 
-// The segment of a run with `left` steps to go that begins at step `step` of a tile.
-template <int TM, int BN>
-__device__ __forceinline__ LatentSegment latent_segment(const LatentAttnP& p, const LatentSeq<TM, BN>& s, int b, int tile,
-                                                        int step, int64_t left) {
+// The segment of a run with `left` units to go that begins at offset `off` of a tile; not
+// valid if the run ends before the tile's first step (then the run has no more segments).
+template <int TM, int BN, int START>
+__device__ __forceinline__ LatentSegment latent_segment(const LatentAttnP& p, const LatentSeq<TM, BN, START>& s, int b,
+                                                        int tile, int off, int64_t left) {
   LatentSegment g;
-  g.valid = 1;
   g.b = b;
   g.L = s.L;
   g.base = s.base;
@@ -116,8 +119,9 @@ __device__ __forceinline__ LatentSegment latent_segment(const LatentAttnP& p, co
   g.row0 = __ldg(p.cu + b) * p.H + tile * TM;
   g.nrows = min(TM, s.rows - tile * TM);
   g.n = s.steps(tile);
-  g.j0 = step;
-  g.j1 = (int)min((int64_t)g.n, step + left);
+  g.j0 = max(0, off - START);
+  g.j1 = (int)min((int64_t)g.n, off - START + left);
+  g.valid = g.j0 < g.j1;
   return g;
 }
 
@@ -125,15 +129,15 @@ __device__ __forceinline__ LatentSegment latent_segment(const LatentAttnP& p, co
 template <int NTHREADS>
 struct LatentPlan {
   int64_t scan[NTHREADS / 32];
-  int64_t run, each;   // steps of this worker's run, and of every worker's but the last
-  int b, tile, step;
+  int64_t run, each;   // units of this worker's run, and of every worker's but the last
+  int b, tile, off;
 };
 
-// By all threads of a CTA: every CTA counts the whole tick's steps and finds where
+// By all threads of a CTA: every CTA counts the whole tick's units and finds where
 // its own run starts. Reads only the lengths, so it may run before the wait for the
 // kernel before. One thread has set pl->run and first->valid to 0 before; the results,
 // the run's first segment among them, are visible after the caller's next block barrier.
-template <int TM, int BN, int NTHREADS>
+template <int TM, int BN, int START, int NTHREADS>
 __device__ __forceinline__ void latent_plan(const LatentAttnP& p, int worker, int workers, LatentPlan<NTHREADS>* pl,
                                             LatentSegment* first) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -141,7 +145,7 @@ __device__ __forceinline__ void latent_plan(const LatentAttnP& p, int worker, in
   const int per = (p.B + NTHREADS - 1) / NTHREADS;
   const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
   int64_t mine = 0;
-  LatentSeq<TM, BN> s;
+  LatentSeq<TM, BN, START> s;
   for (int b = b_lo; b < b_hi; ++b) {
     s.load(p, b, blockIdx.x == 0);
     bad |= s.q < 0;
@@ -174,13 +178,14 @@ __device__ __forceinline__ void latent_plan(const LatentAttnP& p, int worker, in
       s.load(p, b, false);
       const int64_t n = s.total();
       if (at < n) {
-        int tile, step;
-        s.seek(at, &tile, &step);
+        int tile, off;
+        s.seek(at, &tile, &off);
         pl->b = b;
         pl->tile = tile;
-        pl->step = step;
-        prefetch_l2(p.page_tables + (int64_t)b * p.max_pages + (int64_t)step * BN / p.P);   // wanted first
-        *first = latent_segment<TM, BN>(p, s, b, tile, step, hi - lo);
+        pl->off = off;
+        const LatentSegment g = latent_segment(p, s, b, tile, off, hi - lo);
+        prefetch_l2(p.page_tables + (int64_t)b * p.max_pages + (int64_t)g.j0 * BN / p.P);   // wanted first
+        *first = g;
         break;
       }
       at -= n;
@@ -192,11 +197,11 @@ __device__ __forceinline__ void latent_plan(const LatentAttnP& p, int worker, in
 
 // A worker's segments, one after the other, and the record of the tile that its
 // run cuts at the end.
-template <int TM, int BN>
+template <int TM, int BN, int START>
 struct LatentRun {
   int64_t left, done, each;
-  int worker, b, tile, step;
-  LatentSeq<TM, BN> s;
+  int worker, b, tile, off;
+  LatentSeq<TM, BN, START> s;
   LatentRecord r;
   template <int NTHREADS>
   __device__ __forceinline__ LatentRun(const LatentAttnP& p, const LatentPlan<NTHREADS>& pl, int w) {
@@ -204,13 +209,13 @@ struct LatentRun {
     done = 0;
     each = pl.each;
     worker = w;
-    b = tile = step = 0;
+    b = tile = off = 0;
     s.tiles = 0;
     r = LatentRecord{0, 0, 0, 0};
     if (left > 0) {
       b = pl.b;
       tile = pl.tile;
-      step = pl.step;
+      off = pl.off;
       s.load(p, b, false);
     }
   }
@@ -224,19 +229,21 @@ struct LatentRun {
       tile = 0;
     }
     if (tile >= s.tiles) return g;
-    g = latent_segment<TM, BN>(p, s, b, tile, step, left);
+    g = latent_segment(p, s, b, tile, off, left);
+    if (!g.valid) return g;
     if (g.j1 < g.n) {
-      // the tile's first step among the tick's (this run starts at worker * each)
-      const int64_t begin = worker * each + done - g.j0;
+      // the tile's first step among the tick's units (this run starts at worker * each)
+      const int64_t begin = worker * each + done - off + START;
       r.owner = (int)(begin / each);
       r.parts = (int)((begin + g.n - 1) / each) - r.owner + 1;
       r.row0 = g.row0;
       r.nrows = g.nrows;
     }
-    left -= g.j1 - g.j0;
-    done += g.j1 - g.j0;
+    const int used = g.j1 + START - off;
+    left -= used;
+    done += used;
     ++tile;
-    step = 0;
+    off = 0;
     return g;
   }
 };
