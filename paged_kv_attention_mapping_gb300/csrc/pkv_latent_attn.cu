@@ -39,8 +39,8 @@
 // start and end) are cut into equal runs, one per pair. A tile cut by a run's end leaves partial results
 // (normalised output in fp32 and log2 sum) that latent_combine_kernel joins.
 //
-// Decode of 128 sequences of 512-8192 keys at 128 heads (bf16): 142 us, 4.7 TB/s and 1.09
-// PFLOP/s, tensor pipe 45 % busy; with the combine 149 us. A step takes about 3800
+// Decode of 128 sequences of 512-8192 keys at 128 heads (bf16): 139 us, 4.8 TB/s and 1.11
+// PFLOP/s, tensor pipe 45 % busy; with the combine 146 us. A step takes about 3800
 // cycles, of which the tensor pipe needs 2200 and HBM 3200 at its measured rate: two step
 // slots fit beside Q, and a slot's turn (load 2700 cycles, S, softmax 1400, O, the
 // hand-offs between them) takes two steps' time. Tried and no faster: keys prefetched into
@@ -827,8 +827,9 @@ cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t s) {
   // Up to 16 rows a sequence on average go 16 to a tile on mma.sync, which HBM
   // bounds; with more of them the tensor cores' tiles of 128 rows read the keys
   // less often (rows of one sequence share a pass over its keys). Decode of 96 sequences
-  // of 1000-8000 keys, latent 512, mma.sync against tcgen05: 8 heads 90 / 106 us,
-  // 16 heads 96 / 108, 20 heads 156 / 110, 64 heads 302 / 119.
+  // of 1000-8000 keys, latent 512, mma.sync against tcgen05: 8 heads 88 / 105 us,
+  // 16 heads 94 / 106, 20 heads 153 / 107, 64 heads 292 / 115; of 4 sequences of up to
+  // 500 keys: 16 heads 11.7 / 12.0, 32 heads 12.7 / 12.5.
   const bool rows = (int64_t)a.T * a.H <= (int64_t)16 * a.B;
   LatentAttnP p;
   p.cu = a.cu;

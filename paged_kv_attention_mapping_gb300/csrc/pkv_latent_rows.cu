@@ -468,7 +468,23 @@ __global__ void __launch_bounds__(CTHREADS) latent_rows_combine_kernel(char* ws,
   const float4* parts = (const float4*)(ws + Layout::o);
   auto slot = [&](int s) { return s == 0 ? 2 * rec.owner + 1 : 2 * (rec.owner + s); };
   const int tid = threadIdx.x, lane = tid & 31, v = tid % NV, pg = tid / NV;
+  constexpr int U = 4;   // parts in flight a thread
   for (int r = r0; r < rec.nrows; r += CY * (rec.parts - 1)) {
+    float w[U];
+    float4 y[U];
+    auto load = [&](int s0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int s = s0 + u * PG;
+        w[u] = -INFINITY;
+        y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s < rec.parts) {
+          w[u] = sums[slot(s) * TM + r];
+          y[u] = parts[((int64_t)slot(s) * TM + r) * NV + v];
+        }
+      }
+    };
+    load(pg);   // under way while the maximum is found
     float m = -INFINITY;
     int any = 0;
     for (int s = lane; s < rec.parts; s += 32) {
@@ -479,15 +495,17 @@ __global__ void __launch_bounds__(CTHREADS) latent_rows_combine_kernel(char* ws,
     m = warp_max(m);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f;
-#pragma unroll 4
-    for (int s = pg; s < rec.parts; s += PG) {
-      const float w = exp2f(sums[slot(s) * TM + r] - m);
-      const float4 y = parts[((int64_t)slot(s) * TM + r) * NV + v];
-      total += w;
-      o.x += w * y.x;
-      o.y += w * y.y;
-      o.z += w * y.z;
-      o.w += w * y.w;
+    for (int s = pg; s < rec.parts;) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float f = exp2f(w[u] - m);
+        total += f;
+        o.x += f * y[u].x;
+        o.y += f * y[u].y;
+        o.z += f * y[u].z;
+        o.w += f * y[u].w;
+      }
+      if ((s += U * PG) < rec.parts) load(s);
     }
     s_o[pg][v] = o;
     if (v == 0) s_t[pg] = total;
