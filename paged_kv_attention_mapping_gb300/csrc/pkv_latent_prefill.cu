@@ -31,6 +31,9 @@
 // Where the tiles are at most half as many as the pairs of CTAs (short chunks, few
 // heads), each tile's keys are cut into parts, as many as there are pairs for; latent_prefill_combine_kernel joins their partial results.
 //
+// A plan kernel counts the tiles; where the call's sizes allow no more of them than pairs
+// of CTAs, each pair finds its own.
+//
 // Tiles go head by head, each head's from its last rows (most keys) to its first:
 // the CTAs that run at one time share few heads' keys, which stay in L2, and the
 // last tiles to be claimed are short. Longer sequences come before shorter ones.
@@ -98,7 +101,8 @@ Layout layout(int32_t B, int32_t Tq, int32_t H) {
 
 struct PrefillP {
   const int32_t *cu_q, *cu_k;
-  int32_t B, H;
+  int32_t B, H, Tq, Tk;
+  int32_t direct;              // no plan: every pair of CTAs finds its one tile itself
   int32_t kn_heads, v_heads;   // 0: every head reads head 0 (a head stride of 0)
   float scale_log2;            // > 0
   void* out;
@@ -123,6 +127,16 @@ __device__ __forceinline__ int wide_tiles(int q) { return q / ROWS + (q % ROWS >
 __device__ __forceinline__ int parts_of(int L, int most) {
   const int n = (L + BN - 1) / BN, parts = max(1, min(most, n / MIN_STEPS));
   return n - (n + parts - 1) / parts >= MIN_SAVED ? parts : 1;
+}
+
+// Work items of a sequence of q rows and L keys: its tiles' parts.
+__device__ __forceinline__ int items_of(int q, int L, int H, int parts) {
+  return (wide_tiles(q) * H + (narrow_rows(q) ? (H + 1) / 2 : 0)) * parts_of(L, parts);
+}
+// The tiles of a call whose lengths are not known: a tile of one head has more than QM
+// rows of it, and no sequence has tiles of two heads more than once.
+int64_t most_tiles(int32_t B, int32_t Tq, int32_t H) {
+  return (int64_t)(Tq / (QM + 1)) * H + (int64_t)(B < Tq ? B : Tq) * ((H + 1) / 2);
 }
 
 // One CTA: checks the lengths, orders the sequences by keys (descending, up to
@@ -155,7 +169,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
       atomicOr(dev_status, PKV_DEV_BAD_LENGTHS);
       return 0;
     }
-    return (wide_tiles(q) * H + (narrow_rows(q) ? (H + 1) / 2 : 0)) * parts_of(L, parts);
+    return items_of(q, L, H, parts);
   };
   if (split) {
     __syncthreads();
@@ -232,6 +246,52 @@ static_assert(sizeof(Tile) <= 128, "record");
 // First step of a part of n steps (fewer than 2^24 steps and 2^7 parts).
 __device__ __forceinline__ int part_begin(int n, int part, int parts) { return n * part / parts; }
 
+// By a warp: what the plan kernel finds out, for calls of no more items than pairs of CTAs
+// (no more sequences either): the number of items, the largest number of parts, and the
+// sequence of item `item` with the number of items before it.
+struct Found {
+  int items, parts, b, before;
+};
+__device__ __forceinline__ Found find_item(const PrefillP& p, int item, int pairs) {
+  const int lane = threadIdx.x & 31;
+  bool bad = lane == 0 && (__ldg(p.cu_q) != 0 || __ldg(p.cu_k) != 0 || __ldg(p.cu_q + p.B) > p.Tq ||
+                           __ldg(p.cu_k + p.B) > p.Tk);
+  for (int b = lane; b < p.B; b += 32)
+    bad |= __ldg(p.cu_q + b + 1) < __ldg(p.cu_q + b) || __ldg(p.cu_k + b + 1) < __ldg(p.cu_k + b);
+  bad = __any_sync(0xffffffffu, bad);
+  Found f{0, 1, 0, 0};
+  auto items = [&](int b) {
+    if (bad || b >= p.B) return 0;
+    const int q = __ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b), L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
+    if (q > 0 && L < q && item == 0) atomicOr(p.dev_status, PKV_DEV_BAD_LENGTHS);
+    return q == 0 || L < q ? 0 : items_of(q, L, p.H, f.parts);
+  };
+  if (bad && item == 0 && lane == 0) atomicOr(p.dev_status, PKV_DEV_BAD_LENGTHS);
+  if (p.rec) {
+    int all = 0;
+    for (int b = lane; b < p.B; b += 32) all += items(b);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if (all > 0) f.parts = max(1, pairs / all);
+  }
+  for (int base = 0; base < p.B; base += 32) {
+    const int n = items(base + lane);
+    int scan = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += y;
+    }
+    const int before = f.items + scan - n;
+    const unsigned here = __ballot_sync(0xffffffffu, before <= item && item < before + n);
+    if (here) {
+      f.b = base + __ffs(here) - 1;
+      f.before = __shfl_sync(0xffffffffu, before, __ffs(here) - 1);
+    }
+    f.items += __shfl_sync(0xffffffffu, scan, 31);
+  }
+  return f;
+}
+
 // Partial outputs: for a part and 128 rows (a CTA's of a query tile), four columns
 // at a time, the rows side by side. The vector of row r (of ROWS) and columns 4 c ..
 __device__ __forceinline__ int64_t part_vec(int item, int r, int c) {
@@ -290,6 +350,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     tma_prefetch_desc(&mr);
   }
   if (warp == 1) tmem_alloc_pair(&s_tmem, TMEM_COLS);
+  Found found{0, 1, 0, 0};
+  // (reads only the lengths, which the kernel before does not write)
+  if (p.direct && rank == 0 && warp == 0) found = find_item(p, blockIdx.x >> 1, gridDim.x >> 1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -325,7 +388,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 
   if (warp == 0) {
     // --------------------------------------------------------------- producer
-    const int n_tiles = *(volatile const int32_t*)&p.ctrl[1], most_parts = *(volatile const int32_t*)&p.ctrl[2];
+    const int n_tiles = p.direct ? found.items : *(volatile const int32_t*)&p.ctrl[1];
+    const int most_parts = p.direct ? found.parts : *(volatile const int32_t*)&p.ctrl[2];
+    if (p.direct && p.rec && blockIdx.x == 0 && lane == 0) {   // for the join
+      p.ctrl[1] = n_tiles;
+      p.ctrl[2] = most_parts;
+    }
     const uint32_t q_bar = map_to_rank(&bar_q, 0);
     uint32_t n_claims = 0;
     uint32_t n_k = 0, n_v = 0, n_tail = 0;    // K, V loads and last tiles with rows to zero so far
@@ -336,11 +404,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         if (t >= 2 && !(ok = wait(&bar_tempty[e], ((t >> 1) - 1) & 1))) break;
         Tile ti{};
         for (bool skip = true; skip;) {
-          int tt = n_claims++ == 0 ? (int)(blockIdx.x >> 1) : lane == 0 ? atomicAdd(&p.ctrl[0], 1) : 0;
+          int tt = n_claims++ == 0 ? (int)(blockIdx.x >> 1) : p.direct ? n_tiles : lane == 0 ? atomicAdd(&p.ctrl[0], 1) : 0;
           tt = __shfl_sync(0xffffffffu, tt, 0);
           if (__any_sync(0xffffffffu, s_abort)) tt = n_tiles;
           int lo = 0;   // the last sequence that starts at or before tile tt, searched 32 ways
-          for (int m = p.B; m > 1;) {
+          for (int m = p.direct || tt >= n_tiles ? 0 : p.B; m > 1;) {
             const int step = (m + 31) / 32, at = lo + lane * step;
             const bool before = lane * step < m && p.first[at] <= tt;
             lo += (__popc(__ballot_sync(0xffffffffu, before)) - 1) * step;
@@ -348,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           skip = false;
           if (tt < n_tiles) {
-            const int b = p.order[lo], before = p.first[lo];
+            const int b = p.direct ? found.b : p.order[lo], before = p.direct ? found.before : p.first[lo];
             const int q_lo = __ldg(p.cu_q + b), q = __ldg(p.cu_q + b + 1) - q_lo;
             ti.k0 = __ldg(p.cu_k + b);
             ti.L = __ldg(p.cu_k + b + 1) - ti.k0;
@@ -774,6 +842,10 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
   p.cu_k = a.cu_k;
   p.B = a.B;
   p.H = a.H;
+  p.Tq = a.Tq;
+  p.Tk = a.Tk;
+  // (3 prompts of 20-300 tokens at 16 heads: 14.0 us, with the plan kernel 15.2)
+  p.direct = a.B <= pairs && most_tiles(a.B, a.Tq, a.H) <= pairs;
   // a stride that no index uses (one head, one row) or 0 (one head for all) is not a
   // stride for the tensor map: such a dimension has one entry there
   p.kn_heads = a.H > 1 && a.kn_sh > 0;
@@ -797,8 +869,8 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
                         BN) ||
       !make_map_rows(&mr, a.kr, dt, 64, a.Tk, row_stride(a.kr_st), BN / 2))
     return cudaErrorInvalidValue;
-  cudaError_t e;
-  {
+  cudaError_t e = cudaSuccess;
+  if (!p.direct) {
     KernelTimer timer("latent_prefill_plan", s);
     e = launch_after_trigger(latent_prefill_plan_kernel, dim3(1),
                              dim3(a.B < PLAN_THREADS ? (a.B + 31) / 32 * 32 : PLAN_THREADS), 0, s, a.cu_q, a.cu_k, a.B, a.Tq,

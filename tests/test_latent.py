@@ -766,6 +766,36 @@ def test_graphs_replay_with_new_lengths_and_side_by_side(dev):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads,q_lens,kv_lens", [(4, [20, 0, 300, 1], [20, 7, 300, 90]), (3, [257], [5000]),
+                                                  (16, [70, 5], [4000, 6000]), (2, [513, 40], [513, 2600])])
+def test_expanded_calls_with_and_without_a_plan_agree(dev, heads, q_lens, kv_lens):
+    """Small calls find their tiles by themselves; a call with more sequences than the GPU
+    has pairs of CTAs takes the planning kernel. Same tiles, same bits; bad lengths are
+    skipped by both."""
+    t = Packed(dev, "bf16", heads, q_lens, kv_lens)
+    few, few_lse = t.call()
+    t.check(few, few_lse)
+    t.cu_q = np.concatenate([t.cu_q, np.full(80, t.cu_q[-1], np.int32)])
+    t.cu_k = np.concatenate([t.cu_k, np.full(80, t.cu_k[-1], np.int32)])
+    many, many_lse = t.call()
+    assert binding.device_status() == 0
+    assert torch.equal(few, many) and torch.equal(few_lse, many_lse)
+    good_k = t.cu_k
+    for empties in (80, 0):
+        t.cu_q, t.cu_k = t.cu_q[:len(q_lens) + 1 + empties], good_k[:len(q_lens) + 1 + empties].copy()
+        t.cu_k[1] = q_lens[0] - 1            # fewer keys than rows: its rows are skipped
+        out = torch.full_like(few, 9.0)
+        t.call(out=out)
+        assert binding.device_status() == binding.DEV_BAD_LENGTHS
+        assert (out[:q_lens[0]] == 9).all() and torch.isfinite(out).all() and (out[q_lens[0]:] != 9).any(-1).all()
+        t.cu_k[-1] = t.Tk + 1                # ends behind the keys: every row is skipped
+        out.fill_(9.0)
+        t.call(out=out)
+        assert binding.device_status() == binding.DEV_BAD_LENGTHS
+        assert (out == 9).all()
+
+
+@pytest.mark.gpu
 def test_eager_calls_on_two_streams_at_once(dev):
     ticks = [Paged(dev, "bf16", 512, 16, 64, [1, 1], [3000, 20], seed=1),
              Paged(dev, "f16", 512, 64, 16, [1, 2], [700, 2500], seed=2)]
