@@ -18,6 +18,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
+// A whole 32-byte sector (p 32-byte aligned).
+__device__ __forceinline__ void st_global_32B(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // Two fp32 values rounded to the 16-bit type T, the first in the low half.
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {

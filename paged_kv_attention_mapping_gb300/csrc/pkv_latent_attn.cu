@@ -118,12 +118,6 @@ struct Layout {
 };
 static_assert(sizeof(LatentRecord) * MAX_PAIRS <= 2048 && 2 * MAX_PAIRS * 4 <= 2048 && Layout::o % 256 == 0, "layout");
 
-__device__ __forceinline__ void st_global_32B(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 __device__ __forceinline__ void row_bar_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void row_bar_arrive(int id) { asm volatile("bar.arrive %0, 128;" ::"r"(id) : "memory"); }
 

@@ -12,8 +12,8 @@
 // The two tiles are 512 rows of one head, which share every key tile, or, for a
 // sequence's 256 rows or fewer that do not fill such a tile, the same rows of two heads.
 // (One CTA with two tiles of 128 rows needs twice the shared memory for a step's
-// keys: beside Q it held 1.6 steps, waited for loads, and took 499 us instead of
-// 450 for 4096 tokens at 128 heads in bf16: 1526 TFLOP/s.)
+// keys: beside Q it held 1.6 steps, waited for loads, and took 499 us for 4096 tokens at
+// 128 heads in bf16, this one 444: 1546 TFLOP/s.)
 //
 //   warp 0     TMA producer (each CTA its halves): Q of both tiles, K_j (nope part
 //              and rotary part) and V_j into rings of three; V rows behind the
@@ -102,6 +102,7 @@ Layout layout(int32_t B, int32_t Tq, int32_t H) {
 struct PrefillP {
   const int32_t *cu_q, *cu_k;
   int32_t B, H, Tq, Tk;
+  int32_t out_32;              // out is 32-byte aligned
   int32_t direct;              // no plan: every pair of CTAs finds its one tile itself
   int32_t kn_heads, v_heads;   // 0: every head reads head 0 (a head stride of 0)
   float scale_log2;            // > 0
@@ -749,13 +750,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                                                    __uint_as_float(o[4 * v + 3]) * inv);
             continue;
           }
+          uint32_t y[16];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t y[4];
+          for (int k = 0; k < 16; ++k)
+            y[k] = pack2<T>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+          if (p.out_32) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              y[k] = pack2<T>(__uint_as_float(o[v * 8 + 2 * k]) * inv, __uint_as_float(o[v * 8 + 2 * k + 1]) * inv);
-            *reinterpret_cast<uint4*>(dst + c * 32 + v * 8) = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int v = 0; v < 2; ++v) st_global_32B(dst + c * 32 + v * 16, y + v * 8);
+          } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              *reinterpret_cast<uint4*>(dst + c * 32 + v * 8) =
+                  make_uint4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
           }
         }
         const float lg = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);   // (NaN scores: m may be -inf, l_run is NaN)
@@ -852,6 +858,7 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
   p.v_heads = a.H > 1 && a.v_sh > 0;
   p.scale_log2 = a.scale * LOG2E;
   p.out = a.out;
+  p.out_32 = ((uintptr_t)a.out & 31) == 0;
   p.lse = a.lse;
   p.ctrl = (int32_t*)a.ws;
   p.order = (int32_t*)(a.ws + lay.order);

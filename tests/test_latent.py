@@ -766,6 +766,20 @@ def test_graphs_replay_with_new_lengths_and_side_by_side(dev):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads", [40, 4])
+def test_outputs_aligned_to_sixteen_bytes_only(dev, heads):
+    def shifted(like):
+        flat = torch.full((like.numel() + 8,), 9.0, dtype=like.dtype, device=dev)
+        return flat, flat[8:].view(like.shape)
+    for t in (Paged(dev, "bf16", 512, heads, 64, [1, 2], [300, 70]), Packed(dev, "bf16", heads, [300, 40], [400, 40])):
+        good, good_lse = t.call()
+        flat, out = shifted(good)
+        assert out.data_ptr() % 32 == 16
+        _, lse = t.call(out=out)
+        assert torch.equal(out, good) and torch.equal(lse, good_lse) and (flat[:8] == 9).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("heads,q_lens,kv_lens", [(4, [20, 0, 300, 1], [20, 7, 300, 90]), (3, [257], [5000]),
                                                   (16, [70, 5], [4000, 6000]), (2, [513, 40], [513, 2600])])
 def test_expanded_calls_with_and_without_a_plan_agree(dev, heads, q_lens, kv_lens):
