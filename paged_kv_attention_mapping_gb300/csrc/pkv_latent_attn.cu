@@ -39,13 +39,15 @@
 // start and end) are cut into equal runs, one per pair. A tile cut by a run's end leaves partial results
 // (normalised output in fp32 and log2 sum) that latent_combine_kernel joins.
 //
-// Decode of 128 sequences of 512-8192 keys at 128 heads (bf16): 139 us, 4.8 TB/s and 1.11
-// PFLOP/s, tensor pipe 45 % busy; with the combine 146 us. A step takes about 3800
-// cycles, of which the tensor pipe needs 2200 and HBM 3200 at its measured rate: two step
-// slots fit beside Q, and a slot's turn (load 2700 cycles, S, softmax 1400, O, the
-// hand-offs between them) takes two steps' time. Tried and no faster: keys prefetched into
-// L2 one to six steps ahead, by TMA or by loads (load 500 cycles, but 5-10 % slower in
-// all), other L2 promotions, rotary columns in a unit of their own.
+// Decode of 128 sequences of 512-8192 keys at 128 heads (bf16): 131 us, 5.1 TB/s and 1.18
+// PFLOP/s; with the combine 138 us. Two step slots fit beside Q, and a slot's turn (load,
+// S, softmax 1300 cycles, O, the hand-offs between them) takes two steps' time. HBM is
+// busy only while loads are under way, so the next step's rows are sent for into L2
+// behind each step's loads (without: 146 us; earlier by half a step 138, by one step 138 or 144, by two
+// steps 144 or 156: what is sent for too early holds up the loads before it; half of the rows 146). With
+// all pages in L2 it takes 115. Weights without exponentials and rows without an exchange
+// of maxima: 1 % faster, so the softmax is not what bounds it. Other L2 promotions,
+// rotary columns in a unit of their own: no faster.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -330,6 +332,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
         unsigned char* stage = sK + st * C::ST_BYTES;
         const int end = g.L - j * BN;        // rows from here on are behind the sequence
         const bool tail = reload && end < BN;
+        // the next step's rows go into L2 while its slot is still taken
+        const bool ahead = !reload && n + 1 >= NST && j + 1 < g.j1;
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
           // units that this warp fills, and their columns
@@ -352,6 +356,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
               for (int u = 0; u < 4; ++u)
                 if (u < nu) cp_async_16(dst + u * UNIT, src + C::chunk(k, c0 + u) * 128);
               if (rot) cp_async_16(smem_u32(sX) + (1 + st) * UNIT + at, src + LD * 2);
+            }
+            if (ahead) {
+              // a lane per row and chunk
+              const int chunk = (lane & 2 ? C::chunk(k, 2) : C::chunk(k, 0)) + (lane & 1);
+#pragma unroll
+              for (int y = 0; y < HM / 8; ++y) {
+                const int from = __shfl_sync(0xffffffffu, y < HM / 16 ? row[0] : row[1], (y * 8 + (lane >> 2)) & 31);
+                prefetch_l2((const char*)p.cache + (int64_t)from * ((LD + 64) * 2) + chunk * 128);
+              }
+              if (rot) {
+                prefetch_l2((const char*)p.cache + (int64_t)row[0] * ((LD + 64) * 2) + LD * 2);
+                prefetch_l2((const char*)p.cache + (int64_t)row[1] * ((LD + 64) * 2) + LD * 2);
+              }
             }
             cp_async_wait_all();
             if (tail) zero_rows(stage + k * C::G_BYTES, end);
@@ -401,6 +418,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
           __syncwarp();
         }
         if (!ok) break;
+        if (!GATHER && ahead) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            if (lane + w * 32 < boxes)
+              prefetch_l2_bulk((const char*)p.cache + (int64_t)row[w] * ((LD + 64) * 2), p.box * (LD + 64) * 2);
+        }
         if (!GATHER && tail) {
 #pragma unroll
           for (int k = 0; k < NG; ++k) {
