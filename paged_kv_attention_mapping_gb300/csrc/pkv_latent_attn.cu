@@ -859,7 +859,8 @@ cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t s) {
 // Rows of a TMA box: they lie in one page and in one slot.
   p.box = gcd(a.P, rows ? latent_rows_slot() : HM);
   // Boxes of fewer than 32 rows lose to thread copies: 64 sequences of 1000-4000 keys at 128
-  // heads, TMA against copies: page size 32 69 / 70 us, 16 74 / 71, 8 92 / 70, 1 352 / 72.
+  // heads, TMA against copies: page size 64 58.5 / 61.8 us, 32 61.9 / 61.8, 16 67.9 / 61.6 (8 and 1,
+  // before other changes: 92 / 70 and 352 / 72); the 16-row kernel takes one box a slot.
   p.gather = p.box < 32;
   if (p.gather) p.box = 1;
   p.cache = a.cache;

@@ -9,14 +9,14 @@
 // one uses warp-level mma.sync (m16n8k16) with the queries in registers, so that
 // 180 KB of a CTA are key rows on their way, and every row serves the scores and the
 // output from the same place. Decode of 96 sequences of 64-16384 keys at 16 heads
-// (f16): 137 us for this kernel, 6.2 TB/s (174 us with the tcgen05 one).
+// (f16): 132 us for this kernel, 6.4 TB/s (174 us with the tcgen05 one).
 //
 //   warps 0-7  all of a step: the scores of 32 keys over a quarter of the columns
 //              (partial sums joined through shared memory), the softmax of two
 //              rows, then LD / 8 columns of O
-//   warp 8     producer (TMA, or cp.async for small boxes): 32-key slots of a ring,
-//              128-byte swizzled
-//   warp 9     scheduler: the segments of this CTA
+//   warp 8     scheduler: the segments of this CTA
+//   warp 9     producer (TMA): 32-key slots of a ring, 128-byte swizzled; for small boxes
+//              (cp.async) several warps, slots in turn
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -41,7 +41,12 @@ constexpr int HB = 32;           // keys of a ring slot
 constexpr int START = 2;
 constexpr int MAX_CTAS = 152;    // SMs of the device; the workspace is laid out for these
 constexpr int WARPS = 8;         // compute warps
-constexpr int NTHREADS = (WARPS + 2) * 32;
+// Warps that copy rows where TMA does not, slots in turn. 64 sequences of 1000-4000 keys at 16
+// heads with 1 / 2 / 3 / 4: pages of 16 50.2 / 45.4 / 45.4 / 51 us, of 8 57.5 / 47.6 / 46.3 / 51.5, of
+// 1 65.5 / 55.5 / 50.6 / 52.5 (by TMA, pages of 32 and more: 45.1).
+constexpr int G_PRODUCERS = 3;
+constexpr int producers(bool gather) { return gather ? G_PRODUCERS : 1; }
+constexpr int nthreads(bool gather) { return (WARPS + 1 + producers(gather)) * 32; }
 constexpr uint32_t UNIT = HB * 128;   // 32 rows x 64 columns of 16 bits
 constexpr int NSEG = 4;
 constexpr int S_LD = 72;         // floats between rows of the partial scores (no bank conflicts)
@@ -57,7 +62,7 @@ struct Cfg {
   static constexpr uint32_t RING = NS * SLOT;
 };
 
-template <int LD>
+template <int LD, int NTHREADS>
 struct State {
   uint64_t full[Cfg<LD>::NS], empty[Cfg<LD>::NS], segfull[NSEG], segempty[NSEG];
   LatentPlan<NTHREADS> plan;
@@ -119,13 +124,14 @@ __device__ __forceinline__ bool work_sync_or(bool x) {
   return r != 0;
 }
 
-template <int LD, typename T>
-__global__ void __launch_bounds__(NTHREADS, 1)
+template <int LD, typename T, bool GATHER>
+__global__ void __launch_bounds__(nthreads(GATHER), 1)
     latent_rows_kernel(const __grid_constant__ CUtensorMap mx, const T* __restrict__ q, LatentAttnP p) {
   using C = Cfg<LD>;
-  constexpr int NS = C::NS, D = LD + 64;
+  constexpr int NS = C::NS, D = LD + 64, PRODUCERS = producers(GATHER), NTHREADS = nthreads(GATHER);
   extern __shared__ __align__(1024) unsigned char sm[];
-  State<LD>& sh = *reinterpret_cast<State<LD>*>(sm + C::RING);
+  using Sh = State<LD, NTHREADS>;
+  Sh& sh = *reinterpret_cast<Sh*>(sm + C::RING);
   volatile int& s_abort = sh.abort;
   if (smem_u32(sm) & 1023u) {   // the swizzled rows need it; the array is declared so
     if (threadIdx.x == 0) atomicOr(p.dev_status, PKV_DEV_TIMEOUT);
@@ -134,12 +140,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == NTHREADS - 1) {   // a thread with no other set-up to do
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&sh.full[s], p.gather ? 32 : 1);
+      mbar_init(&sh.full[s], GATHER ? 32 : 1);
       mbar_init(&sh.empty[s], WARPS);
     }
     for (int e = 0; e < NSEG; ++e) {
       mbar_init(&sh.segfull[e], 1);
-      mbar_init(&sh.segempty[e], WARPS + 1);
+      mbar_init(&sh.segempty[e], WARPS + PRODUCERS);
     }
     fence_mbar_init();
     sh.abort = 0;
@@ -172,7 +178,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   };
 
   bool ok = true;
-  if (warp == WARPS + 1) {
+  if (warp == WARPS) {
     // ------------------------------------------------------------- scheduler
     if (lane == 0) mbar_arrive(&sh.segfull[0]);   // the plan left the first one there
     LatentRun<TM, BN, START> run(p, sh.plan, blockIdx.x);
@@ -189,11 +195,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (!g.valid) break;
     }
     if (lane == 0) ((LatentRecord*)(p.ws + Layout::rec))[blockIdx.x] = run.r;
-  } else if (warp == WARPS) {
+  } else if (warp > WARPS) {
     // --------------------------------------------------------------- producer
     // Lane l takes box l of a slot, or finds row l for the copies. Rows behind the end and bad pages are read from
     // page 0 (masked, or discarded); a slot with no key of the tile is not read.
-    const int boxes = HB / p.box;   // 1 (TMA), or 32 (copies)
+    constexpr int boxes = GATHER ? HB : 1;
+    const uint32_t turn = warp - WARPS - 1;
     uint32_t h = 0;   // slots before the current one
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t % NSEG;
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int keys = min(g.L, g.n * BN);   // keys that the tile needs
       bool bad = false;
       auto box_row = [&](int i) {
-        const int key = i * HB + lane * p.box;
+        const int key = i * HB + lane;
         if (lane >= boxes || key >= keys) return 0;
         const int lp = key / p.P;
         const int id = __ldg(pt + lp);
@@ -219,9 +226,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (bad) sh.bad[e] = 1;
         if (i + 1 < i1) row = box_row(i + 1);
         const uint32_t slot = h % NS;
+        if (GATHER && h % PRODUCERS != turn) continue;
         if (!(ok = wait(&sh.empty[slot], ((h / NS) & 1) ^ 1))) break;
         const bool some = i * HB < keys;
-        if (p.gather) {
+        if constexpr (GATHER) {
           if (some) {
             // eight lanes copy 128 bytes of a row, four rows at a time
             const uint32_t dst = smem_u32(sm) + slot * C::SLOT;
@@ -253,7 +261,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (lane == 0) mbar_arrive(&sh.segempty[e]);
       __syncwarp();
     }
-    if (p.gather) cp_async_wait_all();
+    if (GATHER) cp_async_wait_all();
     if (!ok && lane == 0) {
       // copies may still be on their way: give them time to land
       const uint64_t t0 = globaltimer_ns();
@@ -530,13 +538,13 @@ __global__ void __launch_bounds__(CTHREADS) latent_rows_combine_kernel(char* ws,
   }
 }
 
-template <int LD, typename T>
+template <int LD, typename T, bool GATHER>
 cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s) {
-  constexpr int smem = Cfg<LD>::RING + sizeof(State<LD>);
+  constexpr int smem = Cfg<LD>::RING + sizeof(State<LD, nthreads(GATHER)>);
   static_assert(smem <= 232448, "shared memory");
   static std::atomic<uint64_t> ready{0};   // devices whose kernel attribute is set
   if (!(ready.load() >> a.dev.id & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(latent_rows_kernel<LD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(latent_rows_kernel<LD, T, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << a.dev.id);
   }
@@ -550,12 +558,17 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s
   cudaError_t e;
   {
     KernelTimer timer("latent_rows", s);
-    e = launch_after_trigger(latent_rows_kernel<LD, T>, dim3(ctas), dim3(NTHREADS), smem, s, mx, (const T*)a.q, p);
+    e = launch_after_trigger(latent_rows_kernel<LD, T, GATHER>, dim3(ctas), dim3(nthreads(GATHER)), smem, s, mx, (const T*)a.q, p);
   }
   if (e != cudaSuccess) return e;
   KernelTimer timer("latent_combine", s);
   return launch_after_trigger(latent_rows_combine_kernel<LD, T>, dim3(ctas, CY), dim3(CTHREADS), 0, s, a.ws,
                               (T*)a.out, a.lse);
+}
+
+template <int LD, typename T>
+cudaError_t launch_either(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s) {
+  return p.gather ? launch<LD, T, true>(a, p, s) : launch<LD, T, false>(a, p, s);
 }
 
 }  // namespace
@@ -565,8 +578,9 @@ size_t latent_rows_workspace(int latent_dim) { return Layout::total(latent_dim);
 
 cudaError_t launch_latent_rows(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s) {
   if (a.dtype == PKV_BF16)
-    return a.latent_dim == 512 ? launch<512, __nv_bfloat16>(a, p, s) : launch<256, __nv_bfloat16>(a, p, s);
-  return a.latent_dim == 512 ? launch<512, __half>(a, p, s) : launch<256, __half>(a, p, s);
+    return a.latent_dim == 512 ? launch_either<512, __nv_bfloat16>(a, p, s)
+                               : launch_either<256, __nv_bfloat16>(a, p, s);
+  return a.latent_dim == 512 ? launch_either<512, __half>(a, p, s) : launch_either<256, __half>(a, p, s);
 }
 
 }  // namespace pkv
