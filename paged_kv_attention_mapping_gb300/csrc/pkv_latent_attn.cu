@@ -37,7 +37,8 @@
 //
 // Work split: the tick's steps (all tiles, one after the other, each with START more for its
 // start and end) are cut into equal runs, one per pair. A tile cut by a run's end leaves partial results
-// (normalised output in fp32 and log2 sum) that latent_combine_kernel joins.
+// (normalised output in fp32 and log2 sum) that latent_combine_kernel joins. Ticks of
+// short contexts are split by whole tiles instead.
 //
 // Decode of 128 sequences of 512-8192 keys at 128 heads (bf16): 131 us, 5.1 TB/s and 1.18
 // PFLOP/s; with the combine 138 us. Two step slots fit beside Q, and a slot's turn (load,
@@ -50,6 +51,7 @@
 // rotary columns in a unit of their own: no faster.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 
 #include <atomic>
 
@@ -793,6 +795,24 @@ __global__ void __launch_bounds__(CROWS * CVECS, 4) latent_combine_kernel(char* 
   else latent_join<LD, T, K, 8 / K / 2>(rec, ws, out, lse, r0, step);
 }
 
+int pairs_of(const LatentAttnArgs& a) { return a.dev.num_sms / 2 < MAX_PAIRS ? a.dev.num_sms / 2 : MAX_PAIRS; }
+
+// Whether the contexts are so short that cutting tiles costs more than it gives: a cut
+// shortens the longest worker's way, to the tick's average, and costs the join with
+// its launch and partial results (5 steps' time, and 5 more in proportion to the tiles). Lengths
+// are known by their bound alone; on average they are taken for 0.6 of it.
+// Graph-replayed, whole tiles against cut ones, latent 512, us, at 1 / 16 / 70 / 120 sequences of kv / 8
+// to kv keys: 64 heads, kv 250: 8.8 9.1 11.4 18.5 against 12.9 14.2 19.5 27.5; 500: 12.1 12.2 15.1
+// 24.9 against 13.1 15.5 26.3 32.7; 1000: 16.9 18.2 22.8 36.8 against 13.8 16.9 32.4 40.8.
+// 8 heads, kv 64: 4.6 4.7 4.9 5.5 against 7.4 7.9 8.1 8.1; 500: 11.8 13.5 13.7 15.4 against
+// 8.7 10.3 15.0 22.0; 1000: 20.0 21.5 23.9 25.2 against 8.6 11.5 21.4 27.9.
+bool short_contexts(const LatentAttnArgs& a, const LatentTiling& t) {
+  const int64_t per_seq = ((int64_t)a.T * a.H + a.B - 1) / a.B;   // rows, on average
+  const int64_t tiles = (per_seq + t.rows - 1) / t.rows * a.B;
+  const float steps = (float)((a.max_kv_len + (int64_t)t.keys - 1) / t.keys), share = (float)tiles / t.workers;
+  return steps * (ceilf(share) - 0.6f * share) <= 5.f + 5.f * share;
+}
+
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
 template <int LD, typename T, bool GATHER>
@@ -815,14 +835,14 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s
       !make_map_chunks(&mx, a.cache, dt, Cfg<LD>::CH, pool_rows, LD + 64, box, 1) ||
       !make_map_chunks(&m2, a.cache, dt, Cfg<LD>::CH, pool_rows, LD + 64, box, 2))
     return cudaErrorInvalidValue;
-  const int pairs = a.dev.num_sms / 2 < MAX_PAIRS ? a.dev.num_sms / 2 : MAX_PAIRS;
+  const int pairs = pairs_of(a);
   cudaError_t e;
   {
     KernelTimer timer("latent_attn", s);
     e = launch_after_trigger(latent_attn_kernel<LD, T, GATHER>, dim3(2 * pairs), dim3(nthreads(GATHER)), smem, s, mq,
                              mx, m2, p);
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole) return e;
   KernelTimer timer("latent_combine", s);
   return launch_after_trigger(latent_combine_kernel<LD, T>, dim3(pairs, CY, 2 * LD / 8 / CVECS),
                               dim3(CROWS * CVECS), 0, s, a.ws, (T*)a.out, a.lse);
@@ -863,6 +883,7 @@ cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t s) {
   // before other changes: 92 / 70 and 352 / 72); the 16-row kernel takes one box a slot.
   p.gather = p.box < 32;
   if (p.gather) p.box = 1;
+  p.whole = short_contexts(a, rows ? latent_rows_tiling(a.dev.num_sms) : LatentTiling{BM, BN, pairs_of(a)});
   p.cache = a.cache;
   p.num_pages = a.num_pages;
   p.max_pages = a.max_pages;

@@ -554,13 +554,13 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s
                                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                      Cfg<LD>::CH, (int64_t)a.num_pages * a.P, LD + 64, HB, Cfg<LD>::CH))
     return cudaErrorInvalidValue;
-  const int ctas = a.dev.num_sms < MAX_CTAS ? a.dev.num_sms : MAX_CTAS;
+  const int ctas = latent_rows_tiling(a.dev.num_sms).workers;
   cudaError_t e;
   {
     KernelTimer timer("latent_rows", s);
     e = launch_after_trigger(latent_rows_kernel<LD, T, GATHER>, dim3(ctas), dim3(nthreads(GATHER)), smem, s, mx, (const T*)a.q, p);
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.whole) return e;
   KernelTimer timer("latent_combine", s);
   return launch_after_trigger(latent_rows_combine_kernel<LD, T>, dim3(ctas, CY), dim3(CTHREADS), 0, s, a.ws,
                               (T*)a.out, a.lse);
@@ -574,6 +574,7 @@ cudaError_t launch_either(const LatentAttnArgs& a, const LatentAttnP& p, cudaStr
 }  // namespace
 
 int latent_rows_slot() { return HB; }
+LatentTiling latent_rows_tiling(int num_sms) { return LatentTiling{TM, BN, num_sms < MAX_CTAS ? num_sms : MAX_CTAS}; }
 size_t latent_rows_workspace(int latent_dim) { return Layout::total(latent_dim); }
 
 cudaError_t launch_latent_rows(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s) {

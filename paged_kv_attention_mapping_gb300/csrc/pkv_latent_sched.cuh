@@ -11,10 +11,11 @@ namespace pkv {
 // gather: rows come by 16-byte copies of threads (box is 1), not by TMA boxes. A
 // TMA instruction costs its warp about 90 cycles whatever its box holds, so small
 // boxes (pages that share no large power of two with a slot) starve the tensor cores.
+// whole: no tile is cut, so that nothing is left to join. The split counts tiles, not steps.
 struct LatentAttnP {
   const int32_t *cu, *kv_lens, *page_tables;
   const void* cache;
-  int32_t B, T, H, P, box, gather, num_pages, max_pages, max_kv_len, table_cap, out_32;
+  int32_t B, T, H, P, box, gather, whole, num_pages, max_pages, max_kv_len, table_cap, out_32;
   float scale_log2;   // > 0
   void* out;
   float* lse;
@@ -23,8 +24,12 @@ struct LatentAttnP {
 };
 
 // The kernel for few rows a sequence (pkv_latent_rows.cu): rows of its ring slots,
-// its workspace, its launch.
+// its tiling, its workspace, its launch.
 int latent_rows_slot();
+struct LatentTiling {
+  int rows, keys, workers;   // of a tile, of a step, of the GPU
+};
+LatentTiling latent_rows_tiling(int num_sms);
 size_t latent_rows_workspace(int latent_dim);
 cudaError_t launch_latent_rows(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s);
 
@@ -48,7 +53,7 @@ struct LatentRecord {
 // offset in units; one in the first START of them stands before its first step.
 template <int TM, int BN, int START>
 struct LatentSeq {
-  int q, L, base, H, rows, tiles;
+  int q, L, base, H, rows, tiles, whole;
   __device__ __forceinline__ int steps(int t) const {
     const int last = (min((t + 1) * TM, rows) - 1) / H;
     return (base + last + BN) / BN;
@@ -61,7 +66,7 @@ struct LatentSeq {
     return min(tiles - 1, (int)(e * H / TM));
   }
   __device__ __forceinline__ int64_t total() const {
-    if (tiles == 0) return 0;
+    if (tiles == 0 || whole) return tiles;
     if (tiles == 1) return (L + BN - 1) / BN + START;
     const int lo = steps(0), hi = steps(tiles - 1);
     int64_t s = (int64_t)(hi + START) * tiles;
@@ -70,9 +75,9 @@ struct LatentSeq {
   }
   // tile, and offset in it, of the sequence's unit number `at`
   __device__ __forceinline__ void seek(int64_t at, int* tile, int* off) const {
-    if (tiles == 1) {
-      *tile = 0;
-      *off = (int)at;
+    if (tiles == 1 || whole) {
+      *tile = whole ? (int)at : 0;
+      *off = whole ? 0 : (int)at;
       return;
     }
     const int lo = steps(0), hi = steps(tiles - 1);
@@ -95,6 +100,7 @@ struct LatentSeq {
     q = __ldg(p.cu + b + 1) - c0;
     L = __ldg(p.kv_lens + b);
     H = p.H;
+    whole = p.whole;
     base = L - q;
     rows = q * H;
     tiles = (rows + TM - 1) / TM;
@@ -120,7 +126,7 @@ __device__ __forceinline__ LatentSegment latent_segment(const LatentAttnP& p, co
   g.nrows = min(TM, s.rows - tile * TM);
   g.n = s.steps(tile);
   g.j0 = max(0, off - START);
-  g.j1 = (int)min((int64_t)g.n, off - START + left);
+  g.j1 = p.whole ? g.n : (int)min((int64_t)g.n, off - START + left);
   g.valid = g.j0 < g.j1;
   return g;
 }
@@ -239,7 +245,7 @@ struct LatentRun {
       r.row0 = g.row0;
       r.nrows = g.nrows;
     }
-    const int used = g.j1 + START - off;
+    const int used = p.whole ? 1 : g.j1 + START - off;
     left -= used;
     done += used;
     ++tile;

@@ -324,6 +324,12 @@ ABSORBED = [
     ("f16", 512, 16, 5, [1, 0], [7000, 12]),
     ("bf16", 512, 7, 256, [40] + [0] * 30 + [1], [3000] + [1] * 31),
     ("bf16", 512, 16, 64, [1] * 200, [1 + 97 * k % 500 for k in range(200)]),
+    # short contexts: whole tiles, several a worker; the longest that are not cut, the shortest that are
+    ("bf16", 512, 20, 64, [1] * 170, [1 + 41 * k % 300 for k in range(170)]),
+    ("f16", 256, 40, 24, [k % 5 for k in range(100)], [5 + 37 * k % 400 for k in range(100)]),
+    ("bf16", 256, 4, 64, [1] * 400, [1 + 11 * k % 64 for k in range(400)]),
+    ("bf16", 512, 64, 64, [1] * 3, [640, 640, 5]), ("bf16", 512, 64, 64, [1] * 3, [641, 640, 5]),
+    ("f16", 512, 8, 64, [1] * 2, [320, 7]), ("f16", 512, 8, 64, [1] * 2, [321, 7]),
     # rows by thread copies, more steps than slots, tails of every kind
     ("bf16", 512, 128, 16, [1, 1, 1], [1025, 640, 1000]),
     ("f16", 512, 33, 1, [1, 2], [777, 513]),
