@@ -486,13 +486,24 @@ LATENT_NOPE, LATENT_ROPE, LATENT_V = 128, 64, 128
 # The smallest ticks are a few microseconds of GPU work, so these checks are written
 # for few attribute reads: a tensor's shape, strides or type is read once.
 
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 @functools.lru_cache(maxsize=256)
-def _latent_desc_of(shape, dtype) -> LatentDesc:
+def _latent_desc_of(shape, dtype):
     N, P, R = shape
-    return LatentDesc(N, P, R - LATENT_ROPE, LATENT_ROPE, _code_of(dtype))
+    return R - LATENT_ROPE, ctypes.byref(LatentDesc(N, P, R - LATENT_ROPE, LATENT_ROPE, _code_of(dtype)))
 
 
-def _latent_desc(where, cache) -> LatentDesc:
+def _latent_desc(where, cache):
+    """The cache's latent_dim and its descriptor, as an argument."""
     if cache.dim() != 3 or not cache.is_contiguous():
         raise ValueError(f"{where}: the latent cache must be a contiguous [num_pages, page_size, latent_dim + 64] tensor")
     return _latent_desc_of(cache.shape, cache.dtype)
@@ -507,16 +518,6 @@ def _on_one_device(where, first, *rest) -> int:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{where}: all tensors must be on one CUDA device")
     return dev
-
-
-def _call_on(dev, stream, fn, *args) -> int:
-    """fn(*args, stream) with device `dev` current (the library launches on the
-    current device); stream None is torch's current one there."""
-    import torch
-    if dev != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
-            return fn(*args, _stream_ptr(stream))
-    return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream))
 
 
 def _rows_only(where, *last):
@@ -547,10 +548,13 @@ def latent_append(c_kv, k_rope, positions, cos_sin, slot_mapping, cache, q_rope=
     [T], cache [N, P, latent_dim + 64]. With q_rope [T, H, 64] its rotation goes
     to q_out (strided views allowed; q_out may be q_rope; a new tensor when it is
     None). Returns q_out (None without q_rope)."""
-    import torch
+    torch = _torch or _load_torch()
     where = "latent_append"
-    desc = _latent_desc(where, cache)
+    latent_dim, desc = _latent_desc(where, cache)
     dev = _on_one_device(where, cache, c_kv, k_rope, positions, cos_sin, slot_mapping, q_rope, q_out)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return latent_append(c_kv, k_rope, positions, cos_sin, slot_mapping, cache, q_rope, q_out, stream)
     if (positions.dtype is not torch.int32 or slot_mapping.dtype is not torch.int64
             or cos_sin.dtype is not torch.float32):
         raise TypeError(f"{where}: positions int32, slot_mapping int64, cos_sin float32")
@@ -560,9 +564,9 @@ def latent_append(c_kv, k_rope, positions, cos_sin, slot_mapping, cache, q_rope=
     if len(tokens) != 1 or positions.shape != tokens or len(table) != 3 or table[1:] != (LATENT_ROPE // 2, 2):
         raise ValueError(f"{where}: positions and slot_mapping must be [T], cos_sin [max_pos, {LATENT_ROPE // 2}, 2]")
     T, = tokens
-    if (c_kv.dtype is not dtype or k_rope.dtype is not dtype or c_kv.shape != (T, desc.latent_dim)
+    if (c_kv.dtype is not dtype or k_rope.dtype is not dtype or c_kv.shape != (T, latent_dim)
             or k_rope.shape != (T, LATENT_ROPE)):
-        raise ValueError(f"{where}: c_kv must be [T, {desc.latent_dim}], k_rope [T, {LATENT_ROPE}], of the cache's dtype")
+        raise ValueError(f"{where}: c_kv must be [T, {latent_dim}], k_rope [T, {LATENT_ROPE}], of the cache's dtype")
     (c_st, c_1), (kr_st, kr_1) = c_kv.stride(), k_rope.stride()
     _rows_only(where, c_1, kr_1)
     q = qo = None
@@ -586,10 +590,12 @@ def latent_append(c_kv, k_rope, positions, cos_sin, slot_mapping, cache, q_rope=
         raise ValueError(f"{where}: q_out without q_rope")
     if T == 1:   # (a dimension of one entry may have any stride)
         c_st = kr_st = q_st = qo_st = 0
-    st = _call_on(dev, stream, lib().pkv_latent_append, c_kv.data_ptr(), c_st, k_rope.data_ptr(), kr_st, q, q_st, q_sh,
-                  qo, qo_st, qo_sh, H, positions.data_ptr(), cos_sin.data_ptr(), table[0], slot_mapping.data_ptr(), T,
-                  cache.data_ptr(), desc)
-    _check(st, "pkv_latent_append")
+    on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+    st = lib().pkv_latent_append(c_kv.data_ptr(), c_st, k_rope.data_ptr(), kr_st, q, q_st, q_sh, qo, qo_st, qo_sh, H,
+                                 positions.data_ptr(), cos_sin.data_ptr(), table[0], slot_mapping.data_ptr(), T,
+                                 cache.data_ptr(), desc, on)
+    if st:
+        _check(st, "pkv_latent_append")
     return q_out
 
 
@@ -598,31 +604,36 @@ def latent_gather(cache, page_tables, cu_seqlens_k, total_k: int, out=None, stre
     latent_dim + 64], sequence b in rows cu_seqlens_k[b] .. cu_seqlens_k[b + 1].
     out[:, :latent_dim] is what the up-projection reads, out[:, latent_dim:] the
     k_rope of latent_prefill."""
-    import torch
+    torch = _torch or _load_torch()
     where = "latent_gather"
-    desc = _latent_desc(where, cache)
+    latent_dim, desc = _latent_desc(where, cache)
     if page_tables.dtype is not torch.int32 or cu_seqlens_k.dtype is not torch.int32:
         raise TypeError(f"{where}: index tensors must be int32")
     dev = _on_one_device(where, cache, page_tables, cu_seqlens_k, out)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return latent_gather(cache, page_tables, cu_seqlens_k, total_k, out, stream)
     tables, cu = page_tables.shape, cu_seqlens_k.shape
     if len(tables) != 2 or len(cu) != 1 or not 1 <= cu[0] <= tables[0] + 1:
         raise ValueError(f"{where}: page_tables [B, W] and cu_seqlens_k [B + 1] disagree")
     if not (page_tables.is_contiguous() and cu_seqlens_k.is_contiguous()):
         raise ValueError(f"{where}: index tensors must be contiguous")
-    total_k, R = int(total_k), desc.latent_dim + LATENT_ROPE
+    total_k, R = int(total_k), latent_dim + LATENT_ROPE
     if out is None:
         out = _lent(torch.empty((total_k, R), dtype=cache.dtype, device=cache.device), stream)
     elif out.dtype is not cache.dtype or out.shape != (total_k, R) or not out.is_contiguous():
         raise ValueError(f"{where}: out must be a contiguous [total_k, {R}] tensor of the cache's dtype")
-    st = _call_on(dev, stream, lib().pkv_latent_gather, cache.data_ptr(), desc, page_tables.data_ptr(), tables[1],
-                  cu_seqlens_k.data_ptr(), cu[0] - 1, total_k, out.data_ptr())
-    _check(st, "pkv_latent_gather")
+    on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+    st = lib().pkv_latent_gather(cache.data_ptr(), desc, page_tables.data_ptr(), tables[1], cu_seqlens_k.data_ptr(),
+                                 cu[0] - 1, total_k, out.data_ptr(), on)
+    if st:
+        _check(st, "pkv_latent_gather")
     return out
 
 
 def latent_workspace_size(num_seqs: int, total_q: int, num_q_heads: int, cache) -> int:
-    desc = _latent_desc("latent_workspace_size", cache)
-    n = lib().pkv_latent_attention_workspace_size(int(num_seqs), int(total_q), int(num_q_heads), ctypes.byref(desc))
+    _, desc = _latent_desc("latent_workspace_size", cache)
+    n = lib().pkv_latent_attention_workspace_size(int(num_seqs), int(total_q), int(num_q_heads), desc)
     if n == 0:
         raise PagedKVError(-3, "pkv_latent_attention_workspace_size")
     return int(n)
@@ -641,15 +652,19 @@ def latent_attention(q, cu_seqlens_q, kv_lens, page_tables, cache, scale: float,
     q [T, H, latent_dim + 64] (cache dtype), cu_seqlens_q int32 [B + 1], kv_lens
     int32 [B], page_tables int32 [B, W], cache [N, P, latent_dim + 64]. Returns
     (out [T, H, latent_dim], lse [T, H])."""
-    import torch
+    torch = _torch or _load_torch()
     where = "latent_attention"
-    desc = _latent_desc(where, cache)
-    i32, dtype, width = torch.int32, cache.dtype, desc.latent_dim
+    width, desc = _latent_desc(where, cache)
+    i32, dtype = torch.int32, cache.dtype
     if cu_seqlens_q.dtype is not i32 or kv_lens.dtype is not i32 or page_tables.dtype is not i32:
         raise TypeError(f"{where}: index tensors must be int32")
     if q.dtype is not dtype:
         raise TypeError(f"{where}: q and cache must share one dtype")
     dev = _on_one_device(where, q, cu_seqlens_q, kv_lens, page_tables, cache, out, lse, workspace)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return latent_attention(q, cu_seqlens_q, kv_lens, page_tables, cache, scale, max_kv_len, out, lse, workspace,
+                                    want_lse, stream)
     shape, tables, cu, lens = q.shape, page_tables.shape, cu_seqlens_q.shape, kv_lens.shape
     if len(shape) != 3 or shape[2] != width + LATENT_ROPE or not q.is_contiguous():
         raise ValueError(f"{where}: q must be a contiguous [T, H, {width + LATENT_ROPE}] tensor")
@@ -672,10 +687,12 @@ def latent_attention(q, cu_seqlens_q, kv_lens, page_tables, cache, scale: float,
         workspace = _lent(alloc_latent_workspace(B, T, H, cache), stream)
     elif not workspace.is_contiguous():
         raise ValueError(f"{where}: workspace must be contiguous")
-    st = _call_on(dev, stream, lib().pkv_latent_attention, q.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
-                  page_tables.data_ptr(), B, T, H, tables[1], int(max_kv_len), cache.data_ptr(), desc, scale,
-                  out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes)
-    _check(st, "pkv_latent_attention")
+    on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+    st = lib().pkv_latent_attention(q.data_ptr(), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), page_tables.data_ptr(), B,
+                                    T, H, tables[1], int(max_kv_len), cache.data_ptr(), desc, scale, out.data_ptr(),
+                                    None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, on)
+    if st:
+        _check(st, "pkv_latent_attention")
     return out, lse
 
 
@@ -699,11 +716,15 @@ def latent_prefill(q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, scale: floa
     q [Tq, H, 192]; k_nope and v [Tk, H, 128], k_rope [Tk, 64] (strided rows
     allowed: views of the up-projection's output and of the gathered rows);
     cu_seqlens_q, cu_seqlens_k int32 [B + 1]. Returns (out [Tq, H, 128], lse [Tq, H])."""
-    import torch
+    torch = _torch or _load_torch()
     where = "latent_prefill"
     if cu_seqlens_q.dtype is not torch.int32 or cu_seqlens_k.dtype is not torch.int32:
         raise TypeError(f"{where}: index tensors must be int32")
     dev = _on_one_device(where, q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, out, lse, workspace)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return latent_prefill(q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, scale, out, lse, workspace, want_lse,
+                                  stream)
     shape, dtype, rope, cu = q.shape, q.dtype, k_rope.shape, cu_seqlens_q.shape
     if len(shape) != 3 or shape[2] != LATENT_NOPE + LATENT_ROPE or not q.is_contiguous():
         raise ValueError(f"{where}: q must be a contiguous [T, H, {LATENT_NOPE + LATENT_ROPE}] tensor")
@@ -736,11 +757,13 @@ def latent_prefill(q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, scale: floa
         workspace = _lent(alloc_latent_prefill_workspace(B, q), stream)
     elif not workspace.is_contiguous():
         raise ValueError(f"{where}: workspace must be contiguous")
-    st = _call_on(dev, stream, lib().pkv_latent_prefill, q.data_ptr(), cu_seqlens_q.data_ptr(), k_nope.data_ptr(),
-                  kn_st, kn_sh, v.data_ptr(), v_st, v_sh, k_rope.data_ptr(), kr_st, cu_seqlens_k.data_ptr(), B, Tq, Tk,
-                  H, _code_of(dtype), scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
-                  workspace.data_ptr(), workspace.nbytes)
-    _check(st, "pkv_latent_prefill")
+    on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+    st = lib().pkv_latent_prefill(q.data_ptr(), cu_seqlens_q.data_ptr(), k_nope.data_ptr(), kn_st, kn_sh, v.data_ptr(),
+                                  v_st, v_sh, k_rope.data_ptr(), kr_st, cu_seqlens_k.data_ptr(), B, Tq, Tk, H,
+                                  _code_of(dtype), scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                  workspace.data_ptr(), workspace.nbytes, on)
+    if st:
+        _check(st, "pkv_latent_prefill")
     return out, lse
 
 
