@@ -423,6 +423,26 @@ def test_absorbed_bad_data_skips_the_sequence(dev, heads):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads,page", [(16, 64), (4, 64), (16, 8), (4, 8)])
+def test_absorbed_short_contexts_bad_data(dev, heads, page):
+    """The same where contexts are so short that no tile is cut."""
+    t = Paged(dev, "bf16", 256, heads, page, [1, 2, 1], [60, 150, 100])
+    good, good_lse = t.call()
+    for what, bit in (("page", binding.DEV_BAD_PAGE), ("len", binding.DEV_BAD_LENGTHS)):
+        table, kv = t.table.copy(), list(t.kv_lens)
+        if what == "page":
+            table[1, 1] = -1
+        else:
+            kv[1] = 151
+        out, lse = torch.full_like(good, 9.0), torch.full_like(good_lse, 9.0)
+        binding.latent_attention(t.q, _i32(t.cu, dev), _i32(kv, dev), _i32(table, dev), t.cache, SCALE, 150,
+                                 out=out, lse=lse)
+        assert binding.device_status() == bit, what
+        assert (out[1:3] == 9).all() and (lse[1:3] == 9).all(), what
+        assert torch.equal(out[0], good[0]) and torch.equal(out[3], good[3]), what
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("heads", [16, 40])
 def test_absorbed_pages_beyond_four_gigabytes(dev, heads):
     """Rows whose byte and element offsets pass 32 bits."""
