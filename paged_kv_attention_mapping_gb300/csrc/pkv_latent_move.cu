@@ -52,7 +52,8 @@ template <typename T>
 __global__ void __launch_bounds__(THREADS) latent_append_kernel(const T* __restrict__ c, const T* __restrict__ kr,
                                                                 const T* q, T* q_out, T* __restrict__ cache,
                                                                 AppendP p) {
-  pdl_trigger();   // what the attention call reads before its own wait is not written here
+  pdl_wait();
+  pdl_trigger();   // what the attention call reads before its own wait is not written here, nor by a kernel before
   const int64_t j = (int64_t)blockIdx.x * THREADS + threadIdx.x;
   if (j >= p.items) return;
   const int64_t t = j / p.per_token;
@@ -97,8 +98,8 @@ __global__ void __launch_bounds__(THREADS) latent_append_kernel(const T* __restr
   }
 }
 
-// A block takes R consecutive packed rows (107 k rows of 1152 bytes: 39.4 us, 6.2
-// TB/s; 41.7 with 8 rows a block, 40.0 with 32). Its threads first check cu_seqlens
+// A block takes R consecutive packed rows (107 k rows of 1152 bytes: 38.8 us, 6.3
+// TB/s; 1 to 2 us more with 8 or 32 rows a block). Its threads first check cu_seqlens
 // (every block does, so that a bad array copies nothing), then one thread per
 // row finds the row's sequence and slot, then all copy.
 template <int R>
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(THREADS) latent_gather_kernel(const uint4* __r
                                                                 uint4* __restrict__ out, int32_t* dev_status) {
   __shared__ int64_t s_src[R];
   const int tid = threadIdx.x;
+  pdl_wait();
   bool bad = tid == 0 && __ldg(cu) != 0;
   for (int b = tid; b < B; b += THREADS) bad |= __ldg(cu + b + 1) < __ldg(cu + b);
   const int n = __ldg(cu + B);
@@ -191,24 +193,21 @@ cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t s) {
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   KernelTimer timer("latent_append", s);
   if (a.dtype == PKV_F16)
-    latent_append_kernel<__half><<<(unsigned)blocks, THREADS, 0, s>>>((const __half*)a.c, (const __half*)a.kr,
-                                                                     (const __half*)a.q, (__half*)a.q_out,
-                                                                     (__half*)a.cache, p);
-  else
-    latent_append_kernel<__nv_bfloat16><<<(unsigned)blocks, THREADS, 0, s>>>(
-        (const __nv_bfloat16*)a.c, (const __nv_bfloat16*)a.kr, (const __nv_bfloat16*)a.q, (__nv_bfloat16*)a.q_out,
-        (__nv_bfloat16*)a.cache, p);
-  return cudaGetLastError();
+    return launch_after_trigger(latent_append_kernel<__half>, dim3((unsigned)blocks), dim3(THREADS), 0, s,
+                                (const __half*)a.c, (const __half*)a.kr, (const __half*)a.q, (__half*)a.q_out,
+                                (__half*)a.cache, p);
+  return launch_after_trigger(latent_append_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(THREADS), 0, s,
+                              (const __nv_bfloat16*)a.c, (const __nv_bfloat16*)a.kr, (const __nv_bfloat16*)a.q,
+                              (__nv_bfloat16*)a.q_out, (__nv_bfloat16*)a.cache, p);
 }
 
 cudaError_t launch_latent_gather(const LatentGatherArgs& a, cudaStream_t s) {
   KernelTimer timer("latent_gather", s);
   constexpr int R = 16;
   const unsigned blocks = (unsigned)((a.total + (int64_t)R - 1) / R);
-  latent_gather_kernel<R><<<blocks, THREADS, 0, s>>>((const uint4*)a.cache, a.page_tables, a.cu, a.B, a.total,
-                                                    a.max_pages, a.P, a.num_pages, a.row_vecs, (uint4*)a.out,
-                                                    a.dev_status);
-  return cudaGetLastError();
+  return launch_after_trigger(latent_gather_kernel<R>, dim3(blocks), dim3(THREADS), 0, s, (const uint4*)a.cache,
+                              a.page_tables, a.cu, a.B, a.total, a.max_pages, a.P, a.num_pages, a.row_vecs,
+                              (uint4*)a.out, a.dev_status);
 }
 
 }  // namespace pkv
