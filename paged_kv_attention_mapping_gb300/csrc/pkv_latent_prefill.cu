@@ -353,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   if (warp == 1) tmem_alloc_pair(&s_tmem, TMEM_COLS);
   Found found{0, 1, 0, 0};
   // (reads only the lengths, which the kernel before does not write)
-  if (p.direct && rank == 0 && warp == 0) found = find_item(p, blockIdx.x >> 1, gridDim.x >> 1);
+  if (p.direct && warp == 0) found = find_item(p, blockIdx.x >> 1, gridDim.x >> 1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -400,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     uint32_t n_k = 0, n_v = 0, n_tail = 0;    // K, V loads and last tiles with rows to zero so far
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t & 1;
-      if (rank == 0) {
+      if (rank == 0 || p.direct) {   // (without a plan both CTAs find the tile)
         // entry e is free again once every consumer is done with tile t - 2
         if (t >= 2 && !(ok = wait(&bar_tempty[e], ((t >> 1) - 1) & 1))) break;
         Tile ti{};
@@ -453,20 +453,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
               ti.j1 = part_begin(n, ti.part + 1, ti.parts);
             }
             ti.valid = 1;
-            if (most_parts > 1 && lane == 0) *reinterpret_cast<Tile*>(p.rec + (size_t)tt * 128) = ti;
+            if (most_parts > 1 && rank == 0 && lane == 0) *reinterpret_cast<Tile*>(p.rec + (size_t)tt * 128) = ti;
           } else {
             ti.valid = 0;
           }
         }
         if (lane == 0) {
           s_tile[e] = ti;
-          const uint32_t peer = map_to_rank(&s_tile[e], 1);
-          const uint32_t* words = reinterpret_cast<const uint32_t*>(&ti);
+          if (!p.direct) {
+            const uint32_t peer = map_to_rank(&s_tile[e], 1);
+            const uint32_t* words = reinterpret_cast<const uint32_t*>(&ti);
 #pragma unroll
-          for (int i = 0; i < (int)(sizeof(Tile) / 4); ++i) st_cluster_u32(peer + 4 * i, words[i]);
-          fence_cluster();
+            for (int i = 0; i < (int)(sizeof(Tile) / 4); ++i) st_cluster_u32(peer + 4 * i, words[i]);
+            fence_cluster();
+            mbar_arrive_cluster(map_to_rank(&bar_tfull[e], 1));
+          }
           mbar_arrive(&bar_tfull[e]);
-          mbar_arrive_cluster(map_to_rank(&bar_tfull[e], 1));
         }
         __syncwarp();
       }
@@ -850,7 +852,7 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
   p.H = a.H;
   p.Tq = a.Tq;
   p.Tk = a.Tk;
-  // (3 prompts of 20-300 tokens at 16 heads: 14.0 us, with the plan kernel 15.2)
+  // (3 prompts of 20-300 tokens at 16 heads: 13.8 us, with the plan kernel 15.2)
   p.direct = a.B <= pairs && most_tiles(a.B, a.Tq, a.H) <= pairs;
   // a stride that no index uses (one head, one row) or 0 (one head for all) is not a
   // stride for the tensor map: such a dimension has one entry there
