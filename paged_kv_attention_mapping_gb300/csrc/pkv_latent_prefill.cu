@@ -13,7 +13,7 @@
 // sequence's 256 rows or fewer that do not fill such a tile, the same rows of two heads.
 // (One CTA with two tiles of 128 rows needs twice the shared memory for a step's
 // keys: beside Q it held 1.6 steps, waited for loads, and took 499 us for 4096 tokens at
-// 128 heads in bf16, this one 444: 1546 TFLOP/s.)
+// 128 heads in bf16, this one 447: 1538 TFLOP/s.)
 //
 //   warp 0     TMA producer (each CTA its halves): Q of both tiles, K_j (nope part
 //              and rotary part) and V_j into rings of three; V rows behind the
@@ -397,6 +397,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     }
     const uint32_t q_bar = map_to_rank(&bar_q, 0);
     uint32_t n_claims = 0;
+    // Up to 32 sequences: a lane keeps one, in the plan's order, so that a claim waits for
+    // nothing but its number (16 chunks of 30-128 rows after 2000 keys at 32 heads 154.3 -> 150.2 us).
+    const bool kept = !p.direct && p.B <= 32;
+    int my_b = 0, my_first = INT32_MAX, my_q0 = 0, my_q = 0, my_k0 = 0, my_L = 0;
+    if (rank == 0 && kept && lane < p.B) {
+      my_b = p.order[lane];
+      my_first = p.first[lane];
+      my_q0 = __ldg(p.cu_q + my_b);
+      my_q = __ldg(p.cu_q + my_b + 1) - my_q0;
+      my_k0 = __ldg(p.cu_k + my_b);
+      my_L = __ldg(p.cu_k + my_b + 1) - my_k0;
+    }
     uint32_t n_k = 0, n_v = 0, n_tail = 0;    // K, V loads and last tiles with rows to zero so far
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t & 1;
@@ -409,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           tt = __shfl_sync(0xffffffffu, tt, 0);
           if (__any_sync(0xffffffffu, s_abort)) tt = n_tiles;
           int lo = 0;   // the last sequence that starts at or before tile tt, searched 32 ways
-          for (int m = p.direct || tt >= n_tiles ? 0 : p.B; m > 1;) {
+          for (int m = p.direct || kept || tt >= n_tiles ? 0 : p.B; m > 1;) {
             const int step = (m + 31) / 32, at = lo + lane * step;
             const bool before = lane * step < m && p.first[at] <= tt;
             lo += (__popc(__ballot_sync(0xffffffffu, before)) - 1) * step;
@@ -417,10 +429,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           skip = false;
           if (tt < n_tiles) {
-            const int b = p.direct ? found.b : p.order[lo], before = p.direct ? found.before : p.first[lo];
-            const int q_lo = __ldg(p.cu_q + b), q = __ldg(p.cu_q + b + 1) - q_lo;
-            ti.k0 = __ldg(p.cu_k + b);
-            ti.L = __ldg(p.cu_k + b + 1) - ti.k0;
+            int before, q_lo, q;
+            if (kept) {
+              lo = 31 - __clz(__ballot_sync(0xffffffffu, my_first <= tt));
+              before = __shfl_sync(0xffffffffu, my_first, lo);
+              q_lo = __shfl_sync(0xffffffffu, my_q0, lo);
+              q = __shfl_sync(0xffffffffu, my_q, lo);
+              ti.k0 = __shfl_sync(0xffffffffu, my_k0, lo);
+              ti.L = __shfl_sync(0xffffffffu, my_L, lo);
+            } else {
+              const int b = p.direct ? found.b : p.order[lo];
+              before = p.direct ? found.before : p.first[lo];
+              q_lo = __ldg(p.cu_q + b);
+              q = __ldg(p.cu_q + b + 1) - q_lo;
+              ti.k0 = __ldg(p.cu_k + b);
+              ti.L = __ldg(p.cu_k + b + 1) - ti.k0;
+            }
             const int wide = wide_tiles(q), rest = narrow_rows(q);
             int at = tt - before;
             ti.parts = 1;
