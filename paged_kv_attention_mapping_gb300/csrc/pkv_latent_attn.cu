@@ -799,18 +799,19 @@ int pairs_of(const LatentAttnArgs& a) { return a.dev.num_sms / 2 < MAX_PAIRS ? a
 
 // Whether the contexts are so short that cutting tiles costs more than it gives: a cut
 // shortens the longest worker's way, to the tick's average, and costs the join with
-// its launch and partial results (5 steps' time, and 5 more in proportion to the tiles). Lengths
-// are known by their bound alone; on average they are taken for 0.6 of it.
+// its launch and partial results (5 steps' time, and 5 more for a tile a worker, 10 for two or
+// more). Lengths are known by their bound alone; on average they are taken for 0.6 of it.
 // Graph-replayed, whole tiles against cut ones, latent 512, us, at 1 / 16 / 70 / 120 sequences of kv / 8
 // to kv keys: 64 heads, kv 250: 8.8 9.1 11.4 18.5 against 12.9 14.2 19.5 27.5; 500: 12.1 12.2 15.1
 // 24.9 against 13.1 15.5 26.3 32.7; 1000: 16.9 18.2 22.8 36.8 against 13.8 16.9 32.4 40.8.
 // 8 heads, kv 64: 4.6 4.7 4.9 5.5 against 7.4 7.9 8.1 8.1; 500: 11.8 13.5 13.7 15.4 against
-// 8.7 10.3 15.0 22.0; 1000: 20.0 21.5 23.9 25.2 against 8.6 11.5 21.4 27.9.
+// 8.7 10.3 15.0 22.0; 1000: 20.0 21.5 23.9 25.2 against 8.6 11.5 21.4 27.9. 300 at 64 heads,
+// kv 250: 33 against 40, 1000: 64 against 68; 400 at 8 heads, kv 1000: 61 against 56.
 bool short_contexts(const LatentAttnArgs& a, const LatentTiling& t) {
   const int64_t per_seq = ((int64_t)a.T * a.H + a.B - 1) / a.B;   // rows, on average
   const int64_t tiles = (per_seq + t.rows - 1) / t.rows * a.B;
   const float steps = (float)((a.max_kv_len + (int64_t)t.keys - 1) / t.keys), share = (float)tiles / t.workers;
-  return steps * (ceilf(share) - 0.6f * share) <= 5.f + 5.f * share;
+  return steps * (ceilf(share) - 0.6f * share) <= 5.f + 5.f * fminf(share, 2.f);
 }
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
