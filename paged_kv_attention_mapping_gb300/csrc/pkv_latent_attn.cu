@@ -35,10 +35,10 @@
 //            share no factor of 32 with a step): more loaders beside warp 0 and warp 2,
 //            taking groups in turn, since each waits for its own copies
 //
-// Work split: the tick's steps (all tiles, one after the other, each with START more for its
-// start and end) are cut into equal runs, one per pair. A tile cut by a run's end leaves partial results
-// (normalised output in fp32 and log2 sum) that latent_combine_kernel joins. Ticks of
-// short contexts are split by whole tiles instead.
+// Work split: the tick's steps (all tiles, one after the other, each with START more
+// for its start and end) are cut into equal runs, one per pair. A tile cut by a run's
+// end leaves partial results (normalised output in fp32 and log2 sum) that
+// latent_combine_kernel joins. Ticks of short contexts are split by whole tiles instead.
 //
 // Decode of 128 sequences of 512-8192 keys at 128 heads (bf16): 131 us, 5.1 TB/s and 1.18
 // PFLOP/s; with the combine 138 us. Two step slots fit beside Q, and a slot's turn (load,
@@ -158,7 +158,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
   extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char* sQ = sm;
   unsigned char* sK = sQ + C::Q_BYTES;               // [step][group][unit]
-  unsigned char* sX = sK + NST * C::ST_BYTES;        // unit 0: P, keys 0-63; unit 1 + st: rotary unit of step slot st, then P, keys 64-127
+  // unit 0: P, keys 0-63; unit 1 + st: rotary unit of step slot st, then P, keys 64-127
+  unsigned char* sX = sK + NST * C::ST_BYTES;
   using Sh = State<LD, NTHREADS>;
   Sh& sh = *reinterpret_cast<Sh*>(sX + C::X_BYTES);
   auto& bar_k = sh.k;

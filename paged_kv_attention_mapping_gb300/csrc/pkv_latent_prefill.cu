@@ -29,7 +29,8 @@
 //              halves. O is rescaled only when a row's maximum grows by more than 2^8.
 //
 // Where the tiles are at most half as many as the pairs of CTAs (short chunks, few
-// heads), each tile's keys are cut into parts, as many as there are pairs for; latent_prefill_combine_kernel joins their partial results.
+// heads), each tile's keys are cut into parts, as many as there are pairs for;
+// latent_prefill_combine_kernel joins their partial results.
 //
 // A plan kernel counts the tiles; where the call's sizes allow no more of them than pairs
 // of CTAs, each pair finds its own.

@@ -544,7 +544,8 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s
   static_assert(smem <= 232448, "shared memory");
   static std::atomic<uint64_t> ready{0};   // devices whose kernel attribute is set
   if (!(ready.load() >> a.dev.id & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(latent_rows_kernel<LD, T, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(latent_rows_kernel<LD, T, GATHER>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << a.dev.id);
   }
@@ -558,7 +559,8 @@ cudaError_t launch(const LatentAttnArgs& a, const LatentAttnP& p, cudaStream_t s
   cudaError_t e;
   {
     KernelTimer timer("latent_rows", s);
-    e = launch_after_trigger(latent_rows_kernel<LD, T, GATHER>, dim3(ctas), dim3(nthreads(GATHER)), smem, s, mx, (const T*)a.q, p);
+    e = launch_after_trigger(latent_rows_kernel<LD, T, GATHER>, dim3(ctas), dim3(nthreads(GATHER)), smem, s, mx,
+                             (const T*)a.q, p);
   }
   if (e != cudaSuccess || p.whole) return e;
   KernelTimer timer("latent_combine", s);
