@@ -224,14 +224,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
   if (warp == 1) tmem_alloc_pair(&s_tmem, TMEM_COLS);
   __syncwarp();
   cluster_arrive();     // the peer may use this CTA's barriers once every thread of both is here
+  // lengths, queries, cache rows and page tables may come from the kernel before
+  pdl_wait();
   latent_plan<BM, BN, START, NTHREADS>(p, pair, pairs, &sh.plan, s_seg);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   cluster_wait();
   const uint32_t tmem = s_tmem;
-  // queries, cache rows and page tables may come from the kernel before
-  pdl_wait();
   pdl_trigger();
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {

@@ -153,9 +153,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
                                                                           int32_t* order, int32_t* first,
                                                                           int32_t* dev_status) {
   __shared__ int s_cost[PLAN_THREADS], s_rank[PLAN_THREADS], s_scan[32], s_carry, s_all;
-  pdl_trigger();
+  pdl_trigger();   // (whatever starts now waits for this kernel's end)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nt = blockDim.x;
+  // The kernel before may have written the lengths, and an earlier call may still be
+  // reading the workspace, until here.
+  pdl_wait();
   const bool sorted = B <= nt;
   bool bad = tid == 0 && (__ldg(cu_q) != 0 || __ldg(cu_k) != 0 || __ldg(cu_q + B) > Tq || __ldg(cu_k + B) > Tk);
   for (int b = tid; b < B; b += nt)
@@ -194,7 +197,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_prefill_plan_kernel(const
     __syncthreads();
   }
   if (tid == 0) s_carry = 0;
-  pdl_wait();   // an earlier call may still be reading the workspace until here
   for (int base = 0; base < B; base += nt) {
     __syncthreads();
     const int carry = s_carry;
@@ -352,15 +354,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     tma_prefetch_desc(&mr);
   }
   if (warp == 1) tmem_alloc_pair(&s_tmem, TMEM_COLS);
-  Found found{0, 1, 0, 0};
-  // (reads only the lengths, which the kernel before does not write)
-  if (p.direct && warp == 0) found = find_item(p, blockIdx.x >> 1, gridDim.x >> 1);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   cluster_sync_all();   // the peer's barriers are ready too
   const uint32_t tmem = s_tmem;
-  pdl_wait();   // the plan, and whatever wrote the inputs
+  pdl_wait();   // the plan, and whatever wrote the inputs, the lengths among them
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
@@ -390,6 +389,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 
   if (warp == 0) {
     // --------------------------------------------------------------- producer
+    Found found{0, 1, 0, 0};
+    if (p.direct) found = find_item(p, blockIdx.x >> 1, gridDim.x >> 1);
     const int n_tiles = p.direct ? found.items : *(volatile const int32_t*)&p.ctrl[1];
     const int most_parts = p.direct ? found.parts : *(volatile const int32_t*)&p.ctrl[2];
     if (p.direct && p.rec && blockIdx.x == 0 && lane == 0) {   // for the join

@@ -154,9 +154,9 @@ __global__ void __launch_bounds__(nthreads(GATHER), 1)
     sh.bad[0] = 0;
     tma_prefetch_desc(&mx);
   }
+  pdl_wait();   // lengths, queries, cache rows and page tables may come from the kernel before
   latent_plan<TM, BN, START, NTHREADS>(p, blockIdx.x, gridDim.x, &sh.plan, sh.seg);
   __syncthreads();
-  pdl_wait();   // queries, cache rows and page tables may come from the kernel before
   pdl_trigger();
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {

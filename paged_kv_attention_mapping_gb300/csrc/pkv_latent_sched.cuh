@@ -139,9 +139,9 @@ struct LatentPlan {
   int b, tile, off;
 };
 
-// By all threads of a CTA: every CTA counts the whole tick's units and finds where
-// its own run starts. Reads only the lengths, so it may run before the wait for the
-// kernel before. One thread has set pl->run and first->valid to 0 before; the results,
+// By all threads of a CTA, after the wait for the kernel before, which may have written
+// the lengths: every CTA counts the whole tick's units and finds where its own run starts,
+// and LatentRun reads the same lengths again. One thread has set pl->run and first->valid to 0 before; the results,
 // the run's first segment among them, are visible after the caller's next block barrier.
 template <int TM, int BN, int START, int NTHREADS>
 __device__ __forceinline__ void latent_plan(const LatentAttnP& p, int worker, int workers, LatentPlan<NTHREADS>* pl,
