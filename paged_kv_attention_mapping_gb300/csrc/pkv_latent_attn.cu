@@ -141,7 +141,10 @@ struct State {
   uint64_t p;                         // P written
   uint64_t segfull[NSEG], segempty[NSEG], drain[2];
   LatentPlan<NTHREADS> plan;
-  float x[2][4][HM];                  // row figures of a row's four threads, by step parity
+  // row figures of a row's four threads: maxima by step parity, then the sums of a
+  // segment's end. (The first step of the next segment may write its maxima while a warp
+  // still reads the sums: the barrier between sits in that step, behind the write.)
+  float x[3][4][HM];
   LatentSegment seg[NSEG];
   int bad[NSEG];
   int abort;
@@ -621,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
       }
       if (!ok) break;
       // epilogue: the row's sum, then this thread's OC output columns
-      float (*sx)[HM] = s_x[n & 1];
+      float (*sx)[HM] = s_x[2];
       sx[who][i] = l_run;
       row_bar_sync(bar_id);
       const float l = (sx[0][i] + sx[1][i]) + (sx[2][i] + sx[3][i]);

@@ -364,6 +364,20 @@ def test_absorbed_leaves_padding_rows_and_unrequested_lse_alone(dev, ld, heads, 
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("ld,heads,seqs", [(512, 128, 300), (512, 40, 600), (256, 72, 500)])
+def test_absorbed_many_segments_of_one_step(dev, ld, heads, seqs):
+    """Workers with one segment of one step behind the other, where a row's sums are
+    exchanged right before the next tile's maxima: every call gives the same bits, and the right ones."""
+    t = Paged(dev, "bf16", ld, heads, 64, [1] * seqs, [1 + 7 * k % 128 for k in range(seqs)])
+    first = t.call()
+    for _ in range(20):
+        again = t.call()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert binding.device_status() == 0
+    t.check(*first)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("heads", [128, 12])
 def test_absorbed_same_call_same_bits(dev, heads):
     t = Paged(dev, "bf16", 512, heads, 64, [1, 1, 2], [3000, 50, 700])
