@@ -141,10 +141,7 @@ struct State {
   uint64_t p;                         // P written
   uint64_t segfull[NSEG], segempty[NSEG], drain[2];
   LatentPlan<NTHREADS> plan;
-  // row figures of a row's four threads: maxima by step parity, then the sums of a
-  // segment's end. (The first step of the next segment may write its maxima while a warp
-  // still reads the sums: the barrier between sits in that step, behind the write.)
-  float x[3][4][HM];
+  float x[2][4][HM];                  // row figures of a row's four threads, by exchange parity
   LatentSegment seg[NSEG];
   int bad[NSEG];
   int abort;
@@ -531,6 +528,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
     const uint32_t o_tmem = tmem + lrow + sub * OC;
     const float sc = p.scale_log2;
     uint32_t n = 0;                                  // steps before the current one
+    // Exchanges before the current one: a step's maxima, and a segment's sums, take the
+    // buffers in turn, so that a warp writes one only after every sibling's barrier behind its reads of it.
+    uint32_t n_x = 0;
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t % NSEG;
       if (!(ok = wait(&bar_seg[e], (t / NSEG) & 1))) break;
@@ -565,7 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
 #pragma unroll
         for (int k = 0; k < 32; k += 2)
           mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-        float (*sx)[HM] = s_x[n & 1];
+        float (*sx)[HM] = s_x[n_x++ & 1];
         sx[who][i] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         row_bar_sync(bar_id);
         const float mt = fmaxf(max3(sx[0][i], sx[1][i], sx[2][i]), sx[3][i]) * sc;
@@ -624,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
       }
       if (!ok) break;
       // epilogue: the row's sum, then this thread's OC output columns
-      float (*sx)[HM] = s_x[2];
+      float (*sx)[HM] = s_x[n_x++ & 1];
       sx[who][i] = l_run;
       row_bar_sync(bar_id);
       const float l = (sx[0][i] + sx[1][i]) + (sx[2][i] + sx[3][i]);
