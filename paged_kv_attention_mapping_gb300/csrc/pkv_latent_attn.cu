@@ -374,6 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
               }
             }
             cp_async_wait_all();
+            __syncwarp();   // other lanes' copies too: zeros go over rows that any lane copied
             if (tail) zero_rows(stage + k * C::G_BYTES, end);
             fence_proxy_async_smem();
             __syncwarp();

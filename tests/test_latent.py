@@ -378,6 +378,21 @@ def test_absorbed_many_segments_of_one_step(dev, ld, heads, seqs):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,ld,page", [("bf16", 512, 16), ("f16", 512, 1), ("bf16", 256, 24)])
+def test_absorbed_rows_behind_the_end_copied_by_threads(dev, dtype, ld, page):
+    """Small pages, ends at every place of a step: the NaN rows behind an end are copied
+    and then zeroed, whichever lane copied them."""
+    kv = [1 + 3 * k for k in range(86)] + [1025 + 11 * k for k in range(12)]
+    t = Paged(dev, dtype, ld, 64, page, [1] * len(kv), kv)
+    first = t.call()
+    for _ in range(10):
+        again = t.call()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert binding.device_status() == 0
+    t.check(*first)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("heads", [128, 12])
 def test_absorbed_same_call_same_bits(dev, heads):
     t = Paged(dev, "bf16", 512, heads, 64, [1, 1, 2], [3000, 50, 700])
