@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const uint4* 
                                                                    int32_t row_vecs, int64_t pool_slots,
                                                                    uint4* __restrict__ kc, uint4* __restrict__ vc,
                                                                    int32_t* dev_status) {
-  pdl_trigger();   // the attention call's plan does not read what this kernel writes
+  pdl_trigger();   // the attention call's plan waits for this grid's end before it writes
   const int span = sp.tpb * sp.per_token;
   for (int base = 0; base < span; base += APPEND_THREADS * APPEND_U) {
     uint4 x[APPEND_U];
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_quant_kernel(
     const T* __restrict__ k, const T* __restrict__ v, const int64_t* __restrict__ slots, TokenSpan sp,
     int32_t row_vecs, int32_t head_vecs, int64_t pool_slots, const float* __restrict__ k_scale,
     const float* __restrict__ v_scale, uint4* __restrict__ kc, uint4* __restrict__ vc, int32_t* dev_status) {
-  pdl_trigger();   // the attention call's plan does not read what this kernel writes
+  pdl_trigger();   // the attention call's plan waits for this grid's end before it writes
   const int span = sp.tpb * sp.per_token;
   for (int j = threadIdx.x; j < span; j += APPEND_THREADS) {
     int64_t t;

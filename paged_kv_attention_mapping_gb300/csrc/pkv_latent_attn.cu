@@ -282,7 +282,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
       if (!g.valid) break;
       if (t > 0) ok = load_q(t, g.row0);
     }
-    if (rank == 0 && lane == 0) ((LatentRecord*)(p.ws + Layout::rec))[pair] = run.r;
+    // (whole tiles leave nothing to join)
+    if (!p.whole && rank == 0 && lane == 0) ((LatentRecord*)(p.ws + Layout::rec))[pair] = run.r;
   } else if (warp == 0 || warp == 2 || (GATHER && warp > SCHED)) {
     // --------------------------------------------------------------- producers
     // Warp 0 loads this CTA's 64 keys of each step, warp 2 the peer's 64 keys of this

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(THREADS) latent_append_kernel(const T* __restr
                                                                 const T* q, T* q_out, T* __restrict__ cache,
                                                                 AppendP p) {
   pdl_wait();
-  pdl_trigger();   // what the attention call reads before its own wait is not written here, nor by a kernel before
+  pdl_trigger();   // what starts now waits for this grid's end before it writes, and before it relies on what it read
   const int64_t j = (int64_t)blockIdx.x * THREADS + threadIdx.x;
   if (j >= p.items) return;
   const int64_t t = j / p.per_token;

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(nthreads(GATHER), 1)
       __syncwarp();
       if (!g.valid) break;
     }
-    if (lane == 0) ((LatentRecord*)(p.ws + Layout::rec))[blockIdx.x] = run.r;
+    if (!p.whole && lane == 0) ((LatentRecord*)(p.ws + Layout::rec))[blockIdx.x] = run.r;
   } else if (warp > WARPS) {
     // --------------------------------------------------------------- producer
     // Lane l takes box l of a slot, or finds row l for the copies. Rows behind the end and bad pages are read from

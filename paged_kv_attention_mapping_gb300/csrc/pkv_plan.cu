@@ -73,7 +73,7 @@ __device__ __forceinline__ int upper_bound_written(const volatile int32_t* a, in
   return lo;
 }
 
-// Threads of the plan's one CTA. 512 (~33K registers) lets it start on an SM
+// Threads of the plan's one CTA. 512 (20K registers) lets it start on an SM
 // beside the append kernel's blocks (at most three per SM, ~31K), which it may
 // overlap; 1024 needed an SM with no append block left and started ~5 us later
 // on the mixed tick.
@@ -253,7 +253,7 @@ constexpr int PLAN_SMEM_SEQS = 6144;
 constexpr int PLAN_SMEM_WORDS = (3 + SEQ_OFFS) * PLAN_SMEM_SEQS + 2;
 
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PlanArgs a_in, int32_t* dev_status) {
-  // stage cu_seqlens_q and kv_lens in shared memory: every row below searches them
+  // cu_seqlens_q and kv_lens in shared memory: every row below searches them
   extern __shared__ int32_t s_seq[];
   // A decode kernel launched next may get resident now (it waits for this
   // grid). A prefill kernel launched next is let in only once the append before
@@ -261,13 +261,25 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PlanArgs a_in, int32
   // still needs.
   if (a_in.trigger_early) pdl_trigger();
   PlanArgs a = a_in;
+  // The kernel before this one (as a rule the append) may still run. Until the wait
+  // for it nothing is written to global memory, and the lengths, which that kernel
+  // may be writing, are read as a guess: once it is done they are read
+  // again, behind the plan's stores, and the plan is made anew should they differ.
+  // Mixed tick and TinyLlama-shaped tick, graph-replayed: 219.2 and 39.5 us; with the
+  // wait in front of everything 224.4 and 39.7; without the second reading 218.5 and 38.8.
+  // Lengths that do not fit in shared memory are read after the wait.
   const bool staged = a_in.B <= PLAN_SMEM_SEQS;
+  bool waited = !staged;
+  if (waited) pdl_wait();
+  auto stage = [&] {
+    for (int i = threadIdx.x; i <= a_in.B; i += blockDim.x) s_seq[i] = __ldcg(a_in.cu + i);
+    for (int i = threadIdx.x; i < a_in.B; i += blockDim.x) s_seq[a_in.B + 1 + i] = __ldcg(a_in.kv_lens + i);
+    __syncthreads();
+  };
   if (staged) {
-    for (int i = threadIdx.x; i <= a_in.B; i += blockDim.x) s_seq[i] = __ldg(a_in.cu + i);
-    for (int i = threadIdx.x; i < a_in.B; i += blockDim.x) s_seq[a_in.B + 1 + i] = __ldg(a_in.kv_lens + i);
     a.cu = s_seq;
     a.kv_lens = s_seq + a_in.B + 1;
-    __syncthreads();
+    stage();
   }
   int32_t* ctrl = (int32_t*)(a.ws + a.lay.ctrl);
   int32_t* rp_row = (int32_t*)(a.ws + a.lay.rp_row);
@@ -292,6 +304,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PlanArgs a_in, int32
   const int tid = threadIdx.x;
   const int B = a.B, Hkv = a.Hkv;
 
+  for (;;) {   // twice at most
   // pass 1: check every sequence; count the keys the row path will visit
   const bool ends_bad = a.cu[0] != 0 || a.cu[B] != a.T;
   int my_desc = 0;
@@ -379,38 +392,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PlanArgs a_in, int32
   __syncthreads();   // seq_off complete
   const int n_rp = carry[0], n_items = carry[1], carry_parts = carry[2], carry_split = carry[3];
 
-  // pass 2b: per row-path row j (consecutive rows on consecutive threads), its
-  // sequence by binary search over the sequences' first row-path rows (zero-row
-  // sequences share their successor's offset, so the last sequence whose offset
-  // is <= j owns j), then its arrays from the same closed forms
-  {
-    const unsigned Cu = 1u << c_shift;
-    for (int j = tid; j < n_rp; j += blockDim.x) {
-      int lo = 0, hi = B;   // first b with seq_off[SEQ_OFFS * b] > j
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (seq_off[SEQ_OFFS * mid] <= j) lo = mid + 1; else hi = mid;
-      }
-      const int b = lo - 1;
-      const SeqInfo s = seq_info(a, b, false);
-      const int i = j - seq_off[SEQ_OFFS * b];
-      const unsigned k_lo = (unsigned)(s.L - s.q + 1), k = k_lo + (unsigned)i;
-      rp_row[j] = s.c0 + i;
-      rp_seq[j] = b;
-      rp_keys[j] = (int)k;
-      rp_item_begin[j] = seq_off[SEQ_OFFS * b + 1] +
-                         (int)(ceil_div_prefix(k - 1, c_shift) - ceil_div_prefix(k_lo - 1, c_shift)) * Hkv;
-      int pb = -1;
-      if (k > Cu) {
-        const unsigned k_s = k_lo > Cu + 1 ? k_lo : Cu + 1;
-        pb = seq_off[SEQ_OFFS * b + 2] + (int)(ceil_div_prefix(k - 1, c_shift) - ceil_div_prefix(k_s - 1, c_shift)) * Hkv;
-        split_rows[seq_off[SEQ_OFFS * b + 3] + (int)(k - k_s)] = j;
-      }
-      rp_part_begin[j] = pb;
-    }
-  }
-  if (tid == 0) rp_item_begin[n_rp] = n_items;
-
   // pass 3: (sequence, q tile) pairs of the prefill kernel, longest first
   int carry_pairs = 0;
   for (int base = 0; any_tc && base < a.B; base += blockDim.x) {
@@ -438,12 +419,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PlanArgs a_in, int32
     *qt_out = qt;
     return (keys + TC_BN - 1) / TC_BN;
   };
-  if (n_pairs > 0 && n_pairs <= RANK_SORT_MAX) {   // block-uniform
+  const bool ranked = n_pairs <= RANK_SORT_MAX;   // block-uniform
+  int my_rank = 0, my_b = 0, my_qt = 0;           // of the pair that this thread stores
+  if (n_pairs > 0 && ranked) {
     // few pairs: thread p ranks pair p against all others (longer first, then
-    // lower index), two block barriers instead of the histogram's passes
-    int b = 0, qt = 0, w = 0;
+    // lower index), one block barrier instead of the histogram's passes
+    int w = 0;
     if (tid < n_pairs) {
-      w = pair_work(tid, &b, &qt);
+      w = pair_work(tid, &my_b, &my_qt);
       hist[tid] = w;
     }
     unsigned long long my_steps = (unsigned long long)w;
@@ -452,14 +435,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PlanArgs a_in, int32
     if ((tid & 31) == 0) s_wsteps[tid >> 5] = my_steps;
     __syncthreads();
     if (tid < n_pairs) {
-      int rank = 0;
       for (int q = 0; q < n_pairs; ++q) {
         const int wq = hist[q];
-        rank += (wq > w || (wq == w && q < tid)) ? 1 : 0;
+        my_rank += (wq > w || (wq == w && q < tid)) ? 1 : 0;
       }
-      pairs[rank] = make_int2(b, qt);
     }
-    __syncthreads();
   } else if (n_pairs > 0) {   // block-uniform
     for (int i = tid; i < HIST; i += blockDim.x) hist[i] = 0;
     __syncthreads();
@@ -492,13 +472,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PlanArgs a_in, int32
       }
     }
     __syncthreads();
-    for (int p = tid; p < n_pairs; p += blockDim.x) {
-      int b, qt;
-      const int w = min(pair_work(p, &b, &qt), HIST - 1);
-      const int pos = atomicAdd(&hist[w], 1);
-      pairs[pos] = make_int2(b, qt);
-    }
-    __syncthreads();
   }
   int pf_ctas = a.num_sms;
   if (tid < 32) {
@@ -506,6 +479,56 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PlanArgs a_in, int32
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, o);
     pf_ctas = prefill_ctas(a, n_pairs, steps, s_keys, tid);
+  }
+
+  // from here on the workspace is written
+  if (!waited) pdl_wait();
+  if (!a_in.trigger_early) pdl_trigger();
+  // the lengths as they are now, compared below (later ones are read there)
+  const int cu_now = !waited && tid <= B ? __ldcg(a_in.cu + tid) : 0;
+  const int len_now = !waited && tid < B ? __ldcg(a_in.kv_lens + tid) : 0;
+
+  // pass 2b: per row-path row j (consecutive rows on consecutive threads), its
+  // sequence by binary search over the sequences' first row-path rows (zero-row
+  // sequences share their successor's offset, so the last sequence whose offset
+  // is <= j owns j), then its arrays from the same closed forms
+  {
+    const unsigned Cu = 1u << c_shift;
+    for (int j = tid; j < n_rp; j += blockDim.x) {
+      int lo = 0, hi = B;   // first b with seq_off[SEQ_OFFS * b] > j
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (seq_off[SEQ_OFFS * mid] <= j) lo = mid + 1; else hi = mid;
+      }
+      const int b = lo - 1;
+      const SeqInfo s = seq_info(a, b, false);
+      const int i = j - seq_off[SEQ_OFFS * b];
+      const unsigned k_lo = (unsigned)(s.L - s.q + 1), k = k_lo + (unsigned)i;
+      rp_row[j] = s.c0 + i;
+      rp_seq[j] = b;
+      rp_keys[j] = (int)k;
+      rp_item_begin[j] = seq_off[SEQ_OFFS * b + 1] +
+                         (int)(ceil_div_prefix(k - 1, c_shift) - ceil_div_prefix(k_lo - 1, c_shift)) * Hkv;
+      int pb = -1;
+      if (k > Cu) {
+        const unsigned k_s = k_lo > Cu + 1 ? k_lo : Cu + 1;
+        pb = seq_off[SEQ_OFFS * b + 2] + (int)(ceil_div_prefix(k - 1, c_shift) - ceil_div_prefix(k_s - 1, c_shift)) * Hkv;
+        split_rows[seq_off[SEQ_OFFS * b + 3] + (int)(k - k_s)] = j;
+      }
+      rp_part_begin[j] = pb;
+    }
+  }
+  if (tid == 0) rp_item_begin[n_rp] = n_items;
+
+  if (ranked) {
+    if (tid < n_pairs) pairs[my_rank] = make_int2(my_b, my_qt);
+  } else {
+    for (int p = tid; p < n_pairs; p += blockDim.x) {
+      int b, qt;
+      const int w = min(pair_work(p, &b, &qt), HIST - 1);
+      const int pos = atomicAdd(&hist[w], 1);
+      pairs[pos] = make_int2(b, qt);
+    }
   }
   if (tid == 0) {
     ctrl[CTRL_PF_CTAS] = pf_ctas;
@@ -519,12 +542,16 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PlanArgs a_in, int32
     ctrl[CTRL_CHUNK] = (int)(1u << c_shift);
     ctrl[CTRL_N_SPLIT_ROWS] = carry_split;
     ctrl[CTRL_N_PARTIALS] = carry_parts;
-    if (s_err) atomicOr(dev_status, s_err);
   }
-  // This kernel may have started while the preceding kernel (the append) still
-  // ran; finishing only after it makes every later launch see the appended K/V.
-  pdl_wait();
-  pdl_trigger();
+  if (waited) break;
+  bool moved = (tid <= B && cu_now != s_seq[tid]) || (tid < B && len_now != s_seq[B + 1 + tid]);
+  for (int i = tid + blockDim.x; i <= B; i += blockDim.x) moved |= __ldcg(a_in.cu + i) != s_seq[i];
+  for (int i = tid + blockDim.x; i < B; i += blockDim.x) moved |= __ldcg(a_in.kv_lens + i) != s_seq[B + 1 + i];
+  if (!__syncthreads_or(moved)) break;
+  waited = true;
+  stage();
+  }
+  if (tid == 0 && s_err) atomicOr(dev_status, s_err);
 }
 
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s) {
@@ -535,7 +562,7 @@ cudaError_t launch_plan(const PlanArgs& a, cudaStream_t s) {
   if (carve != cudaSuccess) return carve;
   const size_t smem = a.B <= PLAN_SMEM_SEQS ? (size_t)((3 + SEQ_OFFS) * a.B + 2) * 4 : 0;
   KernelTimer timer("plan", s);
-  // may overlap the preceding append, which it does not read (see pdl_wait above)
+  // may overlap the preceding kernel (see pdl_wait above)
   cudaError_t e = launch_after_trigger(plan_kernel, dim3(1), dim3(PLAN_THREADS), smem, s, a, a.dev_status);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

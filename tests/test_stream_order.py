@@ -186,3 +186,113 @@ def test_a_captured_tick_that_counts_on(dev, dtype, ld, H, P):
         e.cu_q, e.cu_k = t.cu, np.concatenate([[0], np.cumsum(lens)])
         e.q, e.kn, e.v, e.kr = qe, up[..., :128], up[..., 128:], rows[:, ld:]
         e.check(*got["expanded"])
+
+
+def _decode_tick(dev, dtype, Hq, Hkv, d, P, q_lens, kv_lens, seed=0):
+    """Tensors of a paged K/V tick: q, caches, cu_seqlens_q, kv_lens, page tables."""
+    g = torch.Generator(device=dev).manual_seed(seed)
+    need = [-(-L // P) for L in kv_lens]
+    pages = sum(need) + 1
+    perm = np.random.default_rng(seed).permutation(pages).astype(np.int32)
+    table, at = np.zeros((len(need), max(need)), np.int32), 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    r = lambda *s: torch.randn(s, generator=g, device=dev).to(TYPES[dtype])
+    cu = np.concatenate([[0], np.cumsum(q_lens)])
+    return (r(int(cu[-1]), Hq, d), _i32(cu, dev), _i32(kv_lens, dev), _i32(table, dev), r(pages, P, Hkv, d),
+            r(pages, P, Hkv, d))
+
+
+PAGED = [
+    # dtype, query heads, KV heads, head_dim, page, q_lens, kv_lens
+    ("bf16", 32, 8, 128, 64, [1] * 6, [40, 900, 5000, 3, 77, 2100]),
+    ("bf16", 16, 4, 128, 16, [1] * 4 + [300, 40], [40, 900, 30, 70, 400, 40]),
+    ("f16", 8, 2, 64, 16, [1] * 700 + [9], [1 + 13 * k % 200 for k in range(700)] + [90]),
+    ("bf16", 4, 4, 64, 8, [64] * 300, [64 + k for k in range(300)]),               # more tiles than are ranked
+    ("bf16", 4, 4, 64, 8, [1] * 6200, [1 + k % 9 for k in range(6200)]),           # lengths not kept in shared memory
+    ("bf16", 8, 2, 256, 16, [1, 2, 1], [40, 600, 9]),
+]
+
+
+@pytest.mark.parametrize("case", PAGED, ids=lambda c: f"{c[0]}-h{c[1]}-d{c[3]}-n{len(c[5])}-k{max(c[6])}")
+def test_paged_lengths_from_the_kernel_before(dev, late_write, case):
+    dtype, Hq, Hkv, d, P, q_lens, kv_lens = case
+    q, cu, kv, tab, kc, vc = _decode_tick(dev, *case)
+    max_kv = max(kv_lens)
+    out, lse = binding.paged_attention(q, cu, kv, tab, kc, vc, 0.1, max_kv)
+    torch.cuda.synchronize()
+    n = len(q_lens)
+    ends = np.minimum(np.arange(n + 1), int(cu[-1]))
+    ends[-1] = int(cu[-1])
+    # lengths before: no sequence longer than its rows; all rows in one sequence; lengths that are refused
+    for late, stale in ((kv, _i32(q_lens, dev)), (cu, _i32(ends, dev)), (kv, torch.full_like(kv, -5)),
+                        (cu, torch.full_like(cu, 1 << 30))):
+        good = late.clone()
+        late.copy_(stale)
+        torch.cuda.synchronize()
+        late_write(late, good)
+        again = binding.paged_attention(q, cu, kv, tab, kc, vc, 0.1, max_kv)
+        assert binding.device_status() == 0
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("heads,kv_lens", [(64, [100, 64, 65, 300, 2]), (4, [60, 50, 40, 30, 20, 10])])
+def test_one_workspace_for_latent_and_paged_calls(dev, heads, kv_lens):
+    """Calls behind one another on a stream may share their workspace, and memory that a call
+    read may be the next one's workspace."""
+    t = Paged(dev, "bf16", 512, heads, 64, [1] * len(kv_lens), kv_lens)
+    want = t.call()
+    q, cu, kv, tab, kc, vc = _decode_tick(dev, "bf16", 16, 4, 128, 16, [1] * 4 + [300, 40], [40, 900, 30, 70, 400, 40])
+    paged = binding.paged_attention(q, cu, kv, tab, kc, vc, 0.1, 900)
+    chunk = Packed(dev, "bf16", 3, [40, 300], [400, 900])
+    expanded = chunk.call()
+    size = max(binding.workspace_size(6, 344, 16, kc, 900), t.q.nbytes,
+               binding.latent_workspace_size(len(kv_lens), t.total, heads, t.cache),
+               binding.latent_prefill_workspace_size(2, 340, 3))
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    args = _i32(t.cu, dev), _i32(t.kv_lens, dev), _i32(t.table, dev), t.cache, SCALE, max(kv_lens)
+    k = chunk.cu_q, chunk.cu_k
+    k = [_i32(x, dev) for x in k]
+    q_in_ws = ws[:t.q.nbytes].view(torch.bfloat16).view(t.q.shape)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got.append(binding.latent_attention(t.q, *args, workspace=ws) + want)
+        got.append(binding.paged_attention(q, cu, kv, tab, kc, vc, 0.1, 900, workspace=ws) + paged)
+        got.append(binding.latent_prefill(chunk.q, k[0], chunk.kn, chunk.v, chunk.kr, k[1], SCALE, workspace=ws)
+                   + expanded)
+        got.append(binding.paged_attention(q, cu, kv, tab, kc, vc, 0.1, 900, workspace=ws) + paged)
+        q_in_ws.copy_(t.q)                   # the queries lie where the next call's plan goes
+        got.append(binding.latent_attention(q_in_ws, *args) + want)
+        got.append(binding.paged_attention(q, cu, kv, tab, kc, vc, 0.1, 900, workspace=ws) + paged)
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0
+    for i, (out, lse, good, good_lse) in enumerate(got):
+        assert torch.equal(out, good) and torch.equal(lse, good_lse), i
+
+
+def test_appended_rows_may_lie_in_the_next_workspace(dev):
+    q, cu, kv, tab, kc, vc = _decode_tick(dev, "bf16", 16, 4, 128, 16, [1] * 4, [40, 900, 30, 70])
+    T = 6000
+    pool = torch.zeros((T // 16, 16, 4, 128), dtype=torch.bfloat16, device=dev)
+    pool_v = torch.zeros_like(pool)
+    rows = torch.randn((T, 4, 128), device=dev).to(torch.bfloat16)
+    slots = torch.arange(T, dtype=torch.int64, device=dev)
+    latents = rows.view(T, 512)
+    latent_pool = torch.zeros((T // 16, 16, 576), dtype=torch.bfloat16, device=dev)
+    table = torch.from_numpy(binding.rope_table(10000.0, 64, 16)).to(dev)
+    pos, kr = torch.zeros(T, dtype=torch.int32, device=dev), rows[:, 0, :64]
+    want = binding.paged_attention(q, cu, kv, tab, kc, vc, 0.1, 900)
+    ws = torch.empty(max(rows.nbytes, binding.workspace_size(4, 4, 16, kc, 900)), dtype=torch.uint8, device=dev)
+    src = ws[:rows.nbytes].view(torch.bfloat16).view(rows.shape)
+    for latent in (False, True):
+        src.copy_(rows)
+        if latent:
+            binding.latent_append(src.view(T, 512), kr, pos, table, slots, latent_pool)
+        else:
+            binding.kv_append(src, rows, slots, pool, pool_v)
+        got = binding.paged_attention(q, cu, kv, tab, kc, vc, 0.1, 900, workspace=ws)
+        assert binding.device_status() == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(pool.view(T, 4, 128), rows) and torch.equal(latent_pool.view(T, 576)[:, :512], latents)
