@@ -25,6 +25,17 @@ __device__ __forceinline__ void st_global_32B(void* p, const uint32_t* w) {
                : "memory");
 }
 
+// Softmax weights are rounded to the cache type T for their product with the values: a
+// relative half step. fp16 has no more than half a step of 2^-24 below 2^-14 though, and many
+// small weights beside a large one would be lost in O but not in the row's sum. So weights and sums
+// carry a factor 2^SHIFT, near fp16's range: a weight of 2^-w of the row's scale stays normal
+// up to w = 14 + SHIFT. It cancels in O / l; a log sum gives it back. `most`: log2 of the
+// largest weight without it (7 of 15 bits are left where a row's scale may lag by 2^8).
+template <typename T>
+__device__ __forceinline__ constexpr float weight_shift(float most) {
+  return std::is_same<T, __nv_bfloat16>::value ? 0.f : 15.f - most;
+}
+
 // Two fp32 values rounded to the 16-bit type T, the first in the low half.
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {

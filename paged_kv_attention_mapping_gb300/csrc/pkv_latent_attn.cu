@@ -527,6 +527,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
     const int bar_id = 1 + (quarter & 1);           // the four warps of the same rows
     const uint32_t p_bar = map_to_rank(&bar_p, 0), sfree_bar = map_to_rank(bar_sfree, 0);
     constexpr int OC = LD / 4;                      // output columns of a thread
+    constexpr float SHIFT = weight_shift<T>(RESCALE_LOG2);
     const uint32_t o_tmem = tmem + lrow + sub * OC;
     const float sc = p.scale_log2;
     uint32_t n = 0;                                  // steps before the current one
@@ -577,7 +578,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
         const float alpha = grow && !first ? ex2(m_run - m_new) : 1.f;
         const bool rescale = !first && __any_sync(0xffffffffu, grow);
         // a row that sees no key of this run so far has m = -inf: its weights are 0
-        const float nm = m_new == -INFINITY ? 0.f : -m_new;
+        const float nm = m_new == -INFINITY ? 0.f : SHIFT - m_new;
         const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
         float2 ls[4];
 #pragma unroll
@@ -668,7 +669,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
         }
       }
       if (store && who == 0) {
-        const float lg = l == 0.f ? -INFINITY : m_run + __log2f(l);   // (NaN scores: m may be -inf, l is NaN)
+        const float lg = l == 0.f ? -INFINITY : m_run + (__log2f(l) - SHIFT);   // (NaN scores: m may be -inf, l is NaN)
         if (!whole) ((float*)(p.ws + Layout::lse))[slot * BM + r] = lg;
         else if (p.lse) p.lse[row] = lg * LN2;
       }

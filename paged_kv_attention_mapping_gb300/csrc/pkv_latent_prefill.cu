@@ -656,6 +656,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const uint32_t s_col = w * 128, o_col = 256 + w * 128;
     const uint32_t p_bar = map_to_rank(bar_p[w], 0);
     const float sc = p.scale_log2;
+    constexpr float SHIFT = weight_shift<T>(RESCALE_LOG2);
     uint32_t n_s = 0, n_o = 0;                    // S and O hand-offs taken
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t & 1;
@@ -723,7 +724,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
           m_run = m_new;
           // a row that sees no key of this part so far has m = -inf: its weights are 0
-          const float nm = m_run == -INFINITY ? 0.f : -m_run;
+          const float nm = m_run == -INFINITY ? 0.f : SHIFT - m_run;
           const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
           float2 ls[4];
 #pragma unroll
@@ -792,7 +793,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                   make_uint4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
           }
         }
-        const float lg = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);   // (NaN scores: m may be -inf, l_run is NaN)
+        const float lg = l_run == 0.f ? -INFINITY : m_run + (__log2f(l_run) - SHIFT);   // (NaN scores: m may be -inf, l_run is NaN)
         if (store && !whole) p.part_lse[prow] = lg;
         else if (store && p.lse) p.lse[row] = lg * LN2;
         tc_fence_before();

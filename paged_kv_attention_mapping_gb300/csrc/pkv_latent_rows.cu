@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(nthreads(GATHER), 1)
     const int d0 = warp * C::DW;                        // this warp's output columns
     const uint32_t v_unit = (d0 / 64) * UNIT, v_chunk = (d0 % 64) / 8;
     const float sc = p.scale_log2;
+    constexpr float SHIFT = weight_shift<T>(0.f);       // (a row's scale is its maximum so far)
     uint32_t h = 0;   // ring slots before the current step
     for (uint32_t t = 0;; ++t) {
       const uint32_t e = t % NSEG;
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(nthreads(GATHER), 1)
           for (int b = 1; b < 16; b <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, b));
           const float m_new = fmaxf(m_run, mt * sc);
           // a row that sees no key of this run so far has m = -inf: its weights are 0
-          const float nm = m_new == -INFINITY ? 0.f : -m_new;
+          const float nm = m_new == -INFINITY ? 0.f : SHIFT - m_new;
           const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run - m_new);
           m_run = m_new;
           const float a = ex2(fmaf(x.x, sc, nm)), b = ex2(fmaf(x.y, sc, nm)), c = ex2(fmaf(x.z, sc, nm)),
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(nthreads(GATHER), 1)
       }
       if (tid < TM && tid < g.nrows) {
         const float l = sh.l[tid];
-        const float lg = l == 0.f ? -INFINITY : sh.m[tid] + __log2f(l);   // (NaN scores: m may be -inf, l is NaN)
+        const float lg = l == 0.f ? -INFINITY : sh.m[tid] + (__log2f(l) - SHIFT);   // (NaN scores: m may be -inf, l is NaN)
         if (!whole) ((float*)(p.ws + Layout::lse))[slot * TM + tid] = lg;
         else if (p.lse && !bad) p.lse[(int64_t)g.row0 + tid] = lg * LN2;
       }

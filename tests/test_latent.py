@@ -779,6 +779,64 @@ def test_a_tick_through_both_forms(dev, dtype, ld, H, P):
         assert (np.abs(got[at] - want) <= u * (4 * dot[..., None] * mass + 3 * vmass)).all(), b
 
 
+def _sink(t, kv, weight):
+    """Keys of the row's own sequence that share `weight` of a first key that has nearly all
+    of the softmax: 2^weight each. Returns the query and key entry that does it: q k = that score."""
+    score = -weight * math.log(2.0) / SCALE
+    return 16.0, score / 16.0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv", [(40, 40000), (8, 40000), (40, 500), (8, 300)])
+def test_absorbed_small_f16_weights_are_not_lost(dev, heads, kv):
+    """A first key with nearly all of the weight, and the values in the others'. A weight's
+    rounding is half a step where it is normal, and 2^-25 of a unit that is 2^-7 of
+    the row's weight scale or less where it is not: 2^-32 max|v| a key."""
+    t = Paged(dev, "f16", 256, heads, 64, [1], [kv])
+    qv, kx = _sink(t, kv, -25.2)
+    t.q.zero_()
+    t.q[..., -1] = qv
+    rows = t.cache.view(-1, 320)
+    at = torch.from_numpy((t.table[0, np.arange(kv) // 64].astype(np.int64) * 64 + np.arange(kv) % 64)).to(dev)
+    rows[at, -64:] = 0
+    rows[at[0]] = 0
+    rows[at[0], -1] = kx
+    rows[at[1:], :256] = rows[at[1:], :256].abs()
+    out, lse = t.call()
+    assert binding.device_status() == 0
+    own = O.gather_sequence(_host(t.cache), t.table[0], kv)
+    o, l, (mass, dot) = O.attend_absorbed(_host(t.q), own, SCALE)
+    u = HALF_STEP["f16"]
+    ds = 320 * 2.0 ** -23 * dot[..., None]
+    tol = u * np.abs(o) + (u + 2 * ds + (kv + 64) * 2.0 ** -23 + 2.0 ** -20) * mass + kv * 2.0 ** -32 * np.abs(own).max()
+    tol = tol * (1 + u) + 2.0 ** -25                  # (results this small are subnormal themselves)
+    assert (np.abs(_host(out) - o) <= tol).all(), (np.abs(_host(out) - o).max(), tol.min(), np.abs(o).max())
+    assert np.abs(_host(lse) - l).max() <= ds.max() + (kv + 64) * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * np.abs(l).max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,q_len,kv", [(1, 3, 40000), (2, 300, 900), (90, 257, 700)])
+def test_expanded_small_f16_weights_are_not_lost(dev, heads, q_len, kv):
+    """As test_absorbed_small_f16_weights_are_not_lost."""
+    t = Packed(dev, "f16", heads, [q_len], [kv], strided=False)
+    qv, kx = _sink(t, kv, -25.2)
+    t.q.zero_()
+    t.q[..., -1] = qv
+    t.kr.zero_()
+    t.kr[0, -1] = kx
+    t.v[0] = 0
+    t.v.abs_()
+    out, lse = t.call()
+    assert binding.device_status() == 0
+    o, l, (mass, dot) = O.attend_expanded(_host(t.q), _host(t.kn), _host(t.v), _host(t.kr), SCALE)
+    u = HALF_STEP["f16"]
+    ds = 192 * 2.0 ** -23 * dot[..., None]
+    tol = (u * np.abs(o) + (u + 2 * ds + (kv + 64) * 2.0 ** -23 + 2.0 ** -20) * mass
+           + kv * 2.0 ** -32 * float(t.v.abs().max())) * (1 + u) + 2.0 ** -25
+    assert (np.abs(_host(out) - o) <= tol).all(), (np.abs(_host(out) - o).max(), tol.min(), np.abs(o).max())
+    assert np.abs(_host(lse) - l).max() <= ds.max() + (kv + 64) * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -22 * np.abs(l).max()
+
+
 @pytest.mark.gpu
 def test_graphs_replay_with_new_lengths_and_side_by_side(dev):
     """One captured decode tick serves new lengths and tables; two captured graphs
