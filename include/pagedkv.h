@@ -461,10 +461,10 @@ int pkv_latent_gather(const void* cache, const pkv_latent_desc* desc, const int3
  * Bad lengths skip the sequence's rows as in pkv_paged_attention (bad
  * cu_seqlens_q: every row). A page id outside the pool sets PKV_DEV_BAD_PAGE, and the
  * rows that need the page, with up to 127 (token, head) rows of the sequence beside
- * them, are left unwritten. Slots that no sequence owns may hold anything. A NaN or an
- * infinity in a sequence's own row reaches every row that sees it, and may reach
- * earlier rows of the same chunk (0 * NaN, as in a product with a masked weight
- * matrix). num_q_heads is at most 4096.
+ * them, are left unwritten. Slots that no sequence owns may hold anything. A NaN in
+ * a sequence's own row reaches every row that sees it, and a NaN or an infinity may
+ * reach earlier rows of the same chunk (0 * NaN, as in a product with a masked weight
+ * matrix). A row all of whose scores are -inf is NaN, with an lse of -inf. num_q_heads is at most 4096.
  * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_WORKSPACE, PKV_E_DEVICE, PKV_E_CUDA. */
 size_t pkv_latent_attention_workspace_size(int32_t num_seqs, int32_t total_q, int32_t num_q_heads,
                                            const pkv_latent_desc* desc);
@@ -495,8 +495,9 @@ int pkv_latent_attention(const void* q, const int32_t* cu_seqlens_q, const int32
  * PKV_DEV_BAD_LENGTHS and is skipped; a cu_seqlens array that breaks the rules
  * above skips every row. Strides are in elements, multiples of 8; pointers
  * 16-byte aligned. Values of other sequences' rows never reach a row, NaN or not; a
- * NaN or an infinity in a sequence's own key or value reaches every row that sees
- * it, and may reach earlier rows of the same chunk (0 * NaN). Calls of few tiles
+ * NaN in a sequence's own key or value reaches every row that sees it, and a NaN or
+ * an infinity may reach earlier rows of the same chunk (0 * NaN). A row all of whose
+ * scores are -inf is NaN, with an lse of -inf. Calls of few tiles
  * split their keys over the GPU by the tick's total work: the order of a row's
  * fp32 sums then depends on the other rows (the same call gives the same bits).
  * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_WORKSPACE, PKV_E_DEVICE, PKV_E_CUDA. */

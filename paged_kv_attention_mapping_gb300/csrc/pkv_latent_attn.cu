@@ -637,7 +637,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
       const bool whole = g.j0 == 0 && g.j1 == g.n;
       const bool store = r < g.nrows && !(whole && bad);
       const int slot = 2 * pair + (g.j0 == 0 ? 1 : 0);
-      const float inv = l == 0.f ? 0.f : 1.f / l;   // no visible key in a partial run: zeros
+      // No visible key in a partial run: zeros. A whole tile's row always sees keys; where
+      // all their scores are -inf it becomes NaN, as the formula has it.
+      const float inv = l == 0.f && !whole ? 0.f : 1.f / l;
       const int64_t row = (int64_t)g.row0 + r;
       T* dst = (T*)p.out + row * LD + half * (LD / 2) + sub * OC;
       float4* part = (float4*)(p.ws + Layout::o) + Layout::vec(LD, slot, rank, sub * (OC / 4), quarter * 32 + lane);
@@ -746,6 +748,7 @@ __device__ __forceinline__ void latent_join(const LatentRecord& rec, char* ws, T
   for (int k = 0; k < K; ++k) {
     m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 8));
     m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 16));
+    if (m[k] == -INFINITY) m[k] = 0.f;   // all scores -inf: weights 0, a result of NaN, a log sum of -inf
   }
   for (int s = 0; s < rec.parts; s += U) {
     float w[U][K];

@@ -761,7 +761,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         tc_fence_after();
         const bool store = i < ti.nr[w];
         const bool whole = ti.parts == 1;
-        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;   // no visible key in a part: zeros
+        // No visible key in a part: zeros. A whole tile's row always sees keys; where all
+        // their scores are -inf it becomes NaN, as the formula has it.
+        const float inv = l_run == 0.f && !whole ? 0.f : 1.f / l_run;
         const int64_t row = (int64_t)(ti.row0[w] + i) * p.H + ti.h[w];
         const int prow = (ti.item0 + ti.part) * ROWS + w * QM + i;
         float4* part = p.part_o + part_vec(ti.item0 + ti.part, w * QM + i, 0);
@@ -837,6 +839,7 @@ __global__ void __launch_bounds__(CROWS * DV / 4) latent_prefill_combine_kernel(
     while (part_begin(n, parts - 1, ti.parts) >= ti.n[w]) --parts;
     float m = -INFINITY;
     for (int s = 0; s < parts; ++s) m = fmaxf(m, p.part_lse[(ti.item0 + s) * ROWS + r]);
+    if (m == -INFINITY) m = 0.f;   // all scores -inf: weights 0, a result of NaN, a log sum of -inf
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f;
 #pragma unroll 4

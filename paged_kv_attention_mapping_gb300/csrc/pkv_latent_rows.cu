@@ -429,8 +429,9 @@ __global__ void __launch_bounds__(nthreads(GATHER), 1)
       for (int x = 0; x < 2; ++x) {
         const int r = fr + x * 8;
         if (r >= g.nrows || (whole && bad)) continue;
-        // no visible key in a partial run: zeros
-        const float inv = sh.l[r] == 0.f ? 0.f : 1.f / sh.l[r];
+        // No visible key in a partial run: zeros. A whole tile's row always sees keys; where
+        // all their scores are -inf it becomes NaN, as the formula has it.
+        const float inv = sh.l[r] == 0.f && !whole ? 0.f : 1.f / sh.l[r];
         const int64_t row = (int64_t)g.row0 + r;
         T* dst = (T*)p.out + row * LD + d0 + fc;
         float* part = (float*)(p.ws + Layout::o) + ((int64_t)slot * TM + r) * LD + d0 + fc;
@@ -502,6 +503,7 @@ __global__ void __launch_bounds__(CTHREADS) latent_rows_combine_kernel(char* ws,
     }
     if (__any_sync(0xffffffffu, any)) return;   // (every warp looked at every part)
     m = warp_max(m);
+    if (m == -INFINITY) m = 0.f;   // all scores -inf: weights 0, a result of NaN, a log sum of -inf
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f;
     for (int s = pg; s < rec.parts;) {

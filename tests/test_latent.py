@@ -838,6 +838,35 @@ def test_expanded_small_f16_weights_are_not_lost(dev, heads, q_len, kv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv", [(40, 1), (40, 300), (40, 9000), (4, 1), (4, 50), (4, 9000)])
+def test_absorbed_rows_whose_scores_are_all_minus_infinity(dev, heads, kv):
+    """As the formula has it: the softmax of such a row is NaN, its log sum -inf; cut tiles or not."""
+    t = Paged(dev, "bf16", 256, heads, 64, [1, 1], [kv, kv])
+    t.q[..., -1] = 1.0
+    good = t.call()
+    at = t.table[0, np.arange(kv) // 64].astype(np.int64) * 64 + np.arange(kv) % 64
+    t.cache.view(-1, 320)[torch.from_numpy(at).to(dev), -1] = -math.inf
+    out, lse = t.call()
+    assert binding.device_status() == 0
+    assert out[0].isnan().all() and (lse[0] == -math.inf).all()
+    assert torch.equal(out[1], good[0][1]) and torch.equal(lse[1], good[1][1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv", [(2, 4), (2, 300), (3, 6000), (90, 300)])
+def test_expanded_rows_whose_scores_are_all_minus_infinity(dev, heads, kv):
+    """As test_absorbed_rows_whose_scores_are_all_minus_infinity."""
+    t = Packed(dev, "bf16", heads, [3, 2], [kv, kv])
+    t.q[..., -1] = 1.0
+    good = t.call()
+    t.kr[:kv, -1] = -math.inf
+    out, lse = t.call()
+    assert binding.device_status() == 0
+    assert out[:3].isnan().all() and (lse[:3] == -math.inf).all()
+    assert torch.equal(out[3:], good[0][3:]) and torch.equal(lse[3:], good[1][3:])
+
+
+@pytest.mark.gpu
 def test_graphs_replay_with_new_lengths_and_side_by_side(dev):
     """One captured decode tick serves new lengths and tables; two captured graphs
     with a workspace each give their results when replayed on two streams at once."""
