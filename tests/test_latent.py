@@ -779,6 +779,81 @@ def test_a_tick_through_both_forms(dev, dtype, ld, H, P):
         assert (np.abs(got[at] - want) <= u * (4 * dot[..., None] * mass + 3 * vmass)).all(), b
 
 
+def _rel(got, want):
+    return np.linalg.norm(np.asarray(got, np.float64) - want) / np.linalg.norm(want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,ld,H,P", [("bf16", 512, 16, 64), ("f16", 256, 5, 24), ("bf16", 256, 128, 16)])
+def test_every_stage_of_a_tick_on_what_it_read(dev, dtype, ld, H, P):
+    """Append, gather, both attention forms, each against 64 bits on the tensors that it
+    read, so that the bounds of one call apply; and both forms of the same rows against one another.
+
+    The forms differ by roundings of half a step at most, uniform in +-u: root mean square
+    u / sqrt(3) each, of the keys or the absorbed queries (through the scores, whose
+    products then weigh 0.8 and less), the values, the weights, and the results before and after the
+    value projection. Eight of them make 8 ** 0.5 u / 3 ** 0.5 = 1.6 u of relative error in the
+    2-norm; 4 u leaves a factor of 2.5. Results of a wrong page, position or head are off by more than 0.2."""
+    g = np.random.default_rng(11)
+    r = lambda *s, k=1.0: torch.from_numpy((k * g.standard_normal(s)).astype(np.float32)).to(dev, TYPES[dtype])
+    kv, ql = [90, 137, 200], [1, 2, 70]
+    need = [-(-L // P) for L in kv]
+    perm = list(map(int, g.permutation(sum(need) + 2)))
+    ends = np.cumsum([0] + need)
+    pages = [perm[ends[b]:ends[b + 1]] for b in range(3)]
+    pk = binding.pack_tick(ql, kv, pages, P, sum(need) + 2)
+    T, cu, tables = sum(ql), pk["cu_seqlens_q"], pk["page_tables"]
+    assert list(pk["kv_lens"]) == kv
+    cache = r(sum(need) + 2, P, ld + 64)
+    c, kr, q = r(T, ld), r(T, 64), r(T, H, 192)
+    wk, wv = r(H, ld, 128, k=ld ** -0.5), r(H, ld, 128, k=ld ** -0.5)
+    table = torch.from_numpy(binding.rope_table(10000.0, 64, 256)).to(dev)
+    pos = binding.tick_positions(cu, pk["kv_lens"])
+    before, q_before = _host(cache), _host(q)
+    binding.latent_append(c, kr, _i32(pos, dev), table, torch.from_numpy(pk["slot_mapping"]).to(dev), cache,
+                          q_rope=q[..., 128:], q_out=q[..., 128:])
+    u = HALF_STEP[dtype]
+    want = O.append(before, _host(c), _host(kr), pos, pk["slot_mapping"], 10000.0)
+    after = _host(cache)
+    assert np.array_equal(after[..., :ld], want[..., :ld])
+    turned = want[..., ld:].reshape(-1, 64)
+    pair = lambda x: np.concatenate([np.abs(x[..., :32]) + np.abs(x[..., 32:])] * 2, -1)
+    near = lambda a, b: (np.abs(a - b) <= u * np.abs(b) + 2.0 ** -22 * pair(b) + 2.0 ** -25).all()
+    assert near(after[..., ld:].reshape(-1, 64), turned)
+    turned_q = apply_rope(q_before[..., 128:], pos, 10000.0)
+    assert near(_host(q)[..., 128:], turned_q) and np.array_equal(_host(q)[..., :128], q_before[..., :128])
+    assert not near(_host(q)[..., 128:], q_before[..., 128:])
+
+    total = sum(kv)
+    cu_k = _cum(kv)
+    rows = binding.latent_gather(cache, _i32(tables, dev), _i32(cu_k, dev), total)
+    packed = np.concatenate([O.gather_sequence(after, tables[b], kv[b]) for b in range(3)])
+    assert np.array_equal(_host(rows), packed)
+
+    up = torch.einsum("lc,hcd->lhd", rows[:, :ld], torch.cat([wk, wv], -1))
+    e, e_lse = binding.latent_prefill(q, _i32(cu, dev), up[..., :128], up[..., 128:], rows[:, ld:], _i32(cu_k, dev), SCALE)
+    qa = torch.cat([torch.einsum("nhd,hcd->nhc", q[..., :128], wk), q[..., 128:]], -1).contiguous()
+    a, a_lse = binding.latent_attention(qa, _i32(cu, dev), _i32(kv, dev), _i32(tables, dev), cache, SCALE, max(kv))
+    assert binding.device_status() == 0
+    q64, up64, qa64 = _host(q), _host(up), _host(qa)
+    for b in range(3):
+        at, k = slice(int(cu[b]), int(cu[b + 1])), slice(int(cu_k[b]), int(cu_k[b + 1]))
+        own = packed[k]
+        for got, got_lse, (o, l, spread), D, v in (
+                (e, e_lse, O.attend_expanded(q64[at], up64[k, :, :128], up64[k, :, 128:], own[:, ld:], SCALE), 192, up64[k]),
+                (a, a_lse, O.attend_absorbed(qa64[at], own, SCALE), ld + 64, own)):
+            tol, tol_lse = _bounds(dtype, D, kv[b], o, l, spread, np.abs(v).max())
+            assert (np.abs(_host(got)[at] - o) <= tol).all() and (np.abs(_host(got_lse)[at] - l) <= tol_lse).all(), b
+            assert not (np.abs(o) <= tol).mean() > 0.5, b                    # zeros would not pass
+        projected = _host(torch.einsum("nhc,hcd->nhd", a[at], wv))
+        assert _rel(projected, _host(e)[at]) < 4 * u, (b, _rel(projected, _host(e)[at]) / u)
+        # what a wrong page, an unturned query or a head out of place would give is far off
+        other = packed[slice(int(cu_k[(b + 1) % 3]), int(cu_k[(b + 1) % 3 + 1]))][:kv[b]]
+        wrong = np.concatenate([other, own[len(other):]])
+        assert _rel(_host(a)[at], O.attend_absorbed(qa64[at], wrong, SCALE)[0]) > 0.2
+        assert _rel(_host(a)[at], O.attend_absorbed(qa64[at][:, ::-1], own, SCALE)[0]) > 0.2
+
+
 def _sink(t, kv, weight):
     """Keys of the row's own sequence that share `weight` of a first key that has nearly all
     of the softmax: 2^weight each. Returns the query and key entry that does it: q k = that score."""
@@ -864,6 +939,24 @@ def test_expanded_rows_whose_scores_are_all_minus_infinity(dev, heads, kv):
     assert binding.device_status() == 0
     assert out[:3].isnan().all() and (lse[:3] == -math.inf).all()
     assert torch.equal(out[3:], good[0][3:]) and torch.equal(lse[3:], good[1][3:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,H", [("bf16", 2), ("f16", 1)])
+def test_expanded_more_sequences_than_the_plan_sorts(dev, dtype, H):
+    """2100 sequences of 0-3 rows, empty ones between them, one long chunk and one sequence
+    with fewer keys than rows behind the first thousand."""
+    q_lens = [k % 4 for k in range(2100)]
+    kv_lens = [q + 7 * k % 30 for k, q in enumerate(q_lens)]
+    q_lens[1500], kv_lens[1500] = 300, 700
+    q_lens[1201], kv_lens[1201] = 3, 2
+    t = Packed(dev, dtype, H, q_lens, kv_lens)
+    out, lse = torch.full((t.Tq, H, 128), 9.0, dtype=TYPES[dtype], device=dev), torch.full((t.Tq, H), 9.0, device=dev)
+    t.call(out=out, lse=lse)
+    assert binding.device_status() == binding.DEV_BAD_LENGTHS
+    rows = slice(int(t.cu_q[1201]), int(t.cu_q[1202]))
+    assert (out[rows] == 9).all() and (lse[rows] == 9).all()
+    t.check(out, lse, only=set(range(2100)) - {1201})
 
 
 @pytest.mark.gpu
