@@ -42,8 +42,8 @@ def _visible(n, L):
 
 
 def _spread(q, k, w, v, scale):
-    """What the error bounds need of each row: sum_j |w_j v_j|, the largest
-    scale * sum_d |q_d k_d| over its keys, and sum_j |v_j| over them."""
+    """What the error bounds need of each row: sum_j |w_j v_j|, and the largest
+    scale * sum_d |q_d k_d| over its keys."""
     return (np.einsum("hnl,hld->nhd", w, np.abs(v)), scale * (np.abs(q) @ np.abs(k).transpose(0, 2, 1)).max(-1).T)
 
 
