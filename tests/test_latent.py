@@ -1088,3 +1088,31 @@ def test_calls_on_a_stream_argument(dev):
     s.synchronize()
     t.check(*a)
     c.check(*b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ld", [256, 512])
+def test_absorbed_at_the_ends_of_the_ranges(dev, ld):
+    """A pool of one slot; 4096 heads; thousands of sequences, most of them without rows."""
+    for heads in (1, 4, 40):
+        t = Paged(dev, "bf16", ld, heads, 1, [1], [1])
+        t.cache, t.table = t.cache[int(t.table[0, 0]):][:1].contiguous(), np.zeros((1, 1), np.int32)
+        out, lse = t.call()
+        assert binding.device_status() == 0
+        t.check(out, lse)
+    t = Paged(dev, "f16", ld, 4096, 16, [2, 1], [70, 9])
+    t.check(*t.call())
+    lens = [1 + 5 * k % 90 for k in range(5000)]
+    for heads, every in ((40, 7), (4, 3)):
+        q_lens = [int(k % every == 0) for k in range(5000)]
+        t = Paged(dev, "bf16", ld, heads, 16, q_lens, lens)
+        t.check(*t.call())
+    assert binding.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_expanded_at_the_ends_of_the_ranges(dev):
+    for heads, q_lens, kv_lens in ((4096, [3, 1], [40, 200]), (1, [1], [1]), (4095, [1], [130])):
+        t = Packed(dev, "bf16", heads, q_lens, kv_lens)
+        t.check(*t.call())
+    assert binding.device_status() == 0
