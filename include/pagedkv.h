@@ -452,8 +452,9 @@ int pkv_latent_gather(const void* cache, const pkv_latent_desc* desc, const int3
  *   scale         > 0 and finite; multiplies q . [c, r] before the softmax
  *   out           device, contiguous [total_q, num_q_heads, latent_dim], cache dtype
  *   workspace     device, >= pkv_latent_attention_workspace_size(...) bytes, 256-byte
- *                 aligned; needs no initialisation. Calls that may overlap (two streams, two
- *                 captured graphs replayed side by side) need one each.
+ *                 aligned; needs no initialisation; one for the largest call serves smaller
+ *                 ones. Calls that may overlap (two streams, two captured graphs replayed
+ *                 side by side) need one each.
  * Sums and softmax statistics are fp32; the softmax weights are rounded to the
  * cache dtype for the products with the latent parts. Keys of a sequence are
  * split over the GPU by the tick's total work, so the order of a row's fp32 sums
@@ -489,7 +490,8 @@ int pkv_latent_attention(const void* q, const int32_t* cu_seqlens_q, const int32
  *   out           device, contiguous [total_q, num_heads, 128]
  *   lse           device, fp32 [total_q, num_heads] or NULL
  *   workspace     device, >= pkv_latent_prefill_workspace_size(...) bytes, 256-byte aligned;
- *                 needs no initialisation; one for each of calls that may overlap
+ *                 needs no initialisation; one for the largest call serves smaller ones;
+ *                 one for each of calls that may overlap
  * Sequence b has kv_len = cu_k[b+1] - cu_k[b] >= q_len keys; the last q_len of
  * them are the chunk's own. A sequence with rows and fewer keys than rows sets
  * PKV_DEV_BAD_LENGTHS and is skipped; a cu_seqlens array that breaks the rules

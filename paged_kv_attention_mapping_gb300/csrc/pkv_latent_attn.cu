@@ -866,6 +866,8 @@ cudaError_t launch_either(const LatentAttnArgs& a, const LatentAttnP& p, cudaStr
 
 }  // namespace
 
+// The same for every call: a workspace serves larger and smaller calls, and those of
+// either kernel.
 size_t latent_attn_workspace(int32_t, int32_t, int32_t, int32_t latent_dim) {
   const size_t a = Layout::total(latent_dim), b = latent_rows_workspace(latent_dim);
   return a > b ? a : b;

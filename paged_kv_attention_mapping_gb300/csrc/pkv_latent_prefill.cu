@@ -74,7 +74,7 @@ constexpr int PLAN_THREADS = 1024;
 
 // Workspace: the next tile to claim, the number of tiles (parts of one count), the
 // largest number of parts; the sequences in the order they are worked on, the
-// tiles before each; and for calls that may split: a record, log2 sums and outputs
+// tiles before each; and, used by calls that split: a record, log2 sums and outputs
 // (fp32, normalised) per part.
 struct Layout {
   size_t order, first, rec, lse, o, total;
@@ -87,9 +87,11 @@ constexpr int MAX_PAIRS = 76;      // 152 SMs
 constexpr int MIN_STEPS = 4, MIN_SAVED = 8;
 // Whether a call's tiles can be few enough to split (its padding rows aside).
 bool may_split(int32_t Tq, int32_t H) { return (int64_t)Tq * H * 2 <= (int64_t)ROWS * MAX_PAIRS; }
-Layout layout(int32_t B, int32_t Tq, int32_t H) {
+Layout layout(int32_t B) {
   auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
-  const size_t parts = may_split(Tq, H) ? MAX_PAIRS : 0;
+  // Room for parts whether this call may split or not (20 MB): a workspace for a large
+  // call, which does not, serves smaller ones, which do.
+  const size_t parts = MAX_PAIRS;
   Layout l;
   l.order = 256;
   l.first = l.order + al((size_t)B * 4);
@@ -871,7 +873,7 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
   }
   const CUtensorMapDataType dt =
       std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const Layout lay = layout(a.B, a.Tq, a.H);
+  const Layout lay = layout(a.B);
   const int pairs = a.dev.num_sms / 2 < MAX_PAIRS ? a.dev.num_sms / 2 : MAX_PAIRS;
   // (a tile of fewer steps than the two add up to is never cut)
   const bool split = may_split(a.Tq, a.H) && a.Tk > (MIN_SAVED + MIN_STEPS - 1) * BN;
@@ -927,7 +929,7 @@ cudaError_t launch(const LatentPrefillArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t latent_prefill_workspace(int32_t B, int32_t Tq, int32_t H) { return layout(B, Tq, H).total; }
+size_t latent_prefill_workspace(int32_t B, int32_t, int32_t) { return layout(B).total; }
 
 cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, cudaStream_t s) {
   return a.dtype == PKV_BF16 ? launch<__nv_bfloat16>(a, s) : launch<__half>(a, s);

@@ -198,6 +198,19 @@ def test_workspace_sizes(lib):
         binding.latent_prefill_workspace_size(-1, 10, 16)
 
 
+def test_a_workspace_for_a_large_call_serves_smaller_ones(lib):
+    cache = torch.empty((4, 16, 576), dtype=torch.bfloat16)
+    sizes = (1, 2, 17, 300, 4096, 8192)
+    for B in (1, 64, 3000):
+        for T in sizes:
+            for H in (1, 5, 16, 128):
+                for b, t, h in ((max(B // 2, 1), T, H), (B, max(T // 40, 1), H), (B, T, max(H // 5, 1)), (1, 1, 1)):
+                    assert (binding.latent_prefill_workspace_size(b, t, h)
+                            <= binding.latent_prefill_workspace_size(B, T, H)), (B, T, H, b, t, h)
+                    assert (binding.latent_workspace_size(b, t, h, cache)
+                            <= binding.latent_workspace_size(B, T, H, cache)), (B, T, H, b, t, h)
+
+
 def test_binding_refuses_wrong_tensors(lib):
     z = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t)
     i32, i64, f32 = torch.int32, torch.int64, torch.float32
@@ -1115,4 +1128,20 @@ def test_expanded_at_the_ends_of_the_ranges(dev):
     for heads, q_lens, kv_lens in ((4096, [3, 1], [40, 200]), (1, [1], [1]), (4095, [1], [130])):
         t = Packed(dev, "bf16", heads, q_lens, kv_lens)
         t.check(*t.call())
+    assert binding.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_calls_of_every_size(dev):
+    """Allocated for a large call that splits nothing, used by calls that do, and by both absorbed kernels."""
+    ws = torch.empty(binding.latent_prefill_workspace_size(100, 8192, 128), dtype=torch.uint8, device=dev)
+    for case in (("bf16", 1, [5], [5000]), ("f16", 3, [300, 20], [3000, 1500]), ("bf16", 90, [100, 30], [400, 300])):
+        t = Packed(dev, *case)
+        t.check(*t.call(workspace=ws))
+    ws = None
+    for heads, q_lens, kv_lens in ((128, [1, 2], [3000, 700]), (4, [1, 2], [5000, 70]), (40, [1, 1], [90, 60])):
+        t = Paged(dev, "bf16", 512, heads, 64, q_lens, kv_lens)
+        if ws is None:
+            ws = binding.alloc_latent_workspace(200, 200, 128, t.cache)
+        t.check(*t.call(workspace=ws))
     assert binding.device_status() == 0
