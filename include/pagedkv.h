@@ -388,7 +388,9 @@ int pkv_paged_attention_no_alloc(const void* q, const int32_t* cu_seqlens_q, con
  *
  * latent_dim is 256 or 512 and rope_dim 64 (PKV_E_SHAPE otherwise). Any
  * page_size >= 1 is taken; rows of pages that are a multiple of 32 long move by
- * TMA, others by 16-byte copies of threads (1 to 12 % slower, 12 at one row a page). */
+ * TMA, others by 16-byte copies of threads: in decode of 64 sequences of 1000-4000 keys, against
+ * pages of 64, pages of 16 and 8 are 1-8 % slower at latent_dim 512 and 3-9 % at 256, pages
+ * of one row 12 % and 24-32 %. */
 typedef struct {
   int32_t num_pages;
   int32_t page_size;
@@ -409,9 +411,12 @@ typedef struct {
  *              qo_stride_h; may be q_rope itself with the same strides (in place), and must
  *              not overlap it otherwise. NULL with a NULL q_rope.
  *   positions, cos_sin, max_pos, slot_mapping  as pkv_rope_kv_append (half-split
- *              rotation over rope_dim values, in fp32, rounded once)
+ *              rotation over rope_dim values, in fp32, rounded once). Weights made for rotating
+ *              neighbours (x0, x1), (x2, x3), .. need the rotary columns of both the query and
+ *              the key projection reordered once, when they are loaded: the even ones first,
+ *              then the odd ones. Scores are the same.
  * Strides are in elements and may be any multiple of 8 (views of wider
- * projection outputs); c_kv, k_rope, q_rope, q_out and cache must be 16-byte
+ * projection outputs); c_kv, k_rope, q_rope, q_out, cos_sin and cache must be 16-byte
  * aligned. A negative slot skips the token's cache row (its queries are still
  * rotated); a slot past the pool sets PKV_DEV_BAD_SLOT and skips the row. A
  * position outside [0, max_pos) sets PKV_DEV_BAD_POSITION and skips the token
@@ -499,7 +504,8 @@ int pkv_latent_attention(const void* q, const int32_t* cu_seqlens_q, const int32
  * 16-byte aligned. Values of other sequences' rows never reach a row, NaN or not; a
  * NaN in a sequence's own key or value reaches every row that sees it, and a NaN or
  * an infinity may reach earlier rows of the same chunk (0 * NaN). A row all of whose
- * scores are -inf is NaN, with an lse of -inf. Calls of few tiles
+ * scores are -inf is NaN, with an lse of -inf. Sums and softmax statistics are fp32; the
+ * softmax weights are rounded to dtype for the products with the values. Calls of few tiles
  * split their keys over the GPU by the tick's total work: the order of a row's
  * fp32 sums then depends on the other rows (the same call gives the same bits).
  * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_WORKSPACE, PKV_E_DEVICE, PKV_E_CUDA. */

@@ -28,7 +28,9 @@
 //   warps 4-11 softmax. Lane l of TMEM holds row l & 63, keys (or output columns)
 //            of half l / 64; two warps share a lane quarter, each with half of its
 //            columns, so four threads have a row and exchange its maximum through
-//            shared memory. P goes to shared memory in the cache type, O is rescaled
+//            shared memory. P goes to shared memory in the cache type (the tensor cores take
+//            no fp32 operand; tf32 ones would halve their rate and double P's room): half a
+//            step of each weight, the sums stay fp32. O is rescaled
 //            in TMEM only when a row's maximum grows by more than 2^8.
 //   warp 12  scheduler: the segments of this pair, and their Q
 //   warps 13-15  where rows come by thread copies instead of TMA (page sizes that
@@ -40,8 +42,8 @@
 // end leaves partial results (normalised output in fp32 and log2 sum) that
 // latent_combine_kernel joins. Ticks of short contexts are split by whole tiles instead.
 //
-// Decode of 128 sequences of 512-8192 keys at 128 heads (bf16): 131 us, 5.1 TB/s and 1.18
-// PFLOP/s; with the combine 138 us. Two step slots fit beside Q, and a slot's turn (load,
+// Decode of 128 sequences of 512-8192 keys at 128 heads (bf16): 132 us, 5.1 TB/s and 1.17
+// PFLOP/s; with the combine 139 us. Two step slots fit beside Q, and a slot's turn (load,
 // S, softmax 1300 cycles, O, the hand-offs between them) takes two steps' time. HBM is
 // busy only while loads are under way, so the next step's rows are sent for into L2
 // behind each step's loads (without: 146 us; earlier by half a step 138, by one step 138 or 144, by two
@@ -709,8 +711,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(nthreads(GATHER), 1)
 // 2^(lse_s - max), in the order of the keys. A block takes 32 column vectors of one
 // half and every 8th group of 8 rows; 8 threads read the 128 bytes of 8 lanes. The
 // blocks of all pairs but the last that share a tile divide its row groups, so that
-// a tile of many parts has many blocks (one pair's blocks alone took 60 us for a
-// context of 131 k keys, against 18). No shared memory: the blocks get resident beside the attention kernel's,
+// a tile of many parts has many blocks (one pair's blocks alone took more than three times
+// as long for a context of 131 k keys). No shared memory: the blocks get resident beside the attention kernel's,
 // which leave none, and start when the last of those ends.
 constexpr int CROWS = 8, CVECS = 32, CY = 8;
 
@@ -889,11 +891,12 @@ cudaError_t launch_latent_attn(const LatentAttnArgs& a, cudaStream_t s) {
   p.T = a.T;
   p.H = a.H;
   p.P = a.P;
-// Rows of a TMA box: they lie in one page and in one slot.
+  // Rows of a TMA box: they lie in one page and in one slot.
   p.box = gcd(a.P, rows ? latent_rows_slot() : HM);
   // Boxes of fewer than 32 rows lose to thread copies: 64 sequences of 1000-4000 keys at 128
   // heads, TMA against copies: page size 64 58.5 / 61.8 us, 32 61.9 / 61.8, 16 67.9 / 61.6 (8 and 1,
-  // before other changes: 92 / 70 and 352 / 72); the 16-row kernel takes one box a slot.
+  // in an earlier form of the kernel: 92 / 70 and 352 / 72; copies now take 63 and 65); the 16-row
+  // kernel takes one box a slot.
   p.gather = p.box < 32;
   if (p.gather) p.box = 1;
   p.whole = short_contexts(a, rows ? latent_rows_tiling(a.dev.num_sms) : LatentTiling{BM, BN, pairs_of(a)});

@@ -25,8 +25,9 @@
 //              its warp 100-400 cycles: the two take turns, and each does its waits and
 //              commits under the other's MMAs.
 //   warps 4-7, 8-11  softmax of query tile 0, 1, a thread per row; P goes back
-//              over S in TMEM as the A operand of the next product, handed over in two
-//              halves. O is rescaled only when a row's maximum grows by more than 2^8.
+//              over S in TMEM as the A operand of the next product, rounded to the type of
+//              the values (one product's operands have one type: half a step of each weight,
+//              while sums and maxima stay fp32), handed over in two halves. O is rescaled only when a row's maximum grows by more than 2^8.
 //
 // Where the tiles are at most half as many as the pairs of CTAs (short chunks, few
 // heads), each tile's keys are cut into parts, as many as there are pairs for;

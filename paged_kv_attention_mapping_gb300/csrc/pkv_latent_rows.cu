@@ -13,7 +13,8 @@
 //
 //   warps 0-7  all of a step: the scores of 32 keys over a quarter of the columns
 //              (partial sums joined through shared memory), the softmax of two
-//              rows, then LD / 8 columns of O
+//              rows (weights rounded to the cache type, the other operand's: half a step of
+//              each; sums stay fp32), then LD / 8 columns of O
 //   warp 8     scheduler: the segments of this CTA
 //   warp 9     producer (TMA): 32-key slots of a ring, 128-byte swizzled; for small boxes
 //              (cp.async) several warps, slots in turn
