@@ -27,7 +27,8 @@
 //   warps 4-7, 8-11  softmax of query tile 0, 1, a thread per row; P goes back
 //              over S in TMEM as the A operand of the next product, rounded to the type of
 //              the values (one product's operands have one type: half a step of each weight,
-//              while sums and maxima stay fp32), handed over in two halves. O is rescaled only when a row's maximum grows by more than 2^8.
+//              while sums and maxima stay fp32), handed over in two halves. O is rescaled
+//              only when a row's maximum grows by more than 2^8.
 //
 // Where the tiles are at most half as many as the pairs of CTAs (short chunks, few
 // heads), each tile's keys are cut into parts, as many as there are pairs for;
@@ -798,7 +799,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                   make_uint4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
           }
         }
-        const float lg = l_run == 0.f ? -INFINITY : m_run + (__log2f(l_run) - SHIFT);   // (NaN scores: m may be -inf, l_run is NaN)
+        // (NaN scores: m may be -inf, l_run is NaN)
+        const float lg = l_run == 0.f ? -INFINITY : m_run + (__log2f(l_run) - SHIFT);
         if (store && !whole) p.part_lse[prow] = lg;
         else if (store && p.lse) p.lse[row] = lg * LN2;
         tc_fence_before();

@@ -445,7 +445,8 @@ __global__ void __launch_bounds__(nthreads(GATHER), 1)
       }
       if (tid < TM && tid < g.nrows) {
         const float l = sh.l[tid];
-        const float lg = l == 0.f ? -INFINITY : sh.m[tid] + (__log2f(l) - SHIFT);   // (NaN scores: m may be -inf, l is NaN)
+        // (NaN scores: m may be -inf, l is NaN)
+        const float lg = l == 0.f ? -INFINITY : sh.m[tid] + (__log2f(l) - SHIFT);
         if (!whole) ((float*)(p.ws + Layout::lse))[slot * TM + tid] = lg;
         else if (p.lse && !bad) p.lse[(int64_t)g.row0 + tid] = lg * LN2;
       }
