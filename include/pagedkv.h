@@ -81,7 +81,7 @@ typedef enum {
                                    that row's output is left unwritten */
 #define PKV_DEV_TIMEOUT 0x8     /* a kernel's internal wait gave up (a bug, never expected);
                                    the outputs of that call are unspecified */
-#define PKV_DEV_BAD_POSITION 0x10 /* rope and latent append: a position outside [0, max_pos); that row skipped */
+#define PKV_DEV_BAD_POSITION 0x10 /* rope, norm and latent append: a position outside [0, max_pos); that row skipped */
 
 /* One layer's K (or V) page pool: contiguous
  * [num_pages, page_size, num_kv_heads, head_dim] of `dtype`. */
@@ -515,6 +515,166 @@ int pkv_latent_prefill(const void* q, const int32_t* cu_seqlens_q, const void* k
                        const void* k_rope, int64_t kr_stride, const int32_t* cu_seqlens_k, int32_t num_seqs,
                        int32_t total_q, int32_t total_k, int32_t num_heads, int32_t dtype, float scale, void* out,
                        float* lse, void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Layers with a window: norm, rotation and append in one pass; attention with a
+ * sliding window and sinks; pages copied, forked, compacted and freed.
+ * The calls follow the conventions above. None needs a workspace. */
+
+/* pkv_norm_rope_kv_append — norm queries and keys per head, rotate them by position,
+ * write keys and values into their slots and queries to q_out, in one pass.
+ *
+ *   q, k, v       device, head h of token t at + t * stride_t + h * stride_h (elements of
+ *                 src_dtype; strides >= 0 and multiples of 16 bytes; views of one
+ *                 projection's output will do), head_dim values each
+ *   src_dtype     PKV_F32, PKV_F16 or PKV_BF16: of q, k, v, the weights and q_out. The
+ *                 cache has the same type, or is PKV_FP8_E4M3 with k_scale and v_scale
+ *   q_weight, k_weight  device, head_dim weights of the norm each, or NULL (that
+ *                 tensor is not normed): y = w x / sqrt(mean(x^2) + eps)
+ *   eps           >= 0 and finite
+ *   cos_sin       device, fp32 [max_pos, rotary_dim / 2, 2], 16-byte aligned
+ *                 (pkv_rope_table, pkv_rope_table_scaled)
+ *   rotary_dim    the first rotary_dim values of each head are rotated, the others are
+ *                 kept: a multiple of 16, 16 .. head_dim
+ *   interleaved   0: pair i is (y_i, y_{i + rotary_dim / 2}); 1: (y_2i, y_2i+1)
+ *   positions     device, int32 [num_tokens]: each token's entry of the table
+ *   slot_mapping  device, int64 [num_tokens]; negative: the token's key and value are not
+ *                 stored (its query is written). A slot named twice gets one of its tokens
+ *   k_cache, v_cache  the pools, head_dim 64, 128 or 256
+ *   k_scale, v_scale  device, fp32 [num_kv_heads] (> 0) for an e4m3 cache, NULL otherwise:
+ *                 codes of x / scale, the float32 quotient rounded to nearest, saturating
+ *   q_out         device, as q (strides must keep heads apart); may be q itself with the
+ *                 same strides (in place), and must not overlap it otherwise
+ * Norm and rotation are fp32 and rounded once; a head whose squares sum beyond the fp32
+ * range comes out as zeros. A position outside [0, max_pos) sets PKV_DEV_BAD_POSITION and
+ * nothing of that token is written; a slot outside the pool sets PKV_DEV_BAD_SLOT and the
+ * token's key and value are not written.
+ * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_DEVICE, PKV_E_CUDA. */
+int pkv_norm_rope_kv_append(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                            int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                            int64_t v_stride_h, int32_t src_dtype, const void* q_weight, const void* k_weight,
+                            float eps, const int32_t* positions, const float* cos_sin, int32_t max_pos,
+                            int32_t rotary_dim, int32_t interleaved, const int64_t* slot_mapping,
+                            int32_t num_tokens, int32_t num_q_heads, void* k_cache, void* v_cache,
+                            const pkv_cache_desc* cache, const float* k_scale, const float* v_scale, void* q_out,
+                            int64_t qo_stride_t, int64_t qo_stride_h, pkv_stream_t stream);
+
+/* How the angles f_i = base^(-2i / rotary_dim) of the pairs are stretched for contexts
+ * longer than the model was trained on. */
+typedef enum {
+  PKV_ROPE_PLAIN = 0,  /* f_i */
+  PKV_ROPE_LINEAR = 1, /* f_i / factor */
+  PKV_ROPE_BASE = 2,   /* base * factor^(r / (r - 2)) in place of base, r = rotary_dim >= 4 */
+  PKV_ROPE_BANDS = 3,  /* by n_i = original_max_pos f_i / 2 pi turns: f_i from `high` turns up,
+                          f_i / factor up to `low` turns, between them s f_i + (1 - s) f_i / factor
+                          with s = (n_i - low) / (high - low) */
+  PKV_ROPE_RAMP = 4    /* by pair number: f_i up to the pair floor(c(high)), f_i / factor from
+                          ceil(c(low)) on, linear between, c(n) = r ln(original_max_pos / (2 pi n)) /
+                          (2 ln base), both kept in [0, r - 1] */
+} pkv_rope_kind;
+typedef struct {
+  int32_t kind;             /* pkv_rope_kind */
+  double factor;            /* >= 1 (not read by PKV_ROPE_PLAIN) */
+  double low, high;         /* 0 < low < high, turns over the original context (BANDS, RAMP) */
+  double original_max_pos;  /* >= 1 (BANDS, RAMP) */
+  double attention_factor;  /* on cos and sin; 0: 1, and 0.1 ln(factor) + 1 for RAMP */
+} pkv_rope_scaling;
+
+/* pkv_rope_table_scaled — host: entry (p, i) = attention_factor * (cos, sin)(p f'_i) of
+ * the stretched angles, [max_pos][rotary_dim / 2][2], computed in double and stored as
+ * float. rotary_dim is even. Errors: PKV_E_NULL, PKV_E_SHAPE. */
+int pkv_rope_table_scaled(double base, int32_t rotary_dim, const pkv_rope_scaling* scaling, int32_t max_pos,
+                          float* cos_sin);
+
+/* pkv_window_attention — attention of packed rows over the pages, where the row at
+ * position p = kv_len - q_len + i sees the keys j <= p with j > p - window or j < sinks:
+ * the `window` keys up to its own, and the first `sinks` keys.
+ *
+ *   q, out        device, contiguous [total_q, num_q_heads, head_dim] of q_dtype
+ *   q_dtype       the cache's dtype; PKV_BF16 or PKV_F16 over a PKV_FP8_E4M3 cache
+ *   cu_seqlens_q, kv_lens, page_tables  as pkv_paged_attention; cu_seqlens_q may end
+ *                 before total_q (rows behind are padding and left as they were)
+ *   window, sinks >= 1 and >= 0; any size (a window of kv_len or more is plain causal
+ *                 attention)
+ *   scale         > 0 and finite
+ *   k_scale, v_scale  device, fp32 [num_kv_heads] for an e4m3 cache, NULL otherwise
+ *   lse           device, fp32 [total_q, num_q_heads] or NULL
+ * head_dim is 64, 128 or 256; num_q_heads / num_kv_heads 1 to 8 or 16; any page_size.
+ * Pages without a key that some row of their sequence sees are not read, nor are their
+ * table entries: they may be freed, entries behind the window and past the sinks may be
+ * -1 (pkv_pool_trim, pkv_pack_tick_window), and slots that no row sees may hold anything.
+ * A key or value that is NaN or infinite reaches every row that sees it, and may reach
+ * other rows of the same chunk (0 * NaN, as in a product with a masked weight matrix). A
+ * row all of whose scores are -inf is NaN, with an lse of -inf. Sums and softmax statistics
+ * are fp32; softmax weights are rounded to the type of the products with the values (f16 and
+ * e4m3 caches: f16 with a power of two in front that keeps small weights; bf16: bf16; f32: none).
+ * How a row's keys are split over the GPU goes by the call's sizes, so the order of
+ * its sums may differ from call shape to call shape (the same call gives the same bits).
+ * A sequence with rows whose kv_len is below q_len or above max_pages_per_seq * page_size
+ * sets PKV_DEV_BAD_LENGTHS and is skipped; a cu_seqlens_q that does not start at 0, decreases or
+ * ends beyond total_q sets PKV_DEV_BAD_LENGTHS (the call's rows are then unspecified). A needed
+ * page outside the pool sets PKV_DEV_BAD_PAGE and the rows that need it, or share a tile of rows with
+ * one that does, are left as they were.
+ * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_DEVICE, PKV_E_CUDA. */
+int pkv_window_attention(const void* q, int32_t q_dtype, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
+                         const int32_t* page_tables, int32_t num_seqs, int32_t total_q, int32_t num_q_heads,
+                         int32_t max_pages_per_seq, int32_t window, int32_t sinks, const void* k_cache,
+                         const void* v_cache, const pkv_cache_desc* cache, const float* k_scale,
+                         const float* v_scale, float scale, void* out, float* lse, pkv_stream_t stream);
+
+/* pkv_copy_pages — copy pages within each of several caches of one pool's page ids (all
+ * layers' keys and values, latent caches, e4m3 caches).
+ *
+ *   caches      host array of num_caches device pointers, each a contiguous
+ *               [num_pages, page_size, slot_bytes]; read before the call returns
+ *   slot_bytes  bytes of one token in one cache, a multiple of 16
+ *   src, dst    device, int32 [num_copies]: page dst[i] gets what page src[i] holds, in every
+ *               cache; a negative src or dst: no copy
+ *   tokens      device, int32 [num_copies] or NULL: only the first tokens[i] slots are
+ *               copied (the rest of page dst[i] is left as it was); NULL: the whole page
+ * No page may be dst of one copy and src or dst of another. An id outside the pool sets
+ * PKV_DEV_BAD_PAGE and a count outside 0 .. page_size sets PKV_DEV_BAD_LENGTHS; that copy is skipped.
+ * Errors: PKV_E_NULL, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_DEVICE, PKV_E_CUDA. */
+int pkv_copy_pages(void* const* caches, int32_t num_caches, int32_t num_pages, int32_t page_size,
+                   int64_t slot_bytes, const int32_t* src, const int32_t* dst, const int32_t* tokens,
+                   int32_t num_copies, pkv_stream_t stream);
+
+/* pkv_remap_pages — rewrite page tables in place for pages that have moved: entry e >= 0
+ * becomes page_map[e] (device, int32 [num_pages]; pkv_pool_compact gives it, a negative one frees the entry), negative entries
+ * stay. An entry or a map value outside the pool sets PKV_DEV_BAD_PAGE and stays as it was.
+ * Errors: PKV_E_NULL, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_DEVICE, PKV_E_CUDA. */
+int pkv_remap_pages(int32_t* page_tables, int64_t num_entries, const int32_t* page_map, int32_t num_pages,
+                    pkv_stream_t stream);
+
+/* pkv_pool_fork — host: pages of a sequence forked after kv_len tokens. The child shares
+ * the full pages (one more reference each; -1 entries of freed pages are handed on) and, where
+ * kv_len ends inside a page, gets a new page for the rest: the call then returns 1 and *src,
+ * *dst, *tokens say what pkv_copy_pages has to copy; it returns 0 where nothing is to copy.
+ * child has room for ceil(kv_len / page_size) pages. On an error (PKV_E_NULL, PKV_E_SHAPE, PKV_E_PAGES,
+ * PKV_E_CAPACITY: no free page) nothing changes. */
+int pkv_pool_fork(pkv_pool* pool, const int32_t* pages, int32_t n_pages, int32_t kv_len, int32_t* child,
+                  int32_t* src, int32_t* dst, int32_t* tokens);
+
+/* pkv_pool_compact — host: move held pages with the highest ids to the lowest free ids, at
+ * most max_moves of them, so that the held pages come to be the lowest. Returns the number of
+ * moves, writes them to src and dst (no page is in both; room for max_moves) and page_map[num_pages],
+ * the new id of every page. Reference counts and prefix-cache entries move along. The caller copies
+ * the pages (pkv_copy_pages) and rewrites its tables (pkv_remap_pages, and its own lists)
+ * before it uses either. Errors: PKV_E_NULL, PKV_E_SHAPE. */
+int pkv_pool_compact(pkv_pool* pool, int32_t max_moves, int32_t* src, int32_t* dst, int32_t* page_map);
+
+/* pkv_pool_trim — host: let go of a sequence's pages that no row at position kv_len or
+ * later sees through a window with sinks; their entries in `pages` become -1. Returns how many.
+ * On an error (PKV_E_NULL, PKV_E_SHAPE, PKV_E_PAGES) nothing changes. */
+int pkv_pool_trim(pkv_pool* pool, int32_t* pages, int32_t n_pages, int32_t kv_len, int32_t window, int32_t sinks);
+
+/* pkv_pack_tick_window — pkv_pack_tick for a tick whose attention has a window: page ids may
+ * be -1 where no row of the tick sees a key of the page. window >= 1, sinks >= 0. */
+int pkv_pack_tick_window(int32_t num_seqs, const int32_t* q_lens, const int32_t* kv_lens,
+                         const int32_t* page_offsets, const int32_t* page_ids, int32_t page_size,
+                         int32_t num_pages, int32_t max_pages_per_seq, int32_t slot_capacity, int32_t window,
+                         int32_t sinks, int32_t* order, int32_t* cu_seqlens_q, int32_t* kv_lens_out,
+                         int32_t* page_tables, int64_t* slot_mapping, int32_t* total_q_out);
 
 /* ---------------------------------------------------------------------------
  * Status and instrumentation. */

@@ -56,6 +56,15 @@ EXPORTED = (
     "pkv_latent_attention",
     "pkv_latent_prefill_workspace_size",
     "pkv_latent_prefill",
+    "pkv_norm_rope_kv_append",
+    "pkv_rope_table_scaled",
+    "pkv_window_attention",
+    "pkv_copy_pages",
+    "pkv_remap_pages",
+    "pkv_pool_fork",
+    "pkv_pool_compact",
+    "pkv_pool_trim",
+    "pkv_pack_tick_window",
 )
 
 
@@ -74,6 +83,11 @@ class CacheDesc(ctypes.Structure):
 class LatentDesc(ctypes.Structure):
     _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
                 ("rope_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("original_max_pos", ctypes.c_double), ("attention_factor", ctypes.c_double)]
 
 
 _lib = None
@@ -160,6 +174,28 @@ def lib():
     L.pkv_latent_prefill.argtypes = [vp, vp, vp, i64, i64, vp, i64, i64, vp, i64, vp, i32, i32, i32, i32, i32,
                                      ctypes.c_float, vp, vp, vp, sz, vp]
     L.pkv_latent_prefill.restype = ctypes.c_int
+    PC, f32 = ctypes.POINTER(CacheDesc), ctypes.c_float
+    L.pkv_norm_rope_kv_append.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, vp, vp, f32, vp, vp, i32, i32,
+                                          i32, vp, i32, i32, vp, vp, PC, vp, vp, vp, i64, i64, vp]
+    L.pkv_norm_rope_kv_append.restype = ctypes.c_int
+    L.pkv_rope_table_scaled.argtypes = [ctypes.c_double, i32, ctypes.POINTER(RopeScaling), i32,
+                                        ctypes.POINTER(f32)]
+    L.pkv_rope_table_scaled.restype = ctypes.c_int
+    L.pkv_window_attention.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, PC, vp, vp, f32, vp,
+                                       vp, vp]
+    L.pkv_window_attention.restype = ctypes.c_int
+    L.pkv_copy_pages.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i64, vp, vp, vp, i32, vp]
+    L.pkv_copy_pages.restype = ctypes.c_int
+    L.pkv_remap_pages.argtypes = [vp, i64, vp, i32, vp]
+    L.pkv_remap_pages.restype = ctypes.c_int
+    L.pkv_pool_fork.argtypes = [vp, P32, i32, i32, P32, P32, P32, P32]
+    L.pkv_pool_fork.restype = ctypes.c_int
+    L.pkv_pool_compact.argtypes = [vp, i32, P32, P32, P32]
+    L.pkv_pool_compact.restype = ctypes.c_int
+    L.pkv_pool_trim.argtypes = [vp, P32, i32, i32, i32, i32]
+    L.pkv_pool_trim.restype = ctypes.c_int
+    L.pkv_pack_tick_window.argtypes = [i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+    L.pkv_pack_tick_window.restype = ctypes.c_int
     L.pkv_version.argtypes = []
     L.pkv_version.restype = ctypes.c_char_p
     _lib = L
@@ -183,9 +219,10 @@ def _check(status: int, where: str):
 # host packing
 
 def pack_tick(q_lens: Sequence[int], kv_lens: Sequence[int], pages: Sequence[Sequence[int]], page_size: int,
-              num_pages: int, max_pages_per_seq: Optional[int] = None):
+              num_pages: int, max_pages_per_seq: Optional[int] = None, window: Optional[int] = None, sinks: int = 0):
     """Host packing of one tick (pkv_pack_tick). Returns numpy arrays:
-    order, cu_seqlens_q, kv_lens, page_tables [B, W] (-1 padded), slot_mapping."""
+    order, cu_seqlens_q, kv_lens, page_tables [B, W] (-1 padded), slot_mapping.
+    With a `window` (pkv_pack_tick_window) pages that no row of the tick sees may be -1."""
     B = len(q_lens)
     counts = [len(p) for p in pages]
     offs = np.zeros(B + 1, dtype=np.int32)
@@ -193,11 +230,12 @@ def pack_tick(q_lens: Sequence[int], kv_lens: Sequence[int], pages: Sequence[Seq
         np.cumsum(counts, out=offs[1:])
     ids = np.fromiter(itertools.chain.from_iterable(pages), dtype=np.int32, count=int(offs[-1]))
     return pack_tick_flat(np.asarray(q_lens, dtype=np.int32), np.asarray(kv_lens, dtype=np.int32), offs, ids,
-                          page_size, num_pages, max_pages_per_seq)
+                          page_size, num_pages, max_pages_per_seq, window=window, sinks=sinks)
 
 
 def pack_tick_flat(q_lens, kv_lens, page_offsets, page_ids, page_size: int, num_pages: int,
-                   max_pages_per_seq: Optional[int] = None, out: Optional[dict] = None):
+                   max_pages_per_seq: Optional[int] = None, out: Optional[dict] = None, window: Optional[int] = None,
+                   sinks: int = 0):
     """pack_tick on flat int32 arrays, the form a scheduler keeps its block
     tables in: sequence b owns page_ids[page_offsets[b]:page_offsets[b + 1]].
 
@@ -236,11 +274,14 @@ def pack_tick_flat(q_lens, kv_lens, page_offsets, page_ids, page_size: int, num_
         if not a.flags.c_contiguous:
             raise ValueError("pack_tick_flat: out arrays must be C-contiguous")
     total = np.zeros(1, dtype=np.int32)
-    st = lib().pkv_pack_tick(B, ql.ctypes.data if B else None, kl.ctypes.data if B else None, offs.ctypes.data,
-                             ids.ctypes.data, int(page_size), int(num_pages), W, cap, order.ctypes.data,
-                             cu.ctypes.data, kv_out.ctypes.data, tables.ctypes.data, slots.ctypes.data,
-                             total.ctypes.data)
-    _check(st, "pkv_pack_tick")
+    given = (B, ql.ctypes.data if B else None, kl.ctypes.data if B else None, offs.ctypes.data, ids.ctypes.data,
+             int(page_size), int(num_pages), W, cap)
+    wanted = (order.ctypes.data, cu.ctypes.data, kv_out.ctypes.data, tables.ctypes.data, slots.ctypes.data,
+              total.ctypes.data)
+    if window is None:
+        _check(lib().pkv_pack_tick(*given, *wanted), "pkv_pack_tick")
+    else:
+        _check(lib().pkv_pack_tick_window(*given, int(window), int(sinks), *wanted), "pkv_pack_tick_window")
     T = int(total[0])
     return dict(order=order[:B], cu_seqlens_q=cu[:B + 1], kv_lens=kv_out[:B], page_tables=tables[:B],
                 slot_mapping=slots[:T])
@@ -767,6 +808,230 @@ def latent_prefill(q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, scale: floa
     return out, lse
 
 
+# ---------------------------------------------------------------------------
+# layers with a window
+
+@functools.lru_cache(maxsize=256)
+def _cache_desc_of(shape, dtype):
+    return ctypes.byref(CacheDesc(*shape, _code_of(dtype)))
+
+
+def _caches(where, k_cache, v_cache, k_scale, v_scale):
+    """The caches' shape and descriptor, as an argument, and whether they hold codes."""
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dtype:
+        raise ValueError(f"{where}: k_cache and v_cache must share one shape [num_pages, page_size, num_kv_heads, "
+                         "head_dim] and one dtype")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError(f"{where}: caches must be contiguous")
+    codes = _code_of(dtype) == PKV_FP8_E4M3
+    if codes != (k_scale is not None) or codes != (v_scale is not None):
+        raise ValueError(f"{where}: an e4m3 cache needs k_scale and v_scale, other caches take none")
+    if codes:
+        for t in (k_scale, v_scale):
+            if t.dtype is not _torch.float32 or t.shape != (shape[2],) or not t.is_contiguous():
+                raise ValueError(f"{where}: scales must be contiguous float32 [num_kv_heads]")
+    return shape, _cache_desc_of(shape, dtype), codes
+
+
+def _heads(where, name, t, dtype, shape):
+    """Strides of tokens and heads of [T, H, D] rows."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{where}: {name} must be {list(shape)} of dtype {dtype}")
+    st, sh, s1 = t.stride()
+    if s1 != 1:
+        raise ValueError(f"{where}: {name} must be contiguous in its last dimension")
+    # (a dimension of one entry may have any stride)
+    return (st if shape[0] > 1 else 0), (sh if shape[1] > 1 else 0)
+
+
+def norm_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight=None, k_weight=None,
+                        eps: float = 1e-6, interleaved: bool = False, k_scale=None, v_scale=None, q_out=None,
+                        stream=None):
+    """Norm queries and keys per head, rotate them, and append keys and values, in one
+    pass (pkv_norm_rope_kv_append).
+
+    q [T, Hq, d], k and v [T, Hkv, d] of one dtype (strided views allowed); q_weight,
+    k_weight [d] of that dtype or None (not normed); cos_sin float32 [max_pos, r / 2, 2]
+    (rope_table, rope_table_scaled): the first r values of a head are rotated, in pairs
+    r / 2 apart or, interleaved, of neighbours; positions int32 [T]; slot_mapping int64 [T];
+    caches [N, P, Hkv, d] of that dtype, or e4m3 codes with float32 scales [Hkv]. The
+    queries go to q_out (strided views allowed; q_out may be q; a new tensor when it is
+    None). Returns q_out."""
+    torch = _torch or _load_torch()
+    where = "norm_rope_kv_append"
+    dev = _on_one_device(where, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, k_scale,
+                         v_scale, q_out)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return norm_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight,
+                                       eps, interleaved, k_scale, v_scale, q_out, stream)
+    (_, _, Hkv, D), desc, codes = _caches(where, k_cache, v_cache, k_scale, v_scale)
+    if (positions.dtype is not torch.int32 or slot_mapping.dtype is not torch.int64
+            or cos_sin.dtype is not torch.float32):
+        raise TypeError(f"{where}: positions int32, slot_mapping int64, cos_sin float32")
+    if not (positions.is_contiguous() and slot_mapping.is_contiguous() and cos_sin.is_contiguous()):
+        raise ValueError(f"{where}: positions, slot_mapping and cos_sin must be contiguous")
+    dtype, shape, tokens, table = q.dtype, q.shape, slot_mapping.shape, cos_sin.shape
+    if not codes and dtype is not k_cache.dtype:
+        raise TypeError(f"{where}: q, k, v and the caches must share one dtype (but for e4m3 caches)")
+    if len(tokens) != 1 or positions.shape != tokens or len(table) != 3 or table[2] != 2:
+        raise ValueError(f"{where}: positions and slot_mapping must be [T], cos_sin [max_pos, r / 2, 2]")
+    T, = tokens
+    if len(shape) != 3 or shape[0] != T or shape[2] != D:
+        raise ValueError(f"{where}: q must be [T, Hq, {D}]")
+    if q_out is None:
+        q_out = _lent(torch.empty(shape, dtype=dtype, device=q.device), stream)
+    qs, ks, vs = (_heads(where, "q", q, dtype, shape), _heads(where, "k", k, dtype, (T, Hkv, D)),
+                  _heads(where, "v", v, dtype, (T, Hkv, D)))
+    qo = _heads(where, "q_out", q_out, dtype, shape)
+    if (T > 1 and qo[0] == 0) or (shape[1] > 1 and qo[1] == 0):
+        raise ValueError(f"{where}: q_out must not be a broadcast view")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype is not dtype or w.shape != (D,) or not w.is_contiguous()):
+            raise ValueError(f"{where}: norm weights must be contiguous [{D}] of q's dtype")
+    on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+    st = lib().pkv_norm_rope_kv_append(
+        q.data_ptr(), *qs, k.data_ptr(), *ks, v.data_ptr(), *vs, _code_of(dtype), _ptr(q_weight), _ptr(k_weight), eps,
+        positions.data_ptr(), cos_sin.data_ptr(), table[0], 2 * table[1], 1 if interleaved else 0,
+        slot_mapping.data_ptr(), T, shape[1], k_cache.data_ptr(), v_cache.data_ptr(), desc, _ptr(k_scale),
+        _ptr(v_scale), q_out.data_ptr(), *qo, on)
+    if st:
+        _check(st, "pkv_norm_rope_kv_append")
+    return q_out
+
+
+ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+
+
+def rope_table_scaled(base: float, rotary_dim: int, max_pos: int, kind: str = "plain", factor: float = 1.0,
+                      low: float = 1.0, high: float = 32.0, original_max_pos: float = 0.0,
+                      attention_factor: float = 0.0) -> np.ndarray:
+    """Host cos/sin table [max_pos, rotary_dim/2, 2] float32 of stretched angles
+    (pkv_rope_table_scaled): kind "plain", "linear", "base", "bands" or "ramp"."""
+    if kind not in ROPE_KINDS:
+        raise ValueError(f"rope_table_scaled: kind must be one of {', '.join(ROPE_KINDS)}")
+    scaling = RopeScaling(ROPE_KINDS[kind], float(factor), float(low), float(high), float(original_max_pos),
+                          float(attention_factor))
+    out = np.zeros((max(int(max_pos), 1), max(int(rotary_dim) // 2, 1), 2), dtype=np.float32)
+    _check(lib().pkv_rope_table_scaled(float(base), int(rotary_dim), ctypes.byref(scaling), int(max_pos),
+                                       out.ctypes.data_as(ctypes.POINTER(ctypes.c_float))), "pkv_rope_table_scaled")
+    return out
+
+
+def window_attention(q, cu_seqlens_q, kv_lens, page_tables, k_cache, v_cache, scale: float, window: int, sinks: int = 0,
+                     k_scale=None, v_scale=None, out=None, lse=None, want_lse: bool = True, stream=None):
+    """Attention of packed rows over their pages through a sliding window with sinks
+    (pkv_window_attention): the row at position p sees the keys p - window + 1 .. p and
+    the first `sinks` keys.
+
+    q [T, Hq, d]; cu_seqlens_q int32 [B + 1]; kv_lens int32 [B]; page_tables int32 [B, W];
+    caches [N, P, Hkv, d] of q's dtype, or e4m3 codes (q bf16 or f16) with float32 scales
+    [Hkv]. Returns (out [T, Hq, d], lse [T, Hq])."""
+    torch = _torch or _load_torch()
+    where = "window_attention"
+    i32 = torch.int32
+    if cu_seqlens_q.dtype is not i32 or kv_lens.dtype is not i32 or page_tables.dtype is not i32:
+        raise TypeError(f"{where}: index tensors must be int32")
+    dev = _on_one_device(where, q, cu_seqlens_q, kv_lens, page_tables, k_cache, v_cache, k_scale, v_scale, out, lse)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return window_attention(q, cu_seqlens_q, kv_lens, page_tables, k_cache, v_cache, scale, window, sinks,
+                                    k_scale, v_scale, out, lse, want_lse, stream)
+    (_, _, Hkv, D), desc, codes = _caches(where, k_cache, v_cache, k_scale, v_scale)
+    shape, dtype, tables, cu, lens = q.shape, q.dtype, page_tables.shape, cu_seqlens_q.shape, kv_lens.shape
+    if not codes and dtype is not k_cache.dtype:
+        raise TypeError(f"{where}: q and the caches must share one dtype (but for e4m3 caches)")
+    if len(shape) != 3 or shape[2] != D or not q.is_contiguous():
+        raise ValueError(f"{where}: q must be a contiguous [T, Hq, {D}] tensor")
+    T, Hq, _ = shape
+    if len(cu) != 1 or len(lens) != 1 or len(tables) != 2 or not 0 <= cu[0] - 1 <= min(lens[0], tables[0]):
+        raise ValueError(f"{where}: cu_seqlens_q [B + 1], kv_lens [B] and page_tables [B, W] disagree")
+    if not (cu_seqlens_q.is_contiguous() and kv_lens.is_contiguous() and page_tables.is_contiguous()):
+        raise ValueError(f"{where}: index tensors must be contiguous")
+    if out is None:
+        out = _lent(torch.empty(shape, dtype=dtype, device=q.device), stream)
+    elif out.dtype is not dtype or out.shape != shape or not out.is_contiguous():
+        raise _bad_out(where, D)
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous():
+            raise _bad_out(where, D)
+    elif want_lse:
+        lse = _lent(torch.empty((T, Hq), dtype=torch.float32, device=q.device), stream)
+    on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+    st = lib().pkv_window_attention(q.data_ptr(), _code_of(dtype), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
+                                    page_tables.data_ptr(), cu[0] - 1, T, Hq, tables[1], window, sinks,
+                                    k_cache.data_ptr(), v_cache.data_ptr(), desc, _ptr(k_scale), _ptr(v_scale), scale,
+                                    out.data_ptr(), _ptr(lse), on)
+    if st:
+        _check(st, "pkv_window_attention")
+    return out, lse
+
+
+def copy_pages(caches, src, dst, tokens=None, stream=None):
+    """Copy pages within each of several caches of one pool's page ids (pkv_copy_pages).
+
+    caches: contiguous tensors [N, P, ...] of one shape and dtype (keys and values of all
+    layers, latent caches); src, dst int32 [n] on their device: page dst[i] gets page
+    src[i] in every cache (negative: no copy), with tokens int32 [n] only its first
+    tokens[i] slots. No page may be dst of one copy and src or dst of another."""
+    torch = _torch or _load_torch()
+    where = "copy_pages"
+    caches = list(caches)
+    if not caches:
+        return
+    dev = _on_one_device(where, src, dst, tokens, *caches)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return copy_pages(caches, src, dst, tokens, stream)
+    first = caches[0]
+    shape, dtype = first.shape, first.dtype
+    if len(shape) < 3:
+        raise ValueError(f"{where}: a cache must be [num_pages, page_size, ...]")
+    ptrs = []
+    for c in caches:
+        if c.shape != shape or c.dtype is not dtype or not c.is_contiguous():
+            raise ValueError(f"{where}: caches must be contiguous and share one shape and dtype")
+        ptrs.append(c.data_ptr())
+    n = src.shape
+    if src.dtype is not torch.int32 or dst.dtype is not torch.int32 or (tokens is not None
+                                                                       and tokens.dtype is not torch.int32):
+        raise TypeError(f"{where}: src, dst and tokens must be int32")
+    if len(n) != 1 or dst.shape != n or (tokens is not None and tokens.shape != n):
+        raise ValueError(f"{where}: src, dst and tokens must be [n]")
+    if not (src.is_contiguous() and dst.is_contiguous() and (tokens is None or tokens.is_contiguous())):
+        raise ValueError(f"{where}: src, dst and tokens must be contiguous")
+    slot_bytes = first.element_size()
+    for x in shape[2:]:
+        slot_bytes *= x
+    on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+    st = lib().pkv_copy_pages((ctypes.c_void_p * len(ptrs))(*ptrs), len(ptrs), shape[0], shape[1], slot_bytes,
+                              src.data_ptr(), dst.data_ptr(), _ptr(tokens), n[0], on)
+    if st:
+        _check(st, "pkv_copy_pages")
+
+
+def remap_pages(page_tables, page_map, stream=None):
+    """Rewrite page tables in place for pages that have moved (pkv_remap_pages): entry
+    e >= 0 becomes page_map[e]. page_tables int32 (any shape, contiguous), page_map int32
+    [num_pages]. Returns page_tables."""
+    torch = _torch or _load_torch()
+    where = "remap_pages"
+    dev = _on_one_device(where, page_tables, page_map)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return remap_pages(page_tables, page_map, stream)
+    if page_tables.dtype is not torch.int32 or page_map.dtype is not torch.int32:
+        raise TypeError(f"{where}: page_tables and page_map must be int32")
+    if page_map.dim() != 1 or not (page_tables.is_contiguous() and page_map.is_contiguous()):
+        raise ValueError(f"{where}: page_tables and page_map [num_pages] must be contiguous")
+    on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
+    st = lib().pkv_remap_pages(page_tables.data_ptr(), page_tables.numel(), page_map.data_ptr(), page_map.shape[0], on)
+    if st:
+        _check(st, "pkv_remap_pages")
+    return page_tables
+
+
 def selftest_bounded_wait(limit_us: int, result=None, stream=None) -> None:
     """Enqueue the failure-path self-test (pkv_selftest_bounded_wait): a CTA laid
     out like the prefill kernel's waits on barriers that nothing completes; the
@@ -878,3 +1143,42 @@ class PagePool:
 
     def cache_size(self) -> int:
         return int(lib().pkv_prefix_size(self._h))
+
+    # A call of these changes nothing when it raises.
+
+    def fork(self, pages, kv_len: int):
+        """Pages of a sequence forked after kv_len tokens (pkv_pool_fork): (the child's
+        pages, None or the (src, dst, tokens) that copy_pages has to copy)."""
+        a, p = self._arr(pages if len(pages) else [0])
+        used = -(-int(kv_len) // self.page_size)
+        child, cp = self._arr(np.zeros(max(used, len(pages), 1)))
+        what = np.zeros(3, dtype=np.int32)
+        P32 = ctypes.POINTER(ctypes.c_int32)
+        at = [what[i:].ctypes.data_as(P32) for i in range(3)]
+        n = lib().pkv_pool_fork(self._h, p, len(pages), int(kv_len), cp, *at)
+        if n < 0:
+            raise PagedKVError(n, "pkv_pool_fork")
+        return [int(x) for x in child[:used]], (tuple(int(x) for x in what) if n else None)
+
+    def compact(self, max_moves: int = 1 << 30):
+        """Move held pages to the lowest free ids (pkv_pool_compact): int32 arrays src,
+        dst of the moves and page_map [num_pages], for copy_pages and remap_pages."""
+        m = max(min(int(max_moves), self.num_pages), 0) if max_moves >= 0 else int(max_moves)
+        src, sp = self._arr(np.zeros(max(m, 1)))
+        dst, dp = self._arr(np.zeros(max(m, 1)))
+        page_map, mp = self._arr(np.zeros(self.num_pages))
+        n = lib().pkv_pool_compact(self._h, m, sp, dp, mp)
+        if n < 0:
+            raise PagedKVError(n, "pkv_pool_compact")
+        return src[:n], dst[:n], page_map
+
+    def trim(self, pages, kv_len: int, window: int, sinks: int = 0):
+        """Let go of the pages that no row at position kv_len or later sees through a
+        window with sinks (pkv_pool_trim): the list with -1 in their places."""
+        a, p = self._arr(pages if len(pages) else [0])
+        a = a.copy()
+        n = lib().pkv_pool_trim(self._h, a.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), len(pages), int(kv_len),
+                                int(window), int(sinks))
+        if n < 0:
+            raise PagedKVError(n, "pkv_pool_trim")
+        return [int(x) for x in a[:len(pages)]]

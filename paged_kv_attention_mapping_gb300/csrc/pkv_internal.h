@@ -261,6 +261,50 @@ struct LatentPrefillArgs {
 size_t latent_prefill_workspace(int32_t B, int32_t Tq, int32_t H);
 cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, cudaStream_t s);
 
+// Norm, rotation and append in one pass (pkv_norm_rope.cu). Strides in elements.
+struct NormRopeArgs {
+  const void *q, *k, *v, *q_weight, *k_weight;
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, qo_st, qo_sh, pool_slots;
+  float eps;
+  const int32_t* positions;
+  const float* cos_sin;
+  const int64_t* slots;
+  int32_t max_pos, rot, interleaved, T, Hq, Hkv, D, dtype;
+  void *kc, *vc, *q_out;
+  const float *k_scale, *v_scale;   // e4m3 caches, else null
+  int32_t* dev_status;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s);
+
+// Page copies and table rewriting (pkv_pages.cu).
+struct CopyPagesArgs {
+  void* const* caches;
+  int32_t num_caches, num_pages, page_size, num_copies;
+  int64_t slot_bytes;
+  const int32_t *src, *dst, *tokens;
+  int32_t* dev_status;
+};
+cudaError_t launch_copy_pages(const CopyPagesArgs& a, cudaStream_t s);
+cudaError_t launch_remap_pages(int32_t* tables, int64_t n, const int32_t* map, int32_t num_pages,
+                               const DeviceView& dev, cudaStream_t s);
+
+// Attention with a window and sinks (pkv_window_*.cu).
+struct WindowArgs {
+  const void* q;
+  const int32_t *cu, *kv_lens, *page_tables;
+  int32_t B, T, Hq, Hkv, D, P, num_pages, max_pages, window, sinks, dtype, kv_dtype;
+  const void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;   // e4m3 caches, else null
+  float scale;
+  void* out;
+  float* lse;
+  // sequences with fewer new rows than this are the row kernel's, the others the tile
+  // kernel's (INT32_MAX: no tile kernel in this call)
+  int32_t tile_min_q;
+  DeviceView dev;
+};
+cudaError_t launch_window_rows(const WindowArgs& a, cudaStream_t s);
+
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_combine(const AttnArgs& a, cudaStream_t s);
 // Returns cudaErrorNotSupported when the shape has no tensor-core path.

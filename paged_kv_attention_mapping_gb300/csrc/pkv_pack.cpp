@@ -10,11 +10,15 @@
 
 #include "pagedkv.h"
 
-extern "C" int pkv_pack_tick(int32_t num_seqs, const int32_t* q_lens, const int32_t* kv_lens,
-                             const int32_t* page_offsets, const int32_t* page_ids, int32_t page_size,
-                             int32_t num_pages, int32_t max_pages_per_seq, int32_t slot_capacity,
-                             int32_t* order, int32_t* cu_seqlens_q, int32_t* kv_lens_out,
-                             int32_t* page_tables, int64_t* slot_mapping, int32_t* total_q_out) {
+namespace {
+
+// window == 0: every page of a sequence is needed. Otherwise a page may be -1 (freed)
+// where none of its keys is seen by the tick's rows: neither one of the first `sinks`
+// keys nor one of the `window` keys up to a row's own.
+int pack(int32_t num_seqs, const int32_t* q_lens, const int32_t* kv_lens, const int32_t* page_offsets,
+         const int32_t* page_ids, int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
+         int32_t slot_capacity, int32_t window, int32_t sinks, int32_t* order, int32_t* cu_seqlens_q,
+         int32_t* kv_lens_out, int32_t* page_tables, int64_t* slot_mapping, int32_t* total_q_out) {
   if (num_seqs < 0 || page_size < 1 || num_pages < 1 || max_pages_per_seq < 1) return PKV_E_SHAPE;
   if (!cu_seqlens_q || !total_q_out) return PKV_E_NULL;
   if (num_seqs > 0 && (!q_lens || !kv_lens || !page_offsets || !page_ids || !order || !kv_lens_out ||
@@ -32,6 +36,10 @@ extern "C" int pkv_pack_tick(int32_t num_seqs, const int32_t* q_lens, const int3
     if ((int64_t)n * page_size < L) return PKV_E_PAGES;
     for (int32_t j = 0; j < n; ++j) {
       const int32_t p = page_ids[page_offsets[i] + j];
+      if (p == -1 && window > 0) {
+        const int64_t begin = (int64_t)j * page_size, end = begin + page_size;
+        if (begin >= sinks && end <= (int64_t)L - q - window + 1) continue;
+      }
       if (p < 0 || p >= num_pages) return PKV_E_PAGES;
     }
     total_q += q;
@@ -64,6 +72,28 @@ extern "C" int pkv_pack_tick(int32_t num_seqs, const int32_t* q_lens, const int3
   }
   *total_q_out = row;
   return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" int pkv_pack_tick(int32_t num_seqs, const int32_t* q_lens, const int32_t* kv_lens,
+                             const int32_t* page_offsets, const int32_t* page_ids, int32_t page_size,
+                             int32_t num_pages, int32_t max_pages_per_seq, int32_t slot_capacity,
+                             int32_t* order, int32_t* cu_seqlens_q, int32_t* kv_lens_out,
+                             int32_t* page_tables, int64_t* slot_mapping, int32_t* total_q_out) {
+  return pack(num_seqs, q_lens, kv_lens, page_offsets, page_ids, page_size, num_pages, max_pages_per_seq,
+              slot_capacity, 0, 0, order, cu_seqlens_q, kv_lens_out, page_tables, slot_mapping, total_q_out);
+}
+
+extern "C" int pkv_pack_tick_window(int32_t num_seqs, const int32_t* q_lens, const int32_t* kv_lens,
+                                    const int32_t* page_offsets, const int32_t* page_ids, int32_t page_size,
+                                    int32_t num_pages, int32_t max_pages_per_seq, int32_t slot_capacity,
+                                    int32_t window, int32_t sinks, int32_t* order, int32_t* cu_seqlens_q,
+                                    int32_t* kv_lens_out, int32_t* page_tables, int64_t* slot_mapping,
+                                    int32_t* total_q_out) {
+  if (window < 1 || sinks < 0) return PKV_E_SHAPE;
+  return pack(num_seqs, q_lens, kv_lens, page_offsets, page_ids, page_size, num_pages, max_pages_per_seq,
+              slot_capacity, window, sinks, order, cu_seqlens_q, kv_lens_out, page_tables, slot_mapping, total_q_out);
 }
 
 // Position of every packed row (the slot position of its new token):

@@ -228,3 +228,85 @@ extern "C" int pkv_prefix_evict(pkv_pool* p, double now, double ttl, int32_t wan
 }
 
 extern "C" int pkv_prefix_size(const pkv_pool* p) { return p ? (int)p->cache.size() : PKV_E_NULL; }
+
+// A forked sequence holds the pages that its parent has filled (a full page is never
+// written again), and a page of its own for the partly filled last one.
+extern "C" int pkv_pool_fork(pkv_pool* p, const int32_t* pages, int32_t n_pages, int32_t kv_len, int32_t* child,
+                             int32_t* src, int32_t* dst, int32_t* tokens) {
+  if (!p || (n_pages > 0 && (!pages || !child)) || !src || !dst || !tokens) return PKV_E_NULL;
+  if (n_pages < 0 || kv_len < 0) return PKV_E_SHAPE;
+  const int32_t P = p->page_size;
+  const int32_t full = kv_len / P, rest = kv_len - full * P, used = full + (rest > 0 ? 1 : 0);
+  if (used > n_pages) return PKV_E_PAGES;
+  for (int32_t i = 0; i < used; ++i) {
+    const bool freed = pages[i] < 0 && i < full;   // (behind a window)
+    if (!freed && (pages[i] < 0 || pages[i] >= p->num_pages || p->ref[pages[i]] == 0)) return PKV_E_PAGES;
+  }
+  if (rest > 0 && p->free_pages.empty()) return PKV_E_CAPACITY;
+  for (int32_t i = 0; i < full; ++i) {
+    child[i] = pages[i] < 0 ? -1 : pages[i];
+    if (pages[i] >= 0) p->ref[pages[i]] += 1;
+  }
+  if (rest == 0) return 0;
+  const int32_t own = *p->free_pages.begin();
+  p->free_pages.erase(p->free_pages.begin());
+  p->ref[own] = 1;
+  *src = pages[full];
+  *dst = own;
+  *tokens = rest;
+  child[full] = own;
+  return 1;
+}
+
+// Held pages with the highest ids move to the lowest free ids, until the held pages
+// are the lowest or max_moves are made. Sources and targets are then apart: every
+// target was free, and lies below every source.
+extern "C" int pkv_pool_compact(pkv_pool* p, int32_t max_moves, int32_t* src, int32_t* dst, int32_t* page_map) {
+  if (!p || !page_map || (max_moves > 0 && (!src || !dst))) return PKV_E_NULL;
+  if (max_moves < 0) return PKV_E_SHAPE;
+  for (int32_t i = 0; i < p->num_pages; ++i) page_map[i] = i;
+  int32_t n = 0, high = p->num_pages - 1;
+  while (n < max_moves && !p->free_pages.empty()) {
+    while (high >= 0 && p->ref[high] == 0) --high;
+    const int32_t low = *p->free_pages.begin();
+    if (low >= high) break;
+    p->free_pages.erase(p->free_pages.begin());
+    p->ref[low] = p->ref[high];
+    p->ref[high] = 0;
+    p->free_pages.insert(high);
+    page_map[high] = low;
+    src[n] = high;
+    dst[n] = low;
+    ++n;
+  }
+  if (n > 0)
+    for (auto& kv : p->cache) kv.second.page = page_map[kv.second.page];
+  return n;
+}
+
+// Pages that no row at position kv_len or later sees through the window are let go.
+extern "C" int pkv_pool_trim(pkv_pool* p, int32_t* pages, int32_t n_pages, int32_t kv_len, int32_t window,
+                             int32_t sinks) {
+  if (!p || (n_pages > 0 && !pages)) return PKV_E_NULL;
+  if (n_pages < 0 || kv_len < 0 || window < 1 || sinks < 0) return PKV_E_SHAPE;
+  const int32_t P = p->page_size;
+  // the row at position kv_len sees the keys kv_len - window + 1 .. and the sinks
+  const int64_t keep_from = (int64_t)kv_len - window + 1;
+  const int64_t first = ((int64_t)sinks + P - 1) / P;
+  const int64_t last = keep_from > 0 ? keep_from / P : 0;   // first page with a key of the window
+  const int64_t end = last < n_pages ? last : n_pages;
+  // check first, so a bad list changes nothing (a page may appear several times)
+  std::map<int32_t, int32_t> count;
+  for (int64_t i = first; i < end; ++i) {
+    if (pages[i] < 0) continue;
+    if (pages[i] >= p->num_pages || ++count[pages[i]] > p->ref[pages[i]]) return PKV_E_PAGES;
+  }
+  int32_t n = 0;
+  for (int64_t i = first; i < end; ++i) {
+    if (pages[i] < 0) continue;
+    p->drop(pages[i]);
+    pages[i] = -1;
+    ++n;
+  }
+  return n;
+}

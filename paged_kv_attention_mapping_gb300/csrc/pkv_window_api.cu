@@ -1,0 +1,202 @@
+// C-ABI entry points of the windowed layers' calls: host-side checks, then the launches of
+// pkv_norm_rope.cu, pkv_window_rows.cu and pkv_pages.cu.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "pagedkv.h"
+#include "pkv_internal.h"
+
+using namespace pkv;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+int elt_bytes(int dtype) { return dtype == PKV_F32 ? 4 : dtype == PKV_FP8_E4M3 ? 1 : 2; }
+bool source_type(int dtype) { return dtype == PKV_F32 || dtype == PKV_F16 || dtype == PKV_BF16; }
+
+// Strides of rows read or written as 16-byte vectors; the bound keeps a token's offset within 64 bits.
+bool stride_ok(int64_t s, int elt) { return s >= 0 && (s * elt) % 16 == 0 && s < ((int64_t)1 << 31); }
+
+constexpr int32_t MAX_HEADS = 4096;
+
+// head_dim and dtypes that the calls of this file share
+int check(const pkv_cache_desc* c, int32_t src_dtype, const float* k_scale, const float* v_scale) {
+  if (!c) return PKV_E_NULL;
+  if (c->dtype < PKV_F32 || c->dtype > PKV_FP8_E4M3 || !source_type(src_dtype)) return PKV_E_DTYPE;
+  const bool codes = c->dtype == PKV_FP8_E4M3;
+  if (!codes && c->dtype != src_dtype) return PKV_E_DTYPE;
+  if (c->num_pages < 1 || c->page_size < 1 || c->num_kv_heads < 1 || c->num_kv_heads > MAX_HEADS) return PKV_E_SHAPE;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return PKV_E_SHAPE;
+  if ((int64_t)c->num_pages * c->page_size > INT32_MAX) return PKV_E_SHAPE;
+  if (codes && (!k_scale || !v_scale)) return PKV_E_NULL;
+  if (!codes && (k_scale || v_scale)) return PKV_E_DTYPE;
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return PKV_E_ALIGN;
+  return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" int pkv_norm_rope_kv_append(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
+                                       int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
+                                       int64_t v_stride_h, int32_t src_dtype, const void* q_weight,
+                                       const void* k_weight, float eps, const int32_t* positions,
+                                       const float* cos_sin, int32_t max_pos, int32_t rotary_dim,
+                                       int32_t interleaved, const int64_t* slot_mapping, int32_t num_tokens,
+                                       int32_t num_q_heads, void* k_cache, void* v_cache,
+                                       const pkv_cache_desc* cache, const float* k_scale, const float* v_scale,
+                                       void* q_out, int64_t qo_stride_t, int64_t qo_stride_h, pkv_stream_t stream) {
+  const int st = check(cache, src_dtype, k_scale, v_scale);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0 || num_q_heads < 1 || num_q_heads > MAX_HEADS || max_pos < 1) return PKV_E_SHAPE;
+  if (rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > cache->head_dim) return PKV_E_SHAPE;
+  if (!(eps >= 0.f) || !isfinite(eps)) return PKV_E_SHAPE;
+  const int elt = elt_bytes(src_dtype);
+  const int64_t strides[] = {q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h, qo_stride_t,
+                             qo_stride_h};
+  for (int64_t s : strides)
+    if (!stride_ok(s, elt)) return PKV_E_SHAPE;
+  if (num_tokens == 0) return PKV_OK;
+  if (!q || !k || !v || !positions || !cos_sin || !slot_mapping || !k_cache || !v_cache || !q_out) return PKV_E_NULL;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(cos_sin, 16) ||
+      !aligned(slot_mapping, 8) || !aligned(positions, 4))
+    return PKV_E_ALIGN;
+  DeviceView dev;
+  const int ds = current_device(&dev);
+  if (ds != PKV_OK) return ds;
+  NormRopeArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.q_st = q_stride_t;
+  a.q_sh = q_stride_h;
+  a.k_st = k_stride_t;
+  a.k_sh = k_stride_h;
+  a.v_st = v_stride_t;
+  a.v_sh = v_stride_h;
+  a.qo_st = qo_stride_t;
+  a.qo_sh = qo_stride_h;
+  a.pool_slots = (int64_t)cache->num_pages * cache->page_size;
+  a.eps = eps;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.slots = slot_mapping;
+  a.max_pos = max_pos;
+  a.rot = rotary_dim;
+  a.interleaved = interleaved != 0;
+  a.T = num_tokens;
+  a.Hq = num_q_heads;
+  a.Hkv = cache->num_kv_heads;
+  a.D = cache->head_dim;
+  a.dtype = src_dtype;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.q_out = q_out;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.dev_status = dev.status;
+  const cudaError_t e = launch_norm_rope(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "norm_rope_kv_append");
+}
+
+extern "C" int pkv_window_attention(const void* q, int32_t q_dtype, const int32_t* cu_seqlens_q,
+                                    const int32_t* kv_lens, const int32_t* page_tables, int32_t num_seqs,
+                                    int32_t total_q, int32_t num_q_heads, int32_t max_pages_per_seq, int32_t window,
+                                    int32_t sinks, const void* k_cache, const void* v_cache,
+                                    const pkv_cache_desc* cache, const float* k_scale, const float* v_scale,
+                                    float scale, void* out, float* lse, pkv_stream_t stream) {
+  const int st = check(cache, q_dtype, k_scale, v_scale);
+  if (st != PKV_OK) return st;
+  const bool codes = cache->dtype == PKV_FP8_E4M3;
+  if (codes && q_dtype == PKV_F32) return PKV_E_DTYPE;
+  if (num_seqs < 0 || total_q < 0 || num_q_heads < 1 || num_q_heads > MAX_HEADS) return PKV_E_SHAPE;
+  if (window < 1 || sinks < 0 || !(scale > 0.f) || !isfinite(scale)) return PKV_E_SHAPE;
+  if (num_q_heads % cache->num_kv_heads != 0) return PKV_E_SHAPE;
+  const int g = num_q_heads / cache->num_kv_heads;
+  if (g > 8 && g != 16) return PKV_E_SHAPE;
+  if (total_q > 0 && num_seqs > 0 && max_pages_per_seq < 1) return PKV_E_SHAPE;
+  if ((int64_t)max_pages_per_seq * cache->page_size > INT32_MAX) return PKV_E_SHAPE;
+  if (total_q == 0 || num_seqs == 0) return PKV_OK;
+  if (!q || !cu_seqlens_q || !kv_lens || !page_tables || !k_cache || !v_cache || !out) return PKV_E_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(cu_seqlens_q, 4) || !aligned(kv_lens, 4) || !aligned(page_tables, 4) || !aligned(lse, 4))
+    return PKV_E_ALIGN;
+  DeviceView dev;
+  const int ds = current_device(&dev);
+  if (ds != PKV_OK) return ds;
+  WindowArgs a{};
+  a.q = q;
+  a.cu = cu_seqlens_q;
+  a.kv_lens = kv_lens;
+  a.page_tables = page_tables;
+  a.B = num_seqs;
+  a.T = total_q;
+  a.Hq = num_q_heads;
+  a.Hkv = cache->num_kv_heads;
+  a.D = cache->head_dim;
+  a.P = cache->page_size;
+  a.num_pages = cache->num_pages;
+  a.max_pages = max_pages_per_seq;
+  a.window = window;
+  a.sinks = sinks;
+  a.dtype = q_dtype;
+  a.kv_dtype = cache->dtype;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.tile_min_q = INT32_MAX;
+  a.dev = dev;
+  const cudaError_t e = launch_window_rows(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "window_attention");
+}
+
+extern "C" int pkv_copy_pages(void* const* caches, int32_t num_caches, int32_t num_pages, int32_t page_size,
+                              int64_t slot_bytes, const int32_t* src, const int32_t* dst, const int32_t* tokens,
+                              int32_t num_copies, pkv_stream_t stream) {
+  if (num_caches < 0 || num_copies < 0 || num_pages < 1 || page_size < 1) return PKV_E_SHAPE;
+  if (slot_bytes < 16 || slot_bytes % 16 != 0 || slot_bytes > INT32_MAX) return PKV_E_SHAPE;
+  if ((int64_t)num_pages * page_size > INT32_MAX || page_size * slot_bytes > INT32_MAX) return PKV_E_SHAPE;
+  if (num_caches == 0 || num_copies == 0) return PKV_OK;
+  if (!caches || !src || !dst) return PKV_E_NULL;
+  for (int32_t c = 0; c < num_caches; ++c) {
+    if (!caches[c]) return PKV_E_NULL;
+    if (!aligned(caches[c], 16)) return PKV_E_ALIGN;
+  }
+  if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(tokens, 4)) return PKV_E_ALIGN;
+  DeviceView dev;
+  const int ds = current_device(&dev);
+  if (ds != PKV_OK) return ds;
+  CopyPagesArgs a{};
+  a.caches = caches;
+  a.num_caches = num_caches;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.num_copies = num_copies;
+  a.slot_bytes = slot_bytes;
+  a.src = src;
+  a.dst = dst;
+  a.tokens = tokens;
+  a.dev_status = dev.status;
+  const cudaError_t e = launch_copy_pages(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "copy_pages");
+}
+
+extern "C" int pkv_remap_pages(int32_t* page_tables, int64_t num_entries, const int32_t* page_map,
+                               int32_t num_pages, pkv_stream_t stream) {
+  if (num_entries < 0 || num_pages < 1) return PKV_E_SHAPE;
+  if (num_entries == 0) return PKV_OK;
+  if (!page_tables || !page_map) return PKV_E_NULL;
+  if (!aligned(page_tables, 4) || !aligned(page_map, 4)) return PKV_E_ALIGN;
+  DeviceView dev;
+  const int ds = current_device(&dev);
+  if (ds != PKV_OK) return ds;
+  const cudaError_t e = launch_remap_pages(page_tables, num_entries, page_map, num_pages, dev, (cudaStream_t)stream);
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "remap_pages");
+}
