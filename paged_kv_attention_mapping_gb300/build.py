@@ -23,7 +23,7 @@ SOURCES = ["pkv_api.cu", "pkv_append.cu", "pkv_plan.cu", "pkv_rows.cu", "pkv_pre
            "pkv_prefill_tc2.cu", "pkv_pool.cpp", "pkv_rope.cu", "pkv_selftest.cu",
            "pkv_latent_api.cu", "pkv_latent_move.cu", "pkv_latent_attn.cu",
            "pkv_latent_rows.cu", "pkv_latent_prefill.cu",
-           "pkv_window_api.cu", "pkv_window_rows.cu", "pkv_norm_rope.cu", "pkv_pages.cu"]
+           "pkv_window_api.cu", "pkv_window_rows.cu", "pkv_window_tiles.cu", "pkv_norm_rope.cu", "pkv_pages.cu"]
 
 
 def nvcc():

@@ -304,6 +304,8 @@ struct WindowArgs {
   DeviceView dev;
 };
 cudaError_t launch_window_rows(const WindowArgs& a, cudaStream_t s);
+bool window_tiles_supported(int kv_dtype, int D, int P);
+cudaError_t launch_window_tiles(const WindowArgs& a, cudaStream_t s);
 
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_combine(const AttnArgs& a, cudaStream_t s);
@@ -328,6 +330,9 @@ int decode_inflight_bytes(int kv_dtype, int D, int group);
 // TMA tensor map of a contiguous [rows, heads, D] tensor, 128-byte swizzled boxes.
 bool make_map_boxed(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elt, int D, int heads,
                     int64_t rows, int box_cols, int box_rows);
+// The same tensor of 16-bit elements, boxes of 64 columns of several heads.
+bool make_map_heads(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int D, int heads, int64_t rows,
+                    int box_heads, int box_rows);
 
 // 3-D map [rows, heads, cols] with element strides, boxes of 64 columns of one head.
 bool make_map_strided(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int cols, int heads, int64_t rows,

@@ -20,6 +20,9 @@ bool stride_ok(int64_t s, int elt) { return s >= 0 && (s * elt) % 16 == 0 && s <
 
 constexpr int32_t MAX_HEADS = 4096;
 
+// Sequences with this many new rows or more run on the tile kernel where the shape has one.
+constexpr int32_t TILE_MIN_Q = 9;
+
 // head_dim and dtypes that the calls of this file share
 int check(const pkv_cache_desc* c, int32_t src_dtype, const float* k_scale, const float* v_scale) {
   if (!c) return PKV_E_NULL;
@@ -151,9 +154,15 @@ extern "C" int pkv_window_attention(const void* q, int32_t q_dtype, const int32_
   a.scale = scale;
   a.out = out;
   a.lse = lse;
-  a.tile_min_q = INT32_MAX;
   a.dev = dev;
-  const cudaError_t e = launch_window_rows(a, (cudaStream_t)stream);
+  a.tile_min_q = INT32_MAX;
+  // a call of no more rows than sequences is one of single rows (were it not, the row kernel
+  // takes its chunks too)
+  if (total_q > num_seqs && total_q >= TILE_MIN_Q && window_tiles_supported(cache->dtype, cache->head_dim, cache->page_size))
+    a.tile_min_q = TILE_MIN_Q;
+  cudaError_t e = cudaSuccess;
+  if (a.tile_min_q != INT32_MAX) e = launch_window_tiles(a, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = launch_window_rows(a, (cudaStream_t)stream);
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "window_attention");
 }
 

@@ -1,0 +1,791 @@
+// Window attention for chunks of rows, on the tensor cores (tcgen05, TMEM).
+//
+// A query tile is 128 rows of the MMA: PP consecutive positions of one sequence times the
+// G query heads of one KV head (PP = 128 / G), so that a tile's positions, and with them the
+// keys that some row sees beside each row's own window, are few: window + PP - 1 keys and
+// the sinks, against window + 127 for a tile of one head. A work tile is two query tiles
+// (2 PP positions) over the keys that either sees; they share each key and value tile.
+//
+//   warp 0      producer: finds the work tiles, loads Q, then K_j and V_j of each step (128
+//               keys) into a ring of shared-memory slots by TMA
+//   warp 1      TMEM owner and MMA issuer: O_w += P_w V_{j-1} (P_w read from TMEM), S_w =
+//               Q_w K_j^T into the same columns; the pipe runs in issue order
+//   warps 2-5   softmax of query tile 0, one thread a row; warps 6-9 of query tile 1
+//   warp 10     zeroes the rows of a value tile that no row of the work tile sees (the keys
+//               before the first window and after the last row): 0 * NaN must not reach O.
+//               Over an e4m3 cache warps 10 and 11 instead widen every key and value tile to
+//               f16 in its slot, with those rows as zeros.
+// Steps are the key tiles that hold sinks and those from the first window's to the last
+// row's. Each step has a range of 32-key pieces that a query tile sees at all; loads,
+// products and the softmax take that range only (a window's ends are a quarter of a tile
+// wide on average, not half of one and a half), and a query tile without one skips the step.
+// The softmax keeps a running maximum and sum; O is rescaled in TMEM only when a row's
+// maximum grows by more than 2^8. A row can start with pieces that it does not see: its
+// maximum is then -inf, and its weights 0.
+// The bound is the tensor pipe in long windows and the softmax in narrow ones.
+// Every mbarrier wait is bounded (PKV_DEV_TIMEOUT); TMEM accesses are warp-uniform.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "pkv_sm100.cuh"
+#include "pkv_window_common.cuh"
+
+namespace pkv {
+using namespace sm100;
+using namespace window;
+
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr int NQ = 2;                    // query tiles of a work tile
+constexpr int PIECE = 32;                // keys of a piece
+constexpr int SOFTMAX_WARPS = 4 * NQ;
+constexpr int HELPER = 2 + SOFTMAX_WARPS;   // first helper warp
+constexpr uint32_t TMEM_COLS = 512;
+constexpr float RESCALE_LOG2 = 8.f;
+// f16 weights carry this power of two, so that small ones are not lost to f16's smallest
+// exponents; a weight is at most 2^8 (above), 2^15 with it
+constexpr float F16_SHIFT = 7.f;
+
+struct TilesP {
+  const int32_t *cu, *kv_lens, *tables;
+  int32_t B, T, Hq, Hkv, G, PP, P, num_pages, max_pages, window, sinks, min_q, box;
+  int64_t units;
+  PageDiv div;
+  float scale_log2;
+  const float *ks, *vs;
+  void* out;
+  float* lse;
+  int32_t* dev_status;
+};
+
+struct Tile {
+  int valid, b, kvh, row0, np, p_first;
+  int lo, sinks;          // keys of the work tile: [0, sinks) and [lo, p_first + np)
+  int js, j0, steps;      // steps 0 .. js - 1 are key tiles 0 .. js - 1, later ones j0 + step - js
+  int bad;                // a page outside the pool
+};
+
+// Rows [0, a) and [b, e) of a key tile are seen, in the pieces [c0, c1); c0 == c1: none is.
+struct Range {
+  int a, b, e, c0, c1;
+};
+__device__ __forceinline__ Range range_of(int k0, int sinks, int lo, int end) {
+  Range r;
+  r.a = min(max(sinks - k0, 0), BN);
+  r.b = min(max(lo - k0, 0), BN);
+  r.e = min(max(end - k0, 0), BN);
+  if (r.e <= r.b) r.b = r.e = r.a;   // nothing of the window here
+  const int first = r.a > 0 ? 0 : r.b, last = max(r.a, r.e);
+  r.c0 = first / PIECE;
+  r.c1 = last > first ? (last + PIECE - 1) / PIECE : r.c0;
+  return r;
+}
+__device__ __forceinline__ int step_tile(const Tile& t, int i) { return i < t.js ? i : t.j0 + i - t.js; }
+__device__ __forceinline__ Range union_range(const Tile& t, int k0) {
+  return range_of(k0, t.sinks, t.lo, t.p_first + t.np);
+}
+// What query tile w sees.
+__device__ __forceinline__ Range tile_range(const Tile& t, int w, int PP, int window, int sinks, int k0) {
+  const int pa = t.p_first + w * PP, pe = t.p_first + min((w + 1) * PP, t.np);
+  const int lo = max(0, pa - window + 1);
+  return range_of(k0, min(sinks, lo), lo, pe);
+}
+// Rows of the pieces that no row of the work tile sees.
+__device__ __forceinline__ bool has_gaps(const Range& r) { return r.b > r.a || r.e < r.c1 * PIECE; }
+
+// What the widening warps need of one load (e4m3 caches).
+struct LoadDesc {
+  Range r;
+  int zero, q_first, q_par, entry, nq, stop;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int HALVES = D / 64;
+  static constexpr int NS = D == 128 ? 5 : 8;
+  static constexpr uint32_t Q_BYTES = BM * D * 2;
+  static constexpr uint32_t SLOT = BN * D * 2;
+  static constexpr uint32_t SMEM = NQ * Q_BYTES + NS * SLOT + 1024;
+  static_assert(SMEM <= 232448 - 2048, "shared memory");
+};
+
+__device__ __forceinline__ void mma_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]));
+}
+
+// max(a, b, c) in one instruction; a NaN is passed over, as by fmaxf.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+  uint32_t out;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out) : "h"((uint16_t)codes));
+  return out;
+}
+
+// e4m3 tiles: codes lie in the upper half of the slot, 128 a row, 128-byte swizzled; the
+// f16 tile is what a 16-bit load would have made of it (two 64-column halves). A lane reads a
+// row's codes before it writes the row, and row r's codes are overwritten by row r alone.
+__device__ __forceinline__ void widen_rows(unsigned char* slot, const LoadDesc& d, int warp, int lane) {
+  const unsigned char* stg = slot + BN * 128;
+  for (int r = d.r.c0 * PIECE + warp * 32 + lane; r < d.r.c1 * PIECE; r += 64) {
+    const int sw = r & 7;
+    uint4 c[8];
+    if (d.zero && !(r < d.r.a || (r >= d.r.b && r < d.r.e))) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) c[k] = make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) c[k] = *reinterpret_cast<const uint4*>(stg + r * 128 + ((k ^ sw) << 4));
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+      uint32_t h[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        h[2 * q] = widen2(w[q]);
+        h[2 * q + 1] = widen2(w[q] >> 16);
+      }
+      unsigned char* row = slot + (k >> 2) * BN * 128 + r * 128;
+      const int ch = (k & 3) * 2;
+      *reinterpret_cast<uint4*>(row + ((ch ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(row + (((ch + 1) ^ sw) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+  }
+}
+
+// bf16 queries over an e4m3 cache: f16 in place, each row times the power of two that brings its
+// largest value to 2^8 .. 2^9 (bf16 has exponents that f16 lacks); its inverse's exponent goes to `back`.
+__device__ __forceinline__ void narrow_q(unsigned char* q, uint8_t* back, int lane) {
+  for (int r = lane; r < BM; r += 32) {
+    float top = 0.f;
+    for (int c = 0; c < 16; ++c) {
+      const uint4 x = *reinterpret_cast<const uint4*>(q + (c >> 3) * BM * 128 + r * 128 + ((c & 7) << 4));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+    }
+    const int eb = (int)(__float_as_uint(top) >> 23);
+    const int fe = eb == 0 || eb == 255 ? 127 : min(max(262 - eb, 2), 252);
+    const float f = __uint_as_float((uint32_t)fe << 23);
+    back[r] = (uint8_t)(254 - fe);
+    for (int c = 0; c < 16; ++c) {
+      uint4* at = reinterpret_cast<uint4*>(q + (c >> 3) * BM * 128 + r * 128 + ((c & 7) << 4));
+      uint4 x = *at;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = pack2<__half>(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+      *at = x;
+    }
+  }
+}
+
+// TQ: type of q and out. KV8: e4m3 caches (head_dim 128), products in f16.
+template <int D, typename TQ, bool KV8>
+__global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
+    window_tiles_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                        const __grid_constant__ CUtensorMap mv, const __grid_constant__ TilesP p) {
+  using C = Cfg<D>;
+  using MT = typename std::conditional<KV8, __half, TQ>::type;
+  constexpr bool BF16 = std::is_same<MT, __nv_bfloat16>::value;
+  constexpr bool QCONV = KV8 && std::is_same<TQ, __nv_bfloat16>::value;
+  constexpr float SHIFT = BF16 ? 0.f : F16_SHIFT;
+  constexpr int NS = C::NS;
+  static_assert(!KV8 || D == 128, "e4m3 tiles are one 128-code row wide");
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = (unsigned char*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  unsigned char* sQ = sm;
+  unsigned char* sRing = sQ + NQ * C::Q_BYTES;
+
+  // Work tiles pass through two entries (tile t in entry t & 1): the producer fills the next
+  // one and loads its Q while tile t finishes.
+  __shared__ __align__(8) uint64_t bar_q, bar_qempty, bar_full[NS], bar_empty[NS], bar_sfull[NQ],
+      bar_pfull[NQ], bar_odone[NQ], bar_tfull[2], bar_tempty[2], bar_drain;
+  // loads that a helper warp works on before the MMA may read them land here: the value tiles
+  // with rows to zero; over an e4m3 cache every tile, and bf16 queries
+  __shared__ __align__(8) uint64_t bar_land[NS], bar_qland;
+  __shared__ LoadDesc s_ld[KV8 ? NS : 1];
+  __shared__ uint8_t s_back[2][QCONV ? NQ * BM : 1];   // (by entry: a slow softmax may still read the last tile's)
+  __shared__ Tile s_tile[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int32_t s_err;
+  __shared__ volatile int s_abort;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0) check_cu(p.cu, p.B, p.T, p.dev_status);
+  if (tid == 0) {
+    mbar_init(&bar_q, QCONV ? 2 : 1);
+    mbar_init(&bar_qempty, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&bar_full[s], KV8 ? 2 : 1);
+      mbar_init(&bar_empty[s], 1);
+      mbar_init(&bar_land[s], 1);
+    }
+    mbar_init(&bar_qland, 1);
+    for (int w = 0; w < NQ; ++w) {
+      mbar_init(&bar_sfull[w], 1);
+      mbar_init(&bar_pfull[w], BM);
+      mbar_init(&bar_odone[w], 1);
+    }
+    for (int e = 0; e < 2; ++e) {
+      mbar_init(&bar_tfull[e], 1);
+      mbar_init(&bar_tempty[e], 1 + SOFTMAX_WARPS + (KV8 ? 0 : 1));   // MMA, softmax and zeroing warps
+    }
+    mbar_init(&bar_drain, 1);
+    fence_mbar_init();
+    s_abort = 0;
+    s_err = 0;
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
+  }
+  if (warp == 1) tmem_alloc(&s_tmem, TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return warp_wait_or_abort(bar, parity, &s_abort, &s_err, p.dev_status);
+  };
+
+  if (warp == 0) {
+    // --------------------------------------------------------------- producer
+    // a bit a slot: parity of its loads, of those that land for a helper, and whether the last did
+    uint32_t ring = 0, loads = 0, landing = 0, last_land = 0, used = 0;
+    bool ok = true;
+    int64_t u = blockIdx.x;
+    for (uint32_t t = 0; ok; ++t) {
+      // the next unit with rows for this kernel
+      Tile ti;
+      ti.valid = 0;
+      ti.bad = 0;
+      for (; u < p.units && !ti.valid; u += gridDim.x) {
+        const int64_t slot = u / p.Hkv;
+        const int b = find_seq(p.cu, p.B, slot, NQ * p.PP, lane);
+        const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), L = __ldg(p.kv_lens + b);
+        const int64_t q0 = (slot - first_piece(b, c0, NQ * p.PP)) * (NQ * p.PP);
+        const int n = c1 - c0;
+        if (c0 < 0 || c1 > p.T || q0 < 0 || q0 >= n || n < p.min_q) continue;
+        ti.kvh = (int)(u - slot * p.Hkv);
+        if (L < n || L > (int64_t)p.max_pages * p.P) {
+          if (q0 == 0 && ti.kvh == 0 && lane == 0) atomicOr(p.dev_status, PKV_DEV_BAD_LENGTHS);
+          continue;
+        }
+        ti.b = b;
+        ti.row0 = c0 + (int)q0;
+        ti.np = min(NQ * p.PP, n - (int)q0);
+        ti.p_first = L - n + (int)q0;
+        const int p_last = ti.p_first + ti.np - 1;
+        ti.lo = max(0, ti.p_first - p.window + 1);
+        ti.sinks = min(p.sinks, ti.lo);
+        ti.js = (ti.sinks + BN - 1) / BN;
+        ti.j0 = max(ti.js, ti.lo / BN);
+        ti.steps = ti.js + max(0, p_last / BN - ti.j0 + 1);
+        ti.valid = 1;
+      }
+      const uint32_t e = t & 1;
+      // entry e is free again once every consumer is done with tile t - 2
+      if (t >= 2 && !wait(&bar_tempty[e], ((t >> 1) - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        s_tile[e] = ti;
+        mbar_arrive(&bar_tfull[e]);   // releases the entry's fields to its waiters
+      }
+      __syncwarp();
+      if (!ti.valid) break;
+      const int nq = ti.np > p.PP ? 2 : 1;
+      if (t >= 1 && !wait(&bar_qempty, (t - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        uint64_t* bar = QCONV ? &bar_qland : &bar_q;
+        mbar_arrive_expect_tx(bar, nq * C::HALVES * (uint32_t)(p.G * p.PP * 128));
+        for (int w = 0; w < nq; ++w)
+#pragma unroll
+          for (int h = 0; h < C::HALVES; ++h)
+            tma_load_3d(sQ + w * C::Q_BYTES + h * BM * 128, &mq, bar, h * 64, ti.kvh * p.G, ti.row0 + w * p.PP);
+      }
+      const int32_t* pt = p.tables + (int64_t)ti.b * p.max_pages;
+      for (int i = 0; i < ti.steps && ok; ++i) {
+        const int k0 = step_tile(ti, i) * BN;
+        const Range r = union_range(ti, k0);
+        // lane (block, half): box rows of one page, 64 channels (e4m3: all 128); the rows of
+        // blocks without a key that is seen are left as they are
+        constexpr int LH = KV8 ? 1 : C::HALVES;
+        const int row = (lane / LH) * p.box, half = lane % LH;
+        const bool in = row < r.c1 * PIECE && row + p.box > r.c0 * PIECE && row < BN &&
+                        (row < r.a || (row < r.e && row + p.box > r.b));
+        int at = 0;
+        bool bad = false;
+        if (in) {
+          const int pg = page_of(k0 + row, p.div);
+          const int id = __ldg(pt + pg);
+          bad = id < 0 || id >= p.num_pages;
+          at = id * p.P + (k0 + row - pg * p.P);
+        }
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&s_tile[e].bad, 1);
+        const bool load = in && !bad;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)(p.box * 128);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t slot = ring % NS, round = ring / NS;
+          ++ring;
+          if (!wait(&bar_empty[slot], (round & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          unsigned char* dst = sRing + slot * C::SLOT + (KV8 ? BN * 128 : 0);
+          const bool land = KV8 || (kv == 1 && has_gaps(r));
+          uint64_t* bar = land ? &bar_land[slot] : &bar_full[slot];
+          const uint32_t bit = 1u << slot;
+          used |= bit;
+          loads ^= bit;
+          if (land) landing ^= bit;
+          last_land = land ? last_land | bit : last_land & ~bit;
+          if constexpr (KV8) {
+            if (lane == 0) {
+              LoadDesc d;
+              d.r = r;
+              d.zero = kv;
+              d.q_first = QCONV && i == 0 && kv == 0;
+              d.q_par = t & 1;
+              d.entry = (int)e;
+              d.nq = nq;
+              d.stop = 0;
+              s_ld[slot] = d;
+            }
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          __syncwarp();
+          if (load) tma_load_3d(dst + half * BN * 128 + row * 128, kv ? &mv : &mk, bar, half * 64, ti.kvh, at);
+        }
+      }
+    }
+    if constexpr (KV8) {
+      // no more loads: let the widening warps leave
+      const uint32_t slot = ring % NS, round = ring / NS;
+      if (ok && wait(&bar_empty[slot], (round & 1) ^ 1) && lane == 0) {
+        s_ld[slot].stop = 1;
+        mbar_arrive(&bar_land[slot]);
+      }
+    }
+    if (!ok && lane == 0) {
+      // let every copy this warp issued land before the CTA may exit (a slot's loads before its last were
+      // consumed; parity 1 after the first load: phase 0)
+      for (int s = 0; s < NS; ++s)
+        if (used >> s & 1) {
+          const bool land = last_land >> s & 1;
+          mbar_wait(land ? &bar_land[s] : &bar_full[s], (((land ? landing : loads) >> s) & 1) ^ 1, 500000000ull);
+        }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMA issuer
+    const uint32_t id_pv = idesc_f16(BM, D, BF16, true), id_qk = idesc_f16(BM, 0, BF16, false);
+    const uint32_t ring_u32 = smem_u32(sRing);
+    const uint64_t qd = smem_desc(smem_u32(sQ), 16, 1024, LAYOUT_SW128);
+    uint32_t p_use[NQ] = {0, 0}, ring = 0;
+    auto issue_qk = [&](int w, uint32_t slot, const Range& r) {
+      const uint32_t idesc = id_qk | ((uint32_t)((r.c1 - r.c0) * (PIECE >> 3)) << 17);
+      const uint64_t kd = smem_desc(ring_u32 + slot * C::SLOT + r.c0 * PIECE * 128, 16, 1024, LAYOUT_SW128);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk / 4) * BM * 128 + (kk % 4) * 32, offk = (kk / 4) * BN * 128 + (kk % 4) * 32;
+        mma_f16_ss_warp(tmem + w * 128 + r.c0 * PIECE, qd + (uint64_t)((w * C::Q_BYTES + off) >> 4),
+                        kd + (uint64_t)(offk >> 4), idesc, kk > 0 ? 1u : 0u);
+      }
+      mma_commit_warp(&bar_sfull[w]);
+    };
+    bool ok = true;
+    for (uint32_t t = 0; ok; ++t) {
+      const uint32_t e = t & 1;
+      if (!wait(&bar_tfull[e], (t >> 1) & 1)) break;
+      const Tile ti = s_tile[e];
+      if (!ti.valid) break;
+      const int nq = ti.np > p.PP ? 2 : 1;
+      ok = wait(&bar_q, t & 1);
+      tc_fence_after();
+      Range prev[NQ];
+      bool begun[NQ] = {false, false};
+      // step j: O_w (+)= P_w V_{j-1}, then S_w = Q_w K_j^T, for each query tile w that sees it
+      for (int j = 0; j <= ti.steps && ok; ++j) {
+        const bool qk = j < ti.steps;
+        const int k0 = qk ? step_tile(ti, j) * BN : 0;
+        const uint32_t lk = ring + 2 * j, lv = lk - 1;          // ring numbers of K_j and V_{j-1}
+        const uint32_t ks = lk % NS, vs = lv % NS;
+        bool k_here = false;
+        if (j > 0) {
+          ok = wait(&bar_full[vs], (lv / NS) & 1);
+          if (!ok) break;
+        }
+        const uint64_t vd = smem_desc(ring_u32 + vs * C::SLOT, BN * 128, 1024, LAYOUT_SW128);
+#pragma unroll
+        for (int w = 0; w < NQ; ++w) {
+          if (w >= nq) break;
+          if (j > 0 && prev[w].c1 > prev[w].c0) {
+            if (!wait(&bar_pfull[w], p_use[w] & 1)) {
+              ok = false;
+              break;
+            }
+            ++p_use[w];
+            tc_fence_after();
+            for (int c = prev[w].c0; c < prev[w].c1; ++c) {
+#pragma unroll
+              for (int h = 0; h < PIECE / 16; ++h) {
+                const int kk = c * (PIECE / 16) + h;
+                mma_ts_warp(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), id_pv,
+                            begun[w] ? 1u : 0u);
+                begun[w] = true;
+              }
+            }
+            // the key tile of the query tile's last row is its last step
+            const int last = (ti.p_first + min((w + 1) * p.PP, ti.np) - 1) / BN;
+            if (step_tile(ti, j - 1) == last) mma_commit_warp(&bar_odone[w]);
+          }
+          if (j > 0 && w == nq - 1) mma_commit_warp(&bar_empty[vs]);
+          prev[w].c0 = prev[w].c1 = 0;
+          if (qk) {
+            prev[w] = tile_range(ti, w, p.PP, p.window, p.sinks, k0);
+            if (!k_here) {
+              if (!wait(&bar_full[ks], (lk / NS) & 1)) {
+                ok = false;
+                break;
+              }
+              k_here = true;
+            }
+            if (prev[w].c1 > prev[w].c0) issue_qk(w, ks, prev[w]);
+          }
+        }
+        if (!ok) break;
+        if (qk) {
+          mma_commit_warp(&bar_empty[ks]);
+          if (j == ti.steps - 1) mma_commit_warp(&bar_qempty);
+        }
+      }
+      ring += 2 * ti.steps;
+      if (ok && lane == 0) mbar_arrive(&bar_tempty[e]);
+      __syncwarp();
+    }
+  } else if (warp >= HELPER) {
+    if constexpr (KV8) {
+      // ------------------------------------------------------ e4m3: widening
+      const int cw = warp - HELPER;
+      for (uint32_t n = 0;; ++n) {
+        const uint32_t slot = n % NS;
+        if (!wait(&bar_land[slot], (n / NS) & 1)) break;
+        // (written before the load's barrier completed)
+        const LoadDesc d = s_ld[slot];
+        if (d.stop) break;
+        if (QCONV && d.q_first) {
+          if (!wait(&bar_qland, d.q_par)) break;
+          if (cw < d.nq) narrow_q(sQ + cw * C::Q_BYTES, &s_back[d.entry][cw * BM], lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_q);
+        }
+        widen_rows(sRing + slot * C::SLOT, d, cw, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_full[slot]);
+      }
+    } else {
+      // -------------------------------------- zeros for values that nobody sees
+      uint32_t ring = 0, landed = 0;   // landed: parity of each slot's loads of this kind, a bit a slot
+      bool ok = true;
+      for (uint32_t t = 0; ok; ++t) {
+        const uint32_t e = t & 1;
+        if (!wait(&bar_tfull[e], (t >> 1) & 1)) break;
+        const Tile ti = s_tile[e];
+        if (!ti.valid) break;
+        for (int i = 0; i < ti.steps; ++i) {
+          const Range r = union_range(ti, step_tile(ti, i) * BN);
+          const uint32_t slot = (ring + 2 * i + 1) % NS;
+          if (!has_gaps(r)) continue;
+          if (!wait(&bar_land[slot], (landed >> slot) & 1)) {
+            ok = false;
+            break;
+          }
+          landed ^= 1u << slot;
+          for (int h = 0; h < C::HALVES; ++h) {
+            uint4* base = reinterpret_cast<uint4*>(sRing + slot * C::SLOT + h * BN * 128);
+            for (int q = max(r.a, r.c0 * PIECE) * 8 + lane; q < r.b * 8; q += 32) base[q] = make_uint4(0, 0, 0, 0);
+            for (int q = r.e * 8 + lane; q < r.c1 * PIECE * 8; q += 32) base[q] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();   // the MMA (async proxy) reads what these threads wrote
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_full[slot]);
+        }
+        ring += 2 * ti.steps;
+        if (ok && lane == 0) mbar_arrive(&bar_tempty[e]);
+        __syncwarp();
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int w = (warp - 2) >> 2;
+    const int i = (warp & 3) * 32 + lane;         // row within the tile; warp & 3: its TMEM lane quarter
+    const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = w * 128, o_col = 256 + w * 128;
+    const int pi = i / p.G, head = i - pi * p.G;
+    uint32_t my_s = 0, my_o = 0;
+    for (uint32_t t = 0;; ++t) {
+      const uint32_t e = t & 1;
+      if (!wait(&bar_tfull[e], (t >> 1) & 1)) break;
+      const Tile ti = s_tile[e];
+      if (!ti.valid) break;
+      bool ok = true;
+      // (each tile's: a phase that is not waited for would be mistaken for the next)
+      if constexpr (QCONV) {
+        if (!wait(&bar_q, t & 1)) break;
+      }
+      const int npw = min(ti.np - w * p.PP, p.PP);   // positions of this query tile
+      if (npw > 0) {
+        const int pa = ti.p_first + w * p.PP, pb = pa + npw - 1;
+        const int p_i = min(pa + pi, pb);
+        float sc = p.scale_log2;
+        if constexpr (KV8) sc *= __ldg(p.ks + ti.kvh);
+        if constexpr (QCONV) sc *= __uint_as_float((uint32_t)s_back[e][w * BM + i] << 23);
+        float m_run = -INFINITY, l_run = 0.f;
+        bool first = true;
+        for (int j = 0; j < ti.steps; ++j) {
+          const int k0 = step_tile(ti, j) * BN;
+          const Range rg = tile_range(ti, w, p.PP, p.window, p.sinks, k0);
+          if (rg.c1 <= rg.c0) continue;
+          // S_w complete also means every earlier MMA (the PV that read P_w) is done
+          if (!wait(&bar_sfull[w], my_s & 1)) {
+            ok = false;
+            break;
+          }
+          ++my_s;
+          tc_fence_after();
+          uint32_t r[BN / PIECE][PIECE];
+#pragma unroll
+          for (int c = 0; c < BN / PIECE; ++c)
+            if (c >= rg.c0 && c < rg.c1) tmem_ld32(tmem + lrow + s_col + c * PIECE, r[c]);
+          tmem_wait_ld();
+          // columns <= hi, and > lo or < se, are seen
+          const int hi = p_i - k0, lo = max(p_i - p.window, -1) - k0, se = p.sinks - k0;
+          const bool mask_hi = rg.c1 * PIECE - 1 > pa - k0;
+          const bool mask_lo = rg.c0 * PIECE <= max(pb - p.window, -1) - k0 && rg.c1 * PIECE > se;
+          float mx[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < BN / PIECE; ++c) {
+            if (c >= rg.c0 && c < rg.c1) {
+              reg_fence(r[c]);
+              if (mask_hi) {
+#pragma unroll
+                for (int x = 0; x < PIECE; ++x)
+                  if (c * PIECE + x > hi) r[c][x] = __float_as_uint(-INFINITY);
+              }
+              if (mask_lo) {
+#pragma unroll
+                for (int x = 0; x < PIECE; ++x)
+                  if (c * PIECE + x <= lo && c * PIECE + x >= se) r[c][x] = __float_as_uint(-INFINITY);
+              }
+#pragma unroll
+              for (int x = 0; x < PIECE; x += 2)
+                mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(r[c][x]), __uint_as_float(r[c][x + 1]));
+            }
+          }
+          const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
+          const bool grow = mt > m_run + RESCALE_LOG2 || (m_run == -INFINITY && mt > m_run);
+          const float m_new = grow ? mt : m_run;
+          if (!first && __any_sync(0xffffffffu, grow)) {
+            const float alpha = grow ? ex2(m_run - m_new) : 1.f;
+            l_run *= alpha;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32_wait(tmem + lrow + o_col + c * 32, o);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+              tmem_st32_wait(tmem + lrow + o_col + c * 32, o);
+            }
+          }
+          m_run = m_new;
+          first = false;
+          const float nm = SHIFT - (m_run == -INFINITY ? 0.f : m_run);
+          const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
+          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < BN / PIECE; ++c) {
+            if (c >= rg.c0 && c < rg.c1) {
+              uint32_t pw[16];
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                const float2 y = __ffma2_rn(
+                    make_float2(__uint_as_float(r[c][2 * x]), __uint_as_float(r[c][2 * x + 1])), sc2, nm2);
+                const float a = ex2(y.x), b = ex2(y.y);
+                ls[x & 1] = __fadd2_rn(ls[x & 1], make_float2(a, b));
+                pw[x] = pack2<MT>(a, b);
+              }
+              tmem_st16(tmem + lrow + s_col + c * 16, pw);
+              tmem_wait_st();
+              reg_fence16(pw);
+            }
+          }
+          l_run += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+          tc_fence_before();
+          mbar_arrive(&bar_pfull[w]);
+        }
+        if (ok) ok = wait(&bar_odone[w], my_o & 1);
+        ++my_o;
+        tc_fence_after();
+        if (ok) {
+          const int bad = *(volatile const int*)&s_tile[e].bad;
+          const bool store = pi < npw && !bad;
+          const float inv = (KV8 ? __ldg(p.vs + ti.kvh) : 1.f) / l_run;
+          const int64_t at = (int64_t)(ti.row0 + w * p.PP + pi) * p.Hq + ti.kvh * p.G + head;
+          TQ* dst = (TQ*)p.out + at * D;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32_wait(tmem + lrow + o_col + c * 32, o);
+            if (!store) continue;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              uint4 pk;
+              pk.x = pack2<TQ>(__uint_as_float(o[v * 8 + 0]) * inv, __uint_as_float(o[v * 8 + 1]) * inv);
+              pk.y = pack2<TQ>(__uint_as_float(o[v * 8 + 2]) * inv, __uint_as_float(o[v * 8 + 3]) * inv);
+              pk.z = pack2<TQ>(__uint_as_float(o[v * 8 + 4]) * inv, __uint_as_float(o[v * 8 + 5]) * inv);
+              pk.w = pack2<TQ>(__uint_as_float(o[v * 8 + 6]) * inv, __uint_as_float(o[v * 8 + 7]) * inv);
+              *reinterpret_cast<uint4*>(dst + c * 32 + v * 8) = pk;
+            }
+          }
+          if (store && p.lse) p.lse[at] = (m_run + __log2f(l_run) - SHIFT) * LN2;
+          if (bad && i == 0) atomicOr(p.dev_status, PKV_DEV_BAD_PAGE);
+        }
+        tc_fence_before();
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_tempty[e]);
+    }
+  }
+
+  if (warp == 1) {
+    // every MMA this warp issued is complete before TMEM is released
+    mma_commit_warp(&bar_drain);
+    mbar_wait(&bar_drain, 0, 500000000ull);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+template <int D, typename TQ, bool KV8>
+cudaError_t launch(const WindowArgs& a, cudaStream_t s) {
+  using C = Cfg<D>;
+  static std::atomic<uint64_t> ready{0};   // devices whose kernel attribute is set
+  const uint64_t bit = (uint64_t)1 << (a.dev.id & 63);
+  if (!(ready.load() & bit)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(window_tiles_kernel<D, TQ, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit);
+  }
+  TilesP p;
+  p.cu = a.cu;
+  p.kv_lens = a.kv_lens;
+  p.tables = a.page_tables;
+  p.B = a.B;
+  p.T = a.T;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.G = a.Hq / a.Hkv;
+  p.PP = BM / p.G;
+  p.P = a.P;
+  p.num_pages = a.num_pages;
+  p.max_pages = a.max_pages;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.min_q = a.tile_min_q;
+  p.box = a.P < PIECE ? a.P : PIECE;
+  p.units = ((int64_t)a.B + a.T / (NQ * p.PP)) * a.Hkv;
+  p.div = page_div(a.P);
+  p.scale_log2 = a.scale * LOG2E;
+  p.ks = a.k_scale;
+  p.vs = a.v_scale;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.dev_status = a.dev.status;
+  const CUtensorMapDataType dt =
+      std::is_same<TQ, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapDataType kdt = KV8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : dt;
+  const int kelt = KV8 ? 1 : 2;
+  const int64_t rows = (int64_t)a.num_pages * a.P;
+  CUtensorMap mq, mk, mv;
+  if (!make_map_heads(&mq, a.q, dt, D, a.Hq, a.T, p.G, p.PP) ||
+      !make_map_boxed(&mk, a.k_cache, kdt, kelt, D, a.Hkv, rows, 128 / kelt, p.box) ||
+      !make_map_boxed(&mv, a.v_cache, kdt, kelt, D, a.Hkv, rows, 128 / kelt, p.box))
+    return cudaErrorInvalidValue;
+  const int64_t grid = p.units < a.dev.num_sms ? p.units : a.dev.num_sms;
+  KernelTimer timer("window_tiles", s);
+  return launch_after_trigger(window_tiles_kernel<D, TQ, KV8>, dim3((unsigned)grid),
+                              dim3((HELPER + (KV8 ? 2 : 1)) * 32), C::SMEM, s, mq, mk, mv, p);
+}
+
+}  // namespace
+
+// 16-bit caches at head_dim 64 and 128, e4m3 caches at 128, pages that 128-key tiles divide or that
+// divide them (blocks of at least 8 rows: one swizzle pattern).
+bool window_tiles_supported(int kv_dtype, int D, int P) {
+  if (kv_dtype == PKV_F32 || D == 256 || (kv_dtype == PKV_FP8_E4M3 && D != 128)) return false;
+  return P % BN == 0 || (P >= 8 && BN % P == 0);
+}
+
+cudaError_t launch_window_tiles(const WindowArgs& a, cudaStream_t s) {
+  if (a.kv_dtype == PKV_FP8_E4M3)
+    return a.dtype == PKV_BF16 ? launch<128, __nv_bfloat16, true>(a, s) : launch<128, __half, true>(a, s);
+  if (a.dtype == PKV_BF16) return a.D == 64 ? launch<64, __nv_bfloat16, false>(a, s) : launch<128, __nv_bfloat16, false>(a, s);
+  return a.D == 64 ? launch<64, __half, false>(a, s) : launch<128, __half, false>(a, s);
+}
+
+}  // namespace pkv
