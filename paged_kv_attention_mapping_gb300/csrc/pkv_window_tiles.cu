@@ -129,13 +129,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                 "+r"(r[15]));
-}
-
 // max(a, b, c) in one instruction; a NaN is passed over, as by fmaxf.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
@@ -217,6 +210,122 @@ __device__ __forceinline__ void narrow_q(unsigned char* q, uint8_t* back, int la
       *at = x;
     }
   }
+}
+
+// One row of one step: its scores from TMEM, the running maximum and sum, O rescaled where the
+// maximum grew, the weights written over the scores (16-bit pairs: the layout of an A operand).
+struct RowStep {
+  float sc;          // raw scores to log2 units
+  int hi, lo, se;    // columns <= hi, and > lo or < se, are seen
+  int c0, c1;        // pieces
+  uint32_t ts, to;   // TMEM: scores and output of this row's lanes
+};
+
+// Which of a piece's 32 columns are seen: a few shifts a piece, then a select a column.
+__device__ __forceinline__ uint32_t seen_bits(const RowStep& st, int c) {
+  const int h = st.hi - c * PIECE, l = st.lo - c * PIECE, s = st.se - c * PIECE;
+  const uint32_t mh = h < 0 ? 0u : h >= 31 ? ~0u : (2u << h) - 1u;
+  const uint32_t ml = l < 0 ? ~0u : l >= 31 ? 0u : ~((2u << l) - 1u);
+  const uint32_t ms = s <= 0 ? 0u : s >= 32 ? ~0u : (1u << s) - 1u;
+  return mh & (ml | ms);
+}
+__device__ __forceinline__ void hide(uint32_t (&r)[PIECE], uint32_t seen) {
+#pragma unroll
+  for (int x = 0; x < PIECE; ++x)
+    if (!(seen >> x & 1)) r[x] = __float_as_uint(-INFINITY);
+}
+__device__ __forceinline__ void max_of(const uint32_t (&r)[PIECE], float (&mx)[8]) {
+#pragma unroll
+  for (int x = 0; x < PIECE; x += 2)
+    mx[(x >> 1) & 7] = max3(mx[(x >> 1) & 7], __uint_as_float(r[x]), __uint_as_float(r[x + 1]));
+}
+
+template <int D>
+__device__ __forceinline__ void new_maximum(const RowStep& st, const float (&mx)[8], bool first, float& m_run,
+                                            float& l_run) {
+  const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * st.sc;
+  const bool grow = mt > m_run + RESCALE_LOG2;   // (from -inf: any maximum but -inf)
+  const float m_new = grow ? mt : m_run;
+  if (!first && __any_sync(0xffffffffu, grow)) {
+    const float alpha = grow ? ex2(m_run - m_new) : 1.f;
+    l_run *= alpha;
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      tmem_ld32_wait(st.to + c * 32, o);
+#pragma unroll
+      for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+      tmem_st32_wait(st.to + c * 32, o);
+    }
+  }
+  m_run = m_new;
+}
+
+// Weights of a piece, their sums by pairs of columns, and where they go.
+template <typename MT>
+__device__ __forceinline__ void weigh(const uint32_t (&r)[PIECE], float2 sc2, float2 nm2, float2 (&ls)[4], uint32_t to) {
+  uint32_t pw[16];
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * x]), __uint_as_float(r[2 * x + 1])), sc2, nm2);
+    const float a = ex2(y.x), b = ex2(y.y);
+    ls[x & 3] = __fadd2_rn(ls[x & 3], make_float2(a, b));
+    pw[x] = pack2<MT>(a, b);
+  }
+  tmem_st16(to, pw);
+}
+
+// The softmax threads share their sub-partitions with the MMA warp, whose issue slots dense work
+// here takes away: three-input maxima, and fp32x2 multiply-adds and sums. A whole step (all
+// four pieces, every column seen) keeps its scores in registers; another reads them twice, a
+// piece at a time: with both forms over registers the kernel spills (window 2048, 16384 tokens:
+// 2261 us against 588 with one masked form for all steps).
+template <int D, typename MT>
+__device__ __forceinline__ void softmax_step(const RowStep& st, bool whole, bool first, float& m_run, float& l_run) {
+  constexpr float SHIFT = std::is_same<MT, __nv_bfloat16>::value ? 0.f : F16_SHIFT;
+  constexpr int NC = BN / PIECE;
+  float mx[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
+  float2 ls[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
+  if (whole) {
+    uint32_t r[NC][PIECE];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) tmem_ld32(st.ts + c * PIECE, r[c]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < NC; ++c) reg_fence(r[c]);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) max_of(r[c], mx);
+    new_maximum<D>(st, mx, first, m_run, l_run);
+    const float nm = SHIFT - (m_run == -INFINITY ? 0.f : m_run);
+    const float2 sc2 = make_float2(st.sc, st.sc), nm2 = make_float2(nm, nm);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) weigh<MT>(r[c], sc2, nm2, ls, st.ts + c * 16);
+  } else {
+#pragma unroll 1
+    for (int c = st.c0; c < st.c1; ++c) {
+      uint32_t r[PIECE];
+      tmem_ld32_wait(st.ts + c * PIECE, r);
+      hide(r, seen_bits(st, c));
+      max_of(r, mx);
+    }
+    new_maximum<D>(st, mx, first, m_run, l_run);
+    const float nm = SHIFT - (m_run == -INFINITY ? 0.f : m_run);
+    const float2 sc2 = make_float2(st.sc, st.sc), nm2 = make_float2(nm, nm);
+    // (the weights of piece c go over scores of pieces up to c / 2)
+#pragma unroll 1
+    for (int c = st.c0; c < st.c1; ++c) {
+      uint32_t r[PIECE];
+      tmem_ld32_wait(st.ts + c * PIECE, r);
+      hide(r, seen_bits(st, c));
+      weigh<MT>(r, sc2, nm2, ls, st.ts + c * 16);
+    }
+  }
+  tmem_wait_st();
+  l_run += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
 }
 
 // TQ: type of q and out. KV8: e4m3 caches (head_dim 128), products in f16.
@@ -448,20 +557,22 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
       const int nq = ti.np > p.PP ? 2 : 1;
       ok = wait(&bar_q, t & 1);
       tc_fence_after();
-      Range prev[NQ];
+      Range prev[NQ], now[NQ];
       bool begun[NQ] = {false, false};
-      // step j: O_w (+)= P_w V_{j-1}, then S_w = Q_w K_j^T, for each query tile w that sees it
+      // step j: O_w (+)= P_w V_{j-1}, then S_w = Q_w K_j^T, for each query tile w that sees it. The
+      // ranges are found before the wait for the softmax, and the waits for K_j and V_j stand behind
+      // products already queued.
       for (int j = 0; j <= ti.steps && ok; ++j) {
         const bool qk = j < ti.steps;
-        const int k0 = qk ? step_tile(ti, j) * BN : 0;
+        const int kt = qk ? step_tile(ti, j) : 0, kt_prev = j > 0 ? step_tile(ti, j - 1) : 0;
         const uint32_t lk = ring + 2 * j, lv = lk - 1;          // ring numbers of K_j and V_{j-1}
         const uint32_t ks = lk % NS, vs = lv % NS;
-        bool k_here = false;
-        if (j > 0) {
-          ok = wait(&bar_full[vs], (lv / NS) & 1);
-          if (!ok) break;
-        }
         const uint64_t vd = smem_desc(ring_u32 + vs * C::SLOT, BN * 128, 1024, LAYOUT_SW128);
+#pragma unroll
+        for (int w = 0; w < NQ; ++w) {
+          now[w].c0 = now[w].c1 = 0;
+          if (qk && w < nq) now[w] = tile_range(ti, w, p.PP, p.window, p.sinks, kt * BN);
+        }
 #pragma unroll
         for (int w = 0; w < NQ; ++w) {
           if (w >= nq) break;
@@ -472,37 +583,40 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
             }
             ++p_use[w];
             tc_fence_after();
-            for (int c = prev[w].c0; c < prev[w].c1; ++c) {
+            if (prev[w].c0 == 0 && prev[w].c1 == BN / PIECE) {
 #pragma unroll
-              for (int h = 0; h < PIECE / 16; ++h) {
-                const int kk = c * (PIECE / 16) + h;
+              for (int kk = 0; kk < BN / 16; ++kk)
                 mma_ts_warp(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), id_pv,
-                            begun[w] ? 1u : 0u);
-                begun[w] = true;
+                            kk > 0 || begun[w] ? 1u : 0u);
+              begun[w] = true;
+            } else {
+              for (int c = prev[w].c0; c < prev[w].c1; ++c) {
+#pragma unroll
+                for (int h = 0; h < PIECE / 16; ++h) {
+                  const int kk = c * (PIECE / 16) + h;
+                  mma_ts_warp(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), id_pv,
+                              begun[w] ? 1u : 0u);
+                  begun[w] = true;
+                }
               }
             }
             // the key tile of the query tile's last row is its last step
-            const int last = (ti.p_first + min((w + 1) * p.PP, ti.np) - 1) / BN;
-            if (step_tile(ti, j - 1) == last) mma_commit_warp(&bar_odone[w]);
+            if (kt_prev == (ti.p_first + min((w + 1) * p.PP, ti.np) - 1) / BN) mma_commit_warp(&bar_odone[w]);
           }
-          if (j > 0 && w == nq - 1) mma_commit_warp(&bar_empty[vs]);
-          prev[w].c0 = prev[w].c1 = 0;
+          if (w == nq - 1 && j > 0) mma_commit_warp(&bar_empty[vs]);
           if (qk) {
-            prev[w] = tile_range(ti, w, p.PP, p.window, p.sinks, k0);
-            if (!k_here) {
-              if (!wait(&bar_full[ks], (lk / NS) & 1)) {
-                ok = false;
-                break;
-              }
-              k_here = true;
-            }
-            if (prev[w].c1 > prev[w].c0) issue_qk(w, ks, prev[w]);
+            if (w == 0) ok = wait(&bar_full[ks], (lk / NS) & 1);
+            if (w == nq - 1 && j > 0 && ok) ok = wait(&bar_full[(lk + 1) % NS], ((lk + 1) / NS) & 1);   // V_j
+            if (!ok) break;
+            if (now[w].c1 > now[w].c0) issue_qk(w, ks, now[w]);
           }
+          prev[w] = now[w];
         }
         if (!ok) break;
         if (qk) {
           mma_commit_warp(&bar_empty[ks]);
           if (j == ti.steps - 1) mma_commit_warp(&bar_qempty);
+          if (j == 0) ok = wait(&bar_full[(lk + 1) % NS], ((lk + 1) / NS) & 1);   // V_0
         }
       }
       ring += 2 * ti.steps;
@@ -601,75 +715,13 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
           }
           ++my_s;
           tc_fence_after();
-          uint32_t r[BN / PIECE][PIECE];
-#pragma unroll
-          for (int c = 0; c < BN / PIECE; ++c)
-            if (c >= rg.c0 && c < rg.c1) tmem_ld32(tmem + lrow + s_col + c * PIECE, r[c]);
-          tmem_wait_ld();
           // columns <= hi, and > lo or < se, are seen
           const int hi = p_i - k0, lo = max(p_i - p.window, -1) - k0, se = p.sinks - k0;
           const bool mask_hi = rg.c1 * PIECE - 1 > pa - k0;
           const bool mask_lo = rg.c0 * PIECE <= max(pb - p.window, -1) - k0 && rg.c1 * PIECE > se;
-          float mx[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < BN / PIECE; ++c) {
-            if (c >= rg.c0 && c < rg.c1) {
-              reg_fence(r[c]);
-              if (mask_hi) {
-#pragma unroll
-                for (int x = 0; x < PIECE; ++x)
-                  if (c * PIECE + x > hi) r[c][x] = __float_as_uint(-INFINITY);
-              }
-              if (mask_lo) {
-#pragma unroll
-                for (int x = 0; x < PIECE; ++x)
-                  if (c * PIECE + x <= lo && c * PIECE + x >= se) r[c][x] = __float_as_uint(-INFINITY);
-              }
-#pragma unroll
-              for (int x = 0; x < PIECE; x += 2)
-                mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(r[c][x]), __uint_as_float(r[c][x + 1]));
-            }
-          }
-          const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
-          const bool grow = mt > m_run + RESCALE_LOG2 || (m_run == -INFINITY && mt > m_run);
-          const float m_new = grow ? mt : m_run;
-          if (!first && __any_sync(0xffffffffu, grow)) {
-            const float alpha = grow ? ex2(m_run - m_new) : 1.f;
-            l_run *= alpha;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32_wait(tmem + lrow + o_col + c * 32, o);
-#pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-              tmem_st32_wait(tmem + lrow + o_col + c * 32, o);
-            }
-          }
-          m_run = m_new;
+          const RowStep st{sc, hi, lo, se, rg.c0, rg.c1, tmem + lrow + s_col, tmem + lrow + o_col};
+          softmax_step<D, MT>(st, rg.c0 == 0 && rg.c1 == BN / PIECE && !mask_hi && !mask_lo, first, m_run, l_run);
           first = false;
-          const float nm = SHIFT - (m_run == -INFINITY ? 0.f : m_run);
-          const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
-          float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int c = 0; c < BN / PIECE; ++c) {
-            if (c >= rg.c0 && c < rg.c1) {
-              uint32_t pw[16];
-#pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                const float2 y = __ffma2_rn(
-                    make_float2(__uint_as_float(r[c][2 * x]), __uint_as_float(r[c][2 * x + 1])), sc2, nm2);
-                const float a = ex2(y.x), b = ex2(y.y);
-                ls[x & 1] = __fadd2_rn(ls[x & 1], make_float2(a, b));
-                pw[x] = pack2<MT>(a, b);
-              }
-              tmem_st16(tmem + lrow + s_col + c * 16, pw);
-              tmem_wait_st();
-              reg_fence16(pw);
-            }
-          }
-          l_run += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
           tc_fence_before();
           mbar_arrive(&bar_pfull[w]);
         }
