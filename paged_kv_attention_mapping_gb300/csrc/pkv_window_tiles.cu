@@ -51,7 +51,7 @@ constexpr float F16_SHIFT = 7.f;
 
 struct TilesP {
   const int32_t *cu, *kv_lens, *tables;
-  int32_t B, T, Hq, Hkv, G, PP, P, num_pages, max_pages, window, sinks, min_q, box;
+  int32_t B, T, Hq, Hkv, G, PP, P, num_pages, max_pages, window, sinks, min_q, box, wide;
   int64_t units;
   PageDiv div;
   float scale_log2;
@@ -93,6 +93,20 @@ __device__ __forceinline__ Range tile_range(const Tile& t, int w, int PP, int wi
   const int lo = max(0, pa - window + 1);
   return range_of(k0, min(sinks, lo), lo, pe);
 }
+// What the MMA warp has to know of a step, a word that the producer works out (a warp that issues
+// products back to back has no time for it): for query tile w, in byte w, the first piece and (3 bits on) the
+// number of pieces it sees, and (bit 7) whether this is its last step.
+constexpr uint32_t WHOLE_STEP = (uint32_t)(BN / PIECE) << 3;   // of one query tile
+__device__ __forceinline__ uint32_t step_word(const Tile& t, int nq, int PP, int window, int sinks, int kt) {
+  uint32_t word = 0;
+  for (int w = 0; w < nq; ++w) {
+    const Range r = tile_range(t, w, PP, window, sinks, kt * BN);
+    const uint32_t last = kt == (t.p_first + min((w + 1) * PP, t.np) - 1) / BN;
+    word |= ((uint32_t)r.c0 | (uint32_t)(r.c1 - r.c0) << 3 | last << 7) << (8 * w);
+  }
+  return word;
+}
+
 // Rows of the pieces that no row of the work tile sees.
 __device__ __forceinline__ bool has_gaps(const Range& r) { return r.b > r.a || r.e < r.c1 * PIECE; }
 
@@ -129,6 +143,35 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]));
+}
+
+// 16 values of an output row: one 32-byte store where out is aligned to it (half the store
+// instructions, whole sectors), else two.
+template <typename T>
+__device__ __forceinline__ void store16(T* dst, const uint32_t (&x)[8], int wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
 // max(a, b, c) in one instruction; a NaN is passed over, as by fmaxf.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
@@ -212,13 +255,9 @@ __device__ __forceinline__ void narrow_q(unsigned char* q, uint8_t* back, int la
   }
 }
 
-// One row of one step: its scores from TMEM, the running maximum and sum, O rescaled where the
-// maximum grew, the weights written over the scores (16-bit pairs: the layout of an A operand).
+// What a row sees of a step: the columns <= hi that are > lo or < se.
 struct RowStep {
-  float sc;          // raw scores to log2 units
-  int hi, lo, se;    // columns <= hi, and > lo or < se, are seen
-  int c0, c1;        // pieces
-  uint32_t ts, to;   // TMEM: scores and output of this row's lanes
+  int hi, lo, se;
 };
 
 // Which of a piece's 32 columns are seen: a few shifts a piece, then a select a column.
@@ -240,30 +279,35 @@ __device__ __forceinline__ void max_of(const uint32_t (&r)[PIECE], float (&mx)[8
     mx[(x >> 1) & 7] = max3(mx[(x >> 1) & 7], __uint_as_float(r[x]), __uint_as_float(r[x + 1]));
 }
 
+// The running maximum after a step (log2 units); O and the sum follow it where it grows by more
+// than 2^8.
 template <int D>
-__device__ __forceinline__ void new_maximum(const RowStep& st, const float (&mx)[8], bool first, float& m_run,
-                                            float& l_run) {
-  const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * st.sc;
+__device__ __forceinline__ void new_maximum(float mt, uint32_t to, bool first, float& m_run, float& l_run) {
   const bool grow = mt > m_run + RESCALE_LOG2;   // (from -inf: any maximum but -inf)
   const float m_new = grow ? mt : m_run;
   if (!first && __any_sync(0xffffffffu, grow)) {
     const float alpha = grow ? ex2(m_run - m_new) : 1.f;
     l_run *= alpha;
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      uint32_t o[32];
-      tmem_ld32_wait(st.to + c * 32, o);
+    for (int c = 0; c < D / 16; ++c) {   // (16 columns at a time: a whole step's scores stay in registers)
+      uint32_t o[16];
+      tmem_ld16(to + c * 16, o);
+      tmem_wait_ld();
+      reg_fence16(o);
 #pragma unroll
-      for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-      tmem_st32_wait(st.to + c * 32, o);
+      for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+      tmem_st16(to + c * 16, o);
     }
+    tmem_wait_st();
   }
   m_run = m_new;
 }
 
-// Weights of a piece, their sums by pairs of columns, and where they go.
+// Weights of a piece, their sums by pairs of columns, and where they go (16-bit pairs: the layout
+// of an A operand).
 template <typename MT>
-__device__ __forceinline__ void weigh(const uint32_t (&r)[PIECE], float2 sc2, float2 nm2, float2 (&ls)[4], uint32_t to) {
+__device__ __forceinline__ void weigh(const uint32_t (&r)[PIECE], float sc, float nm, float2 (&ls)[4], uint32_t to) {
+  const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nm, nm);
   uint32_t pw[16];
 #pragma unroll
   for (int x = 0; x < 16; ++x) {
@@ -273,59 +317,6 @@ __device__ __forceinline__ void weigh(const uint32_t (&r)[PIECE], float2 sc2, fl
     pw[x] = pack2<MT>(a, b);
   }
   tmem_st16(to, pw);
-}
-
-// The softmax threads share their sub-partitions with the MMA warp, whose issue slots dense work
-// here takes away: three-input maxima, and fp32x2 multiply-adds and sums. A whole step (all
-// four pieces, every column seen) keeps its scores in registers; another reads them twice, a
-// piece at a time: with both forms over registers the kernel spills (window 2048, 16384 tokens:
-// 2261 us against 588 with one masked form for all steps).
-template <int D, typename MT>
-__device__ __forceinline__ void softmax_step(const RowStep& st, bool whole, bool first, float& m_run, float& l_run) {
-  constexpr float SHIFT = std::is_same<MT, __nv_bfloat16>::value ? 0.f : F16_SHIFT;
-  constexpr int NC = BN / PIECE;
-  float mx[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
-  float2 ls[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
-  if (whole) {
-    uint32_t r[NC][PIECE];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) tmem_ld32(st.ts + c * PIECE, r[c]);
-    tmem_wait_ld();
-#pragma unroll
-    for (int c = 0; c < NC; ++c) reg_fence(r[c]);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) max_of(r[c], mx);
-    new_maximum<D>(st, mx, first, m_run, l_run);
-    const float nm = SHIFT - (m_run == -INFINITY ? 0.f : m_run);
-    const float2 sc2 = make_float2(st.sc, st.sc), nm2 = make_float2(nm, nm);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) weigh<MT>(r[c], sc2, nm2, ls, st.ts + c * 16);
-  } else {
-#pragma unroll 1
-    for (int c = st.c0; c < st.c1; ++c) {
-      uint32_t r[PIECE];
-      tmem_ld32_wait(st.ts + c * PIECE, r);
-      hide(r, seen_bits(st, c));
-      max_of(r, mx);
-    }
-    new_maximum<D>(st, mx, first, m_run, l_run);
-    const float nm = SHIFT - (m_run == -INFINITY ? 0.f : m_run);
-    const float2 sc2 = make_float2(st.sc, st.sc), nm2 = make_float2(nm, nm);
-    // (the weights of piece c go over scores of pieces up to c / 2)
-#pragma unroll 1
-    for (int c = st.c0; c < st.c1; ++c) {
-      uint32_t r[PIECE];
-      tmem_ld32_wait(st.ts + c * PIECE, r);
-      hide(r, seen_bits(st, c));
-      weigh<MT>(r, sc2, nm2, ls, st.ts + c * 16);
-    }
-  }
-  tmem_wait_st();
-  l_run += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
 }
 
 // TQ: type of q and out. KV8: e4m3 caches (head_dim 128), products in f16.
@@ -348,13 +339,14 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
   // Work tiles pass through two entries (tile t in entry t & 1): the producer fills the next
   // one and loads its Q while tile t finishes.
   __shared__ __align__(8) uint64_t bar_q, bar_qempty, bar_full[NS], bar_empty[NS], bar_sfull[NQ],
-      bar_pfull[NQ], bar_odone[NQ], bar_tfull[2], bar_tempty[2], bar_drain;
+      bar_pfull[NQ][2], bar_odone[NQ], bar_tfull[2], bar_tempty[2], bar_drain;
   // loads that a helper warp works on before the MMA may read them land here: the value tiles
   // with rows to zero; over an e4m3 cache every tile, and bf16 queries
   __shared__ __align__(8) uint64_t bar_land[NS], bar_qland;
   __shared__ LoadDesc s_ld[KV8 ? NS : 1];
   __shared__ uint8_t s_back[2][QCONV ? NQ * BM : 1];   // (by entry: a slow softmax may still read the last tile's)
   __shared__ Tile s_tile[2];
+  __shared__ uint32_t s_step[8];
   __shared__ uint32_t s_tmem;
   __shared__ int32_t s_err;
   __shared__ volatile int s_abort;
@@ -374,7 +366,7 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
     mbar_init(&bar_qland, 1);
     for (int w = 0; w < NQ; ++w) {
       mbar_init(&bar_sfull[w], 1);
-      mbar_init(&bar_pfull[w], BM);
+      for (int h = 0; h < 2; ++h) mbar_init(&bar_pfull[w][h], SOFTMAX_WARPS / NQ);
       mbar_init(&bar_odone[w], 1);
     }
     for (int e = 0; e < 2; ++e) {
@@ -478,6 +470,7 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&s_tile[e].bad, 1);
         const bool load = in && !bad;
+        const uint32_t word = step_word(ti, nq, p.PP, p.window, p.sinks, k0 / BN);
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)(p.box * 128);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -488,6 +481,8 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
             break;
           }
           unsigned char* dst = sRing + slot * C::SLOT + (KV8 ? BN * 128 : 0);
+          // (the word of step n is read with K_n; with the slot of K_{n + 8} free, K_{n + 4} at least is used up)
+          if (kv == 0 && lane == 0) s_step[(ring - 1) / 2 % 8] = word;
           const bool land = KV8 || (kv == 1 && has_gaps(r));
           uint64_t* bar = land ? &bar_land[slot] : &bar_full[slot];
           const uint32_t bit = 1u << slot;
@@ -533,93 +528,119 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer
+    // The whole warp runs this loop and elect.sync picks the lane that issues. The tensor pipe holds
+    // only a few products ahead of the issue, so every instruction between them counts: ring
+    // positions advance step by step, ranges come as words, and a whole step's products are unrolled.
     const uint32_t id_pv = idesc_f16(BM, D, BF16, true), id_qk = idesc_f16(BM, 0, BF16, false);
     const uint32_t ring_u32 = smem_u32(sRing);
     const uint64_t qd = smem_desc(smem_u32(sQ), 16, 1024, LAYOUT_SW128);
-    uint32_t p_use[NQ] = {0, 0}, ring = 0;
-    auto issue_qk = [&](int w, uint32_t slot, const Range& r) {
-      const uint32_t idesc = id_qk | ((uint32_t)((r.c1 - r.c0) * (PIECE >> 3)) << 17);
-      const uint64_t kd = smem_desc(ring_u32 + slot * C::SLOT + r.c0 * PIECE * 128, 16, 1024, LAYOUT_SW128);
+    uint32_t p_use = 0;                           // parity of each query tile's hand-offs, a bit a tile
+    uint32_t ks = 0, kph = 0, n = 0;              // slot and phase of the next K; steps so far
+    auto issue_qk = [&](int w, uint32_t slot, uint32_t b) {
+      const uint64_t kd = smem_desc(ring_u32 + slot * C::SLOT, 16, 1024, LAYOUT_SW128);
+      const uint32_t c0 = b & 7, nc = b >> 3 & 7;
+      const uint32_t idesc = id_qk | (nc * (PIECE >> 3)) << 17;
+      const uint32_t dt = tmem + w * 128 + c0 * PIECE;
+      const uint64_t kc = kd + (uint64_t)(c0 * (PIECE * 128 >> 4)), qw = qd + (uint64_t)(w * (C::Q_BYTES >> 4));
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk / 4) * BM * 128 + (kk % 4) * 32, offk = (kk / 4) * BN * 128 + (kk % 4) * 32;
-        mma_f16_ss_warp(tmem + w * 128 + r.c0 * PIECE, qd + (uint64_t)((w * C::Q_BYTES + off) >> 4),
-                        kd + (uint64_t)(offk >> 4), idesc, kk > 0 ? 1u : 0u);
+        mma_f16_ss_warp(dt, qw + (uint64_t)(off >> 4), kc + (uint64_t)(offk >> 4), idesc, kk > 0 ? 1u : 0u);
       }
       mma_commit_warp(&bar_sfull[w]);
+    };
+    // O_w (+)= P_w V, the weights handed over in two halves of the step's pieces
+    auto issue_pv = [&](int w, uint64_t vd, uint32_t b, uint32_t acc, uint32_t par) {
+      const uint32_t dt = tmem + 256 + w * 128, at = tmem + w * 128;
+      if (!wait(&bar_pfull[w][0], par)) return false;
+      tc_fence_after();
+      if ((b & 63) == WHOLE_STEP) {
+#pragma unroll
+        for (int kk = 0; kk < BN / 32; ++kk)
+          mma_ts_warp(dt, at + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), id_pv, kk > 0 ? 1u : acc);
+        if (!wait(&bar_pfull[w][1], par)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = BN / 32; kk < BN / 16; ++kk)
+          mma_ts_warp(dt, at + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), id_pv, 1u);
+      } else {
+        const uint32_t c0 = b & 7, c1 = c0 + (b >> 3 & 7), mid = (c0 + c1 + 1) >> 1;
+        for (uint32_t c = c0; c < c1; ++c) {
+          if (c == mid) {
+            if (!wait(&bar_pfull[w][1], par)) return false;
+            tc_fence_after();
+          }
+#pragma unroll
+          for (uint32_t h = 0; h < PIECE / 16; ++h) {
+            const uint32_t kk = c * (PIECE / 16) + h;
+            mma_ts_warp(dt, at + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), id_pv, acc);
+            acc = 1;
+          }
+        }
+        if (mid == c1 && !wait(&bar_pfull[w][1], par)) return false;   // (one piece: an empty second half)
+      }
+      return true;
     };
     bool ok = true;
     for (uint32_t t = 0; ok; ++t) {
       const uint32_t e = t & 1;
       if (!wait(&bar_tfull[e], (t >> 1) & 1)) break;
-      const Tile ti = s_tile[e];
-      if (!ti.valid) break;
-      const int nq = ti.np > p.PP ? 2 : 1;
+      if (!s_tile[e].valid) break;
+      const int nq = s_tile[e].np > p.PP ? 2 : 1, steps = s_tile[e].steps;
       ok = wait(&bar_q, t & 1);
       tc_fence_after();
-      Range prev[NQ], now[NQ];
-      bool begun[NQ] = {false, false};
+      uint32_t vs = ks, prev = 0, acc = 0;   // V_{j-1}; the last step's word; a bit a query tile begun
       // step j: O_w (+)= P_w V_{j-1}, then S_w = Q_w K_j^T, for each query tile w that sees it. The
-      // ranges are found before the wait for the softmax, and the waits for K_j and V_j stand behind
-      // products already queued.
-      for (int j = 0; j <= ti.steps && ok; ++j) {
-        const bool qk = j < ti.steps;
-        const int kt = qk ? step_tile(ti, j) : 0, kt_prev = j > 0 ? step_tile(ti, j - 1) : 0;
-        const uint32_t lk = ring + 2 * j, lv = lk - 1;          // ring numbers of K_j and V_{j-1}
-        const uint32_t ks = lk % NS, vs = lv % NS;
+      // waits for K_j and V_j stand behind products already queued.
+      for (int j = 0; j <= steps && ok; ++j) {
+        const bool qk = j < steps;
+        uint32_t now = 0;
         const uint64_t vd = smem_desc(ring_u32 + vs * C::SLOT, BN * 128, 1024, LAYOUT_SW128);
-#pragma unroll
-        for (int w = 0; w < NQ; ++w) {
-          now[w].c0 = now[w].c1 = 0;
-          if (qk && w < nq) now[w] = tile_range(ti, w, p.PP, p.window, p.sinks, kt * BN);
+        const uint32_t kslot = ks, kphase = kph;
+        uint32_t nvs = ks + 1, nvph = kph;   // V_j
+        if (nvs == (uint32_t)NS) {
+          nvs = 0;
+          nvph ^= 1;
         }
 #pragma unroll
         for (int w = 0; w < NQ; ++w) {
           if (w >= nq) break;
-          if (j > 0 && prev[w].c1 > prev[w].c0) {
-            if (!wait(&bar_pfull[w], p_use[w] & 1)) {
-              ok = false;
-              break;
-            }
-            ++p_use[w];
-            tc_fence_after();
-            if (prev[w].c0 == 0 && prev[w].c1 == BN / PIECE) {
-#pragma unroll
-              for (int kk = 0; kk < BN / 16; ++kk)
-                mma_ts_warp(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), id_pv,
-                            kk > 0 || begun[w] ? 1u : 0u);
-              begun[w] = true;
-            } else {
-              for (int c = prev[w].c0; c < prev[w].c1; ++c) {
-#pragma unroll
-                for (int h = 0; h < PIECE / 16; ++h) {
-                  const int kk = c * (PIECE / 16) + h;
-                  mma_ts_warp(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, vd + (uint64_t)((kk * 16 * 128) >> 4), id_pv,
-                              begun[w] ? 1u : 0u);
-                  begun[w] = true;
-                }
-              }
-            }
-            // the key tile of the query tile's last row is its last step
-            if (kt_prev == (ti.p_first + min((w + 1) * p.PP, ti.np) - 1) / BN) mma_commit_warp(&bar_odone[w]);
+          const uint32_t pb = prev >> (8 * w);
+          if (pb & 56) {
+            ok = issue_pv(w, vd, pb, acc >> w & 1, p_use >> w & 1);
+            if (!ok) break;
+            p_use ^= 1u << w;
+            acc |= 1u << w;
+            if (pb & 128) mma_commit_warp(&bar_odone[w]);
           }
           if (w == nq - 1 && j > 0) mma_commit_warp(&bar_empty[vs]);
           if (qk) {
-            if (w == 0) ok = wait(&bar_full[ks], (lk / NS) & 1);
-            if (w == nq - 1 && j > 0 && ok) ok = wait(&bar_full[(lk + 1) % NS], ((lk + 1) / NS) & 1);   // V_j
+            if (w == 0) {
+              ok = wait(&bar_full[kslot], kphase);
+              now = s_step[n % 8];
+            }
+            if (w == nq - 1 && j > 0 && ok) ok = wait(&bar_full[nvs], nvph);
             if (!ok) break;
-            if (now[w].c1 > now[w].c0) issue_qk(w, ks, now[w]);
+            const uint32_t nb = now >> (8 * w);
+            if (nb & 56) issue_qk(w, kslot, nb);
           }
-          prev[w] = now[w];
         }
         if (!ok) break;
         if (qk) {
-          mma_commit_warp(&bar_empty[ks]);
-          if (j == ti.steps - 1) mma_commit_warp(&bar_qempty);
-          if (j == 0) ok = wait(&bar_full[(lk + 1) % NS], ((lk + 1) / NS) & 1);   // V_0
+          mma_commit_warp(&bar_empty[kslot]);
+          if (j == steps - 1) mma_commit_warp(&bar_qempty);
+          if (j == 0) ok = wait(&bar_full[nvs], nvph);
+          vs = nvs;
+          ks = nvs + 1;
+          kph = nvph;
+          if (ks == (uint32_t)NS) {
+            ks = 0;
+            kph ^= 1;
+          }
+          ++n;
         }
+        prev = now;
       }
-      ring += 2 * ti.steps;
       if (ok && lane == 0) mbar_arrive(&bar_tempty[e]);
       __syncwarp();
     }
@@ -679,35 +700,51 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
     }
   } else {
     // ---------------------------------------------------------------- softmax
+    // The softmax threads share their sub-partitions with the MMA warp, whose issue slots dense work
+    // here takes away: three-input maxima, fp32x2 multiply-adds and sums. A whole step (all four
+    // pieces, every column seen) keeps its scores in registers; another reads them twice, a piece
+    // at a time (with both forms over registers the kernel spills: 16384 tokens at window 2048 took
+    // 2261 us against 588). The weights go to the MMA warp in two halves of the step's pieces: the first
+    // half's products run during the second half's exponentials.
     const int w = (warp - 2) >> 2;
     const int i = (warp & 3) * 32 + lane;         // row within the tile; warp & 3: its TMEM lane quarter
-    const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_col = w * 128, o_col = 256 + w * 128;
-    const int pi = i / p.G, head = i - pi * p.G;
+    const uint32_t ts = tmem + ((uint32_t)((warp & 3) * 32) << 16) + w * 128, to = ts + 256;
+    const int pi = i / p.G;
     uint32_t my_s = 0, my_o = 0;
+    // (a barrier for each half: the MMA warp may come to either after both are handed over)
+    auto hand = [&](int h) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_pfull[w][h]);
+    };
     for (uint32_t t = 0;; ++t) {
       const uint32_t e = t & 1;
       if (!wait(&bar_tfull[e], (t >> 1) & 1)) break;
-      const Tile ti = s_tile[e];
-      if (!ti.valid) break;
+      const Tile* tile = &s_tile[e];
+      if (!tile->valid) break;
       bool ok = true;
       // (each tile's: a phase that is not waited for would be mistaken for the next)
       if constexpr (QCONV) {
         if (!wait(&bar_q, t & 1)) break;
       }
-      const int npw = min(ti.np - w * p.PP, p.PP);   // positions of this query tile
+      const int npw = min(tile->np - w * p.PP, p.PP);   // positions of this query tile
       if (npw > 0) {
-        const int pa = ti.p_first + w * p.PP, pb = pa + npw - 1;
+        const int pa = tile->p_first + w * p.PP, pb = pa + npw - 1;
         const int p_i = min(pa + pi, pb);
         float sc = p.scale_log2;
-        if constexpr (KV8) sc *= __ldg(p.ks + ti.kvh);
+        if constexpr (KV8) sc *= __ldg(p.ks + tile->kvh);
         if constexpr (QCONV) sc *= __uint_as_float((uint32_t)s_back[e][w * BM + i] << 23);
         float m_run = -INFINITY, l_run = 0.f;
         bool first = true;
-        for (int j = 0; j < ti.steps; ++j) {
-          const int k0 = step_tile(ti, j) * BN;
-          const Range rg = tile_range(ti, w, p.PP, p.window, p.sinks, k0);
-          if (rg.c1 <= rg.c0) continue;
+        // keys that every row of the tile sees: [0, all_sinks) and (all_lo, pa]
+        const int steps = tile->steps, js = tile->js, j0 = tile->j0 - js;
+        const int first_key = max(0, pa - p.window + 1), all_lo = max(pb - p.window, -1);
+        const int my_sinks = min(p.sinks, first_key);
+        for (int j = 0; j < steps; ++j) {
+          const int k0 = (j < js ? j : j0 + j) * BN;
+          if (!(k0 < my_sinks || (k0 + BN > first_key && k0 <= pb))) continue;
+          const bool whole = (k0 > all_lo && k0 + BN - 1 <= pa) || k0 + BN <= my_sinks;
           // S_w complete also means every earlier MMA (the PV that read P_w) is done
           if (!wait(&bar_sfull[w], my_s & 1)) {
             ok = false;
@@ -715,15 +752,58 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
           }
           ++my_s;
           tc_fence_after();
-          // columns <= hi, and > lo or < se, are seen
-          const int hi = p_i - k0, lo = max(p_i - p.window, -1) - k0, se = p.sinks - k0;
-          const bool mask_hi = rg.c1 * PIECE - 1 > pa - k0;
-          const bool mask_lo = rg.c0 * PIECE <= max(pb - p.window, -1) - k0 && rg.c1 * PIECE > se;
-          const RowStep st{sc, hi, lo, se, rg.c0, rg.c1, tmem + lrow + s_col, tmem + lrow + o_col};
-          softmax_step<D, MT>(st, rg.c0 == 0 && rg.c1 == BN / PIECE && !mask_hi && !mask_lo, first, m_run, l_run);
+          float mx[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
+          float2 ls[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) ls[k] = make_float2(0.f, 0.f);
+          auto top = [&]() {
+            return max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * sc;
+          };
+          auto minus = [&]() { return SHIFT - (m_run == -INFINITY ? 0.f : m_run); };
+          if (whole) {
+            uint32_t r[BN / PIECE][PIECE];
+#pragma unroll
+            for (int c = 0; c < BN / PIECE; ++c) tmem_ld32(ts + c * PIECE, r[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < BN / PIECE; ++c) reg_fence(r[c]);
+#pragma unroll
+            for (int c = 0; c < BN / PIECE; ++c) max_of(r[c], mx);
+            new_maximum<D>(top(), to, first, m_run, l_run);
+            const float nm = minus();
+#pragma unroll
+            for (int c = 0; c < BN / PIECE; ++c) {
+              weigh<MT>(r[c], sc, nm, ls, ts + c * 16);
+              if (c == BN / PIECE / 2 - 1) hand(0);
+            }
+          } else {
+            const Range rg = range_of(k0, my_sinks, first_key, pb + 1);
+            const RowStep st{p_i - k0, max(p_i - p.window, -1) - k0, p.sinks - k0};
+#pragma unroll 1
+            for (int c = rg.c0; c < rg.c1; ++c) {
+              uint32_t r[PIECE];
+              tmem_ld32_wait(ts + c * PIECE, r);
+              hide(r, seen_bits(st, c));
+              max_of(r, mx);
+            }
+            new_maximum<D>(top(), to, first, m_run, l_run);
+            const float nm = minus();
+            const int mid = (rg.c0 + rg.c1 + 1) >> 1;
+            // (the weights of piece c go over scores of pieces up to c / 2)
+#pragma unroll 1
+            for (int c = rg.c0; c < rg.c1; ++c) {
+              uint32_t r[PIECE];
+              tmem_ld32_wait(ts + c * PIECE, r);
+              hide(r, seen_bits(st, c));
+              weigh<MT>(r, sc, nm, ls, ts + c * 16);
+              if (c == mid - 1) hand(0);
+            }
+          }
+          hand(1);
           first = false;
-          tc_fence_before();
-          mbar_arrive(&bar_pfull[w]);
+          l_run += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
         }
         if (ok) ok = wait(&bar_odone[w], my_o & 1);
         ++my_o;
@@ -731,22 +811,21 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
         if (ok) {
           const int bad = *(volatile const int*)&s_tile[e].bad;
           const bool store = pi < npw && !bad;
-          const float inv = (KV8 ? __ldg(p.vs + ti.kvh) : 1.f) / l_run;
-          const int64_t at = (int64_t)(ti.row0 + w * p.PP + pi) * p.Hq + ti.kvh * p.G + head;
+          const float inv = (KV8 ? __ldg(p.vs + tile->kvh) : 1.f) / l_run;
+          const int64_t at = (int64_t)(tile->row0 + w * p.PP + pi) * p.Hq + tile->kvh * p.G + (i - pi * p.G);
           TQ* dst = (TQ*)p.out + at * D;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
-            tmem_ld32_wait(tmem + lrow + o_col + c * 32, o);
+            tmem_ld32_wait(to + c * 32, o);
             if (!store) continue;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              uint4 pk;
-              pk.x = pack2<TQ>(__uint_as_float(o[v * 8 + 0]) * inv, __uint_as_float(o[v * 8 + 1]) * inv);
-              pk.y = pack2<TQ>(__uint_as_float(o[v * 8 + 2]) * inv, __uint_as_float(o[v * 8 + 3]) * inv);
-              pk.z = pack2<TQ>(__uint_as_float(o[v * 8 + 4]) * inv, __uint_as_float(o[v * 8 + 5]) * inv);
-              pk.w = pack2<TQ>(__uint_as_float(o[v * 8 + 6]) * inv, __uint_as_float(o[v * 8 + 7]) * inv);
-              *reinterpret_cast<uint4*>(dst + c * 32 + v * 8) = pk;
+            for (int v = 0; v < 2; ++v) {
+              uint32_t x[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                x[k] = pack2<TQ>(__uint_as_float(o[v * 16 + 2 * k]) * inv, __uint_as_float(o[v * 16 + 2 * k + 1]) * inv);
+              store16(dst + c * 32 + v * 16, x, p.wide);
             }
           }
           if (store && p.lse) p.lse[at] = (m_run + __log2f(l_run) - SHIFT) * LN2;
@@ -800,6 +879,7 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t s) {
   p.sinks = a.sinks;
   p.min_q = a.tile_min_q;
   p.box = a.P < PIECE ? a.P : PIECE;
+  p.wide = ((uintptr_t)a.out & 31) == 0;
   p.units = ((int64_t)a.B + a.T / (NQ * p.PP)) * a.Hkv;
   p.div = page_div(a.P);
   p.scale_log2 = a.scale * LOG2E;
