@@ -16,21 +16,29 @@
 namespace pkv {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 
 struct NormP {
   const void *q, *k, *v, *qw, *kw;
-  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, qo_st, qo_sh, pool_slots, units;
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, qo_st, qo_sh, pool_slots;
   const int32_t* positions;
   const float2* cs;   // [max_pos][rot / 2]
   const int64_t* slots;
   void *kc, *vc, *qo;
   const float *ks, *vs;   // e4m3 caches
   float eps;
-  int32_t max_pos, rot, Hq, Hkv, uq, uk;   // uq, uk: units of a token's queries / keys (values: as keys)
+  int32_t max_pos, rot, Hq, Hkv, units, uq, uk;   // uq, uk: units of a token's queries / keys (values: as keys)
   int32_t* dev_status;
 };
 
+// The bound is HBM: (2 Hq + 2 Hkv) D values of the source type and 2 Hkv D of the cache's a token.
+// 4192 tokens at 32 / 8 heads of 128 (bf16, 105 MB) take 24.3 us, 4.3 TB/s, 65 % of the copy
+// bandwidth; 64 tokens 3.1 us, a launch and two rounds of loads. What is left is instructions:
+// 580 a unit of 4 KB moved. Steps taken: angles and weights multiplied once a unit (41 -> 27.7 us),
+// blocks of 128 at 64 registers (26.6), addresses stepped and the approximate root, which is within
+// 2 ulp (24.3). Without gain: two or eight passes in flight (33, 35), a unit's loads issued while the
+// one before is worked on (27 to 37), streaming loads (25.2).
+//
 // A warp's unit: ROWS consecutive head rows of one token, all queries, all keys or
 // all values. LR = lanes of a row, a lane holding NV vectors of E values, E values
 // apart by LR * E. The warp's 32 / LR rows of a pass are neighbours; PASSES of them
@@ -69,17 +77,18 @@ __device__ __forceinline__ void unpack(const uint4& raw, float (&x)[E]) {
 }
 
 template <typename T, int D, bool NEAR, bool CODES>
-__global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormP p) {
+__global__ void __launch_bounds__(THREADS, Shape<T, D>::NV > 1 ? 4 : 8) norm_rope_kernel(const NormP p) {
   using S = Shape<T, D>;
   constexpr int E = S::E, NV = S::NV, LR = S::LR, PASSES = S::PASSES;
   pdl_wait();
   pdl_trigger();   // what starts now waits for this grid's end before it writes, and before it relies on what it read
-  const int64_t unit = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
+  const int unit = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
   if (unit >= p.units) return;
   const int lane = threadIdx.x & 31, l = lane % LR, sub = lane / LR;
   const int per_token = p.uq + 2 * p.uk;
-  const int64_t t = unit / per_token;
-  int u = (int)(unit - t * per_token);
+  const int tok = unit / per_token;
+  const int64_t t = tok;
+  int u = unit - tok * per_token;
   const int kind = u < p.uq ? 0 : u < p.uq + p.uk ? 1 : 2;   // queries, keys, values
   const bool first = u == 0;
   u -= kind == 0 ? 0 : kind == 1 ? p.uq : p.uq + p.uk;
@@ -88,16 +97,17 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormP p) {
   const T* src = kind == 0 ? (const T*)p.q + t * p.q_st : kind == 1 ? (const T*)p.k + t * p.k_st
                                                                     : (const T*)p.v + t * p.v_st;
   const int64_t sh = kind == 0 ? p.q_sh : kind == 1 ? p.k_sh : p.v_sh;
-  uint4 raw[PASSES][NV];
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int h = h0 + i * S::RPW;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-      raw[i][v] = h < H ? *reinterpret_cast<const uint4*>(src + h * sh + (v * LR + l) * E) : make_uint4(0, 0, 0, 0);
-  }
   const int pos = __ldg(p.positions + t);
   const int64_t slot = kind == 0 ? 0 : __ldg(p.slots + t);
+  uint4 raw[PASSES][NV];
+  src += h0 * sh + l * E;
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      raw[i][v] = h0 + i * S::RPW < H ? *reinterpret_cast<const uint4*>(src + v * LR * E) : make_uint4(0, 0, 0, 0);
+    src += S::RPW * sh;
+  }
   if (pos < 0 || pos >= p.max_pos) {
     if (first && lane == 0) atomicOr(p.dev_status, PKV_DEV_BAD_POSITION);
     return;
@@ -112,9 +122,10 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormP p) {
   const T* w = (const T*)(kind == 0 ? p.qw : kind == 1 ? p.kw : nullptr);
   const bool turned = kind != 2;
   const int half = p.rot / 2;
-  // this lane's values: wt their weights, wo those of their partners half a rotation
-  // away; c, s the angles' cosines and sines, s with the sign its value's sum takes
-  float wt[NV][E], wo[NEAR ? 1 : NV][E], c[NV][E], s[NV][E];
+  // A value becomes r (x A + z B): z its partner, A its weight times the cosine, B the partner's
+  // weight times the sine with the sign it takes, r what the norm divides by. Where nothing is
+  // rotated the second term is left out.
+  float2 A[NV][E / 2], B[NV][E / 2];
   int from[NV];   // lane that holds the partners (of vector v or 1 - v where other[v])
   bool other[NV], rotated[NV];
 #pragma unroll
@@ -123,76 +134,80 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormP p) {
     rotated[v] = turned && at < p.rot;
     const bool hi = at >= half;
     const int mate = NEAR ? at : rotated[v] ? (hi ? at - half : at + half) : at;
-    const int mv = mate / (LR * E);
     from[v] = (mate / E) % LR + sub * LR;
-    other[v] = mv != v;
+    other[v] = mate / (LR * E) != v;
+    float own[E], its[E];
     if (w) {
-      unpack<T, E>(__ldg(reinterpret_cast<const uint4*>(w + at)), wt[v]);
-      if constexpr (!NEAR) unpack<T, E>(__ldg(reinterpret_cast<const uint4*>(w + mate)), wo[v]);
+      unpack<T, E>(__ldg(reinterpret_cast<const uint4*>(w + at)), own);
+      unpack<T, E>(__ldg(reinterpret_cast<const uint4*>(w + mate)), its);
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        wt[v][e] = 1.f;
-        if constexpr (!NEAR) wo[v][e] = 1.f;
-      }
+      for (int e = 0; e < E; ++e) own[e] = its[e] = 1.f;
+    }
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      A[v][e / 2] = make_float2(own[e], own[e + 1]);
+      B[v][e / 2] = make_float2(0.f, 0.f);
     }
     if (rotated[v]) {
-      const float2* cs = p.cs + (int64_t)pos * half;
-      if constexpr (NEAR) {
+      const float4* cs = reinterpret_cast<const float4*>(p.cs + (int64_t)pos * half + (NEAR ? at / 2 : hi ? at - half : at));
 #pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          const float4 x = __ldg(reinterpret_cast<const float4*>(cs + (at + e) / 2));
-          c[v][e] = c[v][e + 1] = x.x;
-          s[v][e] = -x.y;
-          s[v][e + 1] = x.y;
-          c[v][e + 2] = c[v][e + 3] = x.z;
-          s[v][e + 2] = -x.w;
-          s[v][e + 3] = x.w;
-        }
-      } else {
-        const int i0 = hi ? at - half : at;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float4 x = __ldg(reinterpret_cast<const float4*>(cs + i0 + e));
-          c[v][e] = x.x;
-          s[v][e] = hi ? x.y : -x.y;
-          c[v][e + 1] = x.z;
-          s[v][e + 1] = hi ? x.w : -x.w;
+      for (int e = 0; e < E; e += 2) {
+        if constexpr (NEAR) {
+          // pairs (e, e + 1): one angle
+          const float4 q = __ldg(cs + e / 4);
+          const float c = e & 2 ? q.z : q.x, sn = e & 2 ? q.w : q.y;
+          A[v][e / 2] = make_float2(own[e] * c, own[e + 1] * c);
+          B[v][e / 2] = make_float2(-its[e + 1] * sn, its[e] * sn);
+        } else {
+          const float4 q = __ldg(cs + e / 2);
+          A[v][e / 2] = make_float2(own[e] * q.x, own[e + 1] * q.z);
+          B[v][e / 2] = hi ? make_float2(its[e] * q.y, its[e + 1] * q.w) : make_float2(-its[e] * q.y, -its[e + 1] * q.w);
         }
       }
     }
   }
+  // where this lane's first row goes, and how far its next one is, in bytes
+  constexpr int CB = CODES ? 1 : (int)sizeof(T);
+  char* dst = kind == 0 ? (char*)((T*)p.qo + t * p.qo_st + h0 * p.qo_sh + l * E)
+                        : (char*)(kind == 1 ? p.kc : p.vc) + ((slot * p.Hkv + h0) * D + l * E) * CB;
+  const int64_t dst_step = kind == 0 ? S::RPW * p.qo_sh * (int64_t)sizeof(T) : S::RPW * D * CB;
+  const float* scales = kind == 1 ? p.ks : p.vs;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int h = h0 + i * S::RPW;
-    float x[NV][E], r = 1.f;
-    float sum = 0.f;
+    float r = 1.f, y[NV][E];
+    if (w) {   // (the same for the whole warp, as is kind)
+      float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      unpack<T, E>(raw[i][v], x[v]);
+      for (int v = 0; v < NV; ++v) {
+        float x[E];
+        unpack<T, E>(raw[i][v], x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum = fmaf(x[v][e], x[v][e], sum);
-    }
-    if (w) {   // (the same for the whole warp, as are kind and pos)
+        for (int e = 0; e < E; e += 2) {
+          const float2 x2 = make_float2(x[e], x[e + 1]);
+          sum2 = __ffma2_rn(x2, x2, sum2);
+        }
+      }
+      float sum = sum2.x + sum2.y;
 #pragma unroll
       for (int o = LR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      r = __frsqrt_rn(fmaf(sum, 1.f / D, p.eps));
+      r = rsqrtf(fmaf(sum, 1.f / D, p.eps));
     }
-    float y[NV][E];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      uint4 mate = make_uint4(0, 0, 0, 0);
+      uint4 mate = raw[i][v];
       if constexpr (!NEAR) {
         if (turned) {
           // the partners' values as they came: one shuffle a 32-bit word
-          const uint4 a = raw[i][0], b = raw[i][NV - 1];
-          uint4 m0, m1;
-          m0.x = __shfl_sync(0xffffffffu, a.x, from[v]);
-          m0.y = __shfl_sync(0xffffffffu, a.y, from[v]);
-          m0.z = __shfl_sync(0xffffffffu, a.z, from[v]);
-          m0.w = __shfl_sync(0xffffffffu, a.w, from[v]);
-          mate = m0;
+          const uint4 a = raw[i][0];
+          mate.x = __shfl_sync(0xffffffffu, a.x, from[v]);
+          mate.y = __shfl_sync(0xffffffffu, a.y, from[v]);
+          mate.z = __shfl_sync(0xffffffffu, a.z, from[v]);
+          mate.w = __shfl_sync(0xffffffffu, a.w, from[v]);
           if constexpr (NV > 1) {
+            const uint4 b = raw[i][NV - 1];
+            uint4 m1;
             m1.x = __shfl_sync(0xffffffffu, b.x, from[v]);
             m1.y = __shfl_sync(0xffffffffu, b.y, from[v]);
             m1.z = __shfl_sync(0xffffffffu, b.z, from[v]);
@@ -201,46 +216,39 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormP p) {
           }
         }
       }
-      float z[E];
-      unpack<T, E>(mate, z);
+      if (turned || CODES) {
+        float x[E], z[E];
+        unpack<T, E>(raw[i][v], x);
+        if constexpr (!NEAR) unpack<T, E>(mate, z);
+        const float2 r2 = make_float2(r, r);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float own = x[v][e] * r * wt[v][e];
-        y[v][e] = own;
-        if constexpr (!NEAR) {
-          if (rotated[v]) y[v][e] = fmaf(own, c[v][e], z[e] * r * wo[v][e] * s[v][e]);
-        }
-      }
-      if constexpr (NEAR) {
-        if (rotated[v]) {
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const float a = y[v][e], b = y[v][e + 1];
-            y[v][e] = fmaf(a, c[v][e], b * s[v][e]);
-            y[v][e + 1] = fmaf(b, c[v][e + 1], a * s[v][e + 1]);
-          }
+        for (int e = 0; e < E; e += 2) {
+          float2 u = __fmul2_rn(make_float2(x[e], x[e + 1]), A[v][e / 2]);
+          if (rotated[v])
+            u = __ffma2_rn(NEAR ? make_float2(x[e + 1], x[e]) : make_float2(z[e], z[e + 1]), B[v][e / 2], u);
+          u = __fmul2_rn(u, r2);
+          y[v][e] = u.x;
+          y[v][e + 1] = u.y;
         }
       }
     }
     if (h >= H) continue;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int at = (v * LR + l) * E;
+      const int at = v * LR * E;
       if (CODES && kind != 0) {
-        uint8_t* dst = (uint8_t*)(kind == 1 ? p.kc : p.vc) + (slot * p.Hkv + h) * D + at;
-        store_codes<E>(y[v], __ldg((kind == 1 ? p.ks : p.vs) + h), dst);
+        store_codes<E>(y[v], __ldg(scales + h), (uint8_t*)dst + at);
       } else {
-        T* dst = kind == 0 ? (T*)p.qo + t * p.qo_st + h * p.qo_sh
-                           : (T*)(kind == 1 ? p.kc : p.vc) + (slot * p.Hkv + h) * D;
         uint4 o = raw[i][v];
         if (turned) {
           T* d = reinterpret_cast<T*>(&o);
 #pragma unroll
           for (int e = 0; e < E; ++e) d[e] = from_f32<T>(y[v][e]);
         }
-        *reinterpret_cast<uint4*>(dst + at) = o;
+        *reinterpret_cast<uint4*>((T*)dst + at) = o;
       }
     }
+    dst += dst_step;
   }
 }
 
@@ -277,10 +285,11 @@ cudaError_t launch(const NormRopeArgs& a, cudaStream_t st) {
   p.Hkv = a.Hkv;
   p.uq = (a.Hq + S::ROWS - 1) / S::ROWS;
   p.uk = (a.Hkv + S::ROWS - 1) / S::ROWS;
-  p.units = (int64_t)a.T * (p.uq + 2 * p.uk);
+  const int64_t units = (int64_t)a.T * (p.uq + 2 * p.uk);
+  if (units > INT32_MAX - THREADS) return cudaErrorInvalidValue;   // (a unit is 1 KB and more)
+  p.units = (int32_t)units;
   p.dev_status = a.dev_status;
-  const int64_t blocks = (p.units + THREADS / 32 - 1) / (THREADS / 32);
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t blocks = (units + THREADS / 32 - 1) / (THREADS / 32);
   KernelTimer timer("norm_rope_append", st);
   const bool codes = a.k_scale != nullptr;
   auto k = a.interleaved ? (codes ? norm_rope_kernel<T, D, true, true> : norm_rope_kernel<T, D, true, false>)

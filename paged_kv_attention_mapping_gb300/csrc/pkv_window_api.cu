@@ -101,6 +101,7 @@ extern "C" int pkv_norm_rope_kv_append(const void* q, int64_t q_stride_t, int64_
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.dev_status = dev.status;
+  a.num_sms = dev.num_sms;
   const cudaError_t e = launch_norm_rope(a, (cudaStream_t)stream);
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "norm_rope_kv_append");
 }
