@@ -6,9 +6,10 @@
 // columns (rows x query heads of one KV head, that is) of one sequence over the keys that
 // some of them sees. The bound is HBM: a key and a value are read once for all columns.
 //
-// Keys and values go from global memory straight into the registers that the matrix
-// instructions take them from: no shared memory, no barrier, no copy engine, so any page
-// size does, and the first products start one load after the page ids. Scores are S^T = K Q^T
+// A lane of a warp copies the pieces of keys and values that it will itself take into its
+// registers as operands: 16-byte asynchronous copies to its own places in shared memory, a few steps
+// ahead, so that many more bytes are in flight than registers would hold, and no warp
+// waits for another (no barrier, no copy engine; any page size does). Scores are S^T = K Q^T
 // with 16 keys as the rows of m16n8k16; the channels of a product are permuted, alike in K
 // and Q, so that a lane's 16 bytes of a key are its own operand. The output is O^T += V^T
 // P^T with 16 channels as the rows; a lane holds 16 bytes of each of four keys and pairs
@@ -17,6 +18,8 @@
 // memory, and the CTAs that share a piece's keys (a cluster) through distributed shared
 // memory: no workspace and one launch.
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "pkv_sm100.cuh"
 #include "pkv_window_common.cuh"
@@ -106,6 +109,17 @@ __device__ __forceinline__ float ld_cluster_f(uint32_t a) {
   return v;
 }
 
+// 16 bytes from global to shared memory, zeros where `from` is null.
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, const void* any) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from ? from : any), "r"(from ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The warps' results, then the cluster's: maximum (log2 units), sum and unnormalised
 // output of every column.
 template <int COLS, int D>
@@ -113,7 +127,6 @@ struct Merge {
   static constexpr int LD = D + 4;
   float m[NW][COLS], l[NW][COLS];
   float cm[COLS], cl[COLS];   // this CTA's
-  int bad, all_bad;
   alignas(16) float o[NW][COLS][LD];
 };
 
@@ -134,7 +147,7 @@ __device__ __forceinline__ void store8(T* dst, const float (&x)[8]) {
 // Column c of the piece is query head kvh * G + part * heads + c % heads of row c / heads. (The
 // last part of a group that HB does not divide has columns without a head.)
 template <typename TQ, int COLS, int D>
-__device__ __forceinline__ void finish(const RowsP& p, const Piece& w, Merge<COLS, D>& s, float shift) {
+__device__ __forceinline__ void finish(const RowsP& p, const Piece& w, Merge<COLS, D>& s, int& s_bad, float shift) {
   const int tid = threadIdx.x, heads = p.heads;
   const int cols = w.np * heads;
   __syncthreads();
@@ -169,10 +182,10 @@ __device__ __forceinline__ void finish(const RowsP& p, const Piece& w, Merge<COL
     cluster_sync_all();
   }
   const int parts = w.splits > 1 ? w.splits : NW;
-  bool any_bad = s.bad != 0;
+  bool any_bad = s_bad != 0;
   if (w.splits > 1) {
     any_bad = false;
-    for (int k = 0; k < parts; ++k) any_bad |= __float_as_int(ld_cluster_f(map_to_rank(&s.bad, k))) != 0;
+    for (int k = 0; k < parts; ++k) any_bad |= __float_as_int(ld_cluster_f(map_to_rank(&s_bad, k))) != 0;
   }
   if (any_bad && tid == 0 && w.split == 0) atomicOr(p.dev_status, PKV_DEV_BAD_PAGE);
   for (int u = tid * w.splits + w.split; u < cols * (D / 8) && !any_bad; u += THREADS * w.splits) {
@@ -254,30 +267,70 @@ __device__ __forceinline__ uint32_t widen(uint32_t codes) {
   return out;
 }
 
+// A warp's step of 16 keys in shared memory: their rows, then their values' rows, each row's 16-byte
+// chunks permuted within 128 bytes (by `turn`), so that the operand loads meet no bank twice: a
+// quarter of a warp takes chunks t + 4 j of keys g and g + 1, or chunks g and g + 1 of values 2t (or 2t + 1).
+template <bool KV8, int D>
+struct Share {
+  static constexpr int RB = D * (KV8 ? 1 : 2);           // bytes of a key's row
+  static constexpr int CH = RB / 16;                     // its chunks
+  static constexpr int KJ = RB / 64;                     // a lane's chunks of a key: t + 4 j
+  static constexpr int SEGS = RB >= 128 ? RB / 128 : 1;  // a lane's pieces of a value: at segment * 128 + g * VB
+  static constexpr int VB = RB >= 128 ? 16 : 8;
+  static constexpr int BYTES = 2 * 16 * RB;              // of a warp's step
+  // steps in flight: 8 KB a step three (two CTAs of 96 KB an SM), smaller ones more
+  static constexpr int STAGES = BYTES >= 8192 ? 3 : BYTES >= 4096 ? 5 : 8;
+  static __device__ __forceinline__ int turn(int r) { return ((r & 6) ^ (r & 1) << 2) & (RB >= 128 ? 7 : 3); }
+};
+
 // TQ: type of q and out. KV8: the caches hold e4m3 codes (products in f16), else TQ.
 template <typename TQ, bool KV8, int D, int NT>
-__global__ void __launch_bounds__(THREADS) window_rows_kernel(const RowsP p) {
+__global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_constant__ RowsP p) {
   using MT = typename std::conditional<KV8, __half, TQ>::type;
+  using H = Share<KV8, D>;
   constexpr bool F16 = std::is_same<MT, __half>::value;
   constexpr float SHIFT = F16 ? F16_SHIFT : 0.f;
-  constexpr int COLS = 8 * NT;
-  constexpr int RB = D * (KV8 ? 1 : 2);           // bytes of a key's row
-  constexpr int KJ = RB / 64;                     // a lane's 16-byte pieces of a key: t + 4 j
+  constexpr int COLS = 8 * NT, RB = H::RB, KJ = H::KJ, SEGS = H::SEGS, VB = H::VB, VR = VB / 4, ST = H::STAGES;
   constexpr int CPR = KV8 ? 4 : 2;                // channels a 32-bit register holds
-  constexpr int SEGS = RB >= 128 ? RB / 128 : 1;  // a lane's pieces of a value: 16 bytes (8 where a
-  constexpr int VR = RB >= 128 ? 4 : 2;           //   row has 64) at segment * 128 + g * 16
   constexpr int MT_SEG = VR * CPR / 2;            // 16-channel output tiles of a segment
-  __shared__ Merge<COLS, D> sm;
+  extern __shared__ __align__(128) unsigned char dyn[];
+  Merge<COLS, D>& sm = *reinterpret_cast<Merge<COLS, D>*>(dyn);   // (once the copies are used up)
+  __shared__ int s_bad;
   Piece w;
   if (!find_piece(p, &w)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  if (threadIdx.x == 0) sm.bad = 0;
-  __syncthreads();
+  if (threadIdx.x == 0) s_bad = 0;
 
-  // The first 16 keys of this warp: lane i % 16 looks up key i
-  const int step = w.splits * NW * 16;
-  int base = (w.split * NW + warp) * 16;
-  int next = slot_of(p, w, base + (lane & 15));
+  // 16 keys of this warp a step; lane i % 16 looks up key i
+  const int step = w.splits * NW * 16, base0 = (w.split * NW + warp) * 16;
+  unsigned char* const mine = dyn + warp * ST * H::BYTES;
+  const int64_t row = (int64_t)p.Hkv * RB;
+  const char* const kb = (const char*)p.kc + w.kvh * RB + lane % H::CH * 16;
+  const int64_t k_to_v = (const char*)p.vc - (const char*)p.kc;
+  bool bad = false;
+  auto fetch = [&](int slot, int stage) {
+    bad |= slot == -2;
+    // a copy instruction takes whole rows: 32 / CH of them
+    const uint32_t to = smem_u32(mine + stage * H::BYTES);
+#pragma unroll
+    for (int i = 0; i < H::CH / 2; ++i) {
+      const int r = i * (32 / H::CH) + lane / H::CH;
+      const int s = __shfl_sync(0xffffffffu, slot, r);
+      const char* src = s >= 0 ? kb + s * row : nullptr;
+      const uint32_t at = to + r * RB + ((lane % H::CH) ^ H::turn(r)) * 16;
+      copy_async(at, src, p.kc);
+      copy_async(at + 16 * RB, src ? src + k_to_v : nullptr, p.kc);
+    }
+  };
+  int slots[ST];
+#pragma unroll
+  for (int i = 0; i < ST; ++i) slots[i] = slot_of(p, w, base0 + i * step + (lane & 15));
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) {
+    if (base0 + i * step < w.keys.n) fetch(slots[i], i);
+    copy_commit();
+  }
+  int next = slots[ST - 1];
 
   // queries: column g of each 8, its channels in the order in which the lane's pieces of a
   // key come
@@ -340,45 +393,21 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const RowsP p) {
       for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.f;
   }
 
-  bool bad = false;
-  for (; base < w.keys.n; base += step) {
-    const int slot = next;
-    bad |= slot == -2;
-    // 16 keys' rows of this KV head; the lane's pieces of keys g, g + 8 and of the values
-    // of keys 2t, 2t + 1, 2t + 8, 2t + 9
-    const char* kb = (const char*)p.kc;
-    const char* vb = (const char*)p.vc;
-    uint4 kr[2][KJ];
-    uint32_t vr[4][SEGS][VR];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int s = __shfl_sync(0xffffffffu, slot, g + 8 * h);
-      const char* src = kb + ((int64_t)s * p.Hkv + w.kvh) * RB + t * 16;
-#pragma unroll
-      for (int j = 0; j < KJ; ++j)
-        kr[h][j] = s >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + j * 64)) : make_uint4(0, 0, 0, 0);
+  int stage = 0;
+  for (int base = base0; base < w.keys.n; base += step) {
+    __syncwarp();   // every lane has read the last step
+    // the step ST - 1 ahead goes where that was, and the page ids of the one behind it are looked up
+    const int ahead = base + (ST - 1) * step;
+    if (ahead < w.keys.n) {
+      fetch(next, stage == 0 ? ST - 1 : stage - 1);
+      next = slot_of(p, w, ahead + step + (lane & 15));
     }
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int s = __shfl_sync(0xffffffffu, slot, 2 * t + (h & 1) + 8 * (h >> 1));
-      const char* src = vb + ((int64_t)s * p.Hkv + w.kvh) * RB + g * (VR * 4);
-#pragma unroll
-      for (int j = 0; j < SEGS; ++j) {
-        if constexpr (VR == 4) {
-          const uint4 x = s >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + j * 128)) : make_uint4(0, 0, 0, 0);
-          vr[h][j][0] = x.x;
-          vr[h][j][1] = x.y;
-          vr[h][j][2] = x.z;
-          vr[h][j][3] = x.w;
-        } else {
-          const uint2 x = s >= 0 ? __ldg(reinterpret_cast<const uint2*>(src + j * 128)) : make_uint2(0, 0);
-          vr[h][j][0] = x.x;
-          vr[h][j][1] = x.y;
-        }
-      }
-    }
-    next = slot_of(p, w, base + step + (lane & 15));   // the next keys' page ids, meanwhile
-
+    copy_commit();
+    copy_wait<ST - 1>();
+    __syncwarp();   // every lane's copies have landed
+    const unsigned char* const ks = mine + stage * H::BYTES;
+    const unsigned char* const vs = ks + 16 * RB;
+    stage = stage + 1 == ST ? 0 : stage + 1;
     float c[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -386,8 +415,11 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const RowsP p) {
       for (int k = 0; k < 4; ++k) c[nt][k] = 0.f;
 #pragma unroll
     for (int j = 0; j < KJ; ++j) {
-      const uint32_t a[4] = {kr[0][j].x, kr[0][j].y, kr[0][j].z, kr[0][j].w};
-      const uint32_t b[4] = {kr[1][j].x, kr[1][j].y, kr[1][j].z, kr[1][j].w};
+      const int at = g * RB + ((t + 4 * j) ^ H::turn(g)) * 16;   // (keys g and g + 8 turn alike)
+      const uint4 k0 = *reinterpret_cast<const uint4*>(ks + at);
+      const uint4 k1 = *reinterpret_cast<const uint4*>(ks + at + 8 * RB);
+      const uint32_t a[4] = {k0.x, k0.y, k0.z, k0.w};
+      const uint32_t b[4] = {k1.x, k1.y, k1.z, k1.w};
       if constexpr (KV8) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -448,10 +480,28 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const RowsP p) {
 
     // O^T += V^T P^T: output tile i of segment j holds channels 2i, 2i + 1 of each lane's piece
 #pragma unroll
-    for (int j = 0; j < SEGS; ++j)
+    for (int j = 0; j < SEGS; ++j) {
+      uint32_t vr[4][VR];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int r = 2 * t + (h & 1) + 8 * (h >> 1);
+        const unsigned char* at = vs + r * RB + (VB == 16 ? (g + 8 * j) ^ H::turn(r) : (g >> 1) ^ H::turn(r)) * 16 +
+                                  (VB == 16 ? 0 : (g & 1) * 8);
+        if constexpr (VR == 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(at);
+          vr[h][0] = x.x;
+          vr[h][1] = x.y;
+          vr[h][2] = x.z;
+          vr[h][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(at);
+          vr[h][0] = x.x;
+          vr[h][1] = x.y;
+        }
+      }
 #pragma unroll
       for (int r = 0; r < VR; ++r) {
-        const uint32_t v0 = vr[0][j][r], v1 = vr[1][j][r], v2 = vr[2][j][r], v3 = vr[3][j][r];
+        const uint32_t v0 = vr[0][r], v1 = vr[1][r], v2 = vr[2][r], v3 = vr[3][r];
         if constexpr (KV8) {
           const uint32_t x0 = __byte_perm(v0, v1, 0x5140), x1 = __byte_perm(v2, v3, 0x5140);
           const uint32_t y0 = __byte_perm(v0, v1, 0x7362), y1 = __byte_perm(v2, v3, 0x7362);
@@ -469,9 +519,11 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const RowsP p) {
           for (int nt = 0; nt < NT; ++nt) mma<MT>(o[nt][j * MT_SEG + r], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
         }
       }
+    }
   }
-
-  if (bad) sm.bad = 1;
+  copy_wait<0>();
+  __syncthreads();   // every warp's copies are used up (and s_bad is cleared)
+  if (bad) s_bad = 1;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -492,7 +544,7 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const RowsP p) {
           *reinterpret_cast<float2*>(&sm.o[warp][c][j * (D / SEGS) + g * (MT_SEG * 2) + 2 * i]) =
               make_float2(o[nt][j * MT_SEG + i][k], o[nt][j * MT_SEG + i][2 + k]);
     }
-  finish<TQ, COLS, D>(p, w, sm, SHIFT);
+  finish<TQ, COLS, D>(p, w, sm, s_bad, SHIFT);
 }
 
 // fp32 caches, on the fused multiply-adds (tensor cores have no fp32 products): a piece is
@@ -502,10 +554,11 @@ template <int D, int HB>
 __global__ void __launch_bounds__(THREADS) window_rows_f32_kernel(const RowsP p) {
   constexpr int J = D / 32;   // a lane's pieces
   __shared__ Merge<HB, D> sm;
+  __shared__ int s_bad;
   Piece w;
   if (!find_piece(p, &w)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = lane & 7, sub = lane >> 3;
-  if (threadIdx.x == 0) sm.bad = 0;
+  if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
   float4 q[HB][J], o[HB][J];
   float m[HB], l[HB];
@@ -564,7 +617,7 @@ __global__ void __launch_bounds__(THREADS) window_rows_f32_kernel(const RowsP p)
       }
     }
   }
-  if (bad) sm.bad = 1;
+  if (bad) s_bad = 1;
 #pragma unroll
   for (int h = 0; h < HB; ++h) {
     // the warp's four groups of lanes into one
@@ -592,15 +645,16 @@ __global__ void __launch_bounds__(THREADS) window_rows_f32_kernel(const RowsP p)
       }
     }
   }
-  finish<float, HB, D>(p, w, sm, 0.f);
+  finish<float, HB, D>(p, w, sm, s_bad, 0.f);
 }
 
 template <typename K>
-cudaError_t launch_split(K kernel, int64_t pieces, int splits, cudaStream_t s, const RowsP& p) {
+cudaError_t launch_split(K kernel, int64_t pieces, int splits, cudaStream_t s, const RowsP& p, int smem = 0) {
   if (pieces * splits > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(pieces * splits));
   cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -614,15 +668,32 @@ cudaError_t launch_split(K kernel, int64_t pieces, int splits, cudaStream_t s, c
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <typename TQ, bool KV8, int D, int NT>
+cudaError_t launch_rows_kernel(const WindowArgs& a, int64_t pieces, int splits, cudaStream_t s, const RowsP& p) {
+  using H = Share<KV8, D>;
+  constexpr int ring = NW * H::STAGES * H::BYTES, merge = sizeof(Merge<8 * NT, D>);
+  constexpr int smem = ring > merge ? ring : merge;
+  static_assert(smem <= 232448 - 256, "shared memory");
+  static std::atomic<uint64_t> ready{0};   // devices whose kernel attribute is set
+  const uint64_t bit = (uint64_t)1 << (a.dev.id & 63);
+  if (!(ready.load() & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(window_rows_kernel<TQ, KV8, D, NT>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit);
+  }
+  return launch_split(window_rows_kernel<TQ, KV8, D, NT>, pieces, splits, s, p, smem);
+}
+
 template <typename TQ, bool KV8>
 cudaError_t by_shape(const WindowArgs& a, int nt, int64_t pieces, int splits, cudaStream_t s, const RowsP& p) {
   if (nt == 2) {
-    if (a.D == 64) return launch_split(window_rows_kernel<TQ, KV8, 64, 2>, pieces, splits, s, p);
-    return launch_split(window_rows_kernel<TQ, KV8, 128, 2>, pieces, splits, s, p);
+    if (a.D == 64) return launch_rows_kernel<TQ, KV8, 64, 2>(a, pieces, splits, s, p);
+    return launch_rows_kernel<TQ, KV8, 128, 2>(a, pieces, splits, s, p);
   }
-  if (a.D == 64) return launch_split(window_rows_kernel<TQ, KV8, 64, 1>, pieces, splits, s, p);
-  if (a.D == 128) return launch_split(window_rows_kernel<TQ, KV8, 128, 1>, pieces, splits, s, p);
-  return launch_split(window_rows_kernel<TQ, KV8, 256, 1>, pieces, splits, s, p);
+  if (a.D == 64) return launch_rows_kernel<TQ, KV8, 64, 1>(a, pieces, splits, s, p);
+  if (a.D == 128) return launch_rows_kernel<TQ, KV8, 128, 1>(a, pieces, splits, s, p);
+  return launch_rows_kernel<TQ, KV8, 256, 1>(a, pieces, splits, s, p);
 }
 
 }  // namespace
