@@ -42,6 +42,7 @@ struct RowsP {
   const int32_t *cu, *kv_lens, *tables;
   int32_t B, T, Hq, Hkv, G, per, P, num_pages, max_pages, window, sinks, tile_min_q, parts, heads;
   int32_t per_seq;   // pieces numbered for each sequence (0: as first_piece has it)
+  int32_t beside;    // launched beside the tile kernel, which is the one before it
   PageDiv div;
   float scale_log2;
   const float *ks, *vs;
@@ -60,9 +61,11 @@ struct Piece {
 // False: nothing to do (for every CTA of the cluster).
 __device__ __forceinline__ bool find_piece(const RowsP& p, Piece* w) {
   const int lane = threadIdx.x & 31;
-  pdl_wait();
+  // The tile kernel lets this one start once the kernel before it is done, so nothing is
+  // left to wait for but its end, which the last block sees to: this grid is not over before it.
+  if (!p.beside) pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0) check_cu(p.cu, p.B, p.T, p.dev_status);
+  if (blockIdx.x == 0 && !p.beside) check_cu(p.cu, p.B, p.T, p.dev_status);
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(w->splits));
   w->split = (int)cluster_rank();
   int64_t u = blockIdx.x / w->splits;
@@ -89,6 +92,10 @@ __device__ __forceinline__ bool find_piece(const RowsP& p, Piece* w) {
   return true;
 }
 
+__device__ __forceinline__ void end(const RowsP& p) {
+  if (p.beside && blockIdx.x == gridDim.x - 1) pdl_wait();
+}
+
 // Slot of key number i in the pool: -1 past the last key, -2 where its page is outside it.
 __device__ __forceinline__ int slot_of(const RowsP& p, const Piece& w, int i) {
   if (i >= w.keys.n) return -1;
@@ -109,6 +116,9 @@ __device__ __forceinline__ float ld_cluster_f(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 // 16 bytes from global to shared memory, zeros where `from` is null.
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from, const void* any) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from ? from : any), "r"(from ? 16 : 0)
@@ -279,7 +289,7 @@ struct Share {
   static constexpr int VB = RB >= 128 ? 16 : 8;
   static constexpr int BYTES = 2 * 16 * RB;              // of a warp's step
   // steps in flight: 8 KB a step three (two CTAs of 96 KB an SM), smaller ones more
-  static constexpr int STAGES = BYTES >= 8192 ? 3 : BYTES >= 4096 ? 5 : 8;
+  static constexpr int STAGES = BYTES >= 8192 ? 3 : BYTES >= 4096 ? 3 : 4;
   static __device__ __forceinline__ int turn(int r) { return ((r & 6) ^ (r & 1) << 2) & (RB >= 128 ? 7 : 3); }
 };
 
@@ -297,7 +307,7 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_const
   Merge<COLS, D>& sm = *reinterpret_cast<Merge<COLS, D>*>(dyn);   // (once the copies are used up)
   __shared__ int s_bad;
   Piece w;
-  if (!find_piece(p, &w)) return;
+  if (!find_piece(p, &w)) return end(p);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (threadIdx.x == 0) s_bad = 0;
 
@@ -310,8 +320,22 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_const
   bool bad = false;
   auto fetch = [&](int slot, int stage) {
     bad |= slot == -2;
-    // a copy instruction takes whole rows: 32 / CH of them
+    // a copy instruction takes whole rows: 32 / CH of them. Keys that follow one another in one page
+    // (most steps) need no look-up a row
     const uint32_t to = smem_u32(mine + stage * H::BYTES);
+    const int s0 = __shfl_sync(0xffffffffu, slot, 0);
+    if (__all_sync(0xffffffffu, slot >= 0 && slot == s0 + (lane & 15))) {
+      const char* src = kb + (s0 + lane / H::CH) * row;
+#pragma unroll
+      for (int i = 0; i < H::CH / 2; ++i) {
+        const int r = i * (32 / H::CH) + lane / H::CH;
+        const uint32_t at = to + r * RB + ((lane % H::CH) ^ H::turn(r)) * 16;
+        copy_async(at, src);
+        copy_async(at + 16 * RB, src + k_to_v);
+        src += 32 / H::CH * row;
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < H::CH / 2; ++i) {
       const int r = i * (32 / H::CH) + lane / H::CH;
@@ -379,6 +403,11 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_const
     cs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
   }
 
+  int pos[NT][2];   // positions of columns 2t, 2t + 1
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) pos[nt][k] = w.p_first + (nt * 8 + 2 * t + k) / p.heads;
   float m[NT][2], l[NT][2], o[NT][SEGS * MT_SEG][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -393,7 +422,10 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_const
       for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.f;
   }
 
+  // TT: tiles of columns that have any (a count known when compiled lets them overlap)
   int stage = 0;
+  auto work = [&](auto tt) {
+  constexpr int TT = decltype(tt)::value;
   for (int base = base0; base < w.keys.n; base += step) {
     __syncwarp();   // every lane has read the last step
     // the step ST - 1 ahead goes where that was, and the page ids of the one behind it are looked up
@@ -408,9 +440,9 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_const
     const unsigned char* const ks = mine + stage * H::BYTES;
     const unsigned char* const vs = ks + 16 * RB;
     stage = stage + 1 == ST ? 0 : stage + 1;
-    float c[NT][4];
+    float c[TT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < TT; ++nt)
 #pragma unroll
       for (int k = 0; k < 4; ++k) c[nt][k] = 0.f;
 #pragma unroll
@@ -425,34 +457,36 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_const
         for (int r = 0; r < 4; ++r) {
           const uint32_t a0 = widen(a[r]), a1 = widen(b[r]), a2 = widen(a[r] >> 16), a3 = widen(b[r] >> 16);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma<MT>(c[nt], a0, a1, a2, a3, qf[nt][4 * j + r][0], qf[nt][4 * j + r][1]);
+          for (int nt = 0; nt < TT; ++nt) mma<MT>(c[nt], a0, a1, a2, a3, qf[nt][4 * j + r][0], qf[nt][4 * j + r][1]);
         }
       } else {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < TT; ++nt)
             mma<MT>(c[nt], a[2 * r], b[2 * r], a[2 * r + 1], b[2 * r + 1], qf[nt][2 * j + r][0], qf[nt][2 * j + r][1]);
       }
     }
 
-    // scores of keys g, g + 8 for columns 2t, 2t + 1, in log2 units
-    uint32_t pb[NT][2];
+    // scores of keys g, g + 8 for columns 2t, 2t + 1, in log2 units. Most steps have 16 keys that
+    // every row sees
+    uint32_t pb[TT][2];
+    const int ka = key_at(w.keys, base), kz = key_at(w.keys, base + 15);
+    const bool all = base + 16 <= w.keys.n &&
+                     (w.np == 1 || (kz <= w.p_first && (ka > w.p_first + w.np - 1 - p.window || kz < p.sinks)));
     const int i0 = base + g, i1 = i0 + 8;
     const int k0 = key_at(w.keys, i0), k1 = key_at(w.keys, i1);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < TT; ++nt) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float a = c[nt][k] * cs[nt][k], b = c[nt][2 + k] * cs[nt][k];
-        bool va = i0 < w.keys.n, vb2 = i1 < w.keys.n;
-        if (w.np > 1) {
-          const int pos = w.p_first + (nt * 8 + 2 * t + k) / p.heads;
-          va = va && seen(k0, pos, p.window, p.sinks);
-          vb2 = vb2 && seen(k1, pos, p.window, p.sinks);
+        if (!all) {
+          const bool va = i0 < w.keys.n && (w.np == 1 || seen(k0, pos[nt][k], p.window, p.sinks));
+          const bool vb2 = i1 < w.keys.n && (w.np == 1 || seen(k1, pos[nt][k], p.window, p.sinks));
+          a = va ? a : -INFINITY;
+          b = vb2 ? b : -INFINITY;
         }
-        a = va ? a : -INFINITY;
-        b = vb2 ? b : -INFINITY;
         float top = fmaxf(a, b);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
@@ -508,7 +542,7 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_const
           const uint32_t a0 = widen(x0), a1 = widen(x0 >> 16), a2 = widen(x1), a3 = widen(x1 >> 16);
           const uint32_t b0 = widen(y0), b1 = widen(y0 >> 16), b2 = widen(y1), b3 = widen(y1 >> 16);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+          for (int nt = 0; nt < TT; ++nt) {
             mma<MT>(o[nt][j * MT_SEG + 2 * r], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
             mma<MT>(o[nt][j * MT_SEG + 2 * r + 1], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
           }
@@ -516,11 +550,14 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_const
           const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
           const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma<MT>(o[nt][j * MT_SEG + r], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          for (int nt = 0; nt < TT; ++nt) mma<MT>(o[nt][j * MT_SEG + r], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
         }
       }
     }
   }
+  };
+  if (NT == 1 || w.np * p.heads <= 8) work(std::integral_constant<int, 1>());
+  else work(std::integral_constant<int, NT>());
   copy_wait<0>();
   __syncthreads();   // every warp's copies are used up (and s_bad is cleared)
   if (bad) s_bad = 1;
@@ -545,6 +582,7 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_const
               make_float2(o[nt][j * MT_SEG + i][k], o[nt][j * MT_SEG + i][2 + k]);
     }
   finish<TQ, COLS, D>(p, w, sm, s_bad, SHIFT);
+  end(p);
 }
 
 // fp32 caches, on the fused multiply-adds (tensor cores have no fp32 products): a piece is
@@ -725,8 +763,10 @@ cudaError_t launch_window_rows(const WindowArgs& a, cudaStream_t s) {
   p.lse = a.lse;
   p.dev_status = a.dev.status;
   const bool f32 = a.kv_dtype == PKV_F32;
-  // 16 heads of a KV head are 16 columns, but at head_dim 256 two parts of 8 (registers)
-  const int nt = p.G > 8 && a.D <= 128 ? 2 : 1;
+  // 16 heads of a KV head are 16 columns, but at head_dim 256 two parts of 8 (registers). Calls
+  // with more rows than sequences take 16 columns too, so that more rows of a sequence share its
+  // keys (a piece of 8 columns or fewer leaves the second tile's products out)
+  const int nt = (p.G > 8 || a.T > a.B) && a.D <= 128 && !f32 ? 2 : 1;
   p.heads = f32 ? (a.D == 256 ? 2 : 4) : p.G < 8 * nt ? p.G : 8 * nt;
   p.parts = (p.G + p.heads - 1) / p.heads;
   p.per = f32 ? 1 : 8 * nt / p.heads;
@@ -741,14 +781,19 @@ cudaError_t launch_window_rows(const WindowArgs& a, cudaStream_t s) {
     slots = p.per == 1 ? a.T : (int64_t)a.B + a.T / p.per;
   }
   const int64_t pieces = slots * a.Hkv * p.parts;
-  // CTAs that share a piece's keys: more while the GPU has room for them and each still has
-  // two rounds of its warps
-  const int64_t busy = (p.per_seq ? (int64_t)a.B : slots) * a.Hkv * p.parts;
+  // CTAs that share a piece's keys: more while all have a place at once (2.6 an SM) and each still
+  // has two rounds of its warps. bf16, 4096 keys, D 128: 8 pieces by 1 / 2 / 4 / 8: 54 / 31 / 19 / 13 us,
+  // 64 pieces 56 / 34 / 27 / 33; of 516 keys 10.6 / 9.3 / 8.6 / 14.1; 256 pieces of 260 keys 10 / 17 / 27 / 49.
+  // (with the tile kernel: about the pieces of the sequences, as even as the rows are)
+  int64_t a_seq = p.per_seq;
+  if (a_seq && ((int64_t)a.T / a.B + p.per) / p.per < a_seq) a_seq = ((int64_t)a.T / a.B + p.per) / p.per;
+  const int64_t busy = (p.per_seq ? a.B * a_seq : slots) * a.Hkv * p.parts;
   const int64_t cap = (int64_t)a.max_pages * a.P;
   const int64_t keys = (int64_t)a.window + a.sinks < cap ? (int64_t)a.window + a.sinks : cap;
   int splits = 1;
-  while (splits < MAX_SPLIT && busy * splits * 2 <= (int64_t)a.dev.num_sms * 4 && keys >= splits * 2 * NW * 32)
+  while (splits < MAX_SPLIT && busy * splits * 2 * 10 <= (int64_t)a.dev.num_sms * 26 && keys >= splits * 2 * NW * 32)
     splits *= 2;
+  p.beside = a.tile_min_q != INT32_MAX;
   KernelTimer timer("window_rows", s);
   if (f32) {
     if (a.D == 64) return launch_split(window_rows_f32_kernel<64, 4>, pieces, splits, s, p);
