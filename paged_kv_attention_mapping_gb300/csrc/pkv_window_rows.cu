@@ -61,10 +61,12 @@ struct Piece {
 // False: nothing to do (for every CTA of the cluster).
 __device__ __forceinline__ bool find_piece(const RowsP& p, Piece* w) {
   const int lane = threadIdx.x & 31;
-  // The tile kernel lets this one start once the kernel before it is done, so nothing is
-  // left to wait for but its end, which the last block sees to: this grid is not over before it.
-  if (!p.beside) pdl_wait();
-  pdl_trigger();
+  // The tile kernel lets this one start once the kernel before it is done, so nothing is left to wait
+  // for but its end, which the last block sees to: this grid is not over before it.
+  if (!p.beside) {
+    pdl_wait();
+    pdl_trigger();
+  }
   if (blockIdx.x == 0 && !p.beside) check_cu(p.cu, p.B, p.T, p.dev_status);
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(w->splits));
   w->split = (int)cluster_rank();
@@ -686,11 +688,37 @@ __global__ void __launch_bounds__(THREADS) window_rows_f32_kernel(const RowsP p)
   finish<float, HB, D>(p, w, sm, s_bad, 0.f);
 }
 
+struct Call {
+  int64_t pieces, busy, keys;   // pieces of the grid, those of them with rows, keys of the longest
+};
+
+// CTAs that share a piece's keys: as many as have a place at once (`occupancy` an SM, an eighth of them
+// left for sequences that have more pieces than the estimate), while each has two rounds of its warps.
+// A second wave costs more than the wider split gains: bf16, D 128, 4096 keys: 8 pieces by 1 / 2 / 4 / 8
+// CTAs take 54 / 31 / 19 / 13 us, 64 pieces 56 / 34 / 27 / 33; 64 of 516 keys 10.6 / 9.3 / 8.6 / 14.1; 256 of
+// 260 keys 10 / 17 / 27 / 49; 72 pieces of 8000 e4m3 keys by 4 / 5 / 6 / 7: 59 / 51 / 46 / 68.
+int splits_of(const Call& c, int occupancy, int num_sms) {
+  int64_t s = (int64_t)occupancy * num_sms * 7 / 8 / c.busy;
+  if (s > MAX_SPLIT) s = MAX_SPLIT;
+  if (s > c.keys / (2 * NW * 16)) s = c.keys / (2 * NW * 16);
+  return s < 1 ? 1 : (int)s;
+}
+
 template <typename K>
-cudaError_t launch_split(K kernel, int64_t pieces, int splits, cudaStream_t s, const RowsP& p, int smem = 0) {
-  if (pieces * splits > INT32_MAX) return cudaErrorInvalidValue;
+cudaError_t launch_kernel(K kernel, const WindowArgs& a, const Call& c, int smem, std::atomic<int>* occupancy,
+                          cudaStream_t s, const RowsP& p) {
+  int occ = occupancy[a.dev.id & 63].load();   // (the same for every call of this kernel on the device)
+  if (occ == 0) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, THREADS, smem);
+    if (e != cudaSuccess) return e;
+    if (occ < 1) return cudaErrorInvalidConfiguration;
+    occupancy[a.dev.id & 63].store(occ);
+  }
+  const int splits = splits_of(c, occ, a.dev.num_sms);
+  if (c.pieces * splits > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(pieces * splits));
+  cfg.gridDim = dim3((unsigned)(c.pieces * splits));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -707,31 +735,27 @@ cudaError_t launch_split(K kernel, int64_t pieces, int splits, cudaStream_t s, c
 }
 
 template <typename TQ, bool KV8, int D, int NT>
-cudaError_t launch_rows_kernel(const WindowArgs& a, int64_t pieces, int splits, cudaStream_t s, const RowsP& p) {
+cudaError_t launch16(const WindowArgs& a, const Call& c, cudaStream_t s, const RowsP& p) {
   using H = Share<KV8, D>;
   constexpr int ring = NW * H::STAGES * H::BYTES, merge = sizeof(Merge<8 * NT, D>);
   constexpr int smem = ring > merge ? ring : merge;
   static_assert(smem <= 232448 - 256, "shared memory");
-  static std::atomic<uint64_t> ready{0};   // devices whose kernel attribute is set
-  const uint64_t bit = (uint64_t)1 << (a.dev.id & 63);
-  if (!(ready.load() & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(window_rows_kernel<TQ, KV8, D, NT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(bit);
-  }
-  return launch_split(window_rows_kernel<TQ, KV8, D, NT>, pieces, splits, s, p, smem);
+  static std::atomic<int> occupancy[64];
+  return launch_kernel(window_rows_kernel<TQ, KV8, D, NT>, a, c, smem, occupancy, s, p);
 }
 
 template <typename TQ, bool KV8>
-cudaError_t by_shape(const WindowArgs& a, int nt, int64_t pieces, int splits, cudaStream_t s, const RowsP& p) {
-  if (nt == 2) {
-    if (a.D == 64) return launch_rows_kernel<TQ, KV8, 64, 2>(a, pieces, splits, s, p);
-    return launch_rows_kernel<TQ, KV8, 128, 2>(a, pieces, splits, s, p);
-  }
-  if (a.D == 64) return launch_rows_kernel<TQ, KV8, 64, 1>(a, pieces, splits, s, p);
-  if (a.D == 128) return launch_rows_kernel<TQ, KV8, 128, 1>(a, pieces, splits, s, p);
-  return launch_rows_kernel<TQ, KV8, 256, 1>(a, pieces, splits, s, p);
+cudaError_t by_shape(const WindowArgs& a, int nt, const Call& c, cudaStream_t s, const RowsP& p) {
+  if (nt == 2) return a.D == 64 ? launch16<TQ, KV8, 64, 2>(a, c, s, p) : launch16<TQ, KV8, 128, 2>(a, c, s, p);
+  if (a.D == 64) return launch16<TQ, KV8, 64, 1>(a, c, s, p);
+  if (a.D == 128) return launch16<TQ, KV8, 128, 1>(a, c, s, p);
+  return launch16<TQ, KV8, 256, 1>(a, c, s, p);
+}
+
+template <int D, int HB>
+cudaError_t launch32(const WindowArgs& a, const Call& c, cudaStream_t s, const RowsP& p) {
+  static std::atomic<int> occupancy[64];
+  return launch_kernel(window_rows_f32_kernel<D, HB>, a, c, 0, occupancy, s, p);
 }
 
 }  // namespace
@@ -781,30 +805,25 @@ cudaError_t launch_window_rows(const WindowArgs& a, cudaStream_t s) {
     slots = p.per == 1 ? a.T : (int64_t)a.B + a.T / p.per;
   }
   const int64_t pieces = slots * a.Hkv * p.parts;
-  // CTAs that share a piece's keys: more while all have a place at once (2.6 an SM) and each still
-  // has two rounds of its warps. bf16, 4096 keys, D 128: 8 pieces by 1 / 2 / 4 / 8: 54 / 31 / 19 / 13 us,
-  // 64 pieces 56 / 34 / 27 / 33; of 516 keys 10.6 / 9.3 / 8.6 / 14.1; 256 pieces of 260 keys 10 / 17 / 27 / 49.
-  // (with the tile kernel: about the pieces of the sequences, as even as the rows are)
-  int64_t a_seq = p.per_seq;
-  if (a_seq && ((int64_t)a.T / a.B + p.per) / p.per < a_seq) a_seq = ((int64_t)a.T / a.B + p.per) / p.per;
-  const int64_t busy = (p.per_seq ? a.B * a_seq : slots) * a.Hkv * p.parts;
+  // pieces that have rows: all, or (with the tile kernel) as many as the rows of even sequences make
+  int64_t busy = slots;
+  if (p.per_seq) {
+    const int64_t even = ((int64_t)a.T + (int64_t)a.B * (p.per - 1) / 2) / p.per;
+    if (even < busy) busy = even < 1 ? 1 : even;
+  }
+  Call call{pieces, busy * a.Hkv * p.parts, 0};
   const int64_t cap = (int64_t)a.max_pages * a.P;
-  const int64_t keys = (int64_t)a.window + a.sinks < cap ? (int64_t)a.window + a.sinks : cap;
-  int splits = 1;
-  while (splits < MAX_SPLIT && busy * splits * 2 * 10 <= (int64_t)a.dev.num_sms * 26 && keys >= splits * 2 * NW * 32)
-    splits *= 2;
+  call.keys = (int64_t)a.window + a.sinks < cap ? (int64_t)a.window + a.sinks : cap;
   p.beside = a.tile_min_q != INT32_MAX;
   KernelTimer timer("window_rows", s);
   if (f32) {
-    if (a.D == 64) return launch_split(window_rows_f32_kernel<64, 4>, pieces, splits, s, p);
-    if (a.D == 128) return launch_split(window_rows_f32_kernel<128, 4>, pieces, splits, s, p);
-    return launch_split(window_rows_f32_kernel<256, 2>, pieces, splits, s, p);
+    if (a.D == 64) return launch32<64, 4>(a, call, s, p);
+    if (a.D == 128) return launch32<128, 4>(a, call, s, p);
+    return launch32<256, 2>(a, call, s, p);
   }
   if (a.kv_dtype == PKV_FP8_E4M3)
-    return a.dtype == PKV_BF16 ? by_shape<__nv_bfloat16, true>(a, nt, pieces, splits, s, p)
-                               : by_shape<__half, true>(a, nt, pieces, splits, s, p);
-  return a.dtype == PKV_BF16 ? by_shape<__nv_bfloat16, false>(a, nt, pieces, splits, s, p)
-                             : by_shape<__half, false>(a, nt, pieces, splits, s, p);
+    return a.dtype == PKV_BF16 ? by_shape<__nv_bfloat16, true>(a, nt, call, s, p) : by_shape<__half, true>(a, nt, call, s, p);
+  return a.dtype == PKV_BF16 ? by_shape<__nv_bfloat16, false>(a, nt, call, s, p) : by_shape<__half, false>(a, nt, call, s, p);
 }
 
 }  // namespace pkv
