@@ -7,6 +7,7 @@ or cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import itertools
@@ -184,7 +185,7 @@ def lib():
     L.pkv_window_attention.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, PC, vp, vp, f32, vp,
                                        vp, vp]
     L.pkv_window_attention.restype = ctypes.c_int
-    L.pkv_copy_pages.argtypes = [ctypes.POINTER(vp), i32, i32, i32, i64, vp, vp, vp, i32, vp]
+    L.pkv_copy_pages.argtypes = [vp, i32, i32, i32, i64, vp, vp, vp, i32, vp]
     L.pkv_copy_pages.restype = ctypes.c_int
     L.pkv_remap_pages.argtypes = [vp, i64, vp, i32, vp]
     L.pkv_remap_pages.restype = ctypes.c_int
@@ -813,36 +814,45 @@ def latent_prefill(q, cu_seqlens_q, k_nope, v, k_rope, cu_seqlens_k, scale: floa
 
 @functools.lru_cache(maxsize=256)
 def _cache_desc_of(shape, dtype):
-    return ctypes.byref(CacheDesc(*shape, _code_of(dtype)))
+    """Heads, head_dim, the descriptor as an argument and whether the cache holds codes."""
+    if len(shape) != 4:
+        raise ValueError("a cache must be [num_pages, page_size, num_kv_heads, head_dim]")
+    return shape[2], shape[3], ctypes.byref(CacheDesc(*shape, _code_of(dtype))), _code_of(dtype) == PKV_FP8_E4M3
 
 
-def _caches(where, k_cache, v_cache, k_scale, v_scale):
-    """The caches' shape and descriptor, as an argument, and whether they hold codes."""
+def _bad_device(where, dev):
+    return ValueError(f"{where} needs CUDA tensors" if dev < 0 else f"{where}: all tensors must be on one CUDA device")
+
+
+def _caches(where, k_cache, v_cache):
     shape, dtype = k_cache.shape, k_cache.dtype
-    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dtype:
-        raise ValueError(f"{where}: k_cache and v_cache must share one shape [num_pages, page_size, num_kv_heads, "
-                         "head_dim] and one dtype")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        raise ValueError(f"{where}: caches must be contiguous")
-    codes = _code_of(dtype) == PKV_FP8_E4M3
-    if codes != (k_scale is not None) or codes != (v_scale is not None):
+    if v_cache.dtype is not dtype or v_cache.shape != shape or not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError(f"{where}: k_cache and v_cache must be contiguous and share one shape [num_pages, page_size, "
+                         "num_kv_heads, head_dim] and one dtype")
+    return _cache_desc_of(shape, dtype)
+
+
+def _scales(where, k_scale, v_scale, heads, dev, codes):
+    """Pointers of an e4m3 cache's scales."""
+    if not codes or k_scale is None or v_scale is None:
         raise ValueError(f"{where}: an e4m3 cache needs k_scale and v_scale, other caches take none")
-    if codes:
-        for t in (k_scale, v_scale):
-            if t.dtype is not _torch.float32 or t.shape != (shape[2],) or not t.is_contiguous():
-                raise ValueError(f"{where}: scales must be contiguous float32 [num_kv_heads]")
-    return shape, _cache_desc_of(shape, dtype), codes
+    for t in (k_scale, v_scale):
+        if t.get_device() != dev:
+            raise _bad_device(where, dev)
+        if t.dtype is not _torch.float32 or t.shape != (heads,) or not t.is_contiguous():
+            raise ValueError(f"{where}: scales must be contiguous float32 [num_kv_heads]")
+    return k_scale.data_ptr(), v_scale.data_ptr()
 
 
-def _heads(where, name, t, dtype, shape):
+def _heads(where, name, t, dtype, T, H, D):
     """Strides of tokens and heads of [T, H, D] rows."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{where}: {name} must be {list(shape)} of dtype {dtype}")
+    if t.dtype is not dtype or t.shape != (T, H, D):
+        raise ValueError(f"{where}: {name} must be [{T}, {H}, {D}] of dtype {dtype}")
     st, sh, s1 = t.stride()
     if s1 != 1:
         raise ValueError(f"{where}: {name} must be contiguous in its last dimension")
     # (a dimension of one entry may have any stride)
-    return (st if shape[0] > 1 else 0), (sh if shape[1] > 1 else 0)
+    return (st if T > 1 else 0), (sh if H > 1 else 0)
 
 
 def norm_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight=None, k_weight=None,
@@ -860,42 +870,57 @@ def norm_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
     None). Returns q_out."""
     torch = _torch or _load_torch()
     where = "norm_rope_kv_append"
-    dev = _on_one_device(where, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, k_scale,
-                         v_scale, q_out)
+    dev = q.get_device()
+    if (dev < 0 or k.get_device() != dev or v.get_device() != dev or positions.get_device() != dev
+            or cos_sin.get_device() != dev or slot_mapping.get_device() != dev or k_cache.get_device() != dev
+            or v_cache.get_device() != dev or (q_out is not None and q_out.get_device() != dev)):
+        raise _bad_device(where, dev)
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return norm_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight,
                                        eps, interleaved, k_scale, v_scale, q_out, stream)
-    (_, _, Hkv, D), desc, codes = _caches(where, k_cache, v_cache, k_scale, v_scale)
+    Hkv, D, desc, codes = _caches(where, k_cache, v_cache)
+    ks = vs = qw = kw = None
+    if codes or k_scale is not None or v_scale is not None:
+        ks, vs = _scales(where, k_scale, v_scale, Hkv, dev, codes)
     if (positions.dtype is not torch.int32 or slot_mapping.dtype is not torch.int64
             or cos_sin.dtype is not torch.float32):
         raise TypeError(f"{where}: positions int32, slot_mapping int64, cos_sin float32")
     if not (positions.is_contiguous() and slot_mapping.is_contiguous() and cos_sin.is_contiguous()):
         raise ValueError(f"{where}: positions, slot_mapping and cos_sin must be contiguous")
-    dtype, shape, tokens, table = q.dtype, q.shape, slot_mapping.shape, cos_sin.shape
+    dtype, tokens, table = q.dtype, slot_mapping.shape, cos_sin.shape
     if not codes and dtype is not k_cache.dtype:
         raise TypeError(f"{where}: q, k, v and the caches must share one dtype (but for e4m3 caches)")
     if len(tokens) != 1 or positions.shape != tokens or len(table) != 3 or table[2] != 2:
         raise ValueError(f"{where}: positions and slot_mapping must be [T], cos_sin [max_pos, r / 2, 2]")
     T, = tokens
-    if len(shape) != 3 or shape[0] != T or shape[2] != D:
+    if q.dim() != 3:
         raise ValueError(f"{where}: q must be [T, Hq, {D}]")
+    Hq = q.shape[1]
     if q_out is None:
-        q_out = _lent(torch.empty(shape, dtype=dtype, device=q.device), stream)
-    qs, ks, vs = (_heads(where, "q", q, dtype, shape), _heads(where, "k", k, dtype, (T, Hkv, D)),
-                  _heads(where, "v", v, dtype, (T, Hkv, D)))
-    qo = _heads(where, "q_out", q_out, dtype, shape)
-    if (T > 1 and qo[0] == 0) or (shape[1] > 1 and qo[1] == 0):
+        q_out = _lent(torch.empty(q.shape, dtype=dtype, device=q.device), stream)
+    qo_t, qo_h = _heads(where, "q_out", q_out, dtype, T, Hq, D)
+    if (T > 1 and qo_t == 0) or (Hq > 1 and qo_h == 0):
         raise ValueError(f"{where}: q_out must not be a broadcast view")
+    q_t, q_h = _heads(where, "q", q, dtype, T, Hq, D)
+    k_t, k_h = _heads(where, "k", k, dtype, T, Hkv, D)
+    v_t, v_h = _heads(where, "v", v, dtype, T, Hkv, D)
     for w in (q_weight, k_weight):
-        if w is not None and (w.dtype is not dtype or w.shape != (D,) or not w.is_contiguous()):
-            raise ValueError(f"{where}: norm weights must be contiguous [{D}] of q's dtype")
+        if w is not None:
+            if w.get_device() != dev:
+                raise _bad_device(where, dev)
+            if w.dtype is not dtype or w.shape != (D,) or not w.is_contiguous():
+                raise ValueError(f"{where}: norm weights must be contiguous [{D}] of q's dtype")
+    if q_weight is not None:
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        kw = k_weight.data_ptr()
     on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
-    st = lib().pkv_norm_rope_kv_append(
-        q.data_ptr(), *qs, k.data_ptr(), *ks, v.data_ptr(), *vs, _code_of(dtype), _ptr(q_weight), _ptr(k_weight), eps,
+    st = (_lib or lib()).pkv_norm_rope_kv_append(
+        q.data_ptr(), q_t, q_h, k.data_ptr(), k_t, k_h, v.data_ptr(), v_t, v_h, _code_of(dtype), qw, kw, eps,
         positions.data_ptr(), cos_sin.data_ptr(), table[0], 2 * table[1], 1 if interleaved else 0,
-        slot_mapping.data_ptr(), T, shape[1], k_cache.data_ptr(), v_cache.data_ptr(), desc, _ptr(k_scale),
-        _ptr(v_scale), q_out.data_ptr(), *qo, on)
+        slot_mapping.data_ptr(), T, Hq, k_cache.data_ptr(), v_cache.data_ptr(), desc, ks, vs, q_out.data_ptr(), qo_t,
+        qo_h, on)
     if st:
         _check(st, "pkv_norm_rope_kv_append")
     return q_out
@@ -933,12 +958,19 @@ def window_attention(q, cu_seqlens_q, kv_lens, page_tables, k_cache, v_cache, sc
     i32 = torch.int32
     if cu_seqlens_q.dtype is not i32 or kv_lens.dtype is not i32 or page_tables.dtype is not i32:
         raise TypeError(f"{where}: index tensors must be int32")
-    dev = _on_one_device(where, q, cu_seqlens_q, kv_lens, page_tables, k_cache, v_cache, k_scale, v_scale, out, lse)
+    dev = q.get_device()
+    if (dev < 0 or cu_seqlens_q.get_device() != dev or kv_lens.get_device() != dev or page_tables.get_device() != dev
+            or k_cache.get_device() != dev or v_cache.get_device() != dev
+            or (out is not None and out.get_device() != dev) or (lse is not None and lse.get_device() != dev)):
+        raise _bad_device(where, dev)
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return window_attention(q, cu_seqlens_q, kv_lens, page_tables, k_cache, v_cache, scale, window, sinks,
                                     k_scale, v_scale, out, lse, want_lse, stream)
-    (_, _, Hkv, D), desc, codes = _caches(where, k_cache, v_cache, k_scale, v_scale)
+    Hkv, D, desc, codes = _caches(where, k_cache, v_cache)
+    ks = vs = None
+    if codes or k_scale is not None or v_scale is not None:
+        ks, vs = _scales(where, k_scale, v_scale, Hkv, dev, codes)
     shape, dtype, tables, cu, lens = q.shape, q.dtype, page_tables.shape, cu_seqlens_q.shape, kv_lens.shape
     if not codes and dtype is not k_cache.dtype:
         raise TypeError(f"{where}: q and the caches must share one dtype (but for e4m3 caches)")
@@ -953,16 +985,19 @@ def window_attention(q, cu_seqlens_q, kv_lens, page_tables, k_cache, v_cache, sc
         out = _lent(torch.empty(shape, dtype=dtype, device=q.device), stream)
     elif out.dtype is not dtype or out.shape != shape or not out.is_contiguous():
         raise _bad_out(where, D)
+    lse_ptr = None
     if lse is not None:
         if lse.dtype is not torch.float32 or lse.shape != (T, Hq) or not lse.is_contiguous():
             raise _bad_out(where, D)
+        lse_ptr = lse.data_ptr()
     elif want_lse:
         lse = _lent(torch.empty((T, Hq), dtype=torch.float32, device=q.device), stream)
+        lse_ptr = lse.data_ptr()
     on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
-    st = lib().pkv_window_attention(q.data_ptr(), _code_of(dtype), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(),
-                                    page_tables.data_ptr(), cu[0] - 1, T, Hq, tables[1], window, sinks,
-                                    k_cache.data_ptr(), v_cache.data_ptr(), desc, _ptr(k_scale), _ptr(v_scale), scale,
-                                    out.data_ptr(), _ptr(lse), on)
+    st = (_lib or lib()).pkv_window_attention(
+        q.data_ptr(), _code_of(dtype), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), page_tables.data_ptr(), cu[0] - 1, T,
+        Hq, tables[1], window, sinks, k_cache.data_ptr(), v_cache.data_ptr(), desc, ks, vs, scale, out.data_ptr(), lse_ptr,
+        on)
     if st:
         _check(st, "pkv_window_attention")
     return out, lse
@@ -980,19 +1015,22 @@ def copy_pages(caches, src, dst, tokens=None, stream=None):
     caches = list(caches)
     if not caches:
         return
-    dev = _on_one_device(where, src, dst, tokens, *caches)
+    dev = src.get_device()
+    devices = {c.get_device() for c in caches}
+    devices.add(dst.get_device())
+    if dev < 0 or devices != {dev} or (tokens is not None and tokens.get_device() != dev):
+        raise _bad_device(where, min(dev, *devices))
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return copy_pages(caches, src, dst, tokens, stream)
     first = caches[0]
-    shape, dtype = first.shape, first.dtype
-    if len(shape) < 3:
+    shape = first.shape
+    # (sets of all caches' attributes: the cheapest way to compare many of them)
+    if len({c.shape for c in caches}) != 1 or len({c.dtype for c in caches}) != 1 or not all(
+            [c.is_contiguous() for c in caches]):
+        raise ValueError(f"{where}: caches must be contiguous and share one shape and dtype")
+    if len(shape) < 3 or 0 in shape:
         raise ValueError(f"{where}: a cache must be [num_pages, page_size, ...]")
-    ptrs = []
-    for c in caches:
-        if c.shape != shape or c.dtype is not dtype or not c.is_contiguous():
-            raise ValueError(f"{where}: caches must be contiguous and share one shape and dtype")
-        ptrs.append(c.data_ptr())
     n = src.shape
     if src.dtype is not torch.int32 or dst.dtype is not torch.int32 or (tokens is not None
                                                                        and tokens.dtype is not torch.int32):
@@ -1001,11 +1039,9 @@ def copy_pages(caches, src, dst, tokens=None, stream=None):
         raise ValueError(f"{where}: src, dst and tokens must be [n]")
     if not (src.is_contiguous() and dst.is_contiguous() and (tokens is None or tokens.is_contiguous())):
         raise ValueError(f"{where}: src, dst and tokens must be contiguous")
-    slot_bytes = first.element_size()
-    for x in shape[2:]:
-        slot_bytes *= x
     on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
-    st = lib().pkv_copy_pages((ctypes.c_void_p * len(ptrs))(*ptrs), len(ptrs), shape[0], shape[1], slot_bytes,
+    ptrs = array.array("Q", [c.data_ptr() for c in caches])
+    st = lib().pkv_copy_pages(ptrs.buffer_info()[0], len(ptrs), shape[0], shape[1], first.nbytes // (shape[0] * shape[1]),
                               src.data_ptr(), dst.data_ptr(), _ptr(tokens), n[0], on)
     if st:
         _check(st, "pkv_copy_pages")
