@@ -1006,10 +1006,11 @@ def window_attention(q, cu_seqlens_q, kv_lens, page_tables, k_cache, v_cache, sc
 def copy_pages(caches, src, dst, tokens=None, stream=None):
     """Copy pages within each of several caches of one pool's page ids (pkv_copy_pages).
 
-    caches: contiguous tensors [N, P, ...] of one shape and dtype (keys and values of all
-    layers, latent caches); src, dst int32 [n] on their device: page dst[i] gets page
-    src[i] in every cache (negative: no copy), with tokens int32 [n] only its first
-    tokens[i] slots. No page may be dst of one copy and src or dst of another."""
+    caches: contiguous tensors of one size in bytes (keys and values of all layers,
+    latent caches), all with the N pages of P slots of the first, [N, P, ...]; src, dst int32
+    [n] on their device: page dst[i] gets page src[i] in every cache (negative: no copy),
+    with tokens int32 [n] only its first tokens[i] slots. No page may be dst of one copy and
+    src or dst of another."""
     torch = _torch or _load_torch()
     where = "copy_pages"
     caches = list(caches)
@@ -1026,9 +1027,8 @@ def copy_pages(caches, src, dst, tokens=None, stream=None):
     first = caches[0]
     shape = first.shape
     # (sets of all caches' attributes: the cheapest way to compare many of them)
-    if len({c.shape for c in caches}) != 1 or len({c.dtype for c in caches}) != 1 or not all(
-            [c.is_contiguous() for c in caches]):
-        raise ValueError(f"{where}: caches must be contiguous and share one shape and dtype")
+    if len({c.nbytes for c in caches}) != 1 or not all([c.is_contiguous() for c in caches]):
+        raise ValueError(f"{where}: caches must be contiguous and of one size in bytes")
     if len(shape) < 3 or 0 in shape:
         raise ValueError(f"{where}: a cache must be [num_pages, page_size, ...]")
     n = src.shape

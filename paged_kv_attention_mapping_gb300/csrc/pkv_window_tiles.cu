@@ -15,8 +15,8 @@
 //               before the first window and after the last row): 0 * NaN must not reach O.
 //               Over an e4m3 cache warps 10 and 11 instead widen every key and value tile to
 //               f16 in its slot, with those rows as zeros.
-// Steps are the key tiles that hold sinks and those from the first window's to the last
-// row's. Each step has a range of 32-key pieces that a query tile sees at all; loads,
+// Steps are 128 keys each: from key 0 on while there are sinks, then from the first window's first key
+// (rounded down to 32) to the last row's. Each step has a range of 32-key pieces that a query tile sees at all; loads,
 // products and the softmax take that range only (a window's ends are a quarter of a tile
 // wide on average, not half of one and a half), and a query tile without one skips the step.
 // The softmax keeps a running maximum and sum; O is rescaled in TMEM only when a row's
@@ -64,7 +64,7 @@ struct TilesP {
 struct Tile {
   int valid, b, kvh, row0, np, p_first;
   int lo, sinks;          // keys of the work tile: [0, sinks) and [lo, p_first + np)
-  int js, j0, steps;      // steps 0 .. js - 1 are key tiles 0 .. js - 1, later ones j0 + step - js
+  int js, ws, steps;      // steps 0 .. js - 1 begin at key 128 step, later ones at ws + 128 (step - js)
   int bad;                // a page outside the pool
 };
 
@@ -83,7 +83,7 @@ __device__ __forceinline__ Range range_of(int k0, int sinks, int lo, int end) {
   r.c1 = last > first ? (last + PIECE - 1) / PIECE : r.c0;
   return r;
 }
-__device__ __forceinline__ int step_tile(const Tile& t, int i) { return i < t.js ? i : t.j0 + i - t.js; }
+__device__ __forceinline__ int step_key(const Tile& t, int i) { return i < t.js ? i * BN : t.ws + (i - t.js) * BN; }
 __device__ __forceinline__ Range union_range(const Tile& t, int k0) {
   return range_of(k0, t.sinks, t.lo, t.p_first + t.np);
 }
@@ -97,11 +97,12 @@ __device__ __forceinline__ Range tile_range(const Tile& t, int w, int PP, int wi
 // products back to back has no time for it): for query tile w, in byte w, the first piece and (3 bits on) the
 // number of pieces it sees, and (bit 7) whether this is its last step.
 constexpr uint32_t WHOLE_STEP = (uint32_t)(BN / PIECE) << 3;   // of one query tile
-__device__ __forceinline__ uint32_t step_word(const Tile& t, int nq, int PP, int window, int sinks, int kt) {
+__device__ __forceinline__ uint32_t step_word(const Tile& t, int nq, int PP, int window, int sinks, int k0) {
   uint32_t word = 0;
   for (int w = 0; w < nq; ++w) {
-    const Range r = tile_range(t, w, PP, window, sinks, kt * BN);
-    const uint32_t last = kt == (t.p_first + min((w + 1) * PP, t.np) - 1) / BN;
+    const Range r = tile_range(t, w, PP, window, sinks, k0);
+    const int last_key = t.p_first + min((w + 1) * PP, t.np) - 1;
+    const uint32_t last = last_key >= k0 && last_key < k0 + BN;
     word |= ((uint32_t)r.c0 | (uint32_t)(r.c1 - r.c0) << 3 | last << 7) << (8 * w);
   }
   return word;
@@ -424,8 +425,8 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
         ti.lo = max(0, ti.p_first - p.window + 1);
         ti.sinks = min(p.sinks, ti.lo);
         ti.js = (ti.sinks + BN - 1) / BN;
-        ti.j0 = max(ti.js, ti.lo / BN);
-        ti.steps = ti.js + max(0, p_last / BN - ti.j0 + 1);
+        ti.ws = max(ti.js * BN, ti.lo / PIECE * PIECE);
+        ti.steps = ti.js + (p_last >= ti.ws ? (p_last - ti.ws) / BN + 1 : 0);
         ti.valid = 1;
       }
       const uint32_t e = t & 1;
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
       }
       const int32_t* pt = p.tables + (int64_t)ti.b * p.max_pages;
       for (int i = 0; i < ti.steps && ok; ++i) {
-        const int k0 = step_tile(ti, i) * BN;
+        const int k0 = step_key(ti, i);
         const Range r = union_range(ti, k0);
         // lane (block, half): box rows of one page, 64 channels (e4m3: all 128); the rows of
         // blocks without a key that is seen are left as they are
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&s_tile[e].bad, 1);
         const bool load = in && !bad;
-        const uint32_t word = step_word(ti, nq, p.PP, p.window, p.sinks, k0 / BN);
+        const uint32_t word = step_word(ti, nq, p.PP, p.window, p.sinks, k0);
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)(p.box * 128);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
         const Tile ti = s_tile[e];
         if (!ti.valid) break;
         for (int i = 0; i < ti.steps; ++i) {
-          const Range r = union_range(ti, step_tile(ti, i) * BN);
+          const Range r = union_range(ti, step_key(ti, i));
           const uint32_t slot = (ring + 2 * i + 1) % NS;
           if (!has_gaps(r)) continue;
           if (!wait(&bar_land[slot], (landed >> slot) & 1)) {
@@ -741,11 +742,11 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
         float m_run = -INFINITY, l_run = 0.f;
         bool first = true;
         // keys that every row of the tile sees: [0, all_sinks) and (all_lo, pa]
-        const int steps = tile->steps, js = tile->js, j0 = tile->j0 - js;
+        const int steps = tile->steps, js = tile->js, ws = tile->ws - js * BN;
         const int first_key = max(0, pa - p.window + 1), all_lo = max(pb - p.window, -1);
         const int my_sinks = min(p.sinks, first_key);
         for (int j = 0; j < steps; ++j) {
-          const int k0 = (j < js ? j : j0 + j) * BN;
+          const int k0 = j * BN + (j < js ? 0 : ws);
           if (!(k0 < my_sinks || (k0 + BN > first_key && k0 <= pb))) continue;
           const bool whole = (k0 > all_lo && k0 + BN - 1 <= pa) || k0 + BN <= my_sinks;
           // S_w complete also means every earlier MMA (the PV that read P_w) is done
