@@ -599,7 +599,8 @@ int pkv_rope_table_scaled(double base, int32_t rotary_dim, const pkv_rope_scalin
  *   scale         > 0 and finite
  *   k_scale, v_scale  device, fp32 [num_kv_heads] for an e4m3 cache, NULL otherwise
  *   lse           device, fp32 [total_q, num_q_heads] or NULL
- * head_dim is 64, 128 or 256; num_q_heads / num_kv_heads 1 to 8 or 16; any page_size.
+ * head_dim is 64, 128 or 256; num_q_heads / num_kv_heads 1 to 8 or 16, num_q_heads up to 4096; any
+ * page_size, with max_pages_per_seq * page_size at most 2^31 - 65536.
  * Pages without a key that some row of their sequence sees are not read, nor are their
  * table entries: they may be freed, entries behind the window and past the sinks may be
  * -1 (pkv_pool_trim, pkv_pack_tick_window), and slots that no row sees may hold anything.

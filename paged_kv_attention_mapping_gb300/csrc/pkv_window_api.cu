@@ -126,7 +126,8 @@ extern "C" int pkv_window_attention(const void* q, int32_t q_dtype, const int32_
   const int g = num_q_heads / cache->num_kv_heads;
   if (g > 8 && g != 16) return PKV_E_SHAPE;
   if (total_q > 0 && num_seqs > 0 && max_pages_per_seq < 1) return PKV_E_SHAPE;
-  if ((int64_t)max_pages_per_seq * cache->page_size > INT32_MAX) return PKV_E_SHAPE;
+  // (positions a few steps past the last key stay within 32 bits)
+  if ((int64_t)max_pages_per_seq * cache->page_size > INT32_MAX - 65535) return PKV_E_SHAPE;
   if (total_q == 0 || num_seqs == 0) return PKV_OK;
   if (!q || !cu_seqlens_q || !kv_lens || !page_tables || !k_cache || !v_cache || !out) return PKV_E_NULL;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||

@@ -66,6 +66,8 @@ __device__ __forceinline__ bool find_piece(const RowsP& p, Piece* w) {
   if (!p.beside) {
     pdl_wait();
     pdl_trigger();
+  } else {
+    __threadfence();   // (no line that an earlier kernel left in this SM's L1 is read)
   }
   if (blockIdx.x == 0 && !p.beside) check_cu(p.cu, p.B, p.T, p.dev_status);
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(w->splits));
