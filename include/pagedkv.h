@@ -524,6 +524,7 @@ int pkv_latent_prefill(const void* q, const int32_t* cu_seqlens_q, const void* k
 /* pkv_norm_rope_kv_append — norm queries and keys per head, rotate them by position,
  * write keys and values into their slots and queries to q_out, in one pass.
  *
+ * Its arguments come as a struct (there are thirty of them):
  *   q, k, v       device, head h of token t at + t * stride_t + h * stride_h (elements of
  *                 src_dtype; strides >= 0 and multiples of 16 bytes; views of one
  *                 projection's output will do), head_dim values each
@@ -540,7 +541,7 @@ int pkv_latent_prefill(const void* q, const int32_t* cu_seqlens_q, const void* k
  *   positions     device, int32 [num_tokens]: each token's entry of the table
  *   slot_mapping  device, int64 [num_tokens]; negative: the token's key and value are not
  *                 stored (its query is written). A slot named twice gets one of its tokens
- *   k_cache, v_cache  the pools, head_dim 64, 128 or 256
+ *   k_cache, v_cache, cache  the pools and their description, head_dim 64, 128 or 256
  *   k_scale, v_scale  device, fp32 [num_kv_heads] (> 0) for an e4m3 cache, NULL otherwise:
  *                 codes of x / scale, the float32 quotient rounded to nearest, saturating
  *   q_out         device, as q (strides must keep heads apart); may be q itself with the
@@ -550,14 +551,23 @@ int pkv_latent_prefill(const void* q, const int32_t* cu_seqlens_q, const void* k
  * nothing of that token is written; a slot outside the pool sets PKV_DEV_BAD_SLOT and the
  * token's key and value are not written.
  * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_DEVICE, PKV_E_CUDA. */
-int pkv_norm_rope_kv_append(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
-                            int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
-                            int64_t v_stride_h, int32_t src_dtype, const void* q_weight, const void* k_weight,
-                            float eps, const int32_t* positions, const float* cos_sin, int32_t max_pos,
-                            int32_t rotary_dim, int32_t interleaved, const int64_t* slot_mapping,
-                            int32_t num_tokens, int32_t num_q_heads, void* k_cache, void* v_cache,
-                            const pkv_cache_desc* cache, const float* k_scale, const float* v_scale, void* q_out,
-                            int64_t qo_stride_t, int64_t qo_stride_h, pkv_stream_t stream);
+typedef struct {
+  const void *q, *k, *v;
+  void* q_out;
+  int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h, qo_stride_t, qo_stride_h;
+  const void *q_weight, *k_weight;
+  const int32_t* positions;
+  const float* cos_sin;
+  const int64_t* slot_mapping;
+  void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  int32_t src_dtype, num_tokens, num_q_heads, max_pos, rotary_dim, interleaved;
+  float eps;
+  pkv_cache_desc cache;
+} pkv_norm_rope_args;
+
+/* args is read before the call returns. */
+int pkv_norm_rope_kv_append(const pkv_norm_rope_args* args, pkv_stream_t stream);
 
 /* How the angles f_i = base^(-2i / rotary_dim) of the pairs are stretched for contexts
  * longer than the model was trained on. */

@@ -12,6 +12,7 @@ import ctypes
 import functools
 import itertools
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -84,6 +85,10 @@ class CacheDesc(ctypes.Structure):
 class LatentDesc(ctypes.Structure):
     _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
                 ("rope_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+# pkv_norm_rope_args: pointers, strides, pointers, sizes, the cache's description
+_NORM_ROPE_ARGS = struct.Struct("@4P8q9P6if5i")
 
 
 class RopeScaling(ctypes.Structure):
@@ -176,8 +181,7 @@ def lib():
                                      ctypes.c_float, vp, vp, vp, sz, vp]
     L.pkv_latent_prefill.restype = ctypes.c_int
     PC, f32 = ctypes.POINTER(CacheDesc), ctypes.c_float
-    L.pkv_norm_rope_kv_append.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, vp, vp, f32, vp, vp, i32, i32,
-                                          i32, vp, i32, i32, vp, vp, PC, vp, vp, vp, i64, i64, vp]
+    L.pkv_norm_rope_kv_append.argtypes = [ctypes.c_char_p, vp]
     L.pkv_norm_rope_kv_append.restype = ctypes.c_int
     L.pkv_rope_table_scaled.argtypes = [ctypes.c_double, i32, ctypes.POINTER(RopeScaling), i32,
                                         ctypes.POINTER(f32)]
@@ -879,8 +883,8 @@ def norm_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
         with torch.cuda.device(dev):
             return norm_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight,
                                        eps, interleaved, k_scale, v_scale, q_out, stream)
-    Hkv, D, desc, codes = _caches(where, k_cache, v_cache)
-    ks = vs = qw = kw = None
+    Hkv, D, _, codes = _caches(where, k_cache, v_cache)
+    ks = vs = qw = kw = 0
     if codes or k_scale is not None or v_scale is not None:
         ks, vs = _scales(where, k_scale, v_scale, Hkv, dev, codes)
     if (positions.dtype is not torch.int32 or slot_mapping.dtype is not torch.int64
@@ -916,11 +920,12 @@ def norm_rope_kv_append(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
     if k_weight is not None:
         kw = k_weight.data_ptr()
     on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
-    st = (_lib or lib()).pkv_norm_rope_kv_append(
-        q.data_ptr(), q_t, q_h, k.data_ptr(), k_t, k_h, v.data_ptr(), v_t, v_h, _code_of(dtype), qw, kw, eps,
-        positions.data_ptr(), cos_sin.data_ptr(), table[0], 2 * table[1], 1 if interleaved else 0,
-        slot_mapping.data_ptr(), T, Hq, k_cache.data_ptr(), v_cache.data_ptr(), desc, ks, vs, q_out.data_ptr(), qo_t,
-        qo_h, on)
+    args = _NORM_ROPE_ARGS.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), q_t, q_h, k_t, k_h, v_t, v_h, qo_t, qo_h, qw, kw,
+        positions.data_ptr(), cos_sin.data_ptr(), slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs,
+        _code_of(dtype), T, Hq, table[0], 2 * table[1], 1 if interleaved else 0, eps, *k_cache.shape,
+        _code_of(k_cache.dtype))
+    st = (_lib or lib()).pkv_norm_rope_kv_append(args, on)
     if st:
         _check(st, "pkv_norm_rope_kv_append")
     return q_out

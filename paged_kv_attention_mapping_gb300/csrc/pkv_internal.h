@@ -273,7 +273,6 @@ struct NormRopeArgs {
   void *kc, *vc, *q_out;
   const float *k_scale, *v_scale;   // e4m3 caches, else null
   int32_t* dev_status;
-  int num_sms;
 };
 cudaError_t launch_norm_rope(const NormRopeArgs& a, cudaStream_t s);
 

@@ -44,68 +44,63 @@ int check(const pkv_cache_desc* c, int32_t src_dtype, const float* k_scale, cons
 
 }  // namespace
 
-extern "C" int pkv_norm_rope_kv_append(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
-                                       int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
-                                       int64_t v_stride_h, int32_t src_dtype, const void* q_weight,
-                                       const void* k_weight, float eps, const int32_t* positions,
-                                       const float* cos_sin, int32_t max_pos, int32_t rotary_dim,
-                                       int32_t interleaved, const int64_t* slot_mapping, int32_t num_tokens,
-                                       int32_t num_q_heads, void* k_cache, void* v_cache,
-                                       const pkv_cache_desc* cache, const float* k_scale, const float* v_scale,
-                                       void* q_out, int64_t qo_stride_t, int64_t qo_stride_h, pkv_stream_t stream) {
-  const int st = check(cache, src_dtype, k_scale, v_scale);
+extern "C" int pkv_norm_rope_kv_append(const pkv_norm_rope_args* args, pkv_stream_t stream) {
+  if (!args) return PKV_E_NULL;
+  const pkv_norm_rope_args& g = *args;
+  const pkv_cache_desc& cache = g.cache;
+  const int st = check(&cache, g.src_dtype, g.k_scale, g.v_scale);
   if (st != PKV_OK) return st;
-  if (num_tokens < 0 || num_q_heads < 1 || num_q_heads > MAX_HEADS || max_pos < 1) return PKV_E_SHAPE;
-  if (rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > cache->head_dim) return PKV_E_SHAPE;
-  if (!(eps >= 0.f) || !isfinite(eps)) return PKV_E_SHAPE;
-  const int elt = elt_bytes(src_dtype);
-  const int64_t strides[] = {q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h, qo_stride_t,
-                             qo_stride_h};
+  if (g.num_tokens < 0 || g.num_q_heads < 1 || g.num_q_heads > MAX_HEADS || g.max_pos < 1) return PKV_E_SHAPE;
+  if (g.rotary_dim < 16 || g.rotary_dim % 16 != 0 || g.rotary_dim > cache.head_dim) return PKV_E_SHAPE;
+  if (!(g.eps >= 0.f) || !isfinite(g.eps)) return PKV_E_SHAPE;
+  const int elt = elt_bytes(g.src_dtype);
+  const int64_t strides[] = {g.q_stride_t, g.q_stride_h, g.k_stride_t,  g.k_stride_h,
+                             g.v_stride_t, g.v_stride_h, g.qo_stride_t, g.qo_stride_h};
   for (int64_t s : strides)
     if (!stride_ok(s, elt)) return PKV_E_SHAPE;
-  if (num_tokens == 0) return PKV_OK;
-  if (!q || !k || !v || !positions || !cos_sin || !slot_mapping || !k_cache || !v_cache || !q_out) return PKV_E_NULL;
-  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) ||
-      !aligned(v_cache, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(cos_sin, 16) ||
-      !aligned(slot_mapping, 8) || !aligned(positions, 4))
+  if (g.num_tokens == 0) return PKV_OK;
+  if (!g.q || !g.k || !g.v || !g.positions || !g.cos_sin || !g.slot_mapping || !g.k_cache || !g.v_cache || !g.q_out)
+    return PKV_E_NULL;
+  if (!aligned(g.q, 16) || !aligned(g.k, 16) || !aligned(g.v, 16) || !aligned(g.q_out, 16) || !aligned(g.k_cache, 16) ||
+      !aligned(g.v_cache, 16) || !aligned(g.q_weight, 16) || !aligned(g.k_weight, 16) || !aligned(g.cos_sin, 16) ||
+      !aligned(g.slot_mapping, 8) || !aligned(g.positions, 4))
     return PKV_E_ALIGN;
   DeviceView dev;
   const int ds = current_device(&dev);
   if (ds != PKV_OK) return ds;
   NormRopeArgs a{};
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.q_weight = q_weight;
-  a.k_weight = k_weight;
-  a.q_st = q_stride_t;
-  a.q_sh = q_stride_h;
-  a.k_st = k_stride_t;
-  a.k_sh = k_stride_h;
-  a.v_st = v_stride_t;
-  a.v_sh = v_stride_h;
-  a.qo_st = qo_stride_t;
-  a.qo_sh = qo_stride_h;
-  a.pool_slots = (int64_t)cache->num_pages * cache->page_size;
-  a.eps = eps;
-  a.positions = positions;
-  a.cos_sin = cos_sin;
-  a.slots = slot_mapping;
-  a.max_pos = max_pos;
-  a.rot = rotary_dim;
-  a.interleaved = interleaved != 0;
-  a.T = num_tokens;
-  a.Hq = num_q_heads;
-  a.Hkv = cache->num_kv_heads;
-  a.D = cache->head_dim;
-  a.dtype = src_dtype;
-  a.kc = k_cache;
-  a.vc = v_cache;
-  a.q_out = q_out;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
+  a.q = g.q;
+  a.k = g.k;
+  a.v = g.v;
+  a.q_weight = g.q_weight;
+  a.k_weight = g.k_weight;
+  a.q_st = g.q_stride_t;
+  a.q_sh = g.q_stride_h;
+  a.k_st = g.k_stride_t;
+  a.k_sh = g.k_stride_h;
+  a.v_st = g.v_stride_t;
+  a.v_sh = g.v_stride_h;
+  a.qo_st = g.qo_stride_t;
+  a.qo_sh = g.qo_stride_h;
+  a.pool_slots = (int64_t)cache.num_pages * cache.page_size;
+  a.eps = g.eps;
+  a.positions = g.positions;
+  a.cos_sin = g.cos_sin;
+  a.slots = g.slot_mapping;
+  a.max_pos = g.max_pos;
+  a.rot = g.rotary_dim;
+  a.interleaved = g.interleaved != 0;
+  a.T = g.num_tokens;
+  a.Hq = g.num_q_heads;
+  a.Hkv = cache.num_kv_heads;
+  a.D = cache.head_dim;
+  a.dtype = g.src_dtype;
+  a.kc = g.k_cache;
+  a.vc = g.v_cache;
+  a.q_out = g.q_out;
+  a.k_scale = g.k_scale;
+  a.v_scale = g.v_scale;
   a.dev_status = dev.status;
-  a.num_sms = dev.num_sms;
   const cudaError_t e = launch_norm_rope(a, (cudaStream_t)stream);
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "norm_rope_kv_append");
 }

@@ -266,8 +266,11 @@ def _desc(N=4, P=16, H=2, D=64, t="bf16"):
 def _append(lib, desc=None, q=FAKE, qs=(512, 64), k=FAKE, ks=(128, 64), v=FAKE, t="bf16", qw=None, kw=None, eps=1e-6,
             pos=FAKE, cs=FAKE, max_pos=8, rot=64, slots=FAKE, T=2, H=8, kc=FAKE, sc=None, qo=FAKE):
     d = desc or _desc()
-    return lib.pkv_norm_rope_kv_append(q, *qs, k, *ks, v, 128, 64, CODES[t], qw, kw, eps, pos, cs, max_pos, rot, 0, slots,
-                                       T, H, kc, FAKE, ctypes.byref(d), sc, sc, qo, 512, 64, None)
+    at = lambda x: 0 if x is None else x.value
+    args = binding._NORM_ROPE_ARGS.pack(at(q), at(k), at(v), at(qo), *qs, *ks, 128, 64, 512, 64, at(qw), at(kw), at(pos),
+                                        at(cs), at(slots), at(kc), FAKE.value, at(sc), at(sc), CODES[t], T, H, max_pos, rot,
+                                        0, eps, d.num_pages, d.page_size, d.num_kv_heads, d.head_dim, d.dtype)
+    return lib.pkv_norm_rope_kv_append(args, None)
 
 
 def _attend(lib, desc=None, q=FAKE, t="bf16", cu=FAKE, B=1, T=2, H=8, W=4, window=8, sinks=0, kc=FAKE, ks=None, vs=None,
@@ -284,6 +287,7 @@ def test_bad_caches_are_refused(lib, kw, status):
 
 
 def test_append_refusals(lib):
+    assert lib.pkv_norm_rope_kv_append(None, None) == -1
     for kw in (dict(T=-1), dict(H=0), dict(H=5000), dict(max_pos=0), dict(rot=0), dict(rot=8), dict(rot=24), dict(rot=80),
                dict(eps=-1.0), dict(eps=math.nan), dict(qs=(510, 64)), dict(qs=(512, -64)), dict(ks=(1 << 31, 64))):
         assert _append(lib, **kw) == -3, kw
