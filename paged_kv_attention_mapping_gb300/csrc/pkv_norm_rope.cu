@@ -16,7 +16,7 @@
 namespace pkv {
 namespace {
 
-constexpr int THREADS = 128;
+constexpr int THREADS = 128, MIN_BLOCKS = 7;   // (72 registers a thread)
 
 struct NormP {
   const void *q, *k, *v, *qw, *kw;
@@ -32,25 +32,28 @@ struct NormP {
 };
 
 // The bound is HBM: (2 Hq + 2 Hkv) D values of the source type and 2 Hkv D of the cache's a token.
-// 4192 tokens at 32 / 8 heads of 128 (bf16, 105 MB) take 24.3 us, 4.3 TB/s, 65 % of the copy
-// bandwidth; 64 tokens 3.1 us, a launch and two rounds of loads. What is left is instructions:
-// 580 a unit of 4 KB moved. Steps taken: angles and weights multiplied once a unit (41 -> 27.7 us),
-// blocks of 128 at 64 registers (26.6), addresses stepped and the approximate root, which is within
-// 2 ulp (24.3). Without gain: two or eight passes in flight (33, 35), a unit's loads issued while the
-// one before is worked on (27 to 37), streaming loads (25.2).
+// 4192 tokens at 32 / 8 heads of 128 (bf16, 105 MB) take 23.4 us, 4.5 TB/s, 67 % of the copy
+// bandwidth; 64 tokens 2.8 us, a launch and two rounds of loads. What is left is latency and
+// instructions (issue slots 57 % busy, 41 % of the warps resident). Steps taken: angles and weights
+// multiplied once a unit (41 -> 27.7 us), blocks of 128 at 64 registers (26.6), addresses stepped and the
+// approximate root, which is within 2 ulp (24.3), a lane holding both halves of its pairs (23.4;
+// 64 tokens 3.1 -> 2.8). Without gain: more passes in flight (33, 35), a unit's loads issued while the one
+// before is worked on (27 to 37), streaming loads (25.2), two chunks a unit (24.6), six or eight blocks
+// an SM in place of seven (23.9, 26.2).
 //
 // A warp's unit: ROWS consecutive head rows of one token, all queries, all keys or
-// all values. LR = lanes of a row, a lane holding NV vectors of E values, E values
-// apart by LR * E. The warp's 32 / LR rows of a pass are neighbours; PASSES of them
-// are in flight at once. A lane keeps the angles and weights of its values for the
-// whole unit: the table's row is then read once a unit, not once a head.
+// all values. A lane holds two vectors of E values of a row, those that the rotation pairs
+// with one another where it pairs halves, so that nothing is exchanged for it; LR = D / (2 E) lanes hold
+// a row. The warp's 32 / LR rows of a pass are neighbours; PASSES of them are in flight at once.
+// A lane keeps the angles and weights of its values for the whole unit: the table's
+// row is then read once a unit, not once a head.
 template <typename T, int D>
 struct Shape {
   static constexpr int E = 16 / sizeof(T);
-  static constexpr int NV = D / E > 32 ? D / E / 32 : 1;
+  static constexpr int NV = 2;
   static constexpr int LR = D / E / NV;
   static constexpr int RPW = 32 / LR;
-  static constexpr int PASSES = NV > 1 ? 2 : 4;
+  static constexpr int PASSES = 2;
   static constexpr int ROWS = RPW * PASSES;
 };
 
@@ -77,9 +80,9 @@ __device__ __forceinline__ void unpack(const uint4& raw, float (&x)[E]) {
 }
 
 template <typename T, int D, bool NEAR, bool CODES>
-__global__ void __launch_bounds__(THREADS, Shape<T, D>::NV > 1 ? 4 : 8) norm_rope_kernel(const NormP p) {
+__global__ void __launch_bounds__(THREADS, MIN_BLOCKS) norm_rope_kernel(const NormP p) {
   using S = Shape<T, D>;
-  constexpr int E = S::E, NV = S::NV, LR = S::LR, PASSES = S::PASSES;
+  constexpr int E = S::E, LR = S::LR, PASSES = S::PASSES, NVEC = D / E;
   pdl_wait();
   pdl_trigger();   // what starts now waits for this grid's end before it writes, and before it relies on what it read
   const int unit = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
@@ -94,18 +97,22 @@ __global__ void __launch_bounds__(THREADS, Shape<T, D>::NV > 1 ? 4 : 8) norm_rop
   u -= kind == 0 ? 0 : kind == 1 ? p.uq : p.uq + p.uk;
   const int H = kind == 0 ? p.Hq : p.Hkv;
   const int h0 = u * S::ROWS + sub;
+  // this lane's vectors: l and its partner half a rotation on, or two that are not rotated
+  const int half = p.rot / 2, hv = NEAR ? 0 : half / E, rest = NVEC - 2 * hv;
+  const bool paired = !NEAR && l < hv;
+  const int at0 = (paired ? l : hv + l) * E, at1 = at0 + (paired ? hv : rest / 2) * E;
   const T* src = kind == 0 ? (const T*)p.q + t * p.q_st : kind == 1 ? (const T*)p.k + t * p.k_st
                                                                     : (const T*)p.v + t * p.v_st;
   const int64_t sh = kind == 0 ? p.q_sh : kind == 1 ? p.k_sh : p.v_sh;
   const int pos = __ldg(p.positions + t);
   const int64_t slot = kind == 0 ? 0 : __ldg(p.slots + t);
-  uint4 raw[PASSES][NV];
-  src += h0 * sh + l * E;
+  uint4 raw[PASSES][2];
+  src += h0 * sh;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-      raw[i][v] = h0 + i * S::RPW < H ? *reinterpret_cast<const uint4*>(src + v * LR * E) : make_uint4(0, 0, 0, 0);
+    const bool have = h0 + i * S::RPW < H;
+    raw[i][0] = have ? *reinterpret_cast<const uint4*>(src + at0) : make_uint4(0, 0, 0, 0);
+    raw[i][1] = have ? *reinterpret_cast<const uint4*>(src + at1) : make_uint4(0, 0, 0, 0);
     src += S::RPW * sh;
   }
   if (pos < 0 || pos >= p.max_pos) {
@@ -121,131 +128,116 @@ __global__ void __launch_bounds__(THREADS, Shape<T, D>::NV > 1 ? 4 : 8) norm_rop
   }
   const T* w = (const T*)(kind == 0 ? p.qw : kind == 1 ? p.kw : nullptr);
   const bool turned = kind != 2;
-  const int half = p.rot / 2;
   // A value becomes r (x A + z B): z its partner, A its weight times the cosine, B the partner's
   // weight times the sine with the sign it takes, r what the norm divides by. Where nothing is
   // rotated the second term is left out.
-  float2 A[NV][E / 2], B[NV][E / 2];
-  int from[NV];   // lane that holds the partners (of vector v or 1 - v where other[v])
-  bool other[NV], rotated[NV];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int at = (v * LR + l) * E;
-    rotated[v] = turned && at < p.rot;
-    const bool hi = at >= half;
-    const int mate = NEAR ? at : rotated[v] ? (hi ? at - half : at + half) : at;
-    from[v] = (mate / E) % LR + sub * LR;
-    other[v] = mate / (LR * E) != v;
-    float own[E], its[E];
+  float2 A[2][E / 2], B[2][E / 2];
+  bool rotated[2];
+  {
+    float w0[E], w1[E];
     if (w) {
-      unpack<T, E>(__ldg(reinterpret_cast<const uint4*>(w + at)), own);
-      unpack<T, E>(__ldg(reinterpret_cast<const uint4*>(w + mate)), its);
+      unpack<T, E>(__ldg(reinterpret_cast<const uint4*>(w + at0)), w0);
+      unpack<T, E>(__ldg(reinterpret_cast<const uint4*>(w + at1)), w1);
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) own[e] = its[e] = 1.f;
+      for (int e = 0; e < E; ++e) w0[e] = w1[e] = 1.f;
     }
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
-      A[v][e / 2] = make_float2(own[e], own[e + 1]);
-      B[v][e / 2] = make_float2(0.f, 0.f);
+      A[0][e / 2] = make_float2(w0[e], w0[e + 1]);
+      A[1][e / 2] = make_float2(w1[e], w1[e + 1]);
+      B[0][e / 2] = B[1][e / 2] = make_float2(0.f, 0.f);
     }
-    if (rotated[v]) {
-      const float4* cs = reinterpret_cast<const float4*>(p.cs + (int64_t)pos * half + (NEAR ? at / 2 : hi ? at - half : at));
+    const float2* cs = p.cs + (int64_t)pos * half;
+    if constexpr (NEAR) {
+      rotated[0] = turned && at0 < p.rot;
+      rotated[1] = turned && at1 < p.rot;
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        if constexpr (NEAR) {
-          // pairs (e, e + 1): one angle
-          const float4 q = __ldg(cs + e / 4);
-          const float c = e & 2 ? q.z : q.x, sn = e & 2 ? q.w : q.y;
-          A[v][e / 2] = make_float2(own[e] * c, own[e + 1] * c);
-          B[v][e / 2] = make_float2(-its[e + 1] * sn, its[e] * sn);
-        } else {
-          const float4 q = __ldg(cs + e / 2);
-          A[v][e / 2] = make_float2(own[e] * q.x, own[e + 1] * q.z);
-          B[v][e / 2] = hi ? make_float2(its[e] * q.y, its[e + 1] * q.w) : make_float2(-its[e] * q.y, -its[e + 1] * q.w);
+      for (int v = 0; v < 2; ++v)
+        if (rotated[v]) {
+          const float4* c = reinterpret_cast<const float4*>(cs + (v ? at1 : at0) / 2);
+#pragma unroll
+          for (int e = 0; e < E; e += 4) {
+            // pairs (e, e + 1), (e + 2, e + 3): an angle each
+            const float4 q = __ldg(c + e / 4);
+            const float2 a = A[v][e / 2], b = A[v][e / 2 + 1];
+            A[v][e / 2] = make_float2(a.x * q.x, a.y * q.x);
+            B[v][e / 2] = make_float2(-a.y * q.y, a.x * q.y);
+            A[v][e / 2 + 1] = make_float2(b.x * q.z, b.y * q.z);
+            B[v][e / 2 + 1] = make_float2(-b.y * q.w, b.x * q.w);
+          }
+        }
+    } else {
+      rotated[0] = rotated[1] = turned && paired;
+      if (rotated[0]) {
+        const float4* c = reinterpret_cast<const float4*>(cs + at0);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float4 q = __ldg(c + e / 2);
+          const float2 a = A[0][e / 2], b = A[1][e / 2];
+          A[0][e / 2] = make_float2(a.x * q.x, a.y * q.z);
+          B[0][e / 2] = make_float2(-b.x * q.y, -b.y * q.w);
+          A[1][e / 2] = make_float2(b.x * q.x, b.y * q.z);
+          B[1][e / 2] = make_float2(a.x * q.y, a.y * q.w);
         }
       }
     }
   }
   // where this lane's first row goes, and how far its next one is, in bytes
   constexpr int CB = CODES ? 1 : (int)sizeof(T);
-  char* dst = kind == 0 ? (char*)((T*)p.qo + t * p.qo_st + h0 * p.qo_sh + l * E)
-                        : (char*)(kind == 1 ? p.kc : p.vc) + ((slot * p.Hkv + h0) * D + l * E) * CB;
+  char* dst = kind == 0 ? (char*)((T*)p.qo + t * p.qo_st + h0 * p.qo_sh)
+                        : (char*)(kind == 1 ? p.kc : p.vc) + (slot * p.Hkv + h0) * D * CB;
   const int64_t dst_step = kind == 0 ? S::RPW * p.qo_sh * (int64_t)sizeof(T) : S::RPW * D * CB;
   const float* scales = kind == 1 ? p.ks : p.vs;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int h = h0 + i * S::RPW;
-    float r = 1.f, y[NV][E];
+    float2 x[2][E / 2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      float f[E];
+      unpack<T, E>(raw[i][v], f);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) x[v][e / 2] = make_float2(f[e], f[e + 1]);
+    }
+    float r = 1.f;
     if (w) {   // (the same for the whole warp, as is kind)
       float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float x[E];
-        unpack<T, E>(raw[i][v], x);
+      for (int v = 0; v < 2; ++v)
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 x2 = make_float2(x[e], x[e + 1]);
-          sum2 = __ffma2_rn(x2, x2, sum2);
-        }
-      }
+        for (int e = 0; e < E / 2; ++e) sum2 = __ffma2_rn(x[v][e], x[v][e], sum2);
       float sum = sum2.x + sum2.y;
 #pragma unroll
       for (int o = LR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       r = rsqrtf(fmaf(sum, 1.f / D, p.eps));
     }
+    if (h < H) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      uint4 mate = raw[i][v];
-      if constexpr (!NEAR) {
-        if (turned) {
-          // the partners' values as they came: one shuffle a 32-bit word
-          const uint4 a = raw[i][0];
-          mate.x = __shfl_sync(0xffffffffu, a.x, from[v]);
-          mate.y = __shfl_sync(0xffffffffu, a.y, from[v]);
-          mate.z = __shfl_sync(0xffffffffu, a.z, from[v]);
-          mate.w = __shfl_sync(0xffffffffu, a.w, from[v]);
-          if constexpr (NV > 1) {
-            const uint4 b = raw[i][NV - 1];
-            uint4 m1;
-            m1.x = __shfl_sync(0xffffffffu, b.x, from[v]);
-            m1.y = __shfl_sync(0xffffffffu, b.y, from[v]);
-            m1.z = __shfl_sync(0xffffffffu, b.z, from[v]);
-            m1.w = __shfl_sync(0xffffffffu, b.w, from[v]);
-            if ((v == 1) != other[v]) mate = m1;
-          }
+      for (int v = 0; v < 2; ++v) {
+        const int at = v ? at1 : at0;
+        if (!turned && !CODES) {
+          *reinterpret_cast<uint4*>((T*)dst + at) = raw[i][v];
+          continue;
         }
-      }
-      if (turned || CODES) {
-        float x[E], z[E];
-        unpack<T, E>(raw[i][v], x);
-        if constexpr (!NEAR) unpack<T, E>(mate, z);
-        const float2 r2 = make_float2(r, r);
+        float y[E];
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          float2 u = __fmul2_rn(make_float2(x[e], x[e + 1]), A[v][e / 2]);
-          if (rotated[v])
-            u = __ffma2_rn(NEAR ? make_float2(x[e + 1], x[e]) : make_float2(z[e], z[e + 1]), B[v][e / 2], u);
-          u = __fmul2_rn(u, r2);
-          y[v][e] = u.x;
-          y[v][e + 1] = u.y;
+        for (int e = 0; e < E / 2; ++e) {
+          float2 o = __fmul2_rn(x[v][e], A[v][e]);
+          if (rotated[v]) o = __ffma2_rn(NEAR ? make_float2(x[v][e].y, x[v][e].x) : x[1 - v][e], B[v][e], o);
+          o = __fmul2_rn(o, make_float2(r, r));
+          y[2 * e] = o.x;
+          y[2 * e + 1] = o.y;
         }
-      }
-    }
-    if (h >= H) continue;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int at = v * LR * E;
-      if (CODES && kind != 0) {
-        store_codes<E>(y[v], __ldg(scales + h), (uint8_t*)dst + at);
-      } else {
-        uint4 o = raw[i][v];
-        if (turned) {
+        if (CODES && kind != 0) {
+          store_codes<E>(y, __ldg(scales + h), (uint8_t*)dst + at);
+        } else {
+          uint4 o;
           T* d = reinterpret_cast<T*>(&o);
 #pragma unroll
-          for (int e = 0; e < E; ++e) d[e] = from_f32<T>(y[v][e]);
+          for (int e = 0; e < E; ++e) d[e] = from_f32<T>(y[e]);
+          *reinterpret_cast<uint4*>((T*)dst + at) = o;
         }
-        *reinterpret_cast<uint4*>((T*)dst + at) = o;
       }
     }
     dst += dst_step;
