@@ -676,7 +676,8 @@ int pkv_pool_compact(pkv_pool* pool, int32_t max_moves, int32_t* src, int32_t* d
 
 /* pkv_pool_trim — host: let go of a sequence's pages that no row at position kv_len or
  * later sees through a window with sinks; their entries in `pages` become -1. Returns how many.
- * On an error (PKV_E_NULL, PKV_E_SHAPE, PKV_E_PAGES) nothing changes. */
+ * On an error (PKV_E_NULL, PKV_E_SHAPE, PKV_E_PAGES) nothing changes; PKV_E_CAPACITY: out of host memory,
+ * the pages that are not -1 are still held. */
 int pkv_pool_trim(pkv_pool* pool, int32_t* pages, int32_t n_pages, int32_t kv_len, int32_t window, int32_t sinks);
 
 /* pkv_pack_tick_window — pkv_pack_tick for a tick whose attention has a window: page ids may

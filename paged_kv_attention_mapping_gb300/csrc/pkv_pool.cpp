@@ -23,6 +23,7 @@
 #include <new>
 #include <set>
 #include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "pagedkv.h"
@@ -270,10 +271,11 @@ extern "C" int pkv_pool_compact(pkv_pool* p, int32_t max_moves, int32_t* src, in
     while (high >= 0 && p->ref[high] == 0) --high;
     const int32_t low = *p->free_pages.begin();
     if (low >= high) break;
-    p->free_pages.erase(p->free_pages.begin());
+    auto node = p->free_pages.extract(p->free_pages.begin());   // the same node takes the other page: no allocation
+    node.value() = high;
+    p->free_pages.insert(std::move(node));
     p->ref[low] = p->ref[high];
     p->ref[high] = 0;
-    p->free_pages.insert(high);
     page_map[high] = low;
     src[n] = high;
     dst[n] = low;
@@ -295,16 +297,26 @@ extern "C" int pkv_pool_trim(pkv_pool* p, int32_t* pages, int32_t n_pages, int32
   const int64_t first = ((int64_t)sinks + P - 1) / P;
   const int64_t last = keep_from > 0 ? keep_from / P : 0;   // first page with a key of the window
   const int64_t end = last < n_pages ? last : n_pages;
-  // check first, so a bad list changes nothing (a page may appear several times)
-  std::map<int32_t, int32_t> count;
-  for (int64_t i = first; i < end; ++i) {
+  // check first, so a bad list changes nothing (a page may appear several times): references are taken
+  // off, and put back where one is missing
+  int64_t bad = -1;
+  for (int64_t i = first; i < end && bad < 0; ++i) {
     if (pages[i] < 0) continue;
-    if (pages[i] >= p->num_pages || ++count[pages[i]] > p->ref[pages[i]]) return PKV_E_PAGES;
+    if (pages[i] >= p->num_pages || p->ref[pages[i]] == 0) bad = i;
+    else p->ref[pages[i]] -= 1;
   }
+  for (int64_t i = first; i < (bad < 0 ? end : bad); ++i)
+    if (pages[i] >= 0) p->ref[pages[i]] += 1;
+  if (bad >= 0) return PKV_E_PAGES;
   int32_t n = 0;
   for (int64_t i = first; i < end; ++i) {
     if (pages[i] < 0) continue;
-    p->drop(pages[i]);
+    try {
+      p->drop(pages[i]);
+    } catch (...) {   // (no memory for the free list's node)
+      p->ref[pages[i]] += 1;
+      return PKV_E_CAPACITY;
+    }
     pages[i] = -1;
     ++n;
   }

@@ -15,14 +15,26 @@
 //               before the first window and after the last row): 0 * NaN must not reach O.
 //               Over an e4m3 cache warps 10 and 11 instead widen every key and value tile to
 //               f16 in its slot, with those rows as zeros.
-// Steps are 128 keys each: from key 0 on while there are sinks, then from the first window's first key
-// (rounded down to 32) to the last row's. Each step has a range of 32-key pieces that a query tile sees at all; loads,
-// products and the softmax take that range only (a window's ends are a quarter of a tile
-// wide on average, not half of one and a half), and a query tile without one skips the step.
+// Steps are 128 keys each: from key 0 on while there are sinks, then from the first window's first
+// key (rounded down to 32) to the last row's. Each step has a range of 32-key pieces that a query tile
+// sees at all; loads, products and the softmax take that range only, and a query tile without
+// one skips the step.
 // The softmax keeps a running maximum and sum; O is rescaled in TMEM only when a row's
 // maximum grows by more than 2^8. A row can start with pieces that it does not see: its
 // maximum is then -inf, and its weights 0.
-// The bound is the tensor pipe in long windows and the softmax in narrow ones.
+// What bounds it: in wide windows the chain of a query tile, products - softmax - products, of which
+// two are in flight (tensor memory holds no third): a step of both takes about 3130 cycles of which the
+// tensor pipe works 2048. In narrow ones the ends of work tiles (Q arrives, the first scores, the
+// output's stores), 6 to 8 us a tile of which little overlaps. 16384 tokens, 32 / 8 heads of 128: window 2048
+// 427 us, 1206 TFLOP/s (63 % of the measured burst rate); 512 178 us; 128 105 us. Seven prompts of
+// 300 to 2500 tokens at window 512, 28 / 4 heads: 94 us.
+// Steps taken (16384 tokens at window 2048): ranges in place of whole tiles at the ends, whole steps with
+// their scores in registers and others read twice (610 -> 497 us), ranges as words for the MMA
+// warp, which is short of issue slots (465), weights handed over in halves and 32-byte stores (456).
+// Without gain: two threads a row (526; the exponentials share a unit), an MMA warp for each query
+// tile (479), both forms of a step over registers (2261, spills), masked steps over registers (498) or two
+// pieces at a time (509), partial steps as a function (702), boxes of 128 rows, a ring of four slots,
+// looking the next tile up early.
 // Every mbarrier wait is bounded (PKV_DEV_TIMEOUT); TMEM accesses are warp-uniform.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -51,7 +63,8 @@ constexpr float F16_SHIFT = 7.f;
 
 struct TilesP {
   const int32_t *cu, *kv_lens, *tables;
-  int32_t B, T, Hq, Hkv, G, PP, P, num_pages, max_pages, window, sinks, min_q, box, wide, beside;   // beside: a row kernel follows in this call
+  int32_t B, T, Hq, Hkv, G, PP, P, num_pages, max_pages, window, sinks, min_q;
+  int32_t box, wide, beside;   // rows of a page block; out is 32-byte aligned; a row kernel follows in this call
   int64_t units;
   PageDiv div;
   float scale_log2;
@@ -397,7 +410,7 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
   if (warp == 0) {
     // --------------------------------------------------------------- producer
     // a bit a slot: parity of its loads, of those that land for a helper, and whether the last did
-    uint32_t ring = 0, loads = 0, landing = 0, last_land = 0, used = 0;
+    uint32_t ring = 0, loads = 0, landing = 0, last_land = 0, used = 0, q_loads = 0;
     bool ok = true;
     int64_t u = blockIdx.x;
     for (uint32_t t = 0; ok; ++t) {
@@ -454,6 +467,7 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
           for (int h = 0; h < C::HALVES; ++h)
             tma_load_3d(sQ + w * C::Q_BYTES + h * BM * 128, &mq, bar, h * 64, ti.kvh * p.G, ti.row0 + w * p.PP);
       }
+      ++q_loads;
       const int32_t* pt = p.tables + (int64_t)ti.b * p.max_pages;
       for (int i = 0; i < ti.steps && ok; ++i) {
         const int k0 = step_key(ti, i);
@@ -524,6 +538,7 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
     if (!ok && lane == 0) {
       // let every copy this warp issued land before the CTA may exit (a slot's loads before its last were
       // consumed; parity 1 after the first load: phase 0)
+      if (q_loads > 0) mbar_wait(QCONV ? &bar_qland : &bar_q, (q_loads - 1) & 1, 500000000ull);
       for (int s = 0; s < NS; ++s)
         if (used >> s & 1) {
           const bool land = last_land >> s & 1;
