@@ -6,17 +6,21 @@
 // columns (rows x query heads of one KV head, that is) of one sequence over the keys that
 // some of them sees. The bound is HBM: a key and a value are read once for all columns.
 //
-// A lane of a warp copies the pieces of keys and values that it will itself take into its
-// registers as operands: 16-byte asynchronous copies to its own places in shared memory, a few steps
-// ahead, so that many more bytes are in flight than registers would hold, and no warp
-// waits for another (no barrier, no copy engine; any page size does). Scores are S^T = K Q^T
-// with 16 keys as the rows of m16n8k16; the channels of a product are permuted, alike in K
-// and Q, so that a lane's 16 bytes of a key are its own operand. The output is O^T += V^T
-// P^T with 16 channels as the rows; a lane holds 16 bytes of each of four keys and pairs
-// them with byte permutes, and P^T is S^T transposed in registers. A warp takes 16 keys at a
-// time with a running maximum and sum of its own, warps are merged at the end in shared
-// memory, and the CTAs that share a piece's keys (a cluster) through distributed shared
-// memory: no workspace and one launch.
+// A warp copies 16 keys and values a step, whole rows an instruction, asynchronously into a ring of
+// its own in shared memory, three or four steps ahead: many more bytes are in flight than registers
+// would hold, no warp waits for another, and any page size does. Scores are S^T = K Q^T with 16
+// keys as the rows of m16n8k16; the channels of a product are permuted, alike in K and Q, so that 16
+// bytes of a key are a lane's own operand. The output is O^T += V^T P^T with 16 channels as the rows; a
+// lane takes 16 bytes of each of four keys and pairs them with byte permutes, and P^T is S^T transposed
+// in registers. A warp has a running maximum and sum of its own; warps are merged at the end in shared
+// memory, and the CTAs that share a piece's keys (a cluster) through distributed shared memory: no
+// workspace and one launch.
+//
+// 128 rows of up to 4096 keys, 32 / 8 heads of 128, bf16: 246 us, 6.5 TB/s, 98 % of the measured copy; 64
+// rows of 132 keys, heads of 64: 5.9 us, four dependent reads and the join. Steps taken (the first case):
+// operands straight from global memory into registers 308 us; copied asynchronously by the lane that
+// consumes them, 64 bytes of eight rows an instruction, 311; whole rows an instruction 252; keys in one
+// page without a look-up a row 244. Ring depths: two steps of 8 KB 243, but 113 us against 100 for 38 rows.
 #include <cuda_runtime.h>
 
 #include <atomic>
