@@ -65,7 +65,6 @@ struct TilesP {
   const int32_t *cu, *kv_lens, *tables;
   int32_t B, T, Hq, Hkv, G, PP, P, num_pages, max_pages, window, sinks, min_q;
   int32_t box, wide, beside;   // rows of a page block; out is 32-byte aligned; a row kernel follows in this call
-  int64_t units;
   PageDiv div;
   float scale_log2;
   const float *ks, *vs;
@@ -412,20 +411,63 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
     // a bit a slot: parity of its loads, of those that land for a helper, and whether the last did
     uint32_t ring = 0, loads = 0, landing = 0, last_land = 0, used = 0, q_loads = 0;
     bool ok = true;
+    // Work tiles are numbered without gaps, sequence by sequence: lane l counts those of `share` sequences
+    // and keeps the number behind them. (A cu_seqlens_q that breaks its rules may count more than the
+    // rows make; no more are worked on.)
+    const int per = NQ * p.PP, share = (p.B + 31) / 32;
+    const int64_t most = (int64_t)p.B + p.T / per;
+    auto count = [&](int b, int& c0, int& c1) {
+      c0 = __ldg(p.cu + b);
+      c1 = __ldg(p.cu + b + 1);
+      return c0 >= 0 && c1 > c0 && c1 <= p.T && c1 - c0 >= p.min_q ? (c1 - c0 - 1) / per + 1 : 0;
+    };
+    int64_t behind = 0;
+    for (int i = 0; i < share; ++i) {
+      int c0, c1;
+      if (lane * share + i < p.B) behind += count(lane * share + i, c0, c1);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, behind, o);
+      if (lane >= o) behind += x;
+    }
+    const int64_t units = min(__shfl_sync(0xffffffffu, behind, 31), most) * p.Hkv;
     int64_t u = blockIdx.x;
     for (uint32_t t = 0; ok; ++t) {
-      // the next unit with rows for this kernel
+      // the next work tile of this CTA
       Tile ti;
       ti.valid = 0;
       ti.bad = 0;
-      for (; u < p.units && !ti.valid; u += gridDim.x) {
-        const int64_t slot = u / p.Hkv;
-        const int b = find_seq(p.cu, p.B, slot, NQ * p.PP, lane);
-        const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), L = __ldg(p.kv_lens + b);
-        const int64_t q0 = (slot - first_piece(b, c0, NQ * p.PP)) * (NQ * p.PP);
-        const int n = c1 - c0;
-        if (c0 < 0 || c1 > p.T || q0 < 0 || q0 >= n || n < p.min_q) continue;
-        ti.kvh = (int)(u - slot * p.Hkv);
+      for (; u < units && !ti.valid; u += gridDim.x) {
+        const int64_t k = u / p.Hkv;
+        ti.kvh = (int)(u - k * p.Hkv);
+        const int l = __ffs(__ballot_sync(0xffffffffu, behind > k)) - 1;   // the lane that counted it
+        int64_t rest = k - (l > 0 ? __shfl_sync(0xffffffffu, behind, max(l - 1, 0)) : 0);
+        int b = -1, c0 = 0, c1 = 0;
+        int64_t q0 = 0;
+        for (int s0 = l * share; s0 < min((l + 1) * share, p.B); s0 += 32) {
+          const int mine = s0 + lane;
+          int m0 = 0, m1 = 0;
+          const int tiles = mine < min((l + 1) * share, p.B) ? count(mine, m0, m1) : 0;
+          int64_t to = tiles;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, to, o);
+            if (lane >= o) to += x;
+          }
+          const unsigned found = __ballot_sync(0xffffffffu, to > rest);
+          if (found) {
+            const int j = __ffs(found) - 1;
+            b = s0 + j;
+            c0 = __shfl_sync(0xffffffffu, m0, j);
+            c1 = __shfl_sync(0xffffffffu, m1, j);
+            q0 = (rest - __shfl_sync(0xffffffffu, to - tiles, j)) * per;
+            break;
+          }
+          rest -= __shfl_sync(0xffffffffu, to, 31);
+        }
+        if (b < 0) continue;
+        const int n = c1 - c0, L = __ldg(p.kv_lens + b);
         if (L < n || L > (int64_t)p.max_pages * p.P) {
           if (q0 == 0 && ti.kvh == 0 && lane == 0) atomicOr(p.dev_status, PKV_DEV_BAD_LENGTHS);
           continue;
@@ -900,7 +942,6 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t s) {
   p.box = a.P < PIECE ? a.P : PIECE;
   p.beside = a.tile_min_q > 1;
   p.wide = ((uintptr_t)a.out & 31) == 0;
-  p.units = ((int64_t)a.B + a.T / (NQ * p.PP)) * a.Hkv;
   p.div = page_div(a.P);
   p.scale_log2 = a.scale * LOG2E;
   p.ks = a.k_scale;
@@ -918,7 +959,7 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t s) {
       !make_map_boxed(&mk, a.k_cache, kdt, kelt, D, a.Hkv, rows, 128 / kelt, p.box) ||
       !make_map_boxed(&mv, a.v_cache, kdt, kelt, D, a.Hkv, rows, 128 / kelt, p.box))
     return cudaErrorInvalidValue;
-  const int64_t grid = p.units < a.dev.num_sms ? p.units : a.dev.num_sms;
+  const int64_t most = ((int64_t)a.B + a.T / (NQ * p.PP)) * a.Hkv, grid = most < a.dev.num_sms ? most : a.dev.num_sms;
   KernelTimer timer("window_tiles", s);
   return launch_after_trigger(window_tiles_kernel<D, TQ, KV8>, dim3((unsigned)grid),
                               dim3((HELPER + (KV8 ? 2 : 1)) * 32), C::SMEM, s, mq, mk, mv, p);
