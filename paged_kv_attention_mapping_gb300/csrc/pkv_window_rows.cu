@@ -85,8 +85,9 @@ __device__ __forceinline__ bool find_piece(const RowsP& p, Piece* w) {
   const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), L = __ldg(p.kv_lens + b);
   const int64_t first = p.per_seq ? (int64_t)b * p.per_seq : first_piece(b, c0, p.per);
   const int64_t q0 = (slot - first) * p.per;
+  if (c0 < 0 || c1 < c0 || c1 > p.T) return false;   // (before the difference, which could wrap to a small count)
   const int n = c1 - c0;
-  if (c0 < 0 || c1 > p.T || q0 < 0 || q0 >= n || n >= p.tile_min_q) return false;
+  if (q0 < 0 || q0 >= n || n >= p.tile_min_q) return false;
   if (L < n || L > (int64_t)p.max_pages * p.P) {
     if (q0 == 0 && w->kvh == 0 && w->part == 0 && w->split == 0 && threadIdx.x == 0)
       atomicOr(p.dev_status, PKV_DEV_BAD_LENGTHS);
