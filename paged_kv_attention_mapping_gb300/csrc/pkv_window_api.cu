@@ -20,8 +20,23 @@ bool stride_ok(int64_t s, int elt) { return s >= 0 && (s * elt) % 16 == 0 && s <
 
 constexpr int32_t MAX_HEADS = 4096;
 
-// Sequences with this many new rows or more run on the tile kernel where the shape has one.
-constexpr int32_t TILE_MIN_Q = 9;
+// Sequences with this many new rows or more run on the tile kernel, which takes all their rows in one
+// pass over the keys but does not split them; the row kernel splits keys over CTAs and reads them
+// again for every 16 columns (rows x heads of a KV head). So the rule counts columns. Row / tile kernel,
+// 8 KV heads of 128 in bf16, B sequences, windows of 512 and 4096 (columns alone matter: 1 to 16
+// heads of a KV head give the same figures):
+//   16 columns  B = 10 15 / 16 us and 47 / 57 (row)   B = 48 42 / 43 and 204 / 159 (tile at the larger)
+//   24 columns  B = 6 15 / 16 and 46 / 56 (row)       B = 10 20 / 16 and 104 / 58 (tile)
+//   40 columns  B = 6 20 / 16 and 103 / 57 (tile)     B = 48 74 / 43 and 396 / 160 (tile)
+// Tiles for fewer than half the SMs leave the larger part idle: 16 columns more. Keys of 64 channels
+// cost a row pass half as much and a tile about as much (24 columns, B = 48: 31 / 38 and 152 / 141; 40
+// columns: 37 / 38 and 183 / 141; B = 6: 12 / 14 and 40 / 51). So do e4m3 keys, which a tile has to widen (32
+// columns, B = 48: 44 / 72 and 207 / 207; 48: 60 / 73 and 292 / 208; 64: 77 / 73 and 383 / 207).
+int32_t tile_rows(bool codes, int32_t D, int32_t group, int64_t tiles, int num_sms) {
+  const int32_t columns = codes ? 48 : (D == 128 ? 16 : 32) + (2 * tiles < num_sms ? 16 : 0);
+  return columns / group + 1;
+}
+
 // Calls with this many rows a sequence on average run on the tile kernel alone: a short sequence
 // among them costs it a work tile for each KV head, a quarter more work at the most, where a row kernel
 // that may find nothing to do costs each call a launch (7 prompts at window 512: 118 us with, 102 without).
@@ -159,8 +174,9 @@ extern "C" int pkv_window_attention(const void* q, int32_t q_dtype, const int32_
   a.tile_min_q = INT32_MAX;
   // a call of no more rows than sequences is one of single rows (were it not, the row kernel
   // takes its chunks too)
-  if (total_q > num_seqs && total_q >= TILE_MIN_Q && window_tiles_supported(cache->dtype, cache->head_dim, cache->page_size))
-    a.tile_min_q = (int64_t)num_seqs * TILES_ONLY <= total_q ? 1 : TILE_MIN_Q;
+  const int32_t many = tile_rows(codes, cache->head_dim, g, (int64_t)num_seqs * cache->num_kv_heads, dev.num_sms);
+  if (total_q > num_seqs && total_q >= many && window_tiles_supported(cache->dtype, cache->head_dim, cache->page_size))
+    a.tile_min_q = (int64_t)num_seqs * TILES_ONLY <= total_q ? 1 : many;
   cudaError_t e = cudaSuccess;
   if (a.tile_min_q != INT32_MAX) e = launch_window_tiles(a, (cudaStream_t)stream);
   if (e == cudaSuccess && a.tile_min_q > 1) e = launch_window_rows(a, (cudaStream_t)stream);
