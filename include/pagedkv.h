@@ -600,7 +600,8 @@ int pkv_rope_table_scaled(double base, int32_t rotary_dim, const pkv_rope_scalin
  * position p = kv_len - q_len + i sees the keys j <= p with j > p - window or j < sinks:
  * the `window` keys up to its own, and the first `sinks` keys.
  *
- *   q, out        device, contiguous [total_q, num_q_heads, head_dim] of q_dtype
+ *   q, out        device, contiguous [total_q, num_q_heads, head_dim] of q_dtype; out must not
+ *                 overlap q (rows of one call read q while others write out)
  *   q_dtype       the cache's dtype; PKV_BF16 or PKV_F16 over a PKV_FP8_E4M3 cache
  *   cu_seqlens_q, kv_lens, page_tables  as pkv_paged_attention; cu_seqlens_q may end
  *                 before total_q (rows behind are padding and left as they were)
@@ -651,8 +652,8 @@ int pkv_copy_pages(void* const* caches, int32_t num_caches, int32_t num_pages, i
                    int32_t num_copies, pkv_stream_t stream);
 
 /* pkv_remap_pages — rewrite page tables in place for pages that have moved: entry e >= 0
- * becomes page_map[e] (device, int32 [num_pages]; pkv_pool_compact gives it, a negative one frees the entry), negative entries
- * stay. An entry or a map value outside the pool sets PKV_DEV_BAD_PAGE and stays as it was.
+ * becomes page_map[e] (device, int32 [num_pages]; pkv_pool_compact gives it, a negative one frees
+ * the entry), negative entries stay. An entry or a map value outside the pool sets PKV_DEV_BAD_PAGE and stays as it was.
  * Errors: PKV_E_NULL, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_DEVICE, PKV_E_CUDA. */
 int pkv_remap_pages(int32_t* page_tables, int64_t num_entries, const int32_t* page_map, int32_t num_pages,
                     pkv_stream_t stream);

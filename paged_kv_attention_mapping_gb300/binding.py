@@ -223,6 +223,12 @@ def _check(status: int, where: str):
 # ---------------------------------------------------------------------------
 # host packing
 
+def _count(n):
+    """A window or a number of sinks as a 32-bit argument: contexts are shorter than 2^31, so what is
+    larger means the same; what is negative is refused by the call, not wrapped."""
+    return -1 if n < 0 else n if n < 2147483648 else 2147483647
+
+
 def pack_tick(q_lens: Sequence[int], kv_lens: Sequence[int], pages: Sequence[Sequence[int]], page_size: int,
               num_pages: int, max_pages_per_seq: Optional[int] = None, window: Optional[int] = None, sinks: int = 0):
     """Host packing of one tick (pkv_pack_tick). Returns numpy arrays:
@@ -286,7 +292,7 @@ def pack_tick_flat(q_lens, kv_lens, page_offsets, page_ids, page_size: int, num_
     if window is None:
         _check(lib().pkv_pack_tick(*given, *wanted), "pkv_pack_tick")
     else:
-        _check(lib().pkv_pack_tick_window(*given, int(window), int(sinks), *wanted), "pkv_pack_tick_window")
+        _check(lib().pkv_pack_tick_window(*given, _count(int(window)), _count(int(sinks)), *wanted), "pkv_pack_tick_window")
     T = int(total[0])
     return dict(order=order[:B], cu_seqlens_q=cu[:B + 1], kv_lens=kv_out[:B], page_tables=tables[:B],
                 slot_mapping=slots[:T])
@@ -957,7 +963,7 @@ def window_attention(q, cu_seqlens_q, kv_lens, page_tables, k_cache, v_cache, sc
 
     q [T, Hq, d]; cu_seqlens_q int32 [B + 1]; kv_lens int32 [B]; page_tables int32 [B, W];
     caches [N, P, Hkv, d] of q's dtype, or e4m3 codes (q bf16 or f16) with float32 scales
-    [Hkv]. Returns (out [T, Hq, d], lse [T, Hq])."""
+    [Hkv]. out must not overlap q. Returns (out [T, Hq, d], lse [T, Hq])."""
     torch = _torch or _load_torch()
     where = "window_attention"
     i32 = torch.int32
@@ -1001,8 +1007,8 @@ def window_attention(q, cu_seqlens_q, kv_lens, page_tables, k_cache, v_cache, sc
     on = torch._C._cuda_getCurrentRawStream(dev) if stream is None else int(stream.cuda_stream)
     st = (_lib or lib()).pkv_window_attention(
         q.data_ptr(), _code_of(dtype), cu_seqlens_q.data_ptr(), kv_lens.data_ptr(), page_tables.data_ptr(), cu[0] - 1, T,
-        Hq, tables[1], window, sinks, k_cache.data_ptr(), v_cache.data_ptr(), desc, ks, vs, scale, out.data_ptr(), lse_ptr,
-        on)
+        Hq, tables[1], _count(window), _count(sinks), k_cache.data_ptr(), v_cache.data_ptr(), desc, ks, vs, scale,
+        out.data_ptr(), lse_ptr, on)
     if st:
         _check(st, "pkv_window_attention")
     return out, lse
@@ -1219,7 +1225,7 @@ class PagePool:
         a, p = self._arr(pages if len(pages) else [0])
         a = a.copy()
         n = lib().pkv_pool_trim(self._h, a.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), len(pages), int(kv_len),
-                                int(window), int(sinks))
+                                _count(int(window)), _count(int(sinks)))
         if n < 0:
             raise PagedKVError(n, "pkv_pool_trim")
         return [int(x) for x in a[:len(pages)]]

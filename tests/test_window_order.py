@@ -216,3 +216,44 @@ def test_two_threads_call_at_once(dev):
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert not wrong and binding.device_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# windows and sinks beyond 32 bits mean what 2^31 - 1 does; negative ones are refused
+
+BEYOND = [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63]
+
+
+@pytest.mark.parametrize("n", BEYOND)
+def test_counts_beyond_32_bits_on_the_host(lib, n):
+    args = ([1, 2], [9, 40], [[3, 0, 5], list(range(10))], 4, 10)
+    for kw in (dict(window=n), dict(window=3, sinks=n)):
+        with pytest.raises(binding.PagedKVError):       # every page is seen
+            binding.pack_tick([1], [9], [[-1, 0, 5]], 4, 10, **kw)
+        for a, b in zip(binding.pack_tick(*args, **kw), binding.pack_tick(*args)):
+            assert np.array_equal(a, b)
+        pool = binding.PagePool(10, 4)
+        pages = [int(x) for x in pool.alloc(10)]
+        assert pool.trim(pages, 40, **kw) == pages and pool.free_count() == 0
+    for kw in (dict(window=-n), dict(window=-n + 5), dict(window=3, sinks=-n), dict(window=3, sinks=-n + 5)):
+        with pytest.raises(binding.PagedKVError):
+            binding.pack_tick(*args, **kw)
+        with pytest.raises(binding.PagedKVError):
+            pool.trim(pages, 40, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", BEYOND)
+@pytest.mark.parametrize("case", [SHAPES[0], SHAPES[2], SHAPES[5]], ids=lambda c: f"{c[0]}-q{max(c[8])}")
+def test_counts_beyond_32_bits(dev, case, n):
+    p = Problem(dev, *case[:6], 2 ** 31 - 1, 0, *case[8:])
+    want = p.run()
+    p.check(*want)
+    for p.W, p.S in ((n, 0), (1, n), (n, n)):
+        got = p.run()
+        p.W, p.S = 2 ** 31 - 1, 0       # (the same keys are seen)
+        p.check(*got)
+    for p.W, p.S in ((-n, 0), (-n + 5, 0), (1, -n), (1, -n + 5)):
+        with pytest.raises(binding.PagedKVError):
+            p.run()
+    assert binding.device_status() == 0
