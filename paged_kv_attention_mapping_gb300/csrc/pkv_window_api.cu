@@ -31,7 +31,7 @@ constexpr int32_t MAX_HEADS = 4096;
 // Tiles for fewer than half the SMs leave the larger part idle: 16 columns more. Keys of 64 channels
 // cost a row pass half as much and a tile about as much (24 columns, B = 48: 31 / 38 and 152 / 141; 40
 // columns: 37 / 38 and 183 / 141; B = 6: 12 / 14 and 40 / 51). So do e4m3 keys, which a tile has to widen (32
-// columns, B = 48: 44 / 72 and 207 / 207; 48: 60 / 73 and 292 / 208; 64: 77 / 73 and 383 / 207).
+// columns, B = 48: 44 / 72 and 207 / 207; 48: 60 / 73 and 290 / 208; 64: 77 / 73 and 383 / 207).
 int32_t tile_rows(bool codes, int32_t D, int32_t group, int64_t tiles, int num_sms) {
   const int32_t columns = codes ? 48 : (D == 128 ? 16 : 32) + (2 * tiles < num_sms ? 16 : 0);
   return columns / group + 1;

@@ -411,60 +411,68 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
     // a bit a slot: parity of its loads, of those that land for a helper, and whether the last did
     uint32_t ring = 0, loads = 0, landing = 0, last_land = 0, used = 0, q_loads = 0;
     bool ok = true;
-    // Work tiles are numbered without gaps, sequence by sequence: lane l counts those of `share` sequences
-    // and keeps the number behind them. (A cu_seqlens_q that breaks its rules may count more than the
-    // rows make; no more are worked on.)
+    // Work tiles are numbered without gaps, sequence by sequence, so that the CTAs' shares differ by one tile
+    // at most: with the row kernel's numbers, which need no counting, 16 sequences of 32 rows (window
+    // 4096, 32 / 8 heads of 128) took 105 us for 60, 12 of 50 rows 130 for 73, 16 of 64 (window 512; no gaps) 24.9
+    // for 25.4. Lane l counts the tiles of `share` sequences and keeps the number behind them. (A cu_seqlens_q that breaks its rules may count more than `most`,
+    // which its rows could make; counts stop there, so that 32 bits hold them, and no more are worked on.)
     const int per = NQ * p.PP, share = (p.B + 31) / 32;
-    const int64_t most = (int64_t)p.B + p.T / per;
+    const uint32_t most = (uint32_t)p.B + (uint32_t)(p.T / per);
     auto count = [&](int b, int& c0, int& c1) {
       c0 = __ldg(p.cu + b);
       c1 = __ldg(p.cu + b + 1);
-      return c0 >= 0 && c1 > c0 && c1 <= p.T && c1 - c0 >= p.min_q ? (c1 - c0 - 1) / per + 1 : 0;
+      return c0 >= 0 && c1 > c0 && c1 <= p.T && c1 - c0 >= p.min_q ? (uint32_t)((c1 - c0 - 1) / per + 1) : 0u;
     };
-    int64_t behind = 0;
+    auto running = [&](uint32_t n) {   // sum over the lanes up to this one
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) n = min(n + x, most);
+      }
+      return n;
+    };
+    uint32_t behind = 0;
     for (int i = 0; i < share; ++i) {
       int c0, c1;
-      if (lane * share + i < p.B) behind += count(lane * share + i, c0, c1);
+      if (lane * share + i < p.B) behind = min(behind + count(lane * share + i, c0, c1), most);
     }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, behind, o);
-      if (lane >= o) behind += x;
-    }
-    const int64_t units = min(__shfl_sync(0xffffffffu, behind, 31), most) * p.Hkv;
-    int64_t u = blockIdx.x;
+    behind = running(behind);
+    const uint32_t units = __shfl_sync(0xffffffffu, behind, 31) * (uint32_t)p.Hkv;
+    uint32_t u = blockIdx.x;
     for (uint32_t t = 0; ok; ++t) {
       // the next work tile of this CTA
       Tile ti;
       ti.valid = 0;
       ti.bad = 0;
       for (; u < units && !ti.valid; u += gridDim.x) {
-        const int64_t k = u / p.Hkv;
-        ti.kvh = (int)(u - k * p.Hkv);
+        const uint32_t k = u / (uint32_t)p.Hkv;
+        ti.kvh = (int)(u - k * (uint32_t)p.Hkv);
         const int l = __ffs(__ballot_sync(0xffffffffu, behind > k)) - 1;   // the lane that counted it
-        int64_t rest = k - (l > 0 ? __shfl_sync(0xffffffffu, behind, max(l - 1, 0)) : 0);
-        int b = -1, c0 = 0, c1 = 0;
-        int64_t q0 = 0;
-        for (int s0 = l * share; s0 < min((l + 1) * share, p.B); s0 += 32) {
-          const int mine = s0 + lane;
-          int m0 = 0, m1 = 0;
-          const int tiles = mine < min((l + 1) * share, p.B) ? count(mine, m0, m1) : 0;
-          int64_t to = tiles;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, to, o);
-            if (lane >= o) to += x;
+        const uint32_t before = __shfl_sync(0xffffffffu, behind, max(l - 1, 0));
+        uint32_t rest = k - (l > 0 ? before : 0u);
+        int b = -1, c0 = 0, c1 = 0, q0 = 0;
+        if (share == 1) {   // (the lane counted one sequence: this one)
+          b = l;
+          c0 = __ldg(p.cu + b);
+          c1 = __ldg(p.cu + b + 1);
+          q0 = (int)rest * per;
+        } else {
+          const int end = min((l + 1) * share, p.B);
+          for (int s0 = l * share; s0 < end; s0 += 32) {
+            int m0 = 0, m1 = 0;
+            const uint32_t tiles = s0 + lane < end ? count(s0 + lane, m0, m1) : 0u, to = running(tiles);
+            const unsigned found = __ballot_sync(0xffffffffu, to > rest);
+            if (found) {
+              const int j = __ffs(found) - 1;
+              b = s0 + j;
+              c0 = __shfl_sync(0xffffffffu, m0, j);
+              c1 = __shfl_sync(0xffffffffu, m1, j);
+              const uint32_t left = __shfl_sync(0xffffffffu, to, max(j - 1, 0));
+              q0 = (int)(rest - (j > 0 ? left : 0u)) * per;
+              break;
+            }
+            rest -= __shfl_sync(0xffffffffu, to, 31);
           }
-          const unsigned found = __ballot_sync(0xffffffffu, to > rest);
-          if (found) {
-            const int j = __ffs(found) - 1;
-            b = s0 + j;
-            c0 = __shfl_sync(0xffffffffu, m0, j);
-            c1 = __shfl_sync(0xffffffffu, m1, j);
-            q0 = (rest - __shfl_sync(0xffffffffu, to - tiles, j)) * per;
-            break;
-          }
-          rest -= __shfl_sync(0xffffffffu, to, 31);
         }
         if (b < 0) continue;
         const int n = c1 - c0, L = __ldg(p.kv_lens + b);
@@ -473,9 +481,9 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
           continue;
         }
         ti.b = b;
-        ti.row0 = c0 + (int)q0;
-        ti.np = min(NQ * p.PP, n - (int)q0);
-        ti.p_first = L - n + (int)q0;
+        ti.row0 = c0 + q0;
+        ti.np = min(per, n - q0);
+        ti.p_first = L - n + q0;
         const int p_last = ti.p_first + ti.np - 1;
         ti.lo = max(0, ti.p_first - p.window + 1);
         ti.sinks = min(p.sinks, ti.lo);
@@ -959,7 +967,9 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t s) {
       !make_map_boxed(&mk, a.k_cache, kdt, kelt, D, a.Hkv, rows, 128 / kelt, p.box) ||
       !make_map_boxed(&mv, a.v_cache, kdt, kelt, D, a.Hkv, rows, 128 / kelt, p.box))
     return cudaErrorInvalidValue;
-  const int64_t most = ((int64_t)a.B + a.T / (NQ * p.PP)) * a.Hkv, grid = most < a.dev.num_sms ? most : a.dev.num_sms;
+  const int64_t most = ((int64_t)a.B + a.T / (NQ * p.PP)) * a.Hkv;   // work tiles
+  if (most > INT32_MAX - 65535) return cudaErrorInvalidValue;         // (their numbers are 32 bits)
+  const int64_t grid = most < a.dev.num_sms ? most : a.dev.num_sms;
   KernelTimer timer("window_tiles", s);
   return launch_after_trigger(window_tiles_kernel<D, TQ, KV8>, dim3((unsigned)grid),
                               dim3((HELPER + (KV8 ? 2 : 1)) * 32), C::SMEM, s, mq, mk, mv, p);
