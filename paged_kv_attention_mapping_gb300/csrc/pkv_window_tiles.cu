@@ -373,7 +373,9 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
   if (blockIdx.x == 0) check_cu(p.cu, p.B, p.T, p.dev_status);
   if (tid == 0) {
     mbar_init(&bar_q, QCONV ? 2 : 1);
-    mbar_init(&bar_qempty, 1);
+    // free for the next Q: its products are done and, with QCONV, every softmax warp has seen this one's phase of
+    // bar_q (only then may the next phase complete: a warp that came late would wait for one that is over)
+    mbar_init(&bar_qempty, QCONV ? 1 + SOFTMAX_WARPS : 1);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&bar_full[s], KV8 ? 2 : 1);
       mbar_init(&bar_empty[s], 1);
@@ -796,6 +798,7 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
       // (each tile's: a phase that is not waited for would be mistaken for the next)
       if constexpr (QCONV) {
         if (!wait(&bar_q, t & 1)) break;
+        if (lane == 0) mbar_arrive(&bar_qempty);
       }
       const int npw = min(tile->np - w * p.PP, p.PP);   // positions of this query tile
       if (npw > 0) {
