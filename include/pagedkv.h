@@ -625,8 +625,8 @@ int pkv_rope_table_scaled(double base, int32_t rotary_dim, const pkv_rope_scalin
  * A sequence with rows whose kv_len is below q_len or above max_pages_per_seq * page_size
  * sets PKV_DEV_BAD_LENGTHS and is skipped; a cu_seqlens_q that does not start at 0, decreases or
  * ends beyond total_q sets PKV_DEV_BAD_LENGTHS (the call's rows are then unspecified). A needed
- * page outside the pool sets PKV_DEV_BAD_PAGE and the rows that need it, or share a tile of rows with
- * one that does, are left as they were.
+ * page outside the pool sets PKV_DEV_BAD_PAGE and the rows that need it are left as they were; so may be rows of the
+ * same sequence less than 256 * num_kv_heads / num_q_heads positions from one (the same rows in every run).
  * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_DEVICE, PKV_E_CUDA. */
 int pkv_window_attention(const void* q, int32_t q_dtype, const int32_t* cu_seqlens_q, const int32_t* kv_lens,
                          const int32_t* page_tables, int32_t num_seqs, int32_t total_q, int32_t num_q_heads,

@@ -77,7 +77,7 @@ struct Tile {
   int valid, b, kvh, row0, np, p_first;
   int lo, sinks;          // keys of the work tile: [0, sinks) and [lo, p_first + np)
   int js, ws, steps;      // steps 0 .. js - 1 begin at key 128 step, later ones at ws + 128 (step - js)
-  int bad;                // a page outside the pool
+  int bad;                // a bit a query tile: one of its pages is outside the pool
 };
 
 // Rows [0, a) and [b, e) of a key tile are seen, in the pieces [c0, c1); c0 == c1: none is.
@@ -538,9 +538,18 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
           bad = id < 0 || id >= p.num_pages;
           at = id * p.P + (k0 + row - pg * p.P);
         }
-        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&s_tile[e].bad, 1);
         const bool load = in && !bad;
         const uint32_t word = step_word(ti, nq, p.PP, p.window, p.sinks, k0);
+        if (__any_sync(0xffffffffu, bad)) {
+          // the query tiles with a block of the bad page among this step's operands (nothing is loaded there). A tile
+          // reads its own bit after its last product, so all of its steps have been looked at by then, and the
+          // same rows are left out in every run
+          for (int w = 0; w < NQ; ++w) {
+            const int c0 = word >> (8 * w) & 7, c1 = c0 + (word >> (8 * w + 3) & 7);
+            if (__any_sync(0xffffffffu, bad && row < c1 * PIECE && row + p.box > c0 * PIECE) && lane == 0)
+              atomicOr(&s_tile[e].bad, 1 << w);
+          }
+        }
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)(p.box * 128);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -881,7 +890,7 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
         ++my_o;
         tc_fence_after();
         if (ok) {
-          const int bad = *(volatile const int*)&s_tile[e].bad;
+          const int bad = *(volatile const int*)&s_tile[e].bad >> w & 1;
           const bool store = pi < npw && !bad;
           const float inv = (KV8 ? __ldg(p.vs + tile->kvh) : 1.f) / l_run;
           const int64_t at = (int64_t)(tile->row0 + w * p.PP + pi) * p.Hq + tile->kvh * p.G + (i - pi * p.G);

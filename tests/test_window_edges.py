@@ -27,3 +27,50 @@ def test_many_short_work_tiles(dev, t, cache):
         again = p.run()
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
     assert binding.device_status() == 0
+
+
+# A page outside the pool. Which rows need it goes by the window alone; rows fewer than 256 / group positions
+# from one of those may be left out with it, all others are as if the page were good.
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,cache,G,P,W", [("bf16", "bf16", 4, 32, 20), ("f16", "f16", 4, 8, 20), ("bf16", "bf16", 1, 64, 50),
+                                           ("bf16", "e4m3", 4, 32, 20), ("f16", "e4m3", 7, 16, 90),
+                                           ("bf16", "bf16", 16, 32, 9)])
+def test_a_bad_page_leaves_out_the_same_rows_every_time(dev, t, cache, G, P, W):
+    n, D = 700, 128
+    p = Problem(dev, t, cache, 2 * G, 2, D, P, W, 0, [n], [n])
+    good, glse = p.run()
+    p.check(good, glse)
+    pos = np.arange(n)
+    for page in (1, 3, n // P // 2, n // P):
+        tables = p.tables.copy()
+        tables[0, page] = p.N + 3
+        needs = (pos >= page * P) & (pos - W < (page + 1) * P - 1)
+        far = (np.abs(pos[:, None] - pos[needs]) >= 256 // G).all(1)
+        left = None
+        for _ in range(20):
+            out, lse = torch.full_like(p.q, 7.0), torch.full(p.q.shape[:2], 7.0, device=dev)
+            binding.window_attention(p.q, _i32([0, n], dev), _i32([n], dev), _i32(tables, dev), p.kc, p.vc, p.scale, W,
+                                     k_scale=p.ks, v_scale=p.vs, out=out, lse=lse)
+            assert binding.device_status() == binding.DEV_BAD_PAGE
+            skipped = (out == 7).flatten(1).all(1).cpu().numpy()
+            assert skipped[needs].all() and not skipped[far].any()
+            # a row is left out whole or is what it would be
+            kept = torch.from_numpy(~skipped).to(dev)
+            assert (lse[~kept] == 7).all() and torch.equal(out[kept], good[kept]) and torch.equal(lse[kept], glse[kept])
+            assert left is None or np.array_equal(left, skipped)
+            left = skipped
+
+
+# The page is that of the second query tile alone: the first (positions 0 .. 31) sees page 0 only.
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,cache,n", [("bf16", "bf16", 64), ("f16", "e4m3", 64), ("bf16", "e4m3", 47), ("f16", "f16", 200)])
+def test_a_bad_page_of_the_second_query_tile(dev, t, cache, n):
+    p = Problem(dev, t, cache, 8, 2, 128, 32, 1000, 0, [n], [n])
+    good, _ = p.run()
+    tables = p.tables.copy()
+    tables[0, 1] = -1
+    out, lse = torch.full_like(p.q, 7.0), torch.full(p.q.shape[:2], 7.0, device=dev)
+    binding.window_attention(p.q, _i32([0, n], dev), _i32([n], dev), _i32(tables, dev), p.kc, p.vc, p.scale, p.W,
+                             k_scale=p.ks, v_scale=p.vs, out=out, lse=lse)
+    assert binding.device_status() == binding.DEV_BAD_PAGE
+    assert torch.equal(out[:32], good[:32]) and (out[32:] == 7).all() and (lse[32:] == 7).all()
