@@ -37,10 +37,20 @@ int32_t tile_rows(bool codes, int32_t D, int32_t group, int64_t tiles, int num_s
   return columns / group + 1;
 }
 
-// Calls with this many rows a sequence on average run on the tile kernel alone: a short sequence
-// among them costs it a work tile for each KV head, a quarter more work at the most, where a row kernel
-// that may find nothing to do costs each call a launch (7 prompts at window 512: 118 us with, 102 without).
-constexpr int32_t TILES_ONLY = 256;
+// Whether the row kernel may be left out of a call with chunks, so that its short sequences become work tiles too. A
+// row kernel that finds nothing to do costs a call 1 to 5 us (7 prompts, 28 / 4 heads of 128, window 512: 95.6 us
+// without / 100.8 with; 16 prompts of 600, 32 / 8 heads: 77 / 81; one of 512 rows: 14.5 / 16.1). A short sequence costs the
+// tile kernel a work tile for each KV head, whose keys one CTA walks. So both have to be few, work tiles that short
+// sequences may add and steps that one takes (without / with the row kernel, in us):
+//   1 row of 8000 keys beside a prompt of 600      W = 512 16.8 / 17.8   1024 19.5 / 17.5   4096 52 / 18
+//   3 rows beside one of 4000                      W = 512 56 / 60       1024 82 / 78       4096 159 / 136
+//   12 rows beside one of 8192                     W = 512 110 / 109     1024 156 / 152     4096 386 / 362
+//   8 rows beside one of 8192, 8 heads of 8        W = 128 32.4 / 31.9   512 47 / 43        4096 162 / 143
+// A call of one sequence has nothing beside it.
+constexpr int64_t FEW_KEYS = 768, TILES_A_SEQUENCE = 8;
+bool tiles_only(int32_t num_seqs, int32_t total_q, int32_t group, int64_t keys) {
+  return num_seqs == 1 || (keys <= FEW_KEYS && total_q / (2 * (128 / group)) >= TILES_A_SEQUENCE * num_seqs);
+}
 
 // head_dim and dtypes that the calls of this file share
 int check(const pkv_cache_desc* c, int32_t src_dtype, const float* k_scale, const float* v_scale) {
@@ -175,8 +185,11 @@ extern "C" int pkv_window_attention(const void* q, int32_t q_dtype, const int32_
   // a call of no more rows than sequences is one of single rows (were it not, the row kernel
   // takes its chunks too)
   const int32_t many = tile_rows(codes, cache->head_dim, g, (int64_t)num_seqs * cache->num_kv_heads, dev.num_sms);
+  // the most that a row sees
+  const int64_t context = (int64_t)max_pages_per_seq * cache->page_size, seen = (int64_t)window + sinks;
+  const int64_t keys = seen < context ? seen : context;
   if (total_q > num_seqs && total_q >= many && window_tiles_supported(cache->dtype, cache->head_dim, cache->page_size))
-    a.tile_min_q = (int64_t)num_seqs * TILES_ONLY <= total_q ? 1 : many;
+    a.tile_min_q = tiles_only(num_seqs, total_q, g, keys) ? 1 : many;
   cudaError_t e = cudaSuccess;
   if (a.tile_min_q != INT32_MAX) e = launch_window_tiles(a, (cudaStream_t)stream);
   if (e == cudaSuccess && a.tile_min_q > 1) e = launch_window_rows(a, (cudaStream_t)stream);

@@ -74,3 +74,34 @@ def test_a_bad_page_of_the_second_query_tile(dev, t, cache, n):
                              k_scale=p.ks, v_scale=p.vs, out=out, lse=lse)
     assert binding.device_status() == binding.DEV_BAD_PAGE
     assert torch.equal(out[:32], good[:32]) and (out[32:] == 7).all() and (lse[32:] == 7).all()
+
+
+def _kernels(p):
+    """The kernels that a call runs, after checking its results."""
+    binding.set_kernel_timing(True)
+    try:
+        binding.kernel_times()
+        out, lse = p.run()
+        torch.cuda.synchronize()
+        names = set(binding.kernel_times())
+    finally:
+        binding.set_kernel_timing(False)
+    assert binding.device_status() == 0
+    p.check(out, lse, sorted({0, len(p.q_lens) // 2, len(p.q_lens) - 1}))
+    return names
+
+
+# Short sequences become work tiles only where those are few and their windows short.
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,W,q_lens,kv_lens,rows", [
+    (4, 8000, [1, 600], [9000, 600], True),            # a long window in one CTA a head
+    (4, 8000, [1, 511], [3000, 511], True),
+    (2, 700, [1, 700], [2000, 700], True),             # 5 work tiles, one of them the short sequence's
+    (1, 100, [1] * 32 + [8416], [150] * 32 + [8416], True),   # as many tiles again
+    (4, 100, [1, 1100], [150, 1100], False),           # one tile a head beside 17
+    (4, 8000, [600], [600], False),                    # nothing beside it
+    (7, 300, [400, 700], [400, 900], False),
+    (7, 3000, [400, 700], [3500, 900], True)])
+def test_when_short_sequences_are_left_to_the_tiles(dev, G, W, q_lens, kv_lens, rows):
+    p = Problem(dev, "bf16", "bf16", G, 1, 128, 64, W, 0, q_lens, kv_lens)
+    assert _kernels(p) == ({"window_tiles", "window_rows"} if rows else {"window_tiles"})
