@@ -605,6 +605,8 @@ int pkv_rope_table_scaled(double base, int32_t rotary_dim, const pkv_rope_scalin
  *   q_dtype       the cache's dtype; PKV_BF16 or PKV_F16 over a PKV_FP8_E4M3 cache
  *   cu_seqlens_q, kv_lens, page_tables  as pkv_paged_attention; cu_seqlens_q may end
  *                 before total_q (rows behind are padding and left as they were)
+ *                 A call of no more rows than sequences is taken as one of single rows: chunks beside
+ *                 idle sequences are right in it, but faster with a total_q above num_seqs (padding will do)
  *   window, sinks >= 1 and >= 0; any size (a window of kv_len or more is plain causal
  *                 attention)
  *   scale         > 0 and finite

@@ -45,6 +45,7 @@ struct RowsP {
   const void *q, *kc, *vc;
   const int32_t *cu, *kv_lens, *tables;
   int32_t B, T, Hq, Hkv, G, per, P, num_pages, max_pages, window, sinks, tile_min_q, parts, heads;
+  int32_t numbered;  // rows for each number of first_piece: per, or 1
   int32_t per_seq;   // pieces numbered for each sequence (0: as first_piece has it)
   int32_t beside;    // launched beside the tile kernel, which is the one before it
   PageDiv div;
@@ -81,9 +82,9 @@ __device__ __forceinline__ bool find_piece(const RowsP& p, Piece* w) {
   u /= p.parts;
   w->kvh = (int)(u % p.Hkv);
   const int64_t slot = u / p.Hkv;
-  const int b = p.per_seq ? (int)(slot / p.per_seq) : find_seq(p.cu, p.B, slot, p.per, lane);
+  const int b = p.per_seq ? (int)(slot / p.per_seq) : find_seq(p.cu, p.B, slot, p.numbered, lane);
   const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), L = __ldg(p.kv_lens + b);
-  const int64_t first = p.per_seq ? (int64_t)b * p.per_seq : first_piece(b, c0, p.per);
+  const int64_t first = p.per_seq ? (int64_t)b * p.per_seq : first_piece(b, c0, p.numbered);
   const int64_t q0 = (slot - first) * p.per;
   if (c0 < 0 || c1 < c0 || c1 > p.T) return false;   // (before the difference, which could wrap to a small count)
   const int n = c1 - c0;
@@ -801,15 +802,20 @@ cudaError_t launch_window_rows(const WindowArgs& a, cudaStream_t s) {
   p.heads = f32 ? (a.D == 256 ? 2 : 4) : p.G < 8 * nt ? p.G : 8 * nt;
   p.parts = (p.G + p.heads - 1) / p.heads;
   p.per = f32 ? 1 : 8 * nt / p.heads;
+  p.numbered = p.per;
   p.per_seq = 0;
   int64_t slots;
   if (a.tile_min_q != INT32_MAX) {   // every sequence of this kernel has fewer rows than that
     p.per_seq = (a.tile_min_q - 1 + p.per - 1) / p.per;
     slots = (int64_t)a.B * p.per_seq;
   } else {
-    // a call of no more rows than sequences is one of single rows: a number for each row
-    if (a.T <= a.B) p.per = 1;
-    slots = p.per == 1 ? a.T : (int64_t)a.B + a.T / p.per;
+    // a call of no more rows than sequences is one of single rows: a number for each row. Where it has a chunk
+    // and idle sequences all the same, the chunk's first numbers take `per` rows each and the others none. 400 rows at
+    // window 1024 in a call of 512 places, 8 KV heads of 128 with 1 / 2 / 4 heads: 39 / 61 / 110 us, 193 with a row a
+    // number. (Pieces of 16 columns there, for 5 to 8 heads: 107 to 159 us in place of 194, but 128 decode rows of
+    // 4096 keys 249 -> 250.5, 64 over e4m3 98 -> 131.)
+    if (a.T <= a.B) p.numbered = 1;
+    slots = p.numbered == 1 ? a.T : (int64_t)a.B + a.T / p.per;
   }
   const int64_t pieces = slots * a.Hkv * p.parts;
   // pieces that have rows: all, or (with the tile kernel) as many as the rows of even sequences make

@@ -105,3 +105,49 @@ def _kernels(p):
 def test_when_short_sequences_are_left_to_the_tiles(dev, G, W, q_lens, kv_lens, rows):
     p = Problem(dev, "bf16", "bf16", G, 1, 128, 64, W, 0, q_lens, kv_lens)
     assert _kernels(p) == ({"window_tiles", "window_rows"} if rows else {"window_tiles"})
+
+
+# Calls with no more rows than places for sequences, most of them idle: chunks in them share their keys too.
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,cache,Hq,Hkv,D,P,W,S", [
+    ("bf16", "bf16", 8, 2, 128, 64, 90, 3), ("f16", "f16", 3, 3, 64, 16, 40, 0), ("bf16", "bf16", 10, 2, 128, 16, 50, 1),
+    ("bf16", "bf16", 8, 1, 64, 8, 30, 0), ("f16", "f16", 16, 1, 128, 32, 20, 0), ("bf16", "bf16", 4, 4, 256, 24, 60, 9),
+    ("bf16", "e4m3", 6, 2, 128, 16, 70, 2), ("f32", "f32", 4, 2, 64, 16, 30, 2)])
+@pytest.mark.parametrize("q", [[0, 33, 0, 1, 7], [1, 1, 0, 16, 2, 0, 90], [130]])
+def test_chunks_in_padded_calls(dev, t, cache, Hq, Hkv, D, P, W, S, q):
+    rows = sum(q)
+    q = q + [0] * (rows - len(q) + 2)
+    kv = [x + (0, 5, 200)[i % 3] for i, x in enumerate(q)]
+    p = Problem(dev, t, cache, Hq, Hkv, D, P, W, S, q, kv, pad=2)
+    out, lse = torch.full_like(p.q, 7.0), torch.full(p.q.shape[:2], 7.0, device=dev)
+    p.run(out=out, lse=lse)
+    assert binding.device_status() == 0 and p.q.shape[0] <= len(q)
+    p.check(out, lse)
+    assert (out[rows:] == 7).all() and (lse[rows:] == 7).all()
+
+
+@pytest.mark.gpu
+def test_a_chunk_in_a_padded_call_reads_its_keys_once_for_several_rows(dev):
+    n, L = 400, 2400
+    p = Problem(dev, "bf16", "bf16", 4, 4, 128, 64, 2000, 0, [n] + [0] * n, [L] + [1] * n)
+    tables = np.full((n, p.tables.shape[1]), -1, np.int32)
+    tables[:] = p.tables[0]
+    kv = np.arange(L - n + 1, L + 1)
+    calls = [([0, n] + [n] * n, p.kv_lens, p.tables), (list(range(n + 1)), kv, tables)]   # one chunk; single rows of the same keys
+    times, outs = [], []
+    for cu, kv, tab in calls:
+        args = (p.q, _i32(cu, dev), _i32(kv, dev), _i32(tab, dev), p.kc, p.vc, p.scale, p.W)
+        outs.append(binding.window_attention(*args)[0])
+        best = []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(5):
+                binding.window_attention(*args)
+            b.record()
+            torch.cuda.synchronize()
+            best.append(a.elapsed_time(b))
+        times.append(min(best))
+    assert binding.device_status() == 0
+    # 8 rows of a piece share each key: an eighth of the reads and products, and less than two thirds of the time
+    assert times[0] < 0.67 * times[1], times
