@@ -669,6 +669,12 @@ int pkv_remap_pages(int32_t* page_tables, int64_t num_entries, const int32_t* pa
 int pkv_pool_fork(pkv_pool* pool, const int32_t* pages, int32_t n_pages, int32_t kv_len, int32_t* child,
                   int32_t* src, int32_t* dst, int32_t* tokens);
 
+/* pkv_pool_fork_window — pkv_pool_fork for a sequence whose pages behind a window have been let go: PKV_E_PAGES also
+ * where a page is -1 that a row at position kv_len or later sees (as when the fork is at fewer tokens than the parent
+ * had when it was trimmed; pkv_pool_fork hands such a page on). window >= 1, sinks >= 0. */
+int pkv_pool_fork_window(pkv_pool* pool, const int32_t* pages, int32_t n_pages, int32_t kv_len, int32_t window,
+                         int32_t sinks, int32_t* child, int32_t* src, int32_t* dst, int32_t* tokens);
+
 /* pkv_pool_compact — host: move held pages with the highest ids to the lowest free ids, at
  * most max_moves of them, so that the held pages come to be the lowest. Returns the number of
  * moves, writes them to src and dst (no page is in both; room for max_moves) and page_map[num_pages],

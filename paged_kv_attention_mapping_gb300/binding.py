@@ -64,6 +64,7 @@ EXPORTED = (
     "pkv_copy_pages",
     "pkv_remap_pages",
     "pkv_pool_fork",
+    "pkv_pool_fork_window",
     "pkv_pool_compact",
     "pkv_pool_trim",
     "pkv_pack_tick_window",
@@ -195,6 +196,8 @@ def lib():
     L.pkv_remap_pages.restype = ctypes.c_int
     L.pkv_pool_fork.argtypes = [vp, P32, i32, i32, P32, P32, P32, P32]
     L.pkv_pool_fork.restype = ctypes.c_int
+    L.pkv_pool_fork_window.argtypes = [vp, P32, i32, i32, i32, i32, P32, P32, P32, P32]
+    L.pkv_pool_fork_window.restype = ctypes.c_int
     L.pkv_pool_compact.argtypes = [vp, i32, P32, P32, P32]
     L.pkv_pool_compact.restype = ctypes.c_int
     L.pkv_pool_trim.argtypes = [vp, P32, i32, i32, i32, i32]
@@ -1193,18 +1196,23 @@ class PagePool:
 
     # A call of these changes nothing when it raises.
 
-    def fork(self, pages, kv_len: int):
+    def fork(self, pages, kv_len: int, window: Optional[int] = None, sinks: int = 0):
         """Pages of a sequence forked after kv_len tokens (pkv_pool_fork): (the child's
-        pages, None or the (src, dst, tokens) that copy_pages has to copy)."""
+        pages, None or the (src, dst, tokens) that copy_pages has to copy). With a `window`
+        (pkv_pool_fork_window) a -1 page that the child's next rows see is refused."""
         a, p = self._arr(pages if len(pages) else [0])
         used = -(-int(kv_len) // self.page_size)
         child, cp = self._arr(np.zeros(max(used, len(pages), 1)))
         what = np.zeros(3, dtype=np.int32)
         P32 = ctypes.POINTER(ctypes.c_int32)
         at = [what[i:].ctypes.data_as(P32) for i in range(3)]
-        n = lib().pkv_pool_fork(self._h, p, len(pages), int(kv_len), cp, *at)
+        if window is None:
+            n = lib().pkv_pool_fork(self._h, p, len(pages), int(kv_len), cp, *at)
+        else:
+            n = lib().pkv_pool_fork_window(self._h, p, len(pages), int(kv_len), _count(int(window)), _count(int(sinks)), cp,
+                                           *at)
         if n < 0:
-            raise PagedKVError(n, "pkv_pool_fork")
+            raise PagedKVError(n, "pkv_pool_fork" if window is None else "pkv_pool_fork_window")
         return [int(x) for x in child[:used]], (tuple(int(x) for x in what) if n else None)
 
     def compact(self, max_moves: int = 1 << 30):

@@ -232,15 +232,20 @@ extern "C" int pkv_prefix_size(const pkv_pool* p) { return p ? (int)p->cache.siz
 
 // A forked sequence holds the pages that its parent has filled (a full page is never
 // written again), and a page of its own for the partly filled last one.
-extern "C" int pkv_pool_fork(pkv_pool* p, const int32_t* pages, int32_t n_pages, int32_t kv_len, int32_t* child,
-                             int32_t* src, int32_t* dst, int32_t* tokens) {
+// A page that was let go (< 0) is handed on where no row at position kv_len or later sees one of its keys; window == 0:
+// wherever it is.
+namespace {
+int fork_pages(pkv_pool* p, const int32_t* pages, int32_t n_pages, int32_t kv_len, int32_t window, int32_t sinks,
+               int32_t* child, int32_t* src, int32_t* dst, int32_t* tokens) {
   if (!p || (n_pages > 0 && (!pages || !child)) || !src || !dst || !tokens) return PKV_E_NULL;
   if (n_pages < 0 || kv_len < 0) return PKV_E_SHAPE;
   const int32_t P = p->page_size;
   const int32_t full = kv_len / P, rest = kv_len - full * P, used = full + (rest > 0 ? 1 : 0);
   if (used > n_pages) return PKV_E_PAGES;
   for (int32_t i = 0; i < used; ++i) {
-    const bool freed = pages[i] < 0 && i < full;   // (behind a window)
+    const int64_t begin = (int64_t)i * P, end = begin + P;
+    const bool seen = window > 0 && (begin < sinks || end > (int64_t)kv_len - window + 1);
+    const bool freed = pages[i] < 0 && i < full && !seen;
     if (!freed && (pages[i] < 0 || pages[i] >= p->num_pages || p->ref[pages[i]] == 0)) return PKV_E_PAGES;
   }
   if (rest > 0 && p->free_pages.empty()) return PKV_E_CAPACITY;
@@ -257,6 +262,18 @@ extern "C" int pkv_pool_fork(pkv_pool* p, const int32_t* pages, int32_t n_pages,
   *tokens = rest;
   child[full] = own;
   return 1;
+}
+}  // namespace
+
+extern "C" int pkv_pool_fork(pkv_pool* p, const int32_t* pages, int32_t n_pages, int32_t kv_len, int32_t* child,
+                             int32_t* src, int32_t* dst, int32_t* tokens) {
+  return fork_pages(p, pages, n_pages, kv_len, 0, 0, child, src, dst, tokens);
+}
+
+extern "C" int pkv_pool_fork_window(pkv_pool* p, const int32_t* pages, int32_t n_pages, int32_t kv_len, int32_t window,
+                                    int32_t sinks, int32_t* child, int32_t* src, int32_t* dst, int32_t* tokens) {
+  if (window < 1 || sinks < 0) return PKV_E_SHAPE;
+  return fork_pages(p, pages, n_pages, kv_len, window, sinks, child, src, dst, tokens);
 }
 
 // Held pages with the highest ids move to the lowest free ids, until the held pages

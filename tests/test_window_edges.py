@@ -151,3 +151,46 @@ def test_a_chunk_in_a_padded_call_reads_its_keys_once_for_several_rows(dev):
     assert binding.device_status() == 0
     # 8 rows of a piece share each key: an eighth of the reads and products, and less than two thirds of the time
     assert times[0] < 0.67 * times[1], times
+
+
+# --- forks of sequences whose pages behind a window have been let go (CPU)
+
+def test_a_fork_below_the_length_of_the_trim_is_refused(lib):
+    pool = binding.PagePool(60, 4)
+    parent = pool.trim(pool.alloc(25), 100, 40, 0)         # the next row sees keys 61 .. 100
+    assert parent[:15] == [-1] * 15 and min(parent[15:]) >= 0
+    held = [pool.refcount(i) for i in range(60)]
+    with pytest.raises(binding.PagedKVError):              # its next row would see keys 31 .. 70
+        pool.fork(parent, 70, 40)
+    assert [pool.refcount(i) for i in range(60)] == held and pool.free_count() == 50
+    assert pool.fork(parent, 70)[0][:15] == [-1] * 15      # (without a window nothing is known of what is seen)
+    child, copy = pool.fork(parent, 100, 40)
+    assert child == parent and copy is None
+    child, copy = pool.fork(parent, 99, 38)                # 62 .. 99
+    assert child[:24] == parent[:24] and copy == (parent[24], child[24], 3)
+    with pytest.raises(binding.PagedKVError):              # the sinks' page is gone
+        pool.fork(parent, 100, 40, sinks=1)
+
+
+@pytest.mark.parametrize("P", [1, 4, 7])
+@pytest.mark.parametrize("W,S", [(1, 0), (5, 0), (5, 3), (16, 4), (100, 0), (2 ** 40, 0), (3, 2 ** 40)])
+def test_a_fork_takes_what_its_rows_need(lib, P, W, S):
+    L = 41
+    for kv in range(L + 1):
+        for gone in range(-(-L // P)):
+            pool = binding.PagePool(64, P)
+            pages = pool.alloc(-(-L // P))
+            pool.release([pages[gone]])
+            pages[gone] = -1
+            first, end = gone * P, gone * P + P
+            used, partly = first < kv, first < kv < end    # a partly filled page is copied, whatever is seen of it
+            seen = first < S or end > kv - W + 1
+            if used and (partly or seen):
+                with pytest.raises(binding.PagedKVError):
+                    pool.fork(pages, kv, W, S)
+            else:
+                child, _ = pool.fork(pages, kv, W, S)
+                assert child[:kv // P] == list(pages[:kv // P])
+    for w, s in ((0, 0), (-1, 0), (1, -1), (-2 ** 40, 0), (1, -2 ** 40)):
+        with pytest.raises(binding.PagedKVError):
+            binding.PagePool(4, P).fork([], 0, w, s)
