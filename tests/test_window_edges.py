@@ -153,6 +153,44 @@ def test_a_chunk_in_a_padded_call_reads_its_keys_once_for_several_rows(dev):
     assert times[0] < 0.67 * times[1], times
 
 
+# --- what may follow a call: kernels that start early and write over what the call reads
+
+# rows beside chunks (the row kernel is through long before the chunks are), chunks alone, single rows alone
+FOLLOWED = [("bf16", "bf16", [1, 1500, 1, 1400], [300, 1500, 90, 2500]), ("bf16", "e4m3", [1, 1500, 1, 1400], [300, 1500, 90, 2500]),
+            ("f16", "f16", [2900], [4000]), ("bf16", "bf16", [1] * 100, [3000] * 100)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,cache,q,kv", FOLLOWED, ids=["mixed", "mixed-e4m3", "chunk", "rows"])
+def test_queries_and_tables_written_right_behind_a_call(dev, t, cache, q, kv):
+    p = Problem(dev, t, cache, 32, 8, 128, 64, 700, 3, q, kv)
+    want, wl = p.run()
+    T = p.q.shape[0]
+    a = _append_inputs(dev, t, cache, T, 32, 8, 128, 64, 64)
+    q0, cu, lens, tab0 = p.q.clone(), _i32(_cum(q), dev), _i32(kv, dev), _i32(p.tables, dev)
+    moved = _i32((np.arange(p.N) + 1) % p.N, dev)
+    for first in ("queries", "tables") * 3:
+        x, tab = q0.clone(), tab0.clone()
+        torch.cuda.synchronize()
+        out, lse = binding.window_attention(x, cu, lens, tab, p.kc, p.vc, p.scale, p.W, sinks=p.S, k_scale=p.ks,
+                                            v_scale=p.vs)
+
+        def append():    # the next layer's queries go where this call's are (its keys elsewhere)
+            binding.norm_rope_kv_append(a["q"], a["k"], a["v"], a["pos"], a["cs"], a["slots"], a["kc"], a["vc"],
+                                        k_scale=a["ks"], v_scale=a["vs"], q_out=x)
+
+        def remap():
+            binding.remap_pages(tab, moved)
+
+        for f in (append, remap) if first == "queries" else (remap, append):
+            f()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+        # (both were written over while or after the call read them)
+        assert (x != q0).flatten(1).any(1).all() and (tab != tab0)[tab0 >= 0].all()
+    assert binding.device_status() == 0
+
+
 # --- forks of sequences whose pages behind a window have been let go (CPU)
 
 def test_a_fork_below_the_length_of_the_trim_is_refused(lib):
