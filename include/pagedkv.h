@@ -547,7 +547,8 @@ int pkv_latent_prefill(const void* q, const int32_t* cu_seqlens_q, const void* k
  *   q_out         device, as q (strides must keep heads apart); may be q itself with the
  *                 same strides (in place), and must not overlap it otherwise
  * Norm and rotation are fp32 and rounded once; a head whose squares sum beyond the fp32
- * range comes out as zeros. A position outside [0, max_pos) sets PKV_DEV_BAD_POSITION and
+ * range comes out as zeros. With an eps of 0 a head whose squares all vanish in fp32 (zeros among
+ * them) is not finite. A position outside [0, max_pos) sets PKV_DEV_BAD_POSITION and
  * nothing of that token is written; a slot outside the pool sets PKV_DEV_BAD_SLOT and the
  * token's key and value are not written.
  * Errors: PKV_E_NULL, PKV_E_DTYPE, PKV_E_SHAPE, PKV_E_ALIGN, PKV_E_DEVICE, PKV_E_CUDA. */

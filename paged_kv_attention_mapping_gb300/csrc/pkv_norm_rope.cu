@@ -211,6 +211,14 @@ __global__ void __launch_bounds__(THREADS, MIN_BLOCKS) norm_rope_kernel(const No
 #pragma unroll
       for (int o = LR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       r = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+      // squares beyond the fp32 range (never of f16 values): zeros, which x A, beyond it too, times r is not. (r
+      // multiplied first serves as well; 4192 tokens then take 23.9 us, this way 23.5.)
+      if (!std::is_same<T, __half>::value && r == 0.f) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) x[v][e] = __fmul2_rn(x[v][e], make_float2(0.f, 0.f));
+      }
     }
     if (h < H) {
 #pragma unroll

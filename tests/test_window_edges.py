@@ -153,6 +153,26 @@ def test_a_chunk_in_a_padded_call_reads_its_keys_once_for_several_rows(dev):
     assert times[0] < 0.67 * times[1], times
 
 
+# Squares beyond the fp32 range: zeros, also where a weight or the rotation would carry the values beyond it.
+@pytest.mark.gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("t,cache,D,rot", [("bf16", "bf16", 128, 64), ("f32", "f32", 64, 64), ("bf16", "e4m3", 256, 256)])
+def test_append_of_heads_whose_squares_pass_the_range(dev, t, cache, D, rot, interleaved):
+    x = _append_inputs(dev, t, cache, 20, 4, 2, D, 16, rot)
+    q0 = x["q"].clone()
+    x["q"][:, 1::2] = torch.where(q0[:, 1::2] < 0, -3e38, 3e38).to(q0.dtype)
+    x["k"][:, 1] = x["q"][:, 1]
+    x["qw"].fill_(2.0)
+    x["kw"].fill_(-2.0)
+    q = binding.norm_rope_kv_append(x["q"], x["k"], x["v"], x["pos"], x["cs"], x["slots"], x["kc"], x["vc"],
+                                    q_weight=x["qw"], k_weight=x["kw"], eps=1e-6, interleaved=interleaved, k_scale=x["ks"],
+                                    v_scale=x["vs"])
+    assert binding.device_status() == 0
+    assert (q[:, 1::2] == 0).all() and q[:, 0::2].isfinite().all() and (q[:, 0::2] != 0).flatten(1).any(1).all()
+    k = x["kc"].flatten(0, 1)[x["slots"][x["slots"] >= 0]][:, 1]
+    assert ((k & 0x7f if cache == "e4m3" else k) == 0).all()
+
+
 # --- what may follow a call: kernels that start early and write over what the call reads
 
 # rows beside chunks (the row kernel is through long before the chunks are), chunks alone, single rows alone
