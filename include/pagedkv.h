@@ -540,12 +540,14 @@ int pkv_latent_prefill(const void* q, const int32_t* cu_seqlens_q, const void* k
  *   interleaved   0: pair i is (y_i, y_{i + rotary_dim / 2}); 1: (y_2i, y_2i+1)
  *   positions     device, int32 [num_tokens]: each token's entry of the table
  *   slot_mapping  device, int64 [num_tokens]; negative: the token's key and value are not
- *                 stored (its query is written). A slot named twice gets one of its tokens
+ *                 stored (its query is written). No slot may be named twice: it would hold
+ *                 values of several tokens
  *   k_cache, v_cache, cache  the pools and their description, head_dim 64, 128 or 256
  *   k_scale, v_scale  device, fp32 [num_kv_heads] (> 0) for an e4m3 cache, NULL otherwise:
  *                 codes of x / scale, the float32 quotient rounded to nearest, saturating
  *   q_out         device, as q (strides must keep heads apart); may be q itself with the
- *                 same strides (in place), and must not overlap it otherwise
+ *                 same strides (in place), and must overlap nothing else that the call reads or
+ *                 writes; nor may a cache overlap anything else
  * Norm and rotation are fp32 and rounded once; a head whose squares sum beyond the fp32
  * range comes out as zeros. With an eps of 0 a head whose squares all vanish in fp32 (zeros among
  * them) is not finite. A position outside [0, max_pos) sets PKV_DEV_BAD_POSITION and

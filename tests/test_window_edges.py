@@ -173,6 +173,27 @@ def test_append_of_heads_whose_squares_pass_the_range(dev, t, cache, D, rot, int
     assert ((k & 0x7f if cache == "e4m3" else k) == 0).all()
 
 
+# A slot named twice: every value is one of the tokens', other slots are not touched.
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,cache", [("bf16", "bf16"), ("f32", "f32"), ("f16", "e4m3")])
+def test_append_of_a_slot_named_twice(dev, t, cache):
+    x = _append_inputs(dev, t, cache, 64, 32, 16, 128, 16, 64)
+    k0, v0 = x["kc"].clone(), x["vc"].clone()
+    args = (x["q"], x["k"], x["v"], x["pos"], x["cs"])
+    kw = dict(q_weight=x["qw"], k_weight=x["kw"], k_scale=x["ks"], v_scale=x["vs"])
+    apart = torch.arange(64, device=dev)
+    kc, vc = torch.zeros_like(k0), torch.zeros_like(v0)
+    want_q = binding.norm_rope_kv_append(*args, apart, kc, vc, **kw)
+    slots = torch.full((64,), 19, dtype=torch.int64, device=dev)
+    q = binding.norm_rope_kv_append(*args, slots, x["kc"], x["vc"], **kw)
+    assert binding.device_status() == 0 and torch.equal(q, want_q)
+    for got, each, before in ((x["kc"], kc, k0), (x["vc"], vc, v0)):
+        got, each, before = (c.flatten(0, 1) for c in (got, each, before))
+        assert (got[19] == each[:64]).any(0).all()
+        rest = torch.arange(got.shape[0], device=dev) != 19
+        assert torch.equal(got[rest], before[rest])
+
+
 # --- what may follow a call: kernels that start early and write over what the call reads
 
 # rows beside chunks (the row kernel is through long before the chunks are), chunks alone, single rows alone
