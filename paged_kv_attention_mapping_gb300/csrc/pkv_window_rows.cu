@@ -7,7 +7,7 @@
 // some of them sees. The bound is HBM: a key and a value are read once for all columns.
 //
 // A warp copies 16 keys and values a step, whole rows an instruction, asynchronously into a ring of
-// its own in shared memory, three or four steps ahead: many more bytes are in flight than registers
+// its own in shared memory, two or three steps ahead: many more bytes are in flight than registers
 // would hold, no warp waits for another, and any page size does. Scores are S^T = K Q^T with 16
 // keys as the rows of m16n8k16; the channels of a product are permuted, alike in K and Q, so that 16
 // bytes of a key are a lane's own operand. The output is O^T += V^T P^T with 16 channels as the rows; a
@@ -126,9 +126,6 @@ __device__ __forceinline__ float ld_cluster_f(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
 // 16 bytes from global to shared memory, zeros where `from` is null.
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from, const void* any) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from ? from : any), "r"(from ? 16 : 0)
@@ -269,24 +266,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
-
-// Two e4m3 codes (the low 16 bits) as two f16 values: exact.
-__device__ __forceinline__ uint32_t widen(uint32_t codes) {
-  uint32_t out;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out) : "h"((uint16_t)codes));
-  return out;
-}
-
 // A warp's step of 16 keys in shared memory: their rows, then their values' rows, each row's 16-byte
 // chunks permuted within 128 bytes (by `turn`), so that the operand loads meet no bank twice: a
 // quarter of a warp takes chunks t + 4 j of keys g and g + 1, or chunks g and g + 1 of values 2t (or 2t + 1).
@@ -298,8 +277,9 @@ struct Share {
   static constexpr int SEGS = RB >= 128 ? RB / 128 : 1;  // a lane's pieces of a value: at segment * 128 + g * VB
   static constexpr int VB = RB >= 128 ? 16 : 8;
   static constexpr int BYTES = 2 * 16 * RB;              // of a warp's step
-  // steps in flight: 8 KB a step three (two CTAs of 96 KB an SM), smaller ones more
-  static constexpr int STAGES = BYTES >= 8192 ? 3 : BYTES >= 4096 ? 3 : 4;
+  // steps of a ring, all but one of them in flight: four of 2 KB, three of more (of 8 KB two CTAs of 96 KB an SM, of 16
+  // KB, head_dim 256 in 16 bits, one of 192)
+  static constexpr int STAGES = BYTES >= 4096 ? 3 : 4;
   static __device__ __forceinline__ int turn(int r) { return ((r & 6) ^ (r & 1) << 2) & (RB >= 128 ? 7 : 3); }
 };
 
@@ -340,8 +320,8 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_const
       for (int i = 0; i < H::CH / 2; ++i) {
         const int r = i * (32 / H::CH) + lane / H::CH;
         const uint32_t at = to + r * RB + ((lane % H::CH) ^ H::turn(r)) * 16;
-        copy_async(at, src);
-        copy_async(at + 16 * RB, src + k_to_v);
+        cp_async_16(at, src);
+        cp_async_16(at + 16 * RB, src + k_to_v);
         src += 32 / H::CH * row;
       }
       return;
@@ -435,136 +415,136 @@ __global__ void __launch_bounds__(THREADS) window_rows_kernel(const __grid_const
   // TT: tiles of columns that have any (a count known when compiled lets them overlap)
   int stage = 0;
   auto work = [&](auto tt) {
-  constexpr int TT = decltype(tt)::value;
-  for (int base = base0; base < w.keys.n; base += step) {
-    __syncwarp();   // every lane has read the last step
-    // the step ST - 1 ahead goes where that was, and the page ids of the one behind it are looked up
-    const int ahead = base + (ST - 1) * step;
-    if (ahead < w.keys.n) {
-      fetch(next, stage == 0 ? ST - 1 : stage - 1);
-      next = slot_of(p, w, ahead + step + (lane & 15));
-    }
-    copy_commit();
-    copy_wait<ST - 1>();
-    __syncwarp();   // every lane's copies have landed
-    const unsigned char* const ks = mine + stage * H::BYTES;
-    const unsigned char* const vs = ks + 16 * RB;
-    stage = stage + 1 == ST ? 0 : stage + 1;
-    float c[TT][4];
-#pragma unroll
-    for (int nt = 0; nt < TT; ++nt)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) c[nt][k] = 0.f;
-#pragma unroll
-    for (int j = 0; j < KJ; ++j) {
-      const int at = g * RB + ((t + 4 * j) ^ H::turn(g)) * 16;   // (keys g and g + 8 turn alike)
-      const uint4 k0 = *reinterpret_cast<const uint4*>(ks + at);
-      const uint4 k1 = *reinterpret_cast<const uint4*>(ks + at + 8 * RB);
-      const uint32_t a[4] = {k0.x, k0.y, k0.z, k0.w};
-      const uint32_t b[4] = {k1.x, k1.y, k1.z, k1.w};
-      if constexpr (KV8) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t a0 = widen(a[r]), a1 = widen(b[r]), a2 = widen(a[r] >> 16), a3 = widen(b[r] >> 16);
-#pragma unroll
-          for (int nt = 0; nt < TT; ++nt) mma<MT>(c[nt], a0, a1, a2, a3, qf[nt][4 * j + r][0], qf[nt][4 * j + r][1]);
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int nt = 0; nt < TT; ++nt)
-            mma<MT>(c[nt], a[2 * r], b[2 * r], a[2 * r + 1], b[2 * r + 1], qf[nt][2 * j + r][0], qf[nt][2 * j + r][1]);
+    constexpr int TT = decltype(tt)::value;
+    for (int base = base0; base < w.keys.n; base += step) {
+      __syncwarp();   // every lane has read the last step
+      // the step ST - 1 ahead goes where that was, and the page ids of the one behind it are looked up
+      const int ahead = base + (ST - 1) * step;
+      if (ahead < w.keys.n) {
+        fetch(next, stage == 0 ? ST - 1 : stage - 1);
+        next = slot_of(p, w, ahead + step + (lane & 15));
       }
-    }
-
-    // scores of keys g, g + 8 for columns 2t, 2t + 1, in log2 units. Most steps have 16 keys that
-    // every row sees
-    uint32_t pb[TT][2];
-    const int ka = key_at(w.keys, base), kz = key_at(w.keys, base + 15);
-    const bool all = base + 16 <= w.keys.n &&
-                     (w.np == 1 || (kz <= w.p_first && (ka > w.p_first + w.np - 1 - p.window || kz < p.sinks)));
-    const int i0 = base + g, i1 = i0 + 8;
-    const int k0 = key_at(w.keys, i0), k1 = key_at(w.keys, i1);
+      copy_commit();
+      copy_wait<ST - 1>();
+      __syncwarp();   // every lane's copies have landed
+      const unsigned char* const ks = mine + stage * H::BYTES;
+      const unsigned char* const vs = ks + 16 * RB;
+      stage = stage + 1 == ST ? 0 : stage + 1;
+      float c[TT][4];
 #pragma unroll
-    for (int nt = 0; nt < TT; ++nt) {
+      for (int nt = 0; nt < TT; ++nt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float a = c[nt][k] * cs[nt][k], b = c[nt][2 + k] * cs[nt][k];
-        if (!all) {
-          const bool va = i0 < w.keys.n && (w.np == 1 || seen(k0, pos[nt][k], p.window, p.sinks));
-          const bool vb2 = i1 < w.keys.n && (w.np == 1 || seen(k1, pos[nt][k], p.window, p.sinks));
-          a = va ? a : -INFINITY;
-          b = vb2 ? b : -INFINITY;
-        }
-        float top = fmaxf(a, b);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        const float mn = fmaxf(m[nt][k], top);
-        const float use = mn == -INFINITY ? 0.f : mn;
-        const float alpha = ex2(m[nt][k] - use);
-        m[nt][k] = mn;
-        a = ex2(a - use + SHIFT);
-        b = ex2(b - use + SHIFT);
-        l[nt][k] = fmaf(l[nt][k], alpha, a + b);
-        c[nt][k] = a;
-        c[nt][2 + k] = b;
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+        for (int k = 0; k < 4; ++k) c[nt][k] = 0.f;
 #pragma unroll
-          for (int i = 0; i < SEGS * MT_SEG; ++i) {
-            o[nt][i][k] *= alpha;
-            o[nt][i][2 + k] *= alpha;
-          }
-        }
-      }
-      pb[nt][0] = transpose8(pack2<MT>(c[nt][0], c[nt][1]));
-      pb[nt][1] = transpose8(pack2<MT>(c[nt][2], c[nt][3]));
-    }
-
-    // O^T += V^T P^T: output tile i of segment j holds channels 2i, 2i + 1 of each lane's piece
-#pragma unroll
-    for (int j = 0; j < SEGS; ++j) {
-      uint32_t vr[4][VR];
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int r = 2 * t + (h & 1) + 8 * (h >> 1);
-        const unsigned char* at = vs + r * RB + (VB == 16 ? (g + 8 * j) ^ H::turn(r) : (g >> 1) ^ H::turn(r)) * 16 +
-                                  (VB == 16 ? 0 : (g & 1) * 8);
-        if constexpr (VR == 4) {
-          const uint4 x = *reinterpret_cast<const uint4*>(at);
-          vr[h][0] = x.x;
-          vr[h][1] = x.y;
-          vr[h][2] = x.z;
-          vr[h][3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(at);
-          vr[h][0] = x.x;
-          vr[h][1] = x.y;
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < VR; ++r) {
-        const uint32_t v0 = vr[0][r], v1 = vr[1][r], v2 = vr[2][r], v3 = vr[3][r];
+      for (int j = 0; j < KJ; ++j) {
+        const int at = g * RB + ((t + 4 * j) ^ H::turn(g)) * 16;   // (keys g and g + 8 turn alike)
+        const uint4 k0 = *reinterpret_cast<const uint4*>(ks + at);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(ks + at + 8 * RB);
+        const uint32_t a[4] = {k0.x, k0.y, k0.z, k0.w};
+        const uint32_t b[4] = {k1.x, k1.y, k1.z, k1.w};
         if constexpr (KV8) {
-          const uint32_t x0 = __byte_perm(v0, v1, 0x5140), x1 = __byte_perm(v2, v3, 0x5140);
-          const uint32_t y0 = __byte_perm(v0, v1, 0x7362), y1 = __byte_perm(v2, v3, 0x7362);
-          const uint32_t a0 = widen(x0), a1 = widen(x0 >> 16), a2 = widen(x1), a3 = widen(x1 >> 16);
-          const uint32_t b0 = widen(y0), b1 = widen(y0 >> 16), b2 = widen(y1), b3 = widen(y1 >> 16);
 #pragma unroll
-          for (int nt = 0; nt < TT; ++nt) {
-            mma<MT>(o[nt][j * MT_SEG + 2 * r], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-            mma<MT>(o[nt][j * MT_SEG + 2 * r + 1], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t a0 = widen(a[r]), a1 = widen(b[r]), a2 = widen(a[r] >> 16), a3 = widen(b[r] >> 16);
+#pragma unroll
+            for (int nt = 0; nt < TT; ++nt) mma<MT>(c[nt], a0, a1, a2, a3, qf[nt][4 * j + r][0], qf[nt][4 * j + r][1]);
           }
         } else {
-          const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
-          const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
 #pragma unroll
-          for (int nt = 0; nt < TT; ++nt) mma<MT>(o[nt][j * MT_SEG + r], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int nt = 0; nt < TT; ++nt)
+              mma<MT>(c[nt], a[2 * r], b[2 * r], a[2 * r + 1], b[2 * r + 1], qf[nt][2 * j + r][0], qf[nt][2 * j + r][1]);
+        }
+      }
+
+      // scores of keys g, g + 8 for columns 2t, 2t + 1, in log2 units. Most steps have 16 keys that
+      // every row sees
+      uint32_t pb[TT][2];
+      const int ka = key_at(w.keys, base), kz = key_at(w.keys, base + 15);
+      const bool all = base + 16 <= w.keys.n &&
+                       (w.np == 1 || (kz <= w.p_first && (ka > w.p_first + w.np - 1 - p.window || kz < p.sinks)));
+      const int i0 = base + g, i1 = i0 + 8;
+      const int k0 = key_at(w.keys, i0), k1 = key_at(w.keys, i1);
+#pragma unroll
+      for (int nt = 0; nt < TT; ++nt) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float a = c[nt][k] * cs[nt][k], b = c[nt][2 + k] * cs[nt][k];
+          if (!all) {
+            const bool va = i0 < w.keys.n && (w.np == 1 || seen(k0, pos[nt][k], p.window, p.sinks));
+            const bool vb2 = i1 < w.keys.n && (w.np == 1 || seen(k1, pos[nt][k], p.window, p.sinks));
+            a = va ? a : -INFINITY;
+            b = vb2 ? b : -INFINITY;
+          }
+          float top = fmaxf(a, b);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          const float mn = fmaxf(m[nt][k], top);
+          const float use = mn == -INFINITY ? 0.f : mn;
+          const float alpha = ex2(m[nt][k] - use);
+          m[nt][k] = mn;
+          a = ex2(a - use + SHIFT);
+          b = ex2(b - use + SHIFT);
+          l[nt][k] = fmaf(l[nt][k], alpha, a + b);
+          c[nt][k] = a;
+          c[nt][2 + k] = b;
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+            for (int i = 0; i < SEGS * MT_SEG; ++i) {
+              o[nt][i][k] *= alpha;
+              o[nt][i][2 + k] *= alpha;
+            }
+          }
+        }
+        pb[nt][0] = transpose8(pack2<MT>(c[nt][0], c[nt][1]));
+        pb[nt][1] = transpose8(pack2<MT>(c[nt][2], c[nt][3]));
+      }
+
+      // O^T += V^T P^T: output tile i of segment j holds channels 2i, 2i + 1 of each lane's piece
+#pragma unroll
+      for (int j = 0; j < SEGS; ++j) {
+        uint32_t vr[4][VR];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int r = 2 * t + (h & 1) + 8 * (h >> 1);
+          const unsigned char* at = vs + r * RB + (VB == 16 ? (g + 8 * j) ^ H::turn(r) : (g >> 1) ^ H::turn(r)) * 16 +
+                                    (VB == 16 ? 0 : (g & 1) * 8);
+          if constexpr (VR == 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(at);
+            vr[h][0] = x.x;
+            vr[h][1] = x.y;
+            vr[h][2] = x.z;
+            vr[h][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(at);
+            vr[h][0] = x.x;
+            vr[h][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < VR; ++r) {
+          const uint32_t v0 = vr[0][r], v1 = vr[1][r], v2 = vr[2][r], v3 = vr[3][r];
+          if constexpr (KV8) {
+            const uint32_t x0 = __byte_perm(v0, v1, 0x5140), x1 = __byte_perm(v2, v3, 0x5140);
+            const uint32_t y0 = __byte_perm(v0, v1, 0x7362), y1 = __byte_perm(v2, v3, 0x7362);
+            const uint32_t a0 = widen(x0), a1 = widen(x0 >> 16), a2 = widen(x1), a3 = widen(x1 >> 16);
+            const uint32_t b0 = widen(y0), b1 = widen(y0 >> 16), b2 = widen(y1), b3 = widen(y1 >> 16);
+#pragma unroll
+            for (int nt = 0; nt < TT; ++nt) {
+              mma<MT>(o[nt][j * MT_SEG + 2 * r], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+              mma<MT>(o[nt][j * MT_SEG + 2 * r + 1], b0, b1, b2, b3, pb[nt][0], pb[nt][1]);
+            }
+          } else {
+            const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
+            const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < TT; ++nt) mma<MT>(o[nt][j * MT_SEG + r], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          }
         }
       }
     }
-  }
   };
   if (NT == 1 || w.np * p.heads <= 8) work(std::integral_constant<int, 1>());
   else work(std::integral_constant<int, NT>());

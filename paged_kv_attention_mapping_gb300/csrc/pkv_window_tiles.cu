@@ -192,23 +192,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return y;
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
-
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
-  uint32_t out;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(out) : "h"((uint16_t)codes));
-  return out;
-}
-
 // e4m3 tiles: codes lie in the upper half of the slot, 128 a row, 128-byte swizzled; the
 // f16 tile is what a 16-bit load would have made of it (two 64-column halves). A lane reads a
 // row's codes before it writes the row, and row r's codes are overwritten by row r alone.
@@ -230,8 +213,8 @@ __device__ __forceinline__ void widen_rows(unsigned char* slot, const LoadDesc& 
       uint32_t h[8];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        h[2 * q] = widen2(w[q]);
-        h[2 * q + 1] = widen2(w[q] >> 16);
+        h[2 * q] = widen(w[q]);
+        h[2 * q + 1] = widen(w[q] >> 16);
       }
       unsigned char* row = slot + (k >> 2) * BN * 128 + r * 128;
       const int ch = (k & 3) * 2;
