@@ -1,5 +1,5 @@
 // C-ABI entry points of the windowed layers' calls: host-side checks, then the launches of
-// pkv_norm_rope.cu, pkv_window_rows.cu and pkv_pages.cu.
+// pkv_norm_rope.cu, pkv_window_rows.cu, pkv_window_tiles.cu and pkv_pages.cu.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

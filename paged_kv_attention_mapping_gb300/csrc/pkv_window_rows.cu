@@ -16,7 +16,7 @@
 // memory, and the CTAs that share a piece's keys (a cluster) through distributed shared memory: no
 // workspace and one launch.
 //
-// 128 rows of up to 4096 keys, 32 / 8 heads of 128, bf16: 246 us, 6.5 TB/s, 98 % of the measured copy; 64
+// 128 rows of up to 4096 keys, 32 / 8 heads of 128, bf16: 249 us, 6.4 TB/s, 96 % of the measured copy; 64
 // rows of 132 keys, heads of 64: 5.9 us, four dependent reads and the join. Steps taken (the first case):
 // operands straight from global memory into registers 308 us; copied asynchronously by the lane that
 // consumes them, 64 bytes of eight rows an instruction, 311; whole rows an instruction 252; keys in one

@@ -22,15 +22,21 @@
 // The softmax keeps a running maximum and sum; O is rescaled in TMEM only when a row's
 // maximum grows by more than 2^8. A row can start with pieces that it does not see: its
 // maximum is then -inf, and its weights 0.
-// What bounds it: in wide windows the chain of a query tile, products - softmax - products, of which
-// two are in flight (tensor memory holds no third): a step of both takes about 3130 cycles of which the
-// tensor pipe works 2048. In narrow ones the ends of work tiles (Q arrives, the first scores, the
-// output's stores), 6 to 8 us a tile of which little overlaps. 16384 tokens, 32 / 8 heads of 128: window 2048
-// 427 us, 1206 TFLOP/s (63 % of the measured burst rate); 512 178 us; 128 105 us. Seven prompts of
-// 300 to 2500 tokens at window 512, 28 / 4 heads: 94 us.
+// What bounds it: the one warp that issues all products, in order. Cycles of a step of both query tiles, by time stamps
+// in it and in a softmax warp of each (which cost 14 %):
+//   16384 tokens, window 2048: 3970, of which the products are 2048. The MMA warp waits 790 for weights (460 for the
+//     first half, 330 for the second; nothing of the other query tile's is issued meanwhile) and 280 for K and V; the
+//     other 850 are its issue and hand-offs, and the stamps. A softmax warp has a step's weights 1310 after its scores
+//     and then waits 1810 for the next ones, so its own work is not the bound (without it the calls take 12 % less).
+//   seven prompts at window 512: 5040, of which 1480 are waits for weights; a work tile is four steps (20990 of
+//     its 22830 cycles), its first scores and last output with nothing beside them, its output's store 2090.
+//   16384 tokens, window 128: two steps of 6530 a work tile, 2320 of each waits for weights.
+// 16384 tokens, 32 / 8 heads of 128, no sinks: window 2048 427 us, 1206 TFLOP/s (63 % of the measured burst rate); 512
+// 178 us; 128 105 us; with 64 sinks at 2048 456. Seven prompts of 300 to 2500 tokens at window 512, 28 / 4 heads: 95 us.
 // Steps taken (16384 tokens at window 2048): ranges in place of whole tiles at the ends, whole steps with
 // their scores in registers and others read twice (610 -> 497 us), ranges as words for the MMA
-// warp, which is short of issue slots (465), weights handed over in halves and 32-byte stores (456).
+// warp, which is short of issue slots (465), weights handed over in halves and 32-byte stores (456; with work tiles numbered
+// without gaps, a bad page's flag a query tile's own: 452, 456).
 // Without gain: two threads a row (526; the exponentials share a unit), an MMA warp for each query
 // tile (479), both forms of a step over registers (2261, spills), masked steps over registers (498) or two
 // pieces at a time (509), partial steps as a function (702), boxes of 128 rows, a ring of four slots,
