@@ -32,14 +32,14 @@ struct NormP {
 };
 
 // The bound is HBM: (2 Hq + 2 Hkv) D values of the source type and 2 Hkv D of the cache's a token.
-// 4192 tokens at 32 / 8 heads of 128 (bf16, 105 MB) take 23.5 us, 4.5 TB/s, 67 % of the copy
-// bandwidth; 64 tokens 2.8 us, a launch and two rounds of loads. What is left is latency: a warp loads, waits,
-// computes, stores and leaves (issue slots 46 % busy, 37 % of the warps resident, at 72 registers). Steps taken: angles and weights
-// multiplied once a unit (41 -> 27.7 us), blocks of 128 at 64 registers (26.6), addresses stepped and the
-// approximate root, which is within 2 ulp (24.3), a lane holding both halves of its pairs (23.4;
-// 64 tokens 3.1 -> 2.8). Without gain: more passes in flight (33, 35), a unit's loads issued while the one
-// before is worked on (27 to 37), streaming loads (25.2), two chunks a unit (24.6), six or eight blocks
-// an SM in place of seven (23.9, 26.2).
+// 4192 tokens at 32 / 8 heads of 128 (bf16, 105 MB) take 23.5 us, 4.5 TB/s, 67 % of the copy bandwidth; 64
+// tokens 2.8 us, a launch and two rounds of loads. What is left is latency: a warp loads, waits, computes,
+// stores and leaves (issue slots 46 % busy, 37 % of the warps resident, at 72 registers). Steps taken: angles
+// and weights multiplied once a unit (41 -> 27.7 us), blocks of 128 at 64 registers (26.6), addresses stepped
+// and the approximate root, which is within 2 ulp (24.3), a lane holding both halves of its pairs (23.4; 64
+// tokens 3.1 -> 2.8). Without gain: more passes in flight (33, 35), a unit's loads issued while the one before
+// is worked on (27 to 37), streaming loads (25.2), two chunks a unit (24.6), six or eight blocks an SM in place
+// of seven (23.9, 26.2).
 //
 // A warp's unit: ROWS consecutive head rows of one token, all queries, all keys or
 // all values. A lane holds two vectors of E values of a row, those that the rotation pairs

@@ -31,12 +31,13 @@
 //   seven prompts at window 512: 5040, of which 1480 are waits for weights; a work tile is four steps (20990 of
 //     its 22830 cycles), its first scores and last output with nothing beside them, its output's store 2090.
 //   16384 tokens, window 128: two steps of 6530 a work tile, 2320 of each waits for weights.
-// 16384 tokens, 32 / 8 heads of 128, no sinks: window 2048 427 us, 1206 TFLOP/s (63 % of the measured burst rate); 512
-// 178 us; 128 105 us; with 64 sinks at 2048 456. Seven prompts of 300 to 2500 tokens at window 512, 28 / 4 heads: 95 us.
-// Steps taken (16384 tokens at window 2048): ranges in place of whole tiles at the ends, whole steps with
-// their scores in registers and others read twice (610 -> 497 us), ranges as words for the MMA
-// warp, which is short of issue slots (465), weights handed over in halves and 32-byte stores (456; with work tiles numbered
-// without gaps, a bad page's flag a query tile's own: 452, 456).
+// 16384 tokens, 32 / 8 heads of 128, no sinks: window 2048 436 us, 1182 TFLOP/s (62 % of the measured burst
+// rate); 512 174 us; 128 104 us; with 64 sinks at 2048 455; over e4m3 with bf16 queries 659, 339 and 250. Seven
+// prompts of 300 to 2500 tokens at window 512, 28 / 4 heads: 95 us.
+// Steps taken (16384 tokens at window 2048): ranges in place of whole tiles at the ends, whole steps with their
+// scores in registers and others read twice (610 -> 497 us), ranges as words for the MMA warp, which is short of
+// issue slots (465), weights handed over in halves and 32-byte stores (456; with work tiles numbered without
+// gaps, a bad page's flag a query tile's own: 452, 456).
 // Without gain: two threads a row (526; the exponentials share a unit), an MMA warp for each query
 // tile (479), both forms of a step over registers (2261, spills), masked steps over registers (498) or two
 // pieces at a time (509), partial steps as a function (702), boxes of 128 rows, a ring of four slots,
@@ -402,11 +403,12 @@ __global__ void __launch_bounds__((HELPER + (KV8 ? 2 : 1)) * 32, 1)
     // a bit a slot: parity of its loads, of those that land for a helper, and whether the last did
     uint32_t ring = 0, loads = 0, landing = 0, last_land = 0, used = 0, q_loads = 0;
     bool ok = true;
-    // Work tiles are numbered without gaps, sequence by sequence, so that the CTAs' shares differ by one tile
-    // at most: with the row kernel's numbers, which need no counting, 16 sequences of 32 rows (window
-    // 4096, 32 / 8 heads of 128) took 105 us for 60, 12 of 50 rows 130 for 73, 16 of 64 (window 512; no gaps) 24.9
-    // for 25.4. Lane l counts the tiles of `share` sequences and keeps the number behind them. (A cu_seqlens_q that breaks its rules may count more than `most`,
-    // which its rows could make; counts stop there, so that 32 bits hold them, and no more are worked on.)
+    // Work tiles are numbered without gaps, sequence by sequence, so that the CTAs' shares differ by one tile at
+    // most: with the row kernel's numbers, which need no counting, 16 sequences of 32 rows (window 4096, 32 / 8
+    // heads of 128) took 105 us for 60, 12 of 50 rows 130 for 73, 16 of 64 (window 512; no gaps) 24.9 for 25.4.
+    // Lane l counts the tiles of `share` sequences and keeps the number behind them. (A cu_seqlens_q that breaks
+    // its rules may count more than `most`, which its rows could make; counts stop there, so that 32 bits hold
+    // them, and no more are worked on.)
     const int per = NQ * p.PP, share = (p.B + 31) / 32;
     const uint32_t most = (uint32_t)p.B + (uint32_t)(p.T / per);
     auto count = [&](int b, int& c0, int& c1) {
